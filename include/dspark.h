@@ -465,6 +465,138 @@ int dspark_markov_draft(const float* U, const void* W1, const void* W2, int rank
                         void* stream);
 
 /* ---------------------------------------------------------------------------
+ * dspark_qk_norm_rope -- from the projections of the packed rows to the q, k_new
+ * and v_new that dspark_verify_attn reads: an RMS norm of each query and key head
+ * and the rotation by the row's position in one pass, the values copied beside
+ * them.  ([lesson] "Ragged verify under full CUDA graphs": the packed rows carry
+ * their own positions.)  For head vector x of the row at position p, in fp32:
+ *     y = w x / sqrt(mean(x^2) + eps)            (weight NULL: y = x)
+ *     c_i = attn_factor cos(p f_i),  s_i = attn_factor sin(p f_i),  i < R / 2
+ *     (y_a, y_b) <- (y_a c_i - y_b s_i, y_b c_i + y_a s_i)
+ * with (a, b) = (i, i + R/2), or (2i, 2i + 1) if interleaved; dims >= R keep y; one
+ * rounding to bf16 at the end.  The angle is reduced to less than a turn in fp64.
+ *
+ *   q_in, k_in, v_in  [rows, H, 128] of `dtype`, heads dense, rows q_stride /
+ *               k_stride / v_stride elements apart (at least H * 128; the parts of
+ *               one fused projection have its row length).  Bases 16-byte aligned,
+ *               strides multiples of 16 bytes.  v_in may be NULL, with v_new.
+ *   q_weight, k_weight  fp32 [128], nullable, 16-byte aligned
+ *   eps         >= 0
+ *   inv_freq    fp32 [rotary_dim / 2] (NULL if rotary_dim is 0)
+ *   rotary_dim  R, a multiple of 16 in 0..128
+ *   row_pos     int32 [rows]: position of each row (dspark_pack's row_pos); a row with
+ *               a negative position is padding, its outputs are left as they are
+ *   n_rows      int32 [1], nullable: rows from *n_rows on (dspark_pack's M_out) are left
+ *               as they are too, whatever row_pos holds there
+ *   q, k_new, v_new  bf16 [rows, H, 128] out, dense, 16-byte aligned.  An output may
+ *               be its own input (bf16, dense); any other overlap is not allowed.
+ * ------------------------------------------------------------------------- */
+int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
+                        long long k_stride, const void* v_in, long long v_stride, int dtype,
+                        const float* q_weight, const float* k_weight, float eps,
+                        const float* inv_freq, int rotary_dim, int interleaved, float attn_factor,
+                        const int32_t* row_pos, const int32_t* n_rows, int rows, int Hq, int Hkv,
+                        void* q, void* k_new, void* v_new, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit paged KV cache (head dim 128): 136 bytes per token and KV head in
+ * place of 512.
+ *
+ * kv_cache  uint8 [n_pages, Hkv, page_size / 16, DSPARK_KV4_BLOCK_BYTES], 16-byte
+ * aligned.  A block holds 16 consecutive tokens of one head:
+ *     bytes    0..1023  K codes  [4 groups of 32 dims][16 tokens][16 B]
+ *     bytes 1024..2047  V codes  [128 channels][8 B = 16 tokens]
+ *     bytes 2048..2111  K scales e4m3 [16 tokens][4 groups]
+ *     bytes 2112..2175  V scales e4m3 [4 groups of 32 channels][16 tokens]
+ * In every little-endian 32-bit word of codes, nibble p (p = 0..3) holds element 2p
+ * and nibble p + 4 element 2p + 1 of eight consecutive ones (dims of a token for K,
+ * tokens of a channel for V).  The value of an element is
+ *     (code - 8) * scale * g,   g = k_scale or v_scale (fp32, > 0, one per tensor).
+ * page_size is a power of two >= 16.  A page belongs to one request while it is
+ * written (two requests may read a page, as with a shared prefix).
+ *
+ * dspark_kv4_store writes row cu_seqlens[r] + i (i < n_r) of k and v ([max_rows,
+ * Hkv, 128] fp32 or bf16 per dtype, rows k_stride / v_stride elements apart, as in
+ * dspark_qk_norm_rope) to position pos0[r] + i of request r, whose page must already
+ * be in the page table.  For a token's group of 32 elements
+ *     t = amax / (7 g);  scale = the smallest e4m3 number >= t (448 above it);
+ *     code = 8 + clamp(rint(x / (scale g)), -7, 7)      (fp32, ties to even)
+ * so an element is off by at most half a step, scale g / 2, unless the group's
+ * amax passes 3136 g.  A NaN is stored as 0, infinities as the largest value.
+ * Other positions keep their values.
+ *
+ * dspark_kv4_load reads positions pos0[r] .. pos0[r] + n_r - 1 back into packed rows
+ * k, v [max_rows, Hkv, 128] (dense, fp32 or bf16 per dtype); rows >= cu_seqlens[B]
+ * are left as they are.
+ *
+ * Both: a position whose page-table slot or page is out of range sets
+ * DSPARK_DEVERR_BAD_INPUT and is skipped with the rest of its block; cu_seqlens[B] >
+ * max_rows sets DSPARK_DEVERR_ROWS_OVERFLOW and nothing is done.  One kernel each.
+ * ------------------------------------------------------------------------- */
+#define DSPARK_KV4_BLOCK_BYTES 2176
+
+int dspark_kv4_store(const void* k, long long k_stride, const void* v, long long v_stride,
+                     int dtype, const int32_t* cu_seqlens, const int32_t* pos0, int B,
+                     int max_rows, int Hkv, int page_size, const int32_t* page_table,
+                     int max_pages, int n_pages, float k_scale, float v_scale, void* kv_cache,
+                     void* stream);
+int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32_t* pos0, int B,
+                    int max_rows, int Hkv, int page_size, const int32_t* page_table,
+                    int max_pages, int n_pages, float k_scale, float v_scale, int dtype, void* k,
+                    void* v, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_verify_attn_kv4 -- dspark_verify_attn (GQA shape) over the 4-bit cache: the
+ * committed keys and values are those its codes stand for, the block rows k_new and
+ * v_new are bf16 as there.  Arguments as dspark_verify_attn, with kv_cache, k_scale
+ * and v_scale in place of the two caches, and
+ *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
+ *   Hq / Hkv <= 64
+ *   max_block_rows: the query tile holds 32 rows of G = Hq / Hkv heads x block rows,
+ *        or 64 where G x max_block_rows is above 32; longer segments run as several
+ *        row tiles.
+ * Rounding: the cached values and the queries are exact in the products' fp16
+ * operands (a query row is scaled by a power of two; elements below 2^-30 of the row's
+ * largest may lose bits), block rows are rounded to fp16 after division by
+ * 16 k_scale / 16 v_scale (saturating: |k_new| < 10^6 k_scale), the probabilities to
+ * fp16; sums are fp32, and out is rounded once to bf16.
+ * A page out of range sets DSPARK_DEVERR_BAD_INPUT; its keys are left out.
+ *
+ * dspark_verify_attn_kv4_planned runs over the work list that dspark_pack_plan wrote
+ * (d_qk = d_v = 128, the same Hq, Hkv, max_rows, max_splits, max_block_rows and
+ * workspace); DSPARK_EUNSUPPORTED if G x max_block_rows is above 64.
+ * ------------------------------------------------------------------------- */
+size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
+                                             int max_block_rows);
+int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
+                           const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                           const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                           const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
+                           int page_size, float scale, int max_splits, int max_block_rows,
+                           void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+int dspark_verify_attn_kv4_planned(const void* q, const void* k_new, const void* v_new,
+                                   const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                                   const int32_t* page_table, int max_pages,
+                                   const int32_t* ctx_len, const int32_t* cu_seqlens, int B,
+                                   int max_rows, int Hq, int Hkv, int page_size, float scale,
+                                   int max_splits, int max_block_rows, void* out, float* lse,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_compact_kv4 -- dspark_compact into the 4-bit cache: the kept rows of k_new and
+ * v_new (bf16 [max_rows, Hkv, 128], dense) are quantised as dspark_kv4_store does.
+ * Everything else as dspark_compact (same workspace size).
+ * ------------------------------------------------------------------------- */
+int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_rows,
+                       const int32_t* cu_seqlens, const int32_t* accept_len,
+                       const int32_t* out_tok, const int32_t* draft_tok, int B, int gamma,
+                       int page_size, int max_pages, int n_pages, int32_t* page_table,
+                       int32_t* ctx_len, int32_t* anchor, const int32_t* free_pages,
+                       int32_t* free_top, void* kv_cache, float k_scale, float v_scale,
+                       int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
  * dspark_step_graph -- the whole verification step as one CUDA graph, with the
  * captured tier chosen on the device ([lesson] "Ragged verify under full CUDA
  * graphs": the packed batch is rounded up to a captured tier and that tier's

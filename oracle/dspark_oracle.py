@@ -762,3 +762,136 @@ def block_accept_estimate(p_target, p_draft, draft_tok, uniforms, windows, cu_se
         else:
             lo[r] = hi[r] = w
     return lo, hi
+
+
+# ----------------------------------------------------------------------------
+# 11. Query/key norm with the position rotation
+# ----------------------------------------------------------------------------
+
+def qk_norm_rope(x, weight, eps, inv_freq, interleaved, attn_factor, row_pos):
+    """One projection's heads x [rows, H, 128] in fp64: RMS norm over each head (weight
+    None: none), then the rotation of the first 2 len(inv_freq) dims by the row's
+    position.  Rows with a negative position come back as NaN (they are not written).
+    Returns (y, mag): mag[., a] = |y_a| + |y_b| before the rotation, what the rounding
+    of the rotation scales with."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, H, D = x.shape
+    out = np.full_like(x, np.nan)
+    mag = np.zeros_like(x)
+    half = len(inv_freq)
+    for r in range(rows):
+        if row_pos[r] < 0:
+            continue
+        for h in range(H):
+            y = x[r, h].copy()
+            if weight is not None:
+                y = y / math.sqrt(float(np.mean(y * y)) + eps) * np.asarray(weight, dtype=np.float64)
+            z, m = y.copy(), np.abs(y)
+            for i in range(half):
+                a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+                ang = math.fmod(float(row_pos[r]) * float(inv_freq[i]), 2.0 * math.pi)
+                c, s = attn_factor * math.cos(ang), attn_factor * math.sin(ang)
+                z[a], z[b] = y[a] * c - y[b] * s, y[b] * c + y[a] * s
+                m[a] = m[b] = abs(attn_factor) * (abs(y[a]) + abs(y[b]))
+            out[r, h], mag[r, h] = z, m
+    return out, mag
+
+
+# ----------------------------------------------------------------------------
+# 12. The 4-bit paged KV cache
+# ----------------------------------------------------------------------------
+
+KV4_BLOCK_BYTES = 2176
+
+
+def e4m3_value(code) -> float:
+    """Value of an e4m3 code (sign, 4 exponent bits of bias 7, 3 mantissa bits; 0x7f and
+    0xff are NaN, no infinities)."""
+    code = int(code)
+    sign = -1.0 if code & 0x80 else 1.0
+    e, m = (code >> 3) & 15, code & 7
+    if e == 15 and m == 7:
+        return math.nan
+    return sign * (m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10))
+
+
+_E4M3 = np.array([e4m3_value(c) for c in range(256)])
+
+
+def kv4_quantise(x, g):
+    """x [..., 128] -> (codes 0..15, scale codes [..., 4], values fp64), in the fp32
+    arithmetic of the rule: t = amax / (7 g) over 32 elements, the smallest e4m3 >= t as
+    scale, code = 8 + clamp(rint(x / (scale g)), -7, 7); NaN and scale 0 give code 8."""
+    x = np.asarray(x, dtype=F32)
+    g = F32(g)
+    grp = x.reshape(*x.shape[:-1], -1, 32)
+    with np.errstate(all="ignore"):
+        amax = np.fmax.reduce(np.abs(grp), axis=-1)
+        amax = np.where(np.isnan(amax), F32(0), amax)
+        t = (amax / (F32(7) * g)).astype(F32)
+        scode = np.minimum(np.searchsorted(_E4M3[:127], t.astype(np.float64)), 126)
+        sg = (_E4M3[scode].astype(F32) * g).astype(F32)[..., None]
+        q = np.rint((grp / sg).astype(F32))
+        q = np.clip(np.where(np.isnan(q) | ~(sg > 0), 0, q), -7, 7)
+    val = (q * _E4M3[scode].astype(F32)[..., None]).astype(F32) * g
+    return ((q + 8).astype(np.uint8).reshape(x.shape), scode.astype(np.uint8),
+            val.astype(np.float64).reshape(x.shape))
+
+
+def _nibble_at(base, element):
+    """(byte, shift) of an element of eight in the word at byte `base`."""
+    nib = (element >> 1) + 4 * (element & 1)
+    return base + (nib >> 1), 4 * (nib & 1)
+
+
+def _kv4_place(page_table_row, pos, page_size):
+    return int(page_table_row[pos // page_size]), (pos % page_size) // 16, pos % 16
+
+
+def kv4_store(k, v, cu_seqlens, pos0, page_table, cache, g_k, g_v, n_keep=None):
+    """Row cu_seqlens[r] + i of k, v [rows, Hkv, 128] into position pos0[r] + i of request
+    r, element by element; `cache` uint8 [pages, Hkv, page / 16, 2176] is copied."""
+    cache = cache.copy()
+    page_size = cache.shape[2] * 16
+    for r in range(len(pos0)):
+        n = int(cu_seqlens[r + 1] - cu_seqlens[r])
+        if n_keep is not None:
+            n = min(n, int(n_keep[r]))
+        for i in range(n):
+            row = int(cu_seqlens[r]) + i
+            page, blk, tok = _kv4_place(page_table[r], int(pos0[r]) + i, page_size)
+            for h in range(cache.shape[1]):
+                b = cache[page, h, blk]
+                kc, ks, _ = kv4_quantise(k[row, h], g_k)
+                vc, vs, _ = kv4_quantise(v[row, h], g_v)
+                for d in range(128):
+                    at, sh = _nibble_at((d // 32) * 256 + tok * 16 + (d % 32) // 8 * 4, d % 8)
+                    b[at] = (int(b[at]) & ~(15 << sh) & 255) | (int(kc[d]) << sh)
+                    at, sh = _nibble_at(1024 + d * 8 + tok // 8 * 4, tok % 8)
+                    b[at] = (int(b[at]) & ~(15 << sh) & 255) | (int(vc[d]) << sh)
+                b[2048 + tok * 4:2048 + tok * 4 + 4] = ks
+                b[2112 + tok::16][:4] = vs
+    return cache
+
+
+def kv4_values(cache, g_k, g_v):
+    """The K and V that a 4-bit cache stands for, fp64 [pages, page_size, Hkv, 128]."""
+    pages, Hkv, per, _ = cache.shape
+    c = cache.astype(np.int64)
+
+    def word_elements(b):          # [..., 4m] bytes -> [..., 8m] elements in order
+        w = b.reshape(*b.shape[:-1], -1, 4)
+        out = np.empty((*w.shape[:-1], 8))
+        for e in range(8):
+            at, sh = _nibble_at(0, e)
+            out[..., e] = ((w[..., at] >> sh) & 15) - 8
+        return out.reshape(*b.shape[:-1], -1)
+
+    k = word_elements(c[..., :1024].reshape(pages, Hkv, per, 4, 16, 16))     # [grp, tok, 32]
+    ks = _E4M3[c[..., 2048:2112]].reshape(pages, Hkv, per, 16, 4)            # [tok, grp]
+    k = k.transpose(0, 1, 2, 4, 3, 5) * ks[..., None] * float(F32(g_k))      # [tok, grp, 32]
+    v = word_elements(c[..., 1024:2048].reshape(pages, Hkv, per, 4, 32, 8))  # [grp, ch, tok]
+    vs = _E4M3[c[..., 2112:2176]].reshape(pages, Hkv, per, 4, 1, 16)
+    v = (v * vs * float(F32(g_v))).transpose(0, 1, 2, 5, 3, 4)               # [tok, grp, ch]
+    shape = (pages, Hkv, per * 16, 128)
+    return (k.reshape(shape).transpose(0, 2, 1, 3), v.reshape(shape).transpose(0, 2, 1, 3))

@@ -19,6 +19,9 @@ __all__ = [
     "schedule", "pack", "verify_attn", "accept", "accept_noalloc", "compact", "read_device_error",
     "verify_attn_workspace_size", "accept_workspace_size", "compact_workspace_size",
     "VerifyStep", "StepGraph", "CalibStore", "DEVERR",
+    "qk_norm_rope", "KV4_BLOCK_BYTES", "kv4_cache", "kv4_store", "kv4_load",
+    "verify_attn_kv4", "verify_attn_kv4_planned", "verify_attn_kv4_workspace_size",
+    "block_rows_hint_for_kv4", "compact_kv4",
 ]
 
 COMPACT, STATIC, CAP_ACCEPT = 0, 1, 2
@@ -31,10 +34,13 @@ DEVERR = {
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
+KV4_BLOCK_BYTES = 2176   # 16 tokens of one KV head in the 4-bit cache
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_longlong
 
 _SIGNATURES = {
     "dspark_status_string": (ctypes.c_char_p, [_I]),
@@ -71,6 +77,18 @@ _SIGNATURES = {
     "dspark_step_graph_flags": (_I, [_P]),
     "dspark_compact": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                             _P, _P, _P, _P, _Z, _P]),
+    "dspark_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _P, _I, _I, _F, _P, _P, _I,
+                                 _I, _I, _P, _P, _P, _P]),
+    "dspark_kv4_store": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _I, _P, _I, _I, _F, _F, _P,
+                              _P]),
+    "dspark_kv4_load": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _F, _F, _I, _P, _P, _P]),
+    "dspark_verify_attn_kv4_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "dspark_verify_attn_kv4": (_I, [_P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I,
+                                    _F, _I, _I, _P, _P, _P, _Z, _P]),
+    "dspark_verify_attn_kv4_planned": (_I, [_P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _I, _I, _I,
+                                            _I, _I, _F, _I, _I, _P, _P, _P, _Z, _P]),
+    "dspark_compact_kv4": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
+                                _P, _P, _F, _F, _P, _P, _P, _Z, _P]),
 }
 
 _lib = None
@@ -353,6 +371,187 @@ def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+# ---- query/key norm with rotation, and the 4-bit cache.  These bindings also check types,
+# shapes and that every tensor is on the current device (whose stream the call goes to).
+
+def _arg(t, name, dtype, shape=None):
+    """Address of a dense tensor of this type on the current device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise ValueError(f"{name}: expected a {dtype} tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _on_current(t, name)
+    return t.data_ptr()
+
+
+def _on_current(t, name):
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+
+
+def _rows(t, name, rows, heads, dtype):
+    """(address, row stride in elements) of [rows, heads, 128] with dense heads."""
+    if t.dtype is not dtype or t.shape != (rows, heads, 128):
+        raise ValueError(f"{name}: expected {dtype} [{rows}, {heads}, 128], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if rows == 1:
+        s0 = max(s0, heads * 128)   # the stride of one row is never used
+        s0 -= s0 % 8
+    if s2 != 1 or (heads > 1 and s1 != 128):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    _on_current(t, name)
+    return t.data_ptr(), s0
+
+
+def _float_dtype(t, name):
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise ValueError(f"{name}: expected a float32 or bfloat16 tensor")
+
+
+def qk_norm_rope(q_in, k_in, v_in, q_weight, k_weight, inv_freq, row_pos, q, k_new, v_new,
+                 eps=1e-6, interleaved=False, attn_factor=1.0, stream=None, n_rows=None):
+    """Projections of packed rows -> q, k_new, v_new of the verify attention
+    (dspark_qk_norm_rope): RMS norm per query / key head (weights fp32 [128], None: no
+    norm), rotation of the first 2 * len(inv_freq) dims by the row's position, values
+    copied.
+
+    q_in [rows, Hq, 128], k_in, v_in [rows, Hkv, 128] fp32 or bf16, possibly views of one
+    fused projection; inv_freq fp32 [R / 2] or None; row_pos int32 [rows] (< 0: padding,
+    left as it is); n_rows int32 [1] or None: rows from there on are left as they are;
+    outputs bf16, dense.  v_in and v_new may be None."""
+    rows, Hq, _ = q.shape
+    Hkv = k_new.shape[1]
+    dt = _float_dtype(q_in, "q_in")
+    qp, qs = _rows(q_in, "q_in", rows, Hq, q_in.dtype)
+    kp, ks = _rows(k_in, "k_in", rows, Hkv, q_in.dtype)
+    if (v_in is None) != (v_new is None):
+        raise ValueError("v_in and v_new go together")
+    vp, vs = (None, 0) if v_in is None else _rows(v_in, "v_in", rows, Hkv, q_in.dtype)
+    f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
+    _check("dspark_qk_norm_rope", lib().dspark_qk_norm_rope(
+        qp, qs, kp, ks, vp, vs, dt,
+        None if q_weight is None else _arg(q_weight, "q_weight", f32, (128,)),
+        None if k_weight is None else _arg(k_weight, "k_weight", f32, (128,)), float(eps),
+        None if inv_freq is None else _arg(inv_freq, "inv_freq", f32),
+        0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
+        float(attn_factor), _arg(row_pos, "row_pos", i32, (rows,)),
+        None if n_rows is None else _arg(n_rows, "n_rows", i32, (1,)), rows, Hq, Hkv,
+        _arg(q, "q", bf16, (rows, Hq, 128)), _arg(k_new, "k_new", bf16, (rows, Hkv, 128)),
+        None if v_new is None else _arg(v_new, "v_new", bf16, (rows, Hkv, 128)), _stream(stream)))
+
+
+def kv4_cache(n_pages, Hkv, page_size, device="cuda"):
+    """A zeroed 4-bit cache: uint8 [n_pages, Hkv, page_size / 16, 2176] (layout: dspark.h)."""
+    page_size = int(page_size)
+    if page_size < 16 or page_size & (page_size - 1):
+        raise ValueError("page_size must be a power of two >= 16")
+    return torch.zeros(n_pages, Hkv, page_size // 16, KV4_BLOCK_BYTES, dtype=torch.uint8,
+                       device=torch.device(device))
+
+
+def _kv4(kv_cache, page_table, cu_seqlens):
+    """(cache address, n_pages, Hkv, page_size, table address, max_pages, B, cu address)."""
+    if kv_cache.dim() != 4 or kv_cache.shape[3] != KV4_BLOCK_BYTES:
+        raise ValueError("kv_cache: expected uint8 [n_pages, Hkv, page_size / 16, "
+                         f"{KV4_BLOCK_BYTES}]")
+    n_pages, Hkv, per, _ = kv_cache.shape
+    B = cu_seqlens.numel() - 1
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected [{B}, max_pages]")
+    i32 = torch.int32
+    return (_arg(kv_cache, "kv_cache", torch.uint8), n_pages, Hkv, per * 16,
+            _arg(page_table, "page_table", i32), page_table.shape[1], B,
+            _arg(cu_seqlens, "cu_seqlens", i32))
+
+
+def kv4_store(k, v, cu_seqlens, pos0, page_table, kv_cache, k_scale=1.0, v_scale=1.0, stream=None):
+    """Quantise packed rows into the 4-bit cache (dspark_kv4_store): row cu_seqlens[r] + i
+    of k, v [rows, Hkv, 128] (fp32 or bf16, possibly views of a fused projection) becomes
+    position pos0[r] + i of request r."""
+    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    rows = k.shape[0]
+    dt = _float_dtype(k, "k")
+    kp, ks = _rows(k, "k", rows, Hkv, k.dtype)
+    vp, vs = _rows(v, "v", rows, Hkv, k.dtype)
+    _check("dspark_kv4_store", lib().dspark_kv4_store(
+        kp, ks, vp, vs, dt, cu, _arg(pos0, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab,
+        max_pages, n_pages, float(k_scale), float(v_scale), c, _stream(stream)))
+
+
+def kv4_load(kv_cache, cu_seqlens, pos0, page_table, k, v, k_scale=1.0, v_scale=1.0, stream=None):
+    """Positions pos0[r] .. of every request back into packed rows k, v [rows, Hkv, 128]
+    (fp32 or bf16; dspark_kv4_load)."""
+    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    rows = k.shape[0]
+    dt = _float_dtype(k, "k")
+    _check("dspark_kv4_load", lib().dspark_kv4_load(
+        c, cu, _arg(pos0, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab, max_pages, n_pages,
+        float(k_scale), float(v_scale), dt, _arg(k, "k", k.dtype, (rows, Hkv, 128)),
+        _arg(v, "v", k.dtype, (rows, Hkv, 128)), _stream(stream)))
+
+
+def verify_attn_kv4_workspace_size(B, max_rows, Hq, Hkv, max_splits, max_block_rows=0) -> int:
+    return lib().dspark_verify_attn_kv4_workspace_size(B, max_rows, Hq, Hkv, max_splits,
+                                                       max_block_rows)
+
+
+def verify_attn_kv4(q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, scale, max_splits,
+                    out, lse, workspace, k_scale=1.0, v_scale=1.0, stream=None, max_block_rows=0):
+    """verify_attn over the 4-bit cache: q [rows, Hq, 128], k_new / v_new [rows, Hkv, 128]
+    bf16, kv_cache as kv4_cache gives it, out bf16 [rows, Hq, 128], lse fp32 [rows, Hq]."""
+    _verify_attn_kv4("dspark_verify_attn_kv4", q, k_new, v_new, kv_cache, page_table, ctx_len,
+                     cu_seqlens, scale, max_splits, out, lse, workspace, k_scale, v_scale, stream,
+                     max_block_rows)
+
+
+def verify_attn_kv4_planned(q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, scale,
+                            max_splits, out, lse, workspace, k_scale=1.0, v_scale=1.0, stream=None,
+                            max_block_rows=0):
+    """verify_attn_kv4 over the work list that pack_plan wrote into ``workspace``."""
+    _verify_attn_kv4("dspark_verify_attn_kv4_planned", q, k_new, v_new, kv_cache, page_table,
+                     ctx_len, cu_seqlens, scale, max_splits, out, lse, workspace, k_scale, v_scale,
+                     stream, max_block_rows)
+
+
+def _verify_attn_kv4(name, q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, scale,
+                     max_splits, out, lse, workspace, k_scale, v_scale, stream, max_block_rows):
+    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    rows, Hq, _ = q.shape
+    bf16 = torch.bfloat16
+    _check(name, getattr(lib(), name)(
+        _arg(q, "q", bf16, (rows, Hq, 128)), _arg(k_new, "k_new", bf16, (rows, Hkv, 128)),
+        _arg(v_new, "v_new", bf16, (rows, Hkv, 128)), c, float(k_scale), float(v_scale), n_pages,
+        tab, max_pages, _arg(ctx_len, "ctx_len", torch.int32, (B,)), cu, B, rows, Hq, Hkv, page,
+        float(scale), int(max_splits), int(max_block_rows), _arg(out, "out", bf16, (rows, Hq, 128)),
+        _arg(lse, "lse", torch.float32, (rows, Hq)), _arg(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream)))
+
+
+def compact_kv4(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table, ctx_len,
+                anchor, free_pages, free_top, kv_cache, committed, n_committed, workspace,
+                k_scale=1.0, v_scale=1.0, stream=None):
+    """compact into the 4-bit cache (dspark_compact_kv4)."""
+    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    gamma, rows = draft_tok.shape[1], k_new.shape[0]
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check("dspark_compact_kv4", lib().dspark_compact_kv4(
+        _arg(k_new, "k_new", bf16, (rows, Hkv, 128)), _arg(v_new, "v_new", bf16, (rows, Hkv, 128)),
+        Hkv, rows, cu, _arg(accept_len, "accept_len", i32, (B,)),
+        _arg(out_tok, "out_tok", i32, (B,)), _arg(draft_tok, "draft_tok", i32, (B, gamma)), B,
+        gamma, page, max_pages, n_pages, tab, _arg(ctx_len, "ctx_len", i32, (B,)),
+        _arg(anchor, "anchor", i32, (B,)), _arg(free_pages, "free_pages", i32),
+        _arg(free_top, "free_top", i32), c, float(k_scale), float(v_scale),
+        _arg(committed, "committed", i32, (B, gamma + 1)),
+        _arg(n_committed, "n_committed", i32, (B,)), _arg(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream)))
+
+
 class StepDesc(ctypes.Structure):
     """dspark_step_desc (field for field)."""
     _fields_ = (
@@ -429,6 +628,12 @@ def block_rows_hint_for(gamma, Hq, Hkv, mode) -> int:
     return gamma + 1
 
 
+def block_rows_hint_for_kv4(gamma, Hq, Hkv) -> int:
+    """Rows per request the query tile of the 4-bit cache's attention is sized for: the
+    block, as far as the largest tile (64 query rows) holds it."""
+    return min(gamma + 1, max(1, 64 // max(1, Hq // Hkv)))
+
+
 class VerifyStep:
     """Device buffers and workspaces for repeated verification steps of one shape.
 
@@ -438,15 +643,28 @@ class VerifyStep:
     (q, k_new, v_new, p_target) are read from the packed buffers the caller
     fills; state (caches, page table, ctx_len, anchor, free stack) is updated in
     place by compact.
+
+    With ``kv4`` the cache is the 4-bit one: ``inp["kv_cache"]`` (see kv4_cache), with
+    ``inp["k_scale"]`` and ``inp["v_scale"]`` (default 1), takes the place of k_cache and
+    v_cache, and ``out`` is bf16.
+
+    Where ``inp`` holds ``q_in``, ``k_in`` and ``v_in`` (the packed rows' projections), ``run``
+    fills q, k_new and v_new from them after the pack (``norm_rope``).
     """
 
     def __init__(self, B, gamma, Hq, Hkv, d_qk, d_v, vocab, max_rows, p_dtype=torch.float32,
-                 max_splits=8, device="cuda", block_rows_hint=None):
+                 max_splits=8, device="cuda", block_rows_hint=None, kv4=False):
+        self.kv4 = bool(kv4)
+        if self.kv4 and (d_qk != 128 or d_v != 128):
+            raise ValueError("the 4-bit cache holds heads of 128 dims")
         self.B, self.gamma, self.Hq, self.Hkv, self.d_qk, self.d_v = B, gamma, Hq, Hkv, d_qk, d_v
         self.vocab, self.max_rows, self.max_splits = vocab, max_rows, max_splits
         # the attention's query tile per mode (block_rows_hint); ``block_rows_hint``
         # fixes one hint for every mode
-        if block_rows_hint is None:
+        if block_rows_hint is None and self.kv4:
+            h = block_rows_hint_for_kv4(gamma, Hq, Hkv)
+            self._hints = {COMPACT: h, STATIC: h, CAP_ACCEPT: h}
+        elif block_rows_hint is None:
             self._hints = {m: block_rows_hint_for(gamma, Hq, Hkv, m)
                            for m in (COMPACT, STATIC, CAP_ACCEPT)}
         else:
@@ -466,7 +684,8 @@ class VerifyStep:
         self.row_req = torch.zeros(max_rows, **i32)
         self.row_pos = torch.zeros(max_rows, **i32)
         self.row_tok = torch.zeros(max_rows, **i32)
-        self.out = torch.zeros(max_rows, Hq, d_v, dtype=torch.float32, device=dev)
+        self.out = torch.zeros(max_rows, Hq, d_v, device=dev,
+                               dtype=torch.bfloat16 if self.kv4 else torch.float32)
         self.lse = torch.zeros(max_rows, Hq, dtype=torch.float32, device=dev)
         self.accept_len = torch.zeros(B, **i32)
         self.cap_len = torch.zeros(B, **i32)
@@ -476,8 +695,11 @@ class VerifyStep:
         self.committed = torch.zeros(B, gamma + 1, **i32)
         self.n_committed = torch.zeros(B, **i32)
         # sized for the smallest tile (the most work items)
-        sz = verify_attn_workspace_size(B, max_rows, Hq, Hkv, d_qk, d_v, max_splits,
-                                        min(self._hints.values()))
+        hint = min(self._hints.values())
+        if self.kv4:
+            sz = verify_attn_kv4_workspace_size(B, max_rows, Hq, Hkv, max_splits, hint)
+        else:
+            sz = verify_attn_workspace_size(B, max_rows, Hq, Hkv, d_qk, d_v, max_splits, hint)
         if sz == 0:
             raise ValueError("unsupported attention shape")
         self.ws_attn = torch.empty(sz, dtype=torch.uint8, device=dev)
@@ -496,7 +718,24 @@ class VerifyStep:
              self.cu_seqlens, self.M_pack, self.tier, self.row_req, self.row_pos, self.row_tok,
              stream)
 
+    def norm_rope(self, inp, stream=None):
+        """q, k_new, v_new of ``inp`` from q_in, k_in, v_in, at the positions of the last pack
+        (q_weight, k_weight, inv_freq, eps, interleaved, attn_factor as in qk_norm_rope)."""
+        qk_norm_rope(inp["q_in"], inp["k_in"], inp["v_in"], inp.get("q_weight"),
+                     inp.get("k_weight"), inp["inv_freq"], self.row_pos, inp["q"], inp["k_new"],
+                     inp["v_new"], inp.get("eps", 1e-6), inp.get("interleaved", False),
+                     inp.get("attn_factor", 1.0), stream, n_rows=self.M_pack)
+
+    def _attention_kv4(self, fn, inp, stream):
+        fn(inp["q"], inp["k_new"], inp["v_new"], inp["kv_cache"], inp["page_table"],
+           inp["ctx_len"], self.cu_seqlens, inp["scale"], self.max_splits, self.out, self.lse,
+           self.ws_attn, inp.get("k_scale", 1.0), inp.get("v_scale", 1.0), stream,
+           max_block_rows=self.block_rows_hint)
+
     def attention(self, inp, stream=None):
+        if self.kv4:
+            self._attention_kv4(verify_attn_kv4, inp, stream)
+            return
         verify_attn(inp["q"], inp["k_new"], inp.get("v_new"), inp["k_cache"], inp.get("v_cache"),
                     inp["page_table"], inp["ctx_len"], self.cu_seqlens, inp["scale"],
                     self.max_splits, self.out, self.lse, self.ws_attn, stream,
@@ -516,6 +755,9 @@ class VerifyStep:
                   self.max_splits, self.ws_attn, stream, max_block_rows=self.block_rows_hint)
 
     def attention_planned(self, inp, stream=None):
+        if self.kv4:
+            self._attention_kv4(verify_attn_kv4_planned, inp, stream)
+            return
         verify_attn_planned(inp["q"], inp["k_new"], inp.get("v_new"), inp["k_cache"],
                             inp.get("v_cache"), inp["page_table"], inp["ctx_len"],
                             self.cu_seqlens, inp["scale"], self.max_splits, self.out, self.lse,
@@ -527,6 +769,13 @@ class VerifyStep:
                self.cap_len, self.out_tok, self.cstar, self.fallback, self.ws_accept, stream)
 
     def compact(self, inp, stream=None):
+        if self.kv4:
+            compact_kv4(inp["k_new"], inp["v_new"], self.cu_seqlens, self.accept_len, self.out_tok,
+                        inp["draft_tok"], inp["page_table"], inp["ctx_len"], inp["anchor"],
+                        inp["free_pages"], inp["free_top"], inp["kv_cache"], self.committed,
+                        self.n_committed, self.ws_compact, inp.get("k_scale", 1.0),
+                        inp.get("v_scale", 1.0), stream)
+            return
         compact(inp["k_new"], inp.get("v_new"), self.cu_seqlens, self.accept_len, self.out_tok,
                 inp["draft_tok"], inp["page_table"], inp["ctx_len"], inp["anchor"],
                 inp["free_pages"], inp["free_top"], inp["k_cache"], inp.get("v_cache"),
@@ -536,7 +785,10 @@ class VerifyStep:
         """The step on these buffers and ``inp``'s tensors as a StepGraph (tier chosen
         on the device).  ``tier_host``: optional pinned host int32 word receiving each
         step's tier; ``body_log``: optional device int32 [1 + n] recording the body
-        index each launch ran (element 0 counts launches; the caller zeroes it)."""
+        index each launch ran (element 0 counts launches; the caller zeroes it).
+        The graph takes the bf16 cache only."""
+        if self.kv4:
+            raise ValueError("the step graph does not take the 4-bit cache")
         pdt = inp["p_target"].dtype
         tiers = inp["tiers"]
         tiers_dev = tiers.to(self.windows.device, torch.int32)
@@ -574,6 +826,8 @@ class VerifyStep:
     def run(self, inp, mode, stream=None):
         self.schedule(inp, mode, stream)
         self.pack_plan(inp, mode, stream)
+        if "q_in" in inp:
+            self.norm_rope(inp, stream)
         self.attention_planned(inp, stream)
         self.accept(inp, mode, stream)
         self.compact(inp, stream)

@@ -47,6 +47,8 @@ DeviceState* state() {
   return &st.value[dev];
 }
 
+constexpr int kMaxHeads = 1024;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -441,6 +443,185 @@ int dspark_markov_draft(const float* U, const void* W1, const void* W2, int rank
   CHECK(ws_bytes >= markov_workspace(V), DSPARK_ENOSPACE);
   return launch_markov_draft(U, W1, W2, anchor, exp_noise, B, gamma, V, draft_tok, p_draft,
                              workspace, static_cast<cudaStream_t>(stream));
+}
+
+// Rows of H heads of 128 elements: base and row stride on 16 bytes, rows not overlapping.
+static bool rows_ok(const void* p, long long stride, int H, int dtype) {
+  const int es = dtype == DSPARK_BF16 ? 2 : 4;
+  return aligned16(p) && stride >= (long long)H * 128 && (stride * es) % 16 == 0;
+}
+
+int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
+                        long long k_stride, const void* v_in, long long v_stride, int dtype,
+                        const float* q_weight, const float* k_weight, float eps,
+                        const float* inv_freq, int rotary_dim, int interleaved, float attn_factor,
+                        const int32_t* row_pos, const int32_t* n_rows, int rows, int Hq, int Hkv,
+                        void* q, void* k_new, void* v_new, void* stream) {
+  CHECK(q_in && k_in && row_pos && q && k_new, DSPARK_EINVAL);
+  CHECK((v_in == nullptr) == (v_new == nullptr), DSPARK_EINVAL);
+  CHECK(dtype == DSPARK_F32 || dtype == DSPARK_BF16, DSPARK_EINVAL);
+  CHECK(rows >= 1 && Hq >= 1 && Hkv >= 1 && Hq <= kMaxHeads && Hkv <= kMaxHeads, DSPARK_EINVAL);
+  CHECK(rotary_dim >= 0 && rotary_dim <= 128 && rotary_dim % 16 == 0, DSPARK_EUNSUPPORTED);
+  CHECK(rotary_dim == 0 || inv_freq, DSPARK_EINVAL);
+  CHECK(eps >= 0.f, DSPARK_EINVAL);
+  CHECK(rows_ok(q_in, q_stride, Hq, dtype) && rows_ok(k_in, k_stride, Hkv, dtype), DSPARK_EINVAL);
+  CHECK(!v_in || rows_ok(v_in, v_stride, Hkv, dtype), DSPARK_EINVAL);
+  CHECK(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(q_weight) &&
+            aligned16(k_weight),
+        DSPARK_EINVAL);
+  int rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  return launch_qk_norm_rope(q_in, q_stride, k_in, k_stride, v_in, v_stride, dtype, q_weight,
+                             k_weight, eps, inv_freq, rotary_dim, interleaved ? 1 : 0, attn_factor,
+                             row_pos, n_rows, rows, Hq, Hkv, q, k_new, v_new,
+                             static_cast<cudaStream_t>(stream));
+}
+
+static bool positive(float x) { return x > 0.f && x <= 3.402823466e38f; }  // finite, no NaN
+
+// What the 4-bit cache's calls have in common.
+static int kv4_args(const void* kv_cache, const int32_t* cu_seqlens, const int32_t* page_table,
+                    int B, int max_rows, int Hkv, int page_size, int max_pages, int n_pages,
+                    float k_scale, float v_scale) {
+  CHECK(kv_cache && cu_seqlens && page_table, DSPARK_EINVAL);
+  CHECK(aligned16(kv_cache), DSPARK_EINVAL);
+  CHECK(page_size >= 16 && (page_size & (page_size - 1)) == 0, DSPARK_EUNSUPPORTED);
+  CHECK(B >= 1 && B <= DSPARK_MAX_B && max_rows >= 1 && max_pages >= 1 && n_pages >= 1,
+        DSPARK_EINVAL);
+  CHECK(Hkv >= 1 && Hkv <= kMaxHeads, DSPARK_EINVAL);
+  CHECK((long long)max_rows * Hkv <= 0x7fffffffLL, DSPARK_EUNSUPPORTED);  // grid size
+  CHECK(positive(k_scale) && positive(v_scale), DSPARK_EINVAL);
+  return DSPARK_OK;
+}
+
+int dspark_kv4_store(const void* k, long long k_stride, const void* v, long long v_stride,
+                     int dtype, const int32_t* cu_seqlens, const int32_t* pos0, int B,
+                     int max_rows, int Hkv, int page_size, const int32_t* page_table,
+                     int max_pages, int n_pages, float k_scale, float v_scale, void* kv_cache,
+                     void* stream) {
+  int rc = kv4_args(kv_cache, cu_seqlens, page_table, B, max_rows, Hkv, page_size, max_pages,
+                    n_pages, k_scale, v_scale);
+  if (rc != DSPARK_OK) return rc;
+  CHECK(k && v && pos0, DSPARK_EINVAL);
+  CHECK(dtype == DSPARK_F32 || dtype == DSPARK_BF16, DSPARK_EINVAL);
+  CHECK(rows_ok(k, k_stride, Hkv, dtype) && rows_ok(v, v_stride, Hkv, dtype), DSPARK_EINVAL);
+  rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  return launch_kv4_store(k, k_stride, v, v_stride, dtype, cu_seqlens, pos0, nullptr, nullptr, B,
+                          max_rows, Hkv, page_size, page_table, max_pages, n_pages, k_scale,
+                          v_scale, kv_cache, static_cast<cudaStream_t>(stream));
+}
+
+int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32_t* pos0, int B,
+                    int max_rows, int Hkv, int page_size, const int32_t* page_table,
+                    int max_pages, int n_pages, float k_scale, float v_scale, int dtype, void* k,
+                    void* v, void* stream) {
+  int rc = kv4_args(kv_cache, cu_seqlens, page_table, B, max_rows, Hkv, page_size, max_pages,
+                    n_pages, k_scale, v_scale);
+  if (rc != DSPARK_OK) return rc;
+  CHECK(k && v && pos0, DSPARK_EINVAL);
+  CHECK(dtype == DSPARK_F32 || dtype == DSPARK_BF16, DSPARK_EINVAL);
+  CHECK(aligned16(k) && aligned16(v), DSPARK_EINVAL);
+  rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  return launch_kv4_load(kv_cache, cu_seqlens, pos0, B, max_rows, Hkv, page_size, page_table,
+                         max_pages, n_pages, k_scale, v_scale, dtype, k, v,
+                         static_cast<cudaStream_t>(stream));
+}
+
+// The attention's query tile over the 4-bit cache holds 64 rows at most.
+static int kv4_block_rows(int Hq, int Hkv, int max_block_rows) {
+  const int most = 64 / (Hq / Hkv);
+  return max_block_rows < most ? max_block_rows : most;
+}
+
+static bool kv4_heads_ok(int Hq, int Hkv) {
+  return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 64 && Hq <= kMaxHeads;
+}
+
+size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
+                                             int max_block_rows) {
+  if (B < 1 || max_rows < 1 || max_splits < 1 || max_splits > 32 || !kv4_heads_ok(Hq, Hkv)) return 0;
+  return attn::plan(B, max_rows, Hq, Hkv, 128, 128, max_splits,
+                    kv4_block_rows(Hq, Hkv, max_block_rows)).bytes;
+}
+
+static int verify_attn_kv4_impl(const void* q, const void* k_new, const void* v_new,
+                                const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                                const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                                const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
+                                int page_size, float scale, int max_splits, int max_block_rows,
+                                void* out, float* lse, void* workspace, size_t ws_bytes,
+                                void* stream, bool planned) {
+  CHECK(kv4_heads_ok(Hq, Hkv), DSPARK_EUNSUPPORTED);
+  int rc = kv4_args(kv_cache, cu_seqlens, page_table, B, max_rows, Hkv, page_size, max_pages,
+                    n_pages, k_scale, v_scale);
+  if (rc != DSPARK_OK) return rc;
+  CHECK(q && k_new && v_new && ctx_len && out && lse && workspace, DSPARK_EINVAL);
+  CHECK(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(out), DSPARK_EINVAL);
+  CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
+  CHECK(max_splits >= 1 && max_splits <= 32, DSPARK_EINVAL);
+  CHECK(positive(scale), DSPARK_EINVAL);
+  const int rows = kv4_block_rows(Hq, Hkv, max_block_rows);
+  CHECK(!planned || max_block_rows <= rows, DSPARK_EUNSUPPORTED);  // the pack call's tile
+  rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  const attn::Plan pl = attn::plan(B, max_rows, Hq, Hkv, 128, 128, max_splits, rows);
+  CHECK(ws_bytes >= pl.bytes, DSPARK_ENOSPACE);
+  return attn::kv4a::launch(q, k_new, v_new, kv_cache, n_pages, page_table, max_pages, ctx_len,
+                            cu_seqlens, B, max_rows, Hq, Hkv, page_size, scale, k_scale, v_scale,
+                            out, lse, static_cast<cudaStream_t>(stream));
+}
+
+int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
+                           const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                           const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                           const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
+                           int page_size, float scale, int max_splits, int max_block_rows,
+                           void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return verify_attn_kv4_impl(q, k_new, v_new, kv_cache, k_scale, v_scale, n_pages, page_table,
+                              max_pages, ctx_len, cu_seqlens, B, max_rows, Hq, Hkv, page_size,
+                              scale, max_splits, max_block_rows, out, lse, workspace, ws_bytes,
+                              stream, false);
+}
+
+int dspark_verify_attn_kv4_planned(const void* q, const void* k_new, const void* v_new,
+                                   const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                                   const int32_t* page_table, int max_pages,
+                                   const int32_t* ctx_len, const int32_t* cu_seqlens, int B,
+                                   int max_rows, int Hq, int Hkv, int page_size, float scale,
+                                   int max_splits, int max_block_rows, void* out, float* lse,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  return verify_attn_kv4_impl(q, k_new, v_new, kv_cache, k_scale, v_scale, n_pages, page_table,
+                              max_pages, ctx_len, cu_seqlens, B, max_rows, Hq, Hkv, page_size,
+                              scale, max_splits, max_block_rows, out, lse, workspace, ws_bytes,
+                              stream, true);
+}
+
+int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_rows,
+                       const int32_t* cu_seqlens, const int32_t* accept_len,
+                       const int32_t* out_tok, const int32_t* draft_tok, int B, int gamma,
+                       int page_size, int max_pages, int n_pages, int32_t* page_table,
+                       int32_t* ctx_len, int32_t* anchor, const int32_t* free_pages,
+                       int32_t* free_top, void* kv_cache, float k_scale, float v_scale,
+                       int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
+                       void* stream) {
+  int rc = kv4_args(kv_cache, cu_seqlens, page_table, B, max_rows, Hkv, page_size, max_pages,
+                    n_pages, k_scale, v_scale);
+  if (rc != DSPARK_OK) return rc;
+  CHECK(k_new && v_new && accept_len && out_tok && draft_tok && ctx_len && anchor && free_pages &&
+            free_top && committed && n_committed && workspace,
+        DSPARK_EINVAL);
+  CHECK(aligned16(k_new) && aligned16(v_new), DSPARK_EINVAL);
+  CHECK(gamma >= 1 && gamma <= DSPARK_MAX_GAMMA, DSPARK_EINVAL);
+  CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
+  rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  CHECK(ws_bytes >= compact_workspace(B), DSPARK_ENOSPACE);
+  return launch_compact_kv4(k_new, v_new, Hkv, max_rows, cu_seqlens, accept_len, out_tok, draft_tok,
+                            B, gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
+                            free_pages, free_top, kv_cache, k_scale, v_scale, committed,
+                            n_committed, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -174,4 +174,24 @@ int launch_compact(const void* k_new, const void* v_new, int row_bytes, int max_
   return DSPARK_OK;
 }
 
+int launch_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_rows,
+                       const int32_t* cu, const int32_t* accept_len, const int32_t* out_tok,
+                       const int32_t* draft_tok, int B, int gamma, int page_size, int max_pages,
+                       int n_pages, int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
+                       const int32_t* free_pages, int32_t* free_top, void* kv_cache, float gk,
+                       float gv, int32_t* committed, int32_t* n_committed, void* ws,
+                       cudaStream_t stream) {
+  CompactWs* cws = static_cast<CompactWs*>(ws);
+  int* old_ctx = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(CompactWs));
+  if (launch_pdl(compact_alloc_kernel, dim3(1), dim3(1024), 0, stream, cu, max_rows, accept_len,
+                 out_tok, draft_tok, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len,
+                 anchor, free_pages, free_top, committed, n_committed, cws, old_ctx,
+                 device_error_word()) != cudaSuccess)
+    return DSPARK_ECUDA;
+  const long long stride = (long long)Hkv * 128;
+  return launch_kv4_store(k_new, stride, v_new, stride, DSPARK_BF16, cu, old_ctx, accept_len,
+                          &cws->ok, B, max_rows, Hkv, page_size, page_table, max_pages, n_pages, gk,
+                          gv, kv_cache, stream);
+}
+
 }  // namespace dspark

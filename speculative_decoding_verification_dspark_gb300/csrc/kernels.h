@@ -99,4 +99,31 @@ int launch_compact(const void* k_new, const void* v_new, int row_bytes, int max_
                    void* k_cache, void* v_cache, int32_t* committed, int32_t* n_committed, void* ws,
                    cudaStream_t stream);
 
+// dspark_compact_kv4: the same allocation, the kept rows quantised into the 4-bit cache.
+int launch_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_rows,
+                       const int32_t* cu, const int32_t* accept_len, const int32_t* out_tok,
+                       const int32_t* draft_tok, int B, int gamma, int page_size, int max_pages,
+                       int n_pages, int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
+                       const int32_t* free_pages, int32_t* free_top, void* kv_cache, float gk,
+                       float gv, int32_t* committed, int32_t* n_committed, void* ws,
+                       cudaStream_t stream);
+
+int launch_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in, long long k_stride,
+                        const void* v_in, long long v_stride, int dtype, const float* q_weight,
+                        const float* k_weight, float eps, const float* inv_freq, int rotary_dim,
+                        int interleaved, float attn_factor, const int32_t* row_pos,
+                        const int32_t* n_rows, int rows, int Hq, int Hkv, void* q, void* k_new,
+                        void* v_new, cudaStream_t stream);
+
+// keep: rows 0 .. keep[r] of a segment are stored (nullable: all); ok: a device flag that
+// must be set for anything to be stored (nullable).
+int launch_kv4_store(const void* k, long long k_stride, const void* v, long long v_stride, int dtype,
+                     const int32_t* cu, const int32_t* pos0, const int32_t* keep, const int* ok,
+                     int B, int max_rows, int Hkv, int page_size, const int32_t* page_table,
+                     int max_pages, int n_pages, float gk, float gv, void* cache,
+                     cudaStream_t stream);
+int launch_kv4_load(const void* cache, const int32_t* cu, const int32_t* pos0, int B, int max_rows,
+                    int Hkv, int page_size, const int32_t* page_table, int max_pages, int n_pages,
+                    float gk, float gv, int dtype, void* k, void* v, cudaStream_t stream);
+
 }  // namespace dspark

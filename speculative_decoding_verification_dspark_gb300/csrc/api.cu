@@ -570,7 +570,8 @@ static int verify_attn_kv4_impl(const void* q, const void* k_new, const void* v_
   CHECK(ws_bytes >= pl.bytes, DSPARK_ENOSPACE);
   return attn::kv4a::launch(q, k_new, v_new, kv_cache, n_pages, page_table, max_pages, ctx_len,
                             cu_seqlens, B, max_rows, Hq, Hkv, page_size, scale, k_scale, v_scale,
-                            out, lse, static_cast<cudaStream_t>(stream));
+                            max_splits, out, lse, workspace, pl, static_cast<cudaStream_t>(stream),
+                            planned);
 }
 
 int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,

@@ -560,7 +560,8 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * largest may lose bits), block rows are rounded to fp16 after division by
  * 16 k_scale / 16 v_scale (saturating: |k_new| < 10^6 k_scale), the probabilities to
  * fp16; sums are fp32, and out is rounded once to bf16.
- * A page out of range sets DSPARK_DEVERR_BAD_INPUT; its keys then count as zero vectors.
+ * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
+ * undefined.
  *
  * dspark_verify_attn_kv4_planned runs over the work list that dspark_pack_plan wrote
  * (d_qk = d_v = 128, the same Hq, Hkv, max_rows, max_splits, max_block_rows and

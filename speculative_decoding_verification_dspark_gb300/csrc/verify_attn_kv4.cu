@@ -32,7 +32,10 @@
 //   warp 2       issues O += V^T P^T.  (Two issuers: an unrolled chain of 8 N = 32 products
 //                takes about 46 cycles a piece to issue, so 16 of them from one thread
 //                would take as long as the tile's share of HBM time.)
-//   warps 4-7    K: thread = key; per-thread cp.async ring, expansion into TMEM
+//   warp 3       copies cache tiles into a ring of shared memory: one bulk copy per run of
+//                blocks that lie together (a block where pages hold 16 tokens), each
+//                from a lane of its own
+//   warps 4-7    K: thread = key; codes from the ring, expanded into TMEM
 //   warps 8-11   V: warp = group of 32 channels, thread = channel; the same
 //   warps 12-15  softmax of columns 0..31, thread = key; epilogue, thread = channel
 //   warps 16-19  (64-column tile only) softmax of columns 32..63
@@ -63,14 +66,14 @@ using namespace dspark::kv4;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kKT = 128;               // keys per tile (MMA M)
-constexpr int kStages = 6;             // ring of cache tiles
-constexpr int kWarpSlot = 2 * kBlockBytes / 2;  // one warp's share of a tile: 2 KB codes + 128 B scales
-constexpr int kSlot = 8 * kWarpSlot;
+constexpr int kStages = 8;             // ring of cache tiles (a power of two)
+constexpr int kBlocks = kKT / kBlock;  // blocks of a tile
+constexpr int kStageBytes = kBlocks * kBlockBytes;
 constexpr int kSmemItems = 32;         // work items of a CTA kept in shared memory
-constexpr int kQkWarp = 0, kQWarp = 1, kPvWarp = 2, kKWarp0 = 4, kVWarp0 = 8, kSmWarp0 = 12;
+constexpr int kQkWarp = 0, kQWarp = 1, kPvWarp = 2, kCopyWarp = 3, kKWarp0 = 4, kVWarp0 = 8, kSmWarp0 = 12;
 constexpr float kRefDrop = 6.f;        // reference = maximum - 6 (log2)
 constexpr float kMove = 14.f;          // a key above reference + 14 moves it
-constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key
+constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key (`ref` holds the negatives)
 
 template <int NT_>
 struct Cfg {
@@ -85,14 +88,15 @@ struct Cfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_RING = OFF_P + 2 * P_BYTES;
-  static constexpr int OFF_VS = OFF_RING + kStages * kSlot;       // V scale pairs: [4 warps][512 B]
+  static constexpr int OFF_VS = OFF_RING + kStages * kStageBytes; // V scale pairs: [4 warps][512 B]
   static constexpr int OFF_CF = OFF_VS + 4 * 512;                 // float cf[2][NT]: softmax scale per row
   static constexpr int OFF_REF = OFF_CF + 2 * NT * 4;             // float ref[WGS][4][32]
   static constexpr int OFF_AL = OFF_REF + WGS * 512;              // float alpha[WGS][4][32]
   static constexpr int OFF_RED = OFF_AL + WGS * 512;              // float red[WGS][4][32]
-  static constexpr int OFF_ITEMS = OFF_RED + WGS * 512;
+  static constexpr int OFF_SUM = OFF_RED + WGS * 512;              // float sum[WGS][4][32]
+  static constexpr int OFF_ITEMS = OFF_SUM + WGS * 512;
   static constexpr int OFF_BAR = OFF_ITEMS + kSmemItems * (int)sizeof(AttnItem);
-  static constexpr int N_BARS = 18;
+  static constexpr int N_BARS = 18 + 2 * kStages;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int TMEM_S = 0, TMEM_O = 2 * NT, TMEM_K = 4 * NT, TMEM_V = 4 * NT + 128;
@@ -199,28 +203,38 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Asynchronous copies global -> shared; zeros where `ok` is false.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
   return h2_bits(__hfma2(bits_h2(a), bits_h2(b), bits_h2(c)));
 }
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, __half2 b) {
-  return h2_bits(__hmul2(bits_h2(a), b));
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  return h2_bits(__hmul2(bits_h2(a), bits_h2(b)));
+}
+// The expansion's constants as fp16 pairs: 1/16, 1/256, -64.5, -4.5.
+constexpr uint32_t kSixteenth = 0x2c002c00u, k256th = 0x1c001c00u, kBiasLow = 0xd408d408u,
+                   kBiasHigh = 0xc480c480u;
+// Two fp32 operations in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
   const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
@@ -284,80 +298,6 @@ __device__ __forceinline__ int visible_keys(int t, int ct, int ctx, int n_r) {
   return v < kKT ? v : kKT;
 }
 
-// The tiles of a CTA in order.
-struct TileIter {
-  int it, t, te, r, kvh, ctx, c0, n_r, ct;
-  bool fresh;  // t is the item's first tile here
-  __device__ __forceinline__ void start(const AttnItem* s, const AttnItem* g, int at, int begin) {
-    const AttnItem x = fetch_item(s, g, at, begin);
-    it = at; t = x.tb; te = x.te; r = x.r; kvh = x.kvh; ctx = x.ctx; c0 = x.c0; n_r = x.n_r;
-    ct = ceil_div(x.ctx, kKT);
-    fresh = true;
-  }
-};
-
-// Copies cache tiles into a warp's share of the ring, kStages - 1 ahead of their use, and
-// looks their pages up a window (32 blocks' worth of lanes) ahead.  BPT: blocks of a tile
-// that this warp reads (2 for K: its 32 keys; 8 for V: all of them).
-template <int BPT>
-struct Feeder {
-  static constexpr int kWin = 32 / BPT;  // tiles per window
-  const Params& p;
-  const AttnItem *s_items, *g_items;
-  int it_begin, it_end, lane, first_block;  // first block of a tile that this warp reads
-  TileIter c;           // the next tile to copy
-  bool more;
-  int win_t, win, nxt;  // window's first tile, this lane's page in it and in the next window
-
-  __device__ __forceinline__ int lookup(int r, int ctx, int t) const {
-    const int pos = (t + lane / BPT) * kKT + (first_block + lane % BPT) * kBlock;
-    if (pos >= ctx) return -1;
-    const int slot = pos >> p.log2_page;
-    const int page = slot < p.max_pages ? __ldg(p.page_table + (long long)r * p.max_pages + slot) : -1;
-    if (page < 0 || page >= p.n_pages) {
-      raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
-      return -1;
-    }
-    return page;
-  }
-  __device__ __forceinline__ void init() {
-    more = it_begin < it_end;
-    if (!more) return;
-    c.start(s_items, g_items, it_begin, it_begin);
-    nxt = lookup(c.r, c.ctx, c.t);
-  }
-  // Slice of block b (of this warp's BPT) of tile c.t; ok: it holds a committed key of a
-  // valid page.
-  __device__ __forceinline__ const uint8_t* block(int b, bool& ok) const {
-    const int page = __shfl_sync(0xffffffffu, win, (c.t - win_t) * BPT + b);
-    const int pos = c.t * kKT + (first_block + b) * kBlock;
-    const int per = 1 << (p.log2_page - 4);
-    ok = page >= 0;
-    return p.cache + (((long long)(ok ? page : 0) * p.Hkv + c.kvh) * per + ((pos >> 4) & (per - 1))) *
-                         kBlockBytes;
-  }
-  // Makes the window hold tile c.t and looks up the window after it.
-  __device__ __forceinline__ void window() {
-    if (c.fresh || c.t - win_t == kWin) {
-      win = nxt;
-      win_t = c.t;
-      if (c.t + kWin < c.te) {
-        nxt = lookup(c.r, c.ctx, c.t + kWin);
-      } else if (c.it + 1 < it_end) {
-        const AttnItem x = fetch_item(s_items, g_items, c.it + 1, it_begin);
-        nxt = lookup(x.r, x.ctx, x.tb);
-      }
-      c.fresh = false;
-    }
-  }
-  __device__ __forceinline__ void advance() {
-    if (++c.t == c.te) {
-      more = c.it + 1 < it_end;
-      if (more) c.start(s_items, g_items, c.it + 1, it_begin);
-    }
-  }
-};
-
 template <int NT>
 __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(const Params prm) {
   using C = Cfg<NT>;
@@ -382,6 +322,8 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
   auto q_full = [&](int b) { return bar(12 + b); };
   auto q_empty = [&](int b) { return bar(14 + b); };
   auto o_free = [&](int b) { return bar(16 + b); };
+  auto c_full = [&](int i) { return bar(18 + i); };             // ring of cache tiles
+  auto c_empty = [&](int i) { return bar(18 + kStages + i); };
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -395,6 +337,10 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
       mbar_init(q_full(b), 1);
       mbar_init(q_empty(b), 1 + 4 * C::WGS);
       mbar_init(o_free(b), 4 * C::WGS);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(c_full(i), 1);
+      mbar_init(c_empty(i), 8);
     }
     fence_mbar_init();
   }
@@ -524,64 +470,100 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             h[j] = h2_bits(__floats2half2_rn(__uint_as_float(w[j] << 16) * f,
                                              __uint_as_float(w[j] & 0xffff0000u) * f));
           st_shared_v4(qd + (l >> 3) * C::Q_CB + sw128_off(n, l & 7), make_uint4(h[0], h[1], h[2], h[3]));
-          if (l == 0) cf[n] = __uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2;
+          if (l == 0)  // (never 0: a masked score is -inf times it)
+            cf[n] = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2, 1.17549435e-38f);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(qb));
     }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------- cache tiles into the ring
+    // Lane j looks up and copies block j % 8 of tile j / 8 of a window of four; `nxt` is its
+    // page in the window after.  Blocks that lie together in a page go as one copy.
+    const int per = 1 << (prm.log2_page - 4);        // blocks of a page
+    const int run = min(per, kBlocks);               // blocks of a copy
+    const int lt = lane >> 3, lb = lane & 7;
+    auto lookup = [&](int r, int ctx, int t) -> int {
+      const int pos = (t + lt) * kKT + lb * kBlock;
+      const int slot = pos >> prm.log2_page;
+      if (pos >= ctx) return -1;
+      return slot < prm.max_pages ? __ldg(prm.page_table + (long long)r * prm.max_pages + slot) : -1;
+    };
+    int gc = 0, nxt = -1;
+    bool ok = true;
+    if (it_begin < it_end) {
+      const AttnItem x = fetch_item(s_items, prm.items, it_begin, it_begin);
+      nxt = lookup(x.r, x.ctx, x.tb);
+    }
+    for (int it = it_begin; it < it_end && ok; ++it) {
+      const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
+      const int te = min(item.te, ceil_div(item.ctx, kKT));  // cache tiles of the item
+      for (int t0 = item.tb; t0 < item.te && ok; t0 += 4) {
+        int page = nxt;
+        if (t0 + 4 < item.te) {
+          nxt = lookup(item.r, item.ctx, t0 + 4);
+        } else if (it + 1 < it_end) {
+          const AttnItem x = fetch_item(s_items, prm.items, it + 1, it_begin);
+          nxt = lookup(x.r, x.ctx, x.tb);
+        }
+        const int pos = (t0 + lt) * kKT + lb * kBlock;
+        const bool want = pos < item.ctx && t0 + lt < te;
+        const bool valid = want && page >= 0 && page < prm.n_pages;
+        if (want && !valid) raise_error(prm.err, DSPARK_DEVERR_BAD_INPUT);
+        // this lane's copy: `run` blocks from its own, as far as the context reaches
+        const int nb = min(run, ceil_div(item.ctx - pos, kBlock));
+        const uint32_t bytes = valid && lb % run == 0 ? (uint32_t)(nb * kBlockBytes) : 0u;
+        const uint8_t* src = prm.cache + (((long long)(valid ? page : 0) * prm.Hkv + item.kvh) * per +
+                                          ((pos >> 4) & (per - 1))) * kBlockBytes;
+        uint32_t total = bytes;                      // of the lane's tile
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        for (int i = 0; i < 4 && t0 + i < te; ++i, ++gc) {
+          const int st = gc & (kStages - 1);
+          if (gc >= kStages) {
+            ok = wait_warp(c_empty(st), ((gc / kStages) - 1) & 1, cx);
+            if (!ok) break;
+          }
+          if (lane == 8 * i) mbar_arrive_expect_tx(c_full(st), total);
+          __syncwarp();
+          if (lt == i && bytes)
+            bulk_load_g2s(base + C::OFF_RING + st * kStageBytes + lb * kBlockBytes, src, bytes, c_full(st));
+        }
+      }
+    }
+    // no copy may be in flight when the CTA ends
+    for (int x = max(gc - kStages, 0); x < gc; ++x)
+      if (lane == 0) drain_bar(c_full(x & (kStages - 1)), (x / kStages) & 1, prm.err);
   } else if (warp >= kKWarp0 && warp < kVWarp0) {
     // ------------------------------------------------------------- K: thread = key
     const int w = warp - kKWarp0, kl = w * 32 + lane;
-    const uint32_t ring = base + C::OFF_RING + w * kWarpSlot;
+    // this key's codes and scales within a stage
+    const uint32_t ring = base + C::OFF_RING + (2 * w + (lane >> 4)) * kBlockBytes;
+    const uint32_t codes = ring + (lane & 15) * 16, scales = ring + kOffKs + (lane & 15) * 4;
     const uint32_t t_k = tmem + (static_cast<uint32_t>(w * 32) << 16) + C::TMEM_K;
-    Feeder<2> f{prm, s_items, prm.items, it_begin, it_end, lane, 2 * w};
-    f.init();
-    int slot_in = 0;
-    auto feed = [&]() {  // the next tile's codes [4 groups][lane][16 B], then scales [lane][4 B]
-      if (f.more) {
-        f.window();
-        if (f.c.t < f.c.ct) {
-          bool ok;
-          const uint8_t* blk = f.block(lane >> 4, ok);
-          const uint32_t dst = ring + slot_in * kSlot;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            cp16(dst + c * 512 + lane * 16, blk + c * 256 + (lane & 15) * 16, ok);
-          cp4(dst + 2048 + lane * 4, blk + kOffKs + (lane & 15) * 4, ok);
-        }
-        f.advance();
-      }
-      cp_commit();
-      if (++slot_in == kStages) slot_in = 0;
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) feed();
-    int g = 0, slot = 0;
+    int g = 0, gc = 0;
     bool ok = true;
     for (int it = it_begin; it < it_end && ok; ++it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
       const int ct = ceil_div(item.ctx, kKT);
       for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1;
-        feed();
-        cp_wait<kStages - 1>();
-        if (g >= 2) ok = wait_warp(s_full(b), ((g >> 1) - 1) & 1, cx);  // QK^T of tile g - 2 done
+        const int b = g & 1, st = gc & (kStages - 1);
+        if (t < ct) ok = wait_warp(c_full(st), (gc / kStages) & 1, cx);
+        if (ok && g >= 2) ok = wait_warp(s_full(b), ((g >> 1) - 1) & 1, cx);  // QK^T of tile g - 2 done
         if (!ok) break;
         tc_fence_after();
         if (t < ct) {
-          const uint32_t src = ring + slot * kSlot;
-          const uint32_t sc = ld_shared(src + 2048 + lane * 4);
+          const uint32_t src = codes + st * kStageBytes;
+          const uint32_t sc = ld_shared(scales + st * kStageBytes);
           const uint32_t s01 = e4m3x2_to_h2(sc & 0xffffu), s23 = e4m3x2_to_h2(sc >> 16);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const uint4 v = ld_shared_v4(src + c * 512 + lane * 16);
+            const uint4 v = ld_shared_v4(src + c * 256);
             const uint32_t s = __byte_perm(c < 2 ? s01 : s23, 0, (c & 1) ? 0x3232 : 0x1010);
-            const uint32_t sl = hmul2_bits(s, __float2half2_rn(0.0625f));
-            const uint32_t bl = hmul2_bits(s, __float2half2_rn(-64.5f));
-            const uint32_t sh = hmul2_bits(s, __float2half2_rn(0.00390625f));
-            const uint32_t bh = hmul2_bits(s, __float2half2_rn(-4.5f));
+            const uint32_t sl = hmul2_bits(s, kSixteenth), bl = hmul2_bits(s, kBiasLow);
+            const uint32_t sh = hmul2_bits(s, k256th), bh = hmul2_bits(s, kBiasHigh);
             const uint32_t ss[4] = {sl, sh, sl, sh}, bb[4] = {bl, bh, bl, bh};
             uint32_t o[16];
             expand(v.x, ss, bb, o);
@@ -590,18 +572,25 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             expand(v.w, ss, bb, o + 12);
             tmem_st16u(t_k + b * 64 + c * 16, o);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c_empty(st));
+          ++gc;
         } else {
           // the request's own rows: bf16 / (16 k_scale)
           const int bi = (t - ct) * kKT + kl;
           const __nv_bfloat16* src = prm.k_new + ((long long)(item.c0 + bi) * prm.Hkv + item.kvh) * kD;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = make_uint4(0, 0, 0, 0);
+              if (bi < item.n_r) v[j] = reinterpret_cast<const uint4*>(src)[c * 4 + j];
+            }
             uint32_t o[16];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (bi < item.n_r) v = reinterpret_cast<const uint4*>(src)[c * 4 + j];
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 o[4 * j + q] = pack16(__uint_as_float(x[q] << 16) * prm.k_unit,
@@ -614,105 +603,75 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full(b));
-        if (++slot == kStages) slot = 0;
       }
     }
-    cp_wait<0>();
   } else if (warp >= kVWarp0 && warp < kSmWarp0) {
     // ------------------------------------------------------------- V: thread = channel
     const int w = warp - kVWarp0;
-    const uint32_t ring = base + C::OFF_RING + (4 + w) * kWarpSlot;
+    const uint32_t ring = base + C::OFF_RING;
+    const uint32_t codes = ring + kOffV + (w * 32 + lane) * 8;
+    const uint32_t scales = ring + (lane >> 2) * kBlockBytes + kOffVs + w * kBlock + (lane & 3) * 4;
     const uint32_t vs = base + C::OFF_VS + w * 512;
     const uint32_t t_v = tmem + (static_cast<uint32_t>(w * 32) << 16) + C::TMEM_V;
-    Feeder<8> f{prm, s_items, prm.items, it_begin, it_end, lane, 0};
-    f.init();
-    int slot_in = 0;
-    auto feed = [&]() {  // codes [8 blocks][32 channels][8 B], then scales [8 blocks][16 B]
-      if (f.more) {
-        f.window();
-        if (f.c.t < f.c.ct) {
-          const uint32_t dst = ring + slot_in * kSlot;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bool ok;
-            const uint8_t* blk = f.block(2 * i + (lane >> 4), ok);
-            cp16(dst + i * 512 + lane * 16, blk + kOffV + w * 256 + (lane & 15) * 16, ok);
-          }
-          bool ok;
-          const uint8_t* blk = f.block(lane & 7, ok);
-          if (lane < 8) cp16(dst + 2048 + lane * 16, blk + kOffVs + w * kBlock, ok);
-        }
-        f.advance();
-      }
-      cp_commit();
-      if (++slot_in == kStages) slot_in = 0;
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) feed();
-    int g = 0, slot = 0;
+    int g = 0, gc = 0;
     bool ok = true;
     for (int it = it_begin; it < it_end && ok; ++it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
       const int ct = ceil_div(item.ctx, kKT);
       for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1;
-        __syncwarp();  // every lane has read the slot that is filled next
-        feed();
-        cp_wait<kStages - 1>();
-        __syncwarp();
+        const int b = g & 1, st = gc & (kStages - 1);
         const int vis = visible_keys(t, ct, item.ctx, item.n_r);
-        const int nch = ceil_div(vis, 16);
-        const uint32_t src = ring + slot * kSlot;
+        const int np = ceil_div(vis, 32);  // pairs of blocks that hold a visible key
         if (t < ct) {
+          ok = wait_warp(c_full(st), (gc / kStages) & 1, cx);
           // scale pairs of the tile's keys 4 lane .. + 3, shared by the warp's channels; keys
           // past the context get scale 0, whatever their page holds
-          uint32_t sc = ld_shared(src + 2048 + lane * 4);
+          uint32_t sc = ld_shared(scales + st * kStageBytes);
           const int left = vis - 4 * lane;
           if (left < 4) sc = left <= 0 ? 0u : sc & ((1u << (8 * left)) - 1u);
           const uint32_t s0 = e4m3x2_to_h2(sc & 0xffffu), s1 = e4m3x2_to_h2(sc >> 16);
           const uint32_t at = vs + (lane >> 1) * 32 + (lane & 1) * 8;
-          st_shared_v2(at, hmul2_bits(s0, __float2half2_rn(0.0625f)),
-                       hmul2_bits(s1, __float2half2_rn(0.00390625f)));
-          st_shared_v2(at + 16, hmul2_bits(s0, __float2half2_rn(-64.5f)),
-                       hmul2_bits(s1, __float2half2_rn(-4.5f)));
+          st_shared_v2(at, hmul2_bits(s0, kSixteenth), hmul2_bits(s1, k256th));
+          st_shared_v2(at + 16, hmul2_bits(s0, kBiasLow), hmul2_bits(s1, kBiasHigh));
+          __syncwarp();
         }
-        __syncwarp();
-        if (g >= 2) ok = wait_warp(pv_done(b), ((g >> 1) - 1) & 1, cx);  // PV of tile g - 2 done
+        if (ok && g >= 2) ok = wait_warp(pv_done(b), ((g >> 1) - 1) & 1, cx);  // PV of tile g - 2 done
         if (!ok) break;
         tc_fence_after();
         if (t < ct) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (2 * i >= nch) break;
+          const uint32_t src = codes + st * kStageBytes;
+#pragma unroll 1
+          for (int i = 0; i < np; ++i) {
             uint32_t o[16];
+            const uint2 v0 = ld_shared_v2(src + 2 * i * kBlockBytes);
+            const uint2 v1 = ld_shared_v2(src + (2 * i + 1) * kBlockBytes);
+            const uint32_t word[4] = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint2 v = ld_shared_v2(src + (2 * i + j) * 256 + lane * 8);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t at = vs + ((2 * i + j) * 2 + h) * 32;
-                const uint4 s = ld_shared_v4(at), c = ld_shared_v4(at + 16);
-                const uint32_t ss[4] = {s.x, s.y, s.z, s.w}, bb[4] = {c.x, c.y, c.z, c.w};
-                expand(h ? v.y : v.x, ss, bb, o + j * 8 + h * 4);
-              }
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t at = vs + (4 * i + j) * 32;
+              const uint4 s = ld_shared_v4(at), c = ld_shared_v4(at + 16);
+              const uint32_t ss[4] = {s.x, s.y, s.z, s.w}, bb[4] = {c.x, c.y, c.z, c.w};
+              expand(word[j], ss, bb, o + j * 4);
             }
             tmem_st16u(t_v + b * 64 + i * 16, o);
           }
+          __syncwarp();  // (also: every lane has read the scale pairs)
+          if (lane == 0) mbar_arrive(c_empty(st));
+          ++gc;
         } else {
           const int b0 = (t - ct) * kKT;
           const __nv_bfloat16* vn = prm.v_new + ((long long)(item.c0 + b0) * prm.Hkv + item.kvh) * kD +
                                     w * 32 + lane;
 #pragma unroll 1
-          for (int i = 0; 2 * i < nch; ++i) {
+          for (int i = 0; i < np; ++i) {
+            const long long step = (long long)prm.Hkv * kD;
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = 32 * i + j < vis ? __bfloat162float(vn[(32 * i + j) * step]) : 0.f;
             uint32_t o[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int k = 32 * i + 2 * j;
-              const long long step = (long long)prm.Hkv * kD;
-              const float x = k < vis ? __bfloat162float(vn[k * step]) * prm.v_unit : 0.f;
-              const float y = k + 1 < vis ? __bfloat162float(vn[(k + 1) * step]) * prm.v_unit : 0.f;
-              o[j] = pack16(x, y);
-            }
+            for (int j = 0; j < 16; ++j) o[j] = pack16(x[2 * j] * prm.v_unit, x[2 * j + 1] * prm.v_unit);
             tmem_st16u(t_v + b * 64 + i * 16, o);
           }
         }
@@ -720,10 +679,8 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full(b));
-        if (++slot == kStages) slot = 0;
       }
     }
-    cp_wait<0>();
   } else if (warp >= kSmWarp0) {
     // ------------------------------------------------------------- softmax and epilogue
     const int sw = warp & 3, wg = (warp - kSmWarp0) >> 2;
@@ -733,6 +690,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
     float* ref = reinterpret_cast<float*>(bp + C::OFF_REF) + (wg * 4 + sw) * 32;   // this warp's copy
     float* alpha = reinterpret_cast<float*>(bp + C::OFF_AL) + (wg * 4 + sw) * 32;
     float* red = reinterpret_cast<float*>(bp + C::OFF_RED) + wg * 128;             // [4 warps][32]
+    float* sums = reinterpret_cast<float*>(bp + C::OFF_SUM) + wg * 128;
     int g = 0, n_it = 0;
     bool bad = false;                            // a wait ran out
     for (int it = it_begin; it < it_end; ++it, ++n_it) {
@@ -772,27 +730,68 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
         }
         const uint32_t s_col = t_lane + C::TMEM_S + b * NT;
         const uint32_t prow = base + C::OFF_P + b * C::P_BYTES;
-        // P of this key against the current references; returns whether a key lies so far
-        // above its row's that it has to move
+        const bool masked = t >= ct || (t + 1) * kKT > ctx;  // some key is not seen by all rows
         float x[32];
-        auto probabilities = [&]() -> bool {
-          bool over = false;
+        auto scores = [&]() {
           tmem_ld32(s_col, x);
           tmem_wait_ld32(x);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = nmin <= k ? x[k] : -INFINITY;
+          }
+        };
+        bool move = t == item.tb;  // the references have to move first
+        for (;;) {
+          if (move) {
+            // ---- the tile's maximum per row, over the group's warps
+            scores();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] *= cf[k];
+            red[sw * 32 + lane] = transpose_reduce<true>(x, lane);
+            // O^T holds the products up to tile g - 1 before it is rescaled
+            if (t > item.tb) bad |= !wait_warp(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, cx);
+            if (group_or(bar_id, bad)) goto done;
+            const float tm = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
+            float al = 1.f;
+            if (tm - kRefDrop > mref + (kMove - kRefDrop)) {
+              al = mref == -INFINITY ? 0.f : fast_exp2(mref - (tm - kRefDrop));
+              mref = tm - kRefDrop;
+            }
+            __syncwarp();
+            ref[lane] = mref == -INFINITY ? -kNoRef : -mref;
+            alpha[lane] = al;
+            __syncwarp();
+            if (t > item.tb) {
+              tc_fence_after();
+              const uint32_t t_o = t_lane + C::TMEM_O + (n_it & 1) * NT;
+              tmem_ld32(t_o, x);
+              tmem_wait_ld32(x);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                lacc[k] *= alpha[k];
+                x[k] *= alpha[k];
+              }
+              tmem_st32(t_o, x);
+              tmem_wait_st();
+              tc_fence_before();
+            }
+          }
+          // ---- P of this key against the references
+          scores();
+          float top = -INFINITY;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (q >= nc8) break;
             uint32_t pk[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              const int k = q * 8 + h * 4;
               const float4 c4 = reinterpret_cast<const float4*>(cf)[q * 2 + h];
               const float4 r4 = reinterpret_cast<const float4*>(ref)[q * 2 + h];
-              const int k = q * 8 + h * 4;
-              x[k] = nmin <= k ? fmaf(x[k], c4.x, -r4.x) : -INFINITY;
-              x[k + 1] = nmin <= k + 1 ? fmaf(x[k + 1], c4.y, -r4.y) : -INFINITY;
-              x[k + 2] = nmin <= k + 2 ? fmaf(x[k + 2], c4.z, -r4.z) : -INFINITY;
-              x[k + 3] = nmin <= k + 3 ? fmaf(x[k + 3], c4.w, -r4.w) : -INFINITY;
-              over |= x[k] > kMove || x[k + 1] > kMove || x[k + 2] > kMove || x[k + 3] > kMove;
+              unpack(fma2(f2(x[k], x[k + 1]), f2(c4.x, c4.y), f2(r4.x, r4.y)), x[k], x[k + 1]);
+              unpack(fma2(f2(x[k + 2], x[k + 3]), f2(c4.z, c4.w), f2(r4.z, r4.w)), x[k + 2], x[k + 3]);
+              top = fmaxf(top, fmaxf(x[k], x[k + 1]));
+              top = fmaxf(top, fmaxf(x[k + 2], x[k + 3]));
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[k + j] = fast_exp2(x[k + j]);
               pk[2 * h] = h2_bits(__floats2half2_rn(x[k], x[k + 1]));
@@ -802,47 +801,13 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             st_shared_v4(prow + off, make_uint4(pk[0], pk[1], pk[2], pk[3]));
           }
           fence_proxy_async_smem();
-          return over;
-        };
-        bool over = true;
-        if (t > item.tb) over = probabilities();
-        if (group_or(bar_id, over || bad)) {
-          // ---- references move: the tile's maximum per row, over the group's warps
-          tmem_ld32(s_col, x);
-          tmem_wait_ld32(x);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = nmin <= k ? x[k] * cf[k] : -INFINITY;
-          red[sw * 32 + lane] = transpose_reduce<true>(x, lane);
-          // O^T holds the products up to tile g - 1 before it is rescaled
-          if (t > item.tb) bad |= !wait_warp(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, cx);
+          // all of P is written when the group passes; a key far above its row's reference
+          // sends the tile through once more, after the references have moved
+          const bool again = group_or(bar_id, top > kMove || bad);
+          if (!again) break;
           if (group_or(bar_id, bad)) goto done;
-          const float tm = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
-          float al = 1.f;
-          if (tm - kRefDrop > mref + (kMove - kRefDrop)) {
-            al = mref == -INFINITY ? 0.f : fast_exp2(mref - (tm - kRefDrop));
-            mref = tm - kRefDrop;
-          }
-          __syncwarp();
-          ref[lane] = mref == -INFINITY ? kNoRef : mref;
-          alpha[lane] = al;
-          __syncwarp();
-          if (t > item.tb) {
-            tc_fence_after();
-            const uint32_t t_o = t_lane + C::TMEM_O + (n_it & 1) * NT;
-            tmem_ld32(t_o, x);
-            tmem_wait_ld32(x);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              lacc[k] *= alpha[k];
-              x[k] *= alpha[k];
-            }
-            tmem_st32(t_o, x);
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          probabilities();
-          // all of P is written, and `red` read, when the group passes
-          if (group_or(bar_id, bad)) goto done;
+          if (move) break;
+          move = true;
         }
         tc_fence_before();
         __syncwarp();
@@ -852,15 +817,16 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
         for (int q = 0; q < 4; ++q) {
           if (q >= nc8) break;
 #pragma unroll
-          for (int k = q * 8; k < q * 8 + 8; ++k) lacc[k] += x[k];
+          for (int k = q * 8; k < q * 8 + 8; k += 2)
+            unpack(add2(f2(lacc[k], lacc[k + 1]), f2(x[k], x[k + 1])), lacc[k], lacc[k + 1]);
         }
       }
       if (nq > 0) {
         // ---- epilogue: row sums over the group, O^T / l
-        red[sw * 32 + lane] = transpose_reduce<false>(lacc, lane);
+        sums[sw * 32 + lane] = transpose_reduce<false>(lacc, lane);
         bad |= !wait_warp(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, cx);
         if (group_or(bar_id, bad)) goto done;
-        const float l = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
+        const float l = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
         const bool split = item.nsplit > 1;
         alpha[lane] = l == 0.f ? 0.f : prm.o_unit / l;
         const long long row0 = (long long)item.c0 + item.i0;
@@ -896,7 +862,6 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             }
           }
         }
-        // `red` is written next after the group's barriers of the next item's first tile
       }
       tc_fence_before();
       __syncwarp();

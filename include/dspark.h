@@ -551,10 +551,10 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * v_new are bf16 as there.  Arguments as dspark_verify_attn, with kv_cache, k_scale
  * and v_scale in place of the two caches, and
  *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
- *   Hq / Hkv <= 64
- *   max_block_rows: the query tile holds 32 rows of G = Hq / Hkv heads x block rows,
- *        or 64 where G x max_block_rows is above 32; longer segments run as several
- *        row tiles.
+ *   Hq / Hkv <= 32
+ *   max_block_rows has no effect but in the planned form: the query tile holds 32 rows
+ *        (32 / G block rows of G = Hq / Hkv heads), longer segments run as several row
+ *        tiles.
  * Rounding: the cached values and the queries are exact in the products' fp16
  * operands (a query row is scaled by a power of two; elements below 2^-30 of the row's
  * largest may lose bits), block rows are rounded to fp16 after division by
@@ -565,7 +565,8 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  *
  * dspark_verify_attn_kv4_planned runs over the work list that dspark_pack_plan wrote
  * (d_qk = d_v = 128, the same Hq, Hkv, max_rows, max_splits, max_block_rows and
- * workspace); DSPARK_EUNSUPPORTED if G x max_block_rows is above 64.
+ * workspace); DSPARK_EUNSUPPORTED if max_block_rows is above 32 / G, the rows of this
+ * kernel's tile.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
                                              int max_block_rows);

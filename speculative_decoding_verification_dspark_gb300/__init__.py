@@ -630,8 +630,8 @@ def block_rows_hint_for(gamma, Hq, Hkv, mode) -> int:
 
 def block_rows_hint_for_kv4(gamma, Hq, Hkv) -> int:
     """Rows per request the query tile of the 4-bit cache's attention is sized for: the
-    block, as far as the largest tile (64 query rows) holds it."""
-    return min(gamma + 1, max(1, 64 // max(1, Hq // Hkv)))
+    block, as far as the tile (32 query rows) holds it."""
+    return min(gamma + 1, max(1, 32 // max(1, Hq // Hkv)))
 
 
 class VerifyStep:

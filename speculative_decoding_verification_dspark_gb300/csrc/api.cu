@@ -529,14 +529,14 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
                          static_cast<cudaStream_t>(stream));
 }
 
-// The attention's query tile over the 4-bit cache holds 64 rows at most.
+// The attention's query tile over the 4-bit cache holds 32 rows.
 static int kv4_block_rows(int Hq, int Hkv, int max_block_rows) {
-  const int most = 64 / (Hq / Hkv);
+  const int most = 32 / (Hq / Hkv);
   return max_block_rows < most ? max_block_rows : most;
 }
 
 static bool kv4_heads_ok(int Hq, int Hkv) {
-  return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 64 && Hq <= kMaxHeads;
+  return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 32 && Hq <= kMaxHeads;
 }
 
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,

@@ -5,13 +5,13 @@
 //   (code - 8) * scale * g, followed by block rows 0..i (bf16); lse = log-sum-exp.
 //
 // As in the bf16 cache's kernel, keys lie on the MMA's M side and the few query rows on
-// N (NT = 32 or 64 columns), and the key tiles of all groups are cut into equal ranges, one per
-// CTA (worklist.cuh):
-//   S^T [128 keys x NT] = K [128 x 128] . Q^T        O^T [128 d x NT] += V^T [128 x 128] . P^T
+// N (32 columns), and the key tiles of all groups are cut into equal ranges, one per CTA
+// (worklist.cuh):
+//   S^T [128 keys x 32] = K [128 x 128] . Q^T        O^T [128 d x 32] += V^T [128 x 128] . P^T
 // The left operands are in tensor memory: a lane of K is a key and a lane of V^T a channel,
-// so the thread that reads a key's (a channel's) codes expands them and writes its own
-// lane.  Through shared memory the expanded tile would cost 64 KB of writes and 64 KB
-// of MMA reads per 17 KB of cache, more than the SM's share of HBM time.
+// and the threads that read codes expand them and write their lanes.  Through shared memory
+// the expanded tile would cost 64 KB of writes and 64 KB of MMA reads per 17 KB of cache,
+// more than the SM's share of HBM time.
 //
 // Expansion, exact in fp16: a masked pair of nibbles in the mantissa of 1024 (0x6400) is
 // 1024 + c (1024 + 16 c for the high nibbles), and one fused multiply-add gives
@@ -26,25 +26,34 @@
 // bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
 // down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
 //
-// Warp roles (one CTA per SM):
-//   warp 0       issues S = K Q^T (one lane); owns the TMEM allocation
-//   warp 1       query loader: the next item's rows into the other Q buffer
-//   warp 2       issues O += V^T P^T.  (Two issuers: an unrolled chain of 8 N = 32 products
-//                takes about 46 cycles a piece to issue, so 16 of them from one thread
-//                would take as long as the tile's share of HBM time.)
-//   warp 3       copies cache tiles into a ring of shared memory: one bulk copy per run of
-//                blocks that lie together (a block where pages hold 16 tokens), each
-//                from a lane of its own
-//   warps 4-7    K: thread = key; codes from the ring, expanded into TMEM
-//   warps 8-11   V: warp = group of 32 channels, thread = channel; the same
-//   warps 12-15  softmax of columns 0..31, thread = key; epilogue, thread = channel
-//   warps 16-19  (64-column tile only) softmax of columns 32..63
-// The softmax takes a tile in one pass against the row references of the tiles before; only
-// if some key lies 2^8 above its row's maximum then (always in an item's first tile)
-// does the tile go through the pass that moves references and rescales O.  Row sums stay in
-// the threads (each sums its own keys) until the item ends.
-// Every wait on an mbarrier is bounded in time (DSPARK_DEVERR_WAIT_TIMEOUT on expiry); a
-// softmax warpgroup's own barriers carry the failure, so its warps leave together.
+// What bounds it is not HBM but instructions: about a thousand per tile and scheduler
+// against 850 cycles of HBM time, most of them in chains of one warp, which issues one
+// in five or six cycles.  So every role is there twice and the CTA runs two streams, of the
+// even and of the odd tiles, each a softmax of its own (references, sums, O^T) that meet
+// at the end of an item.
+//
+// Warp roles (one CTA per SM; stream x = tiles of parity x):
+//   warps 0, 1    issue S^T of stream 0, 1 (one lane)
+//   warps 2, 3    issue O^T of stream 0, 1
+//   warp 4        copies cache tiles into a ring of shared memory: one bulk copy per run
+//                 of blocks that lie together (a block where pages hold 16 tokens), each
+//                 from a lane of its own; owns the TMEM allocation
+//   warp 5        query loader: the next item's rows into the other Q buffer
+//   warps 8-15    K of stream 0, 1: thread = key; codes from the ring, expanded into TMEM
+//   warps 16-23   V of stream 0, 1: warp = group of 32 channels.  A thread expands four
+//                 channels (of every eighth) for a quarter of the tile's keys, so that the
+//                 scales it reads (one per key and 32 channels) serve four words of codes.
+//                 The products' key order is the one this gives: column pair 8 e + 2 q + i of
+//                 V^T holds keys 32 q + 4 e + 2 i, + 1, and P is written in the same order
+//   warps 24-31   softmax of stream 0, 1: thread = key; epilogue, thread = channel, 16 of
+//                 the columns per stream's warps
+// The softmax needs more registers than the launch gives a thread; the others hand theirs over.
+// It takes a tile in one pass against its stream's row references; only if some key lies
+// 2^8 above its row's maximum then (always in the stream's first tile of an item) does
+// the tile go through the pass that moves references and rescales O.  Row sums stay in the
+// threads (each sums its own keys) until the item ends.
+// Every wait on an mbarrier is bounded in time (DSPARK_DEVERR_WAIT_TIMEOUT on expiry); the
+// softmax warps' own barriers carry the failure, so that they leave together.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -69,42 +78,45 @@ constexpr int kKT = 128;               // keys per tile (MMA M)
 constexpr int kStages = 8;             // ring of cache tiles (a power of two)
 constexpr int kBlocks = kKT / kBlock;  // blocks of a tile
 constexpr int kStageBytes = kBlocks * kBlockBytes;
+constexpr int kRingRows = 32;          // block rows of a tile that go through the ring
+constexpr int kRowBytes = kD * 2;
+constexpr int kRingV = kRingRows * kRowBytes;  // their V rows in the stage, after the K rows
 constexpr int kSmemItems = 32;         // work items of a CTA kept in shared memory
-constexpr int kQkWarp = 0, kQWarp = 1, kPvWarp = 2, kCopyWarp = 3, kKWarp0 = 4, kVWarp0 = 8, kSmWarp0 = 12;
+constexpr int kNT = 32;                // query rows of a tile (MMA N)
+constexpr int kPvWarp = 2, kCopyWarp = 4, kQWarp = 5, kKWarp0 = 8, kVWarp0 = 16,
+              kSmWarp0 = 24, kThreads = 1024;
+// Registers per thread at launch, and after the warpgroups have traded them: issuers, copy
+// and query loader, K and V, softmax.
+constexpr int kRegs = 65536 / kThreads, kRegsIssue = 40, kRegsLoad = 40, kRegsExpand = 56,
+              kRegsSoftmax = 104;
+static_assert(kRegsIssue + kRegsLoad + 4 * kRegsExpand + 2 * kRegsSoftmax <= 8 * kRegs, "register split");
 constexpr float kRefDrop = 6.f;        // reference = maximum - 6 (log2)
 constexpr float kMove = 14.f;          // a key above reference + 14 moves it
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key (`ref` holds the negatives)
 
-template <int NT_>
-struct Cfg {
-  static constexpr int NT = NT_;
-  static constexpr int WGS = NT / 32;               // softmax warpgroups
-  static constexpr int THREADS = (kSmWarp0 + 4 * WGS) * 32;
-  static constexpr int Q_CB = NT * 128;             // one 64-wide column block of Q
-  static constexpr int Q_BYTES = 2 * Q_CB;
-  static constexpr int P_ROW = NT * 2;
-  static constexpr int P_BYTES = kKT * P_ROW;
-  static constexpr SwizzleMode P_SW = NT == 32 ? SW_64B : SW_128B;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
-  static constexpr int OFF_RING = OFF_P + 2 * P_BYTES;
-  static constexpr int OFF_VS = OFF_RING + kStages * kStageBytes; // V scale pairs: [4 warps][512 B]
-  static constexpr int OFF_CF = OFF_VS + 4 * 512;                 // float cf[2][NT]: softmax scale per row
-  static constexpr int OFF_REF = OFF_CF + 2 * NT * 4;             // float ref[WGS][4][32]
-  static constexpr int OFF_AL = OFF_REF + WGS * 512;              // float alpha[WGS][4][32]
-  static constexpr int OFF_RED = OFF_AL + WGS * 512;              // float red[WGS][4][32]
-  static constexpr int OFF_SUM = OFF_RED + WGS * 512;              // float sum[WGS][4][32]
-  static constexpr int OFF_ITEMS = OFF_SUM + WGS * 512;
-  static constexpr int OFF_BAR = OFF_ITEMS + kSmemItems * (int)sizeof(AttnItem);
-  static constexpr int N_BARS = 18 + 2 * kStages;
-  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
-  static constexpr int TMEM_S = 0, TMEM_O = 2 * NT, TMEM_K = 4 * NT, TMEM_V = 4 * NT + 128;
-  static constexpr int TMEM_COLS = 512;
-  static_assert(NT == 32 || NT == 64, "query tile");
-  static_assert(TMEM_V + 128 <= TMEM_COLS, "tensor memory");
-  static_assert(SMEM_BYTES <= 232448, "shared memory");
-};
+// Shared memory (offsets from a 1024-byte boundary) and tensor memory (columns).
+constexpr int kQCb = kNT * 128;                            // one 64-wide column block of Q
+constexpr int kQBytes = 2 * kQCb;
+constexpr int kPRow = kNT * 2, kPBytes = kKT * kPRow;
+constexpr int kOffQ = 0;                                   // two items
+constexpr int kOffP = kOffQ + 2 * kQBytes;                 // four tiles
+constexpr int kOffRing = kOffP + 4 * kPBytes;
+constexpr int kOffScale = kOffRing + kStages * kStageBytes;  // V scale pairs [8 warps][512 B]
+constexpr int kOffCf = kOffScale + 8 * 512;                // softmax scale per row [2 items][32]
+constexpr int kOffRef = kOffCf + 2 * 128;                  // negative references [8 warps][32]
+constexpr int kOffAlpha = kOffRef + 8 * 128;               // factors [8 warps][2][32]
+constexpr int kOffMax = kOffAlpha + 8 * 256;               // tile maxima [2 streams][4 warps][32]
+constexpr int kOffSum = kOffMax + 2 * 512;                 // row sums [2 items][2 streams][4 warps][32]
+constexpr int kOffItemRef = kOffSum + 4 * 512;             // references [2 items][2 streams][32]
+constexpr int kOffItems = kOffItemRef + 4 * 128;
+constexpr int kOffBar = kOffItems + kSmemItems * (int)sizeof(AttnItem);
+constexpr int kBars = 26 + 2 * kStages;
+constexpr int kOffMisc = kOffBar + kBars * 8;
+constexpr int kSmemBytes = kOffMisc + 32 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+static_assert(2 * kRingV <= kStageBytes, "block rows in a stage");
+constexpr int kTmemS = 0, kTmemO = 4 * kNT, kTmemK = 8 * kNT, kTmemV = 8 * kNT + 128, kTmemCols = 512;
+static_assert(kTmemV + 128 <= kTmemCols, "tensor memory");
 
 struct Params {
   const __nv_bfloat16 *q, *k_new, *v_new;
@@ -126,8 +138,11 @@ struct Ctx {
   unsigned int* err;
 };
 
+// The barrier suspends the thread for up to 20 us a try; the clock is read only after 64.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctx& cx) {
-  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
@@ -138,6 +153,24 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ct
       return false;
     }
   }
+}
+// The same without suspending: for the issuers, whose wake-up is on every tile's path.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool spin_bar(uint32_t bar, uint32_t parity, const Ctx& cx) {
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
+  return wait_bar(bar, parity, cx);
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Ctx& cx) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, cx));
@@ -152,16 +185,16 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigne
   }
 }
 
-// Barrier of one softmax warpgroup (128 threads) that ors a flag over it.
-__device__ __forceinline__ bool group_or(int id, bool x) {
+// Barrier of `n` softmax threads that ors a flag over them.
+__device__ __forceinline__ bool group_or(int id, int n, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %2, 0;\n\t"
-      "barrier.cta.red.or.pred p, %1, 128, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(id), "r"((uint32_t)x)
+      : "r"(id), "r"(n), "r"((uint32_t)x)
       : "memory");
   return r != 0;
 }
@@ -250,6 +283,22 @@ __device__ __forceinline__ void expand(uint32_t w, const uint32_t (&s)[4], const
   o[2] = hfma2_bits((w8 & 0x000f000fu) | 0x64006400u, s[2], b[2]);
   o[3] = hfma2_bits((w8 & 0x00f000f0u) | 0x64006400u, s[3], b[3]);
 }
+// 16 lanes x 16 columns: thread t holds columns 8 e + 2 (t % 4) + {0, 1} of lane t / 4 in
+// r[4 e], r[4 e + 1] and of lane t / 4 + 8 in r[4 e + 2], r[4 e + 3], e = 0, 1.
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // x in cache units, two of them as fp16, saturating (a NaN stays one).
 __device__ __forceinline__ float sat16(float x) {
   return x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f);
@@ -298,54 +347,55 @@ __device__ __forceinline__ int visible_keys(int t, int ct, int ctx, int n_r) {
   return v < kKT ? v : kKT;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(const Params prm) {
-  using C = Cfg<NT>;
+__global__ void __launch_bounds__(kThreads, 1) verify_attn_kv4_kernel(const Params prm) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* bp = smem_raw + (base - raw);
-  AttnItem* s_items = reinterpret_cast<AttnItem*>(bp + C::OFF_ITEMS);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + C::OFF_MISC);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bp + C::OFF_MISC + 16);
+  AttnItem* s_items = reinterpret_cast<AttnItem*>(bp + kOffItems);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bp + kOffMisc + 16);
   const Ctx cx{abort_flag, prm.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
-  // Barriers, pairs indexed by tile or item parity.  A tile's QK^T releases its K operand with
-  // s_full, its PV its V operand and P with pv_done.
-  auto k_full = [&](int b) { return bar(0 + b); };
-  auto v_full = [&](int b) { return bar(2 + b); };
-  auto s_full = [&](int b) { return bar(4 + b); };
-  auto s_free = [&](int b) { return bar(6 + b); };
-  auto p_full = [&](int b) { return bar(8 + b); };
-  auto pv_done = [&](int b) { return bar(10 + b); };
-  auto q_full = [&](int b) { return bar(12 + b); };
-  auto q_empty = [&](int b) { return bar(14 + b); };
-  auto o_free = [&](int b) { return bar(16 + b); };
-  auto c_full = [&](int i) { return bar(18 + i); };             // ring of cache tiles
-  auto c_empty = [&](int i) { return bar(18 + kStages + i); };
+  auto bar = [&](int i) { return base + kOffBar + 8 * i; };
+  // Barriers.  Tile g belongs to stream g & 1; its operands K and V are that stream's, its
+  // scores and probabilities are in S and P buffer g & 3.  Its QK^T releases the K operand with
+  // s_full, its PV the V operand and P with pv_done.
+  auto k_full = [&](int x) { return bar(0 + x); };
+  auto v_full = [&](int x) { return bar(2 + x); };
+  auto s_full = [&](int i) { return bar(4 + i); };
+  auto s_free = [&](int i) { return bar(8 + i); };
+  auto p_full = [&](int i) { return bar(12 + i); };
+  auto pv_done = [&](int i) { return bar(16 + i); };
+  auto q_full = [&](int i) { return bar(20 + i); };   // by item parity
+  auto q_empty = [&](int i) { return bar(22 + i); };
+  auto o_free = [&](int i) { return bar(24 + i); };
+  auto c_full = [&](int i) { return bar(26 + i); };   // ring of cache tiles
+  auto c_empty = [&](int i) { return bar(26 + kStages + i); };
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(k_full(b), 4);
-      mbar_init(v_full(b), 4);
-      mbar_init(s_full(b), 1);
-      mbar_init(s_free(b), 4 * C::WGS);
-      mbar_init(p_full(b), C::WGS);
-      mbar_init(pv_done(b), 1);
-      mbar_init(q_full(b), 1);
-      mbar_init(q_empty(b), 1 + 4 * C::WGS);
-      mbar_init(o_free(b), 4 * C::WGS);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full(i), 4);
+      mbar_init(v_full(i), 4);
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 2 + 8);  // two issuers, eight softmax warps
+      mbar_init(o_free(i), 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 4);
+      mbar_init(p_full(i), 1);
+      mbar_init(pv_done(i), 1);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(c_full(i), 1);
-      mbar_init(c_empty(i), 8);
+      mbar_init(c_empty(i), 8);  // a K and a V warpgroup
     }
     fence_mbar_init();
   }
-  if (warp == kQkWarp) {
-    tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+  if (warp == kCopyWarp) {
+    tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   pdl_release();
@@ -355,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
   {
     const int n_s = min(kSmemItems, it_end - it_begin);
     constexpr int kWords = (int)(sizeof(AttnItem) / sizeof(uint4));
-    for (int i = threadIdx.x; i < n_s * kWords; i += C::THREADS)
+    for (int i = threadIdx.x; i < n_s * kWords; i += kThreads)
       reinterpret_cast<uint4*>(s_items)[i] = reinterpret_cast<const uint4*>(prm.items + it_begin)[i];
   }
   tc_fence_before();
@@ -364,66 +414,156 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
   const uint32_t tmem = *tmem_slot;
   const int G = prm.Hq / prm.Hkv;
 
-  if (warp == kQkWarp) {
-    // ------------------------------------------------------------- S^T = K Q^T
-    constexpr uint32_t IDESC = idesc_f16_f32(kKT, NT, 0);
-    int g = 0, n_it = 0;
-    bool ok = true;
-    for (int it = it_begin; it < it_end && ok; ++it, ++n_it) {
-      const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
-      const int qb = n_it & 1;
-      if (!wait_warp(q_full(qb), (n_it >> 1) & 1, cx)) break;
-      const uint64_t bd = smem_desc(base + C::OFF_Q + qb * C::Q_BYTES, 16, 1024, SW_128B);
-      for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1;
-        ok = wait_warp(k_full(b), (g >> 1) & 1, cx);
-        if (ok && g >= 2) ok = wait_warp(s_free(b), ((g >> 1) - 1) & 1, cx);
-        if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t a = tmem + C::TMEM_K + b * 64, d = tmem + C::TMEM_S + b * NT;
+  if (warp < kCopyWarp) {
+    regs_down<kRegsIssue>();
+    const int x = warp & 1;
+    if (warp < kPvWarp) {
+      // ----------------------------------------------------------- S^T = K Q^T
+      constexpr uint32_t IDESC = idesc_f16_f32(kKT, kNT, 0);
+      if (lane == 0) {
+        const uint32_t a = tmem + kTmemK + x * 64;
+        int g0 = 0, n_it = 0, last = -1;  // first tile of the item
+        bool ok = true;
+        for (int it = it_begin; it < it_end && ok; ++it, ++n_it) {
+          const int k = it - it_begin;
+          const AttnItem* item = k < kSmemItems ? s_items + k : prm.items + it;
+          const int g1 = g0 + item->te - item->tb, qb = n_it & 1;
+          if (!wait_bar(q_full(qb), (n_it >> 1) & 1, cx)) break;
+          const uint64_t bd = smem_desc(base + kOffQ + qb * kQBytes, 16, 1024, SW_128B);
+          int g = g0 + ((g0 ^ x) & 1);
+          if (g >= g1) mbar_arrive(q_empty(qb));  // no tile of this stream in the item
+          for (; g < g1; g += 2) {
+            const int i = g & 3;
+            ok = wait_bar(k_full(x), (g >> 1) & 1, cx) &&
+                 (g < 4 || wait_bar(s_free(i), ((g >> 2) - 1) & 1, cx));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + kTmemS + i * kNT;
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)
-            umma_bf16_ts(d, a + kk * 8, bd + ((kk >> 2) * C::Q_CB + (kk & 3) * 32) / 16, IDESC,
-                         kk > 0 ? 1u : 0u);
-          umma_commit(s_full(b));
-          if (t == item.te - 1) umma_commit(q_empty(qb));
+            for (int kk = 0; kk < kD / 16; ++kk)
+              umma_bf16_ts(d, a + kk * 8, bd + ((kk >> 2) * kQCb + (kk & 3) * 32) / 16, IDESC,
+                           kk > 0 ? 1u : 0u);
+            umma_commit(s_full(i));
+            if (g + 2 >= g1) umma_commit(q_empty(qb));
+            last = g;
+          }
+          g0 = g1;
         }
-        __syncwarp();
+        if (last >= 0) drain_bar(s_full(last & 3), (last >> 2) & 1, prm.err);
+      }
+    } else {
+      // ----------------------------------------------------------- O^T += V^T P^T
+      constexpr uint32_t IDESC = idesc_f16_f32(kD, kNT, 1);
+      if (lane == 0) {
+        const uint32_t a = tmem + kTmemV + x * 64;
+        int g0 = 0, n_it = 0, last = -1;
+        bool ok = true;
+        for (int it = it_begin; it < it_end && ok; ++it, ++n_it) {
+          const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
+          const int g1 = g0 + item.te - item.tb, ct = ceil_div(item.ctx, kKT);
+          const uint32_t d = tmem + kTmemO + (2 * x + (n_it & 1)) * kNT;
+          const int first = g0 + ((g0 ^ x) & 1);
+          if (first < g1 && n_it >= 2 && !wait_bar(o_free(n_it & 1), ((n_it >> 1) - 1) & 1, cx)) break;
+          for (int g = first; g < g1; g += 2) {
+            ok = wait_bar(v_full(x), (g >> 1) & 1, cx) && wait_bar(p_full(g & 3), (g >> 2) & 1, cx);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bd = smem_desc(base + kOffP + (g & 3) * kPBytes, kKT * 128, 8 * kPRow, SW_64B);
+            const int t = item.tb + g - g0;
+            umma_bf16_ts(d, a, bd, IDESC, g > first ? 1u : 0u);
+            if (t < ct) {
+#pragma unroll
+              for (int kk = 1; kk < kKT / 16; ++kk)
+                umma_bf16_ts(d, a + kk * 8, bd + kk * kPRow, IDESC, 1u);
+            } else {
+              // only the 16-row steps that hold a row
+              const int nch = ceil_div(visible_keys(t, ct, item.ctx, item.n_r), 16);
+#pragma unroll 1
+              for (int kk = 1; kk < nch; ++kk) umma_bf16_ts(d, a + kk * 8, bd + kk * kPRow, IDESC, 1u);
+            }
+            umma_commit(pv_done(g & 3));
+            last = g;
+          }
+          g0 = g1;
+        }
+        if (last >= 0) drain_bar(pv_done(last & 3), (last >> 2) & 1, prm.err);
       }
     }
-    if (lane == 0 && g > 0) drain_bar(s_full((g - 1) & 1), ((g - 1) >> 1) & 1, prm.err);
-  } else if (warp == kPvWarp) {
-    // ------------------------------------------------------------- O^T += V^T P^T
-    constexpr uint32_t IDESC = idesc_f16_f32(kD, NT, 1);
-    int g = 0, n_it = 0;
+    __syncwarp();
+  } else if (warp < kKWarp0) {
+    regs_down<kRegsLoad>();
+    if (warp == kCopyWarp) {
+    // ------------------------------------------------------------- cache tiles into the ring
+    // Lane j looks up and copies block j % 8 of tile j / 8 of a window of four; `nxt` is its
+    // page in the window after.  Blocks that lie together in a page go as one copy.
+    const int per = 1 << (prm.log2_page - 4);        // blocks of a page
+    const int run = min(per, kBlocks);               // blocks of a copy
+    const int lt = lane >> 3, lb = lane & 7;
+    auto lookup = [&](int r, int ctx, int t) -> int {
+      const int pos = (t + lt) * kKT + lb * kBlock;
+      const int slot = pos >> prm.log2_page;
+      if (pos >= ctx) return -1;
+      return slot < prm.max_pages ? __ldg(prm.page_table + (long long)r * prm.max_pages + slot) : -1;
+    };
+    int g = 0, nxt = -1;
     bool ok = true;
-    for (int it = it_begin; it < it_end && ok; ++it, ++n_it) {
+    if (it_begin < it_end) {
+      const AttnItem x = fetch_item(s_items, prm.items, it_begin, it_begin);
+      nxt = lookup(x.r, x.ctx, x.tb);
+    }
+    for (int it = it_begin; it < it_end && ok; ++it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
-      const int ob = n_it & 1, ct = ceil_div(item.ctx, kKT);
-      if (n_it >= 2 && !wait_warp(o_free(ob), ((n_it >> 1) - 1) & 1, cx)) break;
-      for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1;
-        ok = wait_warp(v_full(b), (g >> 1) & 1, cx) && wait_warp(p_full(b), (g >> 1) & 1, cx);
-        if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t a = tmem + C::TMEM_V + b * 64, d = tmem + C::TMEM_O + ob * NT;
-          const uint64_t bd = smem_desc(base + C::OFF_P + b * C::P_BYTES, kKT * 128, 8 * C::P_ROW, C::P_SW);
-          // only the 16-key steps that hold a visible key
-          const int nch = ceil_div(visible_keys(t, ct, item.ctx, item.n_r), 16);
-#pragma unroll
-          for (int kk = 0; kk < kKT / 16; ++kk)
-            if (kk < nch)
-              umma_bf16_ts(d, a + kk * 8, bd + kk * 16 * C::P_ROW / 16, IDESC,
-                           (t > item.tb || kk > 0) ? 1u : 0u);
-          umma_commit(pv_done(b));
+      const int ct = ceil_div(item.ctx, kKT);
+      for (int t0 = item.tb; t0 < item.te && ok; t0 += 4) {
+        const int page = nxt;
+        if (t0 + 4 < item.te) {
+          nxt = lookup(item.r, item.ctx, t0 + 4);
+        } else if (it + 1 < it_end) {
+          const AttnItem x = fetch_item(s_items, prm.items, it + 1, it_begin);
+          nxt = lookup(x.r, x.ctx, x.tb);
         }
-        __syncwarp();
+        const int pos = (t0 + lt) * kKT + lb * kBlock;
+        const bool want = pos < item.ctx && t0 + lt < item.te;
+        const bool valid = want && page >= 0 && page < prm.n_pages;
+        if (want && !valid) raise_error(prm.err, DSPARK_DEVERR_BAD_INPUT);
+        // this lane's copy: `run` blocks from its own, as far as the context reaches
+        const int nb = min(run, ceil_div(item.ctx - pos, kBlock));
+        const uint32_t bytes = valid && lb % run == 0 ? (uint32_t)(nb * kBlockBytes) : 0u;
+        const uint8_t* src = prm.cache + (((long long)(valid ? page : 0) * prm.Hkv + item.kvh) * per +
+                                          ((pos >> 4) & (per - 1))) * kBlockBytes;
+        uint32_t total = bytes;                      // of the lane's tile
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll 1
+        for (int i = 0; i < 4 && t0 + i < item.te; ++i, ++g) {
+          const int st = g & (kStages - 1);
+          if (g >= kStages) {
+            ok = wait_warp(c_empty(st), ((g / kStages) - 1) & 1, cx);
+            if (!ok) break;
+          }
+          const uint32_t dst = base + kOffRing + st * kStageBytes;
+          if (t0 + i < ct) {
+            if (lane == 8 * i) mbar_arrive_expect_tx(c_full(st), total);
+            __syncwarp();
+            if (lt == i && bytes) bulk_load_g2s(dst + lb * kBlockBytes, src, bytes, c_full(st));
+          } else {
+            // the first block rows of a tile of them, K then V
+            const int b0 = (t0 + i - ct) * kKT, rows = min(item.n_r - b0, kRingRows);
+            if (lane == 0) mbar_arrive_expect_tx(c_full(st), (uint32_t)rows * 2 * kRowBytes);
+            __syncwarp();
+            if (lane < rows) {
+              const long long off = ((long long)(item.c0 + b0 + lane) * prm.Hkv + item.kvh) * kD;
+              bulk_load_g2s(dst + lane * kRowBytes, prm.k_new + off, kRowBytes, c_full(st));
+              bulk_load_g2s(dst + kRingV + lane * kRowBytes, prm.v_new + off, kRowBytes, c_full(st));
+            }
+          }
+        }
       }
     }
-    if (lane == 0 && g > 0) drain_bar(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, prm.err);
-  } else if (warp == kQWarp) {
+    // no copy may be in flight when the CTA ends
+    for (int x = max(g - kStages, 0); x < g; ++x)
+      if (lane == 0) drain_bar(c_full(x & (kStages - 1)), (x / kStages) & 1, prm.err);
+    } else if (warp == kQWarp) {
     // ------------------------------------------------------------- query loader
     // Tile row n = (block row n / G, head kvh G + n % G); rows past the item's are zero.  A
     // half-warp holds a row, 8 elements per lane.
@@ -438,13 +578,13 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
       }
       const int nq = item.ni * G, l = lane & 15;
       const long long row0 = item.c0 + item.i0;
-      const uint32_t qd = base + C::OFF_Q + qb * C::Q_BYTES;
-      float* cf = reinterpret_cast<float*>(bp + C::OFF_CF) + qb * NT;
+      const uint32_t qd = base + kOffQ + qb * kQBytes;
+      float* cf = reinterpret_cast<float*>(bp + kOffCf) + qb * kNT;
 #pragma unroll 1
-      for (int n0 = 0; n0 < NT; n0 += 16) {
-        uint4 v[8];
+      for (int n0 = 0; n0 < kNT; n0 += 8) {
+        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int n = n0 + 2 * i + (lane >> 4);
           v[i] = make_uint4(0, 0, 0, 0);
           if (n < nq)
@@ -452,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
                 prm.q + ((row0 + n / G) * prm.Hq + item.kvh * G + n % G) * kD + l * 8);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int n = n0 + 2 * i + (lane >> 4);
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t top = 0;  // largest magnitude, as bits (a NaN is above all)
@@ -469,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
           for (int j = 0; j < 4; ++j)
             h[j] = h2_bits(__floats2half2_rn(__uint_as_float(w[j] << 16) * f,
                                              __uint_as_float(w[j] & 0xffff0000u) * f));
-          st_shared_v4(qd + (l >> 3) * C::Q_CB + sw128_off(n, l & 7), make_uint4(h[0], h[1], h[2], h[3]));
+          st_shared_v4(qd + (l >> 3) * kQCb + sw128_off(n, l & 7), make_uint4(h[0], h[1], h[2], h[3]));
           if (l == 0)  // (never 0: a masked score is -inf times it)
             cf[n] = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2, 1.17549435e-38f);
         }
@@ -478,80 +618,26 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(qb));
     }
-  } else if (warp == kCopyWarp) {
-    // ------------------------------------------------------------- cache tiles into the ring
-    // Lane j looks up and copies block j % 8 of tile j / 8 of a window of four; `nxt` is its
-    // page in the window after.  Blocks that lie together in a page go as one copy.
-    const int per = 1 << (prm.log2_page - 4);        // blocks of a page
-    const int run = min(per, kBlocks);               // blocks of a copy
-    const int lt = lane >> 3, lb = lane & 7;
-    auto lookup = [&](int r, int ctx, int t) -> int {
-      const int pos = (t + lt) * kKT + lb * kBlock;
-      const int slot = pos >> prm.log2_page;
-      if (pos >= ctx) return -1;
-      return slot < prm.max_pages ? __ldg(prm.page_table + (long long)r * prm.max_pages + slot) : -1;
-    };
-    int gc = 0, nxt = -1;
-    bool ok = true;
-    if (it_begin < it_end) {
-      const AttnItem x = fetch_item(s_items, prm.items, it_begin, it_begin);
-      nxt = lookup(x.r, x.ctx, x.tb);
     }
-    for (int it = it_begin; it < it_end && ok; ++it) {
-      const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
-      const int te = min(item.te, ceil_div(item.ctx, kKT));  // cache tiles of the item
-      for (int t0 = item.tb; t0 < item.te && ok; t0 += 4) {
-        int page = nxt;
-        if (t0 + 4 < item.te) {
-          nxt = lookup(item.r, item.ctx, t0 + 4);
-        } else if (it + 1 < it_end) {
-          const AttnItem x = fetch_item(s_items, prm.items, it + 1, it_begin);
-          nxt = lookup(x.r, x.ctx, x.tb);
-        }
-        const int pos = (t0 + lt) * kKT + lb * kBlock;
-        const bool want = pos < item.ctx && t0 + lt < te;
-        const bool valid = want && page >= 0 && page < prm.n_pages;
-        if (want && !valid) raise_error(prm.err, DSPARK_DEVERR_BAD_INPUT);
-        // this lane's copy: `run` blocks from its own, as far as the context reaches
-        const int nb = min(run, ceil_div(item.ctx - pos, kBlock));
-        const uint32_t bytes = valid && lb % run == 0 ? (uint32_t)(nb * kBlockBytes) : 0u;
-        const uint8_t* src = prm.cache + (((long long)(valid ? page : 0) * prm.Hkv + item.kvh) * per +
-                                          ((pos >> 4) & (per - 1))) * kBlockBytes;
-        uint32_t total = bytes;                      // of the lane's tile
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        for (int i = 0; i < 4 && t0 + i < te; ++i, ++gc) {
-          const int st = gc & (kStages - 1);
-          if (gc >= kStages) {
-            ok = wait_warp(c_empty(st), ((gc / kStages) - 1) & 1, cx);
-            if (!ok) break;
-          }
-          if (lane == 8 * i) mbar_arrive_expect_tx(c_full(st), total);
-          __syncwarp();
-          if (lt == i && bytes)
-            bulk_load_g2s(base + C::OFF_RING + st * kStageBytes + lb * kBlockBytes, src, bytes, c_full(st));
-        }
-      }
-    }
-    // no copy may be in flight when the CTA ends
-    for (int x = max(gc - kStages, 0); x < gc; ++x)
-      if (lane == 0) drain_bar(c_full(x & (kStages - 1)), (x / kStages) & 1, prm.err);
-  } else if (warp >= kKWarp0 && warp < kVWarp0) {
+  } else if (warp < kVWarp0) {
+    regs_down<kRegsExpand>();
     // ------------------------------------------------------------- K: thread = key
-    const int w = warp - kKWarp0, kl = w * 32 + lane;
+    const int w = warp & 3, kl = w * 32 + lane;
+    const int b = (warp - kKWarp0) >> 2;               // this warpgroup's tiles and operand buffer
     // this key's codes and scales within a stage
-    const uint32_t ring = base + C::OFF_RING + (2 * w + (lane >> 4)) * kBlockBytes;
+    const uint32_t ring = base + kOffRing + (2 * w + (lane >> 4)) * kBlockBytes;
     const uint32_t codes = ring + (lane & 15) * 16, scales = ring + kOffKs + (lane & 15) * 4;
-    const uint32_t t_k = tmem + (static_cast<uint32_t>(w * 32) << 16) + C::TMEM_K;
-    int g = 0, gc = 0;
+    const uint32_t t_k = tmem + (static_cast<uint32_t>(w * 32) << 16) + kTmemK + b * 64;
+    int g = 0;
     bool ok = true;
     for (int it = it_begin; it < it_end && ok; ++it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
       const int ct = ceil_div(item.ctx, kKT);
       for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1, st = gc & (kStages - 1);
-        if (t < ct) ok = wait_warp(c_full(st), (gc / kStages) & 1, cx);
-        if (ok && g >= 2) ok = wait_warp(s_full(b), ((g >> 1) - 1) & 1, cx);  // QK^T of tile g - 2 done
+        if ((g & 1) != b) continue;
+        const int st = g & (kStages - 1);
+        ok = wait_warp(c_full(st), (g / kStages) & 1, cx);
+        if (ok && g >= 2) ok = wait_warp(s_full((g - 2) & 3), ((g - 2) >> 2) & 1, cx);  // its QK^T done
         if (!ok) break;
         tc_fence_after();
         if (t < ct) {
@@ -570,22 +656,22 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             expand(v.y, ss, bb, o + 4);
             expand(v.z, ss, bb, o + 8);
             expand(v.w, ss, bb, o + 12);
-            tmem_st16u(t_k + b * 64 + c * 16, o);
+            tmem_st16u(t_k + c * 16, o);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(c_empty(st));
-          ++gc;
         } else {
-          // the request's own rows: bf16 / (16 k_scale)
+          // the request's own rows: bf16 / (16 k_scale); the first ones from the ring
           const int bi = (t - ct) * kKT + kl;
           const __nv_bfloat16* src = prm.k_new + ((long long)(item.c0 + bi) * prm.Hkv + item.kvh) * kD;
+          const uint32_t row = base + kOffRing + st * kStageBytes + kl * kRowBytes;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint4 v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               v[j] = make_uint4(0, 0, 0, 0);
-              if (bi < item.n_r) v[j] = reinterpret_cast<const uint4*>(src)[c * 4 + j];
+              if (bi < item.n_r)
+                v[j] = kl < kRingRows ? ld_shared_v4(row + (c * 4 + j) * 16)
+                                      : reinterpret_cast<const uint4*>(src)[c * 4 + j];
             }
             uint32_t o[16];
 #pragma unroll
@@ -596,162 +682,174 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
                 o[4 * j + q] = pack16(__uint_as_float(x[q] << 16) * prm.k_unit,
                                       __uint_as_float(x[q] & 0xffff0000u) * prm.k_unit);
             }
-            tmem_st16u(t_k + b * 64 + c * 16, o);
+            tmem_st16u(t_k + c * 16, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(b));
+        if (lane == 0) {
+          mbar_arrive(c_empty(st));
+          mbar_arrive(k_full(b));
+        }
       }
     }
-  } else if (warp >= kVWarp0 && warp < kSmWarp0) {
+  } else if (warp < kSmWarp0) {
+    regs_down<kRegsExpand>();
     // ------------------------------------------------------------- V: thread = channel
-    const int w = warp - kVWarp0;
-    const uint32_t ring = base + C::OFF_RING;
-    const uint32_t codes = ring + kOffV + (w * 32 + lane) * 8;
+    const int w = warp & 3;
+    const int b = (warp - kVWarp0) >> 2;               // this warpgroup's tiles and operand buffer
+    const uint32_t ring = base + kOffRing;
+    // quad lane % 4 expands blocks 2 (lane % 4) and + 1, channels lane / 4 + 8 j of the warp's 32
+    const uint32_t codes = ring + 2 * (lane & 3) * kBlockBytes + kOffV + (w * 32 + (lane >> 2)) * 8;
     const uint32_t scales = ring + (lane >> 2) * kBlockBytes + kOffVs + w * kBlock + (lane & 3) * 4;
-    const uint32_t vs = base + C::OFF_VS + w * 512;
-    const uint32_t t_v = tmem + (static_cast<uint32_t>(w * 32) << 16) + C::TMEM_V;
-    int g = 0, gc = 0;
+    const uint32_t vs = base + kOffScale + (warp - kVWarp0) * 512;
+    const uint32_t t_v = tmem + (static_cast<uint32_t>(w * 32) << 16) + kTmemV + b * 64;
+    int g = 0;
     bool ok = true;
     for (int it = it_begin; it < it_end && ok; ++it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
       const int ct = ceil_div(item.ctx, kKT);
       for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1, st = gc & (kStages - 1);
+        if ((g & 1) != b) continue;
+        const int st = g & (kStages - 1);
         const int vis = visible_keys(t, ct, item.ctx, item.n_r);
-        const int np = ceil_div(vis, 32);  // pairs of blocks that hold a visible key
+        ok = wait_warp(c_full(st), (g / kStages) & 1, cx);
         if (t < ct) {
-          ok = wait_warp(c_full(st), (gc / kStages) & 1, cx);
           // scale pairs of the tile's keys 4 lane .. + 3, shared by the warp's channels; keys
           // past the context get scale 0, whatever their page holds
           uint32_t sc = ld_shared(scales + st * kStageBytes);
           const int left = vis - 4 * lane;
           if (left < 4) sc = left <= 0 ? 0u : sc & ((1u << (8 * left)) - 1u);
           const uint32_t s0 = e4m3x2_to_h2(sc & 0xffffu), s1 = e4m3x2_to_h2(sc >> 16);
-          const uint32_t at = vs + (lane >> 1) * 32 + (lane & 1) * 8;
+          const uint32_t at = vs + ((lane & 7) >> 1) * 128 + (lane >> 3) * 32 + (lane & 1) * 8;
           st_shared_v2(at, hmul2_bits(s0, kSixteenth), hmul2_bits(s1, k256th));
           st_shared_v2(at + 16, hmul2_bits(s0, kBiasLow), hmul2_bits(s1, kBiasHigh));
           __syncwarp();
         }
-        if (ok && g >= 2) ok = wait_warp(pv_done(b), ((g >> 1) - 1) & 1, cx);  // PV of tile g - 2 done
+        if (ok && g >= 2) ok = wait_warp(pv_done((g - 2) & 3), ((g - 2) >> 2) & 1, cx);  // its PV done
         if (!ok) break;
         tc_fence_after();
         if (t < ct) {
           const uint32_t src = codes + st * kStageBytes;
 #pragma unroll 1
-          for (int i = 0; i < np; ++i) {
-            uint32_t o[16];
-            const uint2 v0 = ld_shared_v2(src + 2 * i * kBlockBytes);
-            const uint2 v1 = ld_shared_v2(src + (2 * i + 1) * kBlockBytes);
-            const uint32_t word[4] = {v0.x, v0.y, v1.x, v1.y};
+          for (int u = 0; u < 2; ++u) {  // the quad's two blocks
+            uint2 v[4];                  // channels 8 j + lane / 4
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t at = vs + (4 * i + j) * 32;
+            for (int j = 0; j < 4; ++j) v[j] = ld_shared_v2(src + u * kBlockBytes + j * 64);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t at = vs + (2 * u + h) * 128 + (lane & 3) * 32;
               const uint4 s = ld_shared_v4(at), c = ld_shared_v4(at + 16);
               const uint32_t ss[4] = {s.x, s.y, s.z, s.w}, bb[4] = {c.x, c.y, c.z, c.w};
-              expand(word[j], ss, bb, o + j * 4);
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {  // lanes 0-15 and 16-31 of the quadrant
+                uint32_t lo[4], hi[4];
+                expand(h ? v[2 * f].y : v[2 * f].x, ss, bb, lo);
+                expand(h ? v[2 * f + 1].y : v[2 * f + 1].x, ss, bb, hi);
+                const uint32_t o[8] = {lo[0], lo[1], hi[0], hi[1], lo[2], lo[3], hi[2], hi[3]};
+                tmem_st_16x256b_x2(t_v + (static_cast<uint32_t>(f * 16) << 16) + (2 * u + h) * 16, o);
+              }
             }
-            tmem_st16u(t_v + b * 64 + i * 16, o);
           }
-          __syncwarp();  // (also: every lane has read the scale pairs)
-          if (lane == 0) mbar_arrive(c_empty(st));
-          ++gc;
         } else {
           const int b0 = (t - ct) * kKT;
+          const long long step = (long long)prm.Hkv * kD;
           const __nv_bfloat16* vn = prm.v_new + ((long long)(item.c0 + b0) * prm.Hkv + item.kvh) * kD +
                                     w * 32 + lane;
+          const __nv_bfloat16* vr = reinterpret_cast<const __nv_bfloat16*>(
+              bp + kOffRing + st * kStageBytes + kRingV) + w * 32 + lane;
+          static_assert(kRingRows == 32, "one pair of V blocks");
 #pragma unroll 1
-          for (int i = 0; i < np; ++i) {
-            const long long step = (long long)prm.Hkv * kD;
+          for (int i = 0; 32 * i < vis; ++i) {
+            const __nv_bfloat16* from = i == 0 ? vr : vn + 32 * i * step;
+            const long long by = i == 0 ? kD : step;
             float x[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              x[j] = 32 * i + j < vis ? __bfloat162float(vn[(32 * i + j) * step]) : 0.f;
+              x[j] = 32 * i + j < vis ? __bfloat162float(from[j * by]) : 0.f;
             uint32_t o[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack16(x[2 * j] * prm.v_unit, x[2 * j + 1] * prm.v_unit);
-            tmem_st16u(t_v + b * 64 + i * 16, o);
+            tmem_st16u(t_v + i * 16, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(b));
+        __syncwarp();  // (also: every lane has read its stage and the scale pairs)
+        if (lane == 0) {
+          mbar_arrive(c_empty(st));
+          mbar_arrive(v_full(b));
+        }
       }
     }
-  } else if (warp >= kSmWarp0) {
+  } else {
+    regs_up<kRegsSoftmax>();
     // ------------------------------------------------------------- softmax and epilogue
-    const int sw = warp & 3, wg = (warp - kSmWarp0) >> 2;
+    const int sw = warp & 3, x = (warp - kSmWarp0) >> 2;
     const int kl = sw * 32 + lane;               // key of a tile, channel of O^T
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(sw * 32) << 16) + wg * 32;
-    const int bar_id = 1 + wg;
-    float* ref = reinterpret_cast<float*>(bp + C::OFF_REF) + (wg * 4 + sw) * 32;   // this warp's copy
-    float* alpha = reinterpret_cast<float*>(bp + C::OFF_AL) + (wg * 4 + sw) * 32;
-    float* red = reinterpret_cast<float*>(bp + C::OFF_RED) + wg * 128;             // [4 warps][32]
-    float* sums = reinterpret_cast<float*>(bp + C::OFF_SUM) + wg * 128;
-    int g = 0, n_it = 0;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(sw * 32) << 16);
+    const int bar_id = 1 + x, kBoth = 3;
+    float* ref = reinterpret_cast<float*>(bp + kOffRef) + (warp - kSmWarp0) * 32;  // this warp's copies
+    float* alpha = reinterpret_cast<float*>(bp + kOffAlpha) + (warp - kSmWarp0) * 64;
+    float* tmax = reinterpret_cast<float*>(bp + kOffMax) + x * 128;                // [4 warps][32]
+    // this key's step of the PV product in a cache tile, and in a block tile
+    const int row_cache = 16 * (lane >> 2) + 4 * sw + (lane & 3);
+    int g0 = 0, n_it = 0, last = -1;
     bool bad = false;                            // a wait ran out
     for (int it = it_begin; it < it_end; ++it, ++n_it) {
       const AttnItem item = fetch_item(s_items, prm.items, it, it_begin);
       const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
-      const int nq = min(max(item.ni * G - wg * 32, 0), 32);  // rows in this group's columns
+      const int nq = item.ni * G;                // rows of the tile
       const int nc8 = (nq + 7) >> 3;
-      const int qb = n_it & 1;
-      const float* cf = reinterpret_cast<const float*>(bp + C::OFF_CF) + qb * NT + wg * 32;
-      bad |= !wait_warp(q_full(qb), (n_it >> 1) & 1, cx);
+      const int ip = n_it & 1;
+      const float* cf = reinterpret_cast<const float*>(bp + kOffCf) + ip * kNT;
+      bad |= !wait_warp(q_full(ip), (n_it >> 1) & 1, cx);
       float mref = -INFINITY;                    // reference of row `lane`
       float lacc[32];                            // this thread's part of each row's sum
 #pragma unroll
       for (int k = 0; k < 32; ++k) lacc[k] = 0.f;
-      for (int t = item.tb; t < item.te; ++t, ++g) {
-        const int b = g & 1;
-        bad |= !wait_warp(s_full(b), (g >> 1) & 1, cx);
-        if (nq == 0) {
-          // no row of the item in these columns: P's are left as they are, they only reach
-          // columns of O^T that nothing reads
-          if (group_or(bar_id, bad)) goto done;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free(b));
-          if (sw == 0 && lane == 0) mbar_arrive(p_full(b));
-          continue;
-        }
-        if (g >= 2) bad |= !wait_warp(pv_done(b), ((g >> 1) - 1) & 1, cx);  // P buffer free
+      const int g1 = g0 + item.te - item.tb, first = g0 + ((g0 ^ x) & 1);
+      const uint32_t t_o = t_lane + kTmemO + (2 * x + ip) * kNT;
+#pragma unroll 1
+      for (int g = first; g < g1; g += 2) {
+        const int t = item.tb + g - g0, i = g & 3;
+        bad |= !wait_warp(s_full(i), (g >> 2) & 1, cx);
+        // the P buffer is free once the PV of tile g - 4 is done; that of g - 2 may still run
+        if (g >= 4) bad |= !wait_warp(pv_done(i), ((g >> 2) - 1) & 1, cx);
         tc_fence_after();
-        // row n of these columns sees this key iff n >= nmin
+        // row n sees this key iff n >= nmin
+        const bool cached = t < ct;
+        const bool masked = !cached || (t + 1) * kKT > ctx;  // some key is not seen by all rows
         int nmin = 0;
-        if (t < ct) {
-          if (t * kKT + kl >= ctx) nmin = 1 << 30;
-        } else {
+        if (masked) {
           const int bi = (t - ct) * kKT + kl;
-          nmin = bi < item.n_r ? (bi - item.i0) * G - wg * 32 : 1 << 30;
+          nmin = cached ? (t * kKT + kl < ctx ? 0 : 1 << 30)
+                        : (bi < item.n_r ? (bi - item.i0) * G : 1 << 30);
         }
-        const uint32_t s_col = t_lane + C::TMEM_S + b * NT;
-        const uint32_t prow = base + C::OFF_P + b * C::P_BYTES;
-        const bool masked = t >= ct || (t + 1) * kKT > ctx;  // some key is not seen by all rows
-        float x[32];
+        const uint32_t s_col = t_lane + kTmemS + i * kNT;
+        const int pr = cached ? row_cache : kl;
+        const uint32_t pbuf = base + kOffP + i * kPBytes;
+        float s[32];
         auto scores = [&]() {
-          tmem_ld32(s_col, x);
-          tmem_wait_ld32(x);
+          tmem_ld32(s_col, s);
+          tmem_wait_ld32(s);
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = nmin <= k ? x[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) s[k] = nmin <= k ? s[k] : -INFINITY;
           }
         };
-        bool move = t == item.tb;  // the references have to move first
+        bool move = g == first;  // the references have to move first
         for (;;) {
           if (move) {
-            // ---- the tile's maximum per row, over the group's warps
+            // ---- the tile's maximum per row, over the stream's warps
             scores();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] *= cf[k];
-            red[sw * 32 + lane] = transpose_reduce<true>(x, lane);
-            // O^T holds the products up to tile g - 1 before it is rescaled
-            if (t > item.tb) bad |= !wait_warp(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, cx);
-            if (group_or(bar_id, bad)) goto done;
-            const float tm = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
+            for (int k = 0; k < 32; ++k) s[k] *= cf[k];
+            tmax[sw * 32 + lane] = transpose_reduce<true>(s, lane);
+            if (group_or(bar_id, 128, bad)) goto done;
+            const float tm =
+                fmaxf(fmaxf(tmax[lane], tmax[32 + lane]), fmaxf(tmax[64 + lane], tmax[96 + lane]));
             float al = 1.f;
             if (tm - kRefDrop > mref + (kMove - kRefDrop)) {
               al = mref == -INFINITY ? 0.f : fast_exp2(mref - (tm - kRefDrop));
@@ -761,19 +859,19 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
             ref[lane] = mref == -INFINITY ? -kNoRef : -mref;
             alpha[lane] = al;
             __syncwarp();
-            if (t > item.tb) {
+            if (g > first) {
+              // O^T holds the products up to the stream's last tile before it is rescaled
+              bad |= !wait_warp(pv_done((g - 2) & 3), ((g - 2) >> 2) & 1, cx);
               tc_fence_after();
-              const uint32_t t_o = t_lane + C::TMEM_O + (n_it & 1) * NT;
-              tmem_ld32(t_o, x);
-              tmem_wait_ld32(x);
+              tmem_ld32(t_o, s);
+              tmem_wait_ld32(s);
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
                 lacc[k] *= alpha[k];
-                x[k] *= alpha[k];
+                s[k] *= alpha[k];
               }
-              tmem_st32(t_o, x);
+              tmem_st32(t_o, s);
               tmem_wait_st();
-              tc_fence_before();
             }
           }
           // ---- P of this key against the references
@@ -788,73 +886,91 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
               const int k = q * 8 + h * 4;
               const float4 c4 = reinterpret_cast<const float4*>(cf)[q * 2 + h];
               const float4 r4 = reinterpret_cast<const float4*>(ref)[q * 2 + h];
-              unpack(fma2(f2(x[k], x[k + 1]), f2(c4.x, c4.y), f2(r4.x, r4.y)), x[k], x[k + 1]);
-              unpack(fma2(f2(x[k + 2], x[k + 3]), f2(c4.z, c4.w), f2(r4.z, r4.w)), x[k + 2], x[k + 3]);
-              top = fmaxf(top, fmaxf(x[k], x[k + 1]));
-              top = fmaxf(top, fmaxf(x[k + 2], x[k + 3]));
+              unpack(fma2(f2(s[k], s[k + 1]), f2(c4.x, c4.y), f2(r4.x, r4.y)), s[k], s[k + 1]);
+              unpack(fma2(f2(s[k + 2], s[k + 3]), f2(c4.z, c4.w), f2(r4.z, r4.w)), s[k + 2], s[k + 3]);
+              top = fmaxf(top, fmaxf(s[k], s[k + 1]));
+              top = fmaxf(top, fmaxf(s[k + 2], s[k + 3]));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[k + j] = fast_exp2(x[k + j]);
-              pk[2 * h] = h2_bits(__floats2half2_rn(x[k], x[k + 1]));
-              pk[2 * h + 1] = h2_bits(__floats2half2_rn(x[k + 2], x[k + 3]));
+              for (int j = 0; j < 4; ++j) s[k + j] = fast_exp2(s[k + j]);
+              pk[2 * h] = h2_bits(__floats2half2_rn(s[k], s[k + 1]));
+              pk[2 * h + 1] = h2_bits(__floats2half2_rn(s[k + 2], s[k + 3]));
             }
-            const uint32_t off = NT == 32 ? sw64_off(kl, q) : sw128_off(kl, wg * 4 + q);
-            st_shared_v4(prow + off, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+            st_shared_v4(pbuf + sw64_off(pr, q), make_uint4(pk[0], pk[1], pk[2], pk[3]));
           }
           fence_proxy_async_smem();
+          tc_fence_before();
           // all of P is written when the group passes; a key far above its row's reference
           // sends the tile through once more, after the references have moved
-          const bool again = group_or(bar_id, top > kMove || bad);
+          const bool again = group_or(bar_id, 128, top > kMove || bad);
           if (!again) break;
-          if (group_or(bar_id, bad)) goto done;
+          if (group_or(bar_id, 128, bad)) goto done;
           if (move) break;
           move = true;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(b));
-        if (sw == 0 && lane == 0) mbar_arrive(p_full(b));
+        if (lane == 0) mbar_arrive(s_free(i));
+        if (sw == 0 && lane == 0) mbar_arrive(p_full(i));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (q >= nc8) break;
 #pragma unroll
           for (int k = q * 8; k < q * 8 + 8; k += 2)
-            unpack(add2(f2(lacc[k], lacc[k + 1]), f2(x[k], x[k + 1])), lacc[k], lacc[k + 1]);
+            unpack(add2(f2(lacc[k], lacc[k + 1]), f2(s[k], s[k + 1])), lacc[k], lacc[k + 1]);
         }
+        last = g;
       }
-      if (nq > 0) {
-        // ---- epilogue: row sums over the group, O^T / l
-        sums[sw * 32 + lane] = transpose_reduce<false>(lacc, lane);
-        bad |= !wait_warp(pv_done((g - 1) & 1), ((g - 1) >> 1) & 1, cx);
-        if (group_or(bar_id, bad)) goto done;
-        const float l = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
+      // ---- epilogue: the two streams' row sums and references meet; the warps of stream x
+      // write columns 16 x .. + 15 of (w0 O0 + w1 O1) / (w0 l0 + w1 l1), w = 2^(ref - max ref)
+      {
+        float* sums = reinterpret_cast<float*>(bp + kOffSum) + ip * 256;
+        float* refs = reinterpret_cast<float*>(bp + kOffItemRef) + ip * 64;
+        sums[x * 128 + sw * 32 + lane] = transpose_reduce<false>(lacc, lane);
+        if (sw == 0) refs[x * 32 + lane] = mref;
+        if (last >= g0) bad |= !wait_warp(pv_done(last & 3), (last >> 2) & 1, cx);  // O^T of this stream whole
+        if (group_or(kBoth, 256, bad)) goto done;
+        tc_fence_after();
+        const float r0 = refs[lane], r1 = refs[32 + lane], m = fmaxf(r0, r1);
+        const float w0 = r0 == -INFINITY ? 0.f : fast_exp2(r0 - m);
+        const float w1 = r1 == -INFINITY ? 0.f : fast_exp2(r1 - m);
+        const float l0 = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
+        const float l1 = (sums[128 + lane] + sums[160 + lane]) + (sums[192 + lane] + sums[224 + lane]);
+        const float l = w0 * l0 + w1 * l1;
+        const float inv = l == 0.f ? 0.f : prm.o_unit / l;
+        alpha[lane] = w0 * inv;
+        alpha[32 + lane] = w1 * inv;
         const bool split = item.nsplit > 1;
-        alpha[lane] = l == 0.f ? 0.f : prm.o_unit / l;
         const long long row0 = (long long)item.c0 + item.i0;
-        const int n_l = wg * 32 + lane;
-        if (sw == 0 && lane < nq) {
-          const float v = (mref + log2f(l)) * 0.69314718055994530942f;
+        if (x == 0 && sw == 0 && lane < nq) {
+          const float v = (m + log2f(l)) * 0.69314718055994530942f;
           if (split)
-            prm.ws_lse[(long long)item.slot * kKT + n_l] = v;
+            prm.ws_lse[(long long)item.slot * kKT + lane] = v;
           else
-            prm.lse[(row0 + n_l / G) * prm.Hq + item.kvh * G + n_l % G] = v;
+            prm.lse[(row0 + lane / G) * prm.Hq + item.kvh * G + lane % G] = v;
         }
         __syncwarp();
-        tc_fence_after();
-        float o[32];
-        tmem_ld32(t_lane + C::TMEM_O + (n_it & 1) * NT, o);
-        tmem_wait_ld32(o);
-        if (split) {
-          float* dst = prm.ws_o + ((long long)item.slot * kKT + wg * 32) * kD + kl;
+        float o[16];
 #pragma unroll
-          for (int n = 0; n < 32; ++n)
-            if (n < nq) dst[n * kD] = o[n] * alpha[n];
+        for (int n = 0; n < 16; ++n) o[n] = 0.f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (g0 + ((g0 ^ y) & 1) >= g1) continue;  // that stream had no tile here
+          float u[16];
+          tmem_ld16(t_lane + kTmemO + (2 * y + ip) * kNT + 16 * x, u);
+          tmem_wait_ld16(u);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) o[n] = fmaf(u[n], alpha[32 * y + 16 * x + n], o[n]);
+        }
+        if (split) {
+          float* dst = prm.ws_o + ((long long)item.slot * kKT + 16 * x) * kD + kl;
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (16 * x + n < nq) dst[n * kD] = o[n];
         } else {
-          int h = (wg * 32) % G;
-          __nv_bfloat16* dst = prm.out + ((row0 + wg * 32 / G) * prm.Hq + item.kvh * G + h) * kD + kl;
+          int h = (16 * x) % G;
+          __nv_bfloat16* dst = prm.out + ((row0 + 16 * x / G) * prm.Hq + item.kvh * G + h) * kD + kl;
           const long long next = (long long)(prm.Hq - G) * kD;  // to the next block row's heads
 #pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            if (n < nq) *dst = __float2bfloat16(o[n] * alpha[n]);
+          for (int n = 0; n < 16; ++n) {
+            if (16 * x + n < nq) *dst = __float2bfloat16(o[n]);
             dst += kD;
             if (++h == G) {
               h = 0;
@@ -866,9 +982,10 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(o_free(n_it & 1));
-        mbar_arrive(q_empty(qb));
+        mbar_arrive(o_free(ip));
+        mbar_arrive(q_empty(ip));
       }
+      g0 = g1;
     }
   done:;
   }
@@ -876,7 +993,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1) verify_attn_kv4_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kQkWarp) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == kCopyWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- split combine
@@ -929,20 +1046,12 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
-template <int NT>
 static bool configure() {
   static PerDevice<bool> done;
   return once_per_device(done, false, [] {
-    return cudaFuncSetAttribute(verify_attn_kv4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg<NT>::SMEM_BYTES) == cudaSuccess;
+    return cudaFuncSetAttribute(verify_attn_kv4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemBytes) == cudaSuccess;
   });
-}
-
-template <int NT>
-static int launch_tile(const Params& p, int ncta, cudaStream_t stream) {
-  if (!configure<NT>()) return DSPARK_ECUDA;
-  return launch_pdl(verify_attn_kv4_kernel<NT>, dim3(ncta), dim3(Cfg<NT>::THREADS),
-                    Cfg<NT>::SMEM_BYTES, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }
 
 int launch(const void* q, const void* k_new, const void* v_new, const void* cache, int n_pages,
@@ -981,9 +1090,11 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   p.k_unit = 1.f / (16.f * gk);
   p.v_unit = 1.f / (16.f * gv);
   p.o_unit = 16.f * gv;
-  const int rc = pl.nt == 32 ? launch_tile<32>(p, pl.ncta, stream) : launch_tile<64>(p, pl.ncta, stream);
-  if (rc != DSPARK_OK) return rc;
-  return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, pl.nt / 8), dim3(256), 0, stream, cu_seqlens,
+  if (!configure()) return DSPARK_ECUDA;
+  if (launch_pdl(verify_attn_kv4_kernel, dim3(pl.ncta), dim3(kThreads), kSmemBytes, stream, p) !=
+      cudaSuccess)
+    return DSPARK_ECUDA;
+  return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, kNT / 8), dim3(256), 0, stream, cu_seqlens,
                     groups, Hq / Hkv, Hq, p.ws_o, p.ws_lse, p.out, lse, B, max_rows,
                     p.err) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }

@@ -47,19 +47,19 @@ def test_host_refusals(pkg):
                     dict(B=1025), dict(rows=0), dict(scale=0.0), dict(scale=float("nan")),
                     dict(splits=0), dict(splits=33)):
             assert call(name, **bad) == -1, (name, bad)
-        for bad in (dict(hq=9), dict(hq=130), dict(hkv=0), dict(page=8), dict(page=40)):
+        for bad in (dict(hq=9), dict(hq=66), dict(hkv=0), dict(page=8), dict(page=40)):
             assert call(name, **bad) == -2, (name, bad)
     # a plan of the pack call on a larger tile than this kernel has
-    assert call(names[1], hint=17) == -2
+    assert call(names[1], hint=9) == -2
     size = lib.dspark_verify_attn_kv4_workspace_size
-    assert size(2, 8, 9, 2, 8, 4) == 0 and size(0, 8, 8, 2, 8, 4) == 0 and size(2, 8, 130, 2, 8, 1) == 0
-    assert size(32, 512, 32, 8, 8, 1) >= size(32, 512, 32, 8, 8, 16) == size(32, 512, 32, 8, 8, 99) > 0
+    assert size(2, 8, 9, 2, 8, 4) == 0 and size(0, 8, 8, 2, 8, 4) == 0 and size(2, 8, 66, 2, 8, 1) == 0
+    assert size(32, 512, 32, 8, 8, 1) == size(32, 512, 32, 8, 8, 99) > 0
 
 
 def test_hint_and_binding_refusals(pkg):
-    assert pkg.block_rows_hint_for_kv4(8, 32, 8) == 9
-    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 16
-    assert pkg.block_rows_hint_for_kv4(6, 128, 2) == 1
+    assert pkg.block_rows_hint_for_kv4(6, 32, 8) == 7
+    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 8
+    assert pkg.block_rows_hint_for_kv4(6, 64, 2) == 1
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     c = pkg.kv4_cache(4, 2, 16, device="cpu")
@@ -180,7 +180,7 @@ SHAPES = [  # ctx, lens, hq, hkv, page
     ([300, 5, 1000, 640], [17, 17, 17, 17], 8, 2, 64),
     ([200, 700], [6, 3], 40, 8, 32),
     ([513, 90], [4, 2], 7, 1, 256),
-    ([140, 300], [3, 1], 64, 1, 16),
+    ([140, 300], [3, 1], 32, 1, 16),
     ([260, 0, 60], [33, 20, 1], 6, 2, 16),
     ([77, 130], [150, 140], 4, 4, 16),
     ([2500], [3], 16, 2, 128),

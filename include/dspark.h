@@ -552,9 +552,9 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * and v_scale in place of the two caches, and
  *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
  *   Hq / Hkv <= 32
- *   max_block_rows has no effect but in the planned form: the query tile holds 32 rows
- *        (32 / G block rows of G = Hq / Hkv heads), longer segments run as several row
- *        tiles.
+ *   max_block_rows: a hint as there; the query tile holds 8, 16 or 32 rows of
+ *        G = Hq / Hkv heads x block rows, the smallest that holds this many block rows
+ *        (or 32); longer segments run as several row tiles.
  * Rounding: the cached values and the queries are exact in the products' fp16
  * operands (a query row is scaled by a power of two; elements below 2^-30 of the row's
  * largest may lose bits), block rows are rounded to fp16 after division by
@@ -562,11 +562,7 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * fp16; sums are fp32, and out is rounded once to bf16.
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
  * undefined.
- *
- * dspark_verify_attn_kv4_planned runs over the work list that dspark_pack_plan wrote
- * (d_qk = d_v = 128, the same Hq, Hkv, max_rows, max_splits, max_block_rows and
- * workspace); DSPARK_EUNSUPPORTED if max_block_rows is above 32 / G, the rows of this
- * kernel's tile.
+ * Two kernels after the work list's; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
                                              int max_block_rows);
@@ -576,14 +572,6 @@ int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
                            const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
                            int page_size, float scale, int max_splits, int max_block_rows,
                            void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
-int dspark_verify_attn_kv4_planned(const void* q, const void* k_new, const void* v_new,
-                                   const void* kv_cache, float k_scale, float v_scale, int n_pages,
-                                   const int32_t* page_table, int max_pages,
-                                   const int32_t* ctx_len, const int32_t* cu_seqlens, int B,
-                                   int max_rows, int Hq, int Hkv, int page_size, float scale,
-                                   int max_splits, int max_block_rows, void* out, float* lse,
-                                   void* workspace, size_t ws_bytes, void* stream);
-
 /* ---------------------------------------------------------------------------
  * dspark_compact_kv4 -- dspark_compact into the 4-bit cache: the kept rows of k_new and
  * v_new (bf16 [max_rows, Hkv, 128], dense) are quantised as dspark_kv4_store does.

@@ -20,7 +20,7 @@ __all__ = [
     "verify_attn_workspace_size", "accept_workspace_size", "compact_workspace_size",
     "VerifyStep", "StepGraph", "CalibStore", "DEVERR",
     "qk_norm_rope", "KV4_BLOCK_BYTES", "kv4_cache", "kv4_store", "kv4_load",
-    "verify_attn_kv4", "verify_attn_kv4_planned", "verify_attn_kv4_workspace_size",
+    "verify_attn_kv4", "verify_attn_kv4_workspace_size",
     "block_rows_hint_for_kv4", "compact_kv4",
 ]
 
@@ -85,8 +85,6 @@ _SIGNATURES = {
     "dspark_verify_attn_kv4_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
     "dspark_verify_attn_kv4": (_I, [_P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I,
                                     _F, _I, _I, _P, _P, _P, _Z, _P]),
-    "dspark_verify_attn_kv4_planned": (_I, [_P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _I, _I, _I,
-                                            _I, _I, _F, _I, _I, _P, _P, _P, _Z, _P]),
     "dspark_compact_kv4": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                                 _P, _P, _F, _F, _P, _P, _P, _Z, _P]),
 }
@@ -505,26 +503,10 @@ def verify_attn_kv4(q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, 
                     out, lse, workspace, k_scale=1.0, v_scale=1.0, stream=None, max_block_rows=0):
     """verify_attn over the 4-bit cache: q [rows, Hq, 128], k_new / v_new [rows, Hkv, 128]
     bf16, kv_cache as kv4_cache gives it, out bf16 [rows, Hq, 128], lse fp32 [rows, Hq]."""
-    _verify_attn_kv4("dspark_verify_attn_kv4", q, k_new, v_new, kv_cache, page_table, ctx_len,
-                     cu_seqlens, scale, max_splits, out, lse, workspace, k_scale, v_scale, stream,
-                     max_block_rows)
-
-
-def verify_attn_kv4_planned(q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, scale,
-                            max_splits, out, lse, workspace, k_scale=1.0, v_scale=1.0, stream=None,
-                            max_block_rows=0):
-    """verify_attn_kv4 over the work list that pack_plan wrote into ``workspace``."""
-    _verify_attn_kv4("dspark_verify_attn_kv4_planned", q, k_new, v_new, kv_cache, page_table,
-                     ctx_len, cu_seqlens, scale, max_splits, out, lse, workspace, k_scale, v_scale,
-                     stream, max_block_rows)
-
-
-def _verify_attn_kv4(name, q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, scale,
-                     max_splits, out, lse, workspace, k_scale, v_scale, stream, max_block_rows):
     c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
     rows, Hq, _ = q.shape
     bf16 = torch.bfloat16
-    _check(name, getattr(lib(), name)(
+    _check("dspark_verify_attn_kv4", lib().dspark_verify_attn_kv4(
         _arg(q, "q", bf16, (rows, Hq, 128)), _arg(k_new, "k_new", bf16, (rows, Hkv, 128)),
         _arg(v_new, "v_new", bf16, (rows, Hkv, 128)), c, float(k_scale), float(v_scale), n_pages,
         tab, max_pages, _arg(ctx_len, "ctx_len", torch.int32, (B,)), cu, B, rows, Hq, Hkv, page,
@@ -644,7 +626,7 @@ class VerifyStep:
     fills; state (caches, page table, ctx_len, anchor, free stack) is updated in
     place by compact.
 
-    With ``kv4`` the cache is the 4-bit one: ``inp["kv_cache"]`` (see kv4_cache), with
+    With ``kv4`` (pack -> verify_attn_kv4, which builds its own work list) the cache is the 4-bit one: ``inp["kv_cache"]`` (see kv4_cache), with
     ``inp["k_scale"]`` and ``inp["v_scale"]`` (default 1), takes the place of k_cache and
     v_cache, and ``out`` is bf16.
 
@@ -726,15 +708,13 @@ class VerifyStep:
                      inp["v_new"], inp.get("eps", 1e-6), inp.get("interleaved", False),
                      inp.get("attn_factor", 1.0), stream, n_rows=self.M_pack)
 
-    def _attention_kv4(self, fn, inp, stream):
-        fn(inp["q"], inp["k_new"], inp["v_new"], inp["kv_cache"], inp["page_table"],
-           inp["ctx_len"], self.cu_seqlens, inp["scale"], self.max_splits, self.out, self.lse,
-           self.ws_attn, inp.get("k_scale", 1.0), inp.get("v_scale", 1.0), stream,
-           max_block_rows=self.block_rows_hint)
-
     def attention(self, inp, stream=None):
         if self.kv4:
-            self._attention_kv4(verify_attn_kv4, inp, stream)
+            verify_attn_kv4(inp["q"], inp["k_new"], inp["v_new"], inp["kv_cache"],
+                            inp["page_table"], inp["ctx_len"], self.cu_seqlens, inp["scale"],
+                            self.max_splits, self.out, self.lse, self.ws_attn,
+                            inp.get("k_scale", 1.0), inp.get("v_scale", 1.0), stream,
+                            max_block_rows=self.block_rows_hint)
             return
         verify_attn(inp["q"], inp["k_new"], inp.get("v_new"), inp["k_cache"], inp.get("v_cache"),
                     inp["page_table"], inp["ctx_len"], self.cu_seqlens, inp["scale"],
@@ -748,6 +728,8 @@ class VerifyStep:
     def pack_plan(self, inp, mode, stream=None):
         """pack, with the attention work list built in the same kernel (for attention_planned,
         which takes the query tile chosen here)."""
+        if self.kv4:
+            raise ValueError("the 4-bit cache's attention builds its own work list")
         self.block_rows_hint = self.hint(mode)
         pack_plan(self.windows, inp["ctx_len"], inp["anchor"], inp["draft_tok"], inp["tiers"], mode,
                   self.cu_seqlens, self.M_pack, self.tier, self.row_req, self.row_pos,
@@ -756,8 +738,7 @@ class VerifyStep:
 
     def attention_planned(self, inp, stream=None):
         if self.kv4:
-            self._attention_kv4(verify_attn_kv4_planned, inp, stream)
-            return
+            raise ValueError("the 4-bit cache's attention builds its own work list")
         verify_attn_planned(inp["q"], inp["k_new"], inp.get("v_new"), inp["k_cache"],
                             inp.get("v_cache"), inp["page_table"], inp["ctx_len"],
                             self.cu_seqlens, inp["scale"], self.max_splits, self.out, self.lse,
@@ -825,9 +806,9 @@ class VerifyStep:
 
     def run(self, inp, mode, stream=None):
         self.schedule(inp, mode, stream)
-        self.pack_plan(inp, mode, stream)
+        (self.pack if self.kv4 else self.pack_plan)(inp, mode, stream)
         if "q_in" in inp:
             self.norm_rope(inp, stream)
-        self.attention_planned(inp, stream)
+        (self.attention if self.kv4 else self.attention_planned)(inp, stream)
         self.accept(inp, mode, stream)
         self.compact(inp, stream)

@@ -542,17 +542,15 @@ static bool kv4_heads_ok(int Hq, int Hkv) {
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
                                              int max_block_rows) {
   if (B < 1 || max_rows < 1 || max_splits < 1 || max_splits > 32 || !kv4_heads_ok(Hq, Hkv)) return 0;
-  return attn::plan(B, max_rows, Hq, Hkv, 128, 128, max_splits,
-                    kv4_block_rows(Hq, Hkv, max_block_rows)).bytes;
+  return attn::kv4a::plan(B, max_rows, Hq, Hkv, kv4_block_rows(Hq, Hkv, max_block_rows)).bytes;
 }
 
-static int verify_attn_kv4_impl(const void* q, const void* k_new, const void* v_new,
-                                const void* kv_cache, float k_scale, float v_scale, int n_pages,
-                                const int32_t* page_table, int max_pages, const int32_t* ctx_len,
-                                const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
-                                int page_size, float scale, int max_splits, int max_block_rows,
-                                void* out, float* lse, void* workspace, size_t ws_bytes,
-                                void* stream, bool planned) {
+int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
+                           const void* kv_cache, float k_scale, float v_scale, int n_pages,
+                           const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                           const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
+                           int page_size, float scale, int max_splits, int max_block_rows,
+                           void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   CHECK(kv4_heads_ok(Hq, Hkv), DSPARK_EUNSUPPORTED);
   int rc = kv4_args(kv_cache, cu_seqlens, page_table, B, max_rows, Hkv, page_size, max_pages,
                     n_pages, k_scale, v_scale);
@@ -562,41 +560,14 @@ static int verify_attn_kv4_impl(const void* q, const void* k_new, const void* v_
   CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
   CHECK(max_splits >= 1 && max_splits <= 32, DSPARK_EINVAL);
   CHECK(positive(scale), DSPARK_EINVAL);
-  const int rows = kv4_block_rows(Hq, Hkv, max_block_rows);
-  CHECK(!planned || max_block_rows <= rows, DSPARK_EUNSUPPORTED);  // the pack call's tile
   rc = device_ok();
   if (rc != DSPARK_OK) return rc;
-  const attn::Plan pl = attn::plan(B, max_rows, Hq, Hkv, 128, 128, max_splits, rows);
+  const attn::Plan pl =
+      attn::kv4a::plan(B, max_rows, Hq, Hkv, kv4_block_rows(Hq, Hkv, max_block_rows));
   CHECK(ws_bytes >= pl.bytes, DSPARK_ENOSPACE);
   return attn::kv4a::launch(q, k_new, v_new, kv_cache, n_pages, page_table, max_pages, ctx_len,
                             cu_seqlens, B, max_rows, Hq, Hkv, page_size, scale, k_scale, v_scale,
-                            max_splits, out, lse, workspace, pl, static_cast<cudaStream_t>(stream),
-                            planned);
-}
-
-int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
-                           const void* kv_cache, float k_scale, float v_scale, int n_pages,
-                           const int32_t* page_table, int max_pages, const int32_t* ctx_len,
-                           const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
-                           int page_size, float scale, int max_splits, int max_block_rows,
-                           void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
-  return verify_attn_kv4_impl(q, k_new, v_new, kv_cache, k_scale, v_scale, n_pages, page_table,
-                              max_pages, ctx_len, cu_seqlens, B, max_rows, Hq, Hkv, page_size,
-                              scale, max_splits, max_block_rows, out, lse, workspace, ws_bytes,
-                              stream, false);
-}
-
-int dspark_verify_attn_kv4_planned(const void* q, const void* k_new, const void* v_new,
-                                   const void* kv_cache, float k_scale, float v_scale, int n_pages,
-                                   const int32_t* page_table, int max_pages,
-                                   const int32_t* ctx_len, const int32_t* cu_seqlens, int B,
-                                   int max_rows, int Hq, int Hkv, int page_size, float scale,
-                                   int max_splits, int max_block_rows, void* out, float* lse,
-                                   void* workspace, size_t ws_bytes, void* stream) {
-  return verify_attn_kv4_impl(q, k_new, v_new, kv_cache, k_scale, v_scale, n_pages, page_table,
-                              max_pages, ctx_len, cu_seqlens, B, max_rows, Hq, Hkv, page_size,
-                              scale, max_splits, max_block_rows, out, lse, workspace, ws_bytes,
-                              stream, true);
+                            max_splits, out, lse, workspace, pl, static_cast<cudaStream_t>(stream));
 }
 
 int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_rows,

@@ -74,12 +74,14 @@ bool encode_f32_map(CUtensorMap* m, const void* base, int rank, const uint64_t* 
 }  // namespace gqa
 
 namespace kv4a {
-// The attention over the 4-bit cache, on plan `pl` (a query tile of 32 rows).
+// The attention over the 4-bit cache.  Its plan: a query tile of 8, 16 or 32 rows, several
+// CTAs per SM.
+Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows);
 int launch(const void* q, const void* k_new, const void* v_new, const void* cache, int n_pages,
            const int32_t* page_table, int max_pages, const int32_t* ctx_len,
            const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv, int page_size,
            float scale, float gk, float gv, int max_splits, void* out, float* lse, void* ws,
-           const Plan& pl, cudaStream_t stream, bool planned);
+           const Plan& pl, cudaStream_t stream);
 }  // namespace kv4a
 
 namespace mla {

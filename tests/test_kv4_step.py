@@ -84,13 +84,7 @@ def test_three_steps(pkg, mode):
                            before["ctx_len"].numpy(), d["page_table"].cpu().numpy(),
                            before["kv_cache"].numpy(), gk, gv, n_keep=keep + 1)
         assert np.array_equal(cache.cpu().numpy(), want)
-    # the call with its own work list gives the same rows, and the graph form is refused
-    d["ctx_len"].copy_(before["ctx_len"])
-    planned = step.out.clone()
-    step.block_rows_hint = step.hint(mode)
-    d["kv_cache"] = before["kv_cache"].cuda()
-    step.attention(d)
-    torch.cuda.synchronize()
-    assert torch.equal(step.out[:M], planned[:M])
-    with pytest.raises(ValueError):
-        step.graph(d, mode)
+    for refused in (lambda: step.graph(d, mode), lambda: step.pack_plan(d, mode),
+                    lambda: step.attention_planned(d)):
+        with pytest.raises(ValueError):
+            refused()

@@ -33,27 +33,24 @@ def pkg():
 # ------------------------------------------------------------------ refusals (CPU)
 def test_host_refusals(pkg):
     lib, f, off = pkg.load(), ctypes.c_void_p(4096), ctypes.c_void_p(4104)
-    names = ("dspark_verify_attn_kv4", "dspark_verify_attn_kv4_planned")
 
-    def call(name, q=f, c=f, gk=1.0, gv=1.0, tab=f, ctx=f, cu=f, B=2, rows=8, hq=8, hkv=2, page=16,
+    def call(q=f, c=f, gk=1.0, gv=1.0, tab=f, ctx=f, cu=f, B=2, rows=8, hq=8, hkv=2, page=16,
              scale=0.1, splits=8, hint=4, out=f, lse=f, ws=f, n=1 << 30):
-        return getattr(lib, name)(q, f, f, c, gk, gv, 9, tab, 4, ctx, cu, B, rows, hq, hkv, page,
+        return lib.dspark_verify_attn_kv4(q, f, f, c, gk, gv, 9, tab, 4, ctx, cu, B, rows, hq, hkv, page,
                                   ctypes.c_float(scale), splits, hint, out, lse, ws, n, None)
 
-    for name in names:
-        for bad in (dict(q=None), dict(c=None), dict(tab=None), dict(ctx=None), dict(cu=None),
-                    dict(out=None), dict(lse=None), dict(ws=None), dict(q=off), dict(c=off),
-                    dict(out=off), dict(ws=off), dict(gk=0.0), dict(gv=float("nan")), dict(B=0),
-                    dict(B=1025), dict(rows=0), dict(scale=0.0), dict(scale=float("nan")),
-                    dict(splits=0), dict(splits=33)):
-            assert call(name, **bad) == -1, (name, bad)
-        for bad in (dict(hq=9), dict(hq=66), dict(hkv=0), dict(page=8), dict(page=40)):
-            assert call(name, **bad) == -2, (name, bad)
-    # a plan of the pack call on a larger tile than this kernel has
-    assert call(names[1], hint=9) == -2
+    for bad in (dict(q=None), dict(c=None), dict(tab=None), dict(ctx=None), dict(cu=None),
+                dict(out=None), dict(lse=None), dict(ws=None), dict(q=off), dict(c=off),
+                dict(out=off), dict(ws=off), dict(gk=0.0), dict(gv=float("nan")), dict(B=0),
+                dict(B=1025), dict(rows=0), dict(scale=0.0), dict(scale=float("nan")),
+                dict(splits=0), dict(splits=33)):
+        assert call(**bad) == -1, bad
+    for bad in (dict(hq=9), dict(hq=66), dict(hkv=0), dict(page=8), dict(page=40)):
+        assert call(**bad) == -2, bad
     size = lib.dspark_verify_attn_kv4_workspace_size
     assert size(2, 8, 9, 2, 8, 4) == 0 and size(0, 8, 8, 2, 8, 4) == 0 and size(2, 8, 66, 2, 8, 1) == 0
-    assert size(32, 512, 32, 8, 8, 1) == size(32, 512, 32, 8, 8, 99) > 0
+    assert size(32, 512, 32, 8, 8, 0) == size(32, 512, 32, 8, 8, 2) > 0
+    assert size(32, 512, 32, 8, 8, 8) == size(32, 512, 32, 8, 8, 99) > 0
 
 
 def test_hint_and_binding_refusals(pkg):

@@ -95,14 +95,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-// 16 bytes, or v as it was where p is NULL.
-__device__ __forceinline__ void ldg16(uint4& v, const uint8_t* p) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.u64 q, %4, 0;\n\t"
-      "@q ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p));
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -179,38 +177,41 @@ struct Smem {
   float sum[4][8 * NT];      // row sums of an item per warp
 };
 
-// The cache tiles of a CTA in order, looked at one tile ahead of their loads.
+// The cache tiles of a CTA in order, looked up two tiles ahead of their use: lane b < 8 of a
+// warp looks for block b of a tile, and turns the page into the block's index only when
+// the tile's loads are issued, so that nothing waits for the page table.
 struct Ahead {
   const Params& p;
-  int it, it_end, t, te, r, ctx, kvh;
-  bool more;
-  __device__ __forceinline__ void take(int at) {
-    more = at < it_end;
-    if (!more) return;
-    it = at;
-    const AttnItem* x = p.items + at;
-    t = x->tb; te = x->te; r = x->r; ctx = x->ctx; kvh = x->kvh;
-  }
-  // Page of block b (0..7) of the tile; kNone where it holds no committed key.
+  int it, it_end, t, te, ctx;
+  const int32_t* table;   // the request's pages
+  int head;               // kvh * blocks of a page
+  int page, sub;          // looked up: the page of this lane's block, its place in the page
   static constexpr int kNone = -0x7fffffff;
-  __device__ __forceinline__ int page(int b) const {
-    const int pos = t * kKT + b * kBlock;
-    if (!more || pos >= ctx) return kNone;
-    const int slot = pos >> p.log2_page;
-    return slot < p.max_pages ? __ldg(p.page_table + (long long)r * p.max_pages + slot) : -1;
+  __device__ __forceinline__ void take(int at) {
+    it = at;
+    if (at >= it_end) return;
+    const AttnItem* x = p.items + at;
+    t = x->tb; te = x->te; ctx = x->ctx;
+    table = p.page_table + (long long)x->r * p.max_pages;
+    head = x->kvh << (p.log2_page - 4);
   }
-  // The block's address; NULL where there is none to load (its keys are masked, or, behind a
-  // bad page, undefined).
-  __device__ __forceinline__ const uint8_t* address(int page, int b) const {
-    const int per = 1 << (p.log2_page - 4);
-    const int pos = t * kKT + b * kBlock;
-    if (page >= 0 && page < p.n_pages)
-      return p.cache + (((long long)page * p.Hkv + kvh) * per + ((pos >> 4) & (per - 1))) * kBlockBytes;
+  __device__ __forceinline__ void look(int b) {
+    const int pos = t * kKT + b * kBlock, slot = pos >> p.log2_page;
+    page = kNone;
+    if (it >= it_end || pos >= ctx) return;
+    sub = head + ((pos >> 4) & ((1 << (p.log2_page - 4)) - 1));
+    page = -1;
+    if (slot < p.max_pages) page = __ldg(table + slot);
+  }
+  // Index of the block among all blocks of the cache; -1 where it holds no committed key or
+  // its page is bad (its keys are then masked, or undefined).
+  __device__ __forceinline__ int block() const {
+    if ((unsigned)page < (unsigned)p.n_pages) return ((page * p.Hkv) << (p.log2_page - 4)) + sub;
     if (page != kNone) raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
-    return nullptr;
+    return -1;
   }
   __device__ __forceinline__ void advance() {
-    if (more && ++t == te) take(it + 1);
+    if (it < it_end && ++t == te) take(it + 1);
   }
 };
 
@@ -225,44 +226,47 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   if (it_begin >= it_end) return;
   const int G = prm.Hq / prm.Hkv;
   const uint32_t sq = smem_u32(S.q), sp = smem_u32(S.p);
+  // Key 16 b + tok of a tile is inner index 64 (b >> 2) + 16 (tok >> 2) + 8 ((tok >> 1) & 1) +
+  // 2 (b & 3) + (tok & 1) of the PV product, the order of V's fragments: this thread's first
+  // key (b = 2 w, tok = g); block 2 w + i is 2 i further, tok + 8 another 32
+  const int p_row = 64 * (w >> 1) + 16 * (g >> 2) + 8 * ((g >> 1) & 1) + 4 * (w & 1) + (g & 1);
 
-  // ---- loads ahead: pages of the next tile, then its K codes and scales
-  Ahead ahead{prm, 0, it_end, 0, 0, 0, 0, 0, false};
+  // ---- loads ahead: blocks of the tile after the next, K codes and scales of the next
+  Ahead ahead{prm, 0, it_end, 0, 0, 0, nullptr, 0, 0, 0};
   ahead.take(it_begin);
-  int kpage[2], vpage[2];   // K: blocks 2 w + {0, 1}; V: blocks t4 + {0, 4}
-  auto look = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      kpage[i] = ahead.page(2 * w + i);
-      vpage[i] = ahead.page(t4 + 4 * i);
-    }
-  };
+  ahead.look(lane & 7);
+  const uint8_t* const base_k = prm.cache + t4 * 256 + g * 16;
+  const uint8_t* const base_ks = prm.cache + kOffKs + g * 4 + t4;
+  const uint8_t* const base_v = prm.cache + kOffV + (32 * w + 2 * g) * 8;
+  const uint8_t* const base_vs = prm.cache + kOffVs + w * kBlock;
+  int vblk[2] = {-1, -1};   // blocks t4, t4 + 4 of the tile that K was loaded for
   uint4 kc[4] = {};         // codes of tokens g, g + 8 of the warp's two blocks, group t4
   uint32_t ks[4] = {};      // their scales
-  const uint8_t* vsrc[2];   // V blocks of the tile that K was loaded for
   auto load_k = [&]() {
+    const int blk = ahead.block();  // lane b: block b of the tile
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint8_t* blk = ahead.address(kpage[i], 2 * w + i);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ldg16(kc[2 * i + h], blk ? blk + t4 * 256 + (g + 8 * h) * 16 : nullptr);
-        if (blk) ks[2 * i + h] = __ldg(blk + kOffKs + (g + 8 * h) * 4 + t4);
+      const int b = __shfl_sync(0xffffffffu, blk, 2 * w + i);
+      vblk[i] = __shfl_sync(0xffffffffu, blk, t4 + 4 * i);
+      if (b >= 0) {  // uniform over the warp
+        const uint8_t* kp = base_k + (long long)b * kBlockBytes;
+        const uint8_t* sp = base_ks + (long long)b * kBlockBytes;
+        kc[2 * i] = ldg16(kp);
+        kc[2 * i + 1] = ldg16(kp + 128);
+        ks[2 * i] = __ldg(sp);
+        ks[2 * i + 1] = __ldg(sp + 32);
       }
-      vsrc[i] = ahead.address(vpage[i], t4 + 4 * i);
     }
+    ahead.advance();
+    ahead.look(lane & 7);
   };
-  look();
   load_k();
-  ahead.advance();
-  look();
   uint4 vc[4] = {}, vsc[2] = {};  // V codes of channels 2 g, 2 g + 1 of 16 i; scales
 
   for (int it = it_begin; it < it_end; ++it) {
     const AttnItem item = prm.items[it];
     const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
     const int nq = item.ni * G;              // rows of the tile
-    const int nj = (nq + 7) >> 3;            // n-tiles that hold one
     const long long row0 = (long long)item.c0 + item.i0;
     // ---- Q: row n = (block row n / G, head kvh G + n % G), fp16 scaled by a power of two; a
     // half-warp holds a row, 8 dims per lane.  Dim 32 t + 4 s + e is at inner index
@@ -318,11 +322,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       // ---- V of this tile on its way
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint8_t* blk = vsrc[u];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          ldg16(vc[2 * u + i], blk ? blk + kOffV + (32 * w + 16 * i + 2 * g) * 8 : nullptr);
-        ldg16(vsc[u], blk ? blk + kOffVs + w * kBlock : nullptr);
+        if (vblk[u] >= 0) {
+          const uint8_t* vp = base_v + (long long)vblk[u] * kBlockBytes;
+          vc[2 * u] = ldg16(vp);
+          vc[2 * u + 1] = ldg16(vp + 128);
+          vsc[u] = ldg16(base_vs + (long long)vblk[u] * kBlockBytes);
+        }
       }
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
@@ -330,91 +335,80 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
-      // inner steps 2 c, 2 c + 1 from the four pairs of the row's and the row + 8's word
-      auto qk = [&](int i, int c, const uint32_t (&lo)[4], const uint32_t (&hi)[4]) {
+      // inner steps 2 c and 2 c + 1: Q's fragments, and the products with those of one m-tile from
+      // the four pairs of row g's and row g + 8's word
+      auto q_frags = [&](int c, uint32_t (&b)[NT][4]) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ldsm4(b[j], sq + q_off(8 * j + (lane & 7), 4 * c + (lane >> 3)));
+      };
+      auto qk = [&](float (&d)[NT][4], const uint32_t (&b)[NT][4], const uint32_t (&lo)[4],
+                    const uint32_t (&hi)[4]) {
         const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j >= nj) break;
-          uint32_t b[4];  // steps 2 c and 2 c + 1 of n-tile j
-          ldsm4(b, sq + q_off(8 * j + (lane & 7), 4 * c + (lane >> 3)));
-          mma(s[i][j], a0, b[0], b[1]);
-          mma(s[i][j], a1, b[2], b[3]);
-        }
+        for (int j = 0; j < NT; ++j) mma(d[j], a0, b[j][0], b[j][1]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma(d[j], a1, b[j][2], b[j][3]);
       };
       if (cached) {
+        uint32_t sl[4], sh[4], bl[4], bh[4];  // per key: m-tile i, row g + 8 h at 2 i + h
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint32_t sl[2], sh[2], bl[2], bh[2];
           const uint32_t two = e4m3x2_to_h2(ks[2 * i] | (ks[2 * i + 1] << 8));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t sc = __byte_perm(two, 0, h ? 0x3232 : 0x1010);
-            sl[h] = hmul2_bits(sc, kSixteenth);
-            sh[h] = hmul2_bits(sc, k256th);
-            bl[h] = hmul2_bits(sc, kBiasLow);
-            bh[h] = hmul2_bits(sc, kBiasHigh);
-          }
-          const uint32_t x[4] = {kc[2 * i].x, kc[2 * i].y, kc[2 * i].z, kc[2 * i].w};
-          const uint32_t y[4] = {kc[2 * i + 1].x, kc[2 * i + 1].y, kc[2 * i + 1].z, kc[2 * i + 1].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t lo[4], hi[4];
-            expand(x[c], sl[0], bl[0], sh[0], bh[0], sl[0], bl[0], sh[0], bh[0], lo);
-            expand(y[c], sl[1], bl[1], sh[1], bh[1], sl[1], bl[1], sh[1], bh[1], hi);
-            qk(i, c, lo, hi);
+            sl[2 * i + h] = hmul2_bits(sc, kSixteenth);
+            sh[2 * i + h] = hmul2_bits(sc, k256th);
+            bl[2 * i + h] = hmul2_bits(sc, kBiasLow);
+            bh[2 * i + h] = hmul2_bits(sc, kBiasHigh);
           }
         }
-      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t b[NT][4];
+          q_frags(c, b);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = 2 * i + h;
+              const uint32_t word = c == 0 ? kc[k].x : c == 1 ? kc[k].y : c == 2 ? kc[k].z : kc[k].w;
+              expand(word, sl[k], bl[k], sh[k], bh[k], sl[k], bl[k], sh[k], bh[k], x[h]);
+            }
+            qk(s[i], b, x[0], x[1]);
+          }
+        }
+      } else if (32 * w < vis) {
         // the request's own rows, bf16 / (16 k_scale)
-        const int b0 = (t - ct) * kKT;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            prm.k_new + ((long long)(item.c0 + (t - ct) * kKT + 32 * w + g) * prm.Hkv + item.kvh) * kD + t4 * 32);
+        const int step = prm.Hkv * kD;  // 8 rows of 8-element pieces
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          if (32 * w + 16 * i >= vis) break;  // uniform over the warp
-          uint4 x[2][4];
+        for (int c = 0; c < 4; ++c) {
+          uint4 v[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = 32 * w + 16 * i + g + 8 * h;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                prm.k_new + ((long long)(item.c0 + b0 + k) * prm.Hkv + item.kvh) * kD + t4 * 32);
+          for (int k = 0; k < 4; ++k)
+            v[k] = 32 * w + g + 8 * k < vis ? src[(long long)k * step + c] : make_uint4(0, 0, 0, 0);
+          uint32_t b[NT][4];
+          q_frags(c, b);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[h][c] = k < vis ? src[c] : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 u = v[2 * i + h];
+              const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                x[h][q] = pack16(bf_lo(y[q]) * prm.k_unit, bf_hi(y[q]) * prm.k_unit);
+            }
+            qk(s[i], b, x[0], x[1]);
           }
-          const float f = prm.k_unit;
-          float z[NT][4];
-#pragma unroll
-          for (int j = 0; j < NT; ++j) z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t u[2][4] = {{x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w},
-                                      {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w}};
-            uint32_t lo[4], hi[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              lo[q] = pack16(bf_lo(u[0][q]) * f, bf_hi(u[0][q]) * f);
-              hi[q] = pack16(bf_lo(u[1][q]) * f, bf_hi(u[1][q]) * f);
-            }
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              uint32_t b[4];
-              ldsm4(b, sq + q_off(8 * j + (lane & 7), 4 * c + (lane >> 3)));
-              mma(z[j], a0, b[0], b[1]);
-              mma(z[j], a1, b[2], b[3]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (i == 0) s[0][j][q] = z[j][q]; else s[1][j][q] = z[j][q];
-            }
         }
       }
-      // ---- K of the next tile on its way (and the pages of the one after)
+      // ---- K of the next tile on its way (and the blocks of the one after looked up)
       load_k();
-      ahead.advance();
-      look();
       // ---- masks: s[i][j][2 h + e] is key 32 w + 16 i + g + 8 h, row 8 j + 2 t4 + e; a block
       // row b is seen by rows n >= (b - i0) G
       if (!cached || vis < kKT) {
@@ -472,15 +466,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            // key 16 b + tok of the tile, b = 2 w + i, is inner index 64 (b >> 2) + 16 (tok >> 2) +
-            // 8 ((tok >> 1) & 1) + 2 (b & 3) + (tok & 1): the order of V's fragments; block
-            // rows keep theirs
-            const int b = 2 * w + i, tok = g + 8 * h;
-            const int at = cached ? 64 * (b >> 2) + 16 * (tok >> 2) + 8 * ((tok >> 1) & 1) + 2 * (b & 3) + (tok & 1)
-                                  : 16 * b + tok;
+            const int at = p_row + 2 * i + 32 * h;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              if (j >= nj) break;
               const float x0 = fmaf(s[i][j][2 * h], cf[j][0], -ref[j][0]);
               const float x1 = fmaf(s[i][j][2 * h + 1], cf[j][1], -ref[j][1]);
               top = fmaxf(top, fmaxf(x0, x1));
@@ -502,84 +490,77 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         }
         move = true;
       }
-      // ---- O^T: two m-tiles of 16 channels, rows g and g + 8 being channels 2 g and 2 g + 1
-      if (cached) {
+      // ---- O^T: two m-tiles of 16 channels, rows g and g + 8 being channels 2 g and 2 g + 1;
+      // inner steps 4 u + 2 h, + 1 from the four key pairs of either channel's word
+      auto pv = [&](int u, int h, const uint32_t (&lo)[2][4], const uint32_t (&hi)[2][4]) {
+        uint32_t b[NT][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {  // 64 keys
-          // scale pairs of block t4 + 4 u, channels' group w; masked keys get scale 0
-          uint32_t x[4] = {vsc[u].x, vsc[u].y, vsc[u].z, vsc[u].w};
-          if (vis < kKT) {
+        for (int j = 0; j < NT; ++j) ldsm4_t(b[j], pbuf + p_off<NT>(64 * u + 32 * h + lane, j));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a0[4] = {lo[i][0], hi[i][0], lo[i][1], hi[i][1]};
+          const uint32_t a1[4] = {lo[i][2], hi[i][2], lo[i][3], hi[i][3]};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma(o[i][j], a0, b[j][0], b[j][1]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma(o[i][j], a1, b[j][2], b[j][3]);
+        }
+      };
+      if (cached) {
+        if (vis < kKT) {  // masked keys get scale 0, whatever their page holds
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t* x = reinterpret_cast<uint32_t*>(&vsc[u]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int left = vis - (t4 + 4 * u) * kBlock - 4 * q;
               if (left < 4) x[q] = left <= 0 ? 0u : x[q] & ((1u << (8 * left)) - 1u);
             }
           }
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 8 keys of the block
-            uint32_t ss[4], bb[4];
+        for (int u = 0; u < 2; ++u)      // block t4 + 4 u
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 8 keys of it
+            uint32_t ss[4], bb[4];       // scale pairs of the channels' group
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint32_t s0 = e4m3x2_to_h2(x[2 * h + q] & 0xffffu), s1 = e4m3x2_to_h2(x[2 * h + q] >> 16);
+              const uint32_t x = h ? (q ? vsc[u].w : vsc[u].z) : (q ? vsc[u].y : vsc[u].x);
+              const uint32_t s0 = e4m3x2_to_h2(x & 0xffffu), s1 = e4m3x2_to_h2(x >> 16);
               ss[2 * q] = hmul2_bits(s0, kSixteenth);
               bb[2 * q] = hmul2_bits(s0, kBiasLow);
               ss[2 * q + 1] = hmul2_bits(s1, k256th);
               bb[2 * q + 1] = hmul2_bits(s1, kBiasHigh);
             }
-            uint32_t a0[2][4], a1[2][4];
+            uint32_t lo[2][4], hi[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint4 c = vc[2 * u + i];  // channel 2 g: x, y; channel 2 g + 1: z, w
-              uint32_t lo[4], hi[4];
-              expand(h ? c.y : c.x, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], lo);
-              expand(h ? c.w : c.z, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], hi);
-              a0[i][0] = lo[0]; a0[i][1] = hi[0]; a0[i][2] = lo[1]; a0[i][3] = hi[1];
-              a1[i][0] = lo[2]; a1[i][1] = hi[2]; a1[i][2] = lo[3]; a1[i][3] = hi[3];
+              expand(h ? c.y : c.x, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], lo[i]);
+              expand(h ? c.w : c.z, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], hi[i]);
             }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              if (j >= nj) break;
-              uint32_t b[4];  // inner steps 4 u + 2 h, + 1
-              ldsm4_t(b, pbuf + p_off<NT>(64 * u + 32 * h + lane, j));
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mma(o[i][j], a0[i], b[0], b[1]);
-                mma(o[i][j], a1[i], b[2], b[3]);
-              }
-            }
+            pv(u, h, lo, hi);
           }
-        }
       } else {
-        const int b0 = (t - ct) * kKT;
         const uint32_t* vn = reinterpret_cast<const uint32_t*>(
-            prm.v_new + ((long long)(item.c0 + b0) * prm.Hkv + item.kvh) * kD) + (32 * w) / 2 + g;
+            prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD) + 16 * w + g;
         const long long step = (long long)prm.Hkv * kD / 2;
-        const float f = prm.v_unit;
 #pragma unroll 1
-        for (int c = 0; 32 * c < vis; ++c) {  // 32 rows: two inner steps
-          uint32_t a[2][2][4];
+        for (int n = 0; n < 4; ++n) {
+          if (64 * (n >> 1) >= vis) break;
+          uint32_t lo[2][4], hi[2][4];
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int k = 32 * c + 16 * x + 8 * h + 2 * t4;
-                const uint32_t y = k < vis ? vn[k * step + 8 * i] : 0u;
-                const uint32_t z = k + 1 < vis ? vn[(k + 1) * step + 8 * i] : 0u;
-                a[x][i][2 * h] = pack16(bf_lo(y) * f, bf_lo(z) * f);
-                a[x][i][2 * h + 1] = pack16(bf_hi(y) * f, bf_hi(z) * f);
-              }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t b[4];
-            ldsm4_t(b, pbuf + p_off<NT>(32 * c + lane, j));
+          for (int p = 0; p < 4; ++p) {
+            const int k = 16 * (t4 + 4 * (n >> 1)) + 8 * (n & 1) + 2 * p;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              mma(o[i][j], a[0][i], b[0], b[1]);
-              mma(o[i][j], a[1][i], b[2], b[3]);
+              const uint32_t y = k < vis ? vn[k * step + 8 * i] : 0u;
+              const uint32_t z = k + 1 < vis ? vn[(k + 1) * step + 8 * i] : 0u;
+              lo[i][p] = pack16(bf_lo(y) * prm.v_unit, bf_lo(z) * prm.v_unit);
+              hi[i][p] = pack16(bf_hi(y) * prm.v_unit, bf_hi(z) * prm.v_unit);
             }
           }
+          pv(n >> 1, n & 1, lo, hi);
         }
       }
     }

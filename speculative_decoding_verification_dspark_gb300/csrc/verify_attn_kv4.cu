@@ -40,8 +40,8 @@
 // The softmax takes a tile in one pass against the row references of the tiles before; only if
 // some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
 // references move and O and the sums with them.  That vote and the hand-over of P are the
-// tile's one barrier.  K's loads for the next tile are issued when this tile's K has been
-// used, V's when the tile begins, so that both are in flight while the team computes.
+// tile's one barrier.  Each thread copies what it will itself expand into a ring of
+// stages by cp.async (its warp shares only the scales), a tile or two ahead.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -66,8 +66,16 @@ constexpr float kMove = 14.f;          // a key above reference + 14 moves it
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key
 constexpr int kMaxCtas = 1024;         // the work list's limit
 
-// CTAs per SM, by registers: the fragments of O^T and S^T are 8 NT registers each.
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 5 : NT == 2 ? 4 : 3; }
+// CTAs per SM, by registers (the fragments of O^T and S^T are 8 NT each), and the cache tiles
+// that each has in its ring.
+__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
+__host__ __device__ constexpr int stages(int NT) { return NT == 1 ? 2 : 3; }
+// A warp's share of a stage: what its threads expand, each in its own order.
+constexpr int kStageK = 0;         // [2 blocks][tokens g, g + 8][lane][16 B]
+constexpr int kStageV = 2048;      // [blocks t4, t4 + 4][16 channels][lane][16 B]
+constexpr int kStageKs = 4096;     // [32 tokens][4 groups]
+constexpr int kStageVs = 4224;     // [8 blocks][16 tokens]
+constexpr int kWarpStage = 4352;
 
 struct Params {
   const __nv_bfloat16 *q, *k_new, *v_new;
@@ -95,12 +103,29 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(addr)
+               : "memory");
   return v;
+}
+__device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -134,20 +159,34 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
 // The expansion's constants as fp16 pairs: 1/16, 1/256, -64.5, -4.5.
 constexpr uint32_t kSixteenth = 0x2c002c00u, k256th = 0x1c001c00u, kBiasLow = 0xd408d408u,
                    kBiasHigh = 0xc480c480u;
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return (uint32_t)r.x | ((uint32_t)r.y << 16);
+// Two e4m3 numbers in the low (high) half of a register as an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3_low(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_high(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+// (w & MASK) | magic in one instruction (magic in a register: two immediates would take two).
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return r;
 }
 // Eight codes of a word -> four pairs (code - 8) s / 16: pair p with s[p], b[p] as the
 // head of the file has them for even (low nibbles) and odd (high nibbles) p.
-__device__ __forceinline__ void expand(uint32_t w, uint32_t s0, uint32_t b0, uint32_t s1,
-                                       uint32_t b1, uint32_t s2, uint32_t b2, uint32_t s3,
-                                       uint32_t b3, uint32_t (&o)[4]) {
+__device__ __forceinline__ void expand(uint32_t w, uint32_t magic, uint32_t s0, uint32_t b0,
+                                       uint32_t s1, uint32_t b1, uint32_t s2, uint32_t b2,
+                                       uint32_t s3, uint32_t b3, uint32_t (&o)[4]) {
   const uint32_t w8 = w >> 8;
-  o[0] = hfma2_bits((w & 0x000f000fu) | 0x64006400u, s0, b0);
-  o[1] = hfma2_bits((w & 0x00f000f0u) | 0x64006400u, s1, b1);
-  o[2] = hfma2_bits((w8 & 0x000f000fu) | 0x64006400u, s2, b2);
-  o[3] = hfma2_bits((w8 & 0x00f000f0u) | 0x64006400u, s3, b3);
+  o[0] = hfma2_bits(masked<0x000f000fu>(w, magic), s0, b0);
+  o[1] = hfma2_bits(masked<0x00f000f0u>(w, magic), s1, b1);
+  o[2] = hfma2_bits(masked<0x000f000fu>(w8, magic), s2, b2);
+  o[3] = hfma2_bits(masked<0x00f000f0u>(w8, magic), s3, b3);
 }
 // x in cache units, two of them as fp16, saturating (a NaN stays one).
 __device__ __forceinline__ float sat16(float x) {
@@ -175,11 +214,12 @@ struct Smem {
   float cf[8 * NT];          // softmax scale per row
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
+  __align__(16) uint8_t ring[stages(NT)][4][kWarpStage];
 };
 
-// The cache tiles of a CTA in order, looked up two tiles ahead of their use: lane b < 8 of a
+// The cache tiles of a CTA in order, looked up a tile ahead of their copies: lane b < 8 of a
 // warp looks for block b of a tile, and turns the page into the block's index only when
-// the tile's loads are issued, so that nothing waits for the page table.
+// the tile's copies are issued, so that nothing waits for the page table.
 struct Ahead {
   const Params& p;
   int it, it_end, t, te, ctx;
@@ -217,7 +257,9 @@ struct Ahead {
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_kernel(const Params prm) {
-  __shared__ Smem<NT> S;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<NT>& S = *reinterpret_cast<Smem<NT>*>(smem_raw);
+  constexpr int ST = stages(NT);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   pdl_release();
   pdl_wait();  // the work list and the step's inputs come from earlier kernels
@@ -225,43 +267,52 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   const int it_end = prm.item_begin[blockIdx.x + 1];
   if (it_begin >= it_end) return;
   const int G = prm.Hq / prm.Hkv;
+  uint32_t magic;  // 1024 twice; opaque, so that it stays in a register
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
   const uint32_t sq = smem_u32(S.q), sp = smem_u32(S.p);
   // Key 16 b + tok of a tile is inner index 64 (b >> 2) + 16 (tok >> 2) + 8 ((tok >> 1) & 1) +
   // 2 (b & 3) + (tok & 1) of the PV product, the order of V's fragments: this thread's first
   // key (b = 2 w, tok = g); block 2 w + i is 2 i further, tok + 8 another 32
   const int p_row = 64 * (w >> 1) + 16 * (g >> 2) + 8 * ((g >> 1) & 1) + 4 * (w & 1) + (g & 1);
 
-  // ---- loads ahead: blocks of the tile after the next, K codes and scales of the next
+  // ---- copies, ST - 1 tiles ahead: what this warp expands of a tile into its part of the ring
   Ahead ahead{prm, 0, it_end, 0, 0, 0, nullptr, 0, 0, 0};
   ahead.take(it_begin);
   ahead.look(lane & 7);
   const uint8_t* const base_k = prm.cache + t4 * 256 + g * 16;
-  const uint8_t* const base_ks = prm.cache + kOffKs + g * 4 + t4;
   const uint8_t* const base_v = prm.cache + kOffV + (32 * w + 2 * g) * 8;
-  const uint8_t* const base_vs = prm.cache + kOffVs + w * kBlock;
-  int vblk[2] = {-1, -1};   // blocks t4, t4 + 4 of the tile that K was loaded for
-  uint4 kc[4] = {};         // codes of tokens g, g + 8 of the warp's two blocks, group t4
-  uint32_t ks[4] = {};      // their scales
-  auto load_k = [&]() {
+  const uint32_t ring = smem_u32(S.ring) + w * kWarpStage;
+  constexpr int kStageBytes = 4 * kWarpStage;
+  uint32_t fill = ring;
+  auto copy = [&]() {
     const int blk = ahead.block();  // lane b: block b of the tile
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int b = __shfl_sync(0xffffffffu, blk, 2 * w + i);
-      vblk[i] = __shfl_sync(0xffffffffu, blk, t4 + 4 * i);
-      if (b >= 0) {  // uniform over the warp
-        const uint8_t* kp = base_k + (long long)b * kBlockBytes;
-        const uint8_t* sp = base_ks + (long long)b * kBlockBytes;
-        kc[2 * i] = ldg16(kp);
-        kc[2 * i + 1] = ldg16(kp + 128);
-        ks[2 * i] = __ldg(sp);
-        ks[2 * i + 1] = __ldg(sp + 32);
+      const int kb = __shfl_sync(0xffffffffu, blk, 2 * w + i);
+      const int vb = __shfl_sync(0xffffffffu, blk, t4 + 4 * i);
+      if (kb >= 0) {  // uniform over the warp
+        const uint8_t* src = base_k + (long long)kb * kBlockBytes;
+        cp16(fill + kStageK + i * 1024 + lane * 16, src);
+        cp16(fill + kStageK + i * 1024 + 512 + lane * 16, src + 128);
+        if (lane < 16) cp4(fill + kStageKs + i * 64 + lane * 4,
+                           prm.cache + (long long)kb * kBlockBytes + kOffKs + lane * 4);
+      }
+      if (vb >= 0) {
+        const uint8_t* src = base_v + (long long)vb * kBlockBytes;
+        cp16(fill + kStageV + i * 1024 + lane * 16, src);
+        cp16(fill + kStageV + i * 1024 + 512 + lane * 16, src + 128);
       }
     }
+    if (lane < 8 && blk >= 0)
+      cp16(fill + kStageVs + lane * 16, prm.cache + (long long)blk * kBlockBytes + kOffVs + w * kBlock);
+    cp_commit();
+    fill = fill == ring + (ST - 1) * kStageBytes ? ring : fill + kStageBytes;
     ahead.advance();
     ahead.look(lane & 7);
   };
-  load_k();
-  uint4 vc[4] = {}, vsc[2] = {};  // V codes of channels 2 g, 2 g + 1 of 16 i; scales
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) copy();
+  uint32_t stage = ring;
 
   for (int it = it_begin; it < it_end; ++it) {
     const AttnItem item = prm.items[it];
@@ -319,16 +370,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       const bool cached = t < ct;
       const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
       const uint32_t pbuf = sp + ((t - item.tb) & 1) * (kKT * 16 * NT);
-      // ---- V of this tile on its way
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (vblk[u] >= 0) {
-          const uint8_t* vp = base_v + (long long)vblk[u] * kBlockBytes;
-          vc[2 * u] = ldg16(vp);
-          vc[2 * u + 1] = ldg16(vp + 128);
-          vsc[u] = ldg16(base_vs + (long long)vblk[u] * kBlockBytes);
-        }
-      }
+      __syncwarp();  // the stage that is filled next has been read
+      copy();
+      cp_wait<ST - 1>();
+      __syncwarp();
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
 #pragma unroll
@@ -350,10 +395,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         for (int j = 0; j < NT; ++j) mma(d[j], a1, b[j][2], b[j][3]);
       };
       if (cached) {
-        uint32_t sl[4], sh[4], bl[4], bh[4];  // per key: m-tile i, row g + 8 h at 2 i + h
+        uint4 kc[4];                          // per key: m-tile i, row g + 8 h at 2 i + h
+#pragma unroll
+        for (int k = 0; k < 4; ++k) kc[k] = ld_shared16(stage + kStageK + k * 512 + lane * 16);
+        uint32_t sl[4], sh[4], bl[4], bh[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t two = e4m3x2_to_h2(ks[2 * i] | (ks[2 * i + 1] << 8));
+          const uint32_t sc_at = stage + kStageKs + i * 64 + g * 4 + t4;
+          const uint32_t two = e4m3_low(ld_shared8(sc_at) | (ld_shared8(sc_at + 32) << 8));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t sc = __byte_perm(two, 0, h ? 0x3232 : 0x1010);
@@ -374,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             for (int h = 0; h < 2; ++h) {
               const int k = 2 * i + h;
               const uint32_t word = c == 0 ? kc[k].x : c == 1 ? kc[k].y : c == 2 ? kc[k].z : kc[k].w;
-              expand(word, sl[k], bl[k], sh[k], bh[k], sl[k], bl[k], sh[k], bh[k], x[h]);
+              expand(word, magic, sl[k], bl[k], sh[k], bh[k], sl[k], bl[k], sh[k], bh[k], x[h]);
             }
             qk(s[i], b, x[0], x[1]);
           }
@@ -407,8 +456,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           }
         }
       }
-      // ---- K of the next tile on its way (and the blocks of the one after looked up)
-      load_k();
       // ---- masks: s[i][j][2 h + e] is key 32 w + 16 i + g + 8 h, row 8 j + 2 t4 + e; a block
       // row b is seen by rows n >= (b - i0) G
       if (!cached || vis < kKT) {
@@ -507,26 +554,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         }
       };
       if (cached) {
-        if (vis < kKT) {  // masked keys get scale 0, whatever their page holds
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t* x = reinterpret_cast<uint32_t*>(&vsc[u]);
+        for (int u = 0; u < 2; ++u) {    // block t4 + 4 u
+          const uint4 vs4 = ld_shared16(stage + kStageVs + (t4 + 4 * u) * 16);
+          uint32_t vsc[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+          uint4 vc[2];                   // channels 2 g (x, y) and 2 g + 1 (z, w) of 16 i
+#pragma unroll
+          for (int i = 0; i < 2; ++i) vc[i] = ld_shared16(stage + kStageV + u * 1024 + i * 512 + lane * 16);
+          if (vis < kKT) {  // masked keys get scale 0, whatever their page holds
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int left = vis - (t4 + 4 * u) * kBlock - 4 * q;
-              if (left < 4) x[q] = left <= 0 ? 0u : x[q] & ((1u << (8 * left)) - 1u);
+              if (left < 4) vsc[q] = left <= 0 ? 0u : vsc[q] & ((1u << (8 * left)) - 1u);
             }
           }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)      // block t4 + 4 u
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 8 keys of it
             uint32_t ss[4], bb[4];       // scale pairs of the channels' group
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint32_t x = h ? (q ? vsc[u].w : vsc[u].z) : (q ? vsc[u].y : vsc[u].x);
-              const uint32_t s0 = e4m3x2_to_h2(x & 0xffffu), s1 = e4m3x2_to_h2(x >> 16);
+              const uint32_t x = vsc[2 * h + q];
+              const uint32_t s0 = e4m3_low(x), s1 = e4m3_high(x);
               ss[2 * q] = hmul2_bits(s0, kSixteenth);
               bb[2 * q] = hmul2_bits(s0, kBiasLow);
               ss[2 * q + 1] = hmul2_bits(s1, k256th);
@@ -535,12 +583,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             uint32_t lo[2][4], hi[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 c = vc[2 * u + i];  // channel 2 g: x, y; channel 2 g + 1: z, w
-              expand(h ? c.y : c.x, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], lo[i]);
-              expand(h ? c.w : c.z, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], hi[i]);
+              expand(h ? vc[i].y : vc[i].x, magic, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], lo[i]);
+              expand(h ? vc[i].w : vc[i].z, magic, ss[0], bb[0], ss[1], bb[1], ss[2], bb[2], ss[3], bb[3], hi[i]);
             }
             pv(u, h, lo, hi);
           }
+        }
       } else {
         const uint32_t* vn = reinterpret_cast<const uint32_t*>(
             prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD) + 16 * w + g;
@@ -563,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           pv(n >> 1, n & 1, lo, hi);
         }
       }
+      stage = stage == ring + (ST - 1) * kStageBytes ? ring : stage + kStageBytes;
     }
 
     // ---- epilogue: row sums over the team, O^T / l
@@ -602,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
     // and cf were last read before the team's last tile barrier, `sum` is written next after
     // two more)
   }
+  cp_wait<0>();
 }
 
 // ---------------------------------------------------------------- split combine
@@ -650,6 +700,18 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
+template <int NT>
+static int launch_tile(const Params& p, int ncta, cudaStream_t stream) {
+  static PerDevice<bool> done;
+  const bool ok = once_per_device(done, false, [] {
+    return cudaFuncSetAttribute(verify_attn_kv4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Smem<NT>)) == cudaSuccess;
+  });
+  if (!ok) return DSPARK_ECUDA;
+  return launch_pdl(verify_attn_kv4_kernel<NT>, dim3(ncta), dim3(kThreads), sizeof(Smem<NT>), stream,
+                    p) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
+}
+
 Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   Plan p{};
   const int G = Hq / Hkv;
@@ -709,10 +771,10 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   p.k_unit = 1.f / (16.f * gk);
   p.v_unit = 1.f / (16.f * gv);
   p.o_unit = 16.f * gv;
-  void (*fn)(Params) = pl.nt == 8    ? verify_attn_kv4_kernel<1>
-                       : pl.nt == 16 ? verify_attn_kv4_kernel<2>
-                                     : verify_attn_kv4_kernel<4>;
-  if (launch_pdl(fn, dim3(pl.ncta), dim3(kThreads), 0, stream, p) != cudaSuccess) return DSPARK_ECUDA;
+  const int lc = pl.nt == 8    ? launch_tile<1>(p, pl.ncta, stream)
+                 : pl.nt == 16 ? launch_tile<2>(p, pl.ncta, stream)
+                               : launch_tile<4>(p, pl.ncta, stream);
+  if (lc != DSPARK_OK) return lc;
   return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, pl.nt / 8), dim3(256), 0, stream, cu_seqlens,
                     reinterpret_cast<const SplitGroup*>(w + pl.off_groups), Hq / Hkv, Hq, p.ws_o,
                     p.ws_lse, p.out, lse) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;

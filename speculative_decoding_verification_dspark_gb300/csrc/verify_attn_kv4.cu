@@ -40,8 +40,8 @@
 // The softmax takes a tile in one pass against the row references of the tiles before; only if
 // some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
 // references move and O and the sums with them.  That vote and the hand-over of P are the
-// tile's one barrier.  Each thread copies what it will itself expand into a ring of
-// stages by cp.async (its warp shares only the scales), a tile or two ahead.
+// tile's one barrier; behind it one warp issues the bulk copies (a block each) of a later
+// tile into the stage that the tile before has left.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,6 +52,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "ptx.cuh"
 
 namespace dspark {
 namespace attn {
@@ -70,12 +71,12 @@ constexpr int kMaxCtas = 1024;         // the work list's limit
 // that each has in its ring.
 __host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 __host__ __device__ constexpr int stages(int NT) { return NT == 1 ? 2 : 3; }
-// A warp's share of a stage: what its threads expand, each in its own order.
-constexpr int kStageK = 0;         // [2 blocks][tokens g, g + 8][lane][16 B]
-constexpr int kStageV = 2048;      // [blocks t4, t4 + 4][16 channels][lane][16 B]
-constexpr int kStageKs = 4096;     // [32 tokens][4 groups]
-constexpr int kStageVs = 4224;     // [8 blocks][16 tokens]
-constexpr int kWarpStage = 4352;
+// A block's place in a stage: 32 bytes of padding put the blocks that a quad's four threads
+// read at once in different banks.
+constexpr int kBlockStride = kBlockBytes + 32;
+constexpr int kBlocks = kKT / kBlock;
+constexpr int kStageBytes = kBlocks * kBlockStride;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 struct Params {
   const __nv_bfloat16 *q, *k_new, *v_new;
@@ -111,21 +112,27 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Wait for a stage's copies; bounded, the error is raised and the call goes on with what is there.
+__device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, unsigned int* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait_sleep(bar, parity, 20000)) return;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000))
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_error(err, DSPARK_DEVERR_WAIT_TIMEOUT);
+      return;
+    }
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -198,60 +205,88 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Row of P in shared memory (16 NT bytes, NT chunks of 8 query rows): chunk j is placed so
-// that eight consecutive rows' chunks lie in different banks.
+// Chunk j (8 query rows, 16 bytes) of row r of P in shared memory, placed so that neither the
+// eight rows of a fragment nor the rows {0, 1, 8, 9, 16, 17, 24, 25} + x that a warp writes at
+// once share banks: by padding after each eight rows (NT = 1, 2) and by the chunk's place.
 template <int NT>
-__device__ __forceinline__ uint32_t p_off(int row, int j) {
-  return row * (16 * NT) + ((j ^ (NT == 4 ? (row >> 1) & 3 : NT == 2 ? (row >> 2) & 1 : 0)) << 4);
+__device__ __forceinline__ uint32_t p_off(int r, int j) {
+  if (NT == 1) return r * 16 + (r >> 3) * 32;
+  if (NT == 2) return r * 32 + (r >> 3) * 64 + ((j ^ (((r >> 2) ^ (r >> 4)) & 1)) << 4);
+  return r * 64 + ((j ^ (((r >> 1) ^ (r >> 3)) & 3)) << 4);
 }
+template <int NT>
+constexpr int p_bytes() { return kKT * 16 * NT + (NT == 1 ? 16 * 32 : NT == 2 ? 16 * 64 : 0); }
 // Row of Q (256 bytes, 16 chunks).
 __device__ __forceinline__ uint32_t q_off(int row, int c) { return row * 256 + ((c ^ (row & 7)) << 4); }
 
 template <int NT>
 struct Smem {
   __align__(128) uint8_t q[8 * NT * 256];
-  __align__(128) uint8_t p[2][kKT * 16 * NT];
+  __align__(128) uint8_t p[2][p_bytes<NT>()];
+  __align__(128) uint8_t ring[stages(NT)][kStageBytes];
   float cf[8 * NT];          // softmax scale per row
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
-  __align__(16) uint8_t ring[stages(NT)][4][kWarpStage];
+  __align__(8) uint64_t full[stages(NT)];
 };
 
-// The cache tiles of a CTA in order, looked up a tile ahead of their copies: lane b < 8 of a
-// warp looks for block b of a tile, and turns the page into the block's index only when
-// the tile's copies are issued, so that nothing waits for the page table.
+// The cache tiles of a CTA in order, four at a time: lane j of the copying warp knows block
+// j % 8 of tile j / 8 of the window.  The pages of a window are read while the window before
+// it is copied, so that nothing waits for the page table.
 struct Ahead {
   const Params& p;
-  int it, it_end, t, te, ctx;
-  const int32_t* table;   // the request's pages
-  int head;               // kvh * blocks of a page
-  int page, sub;          // looked up: the page of this lane's block, its place in the page
+  int it_end;
+  int it, t, te, r, ctx, kvh;  // the next cache tile to copy (te: end of the item's)
+  int window;                  // first tile of the window, -1: none yet
+  int block;                   // this lane's block, by its index among all blocks of the cache; -1: none
+  int page;                    // and its page in the next window
   static constexpr int kNone = -0x7fffffff;
+  // The first item from `at` on that has cache tiles.
   __device__ __forceinline__ void take(int at) {
-    it = at;
-    if (at >= it_end) return;
-    const AttnItem* x = p.items + at;
-    t = x->tb; te = x->te; ctx = x->ctx;
-    table = p.page_table + (long long)x->r * p.max_pages;
-    head = x->kvh << (p.log2_page - 4);
+    for (it = at; it < it_end; ++it) {
+      const AttnItem* x = p.items + it;
+      t = x->tb; r = x->r; ctx = x->ctx; kvh = x->kvh;
+      te = min(x->te, ceil_div(ctx, kKT));
+      if (t < te) return;
+    }
   }
-  __device__ __forceinline__ void look(int b) {
-    const int pos = t * kKT + b * kBlock, slot = pos >> p.log2_page;
+  // Page of this lane's block in the window at tile t0; kNone where it holds no committed key of
+  // the item's tiles.
+  __device__ __forceinline__ void look(int lane, int t0) {
+    const int pos = t0 * kKT + lane * kBlock, slot = pos >> p.log2_page;
     page = kNone;
-    if (it >= it_end || pos >= ctx) return;
-    sub = head + ((pos >> 4) & ((1 << (p.log2_page - 4)) - 1));
+    if (pos >= ctx || t0 + (lane >> 3) >= te) return;
     page = -1;
-    if (slot < p.max_pages) page = __ldg(table + slot);
+    if (slot < p.max_pages) page = __ldg(p.page_table + (long long)r * p.max_pages + slot);
   }
-  // Index of the block among all blocks of the cache; -1 where it holds no committed key or
-  // its page is bad (its keys are then masked, or undefined).
-  __device__ __forceinline__ int block() const {
-    if ((unsigned)page < (unsigned)p.n_pages) return ((page * p.Hkv) << (p.log2_page - 4)) + sub;
-    if (page != kNone) raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
-    return -1;
+  __device__ __forceinline__ void start(int lane, int at) {
+    take(at);
+    window = -1;
+    if (it < it_end) look(lane, t);
   }
-  __device__ __forceinline__ void advance() {
-    if (it < it_end && ++t == te) take(it + 1);
+  // Copies the next tile into the stage at `dst`.
+  __device__ __forceinline__ void copy(int lane, uint32_t dst, uint32_t bar) {
+    if (it >= it_end) return;
+    if (window < 0 || t == window + 4) {
+      window = t;
+      block = -1;
+      if ((unsigned)page < (unsigned)p.n_pages) {
+        const int lp = p.log2_page - 4, pos = t * kKT + lane * kBlock;
+        block = ((page * p.Hkv + kvh) << lp) + ((pos >> 4) & ((1 << lp) - 1));
+      } else if (page != kNone) {
+        raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
+      }
+      if (t + 4 < te) look(lane, t + 4);
+    }
+    const int first = 8 * (t - window);  // lanes first .. first + 7 hold the tile's blocks
+    const bool mine = (lane & ~7) == first && block >= 0;
+    const unsigned n = __popc(__ballot_sync(0xffffffffu, mine));
+    if (lane == first) ptx::mbar_arrive_expect_tx(bar, n * kBlockBytes);
+    __syncwarp();
+    if (mine)
+      ptx::bulk_load_g2s(dst + (lane & 7) * kBlockStride, p.cache + (long long)block * kBlockBytes,
+                         kBlockBytes, bar);
+    if (++t == te) start(lane, it + 1);
   }
 };
 
@@ -275,44 +310,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   // key (b = 2 w, tok = g); block 2 w + i is 2 i further, tok + 8 another 32
   const int p_row = 64 * (w >> 1) + 16 * (g >> 2) + 8 * ((g >> 1) & 1) + 4 * (w & 1) + (g & 1);
 
-  // ---- copies, ST - 1 tiles ahead: what this warp expands of a tile into its part of the ring
-  Ahead ahead{prm, 0, it_end, 0, 0, 0, nullptr, 0, 0, 0};
-  ahead.take(it_begin);
-  ahead.look(lane & 7);
-  const uint8_t* const base_k = prm.cache + t4 * 256 + g * 16;
-  const uint8_t* const base_v = prm.cache + kOffV + (32 * w + 2 * g) * 8;
-  const uint32_t ring = smem_u32(S.ring) + w * kWarpStage;
-  constexpr int kStageBytes = 4 * kWarpStage;
-  uint32_t fill = ring;
-  auto copy = [&]() {
-    const int blk = ahead.block();  // lane b: block b of the tile
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int kb = __shfl_sync(0xffffffffu, blk, 2 * w + i);
-      const int vb = __shfl_sync(0xffffffffu, blk, t4 + 4 * i);
-      if (kb >= 0) {  // uniform over the warp
-        const uint8_t* src = base_k + (long long)kb * kBlockBytes;
-        cp16(fill + kStageK + i * 1024 + lane * 16, src);
-        cp16(fill + kStageK + i * 1024 + 512 + lane * 16, src + 128);
-        if (lane < 16) cp4(fill + kStageKs + i * 64 + lane * 4,
-                           prm.cache + (long long)kb * kBlockBytes + kOffKs + lane * 4);
-      }
-      if (vb >= 0) {
-        const uint8_t* src = base_v + (long long)vb * kBlockBytes;
-        cp16(fill + kStageV + i * 1024 + lane * 16, src);
-        cp16(fill + kStageV + i * 1024 + 512 + lane * 16, src + 128);
-      }
-    }
-    if (lane < 8 && blk >= 0)
-      cp16(fill + kStageVs + lane * 16, prm.cache + (long long)blk * kBlockBytes + kOffVs + w * kBlock);
-    cp_commit();
-    fill = fill == ring + (ST - 1) * kStageBytes ? ring : fill + kStageBytes;
-    ahead.advance();
-    ahead.look(lane & 7);
-  };
+  // ---- copies, ST - 1 tiles ahead, by one warp (another for each CTA of an SM)
+  const uint32_t ring = smem_u32(S.ring), full = smem_u32(S.full);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) ptx::mbar_init(full + 8 * i, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const bool copies = w == (int)(blockIdx.x & 3);
+  Ahead ahead{prm, it_end};
+  if (copies) {
+    ahead.start(lane, it_begin);
 #pragma unroll 1
-  for (int i = 0; i < ST - 1; ++i) copy();
-  uint32_t stage = ring;
+    for (int i = 0; i < ST - 1; ++i) ahead.copy(lane, ring + i * kStageBytes, full + 8 * i);
+  }
+  int stage = 0, parity = 0;   // of the next cache tile
 
   for (int it = it_begin; it < it_end; ++it) {
     const AttnItem item = prm.items[it];
@@ -320,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
     const int nq = item.ni * G;              // rows of the tile
     const long long row0 = (long long)item.c0 + item.i0;
     // ---- Q: row n = (block row n / G, head kvh G + n % G), fp16 scaled by a power of two; a
-    // half-warp holds a row, 8 dims per lane.  Dim 32 t + 4 s + e is at inner index
-    // 16 s + 2 t + (e & 1) + 8 (e >> 1): the order of K's fragments
+    // half-warp holds a row, 8 dims per lane.  In the order of K's fragments: dim 32 t + 8 v + e
+    // (word v of group t) is at inner index 16 s + 2 t + (e & 1) + 8 ((e >> 1) & 1), s = 2 c + (e >> 2),
+    // where thread t of a quad takes word v in turn c, its pairs of words swapped for odd t
     {
       const int l = lane & 15;
 #pragma unroll
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         const float f = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // dims 8 l + 2 j, + 1
-          const int t = l >> 2, s = 2 * (l & 3) + (j >> 1);
+          const int t = l >> 2, c = 2 * ((((l & 3) >> 1) + t) & 1) + (l & 1), s = 2 * c + (j >> 1);
           const int at = 16 * s + 2 * t + 8 * (j & 1);
           st_shared(sq + q_off(n, at >> 3) + (at & 7) * 2,
                     h2_bits(__floats2half2_rn(bf_lo(x[j]) * f, bf_hi(x[j]) * f)));
@@ -369,11 +382,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
     for (int t = item.tb; t < item.te; ++t) {
       const bool cached = t < ct;
       const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
-      const uint32_t pbuf = sp + ((t - item.tb) & 1) * (kKT * 16 * NT);
-      __syncwarp();  // the stage that is filled next has been read
-      copy();
-      cp_wait<ST - 1>();
-      __syncwarp();
+      const uint32_t pbuf = sp + ((t - item.tb) & 1) * p_bytes<NT>();
+      const uint32_t tile = ring + stage * kStageBytes;
+      if (cached) wait_stage(full + 8 * stage, parity, prm.err);
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
 #pragma unroll
@@ -395,14 +406,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         for (int j = 0; j < NT; ++j) mma(d[j], a1, b[j][2], b[j][3]);
       };
       if (cached) {
-        uint4 kc[4];                          // per key: m-tile i, row g + 8 h at 2 i + h
+        // per key (m-tile i, row g + 8 h at 2 i + h): its words in turn, pairs swapped for odd t4 so
+        // that a half-warp's reads lie in different banks; its scale
+        const uint32_t codes = tile + 2 * w * kBlockStride + t4 * 256 + g * 16;
+        uint2 kc[4][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) kc[k] = ld_shared16(stage + kStageK + k * 512 + lane * 16);
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            kc[k][c] = ld_shared_v2(codes + (k >> 1) * kBlockStride + (k & 1) * 128 + ((c + t4) & 1) * 8);
         uint32_t sl[4], sh[4], bl[4], bh[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t sc_at = stage + kStageKs + i * 64 + g * 4 + t4;
-          const uint32_t two = e4m3_low(ld_shared8(sc_at) | (ld_shared8(sc_at + 32) << 8));
+          const uint32_t sc_at = tile + (2 * w + i) * kBlockStride + kOffKs + g * 4 + t4;
+          const uint32_t two = e4m3_low(ld_shared_u8(sc_at) | (ld_shared_u8(sc_at + 32) << 8));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t sc = __byte_perm(two, 0, h ? 0x3232 : 0x1010);
@@ -422,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = 2 * i + h;
-              const uint32_t word = c == 0 ? kc[k].x : c == 1 ? kc[k].y : c == 2 ? kc[k].z : kc[k].w;
+              const uint32_t word = c & 1 ? kc[k][c >> 1].y : kc[k][c >> 1].x;
               expand(word, magic, sl[k], bl[k], sh[k], bh[k], sl[k], bl[k], sh[k], bh[k], x[h]);
             }
             qk(s[i], b, x[0], x[1]);
@@ -438,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           uint4 v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            v[k] = 32 * w + g + 8 * k < vis ? src[(long long)k * step + c] : make_uint4(0, 0, 0, 0);
+            v[k] = 32 * w + g + 8 * k < vis ? src[(long long)k * step + 2 * (((c >> 1) + t4) & 1) + (c & 1)]
+                                            : make_uint4(0, 0, 0, 0);
           uint32_t b[NT][4];
           q_frags(c, b);
 #pragma unroll
@@ -537,6 +555,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         }
         move = true;
       }
+      // the stage of the cache tile before this one has been read by all: the next copy goes there
+      if (copies && cached) {
+        const int to = stage == 0 ? ST - 1 : stage - 1;
+        ahead.copy(lane, ring + to * kStageBytes, full + 8 * to);
+      }
       // ---- O^T: two m-tiles of 16 channels, rows g and g + 8 being channels 2 g and 2 g + 1;
       // inner steps 4 u + 2 h, + 1 from the four key pairs of either channel's word
       auto pv = [&](int u, int h, const uint32_t (&lo)[2][4], const uint32_t (&hi)[2][4]) {
@@ -556,11 +579,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       if (cached) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {    // block t4 + 4 u
-          const uint4 vs4 = ld_shared16(stage + kStageVs + (t4 + 4 * u) * 16);
+          const uint32_t blk = tile + (t4 + 4 * u) * kBlockStride;
+          const uint4 vs4 = ld_shared16(blk + kOffVs + w * kBlock);
           uint32_t vsc[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
           uint4 vc[2];                   // channels 2 g (x, y) and 2 g + 1 (z, w) of 16 i
 #pragma unroll
-          for (int i = 0; i < 2; ++i) vc[i] = ld_shared16(stage + kStageV + u * 1024 + i * 512 + lane * 16);
+          for (int i = 0; i < 2; ++i) vc[i] = ld_shared16(blk + kOffV + (32 * w + 16 * i + 2 * g) * 8);
           if (vis < kKT) {  // masked keys get scale 0, whatever their page holds
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -611,7 +635,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           pv(n >> 1, n & 1, lo, hi);
         }
       }
-      stage = stage == ring + (ST - 1) * kStageBytes ? ring : stage + kStageBytes;
+      if (cached && ++stage == ST) {
+        stage = 0;
+        parity ^= 1;
+      }
     }
 
     // ---- epilogue: row sums over the team, O^T / l
@@ -651,7 +678,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
     // and cf were last read before the team's last tile barrier, `sum` is written next after
     // two more)
   }
-  cp_wait<0>();
 }
 
 // ---------------------------------------------------------------- split combine

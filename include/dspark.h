@@ -552,7 +552,8 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * and v_scale in place of the two caches, and
  *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
  *   Hq / Hkv <= 32
- *   max_block_rows: a hint as there; the query tile holds 8, 16 or 32 rows of
+ *   max_splits: as there, times the CTAs that share an SM (3 to 5)
+ *   max_block_rows: a hint as there; the query tile holds 8, 16, 24 or 32 rows of
  *        G = Hq / Hkv heads x block rows, the smallest that holds this many block rows
  *        (or 32); longer segments run as several row tiles.
  * Rounding: the cached values and the queries are exact in the products' fp16

@@ -141,7 +141,7 @@ int launch_worklist(const int32_t* ctx_len, const int32_t* cu_seqlens, int B, in
                     int max_splits, void* ws, const Plan& pl, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   const int max_items = pl.max_items > 0x7fffffff ? 0x7fffffff : (int)pl.max_items;
-  const int splits = max_splits < 2 ? 2 : (max_splits > 32 ? 32 : max_splits);
+  const int splits = max_splits < 2 ? 2 : max_splits;
   return launch_pdl(worklist_kernel, dim3(1), dim3(1024), 0, stream, ctx_len, cu_seqlens, B, max_rows,
                     Hkv, pl.parts, pl.rows_per_tile, pl.nk, pl.ncta, splits, pl.mla ? 1 : 0,
                     max_items, reinterpret_cast<AttnItem*>(w + pl.off_items),
@@ -168,7 +168,8 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* k_ca
 
   // planned: the pack call already wrote the work list (same plan) into ws
   if (!planned) {
-    const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv, max_splits, ws, pl, stream);
+    const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv,
+                                   max_splits > 32 ? 32 : max_splits, ws, pl, stream);
     if (rc != DSPARK_OK) return rc;
   }
 

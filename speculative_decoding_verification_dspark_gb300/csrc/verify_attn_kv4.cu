@@ -4,7 +4,7 @@
 //   o = softmax(scale q.K^T) V over the ctx_len[r] committed keys, whose K and V are
 //   (code - 8) * scale * g, followed by block rows 0..i (bf16); lse = log-sum-exp.
 //
-// A group's 8 NT query rows (NT = 1, 2, 4) against tiles of 128 keys, on a team of four
+// A group's 8 NT query rows (NT = 1..4) against tiles of 128 keys, on a team of four
 // warps that is a CTA of its own, several to an SM, persistent over equal ranges of the
 // work list (worklist.cuh).  Both products have the cache on the MMA's M side:
 //   S^T [128 keys x 8 NT] = K . Q^T     warp w: keys 32 w .. + 31 (two blocks of the cache)
@@ -69,8 +69,8 @@ constexpr int kMaxCtas = 1024;         // the work list's limit
 
 // CTAs per SM, by registers (the fragments of O^T and S^T are 8 NT each), and the cache tiles
 // that each has in its ring.
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
-__host__ __device__ constexpr int stages(int NT) { return NT == 1 ? 2 : 3; }
+__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 5 : NT == 2 ? 4 : NT == 3 ? 3 : 2; }
+__host__ __device__ constexpr int stages(int NT) { return NT < 4 ? 2 : 3; }
 // A block's place in a stage: 32 bytes of padding put the blocks that a quad's four threads
 // read at once in different banks.
 constexpr int kBlockStride = kBlockBytes + 32;
@@ -207,15 +207,16 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // Chunk j (8 query rows, 16 bytes) of row r of P in shared memory, placed so that neither the
 // eight rows of a fragment nor the rows {0, 1, 8, 9, 16, 17, 24, 25} + x that a warp writes at
-// once share banks: by padding after each eight rows (NT = 1, 2) and by the chunk's place.
+// once share banks: by padding after each eight rows (NT < 4) and by the chunk's place.
 template <int NT>
 __device__ __forceinline__ uint32_t p_off(int r, int j) {
   if (NT == 1) return r * 16 + (r >> 3) * 32;
+  if (NT == 3) return r * 48 + (r >> 3) * 16 + j * 16;
   if (NT == 2) return r * 32 + (r >> 3) * 64 + ((j ^ (((r >> 2) ^ (r >> 4)) & 1)) << 4);
   return r * 64 + ((j ^ (((r >> 1) ^ (r >> 3)) & 3)) << 4);
 }
 template <int NT>
-constexpr int p_bytes() { return kKT * 16 * NT + (NT == 1 ? 16 * 32 : NT == 2 ? 16 * 64 : 0); }
+constexpr int p_bytes() { return kKT * 16 * NT + 16 * (NT == 1 ? 32 : NT == 2 ? 64 : NT == 3 ? 16 : 0); }
 // Row of Q (256 bytes, 16 chunks).
 __device__ __forceinline__ uint32_t q_off(int row, int c) { return row * 256 + ((c ^ (row & 7)) << 4); }
 
@@ -326,13 +327,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   }
   int stage = 0, parity = 0;   // of the next cache tile
 
+  // ---- Q: tile row n = (block row n / G, head kvh G + n % G), a half-warp holds a row, 8 dims per
+  // lane; read in the last tile of the item before
+  uint4 qv[NT];
+  auto load_q = [&](const AttnItem* x) {
+    const long long row = (long long)x->c0 + x->i0;
+    const int n_q = x->ni * G, h0 = x->kvh * G;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int n = 8 * i + 2 * w + (lane >> 4);
+      qv[i] = make_uint4(0, 0, 0, 0);
+      if (n < n_q)
+        qv[i] = *reinterpret_cast<const uint4*>(
+            prm.q + ((row + n / G) * prm.Hq + h0 + n % G) * kD + (lane & 15) * 8);
+    }
+  };
+  load_q(prm.items + it_begin);
+
   for (int it = it_begin; it < it_end; ++it) {
     const AttnItem item = prm.items[it];
     const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
     const int nq = item.ni * G;              // rows of the tile
     const long long row0 = (long long)item.c0 + item.i0;
-    // ---- Q: row n = (block row n / G, head kvh G + n % G), fp16 scaled by a power of two; a
-    // half-warp holds a row, 8 dims per lane.  In the order of K's fragments: dim 32 t + 8 v + e
+    // ---- Q as fp16 scaled by a power of two, in the order of K's fragments: dim 32 t + 8 v + e
     // (word v of group t) is at inner index 16 s + 2 t + (e & 1) + 8 ((e >> 1) & 1), s = 2 c + (e >> 2),
     // where thread t of a quad takes word v in turn c, its pairs of words swapped for odd t
     {
@@ -340,11 +357,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int n = 8 * i + 2 * w + (lane >> 4);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (n < nq)
-          v = *reinterpret_cast<const uint4*>(
-              prm.q + ((row0 + n / G) * prm.Hq + item.kvh * G + n % G) * kD + l * 8);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
         uint32_t top = 0;  // largest magnitude, as bits (a NaN is above all)
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
@@ -384,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
       const uint32_t pbuf = sp + ((t - item.tb) & 1) * p_bytes<NT>();
       const uint32_t tile = ring + stage * kStageBytes;
+      if (t == item.te - 1 && it + 1 < it_end) load_q(prm.items + it + 1);
       if (cached) wait_stage(full + 8 * stage, parity, prm.err);
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
@@ -695,29 +709,30 @@ __global__ void __launch_bounds__(256)
   const int ns = sg.nsplit;
   const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (ns <= 1 || n >= sg.ni * G) return;
-  int slot = 0;
-  float my = -INFINITY;
-  if (lane < ns) {
-    slot = (lane == 0 && sg.slot0_last) ? 2 * sg.c_first + 1 : 2 * (sg.c_first + lane);
-    my = ws_lse[(long long)slot * 32 + n];
-  }
-  float mx = my;
+  // piece s is in slot 2 (c_first + s), but for a first piece that is not its CTA's first
+  auto slot = [&](int s) { return (long long)(2 * (sg.c_first + s) + (s == 0 && sg.slot0_last ? 1 : 0)) * 32 + n; };
+  float mx = -INFINITY;
+  for (int s = lane; s < ns; s += 32) mx = fmaxf(mx, ws_lse[slot(s)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float wgt = lane < ns ? expf(my - mx) : 0.f;
-  float sum = wgt;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const float wgt = s0 + lane < ns ? expf(ws_lse[slot(s0 + lane)] - mx) : 0.f;
+    sum += wgt;
+    const int m = min(32, ns - s0);
+#pragma unroll 4
+    for (int s = 0; s < m; ++s) {
+      const float w = __shfl_sync(0xffffffffu, wgt, s);
+      const float4 v = reinterpret_cast<const float4*>(ws_o + slot(s0 + s) * kD)[lane];
+      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = 1.f / sum;
   const long long row = cu_seqlens[sg.r] + sg.i0 + n / G;
   const int head = sg.kvh * G + n % G;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < ns; ++s) {
-    const float w = __shfl_sync(0xffffffffu, wgt, s);
-    const int sl = __shfl_sync(0xffffffffu, slot, s);
-    const float4 v = reinterpret_cast<const float4*>(ws_o + ((long long)sl * 32 + n) * kD)[lane];
-    acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
-  }
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(out + (row * Hq + head) * kD)[lane] =
@@ -742,7 +757,7 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   Plan p{};
   const int G = Hq / Hkv;
   const long long rows = (long long)G * (max_block_rows > 0 ? max_block_rows : 1);
-  const int NT = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const int NT = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   p.parts = 1;
   p.nt = 8 * NT;
   p.rows_per_tile = p.nt / G;
@@ -772,7 +787,9 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
            float scale, float gk, float gv, int max_splits, void* out, float* lse, void* ws,
            const Plan& pl, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv, max_splits, ws, pl, stream);
+  // a CTA of the bf16 kernels is an SM; here several share it, and a group may be cut finer
+  const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv,
+                                 max_splits * ctas_per_sm(pl.nt / 8), ws, pl, stream);
   if (rc != DSPARK_OK) return rc;
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -799,6 +816,7 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   p.o_unit = 16.f * gv;
   const int lc = pl.nt == 8    ? launch_tile<1>(p, pl.ncta, stream)
                  : pl.nt == 16 ? launch_tile<2>(p, pl.ncta, stream)
+                 : pl.nt == 24 ? launch_tile<3>(p, pl.ncta, stream)
                                : launch_tile<4>(p, pl.ncta, stream);
   if (lc != DSPARK_OK) return lc;
   return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, pl.nt / 8), dim3(256), 0, stream, cu_seqlens,

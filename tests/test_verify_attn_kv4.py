@@ -55,7 +55,8 @@ def test_host_refusals(pkg):
 
 def test_hint_and_binding_refusals(pkg):
     assert pkg.block_rows_hint_for_kv4(6, 32, 8) == 7
-    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 8
+    assert pkg.block_rows_hint_for_kv4(16, 32, 8) == 6      # 17 rows in three tiles
+    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 7      # 33 rows in five
     assert pkg.block_rows_hint_for_kv4(6, 64, 2) == 1
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731

@@ -226,6 +226,7 @@ struct Smem {
   __align__(128) uint8_t p[2][p_bytes<NT>()];
   __align__(128) uint8_t ring[stages(NT)][kStageBytes];
   float cf[8 * NT];          // softmax scale per row
+  float ref[4][8 * NT];      // references, a copy per warp
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
   __align__(8) uint64_t full[stages(NT)];
@@ -379,17 +380,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
     }
     __syncthreads();
     // this thread's rows: 8 j + 2 t4 + {0, 1}
-    float cf[NT][2], ref[NT][2], l[NT][2];
+    float l[NT][2];
     float o[2][NT][4];      // O^T: channels 32 w + 16 i + 2 g + {0, 1} x rows
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      l[j][0] = l[j][1] = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        cf[j][h] = S.cf[8 * j + 2 * t4 + h];
-        ref[j][h] = kNoRef;
-        l[j][h] = 0.f;
-        o[0][j][h] = o[0][j][h + 2] = o[1][j][h] = o[1][j][h + 2] = 0.f;
-      }
+      for (int e = 0; e < 4; ++e) o[0][j][e] = o[1][j][e] = 0.f;
+    }
+    float* const my_ref = S.ref[w];
+    if (lane < 8 * NT) my_ref[lane] = kNoRef;
 
 #pragma unroll 1
     for (int t = item.tb; t < item.te; ++t) {
@@ -423,12 +423,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         // per key (m-tile i, row g + 8 h at 2 i + h): its words in turn, pairs swapped for odd t4 so
         // that a half-warp's reads lie in different banks; its scale
         const uint32_t codes = tile + 2 * w * kBlockStride + t4 * 256 + g * 16;
-        uint2 kc[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            kc[k][c] = ld_shared_v2(codes + (k >> 1) * kBlockStride + (k & 1) * 128 + ((c + t4) & 1) * 8);
+        uint2 kc[4];
         uint32_t sl[4], sh[4], bl[4], bh[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -445,6 +440,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          if ((c & 1) == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              kc[k] = ld_shared_v2(codes + (k >> 1) * kBlockStride + (k & 1) * 128 + (((c >> 1) + t4) & 1) * 8);
+          }
           uint32_t b[NT][4];
           q_frags(c, b);
 #pragma unroll
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = 2 * i + h;
-              const uint32_t word = c & 1 ? kc[k][c >> 1].y : kc[k][c >> 1].x;
+              const uint32_t word = c & 1 ? kc[k].y : kc[k].x;
               expand(word, magic, sl[k], bl[k], sh[k], bh[k], sl[k], bl[k], sh[k], bh[k], x[h]);
             }
             qk(s[i], b, x[0], x[1]);
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
               float m = fmaxf(fmaxf(s[0][j][e], s[0][j][2 + e]), fmaxf(s[1][j][e], s[1][j][2 + e]));
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-              if (g == 0) S.red[w][8 * j + 2 * t4 + e] = m * cf[j][e];
+              if (g == 0) S.red[w][8 * j + 2 * t4 + e] = m * S.cf[8 * j + 2 * t4 + e];
             }
           __syncthreads();
 #pragma unroll
@@ -525,9 +525,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             for (int e = 0; e < 2; ++e) {
               const int n = 8 * j + 2 * t4 + e;
               const float m = fmaxf(fmaxf(S.red[0][n], S.red[1][n]), fmaxf(S.red[2][n], S.red[3][n]));
-              if (m - kRefDrop > ref[j][e] + (kMove - kRefDrop)) {
-                const float al = ref[j][e] == kNoRef ? 0.f : fast_exp2(ref[j][e] - (m - kRefDrop));
-                ref[j][e] = m - kRefDrop;
+              const float old = my_ref[n];
+              __syncwarp();
+              if (m - kRefDrop > old + (kMove - kRefDrop)) {
+                const float al = old == kNoRef ? 0.f : fast_exp2(old - (m - kRefDrop));
+                if (g == 0) my_ref[n] = m - kRefDrop;
                 l[j][e] *= al;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -536,6 +538,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
                 }
               }
             }
+          __syncwarp();
+        }
+        float2 cf[NT], ref[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          cf[j] = *reinterpret_cast<const float2*>(&S.cf[8 * j + 2 * t4]);
+          ref[j] = *reinterpret_cast<const float2*>(&my_ref[8 * j + 2 * t4]);
         }
         float top = -INFINITY;
         float p0[NT][2];    // this thread's part of the tile's row sums
@@ -548,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             const int at = p_row + 2 * i + 32 * h;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              const float x0 = fmaf(s[i][j][2 * h], cf[j][0], -ref[j][0]);
-              const float x1 = fmaf(s[i][j][2 * h + 1], cf[j][1], -ref[j][1]);
+              const float x0 = fmaf(s[i][j][2 * h], cf[j].x, -ref[j].x);
+              const float x1 = fmaf(s[i][j][2 * h + 1], cf[j].y, -ref[j].y);
               top = fmaxf(top, fmaxf(x0, x1));
               const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
               p0[j][0] += e0;
@@ -674,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         if (n >= nq) continue;
         const float sum = (S.sum[0][n] + S.sum[1][n]) + (S.sum[2][n] + S.sum[3][n]);
         const float inv = sum == 0.f ? 0.f : prm.o_unit / sum;
-        const float lse = sum == 0.f ? -INFINITY : (ref[j][e] + log2f(sum)) * 0.69314718055994530942f;
+        const float lse = sum == 0.f ? -INFINITY : (my_ref[n] + log2f(sum)) * 0.69314718055994530942f;
         const long long at = (row0 + n / G) * prm.Hq + item.kvh * G + n % G;
         if (split) {
           if (w == 0 && g == 0) prm.ws_lse[(long long)item.slot * 32 + n] = lse;

@@ -5,7 +5,7 @@
 //   (code - 8) * scale * g, followed by block rows 0..i (bf16); lse = log-sum-exp.
 //
 // A group's 8 NT query rows (NT = 1..4) against tiles of 128 keys, on a team of four
-// warps that is a CTA of its own, several to an SM, persistent over equal ranges of the
+// warps that is a CTA of its own (with a fifth that copies), several to an SM, persistent over equal ranges of the
 // work list (worklist.cuh).  Both products have the cache on the MMA's M side:
 //   S^T [128 keys x 8 NT] = K . Q^T     warp w: keys 32 w .. + 31 (two blocks of the cache)
 //   O^T [128 d    x 8 NT] += V^T . P^T  warp w: channels 32 w .. + 31 (one group of V scales)
@@ -40,8 +40,7 @@
 // The softmax takes a tile in one pass against the row references of the tiles before; only if
 // some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
 // references move and O and the sums with them.  That vote and the hand-over of P are the
-// tile's one barrier; behind it one warp issues the bulk copies (a block each) of a later
-// tile into the stage that the tile before has left.
+// tile's one barrier.  A fifth warp issues the bulk copies (a block each) into a ring of tiles.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -61,7 +60,9 @@ namespace kv4a {
 using namespace dspark::kv4;
 
 constexpr int kKT = 128;               // keys of a tile
-constexpr int kThreads = 128;
+constexpr int kTeam = 128;             // four warps that compute; a fifth copies
+constexpr int kThreads = 160;
+constexpr int kSmemItems = 16;         // work items of a CTA kept in shared memory
 constexpr float kRefDrop = 6.f;        // reference = maximum - 6 (log2)
 constexpr float kMove = 14.f;          // a key above reference + 14 moves it
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key
@@ -69,7 +70,7 @@ constexpr int kMaxCtas = 1024;         // the work list's limit
 
 // CTAs per SM, by registers (the fragments of O^T and S^T are 8 NT each), and the cache tiles
 // that each has in its ring.
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 5 : NT == 2 ? 4 : NT == 3 ? 3 : 2; }
+__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 4 : NT == 4 ? 2 : 3; }
 __host__ __device__ constexpr int stages(int NT) { return NT < 4 ? 2 : 3; }
 // A block's place in a stage: 32 bytes of padding put the blocks that a quad's four threads
 // read at once in different banks.
@@ -122,7 +123,7 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Wait for a stage's copies; bounded, the error is raised and the call goes on with what is there.
+// Wait on a stage's barrier; bounded (the error is raised and the call goes on).
 __device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, unsigned int* err) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
@@ -133,6 +134,22 @@ __device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, unsign
       raise_error(err, DSPARK_DEVERR_WAIT_TIMEOUT);
       return;
     }
+}
+// Barrier of the team, and the same that ors a flag over it.
+__device__ __forceinline__ void team_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(kTeam) : "memory");
+}
+__device__ __forceinline__ bool team_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %2, 0;\n\t"
+      "barrier.cta.red.or.pred p, 1, %1, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "n"(kTeam), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -229,68 +246,68 @@ struct Smem {
   float ref[4][8 * NT];      // references, a copy per warp
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
-  __align__(8) uint64_t full[stages(NT)];
+  __align__(16) AttnItem items[kSmemItems];
+  __align__(8) uint64_t full[stages(NT)], empty[stages(NT)];
 };
 
-// The cache tiles of a CTA in order, four at a time: lane j of the copying warp knows block
-// j % 8 of tile j / 8 of the window.  The pages of a window are read while the window before
-// it is copied, so that nothing waits for the page table.
-struct Ahead {
-  const Params& p;
-  int it_end;
-  int it, t, te, r, ctx, kvh;  // the next cache tile to copy (te: end of the item's)
-  int window;                  // first tile of the window, -1: none yet
-  int block;                   // this lane's block, by its index among all blocks of the cache; -1: none
-  int page;                    // and its page in the next window
-  static constexpr int kNone = -0x7fffffff;
-  // The first item from `at` on that has cache tiles.
-  __device__ __forceinline__ void take(int at) {
-    for (it = at; it < it_end; ++it) {
-      const AttnItem* x = p.items + it;
-      t = x->tb; r = x->r; ctx = x->ctx; kvh = x->kvh;
-      te = min(x->te, ceil_div(ctx, kKT));
-      if (t < te) return;
-    }
-  }
-  // Page of this lane's block in the window at tile t0; kNone where it holds no committed key of
-  // the item's tiles.
-  __device__ __forceinline__ void look(int lane, int t0) {
+__device__ __forceinline__ AttnItem fetch_item(const AttnItem* s_items, const AttnItem* g_items,
+                                               int it, int it_begin) {
+  const int k = it - it_begin;
+  return k < kSmemItems ? s_items[k] : g_items[it];
+}
+
+// The copying warp: the cache tiles of the CTA in order into the ring.  Lane j knows block
+// j % 8 of tile j / 8 of a window of four tiles; the pages of a window are read while the
+// window before it is copied, so that nothing waits for the page table.
+template <int ST>
+__device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_items, int it_begin,
+                                           int it_end, uint32_t ring, uint32_t full, uint32_t empty) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kNone = -0x7fffffff;
+  int stage = 0, parity = 1, page = kNone;
+  // page of this lane's block in the window at tile t0; kNone where it holds no committed key of
+  // the item's tiles
+  auto look = [&](const AttnItem& x, int t0) {
     const int pos = t0 * kKT + lane * kBlock, slot = pos >> p.log2_page;
     page = kNone;
-    if (pos >= ctx || t0 + (lane >> 3) >= te) return;
-    page = -1;
-    if (slot < p.max_pages) page = __ldg(p.page_table + (long long)r * p.max_pages + slot);
-  }
-  __device__ __forceinline__ void start(int lane, int at) {
-    take(at);
-    window = -1;
-    if (it < it_end) look(lane, t);
-  }
-  // Copies the next tile into the stage at `dst`.
-  __device__ __forceinline__ void copy(int lane, uint32_t dst, uint32_t bar) {
-    if (it >= it_end) return;
-    if (window < 0 || t == window + 4) {
-      window = t;
-      block = -1;
-      if ((unsigned)page < (unsigned)p.n_pages) {
-        const int lp = p.log2_page - 4, pos = t * kKT + lane * kBlock;
-        block = ((page * p.Hkv + kvh) << lp) + ((pos >> 4) & ((1 << lp) - 1));
-      } else if (page != kNone) {
+    if (pos >= x.ctx || t0 + (lane >> 3) >= x.te) return;
+    page = slot < p.max_pages ? __ldg(p.page_table + (long long)x.r * p.max_pages + slot) : -1;
+  };
+  AttnItem x = fetch_item(s_items, p.items, it_begin, it_begin);
+  look(x, x.tb);
+  const int lp = p.log2_page - 4;
+  bool fresh = true;  // the first pass over the ring finds it empty
+  for (int it = it_begin; it < it_end; ++it) {
+    AttnItem next = x;
+    if (it + 1 < it_end) next = fetch_item(s_items, p.items, it + 1, it_begin);
+    const int te = min(x.te, ceil_div(x.ctx, kKT));
+    for (int t0 = x.tb; t0 < x.te; t0 += 4) {
+      int block = -1;
+      if ((unsigned)page < (unsigned)p.n_pages)
+        block = ((page * p.Hkv + x.kvh) << lp) + (((t0 * kKT + lane * kBlock) >> 4) & ((1 << lp) - 1));
+      else if (page != kNone)
         raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
+      if (t0 + 4 < x.te) look(x, t0 + 4); else look(next, next.tb);
+      const uint8_t* src = p.cache + (long long)(block < 0 ? 0 : block) * kBlockBytes;
+      const unsigned have = __ballot_sync(0xffffffffu, block >= 0);
+      for (int i = 0; i < 4 && t0 + i < te; ++i) {
+        if (!fresh) wait_stage(empty + 8 * stage, parity, p.err);
+        const uint32_t bar = full + 8 * stage;
+        if (lane == 0)
+          ptx::mbar_arrive_expect_tx(bar, __popc(have >> (8 * i) & 0xffu) * kBlockBytes);
+        __syncwarp();
+        if ((lane >> 3) == i && block >= 0)
+          ptx::bulk_load_g2s(ring + stage * kStageBytes + (lane & 7) * kBlockStride, src, kBlockBytes, bar);
+        if (++stage == ST) {
+          stage = 0;
+          parity ^= 1;
+          fresh = false;
+        }
       }
-      if (t + 4 < te) look(lane, t + 4);
     }
-    const int first = 8 * (t - window);  // lanes first .. first + 7 hold the tile's blocks
-    const bool mine = (lane & ~7) == first && block >= 0;
-    const unsigned n = __popc(__ballot_sync(0xffffffffu, mine));
-    if (lane == first) ptx::mbar_arrive_expect_tx(bar, n * kBlockBytes);
-    __syncwarp();
-    if (mine)
-      ptx::bulk_load_g2s(dst + (lane & 7) * kBlockStride, p.cache + (long long)block * kBlockBytes,
-                         kBlockBytes, bar);
-    if (++t == te) start(lane, it + 1);
+    x = next;
   }
-};
+}
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_kernel(const Params prm) {
@@ -303,6 +320,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   const int it_begin = prm.item_begin[blockIdx.x];
   const int it_end = prm.item_begin[blockIdx.x + 1];
   if (it_begin >= it_end) return;
+  const uint32_t ring = smem_u32(S.ring), full = smem_u32(S.full), empty = smem_u32(S.empty);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 4);
+    }
+    ptx::fence_mbar_init();
+  }
+  {
+    constexpr int kWords = (int)(sizeof(AttnItem) / sizeof(uint4));
+    for (int i = threadIdx.x; i < min(kSmemItems, it_end - it_begin) * kWords; i += kThreads)
+      reinterpret_cast<uint4*>(S.items)[i] = reinterpret_cast<const uint4*>(prm.items + it_begin)[i];
+  }
+  __syncthreads();
+  if (w == kTeam / 32) {
+    copy_tiles<ST>(prm, S.items, it_begin, it_end, ring, full, empty);
+    return;
+  }
+
   const int G = prm.Hq / prm.Hkv;
   uint32_t magic;  // 1024 twice; opaque, so that it stays in a register
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
@@ -311,29 +347,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
   // 2 (b & 3) + (tok & 1) of the PV product, the order of V's fragments: this thread's first
   // key (b = 2 w, tok = g); block 2 w + i is 2 i further, tok + 8 another 32
   const int p_row = 64 * (w >> 1) + 16 * (g >> 2) + 8 * ((g >> 1) & 1) + 4 * (w & 1) + (g & 1);
-
-  // ---- copies, ST - 1 tiles ahead, by one warp (another for each CTA of an SM)
-  const uint32_t ring = smem_u32(S.ring), full = smem_u32(S.full);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) ptx::mbar_init(full + 8 * i, 1);
-    ptx::fence_mbar_init();
-  }
-  __syncthreads();
-  const bool copies = w == (int)(blockIdx.x & 3);
-  Ahead ahead{prm, it_end};
-  if (copies) {
-    ahead.start(lane, it_begin);
-#pragma unroll 1
-    for (int i = 0; i < ST - 1; ++i) ahead.copy(lane, ring + i * kStageBytes, full + 8 * i);
-  }
   int stage = 0, parity = 0;   // of the next cache tile
 
   // ---- Q: tile row n = (block row n / G, head kvh G + n % G), a half-warp holds a row, 8 dims per
   // lane; read in the last tile of the item before
   uint4 qv[NT];
-  auto load_q = [&](const AttnItem* x) {
-    const long long row = (long long)x->c0 + x->i0;
-    const int n_q = x->ni * G, h0 = x->kvh * G;
+  auto load_q = [&](const AttnItem& x) {
+    const long long row = (long long)x.c0 + x.i0;
+    const int n_q = x.ni * G, h0 = x.kvh * G;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int n = 8 * i + 2 * w + (lane >> 4);
@@ -343,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             prm.q + ((row + n / G) * prm.Hq + h0 + n % G) * kD + (lane & 15) * 8);
     }
   };
-  load_q(prm.items + it_begin);
+  load_q(S.items[0]);
 
   for (int it = it_begin; it < it_end; ++it) {
-    const AttnItem item = prm.items[it];
+    const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
     const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
     const int nq = item.ni * G;              // rows of the tile
     const long long row0 = (long long)item.c0 + item.i0;
@@ -378,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           S.cf[n] = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2, 1.17549435e-38f);
       }
     }
-    __syncthreads();
+    team_sync();
     // this thread's rows: 8 j + 2 t4 + {0, 1}
     float l[NT][2];
     float o[2][NT][4];      // O^T: channels 32 w + 16 i + 2 g + {0, 1} x rows
@@ -397,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
       const uint32_t pbuf = sp + ((t - item.tb) & 1) * p_bytes<NT>();
       const uint32_t tile = ring + stage * kStageBytes;
-      if (t == item.te - 1 && it + 1 < it_end) load_q(prm.items + it + 1);
+      if (t == item.te - 1 && it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
       if (cached) wait_stage(full + 8 * stage, parity, prm.err);
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
               for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
               if (g == 0) S.red[w][8 * j + 2 * t4 + e] = m * S.cf[8 * j + 2 * t4 + e];
             }
-          __syncthreads();
+          team_sync();
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -567,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
             }
           }
         // P is whole when the team passes
-        const bool again = __syncthreads_or(top > kMove);
+        const bool again = team_or(top > kMove);
         if (!again || move) {
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -577,11 +598,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           break;
         }
         move = true;
-      }
-      // the stage of the cache tile before this one has been read by all: the next copy goes there
-      if (copies && cached) {
-        const int to = stage == 0 ? ST - 1 : stage - 1;
-        ahead.copy(lane, ring + to * kStageBytes, full + 8 * to);
       }
       // ---- O^T: two m-tiles of 16 channels, rows g and g + 8 being channels 2 g and 2 g + 1;
       // inner steps 4 u + 2 h, + 1 from the four key pairs of either channel's word
@@ -658,9 +674,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
           pv(n >> 1, n & 1, lo, hi);
         }
       }
-      if (cached && ++stage == ST) {
-        stage = 0;
-        parity ^= 1;
+      if (cached) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + 8 * stage);
+        if (++stage == ST) {
+          stage = 0;
+          parity ^= 1;
+        }
       }
     }
 
@@ -673,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         for (int x = 4; x < 32; x <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], x);
         if (g == 0) S.sum[w][8 * j + 2 * t4 + e] = l[j][e];
       }
-    __syncthreads();
+    team_sync();
     const bool split = item.nsplit > 1;
 #pragma unroll
     for (int j = 0; j < NT; ++j)

@@ -9,16 +9,18 @@
 // with (a, b) = (i, i + R/2), or (2i, 2i + 1) in the interleaved form; dims >= R keep y.
 // One rounding, to bf16, at the end.
 //
-// The angle: p f_i reaches 10^6 radians, where an fp32 product is off by 0.06, so the
-// product, the division by 2 pi and the removal of whole turns are done in fp64 (error
-// below 2^-52 of the turns), and the sine and cosine in fp32 on the remaining half turn.
-// They are computed once per row (R/2 threads) and shared by its heads, so the slow fp64
-// pipe sees R/2 angles per row, not per head.
+// The angle: p f_i reaches 10^6 radians, where an fp32 product is off by 0.06.  So f_i / 2 pi
+// is taken once per CTA in fp64 and kept as a 64-bit fixed-point fraction of a turn; its
+// product with p modulo 2^64 is the angle less its whole turns (off by p 2^-53 f_i / 2 pi
+// turns and p 2^-65), which goes to the fp32 sine and cosine.  A row's R/2 angles are computed
+// once and shared by its heads.
 //
-// Layout: one CTA per row; a head is one half-warp, 8 elements per lane (16 bytes of
-// bf16), so the norm is an 8-term sum and four shuffles, and the half form's partner
-// sits (R/2)/8 lanes away.  Bound by HBM: every element is read and written once.
-
+// Layout: a persistent CTA takes `group` rows at a time, its 16 half-warps dealt to the rows;
+// a half-warp holds a head, 8 elements per lane (16 bytes of bf16), so the norm is an
+// 8-term sum and four shuffles, and the half form's partner sits (R/2)/8 lanes away.  The
+// first inputs of a group are under way before its positions are known.  Bound by HBM:
+// every element is read and written once.
+//
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,6 +36,8 @@ constexpr int kD = 128;
 constexpr int kThreads = 256;
 constexpr int kHalfWarps = kThreads / 16;
 constexpr int kBatch = 4;  // heads of a half-warp whose loads are in flight together
+constexpr int kMaxGroup = 16;
+constexpr int kCtasPerSm = 3;
 
 struct RopeParams {
   const void *q_in, *k_in, *v_in;  // v_in nullable
@@ -41,142 +45,217 @@ struct RopeParams {
   const float *q_weight, *k_weight, *inv_freq;
   const int32_t *row_pos, *n_rows;  // n_rows nullable
   __nv_bfloat16 *q, *k, *v;
-  int Hq, Hkv, rotary, heads;
+  int rows, Hq, Hkv, Hv, rotary, log2_group;  // Hv: 0 without values
   float eps, attn_factor;
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// Eight elements of a head as they were read; `x` gives them as four pairs, `from` the eight
+// of another lane of the half-warp.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
-  uint4 a;
+  uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    a = *reinterpret_cast<const uint4*>(p);
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  __device__ __forceinline__ float2 x(int i) const {
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ Vec8 from(unsigned mask, int lane) const {
+    Vec8 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) o.w[i] = __shfl_sync(mask, w[i], lane, 16);
+    return o;
   }
+  __device__ __forceinline__ uint32_t bf16(int i) const { return w[i]; }
 };
 template <>
 struct Vec8<float> {
-  float4 a, b;
+  float2 v[4];
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = make_float2(a.x, a.y); v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y); v[3] = make_float2(b.z, b.w);
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ __forceinline__ float2 x(int i) const { return v[i]; }
+  __device__ __forceinline__ Vec8 from(unsigned mask, int lane) const {
+    Vec8 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o.v[i] = make_float2(__shfl_sync(mask, v[i].x, lane, 16), __shfl_sync(mask, v[i].y, lane, 16));
+    return o;
+  }
+  __device__ __forceinline__ uint32_t bf16(int i) const {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+// The heads first, first + step, .. < n of one part of a row (element pointers of this lane's
+// dims in head 0), N of them in flight.
+template <typename T, int N>
+struct Heads {
+  Vec8<T> in[N];
+  __device__ __forceinline__ void start(const T* src, int first, int step, int n) {
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+      if (first + b * step < n) in[b].load(src + (first + b * step) * kD);
+  }
+  template <typename F>
+  __device__ __forceinline__ void run(const T* src, __nv_bfloat16* dst, int first, int step, int n, F f) {
+    for (int h0 = first; h0 < n; h0 += N * step) {
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        const int h = h0 + b * step;
+        if (h >= n) break;
+        const Vec8<T> x = in[b];
+        if (h + N * step < n) in[b].load(src + (h + N * step) * kD);
+        *reinterpret_cast<uint4*>(dst + h * kD) = f(x);
+      }
+    }
   }
 };
 
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams prm) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(const RopeParams prm) {
   pdl_release();
-  pdl_wait();  // inputs come from the kernels before this one
-  __shared__ float2 s_cs[kD / 2];
-  const long long row = blockIdx.x;
-  const int pos = prm.row_pos[row];
-  if (pos < 0 || (prm.n_rows && row >= *prm.n_rows)) return;  // padding: outputs left as they are
+  __shared__ float2 s_cs[2][kMaxGroup][kD / 2];
+  __shared__ __align__(16) float s_w[2][kD];
   const int hw = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int nqk = prm.Hq + prm.Hkv;
-  const T* q_in = static_cast<const T*>(prm.q_in) + row * prm.q_stride + l * 8;
-  const T* k_in = static_cast<const T*>(prm.k_in) + row * prm.k_stride + l * 8;
-  const T* v_in = static_cast<const T*>(prm.v_in) + row * prm.v_stride + l * 8;
-
-  Vec8<T> in[kBatch];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h0 + b * kHalfWarps;
-      if (h >= prm.heads) continue;
-      in[b].load(h < prm.Hq ? q_in + h * kD : h < nqk ? k_in + (h - prm.Hq) * kD
-                                                      : v_in + (h - nqk) * kD);
-    }
-  };
-  load(hw);
+  const int group = 1 << prm.log2_group, step = kHalfWarps >> prm.log2_group;
   const int half = prm.rotary >> 1;
-  if ((int)threadIdx.x < half) {
-    double turns = (double)pos * (double)prm.inv_freq[threadIdx.x] * 0.15915494309189533577;
-    turns -= rint(turns);
-    float s, c;
-    sincospif(2.f * (float)turns, &s, &c);
-    s_cs[threadIdx.x] = make_float2(c * prm.attn_factor, s * prm.attn_factor);
+  const int my_row = hw & (group - 1), first = hw >> prm.log2_group;
+  const unsigned mask = 0xffffu << (threadIdx.x & 16);  // this half-warp
+  pdl_wait();  // inputs come from the kernels before this one
+  {  // the weights (seen behind the first group's barrier)
+    const float* weight = threadIdx.x < kD ? prm.q_weight : prm.k_weight;
+    s_w[threadIdx.x / kD][threadIdx.x % kD] = weight ? weight[threadIdx.x % kD] : 1.f;
   }
-  __syncthreads();
-  // this lane's cosines and sines: dims 8l .. 8l + 7 (half form: index of the dim within
-  // its half; interleaved: the lane's four pairs)
+  // this thread's angles: frequency i of rows threadIdx.x / 64, + 4, .. of the group
+  const int ai = threadIdx.x & 63;
+  unsigned long long turn = 0;  // f / (2 pi) in 2^-64 turns
+  float factor = prm.attn_factor;
+  if (ai < half) {
+    double t = (double)prm.inv_freq[ai] * 0.15915494309189533577;
+    t -= rint(t);
+    turn = (unsigned long long)__double2ll_rn(t * 18446744073709551616.);
+    if (t != t) factor = __int_as_float(0x7fc00000);
+  }
+  const int n_rows = prm.n_rows ? min(*prm.n_rows, prm.rows) : prm.rows;
   const bool rotated = l * 8 < prm.rotary;
   const bool low = l * 8 < half;
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = INTERLEAVED ? l * 4 + (i >> 1) : l * 8 - (low ? 0 : half) + i;
-    const float2 cs = rotated ? s_cs[at] : make_float2(1.f, 0.f);
-    c[i] = cs.x;
-    // the partner's sign: y_a c - y_b s, y_b c + y_a s
-    s[i] = (INTERLEAVED ? (i & 1) == 0 : low) ? -cs.y : cs.y;
-  }
   const int partner = !rotated ? l : low ? l + (half >> 3) : l - (half >> 3);
 
-  for (int h0 = hw; h0 - hw < prm.heads; h0 += kBatch * kHalfWarps) {
-    if (h0 != hw) load(h0);
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h0 + b * kHalfWarps;
-      if (h - hw >= prm.heads) break;  // uniform over the CTA
-      const bool live = h < prm.heads;
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-      if (live) in[b].get(x);
-      if (h < nqk) {
-        const float* w = h < prm.Hq ? prm.q_weight : prm.k_weight;
-        if (w) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-          const unsigned m = 0xffffu << (threadIdx.x & 16);  // this half-warp
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(m, ss, o);
-          const float r = 1.f / sqrtf(ss * (1.f / kD) + prm.eps);
-          const float4 w0 = reinterpret_cast<const float4*>(w)[2 * l];
-          const float4 w1 = reinterpret_cast<const float4*>(w)[2 * l + 1];
-          x[0] *= r * w0.x; x[1] *= r * w0.y; x[2] *= r * w0.z; x[3] *= r * w0.w;
-          x[4] *= r * w1.x; x[5] *= r * w1.y; x[6] *= r * w1.z; x[7] *= r * w1.w;
-        }
-        float y[8];
-        if (INTERLEAVED) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-        } else {
-          const unsigned m = 0xffffu << (threadIdx.x & 16);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(m, x[i], partner, 16);
-        }
-        if (rotated) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], c[i], y[i] * s[i]);
-        }
-      }
-      if (live) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 v2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-          o[i] = *reinterpret_cast<const uint32_t*>(&v2);
-        }
-        __nv_bfloat16* dst = h < prm.Hq ? prm.q + (row * prm.Hq + h) * kD
-                             : h < nqk  ? prm.k + (row * prm.Hkv + h - prm.Hq) * kD
-                                        : prm.v + (row * prm.Hkv + h - nqk) * kD;
-        reinterpret_cast<uint4*>(dst)[l] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+  int buf = 0;
+  for (int row0 = blockIdx.x << prm.log2_group; row0 < n_rows; row0 += gridDim.x << prm.log2_group, buf ^= 1) {
+    const long long row = row0 + my_row;
+    const bool live = row < n_rows;
+    const T* q_in = static_cast<const T*>(prm.q_in) + row * prm.q_stride + l * 8;
+    const T* k_in = static_cast<const T*>(prm.k_in) + row * prm.k_stride + l * 8;
+    const T* v_in = static_cast<const T*>(prm.v_in) + row * prm.v_stride + l * 8;
+    Heads<T, kBatch * 2 / (int)sizeof(T)> q;
+    Heads<T, kBatch / (int)sizeof(T)> k, v;
+    int pos = -1;
+    if (live) {
+      q.start(q_in, first, step, prm.Hq);
+      k.start(k_in, first, step, prm.Hkv);
+      v.start(v_in, first, step, prm.Hv);
+      pos = prm.row_pos[row];
     }
+    for (int ar = threadIdx.x >> 6; ai < half && ar < group && row0 + ar < n_rows; ar += kThreads / 64) {
+      const unsigned long long z = turn * (unsigned)prm.row_pos[row0 + ar];
+      float s, c;
+      sincospif(__ll2float_rn((long long)z) * 0x1p-63f, &s, &c);
+      s_cs[buf][ar][ai] = make_float2(c * factor, s * factor);
+    }
+    __syncthreads();
+    if (pos < 0) continue;  // a row of padding: outputs left as they are (uniform over the half-warp)
+
+    v.run(v_in, prm.v + row * prm.Hkv * kD + l * 8, first, step, prm.Hv, [&](const Vec8<T>& x) {
+      return make_uint4(x.bf16(0), x.bf16(1), x.bf16(2), x.bf16(3));
+    });
+    // y = r (x c w + partner's x (+- s w of the partner)): the factors of this lane's dims
+    float2 c[4], s[4];
+    auto factors = [&](const float* weight) {
+      float wc[8], ws[8], w[8];
+      load8(weight + l * 8, wc);
+      load8(weight + (INTERLEAVED ? l : partner) * 8, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = INTERLEAVED ? l * 4 + (i >> 1) : l * 8 - (low ? 0 : half) + i;
+        const float2 cs = rotated ? s_cs[buf][my_row][at] : make_float2(1.f, 0.f);
+        wc[i] *= cs.x;
+        // y_a c - y_b s, y_b c + y_a s
+        ws[i] = w[INTERLEAVED ? i ^ 1 : i] * ((INTERLEAVED ? (i & 1) == 0 : low) ? -cs.y : cs.y);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = make_float2(wc[2 * i], wc[2 * i + 1]);
+        s[i] = make_float2(ws[2 * i], ws[2 * i + 1]);
+      }
+    };
+    auto head = [&](const Vec8<T>& v8, bool norm) {
+      float2 r = make_float2(1.f, 1.f);
+      if (norm) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fma2(v8.x(i), v8.x(i), ss);
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+        r.x = r.y = rsqrtf(sum * (1.f / kD) + prm.eps);
+      }
+      float2 y[4];
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = make_float2(v8.x(i).y, v8.x(i).x);
+      } else {
+        const Vec8<T> other = v8.from(mask, partner);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = other.x(i);
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 x = mul2(v8.x(i), c[i]);
+        if (rotated) x = fma2(y[i], s[i], x);
+        x = mul2(x, r);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      return make_uint4(o[0], o[1], o[2], o[3]);
+    };
+    factors(s_w[0]);
+    const bool q_norm = prm.q_weight, k_norm = prm.k_weight;
+    q.run(q_in, prm.q + row * prm.Hq * kD + l * 8, first, step, prm.Hq,
+          [&](const Vec8<T>& x) { return head(x, q_norm); });
+    factors(s_w[1]);
+    k.run(k_in, prm.k + row * prm.Hkv * kD + l * 8, first, step, prm.Hkv,
+          [&](const Vec8<T>& x) { return head(x, k_norm); });
   }
 }
 
@@ -196,14 +275,16 @@ int launch_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in, 
   p.q = static_cast<__nv_bfloat16*>(q);
   p.k = static_cast<__nv_bfloat16*>(k_new);
   p.v = static_cast<__nv_bfloat16*>(v_new);
-  p.Hq = Hq; p.Hkv = Hkv; p.rotary = rotary_dim;
-  p.heads = Hq + Hkv + (v_in ? Hkv : 0);
+  p.rows = rows; p.Hq = Hq; p.Hkv = Hkv; p.rotary = rotary_dim;
+  p.log2_group = rows > 1000 ? 2 : 0;
+  p.Hv = v_in ? Hkv : 0;
   p.eps = eps; p.attn_factor = attn_factor;
   void (*fn)(RopeParams) =
       dtype == DSPARK_BF16
           ? (interleaved ? qk_norm_rope_kernel<__nv_bfloat16, true> : qk_norm_rope_kernel<__nv_bfloat16, false>)
           : (interleaved ? qk_norm_rope_kernel<float, true> : qk_norm_rope_kernel<float, false>);
-  return launch_pdl(fn, dim3(rows), dim3(kThreads), 0, stream, p) == cudaSuccess ? DSPARK_OK
+  const int groups = ceil_div(rows, 1 << p.log2_group), most = num_sms_cached() * kCtasPerSm;
+  return launch_pdl(fn, dim3(groups < most ? groups : most), dim3(kThreads), 0, stream, p) == cudaSuccess ? DSPARK_OK
                                                                                   : DSPARK_ECUDA;
 }
 

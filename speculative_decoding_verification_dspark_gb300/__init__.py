@@ -128,9 +128,9 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(dev)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -372,24 +372,29 @@ def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table
 # ---- query/key norm with rotation, and the 4-bit cache.  These bindings also check types,
 # shapes and that every tensor is on the current device (whose stream the call goes to).
 
-def _arg(t, name, dtype, shape=None):
-    """Address of a dense tensor of this type on the current device."""
+def _current(t):
+    """Index of the current CUDA device, asked for once per call; -2 (no tensor's) if t is not on one."""
+    return torch.cuda.current_device() if t.is_cuda else -2
+
+
+def _arg(t, dev, name, dtype, shape=None):
+    """Address of a dense tensor of this type on the current device `dev`."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise ValueError(f"{name}: expected a {dtype} tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _on_current(t, name)
+    _on_current(t, name, dev)
     return t.data_ptr()
 
 
-def _on_current(t, name):
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _on_current(t, name, dev):
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
-def _rows(t, name, rows, heads, dtype):
+def _rows(t, dev, name, rows, heads, dtype):
     """(address, row stride in elements) of [rows, heads, 128] with dense heads."""
     if t.dtype is not dtype or t.shape != (rows, heads, 128):
         raise ValueError(f"{name}: expected {dtype} [{rows}, {heads}, 128], got {t.dtype} "
@@ -400,7 +405,7 @@ def _rows(t, name, rows, heads, dtype):
         s0 -= s0 % 8
     if s2 != 1 or (heads > 1 and s1 != 128):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    _on_current(t, name)
+    _on_current(t, name, dev)
     return t.data_ptr(), s0
 
 
@@ -425,23 +430,25 @@ def qk_norm_rope(q_in, k_in, v_in, q_weight, k_weight, inv_freq, row_pos, q, k_n
     outputs bf16, dense.  v_in and v_new may be None."""
     rows, Hq, _ = q.shape
     Hkv = k_new.shape[1]
+    dev = _current(q)
     dt = _float_dtype(q_in, "q_in")
-    qp, qs = _rows(q_in, "q_in", rows, Hq, q_in.dtype)
-    kp, ks = _rows(k_in, "k_in", rows, Hkv, q_in.dtype)
+    qp, qs = _rows(q_in, dev, "q_in", rows, Hq, q_in.dtype)
+    kp, ks = _rows(k_in, dev, "k_in", rows, Hkv, q_in.dtype)
     if (v_in is None) != (v_new is None):
         raise ValueError("v_in and v_new go together")
-    vp, vs = (None, 0) if v_in is None else _rows(v_in, "v_in", rows, Hkv, q_in.dtype)
+    vp, vs = (None, 0) if v_in is None else _rows(v_in, dev, "v_in", rows, Hkv, q_in.dtype)
     f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
     _check("dspark_qk_norm_rope", lib().dspark_qk_norm_rope(
         qp, qs, kp, ks, vp, vs, dt,
-        None if q_weight is None else _arg(q_weight, "q_weight", f32, (128,)),
-        None if k_weight is None else _arg(k_weight, "k_weight", f32, (128,)), float(eps),
-        None if inv_freq is None else _arg(inv_freq, "inv_freq", f32),
+        None if q_weight is None else _arg(q_weight, dev, "q_weight", f32, (128,)),
+        None if k_weight is None else _arg(k_weight, dev, "k_weight", f32, (128,)), float(eps),
+        None if inv_freq is None else _arg(inv_freq, dev, "inv_freq", f32),
         0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
-        float(attn_factor), _arg(row_pos, "row_pos", i32, (rows,)),
-        None if n_rows is None else _arg(n_rows, "n_rows", i32, (1,)), rows, Hq, Hkv,
-        _arg(q, "q", bf16, (rows, Hq, 128)), _arg(k_new, "k_new", bf16, (rows, Hkv, 128)),
-        None if v_new is None else _arg(v_new, "v_new", bf16, (rows, Hkv, 128)), _stream(stream)))
+        float(attn_factor), _arg(row_pos, dev, "row_pos", i32, (rows,)),
+        None if n_rows is None else _arg(n_rows, dev, "n_rows", i32, (1,)), rows, Hq, Hkv,
+        _arg(q, dev, "q", bf16, (rows, Hq, 128)), _arg(k_new, dev, "k_new", bf16, (rows, Hkv, 128)),
+        None if v_new is None else _arg(v_new, dev, "v_new", bf16, (rows, Hkv, 128)),
+        _stream(stream, dev)))
 
 
 def kv4_cache(n_pages, Hkv, page_size, device="cuda"):
@@ -454,7 +461,8 @@ def kv4_cache(n_pages, Hkv, page_size, device="cuda"):
 
 
 def _kv4(kv_cache, page_table, cu_seqlens):
-    """(cache address, n_pages, Hkv, page_size, table address, max_pages, B, cu address)."""
+    """(current device, cache address, n_pages, Hkv, page_size, table address, max_pages, B,
+    cu address)."""
     if kv_cache.dim() != 4 or kv_cache.shape[3] != KV4_BLOCK_BYTES:
         raise ValueError("kv_cache: expected uint8 [n_pages, Hkv, page_size / 16, "
                          f"{KV4_BLOCK_BYTES}]")
@@ -462,36 +470,36 @@ def _kv4(kv_cache, page_table, cu_seqlens):
     B = cu_seqlens.numel() - 1
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table: expected [{B}, max_pages]")
-    i32 = torch.int32
-    return (_arg(kv_cache, "kv_cache", torch.uint8), n_pages, Hkv, per * 16,
-            _arg(page_table, "page_table", i32), page_table.shape[1], B,
-            _arg(cu_seqlens, "cu_seqlens", i32))
+    i32, dev = torch.int32, _current(kv_cache)
+    return (dev, _arg(kv_cache, dev, "kv_cache", torch.uint8), n_pages, Hkv, per * 16,
+            _arg(page_table, dev, "page_table", i32), page_table.shape[1], B,
+            _arg(cu_seqlens, dev, "cu_seqlens", i32))
 
 
 def kv4_store(k, v, cu_seqlens, pos0, page_table, kv_cache, k_scale=1.0, v_scale=1.0, stream=None):
     """Quantise packed rows into the 4-bit cache (dspark_kv4_store): row cu_seqlens[r] + i
     of k, v [rows, Hkv, 128] (fp32 or bf16, possibly views of a fused projection) becomes
     position pos0[r] + i of request r."""
-    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    dev, c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
     rows = k.shape[0]
     dt = _float_dtype(k, "k")
-    kp, ks = _rows(k, "k", rows, Hkv, k.dtype)
-    vp, vs = _rows(v, "v", rows, Hkv, k.dtype)
+    kp, ks = _rows(k, dev, "k", rows, Hkv, k.dtype)
+    vp, vs = _rows(v, dev, "v", rows, Hkv, k.dtype)
     _check("dspark_kv4_store", lib().dspark_kv4_store(
-        kp, ks, vp, vs, dt, cu, _arg(pos0, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab,
-        max_pages, n_pages, float(k_scale), float(v_scale), c, _stream(stream)))
+        kp, ks, vp, vs, dt, cu, _arg(pos0, dev, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab,
+        max_pages, n_pages, float(k_scale), float(v_scale), c, _stream(stream, dev)))
 
 
 def kv4_load(kv_cache, cu_seqlens, pos0, page_table, k, v, k_scale=1.0, v_scale=1.0, stream=None):
     """Positions pos0[r] .. of every request back into packed rows k, v [rows, Hkv, 128]
     (fp32 or bf16; dspark_kv4_load)."""
-    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    dev, c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
     rows = k.shape[0]
     dt = _float_dtype(k, "k")
     _check("dspark_kv4_load", lib().dspark_kv4_load(
-        c, cu, _arg(pos0, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab, max_pages, n_pages,
-        float(k_scale), float(v_scale), dt, _arg(k, "k", k.dtype, (rows, Hkv, 128)),
-        _arg(v, "v", k.dtype, (rows, Hkv, 128)), _stream(stream)))
+        c, cu, _arg(pos0, dev, "pos0", torch.int32, (B,)), B, rows, Hkv, page, tab, max_pages,
+        n_pages, float(k_scale), float(v_scale), dt, _arg(k, dev, "k", k.dtype, (rows, Hkv, 128)),
+        _arg(v, dev, "v", k.dtype, (rows, Hkv, 128)), _stream(stream, dev)))
 
 
 def verify_attn_kv4_workspace_size(B, max_rows, Hq, Hkv, max_splits, max_block_rows=0) -> int:
@@ -503,35 +511,35 @@ def verify_attn_kv4(q, k_new, v_new, kv_cache, page_table, ctx_len, cu_seqlens, 
                     out, lse, workspace, k_scale=1.0, v_scale=1.0, stream=None, max_block_rows=0):
     """verify_attn over the 4-bit cache: q [rows, Hq, 128], k_new / v_new [rows, Hkv, 128]
     bf16, kv_cache as kv4_cache gives it, out bf16 [rows, Hq, 128], lse fp32 [rows, Hq]."""
-    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    dev, c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
     rows, Hq, _ = q.shape
     bf16 = torch.bfloat16
     _check("dspark_verify_attn_kv4", lib().dspark_verify_attn_kv4(
-        _arg(q, "q", bf16, (rows, Hq, 128)), _arg(k_new, "k_new", bf16, (rows, Hkv, 128)),
-        _arg(v_new, "v_new", bf16, (rows, Hkv, 128)), c, float(k_scale), float(v_scale), n_pages,
-        tab, max_pages, _arg(ctx_len, "ctx_len", torch.int32, (B,)), cu, B, rows, Hq, Hkv, page,
-        float(scale), int(max_splits), int(max_block_rows), _arg(out, "out", bf16, (rows, Hq, 128)),
-        _arg(lse, "lse", torch.float32, (rows, Hq)), _arg(workspace, "workspace", torch.uint8),
-        workspace.numel(), _stream(stream)))
+        _arg(q, dev, "q", bf16, (rows, Hq, 128)), _arg(k_new, dev, "k_new", bf16, (rows, Hkv, 128)),
+        _arg(v_new, dev, "v_new", bf16, (rows, Hkv, 128)), c, float(k_scale), float(v_scale),
+        n_pages, tab, max_pages, _arg(ctx_len, dev, "ctx_len", torch.int32, (B,)), cu, B, rows, Hq,
+        Hkv, page, float(scale), int(max_splits), int(max_block_rows),
+        _arg(out, dev, "out", bf16, (rows, Hq, 128)), _arg(lse, dev, "lse", torch.float32, (rows, Hq)),
+        _arg(workspace, dev, "workspace", torch.uint8), workspace.numel(), _stream(stream, dev)))
 
 
 def compact_kv4(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table, ctx_len,
                 anchor, free_pages, free_top, kv_cache, committed, n_committed, workspace,
                 k_scale=1.0, v_scale=1.0, stream=None):
     """compact into the 4-bit cache (dspark_compact_kv4)."""
-    c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
+    dev, c, n_pages, Hkv, page, tab, max_pages, B, cu = _kv4(kv_cache, page_table, cu_seqlens)
     gamma, rows = draft_tok.shape[1], k_new.shape[0]
     bf16, i32 = torch.bfloat16, torch.int32
     _check("dspark_compact_kv4", lib().dspark_compact_kv4(
-        _arg(k_new, "k_new", bf16, (rows, Hkv, 128)), _arg(v_new, "v_new", bf16, (rows, Hkv, 128)),
-        Hkv, rows, cu, _arg(accept_len, "accept_len", i32, (B,)),
-        _arg(out_tok, "out_tok", i32, (B,)), _arg(draft_tok, "draft_tok", i32, (B, gamma)), B,
-        gamma, page, max_pages, n_pages, tab, _arg(ctx_len, "ctx_len", i32, (B,)),
-        _arg(anchor, "anchor", i32, (B,)), _arg(free_pages, "free_pages", i32),
-        _arg(free_top, "free_top", i32), c, float(k_scale), float(v_scale),
-        _arg(committed, "committed", i32, (B, gamma + 1)),
-        _arg(n_committed, "n_committed", i32, (B,)), _arg(workspace, "workspace", torch.uint8),
-        workspace.numel(), _stream(stream)))
+        _arg(k_new, dev, "k_new", bf16, (rows, Hkv, 128)),
+        _arg(v_new, dev, "v_new", bf16, (rows, Hkv, 128)), Hkv, rows, cu,
+        _arg(accept_len, dev, "accept_len", i32, (B,)), _arg(out_tok, dev, "out_tok", i32, (B,)),
+        _arg(draft_tok, dev, "draft_tok", i32, (B, gamma)), B, gamma, page, max_pages, n_pages, tab,
+        _arg(ctx_len, dev, "ctx_len", i32, (B,)), _arg(anchor, dev, "anchor", i32, (B,)),
+        _arg(free_pages, dev, "free_pages", i32), _arg(free_top, dev, "free_top", i32), c,
+        float(k_scale), float(v_scale), _arg(committed, dev, "committed", i32, (B, gamma + 1)),
+        _arg(n_committed, dev, "n_committed", i32, (B,)),
+        _arg(workspace, dev, "workspace", torch.uint8), workspace.numel(), _stream(stream, dev)))
 
 
 class StepDesc(ctypes.Structure):

@@ -35,9 +35,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kThreads = 256;
 constexpr int kHalfWarps = kThreads / 16;
-constexpr int kBatch = 4;  // heads of a half-warp whose loads are in flight together
 constexpr int kMaxGroup = 16;
-constexpr int kCtasPerSm = 3;
 
 struct RopeParams {
   const void *q_in, *k_in, *v_in;  // v_in nullable
@@ -140,8 +138,8 @@ struct Heads {
   }
 };
 
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(const RopeParams prm) {
+template <typename T, bool INTERLEAVED, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) qk_norm_rope_kernel(const RopeParams prm) {
   pdl_release();
   __shared__ float2 s_cs[2][kMaxGroup][kD / 2];
   __shared__ __align__(16) float s_w[2][kD];
@@ -151,20 +149,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(cons
   const int my_row = hw & (group - 1), first = hw >> prm.log2_group;
   const unsigned mask = 0xffffu << (threadIdx.x & 16);  // this half-warp
   pdl_wait();  // inputs come from the kernels before this one
-  {  // the weights (seen behind the first group's barrier)
-    const float* weight = threadIdx.x < kD ? prm.q_weight : prm.k_weight;
-    s_w[threadIdx.x / kD][threadIdx.x % kD] = weight ? weight[threadIdx.x % kD] : 1.f;
-  }
-  // this thread's angles: frequency i of rows threadIdx.x / 64, + 4, .. of the group
+  // this thread's angles: frequency i of rows threadIdx.x / 64, + 4, .. of the group; and its weight
   const int ai = threadIdx.x & 63;
+  const float freq = ai < half ? prm.inv_freq[ai] : 0.f;
+  const float* const wp = threadIdx.x < kD ? prm.q_weight : prm.k_weight;
+  const float weight = wp ? wp[threadIdx.x % kD] : 1.f;
   unsigned long long turn = 0;  // f / (2 pi) in 2^-64 turns
   float factor = prm.attn_factor;
-  if (ai < half) {
-    double t = (double)prm.inv_freq[ai] * 0.15915494309189533577;
-    t -= rint(t);
-    turn = (unsigned long long)__double2ll_rn(t * 18446744073709551616.);
-    if (t != t) factor = __int_as_float(0x7fc00000);
-  }
   const int n_rows = prm.n_rows ? min(*prm.n_rows, prm.rows) : prm.rows;
   const bool rotated = l * 8 < prm.rotary;
   const bool low = l * 8 < half;
@@ -177,14 +168,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(cons
     const T* q_in = static_cast<const T*>(prm.q_in) + row * prm.q_stride + l * 8;
     const T* k_in = static_cast<const T*>(prm.k_in) + row * prm.k_stride + l * 8;
     const T* v_in = static_cast<const T*>(prm.v_in) + row * prm.v_stride + l * 8;
-    Heads<T, kBatch * 2 / (int)sizeof(T)> q;
-    Heads<T, kBatch / (int)sizeof(T)> k, v;
+    Heads<T, CTAS == 4 ? 1 : 2> q;
+    Heads<T, 1> k, v;
     int pos = -1;
     if (live) {
       q.start(q_in, first, step, prm.Hq);
       k.start(k_in, first, step, prm.Hkv);
       v.start(v_in, first, step, prm.Hv);
       pos = prm.row_pos[row];
+    }
+    if (row0 == (int)blockIdx.x << prm.log2_group) {  // the first group, whose inputs are under way
+      s_w[threadIdx.x / kD][threadIdx.x % kD] = weight;
+      double t = (double)freq * 0.15915494309189533577;
+      t -= rint(t);
+      turn = (unsigned long long)__double2ll_rn(t * 18446744073709551616.);
+      if (t != t) factor = __int_as_float(0x7fc00000);
     }
     for (int ar = threadIdx.x >> 6; ai < half && ar < group && row0 + ar < n_rows; ar += kThreads / 64) {
       const unsigned long long z = turn * (unsigned)prm.row_pos[row0 + ar];
@@ -259,6 +257,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(cons
   }
 }
 
+// Many rows: four CTAs per SM for bf16 with one query head of a half-warp under way (16384 rows
+// of 56 heads: 94 us; three CTAs 102 with one, 100 with three; two 113), two for fp32 with two
+// (4099 rows of 12 heads: 7.9 us, three CTAs 9.0).  Groups so that a half-warp has two of a
+// row's KV heads, while every CTA has a group: 16384 rows 102 us with groups of 4 against 110
+// with 2 and 111 with 8; 4099 rows 7.4 with 8, 9.1 with 4.  Up to two rows per SM each row has
+// its CTA and the registers of two CTAs per SM (256 rows: 4.8 us, 6.0 with those of three).
+template <typename T, bool INTERLEAVED>
+int launch(RopeParams& p, cudaStream_t stream) {
+  const int sms = num_sms_cached();
+  const bool few = p.rows <= 2 * sms;
+  constexpr int kCtas = sizeof(T) == 2 ? 4 : 2;
+  p.log2_group = 0;
+  if (!few)
+    while ((1 << p.log2_group) < kMaxGroup && (p.Hkv << p.log2_group) < 32 &&
+           (p.rows >> (p.log2_group + 1)) >= kCtas * sms)
+      ++p.log2_group;
+  const int groups = ceil_div(p.rows, 1 << p.log2_group);
+  void (*fn)(RopeParams) =
+      few ? qk_norm_rope_kernel<T, INTERLEAVED, 2> : qk_norm_rope_kernel<T, INTERLEAVED, kCtas>;
+  const int grid = few ? groups : min(groups, kCtas * sms);
+  return launch_pdl(fn, dim3(grid), dim3(kThreads), 0, stream, p) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
+}
+
 }  // namespace
 
 int launch_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in, long long k_stride,
@@ -276,16 +297,11 @@ int launch_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in, 
   p.k = static_cast<__nv_bfloat16*>(k_new);
   p.v = static_cast<__nv_bfloat16*>(v_new);
   p.rows = rows; p.Hq = Hq; p.Hkv = Hkv; p.rotary = rotary_dim;
-  p.log2_group = rows > 1000 ? 2 : 0;
   p.Hv = v_in ? Hkv : 0;
   p.eps = eps; p.attn_factor = attn_factor;
-  void (*fn)(RopeParams) =
-      dtype == DSPARK_BF16
-          ? (interleaved ? qk_norm_rope_kernel<__nv_bfloat16, true> : qk_norm_rope_kernel<__nv_bfloat16, false>)
-          : (interleaved ? qk_norm_rope_kernel<float, true> : qk_norm_rope_kernel<float, false>);
-  const int groups = ceil_div(rows, 1 << p.log2_group), most = num_sms_cached() * kCtasPerSm;
-  return launch_pdl(fn, dim3(groups < most ? groups : most), dim3(kThreads), 0, stream, p) == cudaSuccess ? DSPARK_OK
-                                                                                  : DSPARK_ECUDA;
+  return dtype == DSPARK_BF16
+             ? (interleaved ? launch<__nv_bfloat16, true>(p, stream) : launch<__nv_bfloat16, false>(p, stream))
+             : (interleaved ? launch<float, true>(p, stream) : launch<float, false>(p, stream));
 }
 
 }  // namespace dspark

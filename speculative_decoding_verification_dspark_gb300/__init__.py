@@ -620,10 +620,10 @@ def block_rows_hint_for(gamma, Hq, Hkv, mode) -> int:
 
 def block_rows_hint_for_kv4(gamma, Hq, Hkv) -> int:
     """Rows per request the query tile of the 4-bit cache's attention is sized for: the
-    block's gamma + 1 rows cut into as few tiles of at most 32 query rows as hold them, of
+    block's gamma + 1 rows cut into as few tiles of at most 64 query rows as hold them, of
     even size."""
     G = max(1, Hq // Hkv)
-    tiles = -(-(gamma + 1) // max(1, 32 // G))
+    tiles = -(-(gamma + 1) // max(1, 64 // G))
     return -(-(gamma + 1) // tiles)
 
 

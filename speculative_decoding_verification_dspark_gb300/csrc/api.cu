@@ -529,9 +529,9 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
                          static_cast<cudaStream_t>(stream));
 }
 
-// The attention's query tile over the 4-bit cache holds 32 rows.
+// The attention's query tile over the 4-bit cache holds up to 64 rows.
 static int kv4_block_rows(int Hq, int Hkv, int max_block_rows) {
-  const int most = 32 / (Hq / Hkv);
+  const int most = 64 / (Hq / Hkv);
   return max_block_rows < most ? max_block_rows : most;
 }
 

@@ -42,63 +42,20 @@
 // references move and O and the sums with them.  That vote and the hand-over of P are the
 // tile's one barrier.  A fifth warp issues the bulk copies (a block each) into a ring of tiles.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
-
-#include "attn.h"
-#include "common.cuh"
-#include "kernels.h"
-#include "kv4.cuh"
-#include "ptx.cuh"
+#include "kv4_attn.cuh"
 
 namespace dspark {
 namespace attn {
 namespace kv4a {
 
-using namespace dspark::kv4;
-
-constexpr int kKT = 128;               // keys of a tile
 constexpr int kTeam = 128;             // four warps that compute; a fifth copies
 constexpr int kThreads = 160;
-constexpr int kSmemItems = 16;         // work items of a CTA kept in shared memory
-constexpr float kRefDrop = 6.f;        // reference = maximum - 6 (log2)
-constexpr float kMove = 14.f;          // a key above reference + 14 moves it
-constexpr float kNoRef = -1e30f;       // reference of a row that has seen no key
-constexpr int kMaxCtas = 1024;         // the work list's limit
 
-// CTAs per SM, by registers (the fragments of O^T and S^T are 8 NT each), and the cache tiles
-// that each has in its ring.
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 4 : NT == 4 ? 2 : 3; }
-__host__ __device__ constexpr int stages(int NT) { return NT < 4 ? 2 : 3; }
-// A block's place in a stage: 32 bytes of padding put the blocks that a quad's four threads
-// read at once in different banks.
-constexpr int kBlockStride = kBlockBytes + 32;
-constexpr int kBlocks = kKT / kBlock;
-constexpr int kStageBytes = kBlocks * kBlockStride;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kStages = 2;
+// CTAs per SM for a tile of this many rows, by registers (the fragments of O^T and S^T are one
+// per row); for more than 16 rows those of the wide kernel.
+__host__ __device__ constexpr int ctas_per_sm(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 3 : kWideCtasPerSm; }
 
-struct Params {
-  const __nv_bfloat16 *q, *k_new, *v_new;
-  const uint8_t* cache;
-  const int32_t* page_table;
-  const AttnItem* items;
-  const int* item_begin;
-  __nv_bfloat16* out;
-  float *lse, *ws_o, *ws_lse;
-  unsigned int* err;
-  int Hq, Hkv, log2_page, max_pages, n_pages;
-  float sl2;            // scale * log2(e) * 16 * k_scale
-  float k_unit, v_unit; // 1 / (16 k_scale), 1 / (16 v_scale)
-  float o_unit;         // 16 v_scale
-};
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -122,18 +79,6 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
-}
-// Wait on a stage's barrier; bounded (the error is raised and the call goes on).
-__device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, unsigned int* err) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (ptx::mbar_try_wait_sleep(bar, parity, 20000)) return;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000))
-    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-      raise_error(err, DSPARK_DEVERR_WAIT_TIMEOUT);
-      return;
-    }
 }
 // Barrier of the team, and the same that ors a flag over it.
 __device__ __forceinline__ void team_sync() {
@@ -172,56 +117,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
-  return h2_bits(__hfma2(bits_h2(a), bits_h2(b), bits_h2(c)));
-}
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
-  return h2_bits(__hmul2(bits_h2(a), bits_h2(b)));
-}
-// The expansion's constants as fp16 pairs: 1/16, 1/256, -64.5, -4.5.
-constexpr uint32_t kSixteenth = 0x2c002c00u, k256th = 0x1c001c00u, kBiasLow = 0xd408d408u,
-                   kBiasHigh = 0xc480c480u;
-// Two e4m3 numbers in the low (high) half of a register as an fp16 pair.
-__device__ __forceinline__ uint32_t e4m3_low(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_high(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
-  return r;
-}
-// (w & MASK) | magic in one instruction (magic in a register: two immediates would take two).
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
-  return r;
-}
-// Eight codes of a word -> four pairs (code - 8) s / 16: pair p with s[p], b[p] as the
-// head of the file has them for even (low nibbles) and odd (high nibbles) p.
-__device__ __forceinline__ void expand(uint32_t w, uint32_t magic, uint32_t s0, uint32_t b0,
-                                       uint32_t s1, uint32_t b1, uint32_t s2, uint32_t b2,
-                                       uint32_t s3, uint32_t b3, uint32_t (&o)[4]) {
-  const uint32_t w8 = w >> 8;
-  o[0] = hfma2_bits(masked<0x000f000fu>(w, magic), s0, b0);
-  o[1] = hfma2_bits(masked<0x00f000f0u>(w, magic), s1, b1);
-  o[2] = hfma2_bits(masked<0x000f000fu>(w8, magic), s2, b2);
-  o[3] = hfma2_bits(masked<0x00f000f0u>(w8, magic), s3, b3);
-}
-// x in cache units, two of them as fp16, saturating (a NaN stays one).
-__device__ __forceinline__ float sat16(float x) {
-  return x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f);
-}
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-  return h2_bits(__floats2half2_rn(sat16(a), sat16(b)));
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
 // Chunk j (8 query rows, 16 bytes) of row r of P in shared memory, placed so that neither the
 // eight rows of a fragment nor the rows {0, 1, 8, 9, 16, 17, 24, 25} + x that a warp writes at
 // once share banks: by padding after each eight rows (NT < 4) and by the chunk's place.
@@ -241,20 +136,14 @@ template <int NT>
 struct Smem {
   __align__(128) uint8_t q[8 * NT * 256];
   __align__(128) uint8_t p[2][p_bytes<NT>()];
-  __align__(128) uint8_t ring[stages(NT)][kStageBytes];
+  __align__(128) uint8_t ring[kStages][kStageBytes];
   float cf[8 * NT];          // softmax scale per row
   float ref[4][8 * NT];      // references, a copy per warp
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
   __align__(16) AttnItem items[kSmemItems];
-  __align__(8) uint64_t full[stages(NT)], empty[stages(NT)];
+  __align__(8) uint64_t full[kStages], empty[kStages];
 };
-
-__device__ __forceinline__ AttnItem fetch_item(const AttnItem* s_items, const AttnItem* g_items,
-                                               int it, int it_begin) {
-  const int k = it - it_begin;
-  return k < kSmemItems ? s_items[k] : g_items[it];
-}
 
 // The copying warp: the cache tiles of the CTA in order into the ring.  Lane j knows block
 // j % 8 of tile j / 8 of a window of four tiles; the pages of a window are read while the
@@ -291,7 +180,7 @@ __device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_it
       const uint8_t* src = p.cache + (long long)(block < 0 ? 0 : block) * kBlockBytes;
       const unsigned have = __ballot_sync(0xffffffffu, block >= 0);
       for (int i = 0; i < 4 && t0 + i < te; ++i) {
-        if (!fresh) wait_stage(empty + 8 * stage, parity, p.err);
+        if (!fresh) wait_bar(empty + 8 * stage, parity, p.err);
         const uint32_t bar = full + 8 * stage;
         if (lane == 0)
           ptx::mbar_arrive_expect_tx(bar, __popc(have >> (8 * i) & 0xffu) * kBlockBytes);
@@ -310,10 +199,10 @@ __device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_it
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_kernel(const Params prm) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4_kernel(const Params prm) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<NT>& S = *reinterpret_cast<Smem<NT>*>(smem_raw);
-  constexpr int ST = stages(NT);
+  constexpr int ST = kStages;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   pdl_release();
   pdl_wait();  // the work list and the step's inputs come from earlier kernels
@@ -419,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       const uint32_t pbuf = sp + ((t - item.tb) & 1) * p_bytes<NT>();
       const uint32_t tile = ring + stage * kStageBytes;
       if (t == item.te - 1 && it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
-      if (cached) wait_stage(full + 8 * stage, parity, prm.err);
+      if (cached) wait_bar(full + 8 * stage, parity, prm.err);
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
 #pragma unroll
@@ -483,15 +372,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
       } else if (32 * w < vis) {
         // the request's own rows, bf16 / (16 k_scale)
         const uint4* src = reinterpret_cast<const uint4*>(
-            prm.k_new + ((long long)(item.c0 + (t - ct) * kKT + 32 * w + g) * prm.Hkv + item.kvh) * kD + t4 * 32);
-        const int step = prm.Hkv * kD;  // 8 rows of 8-element pieces
+            prm.k_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD + t4 * 32);
+        const int row_vecs = prm.Hkv * kD / 8;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint4 v[4];
 #pragma unroll
+          for (int k = 0; k < 4; ++k)  // (past the last row that row again: loads in a batch, no branches)
+            v[k] = src[(long long)(min(32 * w + g + 8 * k, vis - 1) * row_vecs) + 2 * (((c >> 1) + t4) & 1) + (c & 1)];
+#pragma unroll
           for (int k = 0; k < 4; ++k)
-            v[k] = 32 * w + g + 8 * k < vis ? src[(long long)k * step + 2 * (((c >> 1) + t4) & 1) + (c & 1)]
-                                            : make_uint4(0, 0, 0, 0);
+            if (32 * w + g + 8 * k >= vis) v[k] = make_uint4(0, 0, 0, 0);
           uint32_t b[NT][4];
           q_frags(c, b);
 #pragma unroll
@@ -658,15 +549,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         const long long step = (long long)prm.Hkv * kD / 2;
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
-          if (64 * (n >> 1) >= vis) break;
+          if (64 * (n >> 1) + 8 * (n & 1) >= vis) continue;  // no key of it
           uint32_t lo[2][4], hi[2][4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const int k = 16 * (t4 + 4 * (n >> 1)) + 8 * (n & 1) + 2 * p;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t y = k < vis ? vn[k * step + 8 * i] : 0u;
-              const uint32_t z = k + 1 < vis ? vn[(k + 1) * step + 8 * i] : 0u;
+              uint32_t y = vn[min(k, vis - 1) * step + 8 * i], z = vn[min(k + 1, vis - 1) * step + 8 * i];
+              if (k >= vis) y = 0;
+              if (k + 1 >= vis) z = 0;
               lo[i][p] = pack16(bf_lo(y) * prm.v_unit, bf_lo(z) * prm.v_unit);
               hi[i][p] = pack16(bf_hi(y) * prm.v_unit, bf_hi(z) * prm.v_unit);
             }
@@ -706,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
         const float lse = sum == 0.f ? -INFINITY : (my_ref[n] + log2f(sum)) * 0.69314718055994530942f;
         const long long at = (row0 + n / G) * prm.Hq + item.kvh * G + n % G;
         if (split) {
-          if (w == 0 && g == 0) prm.ws_lse[(long long)item.slot * 32 + n] = lse;
-          float2* dst = reinterpret_cast<float2*>(prm.ws_o + ((long long)item.slot * 32 + n) * kD + 32 * w) + g;
+          if (w == 0 && g == 0) prm.ws_lse[(long long)item.slot * prm.slot_rows + n] = lse;
+          float2* dst = reinterpret_cast<float2*>(prm.ws_o + ((long long)item.slot * prm.slot_rows + n) * kD + 32 * w) + g;
           dst[0] = make_float2(o[0][j][e] * inv, o[0][j][2 + e] * inv);
           dst[8] = make_float2(o[1][j][e] * inv, o[1][j][2 + e] * inv);
         } else {
@@ -728,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) verify_attn_kv4_ker
 //   lse = log sum_s e^{lse_s},  o = sum_s e^{lse_s - lse} o_s
 __global__ void __launch_bounds__(256)
     combine_kv4_kernel(const int32_t* __restrict__ cu_seqlens, const SplitGroup* __restrict__ groups,
-                       int G, int Hq, const float* __restrict__ ws_o,
+                       int G, int Hq, int slot_rows, const float* __restrict__ ws_o,
                        const float* __restrict__ ws_lse, __nv_bfloat16* __restrict__ out,
                        float* __restrict__ lse) {
   pdl_release();
@@ -739,7 +631,7 @@ __global__ void __launch_bounds__(256)
   const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (ns <= 1 || n >= sg.ni * G) return;
   // piece s is in slot 2 (c_first + s), but for a first piece that is not its CTA's first
-  auto slot = [&](int s) { return (long long)(2 * (sg.c_first + s) + (s == 0 && sg.slot0_last ? 1 : 0)) * 32 + n; };
+  auto slot = [&](int s) { return (long long)(2 * (sg.c_first + s) + (s == 0 && sg.slot0_last ? 1 : 0)) * slot_rows + n; };
   float mx = -INFINITY;
   for (int s = lane; s < ns; s += 32) mx = fmaxf(mx, ws_lse[slot(s)]);
 #pragma unroll
@@ -786,13 +678,12 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   Plan p{};
   const int G = Hq / Hkv;
   const long long rows = (long long)G * (max_block_rows > 0 ? max_block_rows : 1);
-  const int NT = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   p.parts = 1;
-  p.nt = 8 * NT;
+  p.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.rows_per_tile = p.nt / G;
   p.nk = kKT;
   p.d_part = kD;
-  p.ncta = num_sms_cached() * ctas_per_sm(NT);
+  p.ncta = num_sms_cached() * ctas_per_sm(p.nt);
   if (p.ncta > kMaxCtas) p.ncta = kMaxCtas;
   p.max_items = (long long)Hkv * ((long long)max_rows / p.rows_per_tile + B) + p.ncta;
   size_t off = 0;
@@ -804,8 +695,8 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   p.off_items = take(sizeof(AttnItem) * (size_t)p.max_items);
   p.off_begin = take(sizeof(int) * (size_t)(p.ncta + 1));
   p.off_groups = take(sizeof(SplitGroup) * (size_t)p.ncta);
-  p.off_o = take(sizeof(float) * (size_t)2 * p.ncta * 32 * kD);  // slots 2c, 2c + 1 of 32 rows
-  p.off_lse = take(sizeof(float) * (size_t)2 * p.ncta * 32);
+  p.off_o = take(sizeof(float) * (size_t)2 * p.ncta * p.nt * kD);  // slots 2c, 2c + 1
+  p.off_lse = take(sizeof(float) * (size_t)2 * p.ncta * p.nt);
   p.bytes = off;
   return p;
 }
@@ -818,7 +709,7 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   uint8_t* w = static_cast<uint8_t*>(ws);
   // a CTA of the bf16 kernels is an SM; here several share it, and a group may be cut finer
   const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv,
-                                 max_splits * ctas_per_sm(pl.nt / 8), ws, pl, stream);
+                                 max_splits * ctas_per_sm(pl.nt), ws, pl, stream);
   if (rc != DSPARK_OK) return rc;
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -839,17 +730,17 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   while ((1 << p.log2_page) < page_size) ++p.log2_page;
   p.max_pages = max_pages;
   p.n_pages = n_pages;
+  p.slot_rows = pl.nt;
   p.sl2 = scale * 1.4426950408889634f * (16.f * gk);
   p.k_unit = 1.f / (16.f * gk);
   p.v_unit = 1.f / (16.f * gv);
   p.o_unit = 16.f * gv;
   const int lc = pl.nt == 8    ? launch_tile<1>(p, pl.ncta, stream)
                  : pl.nt == 16 ? launch_tile<2>(p, pl.ncta, stream)
-                 : pl.nt == 24 ? launch_tile<3>(p, pl.ncta, stream)
-                               : launch_tile<4>(p, pl.ncta, stream);
+                               : launch_wide(p, pl.nt, pl.ncta, stream);
   if (lc != DSPARK_OK) return lc;
   return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, pl.nt / 8), dim3(256), 0, stream, cu_seqlens,
-                    reinterpret_cast<const SplitGroup*>(w + pl.off_groups), Hq / Hkv, Hq, p.ws_o,
+                    reinterpret_cast<const SplitGroup*>(w + pl.off_groups), Hq / Hkv, Hq, pl.nt, p.ws_o,
                     p.ws_lse, p.out, lse) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }
 

@@ -50,14 +50,14 @@ def test_host_refusals(pkg):
     size = lib.dspark_verify_attn_kv4_workspace_size
     assert size(2, 8, 9, 2, 8, 4) == 0 and size(0, 8, 8, 2, 8, 4) == 0 and size(2, 8, 66, 2, 8, 1) == 0
     assert size(32, 512, 32, 8, 8, 0) == size(32, 512, 32, 8, 8, 2) > 0
-    assert size(32, 512, 32, 8, 8, 8) == size(32, 512, 32, 8, 8, 99) > 0
+    assert size(32, 512, 32, 8, 8, 16) == size(32, 512, 32, 8, 8, 99) > 0
 
 
 def test_hint_and_binding_refusals(pkg):
     assert pkg.block_rows_hint_for_kv4(6, 32, 8) == 7
-    assert pkg.block_rows_hint_for_kv4(16, 32, 8) == 6      # 17 rows in three tiles
-    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 7      # 33 rows in five
-    assert pkg.block_rows_hint_for_kv4(6, 64, 2) == 1
+    assert pkg.block_rows_hint_for_kv4(16, 32, 8) == 9      # 17 rows in two tiles
+    assert pkg.block_rows_hint_for_kv4(32, 32, 8) == 11     # 33 rows in three
+    assert pkg.block_rows_hint_for_kv4(6, 64, 2) == 2       # 7 rows in four
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     c = pkg.kv4_cache(4, 2, 16, device="cpu")
@@ -199,7 +199,7 @@ def test_parity(pkg, ctx, lens, hq, hkv, page, qstd):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("hint,splits", [(0, 2), (1, 32), (8, 3), (16, 8), (99, 1)])
+@pytest.mark.parametrize("hint,splits", [(0, 2), (1, 32), (4, 5), (8, 3), (12, 32), (16, 8), (99, 1)])
 def test_every_tile_and_split(pkg, hint, splits):
     c = _case([700, 1300, 64], [9, 5, 12], 32, 8, 16, seed=5, qstd=3.0)
     call, out, lse = _run(pkg, c, hint, splits)

@@ -217,6 +217,16 @@ struct Two<__nv_bfloat16> {
   __device__ __forceinline__ float2 get() const {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
+  // the two magnitudes, their maximum with others (a NaN stays), and the larger one at the end
+  using Mag = uint32_t;
+  __device__ __forceinline__ Mag mag() const { return w & 0x7fff7fffu; }
+  static __device__ __forceinline__ Mag larger(Mag a, Mag b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float top(Mag a) {
+    return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
 };
 template <>
 struct Two<float> {
@@ -224,6 +234,10 @@ struct Two<float> {
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
   __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
   __device__ __forceinline__ float2 get() const { return v; }
+  using Mag = float;
+  __device__ __forceinline__ Mag mag() const { return max_nan(fabsf(v.x), fabsf(v.y)); }
+  static __device__ __forceinline__ Mag larger(Mag a, Mag b) { return max_nan(a, b); }
+  static __device__ __forceinline__ float top(Mag a) { return a; }
 };
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
@@ -281,29 +295,29 @@ __device__ __forceinline__ void store_v(const T* src, long long stride, uint8_t*
   const int lane = threadIdx.x & 31, c = 64 * part + 2 * lane, tok = lane & 15;
   src += c;
   Two<T> x[kBlock];
+  if (cnt == kBlock) {
 #pragma unroll
-  for (int e = 0; e < kBlock; ++e) {
-    x[e].zero();
-    if (e >= t0 && e < t0 + cnt) x[e].load(src + (e - t0) * stride);
+    for (int e = 0; e < kBlock; ++e) x[e].load(src + e * stride);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kBlock; ++e) {
+      x[e].zero();
+      if (e >= t0 && e < t0 + cnt) x[e].load(src + (e - t0) * stride);
+    }
   }
   // the maxima over the half-warp, token `tok` to this lane
-  float a[kBlock];
+  typename Two<T>::Mag a[kBlock];
 #pragma unroll
-  for (int e = 0; e < kBlock; ++e) {
-    const float2 y = x[e].get();
-    a[e] = max_nan(fabsf(y.x), fabsf(y.y));
-  }
+  for (int e = 0; e < kBlock; ++e) a[e] = x[e].mag();
 #pragma unroll
   for (int o = kBlock / 2; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
-    for (int e = 0; e < o; ++e) {
-      const float other = __shfl_xor_sync(0xffffffffu, up ? a[e] : a[e + o], o);
-      a[e] = max_nan(up ? a[e + o] : a[e], other);
-    }
+    for (int e = 0; e < o; ++e)
+      a[e] = Two<T>::larger(up ? a[e + o] : a[e], __shfl_xor_sync(0xffffffffu, up ? a[e] : a[e + o], o));
   }
   const bool live = tok >= t0 && tok < t0 + cnt;
-  const Step st = step_of(a[0], g);
+  const Step st = step_of(Two<T>::top(a[0]), g);
   uint8_t* const scales = blk + kOffVs + (c >> 5) * kBlock;
   uint32_t w[2][2] = {{0, 0}, {0, 0}};
   if (__all_sync(0xffffffffu, st.plain || !live)) {
@@ -408,7 +422,7 @@ __device__ __forceinline__ void load_v(T* dst, long long stride, const uint8_t* 
 // CTA = (rows_per_cta packed rows, heads_per_cta heads).  The warps take a block's tasks in
 // turn, each another one in the next block: V's are twice as long as K's.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 5)
     kv4_store_kernel(const Kv4Params p, const T* __restrict__ k, long long k_stride,
                      const T* __restrict__ v, long long v_stride, uint8_t* __restrict__ cache) {
   pdl_release();

@@ -474,7 +474,7 @@ int dspark_markov_draft(const float* U, const void* W1, const void* W2, int rank
  *     c_i = attn_factor cos(p f_i),  s_i = attn_factor sin(p f_i),  i < R / 2
  *     (y_a, y_b) <- (y_a c_i - y_b s_i, y_b c_i + y_a s_i)
  * with (a, b) = (i, i + R/2), or (2i, 2i + 1) if interleaved; dims >= R keep y; one
- * rounding to bf16 at the end.  The angle is reduced to less than a turn in fp64.
+ * rounding to bf16 at the end.  The angle is reduced to less than a turn in 64 bits.
  *
  *   q_in, k_in, v_in  [rows, H, 128] of `dtype`, heads dense, rows q_stride /
  *               k_stride / v_stride elements apart (at least H * 128; the parts of
@@ -551,11 +551,11 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * v_new are bf16 as there.  Arguments as dspark_verify_attn, with kv_cache, k_scale
  * and v_scale in place of the two caches, and
  *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
- *   Hq / Hkv <= 32
- *   max_splits: as there, times the CTAs that share an SM (3 to 5)
- *   max_block_rows: a hint as there; the query tile holds 8, 16, 24 or 32 rows of
+ *   Hq / Hkv <= 32; n_pages * Hkv * page_size / 16 < 2^31
+ *   max_splits: as there, times the CTAs that share an SM (2 to 4)
+ *   max_block_rows: a hint as there; the query tile holds 8, 16, 32, 48 or 64 rows of
  *        G = Hq / Hkv heads x block rows, the smallest that holds this many block rows
- *        (or 32); longer segments run as several row tiles.
+ *        (at most 64 / G); longer segments run as several row tiles.
  * Rounding: the cached values and the queries are exact in the products' fp16
  * operands (a query row is scaled by a power of two; elements below 2^-30 of the row's
  * largest may lose bits), block rows are rounded to fp16 after division by
@@ -573,6 +573,7 @@ int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
                            const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
                            int page_size, float scale, int max_splits, int max_block_rows,
                            void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * dspark_compact_kv4 -- dspark_compact into the 4-bit cache: the kept rows of k_new and
  * v_new (bf16 [max_rows, Hkv, 128], dense) are quantised as dspark_kv4_store does.

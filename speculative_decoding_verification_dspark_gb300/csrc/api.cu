@@ -560,6 +560,8 @@ int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
   CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
   CHECK(max_splits >= 1 && max_splits <= 32, DSPARK_EINVAL);
   CHECK(positive(scale), DSPARK_EINVAL);
+  // the kernels number the cache's blocks in 32 bits
+  CHECK(n_pages <= 0x7fffffffLL / ((long long)Hkv * (page_size / 16)), DSPARK_EUNSUPPORTED);
   rc = device_ok();
   if (rc != DSPARK_OK) return rc;
   const attn::Plan pl =

@@ -12,6 +12,11 @@
 // Probabilities are rounded to fp16 (2^-11, a quarter of the output's own rounding in
 // bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
 // down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
+//
+// The softmax takes a tile in one pass against the row references of the tiles before; only if
+// some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
+// references move and O and the sums with them.  Row sums stay in the threads (each sums its
+// own keys) until the item ends.
 #pragma once
 
 #include <cuda_bf16.h>

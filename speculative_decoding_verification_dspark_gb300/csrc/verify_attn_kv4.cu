@@ -4,9 +4,11 @@
 //   o = softmax(scale q.K^T) V over the ctx_len[r] committed keys, whose K and V are
 //   (code - 8) * scale * g, followed by block rows 0..i (bf16); lse = log-sum-exp.
 //
-// A group's 8 NT query rows (NT = 1..4) against tiles of 128 keys, on a team of four
-// warps that is a CTA of its own (with a fifth that copies), several to an SM, persistent over equal ranges of the
-// work list (worklist.cuh).  Both products have the cache on the MMA's M side:
+// Two kernels by the rows of a query tile (G heads x block rows): this one for up to 16, the
+// wide one (verify_attn_kv4_wide.cu) for up to 64.  Here a tile's 8 NT rows (NT = 1, 2) meet
+// tiles of 128 keys on a team of four warps, with a fifth that copies, a CTA of its own,
+// several to an SM, persistent over equal ranges of the work list (worklist.cuh).  Both
+// products have the cache on the MMA's M side:
 //   S^T [128 keys x 8 NT] = K . Q^T     warp w: keys 32 w .. + 31 (two blocks of the cache)
 //   O^T [128 d    x 8 NT] += V^T . P^T  warp w: channels 32 w .. + 31 (one group of V scales)
 // so that warp w expands its keys of K and its channels of V and every code once, and the
@@ -15,33 +17,18 @@
 // thread's 16-byte loads hold it (dims of K: thread t of a quad has group t; keys of V: it
 // has block t of each 64 keys), the same order being given to Q and P in shared memory.
 //
-// Why register fragments (mma.sync) and not tcgen05: the expanded operand of tcgen05 lives in
-// shared or tensor memory, so its threads write every element there and the MMA reads it
-// back.  That kernel was built first (K and V^T expanded into tensor memory by warpgroups of
-// their own, issuers, two softmax streams, 32 warps) and needed about 1200 instructions per
-// tile and scheduler in chains that wait for one another: 2.2 us where HBM needs 0.41 us
-// for the tile's 17 KB.  Here it is 430 + 86 NT, no warp waits for another but at one
-// barrier per tile, and the tensor pipe (2.15 cycles per m16n8k16 and SM, measured) takes
-// 275 cycles per tile and n-tile of 8 rows.
+// Why fragments in registers (mma.sync) for few rows: with tcgen05 the expanded operand goes
+// through tensor memory and the team waits for the products; with mma.sync nothing waits but
+// at one barrier per tile, a tile being 680 instructions on each scheduler.  But m16n8k16
+// takes 2.05 cycles of an SM (measured) and other instructions hardly issue beside it, so
+// each 8 rows more add 260 cycles to a tile for which HBM needs 850.  Measured, this kernel
+// against the wide one: 256 decodes of 5 heads 181 : 293 us, 64 x 3 and 4 rows of 4 heads at
+// 2048 tokens 64 : 77; with tiles of 24 rows 71 : 63 (32 short windows) and 32 rows 194 : 169
+// (131k contexts).
 //
-// Expansion, exact in fp16: a masked pair of nibbles in the mantissa of 1024 (0x6400) is
-// 1024 + c (1024 + 16 c for the high nibbles), and one fused multiply-add gives
-//   (1024 + c) (s / 16) - 64.5 s = (c - 8) s / 16;   (1024 + 16 c) (s / 256) - 4.5 s = the same
-// s has 4 significant bits, so 64.5 s = 129 s / 2 needs 11 and the result 7: every term is
-// an fp16 number for every e4m3 s.  That is 9 instructions for 8 elements.  The factor
-// 16 g goes into the softmax scale (K) and into the output (V).
+// Bound by instruction issue and latency: 256 decodes read 645 MB at 3.6 TB/s.  The copies
+// alone (same blocks, same ring, nothing computed) take 96 us of the 174.
 //
-// Queries become fp16 scaled by a power of two per row (largest element in [2^14, 2^15)),
-// undone in the row's softmax scale: exact but for elements below 2^-30 of the largest.
-// Probabilities are rounded to fp16 (2^-11, a quarter of the output's own rounding in
-// bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
-// down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
-//
-// The softmax takes a tile in one pass against the row references of the tiles before; only if
-// some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
-// references move and O and the sums with them.  That vote and the hand-over of P are the
-// tile's one barrier.  A fifth warp issues the bulk copies (a block each) into a ring of tiles.
-
 #include "kv4_attn.cuh"
 
 namespace dspark {
@@ -50,11 +37,12 @@ namespace kv4a {
 
 constexpr int kTeam = 128;             // four warps that compute; a fifth copies
 constexpr int kThreads = 160;
-
-constexpr int kStages = 2;
+constexpr int kStages = 2;             // cache tiles in a CTA's ring
 // CTAs per SM for a tile of this many rows, by registers (the fragments of O^T and S^T are one
 // per row); for more than 16 rows those of the wide kernel.
-__host__ __device__ constexpr int ctas_per_sm(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 3 : kWideCtasPerSm; }
+__host__ __device__ constexpr int ctas_per_sm(int rows) {
+  return rows <= 8 ? 4 : rows <= 16 ? 3 : kWideCtasPerSm;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -679,6 +667,8 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   const int G = Hq / Hkv;
   const long long rows = (long long)G * (max_block_rows > 0 ? max_block_rows : 1);
   p.parts = 1;
+  // (64 requests of 16 rows of 4 heads: one tile of 64 rows 114 us, two of 32 150; 12 rows: one of
+  // 48 97 us, two of 24 146)
   p.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.rows_per_tile = p.nt / G;
   p.nk = kKT;

@@ -4,45 +4,29 @@
 //   o = softmax(scale q.K^T) V over the ctx_len[r] committed keys, whose K and V are
 //   (code - 8) * scale * g, followed by block rows 0..i (bf16); lse = log-sum-exp.
 //
-// As in the bf16 cache's kernel, keys lie on the MMA's M side and the few query rows on
-// N (up to 32 columns):
+// For query tiles of 17 to 64 rows.  As in the bf16 cache's kernel, keys lie on the MMA's M
+// side and the query rows on N:
 //   S^T [128 keys x N] = K [128 x 128] . Q^T        O^T [128 d x N] += V^T [128 x 128] . P^T
 // by tcgen05.mma with the left operand in tensor memory, written there by the threads that
-// expand the codes.  A team of four warps (one for each quarter of the lanes) is a CTA of its
-// own, four to an SM, each persistent over its range of the work list (worklist.cuh), and all
-// warps run the same code:
-//   1 expand K (thread = key) into tensor memory; barrier; one thread issues S^T
-//   2 expand V into the same columns once S^T is done; softmax (thread = key), P to shared
-//     memory; barrier, which also votes; one thread issues O^T
-// A team waits for its own products twice a tile; the other three teams of the SM work
-// meanwhile.
+// expand the codes.  A CTA, two to an SM, persistent over its range of the work list
+// (worklist.cuh), is nine warps: four expand K (thread = key), a tile ahead; four expand V
+// (the warp's 32 channels); then all eight weigh, each half of them N / 2 of the rows
+// (thread = key).  One barrier of the eight per tile votes on the references, one hands P(t),
+// V(t) and K(t + 1) to the ninth warp, which issues S^T(t + 1) and O^T(t) and refills the ring.
 //
-// Why so.  (a) Warps of different roles (K, V, softmax, issuers, each with its loop) were
-// built first: on a scheduler they fetch from six loops at once and wait for one another, 1.0
-// to 2.2 us a tile.  (b) Fragments in registers and mma.sync: m16n8k16 takes 8.2 cycles of a
-// scheduler and hardly lets other instructions issue beside it (four LOP3 next to each:
-// 11.2 to 12.2), so 32 rows cost 1050 cycles a tile on top of 800 for the rest, where HBM
-// needs 850.  (c) Through shared memory an expanded tile would cost 64 KB of writes and 64 KB
-// of MMA reads per 17 KB of cache.
+// Why so.  Measured with time stamps of the warps: a thread that issues the eight
+// instructions of a product is held for 700 to 1700 cycles (they queue behind the other CTA's), so
+// no warp that computes may issue; with it, and K's and V's operands in columns of their own
+// so that neither waits for the other's product, a tile of 32 rows takes 3500 cycles per CTA
+// (two share an SM), 5800 before.  S^T(t + 1) goes first: K's expansion waits for it and is on
+// the longer path (170 us against 175).  Warps of six different loops (K, V, two softmax
+// streams, issuers) needed 2.2 us a tile, and teams of four warps, four to an SM, 5% more
+// time than this.  More rows than 64 do not fit: N columns of S^T, N of O^T, 64 of K, 64 of V in
+// half of the 512.
 //
-// Expansion, exact in fp16: a masked pair of nibbles in the mantissa of 1024 (0x6400) is
-// 1024 + c (1024 + 16 c for the high nibbles), and one fused multiply-add gives
-//   (1024 + c) (s / 16) - 64.5 s = (c - 8) s / 16;   (1024 + 16 c) (s / 256) - 4.5 s = the same
-// s has 4 significant bits, so 64.5 s = 129 s / 2 needs 11 and the result 7: every term is
-// an fp16 number for every e4m3 s.  That is 9 instructions for 8 elements.  The factor
-// 16 g goes into the softmax scale (K) and into the output (V).
+// Bound by the chain of a tile's steps (no pipe is more than half busy; with one of the 16
+// instructions of the products left it would be 14% faster).  131k contexts of 3 requests (428 MB) 169 us, 2.7 TB/s with the work list and the merge.
 //
-// Queries become fp16 scaled by a power of two per row (largest element in [2^14, 2^15)),
-// undone in the row's softmax scale: exact but for elements below 2^-30 of the largest.
-// Probabilities are rounded to fp16 (2^-11, a quarter of the output's own rounding in
-// bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
-// down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
-//
-// The softmax takes a tile in one pass against the row references of the tiles before; only if
-// some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
-// references move and O and the sums with them.  Row sums stay in the threads (each sums its
-// own keys) until the item ends.
-
 #include "kv4_attn.cuh"
 
 namespace dspark {
@@ -65,7 +49,7 @@ struct WideSmem {
   __align__(1024) uint8_t q[2 * kQBytes];
   __align__(1024) uint8_t p[(N + 31) / 32 * kPBlock];
   __align__(128) uint8_t ring[kStages][kStageBytes];
-  __align__(16) uint8_t scale[8][512];   // V's scale pairs, per warp
+  __align__(16) uint8_t scale[4][512];   // V's scale pairs, per warp of half 1
   __align__(16) float cf[N];             // softmax scale per row
   __align__(16) float ref[8][kHalf];     // negative references, per warp
   __align__(16) float alpha[8][kHalf];   // factors, per warp
@@ -447,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
       if (half == 1) {
         // ---- V's scale pairs of keys 4 lane .. + 3, shared by the warp's channels; keys past the
         // context get scale 0, whatever their page holds
-        const uint32_t vs = smem_addr(S.scale[w]);
+        const uint32_t vs = smem_addr(S.scale[wq]);
         if (cached) {
           uint32_t sc = ld_shared(tile + (lane >> 2) * kBlockStride + kOffVs + wq * kBlock + (lane & 3) * 4);
           const int left = vis - 4 * lane;

@@ -35,8 +35,9 @@ def test_host_refusals(pkg):
     lib, f, off = pkg.load(), ctypes.c_void_p(4096), ctypes.c_void_p(4104)
 
     def call(q=f, c=f, gk=1.0, gv=1.0, tab=f, ctx=f, cu=f, B=2, rows=8, hq=8, hkv=2, page=16,
-             scale=0.1, splits=8, hint=4, out=f, lse=f, ws=f, n=1 << 30):
-        return lib.dspark_verify_attn_kv4(q, f, f, c, gk, gv, 9, tab, 4, ctx, cu, B, rows, hq, hkv, page,
+             scale=0.1, splits=8, hint=4, out=f, lse=f, ws=f, n=1 << 30,
+             pages=9):
+        return lib.dspark_verify_attn_kv4(q, f, f, c, gk, gv, pages, tab, 4, ctx, cu, B, rows, hq, hkv, page,
                                   ctypes.c_float(scale), splits, hint, out, lse, ws, n, None)
 
     for bad in (dict(q=None), dict(c=None), dict(tab=None), dict(ctx=None), dict(cu=None),
@@ -45,7 +46,8 @@ def test_host_refusals(pkg):
                 dict(B=1025), dict(rows=0), dict(scale=0.0), dict(scale=float("nan")),
                 dict(splits=0), dict(splits=33)):
         assert call(**bad) == -1, bad
-    for bad in (dict(hq=9), dict(hq=66), dict(hkv=0), dict(page=8), dict(page=40)):
+    for bad in (dict(hq=9), dict(hq=66), dict(hkv=0), dict(page=8), dict(page=40),
+                dict(page=64, pages=1 << 28), dict(page=1 << 30, pages=1 << 5)):
         assert call(**bad) == -2, bad
     size = lib.dspark_verify_attn_kv4_workspace_size
     assert size(2, 8, 9, 2, 8, 4) == 0 and size(0, 8, 8, 2, 8, 4) == 0 and size(2, 8, 66, 2, 8, 1) == 0

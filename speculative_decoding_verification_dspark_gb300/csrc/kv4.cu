@@ -15,6 +15,12 @@
 // nothing is transposed; a group is a half-warp).  Every warp finds the leaders of the
 // CTA's rows by itself, so the kernels have no barrier.
 //
+// Prompts (65536 rows of 8 heads, bf16): store 82 us, bound by instruction issue (16 per
+// element and lane, 0.60 a cycle; 36 warps per SM by registers, 30 take 88 us), load 58 us,
+// 86% of the copy rate.  Reading the next pair's rows ahead cost more warps than it gave (134
+// us).  A commit of 32 requests is latency: a search of cu_seqlens, the page, the row or the
+// old codes, 5 us a kernel.
+//
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -74,7 +74,7 @@ bool encode_f32_map(CUtensorMap* m, const void* base, int rank, const uint64_t* 
 }  // namespace gqa
 
 namespace kv4a {
-// The attention over the 4-bit cache.  Its plan: a query tile of 8, 16 or 32 rows, several
+// The attention over the 4-bit cache.  Its plan: a query tile of 8 to 64 rows, several
 // CTAs per SM.
 Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows);
 int launch(const void* q, const void* k_new, const void* v_new, const void* cache, int n_pages,

@@ -133,7 +133,11 @@ LENS = [
     ([1, 9, 3, 0, 5], [15, 30, 16, 7, 0], 2, 16, "bf16"),
     ([40, 1, 70, 17], [3, 64, 0, 111], 3, 64, "f32"),
     ([0, 0, 33, 0], [5, 6, 8, 1], 8, 32, "bf16"),
-    ([300, 0, 211], [1, 0, 250], 8, 16, "bf16"),        # many rows: 16 rows to a CTA
+    ([300, 0, 211], [1, 0, 250], 8, 16, "bf16"),
+    # many rows: 16 rows and several heads to a CTA, among them a window of many requests
+    ([1900, 0, 611], [1, 0, 250], 4, 16, "bf16"),
+    ([(7 * i) % 6 for i in range(500)], [(11 * i) % 70 for i in range(500)], 9, 16, "bf16"),
+    ([0] * 40 + [1024] + [0] * 40 + [3] * 9, [5] * 90, 10, 32, "f32"),
     ([1] * 70, list(range(70)), 4, 16, "f32"),
 ]
 
@@ -239,7 +243,7 @@ def test_store_in_a_graph_on_another_stream(pkg):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,gamma,hkv,page", [(1, 1, 1, 16), (7, 6, 2, 16), (40, 16, 8, 64)])
+@pytest.mark.parametrize("B,gamma,hkv,page", [(1, 1, 1, 16), (7, 6, 2, 16), (40, 16, 8, 64), (200, 6, 18, 16)])
 def test_compact_kv4(pkg, B, gamma, hkv, page):
     rng = np.random.default_rng(B)
     ctx = rng.integers(0, 3 * page, size=B)

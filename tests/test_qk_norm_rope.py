@@ -91,6 +91,11 @@ CASES = [  # rows, tail, hq, hkv, rotary, interleaved, dtype, fused, weights, ma
     (3, 1, 1, 1, 96, False, "bf16", False, True, 2 ** 31 - 1, 1.0),
     (9, 0, 16, 16, 16, True, "bf16", True, False, 50, 0.5),
     (4, 0, 70, 3, 0, False, "bf16", True, True, 50, 1.0),
+    # groups of 2, 4, 8 and 16 rows, the last ones cut short
+    (1501, 6, 9, 2, 128, False, "bf16", True, True, 9000, 1.0),
+    (2503, 0, 5, 8, 64, True, "bf16", False, True, 131072, 1.0),
+    (2901, 13, 3, 1, 32, True, "f32", True, True, 1 << 20, 1.0),
+    (9999, 1, 1, 1, 128, False, "bf16", False, True, 2 ** 31 - 1, 1.0),
 ]
 
 
@@ -105,6 +110,8 @@ def _inputs(rows, tail, hq, hkv, rotary, dtype, fused, weights, max_pos, seed=0)
     pos[rows:] = -1
     if rows > 2:
         pos[1] = -1                          # padding in the middle
+    if rows > 100:
+        pos[rows // 2:rows // 2 + 37] = -1
     w = [1 + 0.3 * torch.randn(128, generator=g) if weights else None for _ in range(2)]
     inv = (10000.0 ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / max(rotary, 1))).float()
     dev = [p.cuda() for p in parts]
@@ -155,6 +162,22 @@ def test_rows_from_n_rows_on_and_no_values(pkg):
     pos[7:] = -1
     outs[2] = torch.where((pos >= 0)[:, None, None], parts[2], torch.tensor(7.0).bfloat16()).cuda()
     _check(parts, outs, pos, w, inv, False, 1.0, 1e-6)
+
+
+@pytest.mark.gpu
+def test_one_weight_and_many_rows_cut_by_n_rows(pkg):
+    parts, dev, pos, w, inv = _inputs(2000, 0, 4, 2, 64, "bf16", True, True, 5000)
+    n = torch.tensor([1503], dtype=torch.int32, device="cuda")
+    pos[1503:] = 77                          # (whatever row_pos holds there)
+    for use in ((True, False), (False, True)):
+        wu = [t if u else None for t, u in zip(w, use)]
+        outs = _outputs(2000, 4, 2)
+        pkg.qk_norm_rope(*dev, *[None if t is None else t.cuda() for t in wu], inv.cuda(), pos.cuda(),
+                         *outs, interleaved=True, n_rows=n)
+        torch.cuda.synchronize()
+        cut = pos.clone()
+        cut[1503:] = -1
+        _check(parts, outs, cut, wu, inv, True, 1.0, 1e-6)
 
 
 @pytest.mark.gpu

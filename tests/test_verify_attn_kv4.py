@@ -184,6 +184,8 @@ SHAPES = [  # ctx, lens, hq, hkv, page
     ([260, 0, 60], [33, 20, 1], 6, 2, 16),
     ([77, 130], [150, 140], 4, 4, 16),
     ([2500], [3], 16, 2, 128),
+    ([1700, 3, 900], [16, 12, 15], 8, 2, 16),             # 64 query rows to a tile
+    ([130, 640], [64, 33], 2, 2, 32),
     ([40] * 50, [1] * 50, 4, 2, 16),
 ]
 
@@ -211,8 +213,12 @@ def test_every_tile_and_split(pkg, hint, splits):
     _check(c, out, lse)
 
 
+BOTH = pytest.mark.parametrize("hint", [2, 8, 12, 16])  # both kernels: 8 (or 16), 32, 48, 64 rows
+
+
 @pytest.mark.gpu
-def test_rising_maxima_and_far_scales(pkg):
+@BOTH
+def test_rising_maxima_and_far_scales(pkg, hint):
     """Scores that grow along the context (every tile moves the running maximum), and
     group scales at both ends of e4m3."""
     c = _case([900], [3], 4, 1, 16, seed=2, qstd=4.0)
@@ -221,7 +227,7 @@ def test_rising_maxima_and_far_scales(pkg):
         c["cache"][p, 0, 0, 2048:2112] = torch.tensor(0.02 * 1.12 ** i / c["gk"]).clamp(max=448).to(
             torch.float8_e4m3fn).view(torch.uint8)
     c["cache"][pages[-1], 0, 0, 2048 + 16:2112] = 0x7f      # (900 = 56 * 16 + 4)
-    call, out, lse = _run(pkg, c)
+    call, out, lse = _run(pkg, c, hint)
     call()
     torch.cuda.synchronize()
     _check(c, out, lse)
@@ -229,28 +235,30 @@ def test_rising_maxima_and_far_scales(pkg):
     lo = torch.randint(0, 2, c["cache"][..., 2112:].shape, generator=torch.Generator().manual_seed(1))
     c["cache"][..., 2112:] = torch.where(lo > 0, 1, 0x7e).to(torch.uint8)     # 2^-9 and 448
     c["cache"][int(c["table"][0, 12]), :, 0, 2112:].view(2, 4, 16)[:, :, 8:] = 0x7f
-    call, out, lse = _run(pkg, c)
+    call, out, lse = _run(pkg, c, hint)
     call()
     torch.cuda.synchronize()
     _check(c, out, lse)
 
 
 @pytest.mark.gpu
-def test_query_rows_of_very_different_size(pkg):
+@BOTH
+def test_query_rows_of_very_different_size(pkg, hint):
     c = _case([300], [4], 4, 2, 16, seed=4)
     for i, f in enumerate((1e-20, 1e-3, 30.0, 0.0)):
         c["q"][i] *= f
-    call, out, lse = _run(pkg, c)
+    call, out, lse = _run(pkg, c, hint)
     call()
     torch.cuda.synchronize()
     _check(c, out, lse)
 
 
 @pytest.mark.gpu
-def test_nan_query_stays_in_its_row(pkg):
+@BOTH
+def test_nan_query_stays_in_its_row(pkg, hint):
     c = _case([200, 40], [3, 2], 8, 2, 16, seed=6)
     c["q"][1, 3, 7] = float("nan")
-    call, out, lse = _run(pkg, c)
+    call, out, lse = _run(pkg, c, hint)
     call()
     torch.cuda.synchronize()
     assert bool(out[1, 3].isnan().all())
@@ -261,10 +269,11 @@ def test_nan_query_stays_in_its_row(pkg):
 
 
 @pytest.mark.gpu
-def test_long_context_is_split(pkg):
+@BOTH
+def test_long_context_is_split(pkg, hint):
     c = _case([20011], [2], 8, 2, 64, seed=7)
     for splits in (2, 32):
-        call, out, lse = _run(pkg, c, splits=splits)
+        call, out, lse = _run(pkg, c, hint, splits)
         call()
         torch.cuda.synchronize()
         assert pkg.read_device_error() == 0
@@ -272,12 +281,13 @@ def test_long_context_is_split(pkg):
 
 
 @pytest.mark.gpu
-def test_bad_page_and_row_overflow(pkg):
+@BOTH
+def test_bad_page_and_row_overflow(pkg, hint):
     c = _case([200, 100], [3, 2], 8, 2, 16, seed=8)
     for bad in (-5, c["cache"].shape[0]):
         keep = c["table"].clone()
         c["table"][0, 3] = bad
-        call, out, lse = _run(pkg, c)
+        call, out, lse = _run(pkg, c, hint)
         call()
         assert pkg.read_device_error() == 0x10
         c["table"] = keep
@@ -287,7 +297,7 @@ def test_bad_page_and_row_overflow(pkg):
     d = dict(c)
     for k in ("q", "k_new", "v_new"):
         d[k] = c[k][:4]
-    call, out, lse = _run(pkg, d)
+    call, out, lse = _run(pkg, d, hint)
     call()
     assert pkg.read_device_error() == 0x1
     assert bool((out == 5.0).all())

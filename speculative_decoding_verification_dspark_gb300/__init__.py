@@ -130,7 +130,9 @@ def _ptr(t):
 
 def _stream(stream, dev=None):
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        if dev is not None:  # without a Stream object in between, 1 us less
+            return torch._C._cuda_getCurrentRawStream(dev)
+        stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -379,19 +381,16 @@ def _current(t):
 
 def _arg(t, dev, name, dtype, shape=None):
     """Address of a dense tensor of this type on the current device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise ValueError(f"{name}: expected a {dtype} tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _on_current(t, name, dev)
-    return t.data_ptr()
-
-
-def _on_current(t, name, dev):
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+    raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
 def _rows(t, dev, name, rows, heads, dtype):
@@ -405,7 +404,8 @@ def _rows(t, dev, name, rows, heads, dtype):
         s0 -= s0 % 8
     if s2 != 1 or (heads > 1 and s1 != 128):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    _on_current(t, name, dev)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
     return t.data_ptr(), s0
 
 

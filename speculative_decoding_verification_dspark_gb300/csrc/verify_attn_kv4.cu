@@ -19,15 +19,17 @@
 //
 // Why fragments in registers (mma.sync) for few rows: with tcgen05 the expanded operand goes
 // through tensor memory and the team waits for the products; with mma.sync nothing waits but
-// at one barrier per tile, a tile being 680 instructions on each scheduler.  But m16n8k16
+// at one barrier per tile, a tile of 8 rows being 730 instructions on each scheduler (K 210,
+// V 250).  But m16n8k16
 // takes 2.05 cycles of an SM (measured) and other instructions hardly issue beside it, so
 // each 8 rows more add 260 cycles to a tile for which HBM needs 850.  Measured, this kernel
 // against the wide one: 256 decodes of 5 heads 181 : 293 us, 64 x 3 and 4 rows of 4 heads at
 // 2048 tokens 64 : 77; with tiles of 24 rows 71 : 63 (32 short windows) and 32 rows 194 : 169
 // (131k contexts).
 //
-// Bound by instruction issue and latency: 256 decodes read 645 MB at 3.6 TB/s.  The copies
-// alone (same blocks, same ring, nothing computed) take 96 us of the 174.
+// Bound by instruction issue (0.63 per cycle and scheduler, which 18 warps per SM cannot
+// raise): 256 decodes read 646 MB in 168 us, 3.8 TB/s.  The copies alone (same blocks, same
+// ring) take 96 us.
 //
 #include "kv4_attn.cuh"
 

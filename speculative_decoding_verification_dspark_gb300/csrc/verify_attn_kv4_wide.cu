@@ -24,8 +24,10 @@
 // time than this.  More rows than 64 do not fit: N columns of S^T, N of O^T, 64 of K, 64 of V in
 // half of the 512.
 //
-// Bound by the chain of a tile's steps (no pipe is more than half busy; with one of the 16
-// instructions of the products left it would be 14% faster).  131k contexts of 3 requests (428 MB) 169 us, 2.7 TB/s with the work list and the merge.
+// Bound by the chain of a tile's steps: 0.53 instructions per cycle and scheduler, 950 a tile of
+// 32 rows (K 180, V 190, softmax 110, the rest waits, addresses and loops of nine warps), the
+// tensor pipe 13% busy; with two of the products' 16 instructions left it is 17% faster, without
+// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB) 169 us, 2.7 TB/s with the work list and the merge.
 //
 #include "kv4_attn.cuh"
 

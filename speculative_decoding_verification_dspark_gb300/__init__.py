@@ -375,7 +375,8 @@ def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table
 # shapes and that every tensor is on the current device (whose stream the call goes to).
 
 def _current(t):
-    """Index of the current CUDA device, asked for once per call; -2 (no tensor's) if t is not on one."""
+    """Index of the current CUDA device, asked for once per call; -2, which no tensor has, where
+    t is on the host."""
     return torch.cuda.current_device() if t.is_cuda else -2
 
 
@@ -637,9 +638,10 @@ class VerifyStep:
     fills; state (caches, page table, ctx_len, anchor, free stack) is updated in
     place by compact.
 
-    With ``kv4`` (pack -> verify_attn_kv4, which builds its own work list) the cache is the 4-bit one: ``inp["kv_cache"]`` (see kv4_cache), with
+    With ``kv4`` the cache is the 4-bit one: ``inp["kv_cache"]`` (see kv4_cache), with
     ``inp["k_scale"]`` and ``inp["v_scale"]`` (default 1), takes the place of k_cache and
-    v_cache, and ``out`` is bf16.
+    v_cache, ``out`` is bf16, and ``run`` calls pack and verify_attn_kv4, which builds its
+    own work list.
 
     Where ``inp`` holds ``q_in``, ``k_in`` and ``v_in`` (the packed rows' projections), ``run``
     fills q, k_new and v_new from them after the pack (``norm_rope``).

@@ -30,11 +30,6 @@ constexpr int kOffV = 1024;
 constexpr int kOffKs = 2048;
 constexpr int kOffVs = 2112;
 
-// Bytes of one (page, head) slice.
-__host__ __device__ constexpr long long slice_bytes(int page_size) {
-  return (long long)(page_size / kBlock) * kBlockBytes;
-}
-
 __device__ __forceinline__ float e4m3_to_float(uint8_t c) {
   __nv_fp8_e4m3 v;
   v.__x = c;

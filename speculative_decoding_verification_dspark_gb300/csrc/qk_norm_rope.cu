@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) qk_norm_rope_kernel(const Rope
 }
 
 // Many rows: four CTAs per SM for bf16 with one query head of a half-warp under way (16384 rows
-// of 56 heads: 94 us; three CTAs 102 with one, 100 with three; two 113), two for fp32 with two
+// of 56 heads: 94 us; with two under way 97, three CTAs 102, two CTAs 113), two for fp32 with two
 // (4099 rows of 12 heads: 7.9 us, three CTAs 9.0).  Groups so that a half-warp has two of a
 // row's KV heads, while every CTA has a group: 16384 rows 102 us with groups of 4 against 110
 // with 2 and 111 with 8; 4099 rows 7.4 with 8, 9.1 with 4.  Up to two rows per SM each row has

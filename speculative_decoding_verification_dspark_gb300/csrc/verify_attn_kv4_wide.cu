@@ -304,365 +304,365 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
       }
     }
   } else {
-  const float* const cf = S.cf + half * NH;
-  float* const ref = S.ref[w];
-  float* const alpha = S.alpha[w];
-  int stage = 0;                 // of the next cache tile, for V
-  int k_stage = 0, k_parity = 0;  // and for K, a tile ahead
-  int g = 0;                  // tiles
+    const float* const cf = S.cf + half * NH;
+    float* const ref = S.ref[w];
+    float* const alpha = S.alpha[w];
+    int stage = 0;                 // of the next cache tile, for V
+    int k_stage = 0, k_parity = 0;  // and for K, a tile ahead
+    int g = 0;                  // tiles
 
-  // ---- Q: tile row n = (block row n / G, head kvh G + n % G), a half-warp holds a row, 8 dims per
-  // lane; read at the end of the item before
-  const int G_inv = 65535 / G + 1;             // n / G = n G_inv >> 16 for n < 80, G <= 32
-  uint4 qv[N / 16];
-  auto load_q = [&](const AttnItem& x) {
-    const long long row = (long long)x.c0 + x.i0;
-    const int n_q = x.ni * G;
-#pragma unroll
-    for (int i = 0; i < N / 16; ++i) {
-      const int n = 16 * i + 2 * w + (lane >> 4), r = (n * G_inv) >> 16;
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (n < n_q)
-        qv[i] = *reinterpret_cast<const uint4*>(
-            prm.q + ((row + r) * prm.Hq + x.kvh * G + n - r * G) * kD + (lane & 15) * 8);
-    }
-  };
-  load_q(S.items[0]);
-
-  for (int it = it_begin; it < it_end; ++it) {
-    const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
-    const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
-    const int nq = item.ni * G;              // rows of the tile
-    const long long row0 = (long long)item.c0 + item.i0;
-    // ---- Q as fp16 scaled by a power of two per row
-    {
-      const int l = lane & 15;
+    // ---- Q: tile row n = (block row n / G, head kvh G + n % G), a half-warp holds a row, 8 dims per
+    // lane; read at the end of the item before
+    const int G_inv = 65535 / G + 1;             // n / G = n G_inv >> 16 for n < 80, G <= 32
+    uint4 qv[N / 16];
+    auto load_q = [&](const AttnItem& x) {
+      const long long row = (long long)x.c0 + x.i0;
+      const int n_q = x.ni * G;
 #pragma unroll
       for (int i = 0; i < N / 16; ++i) {
-        const int n = 16 * i + 2 * w + (lane >> 4);
-        const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-        uint32_t top = 0;  // largest magnitude, as bits (a NaN is above all)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the largest element's power of two, no smaller than 2^-100 (fp32 holds 2^114)
-        const int e = max((int)(top >> 23), 27);
-        const float f = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = h2_bits(__floats2half2_rn(bf_lo(x[j]) * f, bf_hi(x[j]) * f));
-        st_shared_v4(smem_addr(S.q) + (l >> 3) * WideSmem<N>::kQBytes + sw128_off(n, l & 7),
-                     make_uint4(h[0], h[1], h[2], h[3]));
-        if (l == 0)  // (never 0: a masked score is -inf times it)
-          S.cf[n] = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2, 1.17549435e-38f);
+        const int n = 16 * i + 2 * w + (lane >> 4), r = (n * G_inv) >> 16;
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (n < n_q)
+          qv[i] = *reinterpret_cast<const uint4*>(
+              prm.q + ((row + r) * prm.Hq + x.kvh * G + n - r * G) * kD + (lane & 15) * 8);
       }
-      fence_proxy_async_smem();
-    }
-    for (int k = lane; k < NH; k += 32) ref[k] = -kNoRef;
-    float lacc[NH];                            // this thread's part of each row's sum
-#pragma unroll
-    for (int k = 0; k < NH; ++k) lacc[k] = 0.f;
-
-    // ---- K of tile t into its operand columns: thread = key (half 0)
-    auto expand_k = [&](int t) {
-      const bool cached = t < ct;
-      const int vis = min(item.n_r - (t - ct) * kKT, kKT);  // (of a block tile)
-      if (cached) {
-        wait_bar(full + 8 * k_stage, k_parity, prm.err);
-        const uint32_t tile = ring + k_stage * kStageBytes;
-        if (++k_stage == kStages) {
-          k_stage = 0;
-          k_parity ^= 1;
-        }
-        const uint32_t blk = tile + (kl >> 4) * kBlockStride;
-        const uint32_t sc = ld_shared(blk + kOffKs + (kl & 15) * 4);
-        const uint32_t s01 = e4m3_low(sc), s23 = e4m3_high(sc);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 v = ld_shared_v4(blk + c * 256 + (kl & 15) * 16);
-          const uint32_t s = __byte_perm(c < 2 ? s01 : s23, 0, (c & 1) ? 0x3232 : 0x1010);
-          const uint32_t sl = hmul2_bits(s, kSixteenth), bl = hmul2_bits(s, kBiasLow);
-          const uint32_t sh = hmul2_bits(s, k256th), bh = hmul2_bits(s, kBiasHigh);
-          uint32_t o[16], x[4];
-          const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            expand(word[q], magic, sl, bl, sh, bh, sl, bl, sh, bh, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * q + e] = x[e];
-          }
-          tmem_st16u(t_lane + kTmemK + c * 16, o);
-        }
-      } else if (32 * wq < vis) {  // (other keys are masked, whatever the columns hold)
-        // the request's own rows: bf16 / (16 k_scale)
-        const int bi = (t - ct) * kKT + min(kl, vis - 1);  // (past the last row that row again)
-        const uint4* src = reinterpret_cast<const uint4*>(
-            prm.k_new + ((long long)(item.c0 + bi) * prm.Hkv + item.kvh) * kD);
-#pragma unroll 2
-        for (int c = 0; c < 4; ++c) {
-          uint4 v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = src[c * 4 + j];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (kl >= vis) v[j] = make_uint4(0, 0, 0, 0);
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              o[4 * j + q] = pack16(bf_lo(x[q]) * prm.k_unit, bf_hi(x[q]) * prm.k_unit);
-          }
-          tmem_st16u(t_lane + kTmemK + c * 16, o);
-        }
-      }
-      tmem_wait_st();
     };
-    if (half == 0) expand_k(item.tb);
-    tc_fence_before();
-    hand_over();
-    team_sync();  // cf
+    load_q(S.items[0]);
 
-#pragma unroll 1
-    for (int t = item.tb; t < item.te; ++t, ++g) {
-      const bool cached = t < ct;
-      const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
-      const uint32_t tile = ring + stage * kStageBytes;
-      if (half == 1) {
-        // ---- V's scale pairs of keys 4 lane .. + 3, shared by the warp's channels; keys past the
-        // context get scale 0, whatever their page holds
-        const uint32_t vs = smem_addr(S.scale[wq]);
-        if (cached) {
-          uint32_t sc = ld_shared(tile + (lane >> 2) * kBlockStride + kOffVs + wq * kBlock + (lane & 3) * 4);
-          const int left = vis - 4 * lane;
-          if (left < 4) sc = left <= 0 ? 0u : sc & ((1u << (8 * left)) - 1u);
-          const uint32_t s0 = e4m3_low(sc), s1 = e4m3_high(sc);
-          const uint32_t at = vs + ((lane & 7) >> 1) * 128 + (lane >> 3) * 32 + (lane & 1) * 8;
-          st_shared_v2(at, hmul2_bits(s0, kSixteenth), hmul2_bits(s1, k256th));
-          st_shared_v2(at + 16, hmul2_bits(s0, kBiasLow), hmul2_bits(s1, kBiasHigh));
-          __syncwarp();
+    for (int it = it_begin; it < it_end; ++it) {
+      const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
+      const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
+      const int nq = item.ni * G;              // rows of the tile
+      const long long row0 = (long long)item.c0 + item.i0;
+      // ---- Q as fp16 scaled by a power of two per row
+      {
+        const int l = lane & 15;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+          const int n = 16 * i + 2 * w + (lane >> 4);
+          const uint32_t x[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+          uint32_t top = 0;  // largest magnitude, as bits (a NaN is above all)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, max((x[j] << 16) & 0x7fffffffu, x[j] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // the largest element's power of two, no smaller than 2^-100 (fp32 holds 2^114)
+          const int e = max((int)(top >> 23), 27);
+          const float f = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = h2_bits(__floats2half2_rn(bf_lo(x[j]) * f, bf_hi(x[j]) * f));
+          st_shared_v4(smem_addr(S.q) + (l >> 3) * WideSmem<N>::kQBytes + sw128_off(n, l & 7),
+                       make_uint4(h[0], h[1], h[2], h[3]));
+          if (l == 0)  // (never 0: a masked score is -inf times it)
+            S.cf[n] = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * prm.sl2, 1.17549435e-38f);
         }
-        if (g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // V's columns and P are free
-        tc_fence_after();
-        // ---- V into the operand columns
+        fence_proxy_async_smem();
+      }
+      for (int k = lane; k < NH; k += 32) ref[k] = -kNoRef;
+      float lacc[NH];                            // this thread's part of each row's sum
+#pragma unroll
+      for (int k = 0; k < NH; ++k) lacc[k] = 0.f;
+
+      // ---- K of tile t into its operand columns: thread = key (half 0)
+      auto expand_k = [&](int t) {
+        const bool cached = t < ct;
+        const int vis = min(item.n_r - (t - ct) * kKT, kKT);  // (of a block tile)
         if (cached) {
-          uint2 v[4];
-          // quad lane % 4 expands blocks 2 (lane % 4) and + 1, channels lane / 4 + 8 j of the warp's 32
-          const uint32_t src = tile + 2 * (lane & 3) * kBlockStride + kOffV + (wq * 32 + (lane >> 2)) * 8;
-#pragma unroll
-          for (int uh = 0; uh < 4; ++uh) {
-            const int h = uh & 1;
-            if (h == 0) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = ld_shared_v2(src + (uh >> 1) * kBlockStride + j * 64);
-            }
-            const uint32_t at = vs + uh * 128 + (lane & 3) * 32;
-            const uint4 s = ld_shared_v4(at), c = ld_shared_v4(at + 16);
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {  // lanes 0-15 and 16-31 of the quadrant
-              uint32_t lo[4], hi[4];
-              expand(h ? v[2 * f].y : v[2 * f].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, lo);
-              expand(h ? v[2 * f + 1].y : v[2 * f + 1].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, hi);
-              const uint32_t o[8] = {lo[0], lo[1], hi[0], hi[1], lo[2], lo[3], hi[2], hi[3]};
-              tmem_st_16x256b_x2(t_lane + (static_cast<uint32_t>(f * 16) << 16) + kTmemV + uh * 16, o);
-            }
+          wait_bar(full + 8 * k_stage, k_parity, prm.err);
+          const uint32_t tile = ring + k_stage * kStageBytes;
+          if (++k_stage == kStages) {
+            k_stage = 0;
+            k_parity ^= 1;
           }
-        } else {
-          const long long step = (long long)prm.Hkv * kD;
-          const __nv_bfloat16* vn =
-              prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD + kl;
-#pragma unroll 1
-          for (int i = 0; 32 * i < vis; ++i) {
+          const uint32_t blk = tile + (kl >> 4) * kBlockStride;
+          const uint32_t sc = ld_shared(blk + kOffKs + (kl & 15) * 4);
+          const uint32_t s01 = e4m3_low(sc), s23 = e4m3_high(sc);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = ld_shared_v4(blk + c * 256 + (kl & 15) * 16);
+            const uint32_t s = __byte_perm(c < 2 ? s01 : s23, 0, (c & 1) ? 0x3232 : 0x1010);
+            const uint32_t sl = hmul2_bits(s, kSixteenth), bl = hmul2_bits(s, kBiasLow);
+            const uint32_t sh = hmul2_bits(s, k256th), bh = hmul2_bits(s, kBiasHigh);
+            uint32_t o[16], x[4];
+            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              expand(word[q], magic, sl, bl, sh, bh, sl, bl, sh, bh, x);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[4 * q + e] = x[e];
+            }
+            tmem_st16u(t_lane + kTmemK + c * 16, o);
+          }
+        } else if (32 * wq < vis) {  // (other keys are masked, whatever the columns hold)
+          // the request's own rows: bf16 / (16 k_scale)
+          const int bi = (t - ct) * kKT + min(kl, vis - 1);  // (past the last row that row again)
+          const uint4* src = reinterpret_cast<const uint4*>(
+              prm.k_new + ((long long)(item.c0 + bi) * prm.Hkv + item.kvh) * kD);
+#pragma unroll 2
+          for (int c = 0; c < 4; ++c) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = src[c * 4 + j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (kl >= vis) v[j] = make_uint4(0, 0, 0, 0);
             uint32_t o[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int k = 32 * i + 2 * j;
-              // (past the last row that row again: loads in a batch, no branches)
-              float x = __bfloat162float(vn[min(k, vis - 1) * step]) * prm.v_unit;
-              float y = __bfloat162float(vn[min(k + 1, vis - 1) * step]) * prm.v_unit;
-              if (k >= vis) x = 0.f;
-              if (k + 1 >= vis) y = 0.f;
-              o[j] = pack16(x, y);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                o[4 * j + q] = pack16(bf_lo(x[q]) * prm.k_unit, bf_hi(x[q]) * prm.k_unit);
             }
-            tmem_st16u(t_lane + kTmemV + i * 16, o);
+            tmem_st16u(t_lane + kTmemK + c * 16, o);
           }
         }
-      } else if (t + 1 < item.te) {
-        wait_bar(qk_done, g & 1, prm.err);  // K's columns are free
-        tc_fence_after();
-        expand_k(t + 1);
-      }
-      wait_bar(qk_done, g & 1, prm.err);
-      if (half == 0 && g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // P is free
-      tc_fence_after();
-      // ---- softmax of rows half NH .. + NH - 1: row n sees this key iff n >= nmin
-      const bool masked = !cached || vis < kKT;
-      int nmin = 0;
-      if (masked) nmin = (kl >= vis ? 1 << 30 : cached ? 0 : ((t - ct) * kKT + kl - item.i0) * G) - half * NH;
-      // this key's step of the PV product: that of V's expansion in a cache tile
-      const int pr = cached ? 16 * (lane >> 2) + 4 * wq + (lane & 3) : kl;
-      const int nc8 = ceil_div(min(nq - half * NH, NH), 8);  // 8-row pieces that hold rows (may be < 0)
-      float s[NH];
-      auto scores = [&]() {
-#pragma unroll
-        for (int q = 0; q < NH / 8; ++q)
-          tmem_ld8(t_lane + kTmemS + half * NH + q * 8, *reinterpret_cast<float(*)[8]>(&s[q * 8]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < NH / 8; ++q)  // (not read before the wait)
-          asm volatile("" : "+f"(s[q * 8]), "+f"(s[q * 8 + 1]), "+f"(s[q * 8 + 2]), "+f"(s[q * 8 + 3]),
-                            "+f"(s[q * 8 + 4]), "+f"(s[q * 8 + 5]), "+f"(s[q * 8 + 6]), "+f"(s[q * 8 + 7]));
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < NH; ++k) s[k] = nmin <= k ? s[k] : -INFINITY;
-        }
+        tmem_wait_st();
       };
-      bool move = t == item.tb;  // the references have to move first
+      if (half == 0) expand_k(item.tb);
+      tc_fence_before();
+      hand_over();
+      team_sync();  // cf
+
 #pragma unroll 1
-      for (;;) {
-        scores();
-        if (move) {
-          // ---- the tile's maximum per row, over the four warps of the half
+      for (int t = item.tb; t < item.te; ++t, ++g) {
+        const bool cached = t < ct;
+        const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
+        const uint32_t tile = ring + stage * kStageBytes;
+        if (half == 1) {
+          // ---- V's scale pairs of keys 4 lane .. + 3, shared by the warp's channels; keys past the
+          // context get scale 0, whatever their page holds
+          const uint32_t vs = smem_addr(S.scale[wq]);
+          if (cached) {
+            uint32_t sc = ld_shared(tile + (lane >> 2) * kBlockStride + kOffVs + wq * kBlock + (lane & 3) * 4);
+            const int left = vis - 4 * lane;
+            if (left < 4) sc = left <= 0 ? 0u : sc & ((1u << (8 * left)) - 1u);
+            const uint32_t s0 = e4m3_low(sc), s1 = e4m3_high(sc);
+            const uint32_t at = vs + ((lane & 7) >> 1) * 128 + (lane >> 3) * 32 + (lane & 1) * 8;
+            st_shared_v2(at, hmul2_bits(s0, kSixteenth), hmul2_bits(s1, k256th));
+            st_shared_v2(at + 16, hmul2_bits(s0, kBiasLow), hmul2_bits(s1, kBiasHigh));
+            __syncwarp();
+          }
+          if (g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // V's columns and P are free
+          tc_fence_after();
+          // ---- V into the operand columns
+          if (cached) {
+            uint2 v[4];
+            // quad lane % 4 expands blocks 2 (lane % 4) and + 1, channels lane / 4 + 8 j of the warp's 32
+            const uint32_t src = tile + 2 * (lane & 3) * kBlockStride + kOffV + (wq * 32 + (lane >> 2)) * 8;
+#pragma unroll
+            for (int uh = 0; uh < 4; ++uh) {
+              const int h = uh & 1;
+              if (h == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = ld_shared_v2(src + (uh >> 1) * kBlockStride + j * 64);
+              }
+              const uint32_t at = vs + uh * 128 + (lane & 3) * 32;
+              const uint4 s = ld_shared_v4(at), c = ld_shared_v4(at + 16);
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {  // lanes 0-15 and 16-31 of the quadrant
+                uint32_t lo[4], hi[4];
+                expand(h ? v[2 * f].y : v[2 * f].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, lo);
+                expand(h ? v[2 * f + 1].y : v[2 * f + 1].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, hi);
+                const uint32_t o[8] = {lo[0], lo[1], hi[0], hi[1], lo[2], lo[3], hi[2], hi[3]};
+                tmem_st_16x256b_x2(t_lane + (static_cast<uint32_t>(f * 16) << 16) + kTmemV + uh * 16, o);
+              }
+            }
+          } else {
+            const long long step = (long long)prm.Hkv * kD;
+            const __nv_bfloat16* vn =
+                prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD + kl;
+#pragma unroll 1
+            for (int i = 0; 32 * i < vis; ++i) {
+              uint32_t o[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int k = 32 * i + 2 * j;
+                // (past the last row that row again: loads in a batch, no branches)
+                float x = __bfloat162float(vn[min(k, vis - 1) * step]) * prm.v_unit;
+                float y = __bfloat162float(vn[min(k + 1, vis - 1) * step]) * prm.v_unit;
+                if (k >= vis) x = 0.f;
+                if (k + 1 >= vis) y = 0.f;
+                o[j] = pack16(x, y);
+              }
+              tmem_st16u(t_lane + kTmemV + i * 16, o);
+            }
+          }
+        } else if (t + 1 < item.te) {
+          wait_bar(qk_done, g & 1, prm.err);  // K's columns are free
+          tc_fence_after();
+          expand_k(t + 1);
+        }
+        wait_bar(qk_done, g & 1, prm.err);
+        if (half == 0 && g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // P is free
+        tc_fence_after();
+        // ---- softmax of rows half NH .. + NH - 1: row n sees this key iff n >= nmin
+        const bool masked = !cached || vis < kKT;
+        int nmin = 0;
+        if (masked) nmin = (kl >= vis ? 1 << 30 : cached ? 0 : ((t - ct) * kKT + kl - item.i0) * G) - half * NH;
+        // this key's step of the PV product: that of V's expansion in a cache tile
+        const int pr = cached ? 16 * (lane >> 2) + 4 * wq + (lane & 3) : kl;
+        const int nc8 = ceil_div(min(nq - half * NH, NH), 8);  // 8-row pieces that hold rows (may be < 0)
+        float s[NH];
+        auto scores = [&]() {
+#pragma unroll
+          for (int q = 0; q < NH / 8; ++q)
+            tmem_ld8(t_lane + kTmemS + half * NH + q * 8, *reinterpret_cast<float(*)[8]>(&s[q * 8]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < NH / 8; ++q)  // (not read before the wait)
+            asm volatile("" : "+f"(s[q * 8]), "+f"(s[q * 8 + 1]), "+f"(s[q * 8 + 2]), "+f"(s[q * 8 + 3]),
+                              "+f"(s[q * 8 + 4]), "+f"(s[q * 8 + 5]), "+f"(s[q * 8 + 6]), "+f"(s[q * 8 + 7]));
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < NH; ++k) s[k] = nmin <= k ? s[k] : -INFINITY;
+          }
+        };
+        bool move = t == item.tb;  // the references have to move first
+#pragma unroll 1
+        for (;;) {
+          scores();
+          if (move) {
+            // ---- the tile's maximum per row, over the four warps of the half
+#pragma unroll
+            for (int q = 0; q < NH / 8; ++q) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = s[q * 8 + k] * cf[q * 8 + k];
+              const float m = reduce8<true>(v, lane);
+              if (lane < 8) S.red[w][q * 8 + lane] = m;
+            }
+            team_sync();
+            for (int k = lane; k < NH; k += 32) {
+              const float tm = fmaxf(fmaxf(S.red[4 * half][k], S.red[4 * half + 1][k]),
+                                     fmaxf(S.red[4 * half + 2][k], S.red[4 * half + 3][k]));
+              const float old = -ref[k];
+              float al = 1.f;
+              if (tm - kRefDrop > old + (kMove - kRefDrop)) {
+                al = old == kNoRef ? 0.f : fast_exp2(old - (tm - kRefDrop));
+                ref[k] = -(tm - kRefDrop);
+              }
+              alpha[k] = al;
+            }
+            __syncwarp();
+            if (t > item.tb) {  // (the products of the tiles before are done)
+#pragma unroll 1
+              for (int q = 0; q < NH / 8; ++q) {
+                float o[8];
+                tmem_ld8(t_lane + kTmemO + half * NH + q * 8, o);
+                tmem_wait_ld8(o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] *= alpha[q * 8 + k];
+                tmem_st8(t_lane + kTmemO + half * NH + q * 8, o);
+              }
+#pragma unroll
+              for (int k = 0; k < NH; ++k) lacc[k] *= alpha[k];
+            }
+          }
+          // ---- P of this key against the references
+          float top = -INFINITY;
 #pragma unroll
           for (int q = 0; q < NH / 8; ++q) {
-            float v[8];
+            if (q >= nc8) break;
+            uint32_t pk[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = s[q * 8 + k] * cf[q * 8 + k];
-            const float m = reduce8<true>(v, lane);
-            if (lane < 8) S.red[w][q * 8 + lane] = m;
-          }
-          team_sync();
-          for (int k = lane; k < NH; k += 32) {
-            const float tm = fmaxf(fmaxf(S.red[4 * half][k], S.red[4 * half + 1][k]),
-                                   fmaxf(S.red[4 * half + 2][k], S.red[4 * half + 3][k]));
-            const float old = -ref[k];
-            float al = 1.f;
-            if (tm - kRefDrop > old + (kMove - kRefDrop)) {
-              al = old == kNoRef ? 0.f : fast_exp2(old - (tm - kRefDrop));
-              ref[k] = -(tm - kRefDrop);
+            for (int h = 0; h < 2; ++h) {
+              const int k = q * 8 + h * 4;
+              const float4 c4 = reinterpret_cast<const float4*>(cf)[q * 2 + h];
+              const float4 r4 = reinterpret_cast<const float4*>(ref)[q * 2 + h];
+              unpack(fma2(f2(s[k], s[k + 1]), f2(c4.x, c4.y), f2(r4.x, r4.y)), s[k], s[k + 1]);
+              unpack(fma2(f2(s[k + 2], s[k + 3]), f2(c4.z, c4.w), f2(r4.z, r4.w)), s[k + 2], s[k + 3]);
+              top = fmaxf(top, fmaxf(s[k], s[k + 1]));
+              top = fmaxf(top, fmaxf(s[k + 2], s[k + 3]));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[k + j] = fast_exp2(s[k + j]);
+              pk[2 * h] = h2_bits(__floats2half2_rn(s[k], s[k + 1]));
+              pk[2 * h + 1] = h2_bits(__floats2half2_rn(s[k + 2], s[k + 3]));
             }
-            alpha[k] = al;
+            const int chunk = half * (NH / 8) + q;
+            st_shared_v4(smem_addr(S.p) + (chunk >> 2) * WideSmem<N>::kPBlock + sw64_off(pr, chunk & 3),
+                         make_uint4(pk[0], pk[1], pk[2], pk[3]));
           }
-          __syncwarp();
-          if (t > item.tb) {  // (the products of the tiles before are done)
-#pragma unroll 1
-            for (int q = 0; q < NH / 8; ++q) {
-              float o[8];
-              tmem_ld8(t_lane + kTmemO + half * NH + q * 8, o);
-              tmem_wait_ld8(o);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= alpha[q * 8 + k];
-              tmem_st8(t_lane + kTmemO + half * NH + q * 8, o);
-            }
-#pragma unroll
-            for (int k = 0; k < NH; ++k) lacc[k] *= alpha[k];
-          }
+          fence_proxy_async_smem();
+          tmem_wait_st();
+          tc_fence_before();
+          // P and V are whole when the team passes; a key far above its row's reference sends the
+          // tile through once more, after the references have moved
+          const bool again = team_or(top > kMove);
+          if (!again || move) break;
+          move = true;
         }
-        // ---- P of this key against the references
-        float top = -INFINITY;
+        hand_over();
+        if (cached) {
+          if (++stage == kStages) stage = 0;
+        }
 #pragma unroll
         for (int q = 0; q < NH / 8; ++q) {
           if (q >= nc8) break;
-          uint32_t pk[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = q * 8 + h * 4;
-            const float4 c4 = reinterpret_cast<const float4*>(cf)[q * 2 + h];
-            const float4 r4 = reinterpret_cast<const float4*>(ref)[q * 2 + h];
-            unpack(fma2(f2(s[k], s[k + 1]), f2(c4.x, c4.y), f2(r4.x, r4.y)), s[k], s[k + 1]);
-            unpack(fma2(f2(s[k + 2], s[k + 3]), f2(c4.z, c4.w), f2(r4.z, r4.w)), s[k + 2], s[k + 3]);
-            top = fmaxf(top, fmaxf(s[k], s[k + 1]));
-            top = fmaxf(top, fmaxf(s[k + 2], s[k + 3]));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[k + j] = fast_exp2(s[k + j]);
-            pk[2 * h] = h2_bits(__floats2half2_rn(s[k], s[k + 1]));
-            pk[2 * h + 1] = h2_bits(__floats2half2_rn(s[k + 2], s[k + 3]));
-          }
-          const int chunk = half * (NH / 8) + q;
-          st_shared_v4(smem_addr(S.p) + (chunk >> 2) * WideSmem<N>::kPBlock + sw64_off(pr, chunk & 3),
-                       make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          for (int k = q * 8; k < q * 8 + 8; k += 2)
+            unpack(add2(f2(lacc[k], lacc[k + 1]), f2(s[k], s[k + 1])), lacc[k], lacc[k + 1]);
         }
-        fence_proxy_async_smem();
-        tmem_wait_st();
-        tc_fence_before();
-        // P and V are whole when the team passes; a key far above its row's reference sends the
-        // tile through once more, after the references have moved
-        const bool again = team_or(top > kMove);
-        if (!again || move) break;
-        move = true;
       }
-      hand_over();
-      if (cached) {
-        if (++stage == kStages) stage = 0;
-      }
+
+      if (it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
+      // ---- epilogue: row sums over the half's warps, O^T / l; thread = channel
 #pragma unroll
       for (int q = 0; q < NH / 8; ++q) {
-        if (q >= nc8) break;
+        float v[8];
 #pragma unroll
-        for (int k = q * 8; k < q * 8 + 8; k += 2)
-          unpack(add2(f2(lacc[k], lacc[k + 1]), f2(s[k], s[k + 1])), lacc[k], lacc[k + 1]);
+        for (int k = 0; k < 8; ++k) v[k] = lacc[q * 8 + k];
+        const float l = reduce8<false>(v, lane);
+        if (lane < 8) S.red[w][q * 8 + lane] = l;
       }
-    }
-
-    if (it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
-    // ---- epilogue: row sums over the half's warps, O^T / l; thread = channel
-#pragma unroll
-    for (int q = 0; q < NH / 8; ++q) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = lacc[q * 8 + k];
-      const float l = reduce8<false>(v, lane);
-      if (lane < 8) S.red[w][q * 8 + lane] = l;
-    }
-    team_sync();
-    const bool split = item.nsplit > 1;
-    const int n_half = min(nq - half * NH, NH);  // rows of this half (may be < 0)
-    for (int k = lane; k < NH; k += 32) {
-      const float l = (S.red[4 * half][k] + S.red[4 * half + 1][k]) +
-                      (S.red[4 * half + 2][k] + S.red[4 * half + 3][k]);
-      alpha[k] = l == 0.f ? 0.f : prm.o_unit / l;
-      if (wq == 0 && k < n_half) {
-        const int n = half * NH + k;
-        const float v = l == 0.f ? -INFINITY : (log2f(l) - ref[k]) * 0.69314718055994530942f;
-        if (split)
-          prm.ws_lse[(long long)item.slot * prm.slot_rows + n] = v;
-        else
-          prm.lse[(row0 + ((n * G_inv) >> 16)) * prm.Hq + item.kvh * G + n - ((n * G_inv) >> 16) * G] = v;
-      }
-    }
-    __syncwarp();
-    wait_bar(pv_done, (g - 1) & 1, prm.err);
-    tc_fence_after();
-    float* dst_ws = prm.ws_o + ((long long)item.slot * prm.slot_rows + half * NH) * kD + kl;
-    int h = half * NH - ((half * NH * G_inv) >> 16) * G;   // head of the group
-    __nv_bfloat16* dst = prm.out + ((row0 + ((half * NH * G_inv) >> 16)) * prm.Hq + item.kvh * G + h) * kD + kl;
-    const long long next = (long long)(prm.Hq - G) * kD;   // to the next block row's heads
-#pragma unroll 1
-    for (int q = 0; q * 8 < n_half; ++q) {
-      float o[8];
-      tmem_ld8(t_lane + kTmemO + half * NH + q * 8, o);
-      tmem_wait_ld8(o);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float y = o[k] * alpha[q * 8 + k];
-        if (q * 8 + k < n_half) {
+      team_sync();
+      const bool split = item.nsplit > 1;
+      const int n_half = min(nq - half * NH, NH);  // rows of this half (may be < 0)
+      for (int k = lane; k < NH; k += 32) {
+        const float l = (S.red[4 * half][k] + S.red[4 * half + 1][k]) +
+                        (S.red[4 * half + 2][k] + S.red[4 * half + 3][k]);
+        alpha[k] = l == 0.f ? 0.f : prm.o_unit / l;
+        if (wq == 0 && k < n_half) {
+          const int n = half * NH + k;
+          const float v = l == 0.f ? -INFINITY : (log2f(l) - ref[k]) * 0.69314718055994530942f;
           if (split)
-            dst_ws[(q * 8 + k) * kD] = y;
+            prm.ws_lse[(long long)item.slot * prm.slot_rows + n] = v;
           else
-            *dst = __float2bfloat16(y);
-        }
-        dst += kD;
-        if (++h == G) {
-          h = 0;
-          dst += next;
+            prm.lse[(row0 + ((n * G_inv) >> 16)) * prm.Hq + item.kvh * G + n - ((n * G_inv) >> 16) * G] = v;
         }
       }
+      __syncwarp();
+      wait_bar(pv_done, (g - 1) & 1, prm.err);
+      tc_fence_after();
+      float* dst_ws = prm.ws_o + ((long long)item.slot * prm.slot_rows + half * NH) * kD + kl;
+      int h = half * NH - ((half * NH * G_inv) >> 16) * G;   // head of the group
+      __nv_bfloat16* dst = prm.out + ((row0 + ((half * NH * G_inv) >> 16)) * prm.Hq + item.kvh * G + h) * kD + kl;
+      const long long next = (long long)(prm.Hq - G) * kD;   // to the next block row's heads
+#pragma unroll 1
+      for (int q = 0; q * 8 < n_half; ++q) {
+        float o[8];
+        tmem_ld8(t_lane + kTmemO + half * NH + q * 8, o);
+        tmem_wait_ld8(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float y = o[k] * alpha[q * 8 + k];
+          if (q * 8 + k < n_half) {
+            if (split)
+              dst_ws[(q * 8 + k) * kD] = y;
+            else
+              *dst = __float2bfloat16(y);
+          }
+          dst += kD;
+          if (++h == G) {
+            h = 0;
+            dst += next;
+          }
+        }
+      }
+      // (the next item's Q, cf and references are written behind this barrier's and the products'
+      // last reads; `red` next after its first tile's barrier)
     }
-    // (the next item's Q, cf and references are written behind this barrier's and the products'
-    // last reads; `red` next after its first tile's barrier)
-  }
   }
 
   tc_fence_before();

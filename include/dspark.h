@@ -563,7 +563,7 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * fp16; sums are fp32, and out is rounded once to bf16.
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
  * undefined.
- * Two kernels after the work list's; nothing waits on another CTA.
+ * Two kernels; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
                                              int max_block_rows);

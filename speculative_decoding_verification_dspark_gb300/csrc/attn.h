@@ -49,10 +49,6 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* k_ca
            int d_qk, int d_v, int page_size, float scale, int max_splits, float* out, float* lse,
            void* ws, const Plan& pl, cudaStream_t stream, bool planned = false);
 
-// The work list of plan `pl` into the workspace, by a kernel of its own.
-int launch_worklist(const int32_t* ctx_len, const int32_t* cu_seqlens, int B, int max_rows, int Hkv,
-                    int max_splits, void* ws, const Plan& pl, cudaStream_t stream);
-
 namespace gqa {
 // Query-row tile (32, 64 or 128) for G = Hq/Hkv heads per KV head and
 // max_block_rows rows per request segment (<= 0 counts as 1); a longer segment

@@ -140,7 +140,6 @@ struct Heads {
 
 template <typename T, bool INTERLEAVED, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) qk_norm_rope_kernel(const RopeParams prm) {
-  pdl_release();
   __shared__ float2 s_cs[2][kMaxGroup][kD / 2];
   __shared__ __align__(16) float s_w[2][kD];
   const int hw = threadIdx.x >> 4, l = threadIdx.x & 15;

@@ -137,21 +137,6 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int d_qk, int d_v, int max_split
   return p;
 }
 
-int launch_worklist(const int32_t* ctx_len, const int32_t* cu_seqlens, int B, int max_rows, int Hkv,
-                    int max_splits, void* ws, const Plan& pl, cudaStream_t stream) {
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  const int max_items = pl.max_items > 0x7fffffff ? 0x7fffffff : (int)pl.max_items;
-  const int splits = max_splits < 2 ? 2 : max_splits;
-  return launch_pdl(worklist_kernel, dim3(1), dim3(1024), 0, stream, ctx_len, cu_seqlens, B, max_rows,
-                    Hkv, pl.parts, pl.rows_per_tile, pl.nk, pl.ncta, splits, pl.mla ? 1 : 0,
-                    max_items, reinterpret_cast<AttnItem*>(w + pl.off_items),
-                    reinterpret_cast<int*>(w + pl.off_begin),
-                    reinterpret_cast<SplitGroup*>(w + pl.off_groups),
-                    device_error_word()) == cudaSuccess
-             ? DSPARK_OK
-             : DSPARK_ECUDA;
-}
-
 int launch(const void* q, const void* k_new, const void* v_new, const void* k_cache,
            const void* v_cache, int n_pages, const int32_t* page_table, int max_pages,
            const int32_t* ctx_len, const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv,
@@ -165,13 +150,16 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* k_ca
   float* ws_lse = reinterpret_cast<float*>(w + pl.off_lse);
   unsigned int* err = device_error_word();
   const int ncta = pl.ncta;
+  const int max_items = pl.max_items > 0x7fffffff ? 0x7fffffff : (int)pl.max_items;
+  const int splits = max_splits < 2 ? 2 : (max_splits > 32 ? 32 : max_splits);
 
   // planned: the pack call already wrote the work list (same plan) into ws
-  if (!planned) {
-    const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv,
-                                   max_splits > 32 ? 32 : max_splits, ws, pl, stream);
-    if (rc != DSPARK_OK) return rc;
-  }
+  if (!planned &&
+      launch_pdl(worklist_kernel, dim3(1), dim3(1024), 0, stream, ctx_len, cu_seqlens, B, max_rows,
+                 Hkv, pl.parts, pl.rows_per_tile, pl.nk, ncta, splits, pl.mla ? 1 : 0, max_items,
+                 items, item_begin,
+                 groups, err) != cudaSuccess)
+    return DSPARK_ECUDA;
 
   if (pl.mla) {
     const int rc = mla::launch_kernel(q, k_new, k_cache, n_pages, page_table, max_pages, max_rows,

@@ -7,7 +7,7 @@
 // Two kernels by the rows of a query tile (G heads x block rows): this one for up to 16, the
 // wide one (verify_attn_kv4_wide.cu) for up to 64.  Here a tile's 8 NT rows (NT = 1, 2) meet
 // tiles of 128 keys on a team of four warps, with a fifth that copies, a CTA of its own,
-// several to an SM, persistent over equal ranges of the work list (worklist.cuh).  Both
+// several to an SM, persistent over an equal share of the key tiles (own_items).  Both
 // products have the cache on the MMA's M side:
 //   S^T [128 keys x 8 NT] = K . Q^T     warp w: keys 32 w .. + 31 (two blocks of the cache)
 //   O^T [128 d    x 8 NT] += V^T . P^T  warp w: channels 32 w .. + 31 (one group of V scales)
@@ -139,8 +139,8 @@ struct Smem {
 // j % 8 of tile j / 8 of a window of four tiles; the pages of a window are read while the
 // window before it is copied, so that nothing waits for the page table.
 template <int ST>
-__device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_items, int it_begin,
-                                           int it_end, uint32_t ring, uint32_t full, uint32_t empty) {
+__device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_items, const OwnItems& own,
+                                           uint32_t ring, uint32_t full, uint32_t empty) {
   const int lane = threadIdx.x & 31;
   constexpr int kNone = -0x7fffffff;
   int stage = 0, parity = 1, page = kNone;
@@ -152,13 +152,13 @@ __device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_it
     if (pos >= x.ctx || t0 + (lane >> 3) >= x.te) return;
     page = slot < p.max_pages ? __ldg(p.page_table + (long long)x.r * p.max_pages + slot) : -1;
   };
-  AttnItem x = fetch_item(s_items, p.items, it_begin, it_begin);
+  AttnItem x = s_items[0];
   look(x, x.tb);
   const int lp = p.log2_page - 4;
   bool fresh = true;  // the first pass over the ring finds it empty
-  for (int it = it_begin; it < it_end; ++it) {
+  for (int it = 0; it < own.n; ++it) {
     AttnItem next = x;
-    if (it + 1 < it_end) next = fetch_item(s_items, p.items, it + 1, it_begin);
+    if (it + 1 < own.n) next = fetch_item(s_items, own.more, it + 1);
     const int te = min(x.te, ceil_div(x.ctx, kKT));
     for (int t0 = x.tb; t0 < x.te; t0 += 4) {
       int block = -1;
@@ -194,11 +194,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
   Smem<NT>& S = *reinterpret_cast<Smem<NT>*>(smem_raw);
   constexpr int ST = kStages;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  pdl_release();
-  pdl_wait();  // the work list and the step's inputs come from earlier kernels
-  const int it_begin = prm.item_begin[blockIdx.x];
-  const int it_end = prm.item_begin[blockIdx.x + 1];
-  if (it_begin >= it_end) return;
+  // (no early release: what follows would take the first SMs that fall free, and the next call's
+  // persistent CTAs come to lie unevenly: 256 decodes 197 us one call after another, 170 without)
+  pdl_wait();  // the step's inputs come from earlier kernels
   const uint32_t ring = smem_u32(S.ring), full = smem_u32(S.full), empty = smem_u32(S.empty);
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -207,14 +205,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
     }
     ptx::fence_mbar_init();
   }
-  {
-    constexpr int kWords = (int)(sizeof(AttnItem) / sizeof(uint4));
-    for (int i = threadIdx.x; i < min(kSmemItems, it_end - it_begin) * kWords; i += kThreads)
-      reinterpret_cast<uint4*>(S.items)[i] = reinterpret_cast<const uint4*>(prm.items + it_begin)[i];
-  }
-  __syncthreads();
+  static_assert(sizeof(ItemScratch) <= sizeof(S.ring), "the scratch lies in the ring");
+  const OwnItems own = own_items<kThreads>(prm, *reinterpret_cast<ItemScratch*>(S.ring), S.items);
+  if (own.n == 0) return;
   if (w == kTeam / 32) {
-    copy_tiles<ST>(prm, S.items, it_begin, it_end, ring, full, empty);
+    copy_tiles<ST>(prm, S.items, own, ring, full, empty);
     return;
   }
 
@@ -245,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
   };
   load_q(S.items[0]);
 
-  for (int it = it_begin; it < it_end; ++it) {
-    const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
+  for (int it = 0; it < own.n; ++it) {
+    const AttnItem item = fetch_item(S.items, own.more, it);
     const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
     const int nq = item.ni * G;              // rows of the tile
     const long long row0 = (long long)item.c0 + item.i0;
@@ -297,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
       const int vis = cached ? min(ctx - t * kKT, kKT) : min(item.n_r - (t - ct) * kKT, kKT);
       const uint32_t pbuf = sp + ((t - item.tb) & 1) * p_bytes<NT>();
       const uint32_t tile = ring + stage * kStageBytes;
-      if (t == item.te - 1 && it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
+      if (t == item.te - 1 && it + 1 < own.n) load_q(fetch_item(S.items, own.more, it + 1));
       if (cached) wait_bar(full + 8 * stage, parity, prm.err);
       // ---- S^T: two m-tiles of 16 keys
       float s[2][NT][4];
@@ -613,7 +608,6 @@ __global__ void __launch_bounds__(256)
                        int G, int Hq, int slot_rows, const float* __restrict__ ws_o,
                        const float* __restrict__ ws_lse, __nv_bfloat16* __restrict__ out,
                        float* __restrict__ lse) {
-  pdl_release();
   pdl_wait();  // inputs come from the kernels before this one
   const int lane = threadIdx.x & 31;
   const SplitGroup sg = groups[blockIdx.x];
@@ -685,7 +679,6 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
     return at;
   };
   p.off_items = take(sizeof(AttnItem) * (size_t)p.max_items);
-  p.off_begin = take(sizeof(int) * (size_t)(p.ncta + 1));
   p.off_groups = take(sizeof(SplitGroup) * (size_t)p.ncta);
   p.off_o = take(sizeof(float) * (size_t)2 * p.ncta * p.nt * kD);  // slots 2c, 2c + 1
   p.off_lse = take(sizeof(float) * (size_t)2 * p.ncta * p.nt);
@@ -699,18 +692,21 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
            float scale, float gk, float gv, int max_splits, void* out, float* lse, void* ws,
            const Plan& pl, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  // a CTA of the bf16 kernels is an SM; here several share it, and a group may be cut finer
-  const int rc = launch_worklist(ctx_len, cu_seqlens, B, max_rows, Hkv,
-                                 max_splits * ctas_per_sm(pl.nt), ws, pl, stream);
-  if (rc != DSPARK_OK) return rc;
   Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
   p.v_new = static_cast<const __nv_bfloat16*>(v_new);
   p.cache = static_cast<const uint8_t*>(cache);
   p.page_table = page_table;
-  p.items = reinterpret_cast<const AttnItem*>(w + pl.off_items);
-  p.item_begin = reinterpret_cast<const int*>(w + pl.off_begin);
+  p.ctx_len = ctx_len;
+  p.cu_seqlens = cu_seqlens;
+  p.items = reinterpret_cast<AttnItem*>(w + pl.off_items);
+  p.groups = reinterpret_cast<SplitGroup*>(w + pl.off_groups);
+  p.B = B;
+  p.max_rows = max_rows;
+  p.rows_per_tile = pl.rows_per_tile;
+  // a CTA of the bf16 kernels is an SM; here several share it, and a group may be cut finer
+  p.max_splits = (max_splits < 2 ? 2 : max_splits) * ctas_per_sm(pl.nt);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.ws_o = reinterpret_cast<float*>(w + pl.off_o);
@@ -732,7 +728,7 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
                                : launch_wide(p, pl.nt, pl.ncta, stream);
   if (lc != DSPARK_OK) return lc;
   return launch_pdl(combine_kv4_kernel, dim3(pl.ncta, pl.nt / 8), dim3(256), 0, stream, cu_seqlens,
-                    reinterpret_cast<const SplitGroup*>(w + pl.off_groups), Hq / Hkv, Hq, pl.nt, p.ws_o,
+                    p.groups, Hq / Hkv, Hq, pl.nt, p.ws_o,
                     p.ws_lse, p.out, lse) == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }
 

@@ -8,8 +8,8 @@
 // side and the query rows on N:
 //   S^T [128 keys x N] = K [128 x 128] . Q^T        O^T [128 d x N] += V^T [128 x 128] . P^T
 // by tcgen05.mma with the left operand in tensor memory, written there by the threads that
-// expand the codes.  A CTA, two to an SM, persistent over its range of the work list
-// (worklist.cuh), is nine warps: four expand K (thread = key), a tile ahead; four expand V
+// expand the codes.  A CTA, two to an SM, persistent over its share of the key tiles
+// (own_items), is nine warps: four expand K (thread = key), a tile ahead; four expand V
 // (the warp's 32 channels); then all eight weigh, each half of them N / 2 of the rows
 // (thread = key).  One barrier of the eight per tile votes on the references, one hands P(t),
 // V(t) and K(t + 1) to the ninth warp, which issues S^T(t + 1) and O^T(t) and refills the ring.
@@ -20,15 +20,15 @@
 // so that neither waits for the other's product, a tile of 32 rows takes 3500 cycles per CTA
 // (two share an SM), 5800 before.  S^T(t + 1) goes first: K's expansion waits for it and is on
 // the longer path (170 us against 175).  Warps of six different loops (K, V, two softmax
-// streams, issuers) needed 2.2 us a tile, and teams of four warps, four to an SM, 5% more
-// time than this.  More rows than 64 do not fit: N columns of S^T, N of O^T, 64 of K, 64 of V in
-// half of the 512.
+// streams, issuers) needed 2.2 us a tile; teams of four warps that do everything in turn, four to
+// an SM, take 32 rows as fast but hold no more (whole blocks of 17 rows 216 us against 170).  More
+// rows than 64 do not fit: N columns of S^T, N of O^T, 64 of K, 64 of V in half of the 512.
 //
 // Bound by the chain of a tile's steps: 0.53 instructions per cycle and scheduler, 950 a tile of
 // 32 rows (K 180, V 190, softmax 110, the rest waits, addresses and loops of nine warps), the
 // tensor pipe 13% busy; with two of the products' 16 instructions left it is 17% faster, without
-// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB) 169 us, 2.7 TB/s with the work list and the merge.
-//
+// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB): 168 us, 2.5 TB/s.
+
 #include "kv4_attn.cuh"
 
 namespace dspark {
@@ -172,7 +172,7 @@ __device__ __forceinline__ void take_over() { asm volatile("barrier.cta.sync 2, 
 struct Copier {
   const Params& p;
   const AttnItem* s_items;
-  int it_begin, it_end;
+  OwnItems own;
   int it, t, te, r, ctx, kvh;  // the next tile to copy (te: end of the item's cache tiles)
   int window;                  // first tile of the window, -1: none yet
   int block;                   // this lane's block, by its index among all blocks of the cache; -1: none
@@ -187,18 +187,18 @@ struct Copier {
   }
   // The first item from `at` on that has cache tiles, and the pages of its first window.
   __device__ __forceinline__ void start(int lane, int at) {
-    for (it = at; it < it_end; ++it) {
-      const AttnItem x = fetch_item(s_items, p.items, it, it_begin);
+    for (it = at; it < own.n; ++it) {
+      const AttnItem x = fetch_item(s_items, own.more, it);
       t = x.tb; r = x.r; ctx = x.ctx; kvh = x.kvh;
       te = min(x.te, ceil_div(ctx, kKT));
       if (t < te) break;
     }
     window = -1;
-    if (it < it_end) look(lane, t);
+    if (it < own.n) look(lane, t);
   }
   // The next tile into its stage.
   __device__ __forceinline__ void copy(int lane, uint32_t ring, uint32_t full) {
-    if (it >= it_end) return;
+    if (it >= own.n) return;
     if (window < 0 || t == window + 4) {
       window = t;
       block = -1;
@@ -241,19 +241,13 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
     mbar_init(pv_done, 1);
     fence_mbar_init();
   }
-  pdl_release();
-  pdl_wait();  // the work list and the step's inputs come from earlier kernels
-  const int it_begin = prm.item_begin[blockIdx.x];
-  const int it_end = prm.item_begin[blockIdx.x + 1];
-  if (it_begin >= it_end) return;
+  pdl_wait();  // the step's inputs come from earlier kernels (no early release, as there)
+  static_assert(sizeof(ItemScratch) <= sizeof(S.ring), "the scratch lies in the ring");
+  const OwnItems own = own_items<kThreads>(prm, *reinterpret_cast<ItemScratch*>(S.ring), S.items);
+  if (own.n == 0) return;
   if (w == 0) {
     tmem_alloc(smem_addr(&S.tmem), kTmemCols);
     tmem_relinquish();
-  }
-  {
-    constexpr int kWords = (int)(sizeof(AttnItem) / sizeof(uint4));
-    for (int i = threadIdx.x; i < min(kSmemItems, it_end - it_begin) * kWords; i += kThreads)
-      reinterpret_cast<uint4*>(S.items)[i] = reinterpret_cast<const uint4*>(prm.items + it_begin)[i];
   }
   tc_fence_before();
   __syncthreads();
@@ -265,14 +259,14 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
   uint32_t magic;  // 1024 twice; opaque, so that it stays in a register
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
   if (w == 8) {
-    Copier cp{prm, S.items, it_begin, it_end};
+    Copier cp{prm, S.items, own};
     cp.stage = 0;
-    cp.start(lane, it_begin);
+    cp.start(lane, 0);
     for (int i = 0; i < kStages; ++i) cp.copy(lane, ring, full);
     const uint64_t q_desc = smem_desc(smem_addr(S.q), 16, 1024, SW_128B);
     const uint64_t p_desc = smem_desc(smem_addr(S.p), WideSmem<N>::kPBlock, 512, SW_64B);
-    for (int it = it_begin; it < it_end; ++it) {
-      const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
+    for (int it = 0; it < own.n; ++it) {
+      const AttnItem item = fetch_item(S.items, own.more, it);
       const int ct = ceil_div(item.ctx, kKT), n_mma = (item.ni * G + 15) & ~15;
       const uint32_t qk_idesc = idesc_f16_f32(kKT, n_mma, 0), pv_idesc = idesc_f16_f32(kD, n_mma, 1);
       for (int t = item.tb - 1; t < item.te; ++t) {
@@ -329,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
     };
     load_q(S.items[0]);
 
-    for (int it = it_begin; it < it_end; ++it) {
-      const AttnItem item = fetch_item(S.items, prm.items, it, it_begin);
+    for (int it = 0; it < own.n; ++it) {
+      const AttnItem item = fetch_item(S.items, own.more, it);
       const int ctx = item.ctx, ct = ceil_div(ctx, kKT);
       const int nq = item.ni * G;              // rows of the tile
       const long long row0 = (long long)item.c0 + item.i0;
@@ -606,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
         }
       }
 
-      if (it + 1 < it_end) load_q(fetch_item(S.items, prm.items, it + 1, it_begin));
+      if (it + 1 < own.n) load_q(fetch_item(S.items, own.more, it + 1));
       // ---- epilogue: row sums over the half's warps, O^T / l; thread = channel
 #pragma unroll
       for (int q = 0; q < NH / 8; ++q) {

@@ -269,6 +269,49 @@ def test_nan_query_stays_in_its_row(pkg, hint):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hint", [1, 20])
+def test_many_short_requests(pkg, hint):
+    """The largest batch, empty requests among it: more items to a CTA than it keeps at hand."""
+    B = 1024
+    c = _case([(7 * i) % 25 for i in range(B)], [(5 * i) % 3 for i in range(B)], 16, 16, 16, seed=11)
+    call, out, lse = _run(pkg, c, hint)
+    call()
+    torch.cuda.synchronize()
+    assert pkg.read_device_error() == 0
+    _check(c, out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hint", [1, 20])
+def test_more_than_2_to_20_tiles(pkg, hint):
+    """Contexts of 2^21 tokens whose page tables repeat two pages: every key counts 4096 times."""
+    B, H, R = 8, 8, 4096
+    c = _case([512], [1], H, H, 256, seed=12)
+    short, one = c["table"], {k: c[k] for k in ("q", "k_new", "v_new")}
+    for k in one:
+        c[k] = one[k].repeat(B, 1, 1)
+    c.update(table=short.repeat(B, R), ctx=torch.full((B,), 512 * R, dtype=torch.int32),
+             cu=torch.arange(B + 1, dtype=torch.int32), M=B)
+    call, out, lse = _run(pkg, c, hint, 32)
+    call()
+    torch.cuda.synchronize()
+    assert pkg.read_device_error() == 0
+    K, V = O.kv4_values(c["cache"].numpy(), c["gk"], c["gv"])
+    for h in range(H):
+        pages = short[0].numpy()
+        k = np.concatenate([K[pages, :, h].reshape(-1, 128), one["k_new"][:, h].double().numpy()])
+        v = np.concatenate([V[pages, :, h].reshape(-1, 128), one["v_new"][:, h].double().numpy()])
+        x = c["scale"] * k @ one["q"][0, h].double().numpy()
+        w = np.exp(x - x.max()) * np.where(np.arange(513) < 512, R, 1)
+        o = w @ v / w.sum()
+        # sums over 2^21 keys in fp32: a CTA's part holds at most ceil(2^20 / 304) tiles, 2^18.8 keys,
+        # of which a thread adds one per tile (2^11.8) and the products eight steps (2^14.8)
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -9 + 2.0 ** 14.8 * 2.0 ** -23) * np.abs(v).max()
+        assert (np.abs(out[:, h].double().cpu().numpy() - o) <= tol).all()
+        assert (np.abs(lse[:, h].double().cpu().numpy() - x.max() - np.log(w.sum())) <= 2.0 ** -10).all()
+
+
+@pytest.mark.gpu
 @BOTH
 def test_long_context_is_split(pkg, hint):
     c = _case([20011], [2], 8, 2, 64, seed=7)

@@ -57,10 +57,12 @@ struct WideSmem {
   __align__(16) float alpha[8][kHalf];   // factors, per warp
   float red[8][kHalf];                   // maxima of a tile, row sums of an item, per warp
   __align__(16) AttnItem items[kSmemItems];
-  __align__(8) uint64_t full[kStages], qk_done, pv_done;
+  __align__(8) uint64_t full[kStages], qk_done, pv_half, pv_done;
   uint32_t tmem;
 };
-constexpr int kTmemCols = 256;         // S^T and O^T N each, K and V 64 each
+constexpr int kTmemCols = 256;         // S^T and O^T N each, K 64, the rest V's
+// V's operand lies in halves of 64 keys (32 columns) that go round as many places as there are.
+constexpr int v_places(int N) { return (kTmemCols - 2 * N - 64) / 32; }
 
 __device__ __forceinline__ uint32_t sw128_off(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
@@ -230,14 +232,16 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
   const uint32_t raw = smem_addr(smem_raw);
   WideSmem<N>& S = *reinterpret_cast<WideSmem<N>*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   constexpr int NH = N / 2;
-  constexpr int kTmemO = 0, kTmemS = N, kTmemK = 2 * N, kTmemV = 2 * N + 64;
-  static_assert(kTmemV + 64 <= kTmemCols, "tensor memory");
+  constexpr int kTmemO = 0, kTmemS = N, kTmemK = 2 * N, kTmemV = 2 * N + 64, kPlaces = v_places(N);
+  static_assert(kPlaces >= 2, "tensor memory");
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = w & 3, half = w >> 2;
   const uint32_t ring = smem_addr(S.ring), full = smem_addr(S.full);
-  const uint32_t qk_done = smem_addr(&S.qk_done), pv_done = smem_addr(&S.pv_done);
+  const uint32_t qk_done = smem_addr(&S.qk_done);
+  const uint32_t pv_half = smem_addr(&S.pv_half), pv_done = smem_addr(&S.pv_done);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1);
     mbar_init(qk_done, 1);
+    mbar_init(pv_half, 1);
     mbar_init(pv_done, 1);
     fence_mbar_init();
   }
@@ -264,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
     cp.start(lane, 0);
     for (int i = 0; i < kStages; ++i) cp.copy(lane, ring, full);
     const uint64_t q_desc = smem_desc(smem_addr(S.q), 16, 1024, SW_128B);
+    int place = 0;  // of V's next half
     const uint64_t p_desc = smem_desc(smem_addr(S.p), WideSmem<N>::kPBlock, 512, SW_64B);
     for (int it = 0; it < own.n; ++it) {
       const AttnItem item = fetch_item(S.items, own.more, it);
@@ -286,14 +291,21 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
             // of a block tile only the 16-row steps that hold a row
             const int nch = cached ? kKT / 16 : ceil_div(min(item.n_r - (t - ct) * kKT, kKT), 16);
             const uint32_t acc = t > item.tb ? 1u : 0u;
+            const uint32_t v0 = tmem + kTmemV + place * 32;
+            const uint32_t v1 = tmem + kTmemV + (place + 1 == kPlaces ? 0 : place + 1) * 32;
 #pragma unroll
-            for (int kk = 0; kk < kKT / 16; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               if (kk < nch)
-                umma_bf16_ts(tmem + kTmemO, tmem + kTmemV + kk * 8, p_desc + kk * 64, pv_idesc, kk > 0 ? 1u : acc);
+                umma_bf16_ts(tmem + kTmemO, v0 + kk * 8, p_desc + kk * 64, pv_idesc, kk > 0 ? 1u : acc);
+            umma_commit(pv_half);
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              if (kk < nch) umma_bf16_ts(tmem + kTmemO, v1 + (kk - 4) * 8, p_desc + kk * 64, pv_idesc, 1u);
             umma_commit(pv_done);
           }
         }
         __syncwarp();
+        if (t >= item.tb) place = (place + 2) % kPlaces;
         if (t >= item.tb && cached) cp.copy(lane, ring, full);  // the stage has been read by all
       }
     }
@@ -303,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
     float* const alpha = S.alpha[w];
     int stage = 0;                 // of the next cache tile, for V
     int k_stage = 0, k_parity = 0;  // and for K, a tile ahead
-    int g = 0;                  // tiles
+    int g = 0;                      // tiles
+    int place = 0;                  // of V's next half
 
     // ---- Q: tile row n = (block row n / G, head kvh G + n % G), a half-warp holds a row, 8 dims per
     // lane; read at the end of the item before
@@ -438,8 +451,17 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
             st_shared_v2(at + 16, hmul2_bits(s0, kBiasLow), hmul2_bits(s1, kBiasHigh));
             __syncwarp();
           }
-          if (g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // V's columns and P are free
-          tc_fence_after();
+          // The places of the next two halves.  The products of the tile before last are done (this
+          // thread waited for them when it wrote P), so with four places both are free, with three
+          // the second half waits for the first half's products of the tile before, with two either
+          // half for its own.
+          auto place_free = [&](int u) {
+            if (g > 0 && kPlaces - u < 3) wait_bar(kPlaces == 2 && u == 1 ? pv_done : pv_half, (g - 1) & 1, prm.err);
+            tc_fence_after();
+          };
+          const uint32_t v_at[2] = {t_lane + kTmemV + place * 32,
+                                    t_lane + kTmemV + (place + 1 == kPlaces ? 0 : place + 1) * 32};
+          place = (place + 2) % kPlaces;
           // ---- V into the operand columns
           if (cached) {
             uint2 v[4];
@@ -449,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
             for (int uh = 0; uh < 4; ++uh) {
               const int h = uh & 1;
               if (h == 0) {
+                place_free(uh >> 1);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = ld_shared_v2(src + (uh >> 1) * kBlockStride + j * 64);
               }
@@ -460,13 +483,15 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
                 expand(h ? v[2 * f].y : v[2 * f].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, lo);
                 expand(h ? v[2 * f + 1].y : v[2 * f + 1].x, magic, s.x, c.x, s.y, c.y, s.z, c.z, s.w, c.w, hi);
                 const uint32_t o[8] = {lo[0], lo[1], hi[0], hi[1], lo[2], lo[3], hi[2], hi[3]};
-                tmem_st_16x256b_x2(t_lane + (static_cast<uint32_t>(f * 16) << 16) + kTmemV + uh * 16, o);
+                tmem_st_16x256b_x2(v_at[uh >> 1] + (static_cast<uint32_t>(f * 16) << 16) + h * 16, o);
               }
             }
           } else {
             const long long step = (long long)prm.Hkv * kD;
             const __nv_bfloat16* vn =
                 prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD + kl;
+            place_free(0);
+            place_free(1);
 #pragma unroll 1
             for (int i = 0; 32 * i < vis; ++i) {
               uint32_t o[16];
@@ -480,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
                 if (k + 1 >= vis) y = 0.f;
                 o[j] = pack16(x, y);
               }
-              tmem_st16u(t_lane + kTmemV + i * 16, o);
+              tmem_st16u((i < 2 ? v_at[0] : v_at[1]) + (i & 1) * 16, o);
             }
           }
         } else if (t + 1 < item.te) {
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
           expand_k(t + 1);
         }
         wait_bar(qk_done, g & 1, prm.err);
-        if (half == 0 && g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // P is free
+        if (g > 0) wait_bar(pv_done, (g - 1) & 1, prm.err);  // P is free
         tc_fence_after();
         // ---- softmax of rows half NH .. + NH - 1: row n sees this key iff n >= nmin
         const bool masked = !cached || vis < kKT;

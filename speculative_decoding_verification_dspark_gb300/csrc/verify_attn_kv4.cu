@@ -24,11 +24,11 @@
 // takes 2.05 cycles of an SM (measured) and other instructions hardly issue beside it, so
 // each 8 rows more add 260 cycles to a tile for which HBM needs 850.  Measured, this kernel
 // against the wide one: 256 decodes of 5 heads 181 : 293 us, 64 x 3 and 4 rows of 4 heads at
-// 2048 tokens 64 : 77; with tiles of 24 rows 71 : 63 (32 short windows) and 32 rows 194 : 169
+// 2048 tokens 58 : 73; with tiles of 24 rows 71 : 62 (32 short windows) and 32 rows 194 : 155
 // (131k contexts).
 //
 // Bound by instruction issue (0.63 per cycle and scheduler, which 18 warps per SM cannot
-// raise): 256 decodes read 646 MB in 168 us, 3.8 TB/s.  The copies alone (same blocks, same
+// raise): 256 decodes read 646 MB in 169 us, 3.8 TB/s.  The copies alone (same blocks, same
 // ring) take 96 us.
 //
 #include "kv4_attn.cuh"
@@ -663,8 +663,8 @@ Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
   const int G = Hq / Hkv;
   const long long rows = (long long)G * (max_block_rows > 0 ? max_block_rows : 1);
   p.parts = 1;
-  // (64 requests of 16 rows of 4 heads: one tile of 64 rows 114 us, two of 32 150; 12 rows: one of
-  // 48 97 us, two of 24 146)
+  // (64 requests of 16 rows of 4 heads: one tile of 64 rows 117 us, two of 32 141; 12 rows: one of
+  // 48 94 us, two of 24 137)
   p.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.rows_per_tile = p.nt / G;
   p.nk = kKT;

@@ -16,18 +16,20 @@
 //
 // Why so.  Measured with time stamps of the warps: a thread that issues the eight
 // instructions of a product is held for 700 to 1700 cycles (they queue behind the other CTA's), so
-// no warp that computes may issue; with it, and K's and V's operands in columns of their own
-// so that neither waits for the other's product, a tile of 32 rows takes 3500 cycles per CTA
-// (two share an SM), 5800 before.  S^T(t + 1) goes first: K's expansion waits for it and is on
-// the longer path (170 us against 175).  Warps of six different loops (K, V, two softmax
-// streams, issuers) needed 2.2 us a tile; teams of four warps that do everything in turn, four to
-// an SM, take 32 rows as fast but hold no more (whole blocks of 17 rows 216 us against 170).  More
-// rows than 64 do not fit: N columns of S^T, N of O^T, 64 of K, 64 of V in half of the 512.
+// no warp that computes may issue; with it, K's and V's operands in columns of their own, and V's
+// in halves that go round, so that an expansion hardly waits for a product, a tile of 32 rows
+// takes 3200 cycles per CTA (two share an SM), 5800 before (131k contexts 194 us -> 155).
+// S^T(t + 1) goes first: K's expansion waits for it and is on the longer path (170 us against
+// 175).  Half of K's expansion given to V's warps: 160.  Warps of six different loops (K, V, two
+// softmax streams, issuers) needed 2.2 us a tile; teams of four warps that do everything in
+// turn, four to an SM, 170 us and no more than 32 rows.  More rows than 64 do not fit: N columns
+// of S^T, N of O^T, 64 of K and 64 or more of V in half of the 512.  A ring of two tiles is a
+// third slower, one of four no faster.
 //
 // Bound by the chain of a tile's steps: 0.53 instructions per cycle and scheduler, 950 a tile of
 // 32 rows (K 180, V 190, softmax 110, the rest waits, addresses and loops of nine warps), the
 // tensor pipe 13% busy; with two of the products' 16 instructions left it is 17% faster, without
-// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB): 168 us, 2.5 TB/s.
+// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB): 155 us, 2.8 TB/s.
 
 #include "kv4_attn.cuh"
 

@@ -562,7 +562,8 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * 16 k_scale / 16 v_scale (saturating: |k_new| < 10^6 k_scale), the probabilities to
  * fp16; sums are fp32, and out is rounded once to bf16.
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
- * undefined.
+ * undefined.  A negative length (cu_seqlens falling, ctx_len below 0) sets it too, and
+ * nothing is written; so with cu_seqlens[B] > max_rows and DSPARK_DEVERR_ROWS_OVERFLOW.
  * Two kernels; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,

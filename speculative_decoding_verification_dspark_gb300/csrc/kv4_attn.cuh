@@ -9,7 +9,7 @@
 //
 // Queries become fp16 scaled by a power of two per row (largest element in [2^14, 2^15)),
 // undone in the row's softmax scale: exact but for elements below 2^-30 of the largest.
-// Probabilities are rounded to fp16 (2^-11, a quarter of the output's own rounding in
+// Probabilities are rounded to fp16 (2^-11, an eighth of the output's own rounding in
 // bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
 // down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
 //
@@ -173,9 +173,11 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
   const int per = (B + THREADS - 1) / THREADS, r_begin = tid * per, r_end = min(B, r_begin + per);
   long long units = 0;
   int groups = 0, tmax = 0;
+  bool bad = false;  // a length below zero (or contexts at int's end): no shares can be made of it
   for (int r = r_begin; r < r_end; ++r) {
-    const int n = p.cu_seqlens[r + 1] - p.cu_seqlens[r];
-    const int t = ceil_div(p.ctx_len[r], kKT) + ceil_div(n, kKT), ng = ceil_div(n, rpt) * p.Hkv;
+    const int n = p.cu_seqlens[r + 1] - p.cu_seqlens[r], ctx = p.ctx_len[r];
+    bad |= n < 0 || ctx < 0 || ctx > 0x7fffff00;
+    const int t = ceil_div(ctx, kKT) + ceil_div(n, kKT), ng = ceil_div(n, rpt) * p.Hkv;
     S.tt[r] = t;
     S.goff[r] = ng;
     units += (long long)t * ng;
@@ -199,7 +201,7 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
     S.w_groups[wid] = g_incl;
     S.w_tmax[wid] = tmax;
   }
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   long long U = 0, u0 = u_incl - units;
   int g0 = g_incl - groups;
 #pragma unroll
@@ -229,8 +231,9 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
     return small ? (unsigned)cc * (unsigned)U / (unsigned)n_cta : (long long)cc * U / n_cta;
   };
   OwnItems own{0, nullptr};
-  const bool active = rows_ok && U > 0 && c < n_cta;
-  if (!rows_ok && c == 0 && tid == 0) raise_error(p.err, DSPARK_DEVERR_ROWS_OVERFLOW);
+  const bool active = rows_ok && !bad && U > 0 && c < n_cta;
+  if (c == 0 && tid == 0 && !rows_ok) raise_error(p.err, DSPARK_DEVERR_ROWS_OVERFLOW);
+  if (c == 0 && tid == 0 && bad) raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
   SplitGroup record{};
   if (active) {
     const long long lo = first_unit(c), hi = first_unit(c + 1);
@@ -282,7 +285,7 @@ __device__ __forceinline__ AttnItem fetch_item(const AttnItem* s_items, const At
   return it < kSmemItems ? s_items[it] : more[it];
 }
 
-// The wide kernel (verify_attn_kv4_wide.cu): tiles of up to 32, 48 or 80 rows.
+// The wide kernel (verify_attn_kv4_wide.cu): tiles of up to 32, 48 or 64 rows.
 constexpr int kWideCtasPerSm = 2;
 int launch_wide(const Params& p, int rows, int ncta, cudaStream_t stream);
 

@@ -347,6 +347,19 @@ def test_bad_page_and_row_overflow(pkg, hint):
 
 
 @pytest.mark.gpu
+@BOTH
+def test_negative_lengths_are_refused(pkg, hint):
+    for key, value in (("cu", [0, 4, 3, 5]), ("cu", [2, 0, 3, 5]), ("ctx", [20, -1, 30]),
+                       ("ctx", [20, 2 ** 31 - 1, 30])):
+        c = _case([20, 40, 30], [1, 2, 2], 4, 2, 16, seed=13)
+        c[key] = torch.tensor(value, dtype=torch.int32)
+        call, out, lse = _run(pkg, c, hint)
+        call()
+        assert pkg.read_device_error() == 0x10
+        assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
+
+
+@pytest.mark.gpu
 def test_graph_streams_and_repeatability(pkg):
     c = _case([900, 300, 2100], [5, 9, 1], 32, 8, 16, seed=9)
     call, out, lse = _run(pkg, c)

@@ -40,8 +40,8 @@ constexpr int kTasks = 6;      // warps of a CTA, and tasks of a block
 constexpr int kThreads = 32 * kTasks;
 constexpr int kWindow = 16;    // packed rows whose leaders one CTA serves, at most
 
-// The largest r < B with cu[r] <= row (cu ascending, cu[0] <= row): a warp narrows the
-// range by 32 per round.
+// The largest r < B with cu[r] <= row, 0 if there is none (cu ascending): a warp narrows
+// the range by 32 per round.
 __device__ __forceinline__ int find_request(const int32_t* __restrict__ cu, int B, int row) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;  // the answer is in [lo, lo + n)
@@ -71,7 +71,8 @@ struct Leaders {
   unsigned mask;     // lanes whose row is a leader
 };
 
-// keep: rows 0 .. keep[r] of a segment take part (nullable: all).
+// keep: rows 0 .. keep[r] of a segment take part (nullable: all).  Rows before cu[0] are no
+// request's (i < 0: find_request gives them to request 0).
 __device__ __forceinline__ Leaders find_leaders(const Kv4Params& p, int row0, int M) {
   const int lane = threadIdx.x & 31, row = row0 + lane;
   Leaders a{0, 0, 0, -1, 0};
@@ -89,7 +90,7 @@ __device__ __forceinline__ Leaders find_leaders(const Kv4Params& p, int row0, in
     a.r = r;
     a.pos = p.pos0[r] + i;
     const int t0 = a.pos & (kBlock - 1);
-    leader = i < n && (i == 0 || t0 == 0);
+    leader = i >= 0 && i < n && (i == 0 || t0 == 0);
     if (leader) {
       a.cnt = min(kBlock - t0, n - i);
       const int slot = a.pos >> p.log2_page;

@@ -364,9 +364,9 @@ int dspark_block_accept_estimate(const void* p_target, const void* p_draft, int 
  *   committed   int32 [B, gamma+1] out; n_committed int32 [B] out
  * If the free stack or a page-table row is too short the device sets
  * DSPARK_DEVERR_NO_FREE_PAGE / _PAGE_ROW_FULL, if cu_seqlens[B] > max_rows it sets
- * DSPARK_DEVERR_ROWS_OVERFLOW, and if accept_len[r] is outside 0..gamma or keeps
- * more rows than request r's packed segment holds it sets DSPARK_DEVERR_BAD_INPUT;
- * in each of these cases it changes nothing.
+ * DSPARK_DEVERR_ROWS_OVERFLOW, and if cu_seqlens[0] < 0 or accept_len[r] is outside
+ * 0..gamma or keeps more rows than request r's packed segment holds it sets
+ * DSPARK_DEVERR_BAD_INPUT; in each of these cases it changes nothing.
  * ------------------------------------------------------------------------- */
 size_t dspark_compact_workspace_size(int B);
 int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
@@ -529,9 +529,11 @@ int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
  * k, v [max_rows, Hkv, 128] (dense, fp32 or bf16 per dtype); rows >= cu_seqlens[B]
  * are left as they are.
  *
- * Both: a position whose page-table slot or page is out of range sets
- * DSPARK_DEVERR_BAD_INPUT and is skipped with the rest of its block; cu_seqlens[B] >
- * max_rows sets DSPARK_DEVERR_ROWS_OVERFLOW and nothing is done.  One kernel each.
+ * Both: cu_seqlens must not fall; it may begin past row 0 (rows before cu_seqlens[0] are
+ * no request's).  A position whose page-table slot or page is out of range sets
+ * DSPARK_DEVERR_BAD_INPUT and is skipped with the rest of its block; cu_seqlens[0] < 0
+ * sets it too, cu_seqlens[B] > max_rows sets DSPARK_DEVERR_ROWS_OVERFLOW, and nothing is
+ * done.  One kernel each.
  * ------------------------------------------------------------------------- */
 #define DSPARK_KV4_BLOCK_BYTES 2176
 
@@ -562,8 +564,9 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * 16 k_scale / 16 v_scale (saturating: |k_new| < 10^6 k_scale), the probabilities to
  * fp16; sums are fp32, and out is rounded once to bf16.
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
- * undefined.  A negative length (cu_seqlens falling, ctx_len below 0) sets it too, and
- * nothing is written; so with cu_seqlens[B] > max_rows and DSPARK_DEVERR_ROWS_OVERFLOW.
+ * undefined.  A negative length or first row (cu_seqlens falling or below 0, ctx_len below
+ * 0) sets it too, and nothing is written; so with cu_seqlens[B] > max_rows and
+ * DSPARK_DEVERR_ROWS_OVERFLOW.
  * Two kernels; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,

@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(1024)
   const int tid = threadIdx.x;
   if (tid == 0) {
     cws->ok = 0;
-    s_flags = cu[B] > max_rows ? DSPARK_DEVERR_ROWS_OVERFLOW : 0;
+    s_flags = (cu[B] > max_rows ? DSPARK_DEVERR_ROWS_OVERFLOW : 0) |
+              (cu[0] < 0 ? DSPARK_DEVERR_BAD_INPUT : 0);
     s_top = *free_top;
   }
   __syncthreads();

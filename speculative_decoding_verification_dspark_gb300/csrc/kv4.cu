@@ -64,6 +64,14 @@ struct Kv4Params {
   float gk, gv;
 };
 
+// Whether the packed rows cu[0] .. M - 1 lie in the buffers.
+__device__ __forceinline__ bool rows_ok(const Kv4Params& p, int M) {
+  const unsigned bits = (M > p.max_rows ? DSPARK_DEVERR_ROWS_OVERFLOW : 0u) |
+                        (p.cu[0] < 0 ? DSPARK_DEVERR_BAD_INPUT : 0u);
+  if (bits && blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, bits);
+  return bits == 0;
+}
+
 // The leaders of a window of packed rows: lane j < 16 holds row row0 + j.
 struct Leaders {
   int r, pos, cnt;   // request, cache position and rows in the block (lanes of `mask`)
@@ -436,10 +444,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 5)
   __shared__ float4 s_step[kTasks][2][kBlock];
   if (p.ok && !*p.ok) return;
   const int M = p.cu[p.B];
-  if (M > p.max_rows) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, DSPARK_DEVERR_ROWS_OVERFLOW);
-    return;
-  }
+  if (!rows_ok(p, M)) return;
   const int groups = ceil_div(p.Hkv, p.heads_per_cta);
   const int h0 = blockIdx.x % groups * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.Hkv);
   const int row0 = blockIdx.x / groups * p.rows_per_cta;
@@ -469,10 +474,7 @@ __global__ void __launch_bounds__(kThreads)
                     T* __restrict__ v) {
   pdl_wait();  // inputs come from the kernels before this one
   const int M = p.cu[p.B];
-  if (M > p.max_rows) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, DSPARK_DEVERR_ROWS_OVERFLOW);
-    return;
-  }
+  if (!rows_ok(p, M)) return;
   const int groups = ceil_div(p.Hkv, p.heads_per_cta);
   const int h0 = blockIdx.x % groups * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.Hkv);
   const int row0 = blockIdx.x / groups * p.rows_per_cta;

@@ -173,10 +173,11 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
   const int per = (B + THREADS - 1) / THREADS, r_begin = tid * per, r_end = min(B, r_begin + per);
   long long units = 0;
   int groups = 0, tmax = 0;
-  bool bad = false;  // a length below zero (or contexts at int's end): no shares can be made of it
+  // a length or a first row below zero (or contexts at int's end): no shares can be made of it
+  bool bad = false;
   for (int r = r_begin; r < r_end; ++r) {
-    const int n = p.cu_seqlens[r + 1] - p.cu_seqlens[r], ctx = p.ctx_len[r];
-    bad |= n < 0 || ctx < 0 || ctx > 0x7fffff00;
+    const int c0 = p.cu_seqlens[r], n = p.cu_seqlens[r + 1] - c0, ctx = p.ctx_len[r];
+    bad |= c0 < 0 || n < 0 || ctx < 0 || ctx > 0x7fffff00;
     const int t = ceil_div(ctx, kKT) + ceil_div(n, kKT), ng = ceil_div(n, rpt) * p.Hkv;
     S.tt[r] = t;
     S.goff[r] = ng;

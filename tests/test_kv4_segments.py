@@ -1,11 +1,12 @@
 """The 4-bit cache's calls on a part of a larger batch: cu_seqlens that begins past row 0 (a
-slice cu[3:] of a batch's), against the oracle, bit for bit."""
+slice cu[3:] of a batch's), against the oracle, bit for bit, and refused where it begins before."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import dspark_oracle as O
 from tests.test_kv4_cache import pkg  # noqa: F401
+from tests.test_verify_attn_kv4 import BOTH, _case, _reference, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,66 @@ def test_compact_of_a_part(pkg):  # noqa: F811
     want = O.kv4_store(k.float().numpy(), v.float().numpy(), cu.numpy(), ctx.numpy(), table.numpy(),
                        cache.numpy(), 0.25, 0.5, n_keep=[a + 1 for a in acc])
     assert np.array_equal(dev.cpu().numpy(), want)
+
+
+@BOTH
+def test_attention_of_a_part(pkg, hint):  # noqa: F811
+    c = _case([200, 40, 300, 129], [5, 2, 4, 9], 8, 2, 16, seed=31)
+    o, lse, to, tl = _reference(c)
+    for k in ("cu", "ctx", "table"):
+        c[k] = c[k][2:]
+    call, out, l = _run(pkg, c, hint)
+    call()
+    torch.cuda.synchronize()
+    assert pkg.read_device_error() == 0
+    assert np.all((np.abs(out.double().cpu().numpy() - o) <= to)[7:])
+    assert np.all((np.abs(l.double().cpu().numpy() - lse) <= tl)[7:])
+    assert bool((out[:7] == 5.0).all()) and bool((l[:7] == 5.0).all())
+
+
+@BOTH
+def test_attention_refuses_a_first_row_below_zero(pkg, hint):  # noqa: F811
+    c = _case([20, 40, 30], [1, 2, 2], 4, 2, 16, seed=32)
+    for first in (-1, -300):
+        c["cu"] = torch.tensor([first, 1, 3, 5], dtype=torch.int32)
+        call, out, lse = _run(pkg, c, hint)
+        call()
+        assert pkg.read_device_error() == 0x10
+        assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
+
+
+@pytest.mark.parametrize("first", [-1, -300])
+@pytest.mark.parametrize("last", [9, 5000])   # a row per CTA, and 16
+def test_store_and_load_refuse_a_first_row_below_zero(pkg, first, last):  # noqa: F811
+    k, v, cu, p0, table, cache = _batch([0, 3, last], [5, 20], 4, 16, 3)
+    cu[0] = first
+    dev = cache.cuda()
+    args = [t.cuda() for t in (cu, p0, table)]
+    pkg.kv4_store(k.cuda(), v.cuda(), *args, dev, 0.25, 0.5)
+    assert pkg.read_device_error() == 0x10 and torch.equal(dev.cpu(), cache)
+    ko, vo = (torch.full(k.shape, 9.0, device="cuda") for _ in range(2))
+    pkg.kv4_load(dev, *args, ko, vo, 0.25, 0.5)
+    assert pkg.read_device_error() == 0x10 and bool((ko == 9.0).all()) and bool((vo == 9.0).all())
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_compact_refuses_a_first_row_below_zero(pkg, kv4):  # noqa: F811
+    gamma, B, page = 4, 2, 16
+    k, v, cu, ctx, table, cache = _batch([0, 3, 6], [14, 20], 2, page, 4)
+    cu[0] = -1
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    kept = dict(table=table.cuda(), ctx=ctx.cuda(), anchor=z(B), top=z(1) + 5, com=z(B, gamma + 1),
+                ncom=z(B))
+    if kv4:
+        caches = [cache.cuda()]
+    else:
+        caches = [torch.ones(cache.shape[0], page, 2, 128, dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2)]
+    before = [t.clone() for t in (*kept.values(), *caches)]
+    ws = torch.empty(pkg.compact_workspace_size(B), dtype=torch.uint8, device="cuda")
+    free = torch.arange(5, dtype=torch.int32, device="cuda")
+    call, scales = (pkg.compact_kv4, (0.25, 0.5)) if kv4 else (pkg.compact, ())
+    call(k.cuda(), v.cuda(), cu.cuda(), z(B) + 1, z(B), z(B, gamma), kept["table"], kept["ctx"],
+         kept["anchor"], free, kept["top"], *caches, kept["com"], kept["ncom"], ws, *scales)
+    assert pkg.read_device_error() == 0x10
+    assert all(torch.equal(a, b) for a, b in zip(before, (*kept.values(), *caches)))

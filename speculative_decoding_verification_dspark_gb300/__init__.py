@@ -780,9 +780,12 @@ class VerifyStep:
         on the device).  ``tier_host``: optional pinned host int32 word receiving each
         step's tier; ``body_log``: optional device int32 [1 + n] recording the body
         index each launch ran (element 0 counts launches; the caller zeroes it).
-        The graph takes the bf16 cache only."""
+        The graph takes the bf16 cache only, and q, k_new and v_new as they are: it has
+        no norm_rope, so an ``inp`` with projections (``q_in``) is refused."""
         if self.kv4:
             raise ValueError("the step graph does not take the 4-bit cache")
+        if "q_in" in inp:
+            raise ValueError("the step graph does not run norm_rope: pass inputs without q_in")
         pdt = inp["p_target"].dtype
         tiers = inp["tiers"]
         tiers_dev = tiers.to(self.windows.device, torch.int32)

@@ -38,6 +38,9 @@ using namespace dspark::kv4;
 
 constexpr int kKT = 128;               // keys of a tile
 constexpr int kSmemItems = 16;         // work items of a CTA kept in shared memory
+// Largest context and segment together.  Each fills tiles of its own, and the lanes of a copying
+// warp form positions up to 31 blocks past the start of the last tile, 622 past this end at most.
+constexpr long long kMaxEnd = 0x7fffffffll - 6 * kKT;
 constexpr int kMaxCtas = 1024;         // (own_items: products of a unit and a CTA in 32 bits)
 constexpr float kRefDrop = 6.f;        // reference = maximum - 6 (log2)
 constexpr float kMove = 14.f;          // a key above reference + 14 moves it
@@ -173,11 +176,12 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
   const int per = (B + THREADS - 1) / THREADS, r_begin = tid * per, r_end = min(B, r_begin + per);
   long long units = 0;
   int groups = 0, tmax = 0;
-  // a length or a first row below zero (or contexts at int's end): no shares can be made of it
+  // a length or a first row below zero, or a segment whose end lies past kMaxEnd: no shares can be
+  // made of it
   bool bad = false;
   for (int r = r_begin; r < r_end; ++r) {
     const int c0 = p.cu_seqlens[r], n = p.cu_seqlens[r + 1] - c0, ctx = p.ctx_len[r];
-    bad |= c0 < 0 || n < 0 || ctx < 0 || ctx > 0x7fffff00;
+    bad |= c0 < 0 || n < 0 || ctx < 0 || (long long)ctx + n > kMaxEnd;
     const int t = ceil_div(ctx, kKT) + ceil_div(n, kKT), ng = ceil_div(n, rpt) * p.Hkv;
     S.tt[r] = t;
     S.goff[r] = ng;

@@ -142,3 +142,15 @@ def test_compact_refuses_a_first_row_below_zero(pkg, kv4):  # noqa: F811
          kept["anchor"], free, kept["top"], *caches, kept["com"], kept["ncom"], ws, *scales)
     assert pkg.read_device_error() == 0x10
     assert all(torch.equal(a, b) for a, b in zip(before, (*kept.values(), *caches)))
+
+
+@BOTH
+def test_attention_refuses_ends_past_32_bits(pkg, hint):  # noqa: F811
+    """Context and rows together: positions of the tiles behind them stay in 32 bits."""
+    for ctx, n in ((2 ** 31 - 769, 1), (2 ** 31 - 1000, 300), (2 ** 31 - 258, 300), (2 ** 31 - 2, 2)):
+        c = _case([20, 40], [1, n], 2, 1, 16, seed=33)
+        c["ctx"][1] = ctx
+        call, out, lse = _run(pkg, c, hint)
+        call()
+        assert pkg.read_device_error() == 0x10
+        assert bool((out == 5.0).all()) and bool((lse == 5.0).all())

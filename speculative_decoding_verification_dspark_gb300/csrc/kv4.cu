@@ -66,10 +66,11 @@ struct Kv4Params {
 
 // Whether the packed rows cu[0] .. M - 1 lie in the buffers.
 __device__ __forceinline__ bool rows_ok(const Kv4Params& p, int M) {
-  const unsigned bits = (M > p.max_rows ? DSPARK_DEVERR_ROWS_OVERFLOW : 0u) |
-                        (p.cu[0] < 0 ? DSPARK_DEVERR_BAD_INPUT : 0u);
-  if (bits && blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, bits);
-  return bits == 0;
+  const int first = p.cu[0];
+  if (M <= p.max_rows && first >= 0) return true;
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    raise_error(p.err, M > p.max_rows ? DSPARK_DEVERR_ROWS_OVERFLOW : DSPARK_DEVERR_BAD_INPUT);
+  return false;
 }
 
 // The leaders of a window of packed rows: lane j < 16 holds row row0 + j.

@@ -13,6 +13,8 @@
 // bf16); their reference sits 2^6 below the maximum it was taken from, so that fp16 reaches
 // down to 2^-30 of it.  Maxima, sums and accumulators are fp32.
 //
+// A NaN in v_new reaches the rows that see it and no others: see pack16_value.
+//
 // The softmax takes a tile in one pass against the row references of the tiles before; only if
 // some key lies 2^8 above its row's maximum then (always in an item's first tile) do the
 // references move and O and the sums with them.  Row sums stay in the threads (each sums its
@@ -132,6 +134,18 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t magic, uint32_t s0, 
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
   const __half2 top = __half2half2(__ushort_as_half(0x7bff));  // 65504
   return h2_bits(__hmax2_nan(__hmin2_nan(__floats2half2_rn(a, b), top), __hneg2(top)));
+}
+// The same for the values of block rows, every number finite: a NaN stands in the operand as a
+// number (the rows that do not see it weigh it 0, which times NaN is NaN) and is kept in `nan`, a
+// pair that has_nan tells; write_nans gives it to the rows that see it.
+__device__ __forceinline__ uint32_t pack16_value(float a, float b, uint32_t& nan) {
+  const __half2 top = __half2half2(__ushort_as_half(0x7bff));
+  const __half2 t = __hmin2_nan(__floats2half2_rn(a, b), top);
+  nan = h2_bits(__hmax2_nan(bits_h2(nan), t));
+  return h2_bits(__hmax2(t, __hneg2(top)));
+}
+__device__ __forceinline__ bool has_nan(uint32_t pair) {
+  return ((pair & 0x7fffu) > 0x7c00u) || ((pair & 0x7fff0000u) > 0x7c000000u);
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -288,6 +302,28 @@ __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, A
 
 __device__ __forceinline__ AttnItem fetch_item(const AttnItem* s_items, const AttnItem* more, int it) {
   return it < kSmemItems ? s_items[it] : more[it];
+}
+
+// After the outputs of rows n0 .. n1 - 1 of an item's tile, in channel ch: NaN for the rows that see
+// a NaN of that channel in the block rows of the item's tiles (row n sees block row b from
+// n = (b - i0) G on).  For the warp that wrote those outputs, where it met a NaN.
+__device__ __forceinline__ void write_nans(const Params& p, const AttnItem& x, int ch, int n0, int n1) {
+  const int G = p.Hq / p.Hkv, ct = ceil_div(x.ctx, kKT);
+  const long long step = (long long)p.Hkv * kD;
+  const __nv_bfloat16* v = p.v_new + ((long long)x.c0 * p.Hkv + x.kvh) * kD + ch;
+  int b = max(x.tb - ct, 0) * kKT;
+  const int end = min((x.te - ct) * kKT, x.n_r);
+#pragma unroll 1
+  while (b < end && !__hisnan(v[b * step])) ++b;
+  if (b >= end) return;
+#pragma unroll 1
+  for (int n = max((b - x.i0) * G, n0); n < n1; ++n) {
+    if (x.nsplit > 1)
+      p.ws_o[((long long)x.slot * p.slot_rows + n) * kD + ch] = __int_as_float(0x7fffffff);
+    else
+      p.out[(((long long)x.c0 + x.i0 + n / G) * p.Hq + x.kvh * G + n % G) * kD + ch] =
+          __ushort_as_bfloat16(0x7fff);
+  }
 }
 
 // The wide kernel (verify_attn_kv4_wide.cu): tiles of up to 32, 48 or 64 rows.

@@ -131,6 +131,7 @@ struct Smem {
   float ref[4][8 * NT];      // references, a copy per warp
   float red[4][8 * NT];      // maxima of a tile per warp
   float sum[4][8 * NT];      // row sums of an item per warp
+  int nan[4];                // a warp met a NaN among the item's values
   __align__(16) AttnItem items[kSmemItems];
   __align__(8) uint64_t full[kStages], empty[kStages];
 };
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
       ptx::mbar_init(empty + 8 * i, 4);
     }
     ptx::fence_mbar_init();
+    for (int i = 0; i < 4; ++i) S.nan[i] = 0;
   }
   static_assert(sizeof(ItemScratch) <= sizeof(S.ring), "the scratch lies in the ring");
   const OwnItems own = own_items<kThreads>(prm, *reinterpret_cast<ItemScratch*>(S.ring), S.items);
@@ -532,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
         const uint32_t* vn = reinterpret_cast<const uint32_t*>(
             prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD) + 16 * w + g;
         const long long step = (long long)prm.Hkv * kD / 2;
+        uint32_t nan = 0;
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
           if (64 * (n >> 1) + 8 * (n & 1) >= vis) continue;  // no key of it
@@ -544,12 +547,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
               uint32_t y = vn[min(k, vis - 1) * step + 8 * i], z = vn[min(k + 1, vis - 1) * step + 8 * i];
               if (k >= vis) y = 0;
               if (k + 1 >= vis) z = 0;
-              lo[i][p] = pack16(bf_lo(y) * prm.v_unit, bf_lo(z) * prm.v_unit);
-              hi[i][p] = pack16(bf_hi(y) * prm.v_unit, bf_hi(z) * prm.v_unit);
+              lo[i][p] = pack16_value(bf_lo(y) * prm.v_unit, bf_lo(z) * prm.v_unit, nan);
+              hi[i][p] = pack16_value(bf_hi(y) * prm.v_unit, bf_hi(z) * prm.v_unit, nan);
             }
           }
           pv(n >> 1, n & 1, lo, hi);
         }
+        if (has_nan(nan)) S.nan[w] = 1;
       }
       if (cached) {
         __syncwarp();
@@ -594,6 +598,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * NT)) verify_attn_kv4
           dst[8] = __floats2bfloat162_rn(o[1][j][e] * inv, o[1][j][2 + e] * inv);
         }
       }
+    __syncwarp();  // (behind the warp's outputs)
+    const int nan = S.nan[w];
+    __syncwarp();
+    if (nan) {
+      write_nans(prm, item, 32 * w + lane, 0, nq);
+      if (lane == 0) S.nan[w] = 0;
+    }
     // (the next item's barriers stand between these reads of shared memory and its writes: Q
     // and cf were last read before the team's last tile barrier, `sum` is written next after
     // two more)

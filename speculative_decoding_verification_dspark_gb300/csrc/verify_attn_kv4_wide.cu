@@ -58,6 +58,7 @@ struct WideSmem {
   __align__(16) float ref[8][kHalf];     // negative references, per warp
   __align__(16) float alpha[8][kHalf];   // factors, per warp
   float red[8][kHalf];                   // maxima of a tile, row sums of an item, per warp
+  int nan[4];                            // a NaN among the item's values, per warp of half 1
   __align__(16) AttnItem items[kSmemItems];
   __align__(8) uint64_t full[kStages], qk_done, pv_half, pv_done;
   uint32_t tmem;
@@ -433,6 +434,10 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
       tc_fence_before();
       hand_over();
       team_sync();  // cf
+      if (half == 1) {
+        if (lane == 0) S.nan[wq] = 0;   // (the epilogue before has been left by all)
+        __syncwarp();
+      }
 
 #pragma unroll 1
       for (int t = item.tb; t < item.te; ++t, ++g) {
@@ -492,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
             const long long step = (long long)prm.Hkv * kD;
             const __nv_bfloat16* vn =
                 prm.v_new + ((long long)(item.c0 + (t - ct) * kKT) * prm.Hkv + item.kvh) * kD + kl;
+            uint32_t nan = 0;
             place_free(0);
             place_free(1);
 #pragma unroll 1
@@ -505,10 +511,11 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
                 float y = __bfloat162float(vn[min(k + 1, vis - 1) * step]) * prm.v_unit;
                 if (k >= vis) x = 0.f;
                 if (k + 1 >= vis) y = 0.f;
-                o[j] = pack16(x, y);
+                o[j] = pack16_value(x, y, nan);
               }
               tmem_st16u((i < 2 ? v_at[0] : v_at[1]) + (i & 1) * 16, o);
             }
+            if (has_nan(nan)) S.nan[wq] = 1;
           }
         } else if (t + 1 < item.te) {
           wait_bar(qk_done, g & 1, prm.err);  // K's columns are free
@@ -681,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, kWideCtasPerSm) verify_attn_kv4_wide
           }
         }
       }
+      if (S.nan[wq]) write_nans(prm, item, kl, half * NH, half * NH + n_half);
       // (the next item's Q, cf and references are written behind this barrier's and the products'
       // last reads; `red` next after its first tile's barrier)
     }

@@ -511,7 +511,7 @@ int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
  * In every little-endian 32-bit word of codes, nibble p (p = 0..3) holds element 2p
  * and nibble p + 4 element 2p + 1 of eight consecutive ones (dims of a token for K,
  * tokens of a channel for V).  The value of an element is
- *     (code - 8) * scale * g,   g = k_scale or v_scale (fp32, > 0, one per tensor).
+ *     (code - 8) * scale * g,   g = k_scale or v_scale (fp32, 2^-100 to 2^100, one per tensor).
  * page_size is a power of two >= 16.  A page belongs to one request while it is
  * written (two requests may read a page, as with a shared prefix).
  *
@@ -553,6 +553,7 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * v_new are bf16 as there.  Arguments as dspark_verify_attn, with kv_cache, k_scale
  * and v_scale in place of the two caches, and
  *   out  bf16 [max_rows, Hq, 128]  out (rows >= M not written)
+ *   scale > 0, with scale * log2(e) * 16 k_scale a normal fp32 number
  *   Hq / Hkv <= 32; n_pages * Hkv * page_size / 16 < 2^31
  *   max_splits: as there, times the CTAs that share an SM (2 to 4)
  *   max_block_rows: a hint as there; the query tile holds 8, 16, 32, 48 or 64 rows of

@@ -477,7 +477,10 @@ int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
                              static_cast<cudaStream_t>(stream));
 }
 
-static bool positive(float x) { return x > 0.f && x <= 3.402823466e38f; }  // finite, no NaN
+// Factors of the 4-bit cache from which every derived one is a finite normal number: 7 g (steps),
+// 16 g, 1 / (16 g) (the attention's units) and the largest value 3136 g.
+static bool kv4_factor_ok(float g) { return g >= 0x1p-100f && g <= 0x1p100f; }  // (a NaN fails)
+static bool normal(float x) { return x >= 1.17549435e-38f && x <= 3.402823466e38f; }
 
 // What the 4-bit cache's calls have in common.
 static int kv4_args(const void* kv_cache, const int32_t* cu_seqlens, const int32_t* page_table,
@@ -490,7 +493,7 @@ static int kv4_args(const void* kv_cache, const int32_t* cu_seqlens, const int32
         DSPARK_EINVAL);
   CHECK(Hkv >= 1 && Hkv <= kMaxHeads, DSPARK_EINVAL);
   CHECK((long long)max_rows * Hkv <= 0x7fffffffLL, DSPARK_EUNSUPPORTED);  // grid size
-  CHECK(positive(k_scale) && positive(v_scale), DSPARK_EINVAL);
+  CHECK(kv4_factor_ok(k_scale) && kv4_factor_ok(v_scale), DSPARK_EINVAL);
   return DSPARK_OK;
 }
 
@@ -559,7 +562,7 @@ int dspark_verify_attn_kv4(const void* q, const void* k_new, const void* v_new,
   CHECK(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(out), DSPARK_EINVAL);
   CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
   CHECK(max_splits >= 1 && max_splits <= 32, DSPARK_EINVAL);
-  CHECK(positive(scale), DSPARK_EINVAL);
+  CHECK(normal(scale) && normal(attn::kv4a::score_factor(scale, k_scale)), DSPARK_EINVAL);
   // the kernels number the cache's blocks in 32 bits
   CHECK(n_pages <= 0x7fffffffLL / ((long long)Hkv * (page_size / 16)), DSPARK_EUNSUPPORTED);
   rc = device_ok();

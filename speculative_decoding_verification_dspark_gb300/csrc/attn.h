@@ -73,6 +73,8 @@ namespace kv4a {
 // The attention over the 4-bit cache.  Its plan: a query tile of 8 to 64 rows, several
 // CTAs per SM.
 Plan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows);
+// scale * log2(e) * 16 g: from a product of operands in cache units to a score in base 2.
+inline float score_factor(float scale, float g) { return scale * 1.4426950408889634f * (16.f * g); }
 int launch(const void* q, const void* k_new, const void* v_new, const void* cache, int n_pages,
            const int32_t* page_table, int max_pages, const int32_t* ctx_len,
            const int32_t* cu_seqlens, int B, int max_rows, int Hq, int Hkv, int page_size,

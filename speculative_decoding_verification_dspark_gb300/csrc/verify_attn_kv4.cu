@@ -730,7 +730,7 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
   p.max_pages = max_pages;
   p.n_pages = n_pages;
   p.slot_rows = pl.nt;
-  p.sl2 = scale * 1.4426950408889634f * (16.f * gk);
+  p.sl2 = score_factor(scale, gk);
   p.k_unit = 1.f / (16.f * gk);
   p.v_unit = 1.f / (16.f * gv);
   p.o_unit = 16.f * gv;

@@ -143,15 +143,14 @@ template <int ST>
 __device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_items, const OwnItems& own,
                                            uint32_t ring, uint32_t full, uint32_t empty) {
   const int lane = threadIdx.x & 31;
-  constexpr int kNone = -0x7fffffff;
-  int stage = 0, parity = 1, page = kNone;
-  // page of this lane's block in the window at tile t0; kNone where it holds no committed key of
-  // the item's tiles
+  int stage = 0, parity = 1, page = -1;
+  bool holds = false;
+  // whether this lane's block in the window at tile t0 holds a committed key of the item's tiles, and
+  // its page (not looked at before the window is copied: nothing waits for the read here)
   auto look = [&](const AttnItem& x, int t0) {
     const int pos = t0 * kKT + lane * kBlock, slot = pos >> p.log2_page;
-    page = kNone;
-    if (pos >= x.ctx || t0 + (lane >> 3) >= x.te) return;
-    page = slot < p.max_pages ? __ldg(p.page_table + (long long)x.r * p.max_pages + slot) : -1;
+    holds = pos < x.ctx && t0 + (lane >> 3) < x.te;
+    page = holds && slot < p.max_pages ? __ldg(p.page_table + (long long)x.r * p.max_pages + slot) : -1;
   };
   AttnItem x = s_items[0];
   look(x, x.tb);
@@ -165,7 +164,7 @@ __device__ __forceinline__ void copy_tiles(const Params& p, const AttnItem* s_it
       int block = -1;
       if ((unsigned)page < (unsigned)p.n_pages)
         block = ((page * p.Hkv + x.kvh) << lp) + (((t0 * kKT + lane * kBlock) >> 4) & ((1 << lp) - 1));
-      else if (page != kNone)
+      else if (holds)
         raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
       if (t0 + 4 < x.te) look(x, t0 + 4); else look(next, next.tb);
       const uint8_t* src = p.cache + (long long)(block < 0 ? 0 : block) * kBlockBytes;

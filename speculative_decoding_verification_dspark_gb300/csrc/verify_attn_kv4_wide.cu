@@ -182,13 +182,12 @@ struct Copier {
   int window;                  // first tile of the window, -1: none yet
   int block;                   // this lane's block, by its index among all blocks of the cache; -1: none
   int page;                    // and its page in the next window
+  bool holds;                  // where that block holds a committed key of the item's tiles
   int stage;
-  static constexpr int kNone = -0x7fffffff;
   __device__ __forceinline__ void look(int lane, int t0) {
     const int pos = t0 * kKT + lane * kBlock, slot = pos >> p.log2_page;
-    page = kNone;
-    if (pos >= ctx || t0 + (lane >> 3) >= te) return;
-    page = slot < p.max_pages ? __ldg(p.page_table + (long long)r * p.max_pages + slot) : -1;
+    holds = pos < ctx && t0 + (lane >> 3) < te;
+    page = holds && slot < p.max_pages ? __ldg(p.page_table + (long long)r * p.max_pages + slot) : -1;
   }
   // The first item from `at` on that has cache tiles, and the pages of its first window.
   __device__ __forceinline__ void start(int lane, int at) {
@@ -210,7 +209,7 @@ struct Copier {
       if ((unsigned)page < (unsigned)p.n_pages) {
         const int lp = p.log2_page - 4, pos = t * kKT + lane * kBlock;
         block = ((page * p.Hkv + kvh) << lp) + ((pos >> 4) & ((1 << lp) - 1));
-      } else if (page != kNone) {
+      } else if (holds) {
         raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
       }
       if (t + 4 < te) look(lane, t + 4);

@@ -1,5 +1,5 @@
 """Verify attention over the 4-bit cache: values that are not numbers in block rows that some
-of the query rows do not see.  Reference and tolerances are those of test_verify_attn_kv4."""
+of the query rows do not see, and pages out of range.  Reference and tolerances are those of test_verify_attn_kv4."""
 import pytest
 import torch
 
@@ -64,4 +64,19 @@ def test_infinite_values_in_unseen_rows(pkg, hint):  # noqa: F811
     c["v_new"][4], c["k_new"][4, 0, 1] = keep, 0
     o, l, _, _ = _reference(c)         # (row 4 itself sees them)
     out[4], lse[4] = torch.tensor(o[4]).bfloat16().cuda(), torch.tensor(l[4]).float().cuda()
+    _check(c, out, lse)
+
+
+@pytest.mark.gpu
+@BOTH
+@pytest.mark.parametrize("page", [-1, -2 ** 31 + 1, -2 ** 31, 2 ** 31 - 1])
+def test_every_page_out_of_range_is_reported(pkg, hint, page):  # noqa: F811
+    c = _case([200, 100], [3, 2], 8, 2, 16, seed=24)
+    c["table"][0, 12] = page
+    call, out, lse = _run(pkg, c, hint)
+    call()
+    assert pkg.read_device_error() == 0x10
+    c["table"][0, 12] = 0              # (the other request is as ever)
+    o, l, _, _ = _reference(c)
+    out[:3], lse[:3] = torch.tensor(o[:3]).bfloat16().cuda(), torch.tensor(l[:3]).float().cuda()
     _check(c, out, lse)

@@ -24,7 +24,6 @@ namespace kv4 {
 
 constexpr int kD = 128;
 constexpr int kBlock = 16;          // tokens of a block
-constexpr int kGroup = 32;          // elements that share a scale
 constexpr int kBlockBytes = 2176;
 constexpr int kOffV = 1024;
 constexpr int kOffKs = 2048;

@@ -109,16 +109,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 
 // Chunk j (8 query rows, 16 bytes) of row r of P in shared memory, placed so that neither the
 // eight rows of a fragment nor the rows {0, 1, 8, 9, 16, 17, 24, 25} + x that a warp writes at
-// once share banks: by padding after each eight rows (NT < 4) and by the chunk's place.
+// once share banks: by padding after each eight rows and, with two chunks, by the chunk's place.
 template <int NT>
 __device__ __forceinline__ uint32_t p_off(int r, int j) {
+  static_assert(NT == 1 || NT == 2, "tiles of 8 or 16 rows");
   if (NT == 1) return r * 16 + (r >> 3) * 32;
-  if (NT == 3) return r * 48 + (r >> 3) * 16 + j * 16;
-  if (NT == 2) return r * 32 + (r >> 3) * 64 + ((j ^ (((r >> 2) ^ (r >> 4)) & 1)) << 4);
-  return r * 64 + ((j ^ (((r >> 1) ^ (r >> 3)) & 3)) << 4);
+  return r * 32 + (r >> 3) * 64 + ((j ^ (((r >> 2) ^ (r >> 4)) & 1)) << 4);
 }
 template <int NT>
-constexpr int p_bytes() { return kKT * 16 * NT + 16 * (NT == 1 ? 32 : NT == 2 ? 64 : NT == 3 ? 16 : 0); }
+constexpr int p_bytes() { return kKT * 16 * NT + 16 * (NT == 1 ? 32 : 64); }
 // Row of Q (256 bytes, 16 chunks).
 __device__ __forceinline__ uint32_t q_off(int row, int c) { return row * 256 + ((c ^ (row & 7)) << 4); }
 

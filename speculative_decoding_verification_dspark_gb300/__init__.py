@@ -128,11 +128,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object in between, 1 us less; private to torch,
+# so not counted on.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, dev=None):
     if stream is None:
-        if dev is not None:  # without a Stream object in between, 1 us less
-            return torch._C._cuda_getCurrentRawStream(dev)
-        stream = torch.cuda.current_stream()
+        if dev is not None and _raw_stream is not None:
+            return _raw_stream(dev)
+        stream = torch.cuda.current_stream(dev)
     return ctypes.c_void_p(stream.cuda_stream)
 
 

@@ -526,8 +526,10 @@ int dspark_qk_norm_rope(const void* q_in, long long q_stride, const void* k_in,
  * Other positions keep their values.
  *
  * dspark_kv4_load reads positions pos0[r] .. pos0[r] + n_r - 1 back into packed rows
- * k, v [max_rows, Hkv, 128] (dense, fp32 or bf16 per dtype); rows >= cu_seqlens[B]
- * are left as they are.
+ * k, v [max_rows, Hkv, 128] (dense, fp32 or bf16 per dtype); rows before cu_seqlens[0]
+ * and from cu_seqlens[B] on are left as they are.  For a program that moves a request to
+ * a bf16 cache, to another k_scale / v_scale or off the device, or looks at its error;
+ * the step itself attends to the codes and does not load.
  *
  * Both: cu_seqlens must not fall; it may begin past row 0 (rows before cu_seqlens[0] are
  * no request's).  A position whose page-table slot or page is out of range sets
@@ -561,9 +563,11 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  *        (at most 64 / G); longer segments run as several row tiles.
  * Rounding: the cached values and the queries are exact in the products' fp16
  * operands (a query row is scaled by a power of two; elements below 2^-30 of the row's
- * largest may lose bits), block rows are rounded to fp16 after division by
- * 16 k_scale / 16 v_scale (saturating: |k_new| < 10^6 k_scale), the probabilities to
- * fp16; sums are fp32, and out is rounded once to bf16.
+ * largest may lose bits), block rows are rounded to fp16 after division by 16 k_scale
+ * (k_new) and 16 v_scale (v_new): elements below 10^-3 of the factor are off by up to 2^-21
+ * of it, those beyond 65504 * 16 of it (10^6 factors) and infinities saturate there.  The
+ * probabilities are rounded to fp16; sums are fp32, and out is rounded once to bf16.
+ * A NaN in v_new reaches the rows that see it, in its channel and heads, and no others.
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
  * undefined.  A negative length or first row (cu_seqlens falling or below 0, ctx_len below
  * 0), or ctx_len[r] and the rows of r together past 2^31 - 769, sets it too, and nothing is

@@ -626,8 +626,9 @@ def block_rows_hint_for(gamma, Hq, Hkv, mode) -> int:
 
 def block_rows_hint_for_kv4(gamma, Hq, Hkv) -> int:
     """Rows per request the query tile of the 4-bit cache's attention is sized for: the
-    block's gamma + 1 rows cut into as few tiles of at most 64 query rows as hold them, of
-    even size."""
+    block's gamma + 1 rows cut evenly into as few tiles of at most 64 query rows as hold
+    them.  The tile is then the next of 8, 16, 32, 48 or 64 rows and takes as many block rows
+    as fit: 17 rows of 4 heads give a hint of 9, a tile of 48 and pieces of 12 and 5 rows."""
     G = max(1, Hq // Hkv)
     tiles = -(-(gamma + 1) // max(1, 64 // G))
     return -(-(gamma + 1) // tiles)

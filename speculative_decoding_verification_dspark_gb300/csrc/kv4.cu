@@ -19,7 +19,7 @@
 // element and lane, 0.60 a cycle; 36 warps per SM by registers, 30 take 88 us), load 58 us,
 // 86% of the copy rate.  Reading the next pair's rows ahead cost more warps than it gave (134
 // us).  A commit of 32 requests is latency: a search of cu_seqlens, the page, the row or the
-// old codes, 4.6 us a kernel (5.1 when what follows is launched early and takes its places).
+// old codes, 4.7 us a kernel (5.1 when what follows is launched early and takes its places).
 //
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

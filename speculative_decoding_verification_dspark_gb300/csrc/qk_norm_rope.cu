@@ -11,9 +11,9 @@
 //
 // The angle: p f_i reaches 10^6 radians, where an fp32 product is off by 0.06.  So f_i / 2 pi
 // is taken once per CTA in fp64 and kept as a 64-bit fixed-point fraction of a turn; its
-// product with p modulo 2^64 is the angle less its whole turns (off by p 2^-53 f_i / 2 pi
-// turns and p 2^-65), which goes to the fp32 sine and cosine.  A row's R/2 angles are computed
-// once and shared by its heads.
+// product with p modulo 2^64 is the angle less its whole turns, off by p 2^-52 f_i / 2 pi turns
+// (1 / 2 pi and the product are rounded, 2^-53 each) and p 2^-65, which goes to the fp32 sine
+// and cosine.  A row's R/2 angles are computed once and shared by its heads.
 //
 // Layout: a persistent CTA takes `group` rows at a time, its 16 half-warps dealt to the rows;
 // a half-warp holds a head, 8 elements per lane (16 bytes of bf16), so the norm is an

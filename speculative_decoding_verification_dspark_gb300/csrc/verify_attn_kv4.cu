@@ -28,7 +28,7 @@
 // (131k contexts).
 //
 // Bound by instruction issue (0.63 per cycle and scheduler, which 18 warps per SM cannot
-// raise): 256 decodes read 646 MB in 169 us, 3.8 TB/s.  The copies alone (same blocks, same
+// raise): 256 decodes read 646 MB in 170 us, 3.8 TB/s.  The copies alone (same blocks, same
 // ring) take 96 us.
 //
 #include "kv4_attn.cuh"

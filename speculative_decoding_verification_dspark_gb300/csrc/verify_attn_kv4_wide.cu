@@ -29,7 +29,9 @@
 // Bound by the chain of a tile's steps: 0.53 instructions per cycle and scheduler, 950 a tile of
 // 32 rows (K 180, V 190, softmax 110, the rest waits, addresses and loops of nine warps), the
 // tensor pipe 13% busy; with two of the products' 16 instructions left it is 17% faster, without
-// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB): 155 us, 2.8 TB/s.
+// the expansion of K (V) 9% (16%).  131k contexts of 3 requests (428 MB): 154 us, 2.8 TB/s.
+// Registers: 96 a thread, the most that two CTAs leave; 44, 152 and 268 bytes are spilled with 32, 48
+// and 64 rows.
 
 #include "kv4_attn.cuh"
 

@@ -571,7 +571,7 @@ int dspark_kv4_load(const void* kv_cache, const int32_t* cu_seqlens, const int32
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; the outputs of its request are then
  * undefined.  A negative length or first row (cu_seqlens falling or below 0, ctx_len below
  * 0), or ctx_len[r] and the rows of r together past 2^31 - 769, sets it too, and nothing is
- * written; so with cu_seqlens[B] > max_rows and DSPARK_DEVERR_ROWS_OVERFLOW.
+ * written; so with cu_seqlens[B] outside 0..max_rows and DSPARK_DEVERR_ROWS_OVERFLOW.
  * Two kernels; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_kv4_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(1024)
       L = L < 0 ? 0 : gamma;
     }
     keep = L + 1;
-    if (keep > cu[tid + 1] - cu[tid]) atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
+    if ((long long)cu[tid] + keep > cu[tid + 1]) atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
     c0 = ctx_len[tid];
     have = ceil_div(c0, page_size);
     need = ceil_div(c0 + keep, page_size);

@@ -185,7 +185,9 @@ template <int THREADS>
 __device__ __forceinline__ OwnItems own_items(const Params& p, ItemScratch& S, AttnItem* s_items) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, c = blockIdx.x;
   const int B = p.B, rpt = p.rows_per_tile;
-  const bool rows_ok = p.cu_seqlens[B] <= p.max_rows;
+  // (with the last row no less than 0, as here, and the others no less than 0, as below, n does not
+  // pass 32 bits)
+  const bool rows_ok = (unsigned)p.cu_seqlens[B] <= (unsigned)p.max_rows;
   // this thread's requests
   const int per = (B + THREADS - 1) / THREADS, r_begin = tid * per, r_end = min(B, r_begin + per);
   long long units = 0;

@@ -154,3 +154,41 @@ def test_attention_refuses_ends_past_32_bits(pkg, hint):  # noqa: F811
         call()
         assert pkg.read_device_error() == 0x10
         assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
+
+
+@BOTH
+def test_attention_refuses_rows_that_fall_to_ints_end(pkg, hint):  # noqa: F811
+    """The difference of two rows may pass 32 bits and look like a length."""
+    c = _case([20, 40, 30], [1, 2, 2], 4, 2, 16, seed=34)
+    for cu in ([0, 1, 3, -2 ** 31], [0, 1, 2000, -2 ** 31], [0, 2 ** 31 - 1, -2 ** 31, 5],
+               [-2 ** 31, -2 ** 31, -2 ** 31, 0]):
+        c["cu"] = torch.tensor(cu, dtype=torch.int32)
+        call, out, lse = _run(pkg, c, hint)
+        call()
+        err = pkg.read_device_error()
+        assert err & (0x1 if cu[-1] < 0 else 0x10) and not err & ~0x11
+        assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("cu_bad", [[0, 3, -2 ** 31], [0, 2000000000, -2 ** 31], [0, 7, 6]])
+def test_compact_refuses_rows_that_fall(pkg, cu_bad, kv4):  # noqa: F811
+    gamma, B, page = 4, 2, 16
+    k, v, cu, ctx, table, cache = _batch([0, 3, 6], [14, 20], 2, page, 4)
+    cu[:] = torch.tensor(cu_bad, dtype=torch.int32)
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    kept = dict(table=table.cuda(), ctx=ctx.cuda(), anchor=z(B), top=z(1) + 5, com=z(B, gamma + 1),
+                ncom=z(B))
+    if kv4:
+        caches = [cache.cuda()]
+    else:
+        caches = [torch.ones(cache.shape[0], page, 2, 128, dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2)]
+    before = [t.clone() for t in (*kept.values(), *caches)]
+    ws = torch.empty(pkg.compact_workspace_size(B), dtype=torch.uint8, device="cuda")
+    free = torch.arange(5, dtype=torch.int32, device="cuda")
+    call, scales = (pkg.compact_kv4, (0.25, 0.5)) if kv4 else (pkg.compact, ())
+    call(k.cuda(), v.cuda(), cu.cuda(), z(B) + 1, z(B), z(B, gamma), kept["table"], kept["ctx"],
+         kept["anchor"], free, kept["top"], *caches, kept["com"], kept["ncom"], ws, *scales)
+    assert pkg.read_device_error() == 0x10
+    assert all(torch.equal(a, b) for a, b in zip(before, (*kept.values(), *caches)))

@@ -79,6 +79,8 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
 #define DSPARK_MAX_CANDS    4096   /* B * gamma for the scheduler's sort          */
 #define DSPARK_MAX_TIERS    64
 #define DSPARK_MAX_ECE_BINS 256
+#define DSPARK_MAX_TREE     512    /* rows of a drafted tree (a multiple of 64)  */
+#define DSPARK_MAX_VOCAB    400000 /* dspark_sample                              */
 
 const char* dspark_status_string(int status);
 
@@ -596,6 +598,125 @@ int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_ro
                        int32_t* free_top, void* kv_cache, float k_scale, float v_scale,
                        int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
                        void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Trees of drafted tokens.  The pages verify one drafted block a request ([lesson]
+ * "Ragged verify under full CUDA graphs"); here a request's packed rows may be the nodes
+ * of a tree instead, each with the position of its depth, and the target's own samples
+ * choose the branch.  A step: dspark_tree_pack, the forward pass with
+ * dspark_verify_attn_tree, dspark_sample, dspark_accept_tree, dspark_compact_path.
+ *
+ *   row_parent  int32 [max_rows]: the row's parent as an index in its segment, less than
+ *               the row's own; -1: none.  Row 0 of a segment is the anchor.
+ * A segment holds up to DSPARK_MAX_TREE rows, or none.
+ *
+ * dspark_tree_pack: row_mask [max_rows, words] 64-bit words, bit j % 64 of word j / 64 for
+ * the row itself and each of its ancestors j; row_pos int32 [max_rows], ctx_len[r] + the
+ * number of ancestors (what dspark_qk_norm_rope takes).  Rows outside cu_seqlens[0] ..
+ * cu_seqlens[B] - 1 are left as they are.  A parent out of range counts as none and sets
+ * DSPARK_DEVERR_BAD_INPUT; a segment of more than 64 words rows or DSPARK_MAX_TREE, a
+ * negative length, first row or context, or a context past 2^31 - 1 - DSPARK_MAX_TREE sets
+ * it too and the segment's rows are left as they are.  cu_seqlens[B] > max_rows sets
+ * DSPARK_DEVERR_ROWS_OVERFLOW and nothing is written.  One kernel.
+ *
+ * dspark_accept_tree walks each tree from its anchor: from row c to the lowest child whose
+ * token row_tok is row_sample[c], the token sampled from the target's distribution at c,
+ * until there is none (or gamma drafts are taken, or the sample is negative).
+ *   row_tok, row_sample  int32 [max_rows]
+ *   path        int32 [B, gamma + 1] out: the rows passed, as indices in the segment, the
+ *               anchor first, -1 beyond
+ *   path_tok    int32 [B, gamma] out: their tokens but the anchor's, -1 beyond
+ *   accept_len  int32 [B] out: drafts taken, L (-1 for an empty segment)
+ *   out_tok     int32 [B] out: the sample at the last row (-1 for an empty segment)
+ * The committed tokens are the target's own samples.  A segment that no buffer holds or of
+ * more than DSPARK_MAX_TREE rows sets DSPARK_DEVERR_BAD_INPUT and counts as empty;
+ * cu_seqlens[B] > max_rows sets DSPARK_DEVERR_ROWS_OVERFLOW and nothing is written.
+ *
+ * dspark_compact_path is dspark_compact with path and path_tok (as draft_tok): the rows kept
+ * of request r are path[r][0 .. accept_len[r]]; with accept_len -1 the request keeps its
+ * state (committed all -1, n_committed 0).  A path entry outside the segment sets
+ * DSPARK_DEVERR_BAD_INPUT and nothing is changed.
+ * ------------------------------------------------------------------------- */
+int dspark_tree_pack(const int32_t* row_parent, const int32_t* cu_seqlens, const int32_t* ctx_len,
+                     int B, int max_rows, int words, uint64_t* row_mask, int32_t* row_pos,
+                     void* stream);
+int dspark_accept_tree(const int32_t* row_tok, const int32_t* row_parent,
+                       const int32_t* row_sample, const int32_t* cu_seqlens, int B, int gamma,
+                       int max_rows, int32_t* path, int32_t* path_tok, int32_t* accept_len,
+                       int32_t* out_tok, void* stream);
+int dspark_compact_path(const void* k_new, const void* v_new, int row_bytes, int max_rows,
+                        const int32_t* cu_seqlens,
+                        const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
+                        const int32_t* path, int B, int gamma, int page_size, int max_pages, int n_pages,
+                        int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
+                        const int32_t* free_pages, int32_t* free_top, void* k_cache, void* v_cache,
+                        int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_verify_attn_tree -- dspark_verify_attn (GQA shape) for trees: packed row
+ * cu_seqlens[r] + i sees the ctx_len[r] committed keys and the block rows j of its segment
+ * whose bit j is set in row_mask[cu_seqlens[r] + i] (dspark_tree_pack's, or any other mask:
+ * the row itself is seen only if its bit is set).  Arguments as dspark_verify_attn, and
+ *   row_mask  [max_rows, words] 64-bit words; rows of the segment from 64 words on are seen
+ *             by none, bits past the segment are ignored
+ *   out       bf16 [max_rows, Hq, 128]; a row that sees no key, or none with a score
+ *             above -inf, gets out = 0 and lse = -inf
+ *   scale     a positive normal number
+ *   max_block_rows  a hint: the largest tree.  Up to 128 / G rows (G = Hq / Hkv <= 128) one query
+ *             tile of 128 rows is used, above that two that share the keys; any segment
+ *             length is handled.  The workspace size depends on it.
+ * Probabilities are rounded to bf16 for the product with V; maxima, sums and accumulators
+ * are fp32; out is rounded once.  What a row does not see has no effect on it, NaN and
+ * infinities included; nor have cache slots past ctx_len and rows outside the segment.
+ * A page out of range sets DSPARK_DEVERR_BAD_INPUT; its request's outputs are then undefined.
+ * A negative length or first row, or ctx_len[r] and the rows of r together past 2^31 - 769,
+ * sets it too, and nothing is written; so with cu_seqlens[B] outside 0..max_rows and
+ * DSPARK_DEVERR_ROWS_OVERFLOW.
+ * ------------------------------------------------------------------------- */
+size_t dspark_verify_attn_tree_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
+                                              int max_block_rows);
+int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
+                            const void* k_cache, const void* v_cache, int n_pages,
+                            const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                            const int32_t* cu_seqlens, const uint64_t* row_mask, int words, int B,
+                            int max_rows, int Hq, int Hkv, int page_size, float scale,
+                            int max_splits, int max_block_rows, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dspark_sample -- from logits to the distributions that dspark_accept reads and to
+ * tokens.  The order of a row's tokens: by logit, falling; the lowest index first among
+ * equals.  With the row's parameters T, k, p, q and l_max its largest logit,
+ *   w_v = exp((l_v - l_max) / T); kept are the tokens that
+ *   top-k leaves (the first k), min-p leaves (w_v >= q), and then top-p: the shortest
+ *   first part of these with at least p of their mass, one token at least;
+ *   probs_v = w_v / sum of the kept w (0 for the others),
+ *   token = argmax over the kept of w_v / e_v, lowest index on ties
+ * (with e ~ Exp(1) a draw from probs, as in dspark_accept).
+ *
+ *   logits      [rows, V] fp32 or bf16 (dtype), rows `stride` >= V elements apart.  NaN
+ *               counts as -inf, +inf as the type's largest number
+ *   row_req     int32 [rows], nullable: the parameters' index of each row (dspark_pack's
+ *               row_req); a row with a negative one is padding, its outputs are left as
+ *               they are.  NULL: row i has index i (B >= rows)
+ *   temperature fp32 [B]: 0 (the first token alone) or 2^-60 .. 2^60; NULL: 1
+ *   top_k       int32 [B]: off where < 1 or >= V; NULL: off
+ *   top_p       fp32 [B]: off where >= 1, the first token alone where <= 0; NULL: off
+ *   min_p       fp32 [B]: off where <= 0, as 1 where above; NULL: off
+ *   exp_noise   fp32 [rows, V] Exp(1) draws, > 0; NULL without tokens
+ *   tokens      int32 [rows] out, nullable
+ *   probs       [rows, V] fp32 or bf16 (probs_dtype) out, dense, nullable
+ * Which tokens are kept and which wins the race is decided as in 64-bit arithmetic (but where
+ * sums lie within 10^-10 of a border); probs are fp32 values (2^-18) rounded once.  A row
+ * without any logit above -inf gets token -1 and probs 0.  An index >= B, or a temperature
+ * outside its range, or a NaN parameter sets DSPARK_DEVERR_BAD_INPUT and the row's outputs
+ * are left as they are.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
+ * ------------------------------------------------------------------------- */
+int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
+                  const int32_t* row_req, int B, const float* temperature, const int32_t* top_k,
+                  const float* top_p, const float* min_p, const float* exp_noise, int32_t* tokens,
+                  void* probs, int probs_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * dspark_step_graph -- the whole verification step as one CUDA graph, with the

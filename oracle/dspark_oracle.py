@@ -895,3 +895,131 @@ def kv4_values(cache, g_k, g_v):
     v = (v * vs * float(F32(g_v))).transpose(0, 1, 2, 5, 3, 4)               # [tok, grp, ch]
     shape = (pages, Hkv, per * 16, 128)
     return (k.reshape(shape).transpose(0, 2, 1, 3), v.reshape(shape).transpose(0, 2, 1, 3))
+
+
+# ---------------------------------------------------------------------------
+# Trees of drafted tokens: row i of a segment has a parent before it in the segment (-1: none).
+def tree_masks(parent, cu_seqlens, ctx_len, words):
+    """(masks uint64 [rows, words], positions int32 [rows], rows written) by climbing."""
+    rows = len(parent)
+    mask, pos = np.zeros((rows, words), np.uint64), np.zeros(rows, np.int32)
+    for r in range(len(ctx_len)):
+        a = int(cu_seqlens[r])
+        for i in range(int(cu_seqlens[r + 1]) - a):
+            at, depth = i, -1
+            while at >= 0:
+                mask[a + i, at // 64] |= np.uint64(1) << np.uint64(at % 64)
+                at, depth = int(parent[a + at]), depth + 1
+            pos[a + i] = ctx_len[r] + depth
+    return mask, pos
+
+
+def verify_attention_tree(q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, cu_seqlens, mask,
+                          scale):
+    """fp64 (out [rows, Hq, 128], lse [rows, Hq], S, A): per row and head the largest
+    scale * sum |q k| over its keys and the weighted sum of |v| (for error bounds)."""
+    rows, Hq, d = q.shape
+    Hkv, page = k_new.shape[1], k_cache.shape[1]
+    G = Hq // Hkv
+    out, lse = np.zeros((rows, Hq, d)), np.full((rows, Hq), -np.inf)
+    S, A = np.zeros((rows, Hq)), np.zeros((rows, Hq, d))
+    for r in range(len(ctx_len)):
+        a, z, ctx = int(cu_seqlens[r]), int(cu_seqlens[r + 1]), int(ctx_len[r])
+        ids = page_table[r, :(ctx + page - 1) // page].astype(np.int64)
+        for h in range(Hkv):
+            kc = k_cache[ids, :, h].reshape(-1, d)[:ctx].astype(np.float64)
+            vc = v_cache[ids, :, h].reshape(-1, d)[:ctx].astype(np.float64)
+            for i in range(a, z):
+                see = [j for j in range(min(z - a, 64 * mask.shape[1]))
+                       if (int(mask[i, j // 64]) >> (j % 64)) & 1]
+                k = np.concatenate([kc, k_new[a:z, h][see].astype(np.float64)])
+                v = np.concatenate([vc, v_new[a:z, h][see].astype(np.float64)])
+                if not len(k):
+                    continue
+                x = q[i, h * G:(h + 1) * G].astype(np.float64)
+                s = scale * (x @ k.T)
+                top = s.max(1, keepdims=True)
+                e = np.exp(s - top)
+                w = e / e.sum(1, keepdims=True)
+                hs = slice(h * G, (h + 1) * G)
+                out[i, hs], lse[i, hs] = w @ v, (top + np.log(e.sum(1, keepdims=True)))[:, 0]
+                S[i, hs], A[i, hs] = scale * (np.abs(x) @ np.abs(k).T).max(1), w @ np.abs(v)
+    return out, lse, S, A
+
+
+def accept_tree(row_tok, row_parent, row_sample, cu_seqlens, gamma):
+    """(path, path_tok, accept_len, out_tok) of the walk along the samples."""
+    B = len(cu_seqlens) - 1
+    path, tok = np.full((B, gamma + 1), -1, np.int32), np.full((B, gamma), -1, np.int32)
+    n, out = np.full(B, -1, np.int32), np.full(B, -1, np.int32)
+    for r in range(B):
+        a, z = int(cu_seqlens[r]), int(cu_seqlens[r + 1])
+        at = 0 if z > a else None
+        while at is not None:
+            n[r] += 1
+            path[r, n[r]] = at
+            if n[r]:
+                tok[r, n[r] - 1] = row_tok[a + at]
+            out[r] = row_sample[a + at]
+            if n[r] == gamma or out[r] < 0:
+                break
+            at = next((j for j in range(at + 1, z - a)
+                       if row_parent[a + j] == at and row_tok[a + j] == out[r]), None)
+    return path, tok, n, out
+
+
+def compact_path(k_new, v_new, cu_seqlens, path, path_tok, accept_len, out_tok, page_size,
+                 page_table, ctx_len, anchor, free_pages, free_top, k_cache, v_cache):
+    """The state after the commit of the paths' rows, as copies in a dict."""
+    B, gamma = path_tok.shape
+    s = dict(page_table=page_table.copy(), ctx_len=ctx_len.copy(), anchor=anchor.copy(),
+             k_cache=k_cache.copy(), v_cache=v_cache.copy(), free_top=int(free_top),
+             committed=np.full((B, gamma + 1), -1, np.int32), n_committed=accept_len + 1)
+    for r in range(B):
+        L = int(accept_len[r])
+        for i in range(L + 1):
+            pos = int(s["ctx_len"][r])
+            if pos % page_size == 0:
+                s["free_top"] -= 1
+                s["page_table"][r, pos // page_size] = free_pages[s["free_top"]]
+            page, row = s["page_table"][r, pos // page_size], int(cu_seqlens[r]) + int(path[r, i])
+            s["k_cache"][page, pos % page_size] = k_new[row]
+            s["v_cache"][page, pos % page_size] = v_new[row]
+            s["ctx_len"][r] += 1
+        if L >= 0:
+            s["committed"][r, :L] = path_tok[r, :L]
+            s["committed"][r, L] = s["anchor"][r] = out_tok[r]
+    return s
+
+
+# ---------------------------------------------------------------------------
+# Sampling from logits
+def sample_row(logits, T, k, p, q, noise=None, top=np.finfo(np.float32).max):
+    """(token, probabilities fp64 [V]) of one row: logits fp32, parameters as fp32 numbers; `top`:
+    what +inf counts as."""
+    l = np.asarray(logits, np.float64).copy()
+    l[np.isnan(l)] = -np.inf
+    l = np.minimum(l, float(top))
+    V, w = len(l), np.zeros(len(l))
+    order = np.argsort(-l, kind="stable")
+    order = order[l[order] > -np.inf]
+    if not len(order):
+        return -1, w
+    if T == 0:
+        w[order[0]] = 1
+        return int(order[0]), w
+    z = (l[order] - l[order[0]]) / float(T)
+    n = len(order) if k < 1 else min(int(k), len(order))
+    if q > 0:
+        n = min(n, int((z >= np.log(min(float(q), 1.0))).sum()))
+    e = np.exp(z[:n])
+    if p < 1:
+        n = max(1, int((np.cumsum(e) - e < float(p) * e.sum()).sum()))
+        e = e[:n]
+    w[order[:n]] = e / e.sum()
+    if noise is None:
+        return -1, w
+    with np.errstate(divide="ignore"):
+        race = z[:n] - np.log(np.asarray(noise, np.float64)[order[:n]])
+    best = np.flatnonzero(race == race.max())
+    return int(order[:n][best].min()), w

@@ -22,6 +22,8 @@ __all__ = [
     "qk_norm_rope", "KV4_BLOCK_BYTES", "kv4_cache", "kv4_store", "kv4_load",
     "verify_attn_kv4", "verify_attn_kv4_workspace_size",
     "block_rows_hint_for_kv4", "compact_kv4",
+    "tree_pack", "verify_attn_tree", "verify_attn_tree_workspace_size", "sample", "accept_tree",
+    "TreeStep",
 ]
 
 COMPACT, STATIC, CAP_ACCEPT = 0, 1, 2
@@ -77,6 +79,14 @@ _SIGNATURES = {
     "dspark_step_graph_flags": (_I, [_P]),
     "dspark_compact": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                             _P, _P, _P, _P, _Z, _P]),
+    "dspark_compact_path": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                 _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "dspark_tree_pack": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "dspark_accept_tree": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "dspark_verify_attn_tree_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "dspark_verify_attn_tree": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I,
+                                     _I, _F, _I, _I, _P, _P, _P, _Z, _P]),
+    "dspark_sample": (_I, [_P, _L, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
     "dspark_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _P, _I, _I, _F, _P, _P, _I,
                                  _I, _I, _P, _P, _P, _P]),
     "dspark_kv4_store": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _I, _P, _I, _I, _F, _F, _P,
@@ -365,12 +375,19 @@ def compact_workspace_size(B) -> int:
 
 
 def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table, ctx_len, anchor,
-            free_pages, free_top, k_cache, v_cache, committed, n_committed, workspace, stream=None):
+            free_pages, free_top, k_cache, v_cache, committed, n_committed, workspace, stream=None,
+            path=None):
+    """``path`` (int32 [B, gamma + 1], accept_tree's): the rows of a tree that are kept, with
+    accept_tree's path_tok as draft_tok (dspark_compact_path)."""
     B, gamma = draft_tok.shape
     row_bytes = k_new[0].numel() * k_new.element_size()
-    _check("dspark_compact", lib().dspark_compact(
+    name, more = "dspark_compact", ()
+    if path is not None:
+        name = "dspark_compact_path"
+        more = (_arg(path, _current(path), "path", torch.int32, (B, gamma + 1)),)
+    _check(name, getattr(lib(), name)(
         _ptr(k_new), _ptr(v_new), row_bytes, k_new.shape[0], _ptr(cu_seqlens), _ptr(accept_len), _ptr(out_tok),
-        _ptr(draft_tok), B, gamma, k_cache.shape[1], page_table.shape[1], k_cache.shape[0],
+        _ptr(draft_tok), *more, B, gamma, k_cache.shape[1], page_table.shape[1], k_cache.shape[0],
         _ptr(page_table), _ptr(ctx_len), _ptr(anchor), _ptr(free_pages), _ptr(free_top),
         _ptr(k_cache), _ptr(v_cache), _ptr(committed), _ptr(n_committed), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -548,6 +565,114 @@ def compact_kv4(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_t
         _arg(workspace, dev, "workspace", torch.uint8), workspace.numel(), _stream(stream, dev)))
 
 
+# ---- trees of drafted tokens, and sampling from logits
+
+def tree_pack(row_parent, cu_seqlens, ctx_len, row_mask, row_pos, stream=None):
+    """Visibility masks and positions of packed trees (dspark_tree_pack): row_parent int32
+    [rows] (index in the segment, -1: none), row_mask int64 [rows, words] out, row_pos int32
+    [rows] out."""
+    i32, dev = torch.int32, _current(row_parent)
+    rows, B = row_parent.numel(), ctx_len.numel()
+    if row_mask.dim() != 2:
+        raise ValueError(f"row_mask: expected int64 [{rows}, words]")
+    words = row_mask.shape[1]
+    _check("dspark_tree_pack", lib().dspark_tree_pack(
+        _arg(row_parent, dev, "row_parent", i32, (rows,)),
+        _arg(cu_seqlens, dev, "cu_seqlens", i32, (B + 1,)), _arg(ctx_len, dev, "ctx_len", i32, (B,)),
+        B, rows, words, _arg(row_mask, dev, "row_mask", torch.int64, (rows, words)),
+        _arg(row_pos, dev, "row_pos", i32, (rows,)), _stream(stream, dev)))
+
+
+def verify_attn_tree_workspace_size(B, max_rows, Hq, Hkv, max_splits, max_block_rows=0) -> int:
+    return lib().dspark_verify_attn_tree_workspace_size(B, max_rows, Hq, Hkv, max_splits,
+                                                        max_block_rows)
+
+
+def verify_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, cu_seqlens, row_mask,
+                     scale, max_splits, out, lse, workspace, stream=None, max_block_rows=0):
+    """verify_attn (GQA) of trees: row_mask int64 [rows, words] says which block rows each row
+    sees (tree_pack's); out bf16 [rows, Hq, 128], lse fp32 [rows, Hq]."""
+    dev = _current(q)
+    rows, Hq, _ = q.shape
+    if k_cache.dim() != 4 or k_cache.shape[3] != 128:
+        raise ValueError("k_cache: expected bf16 [n_pages, page_size, Hkv, 128]")
+    n_pages, page, Hkv, _ = k_cache.shape
+    B = ctx_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected [{B}, max_pages]")
+    if row_mask.dim() != 2:
+        raise ValueError(f"row_mask: expected int64 [{rows}, words]")
+    words = row_mask.shape[1]
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check("dspark_verify_attn_tree", lib().dspark_verify_attn_tree(
+        _arg(q, dev, "q", bf16, (rows, Hq, 128)), _arg(k_new, dev, "k_new", bf16, (rows, Hkv, 128)),
+        _arg(v_new, dev, "v_new", bf16, (rows, Hkv, 128)), _arg(k_cache, dev, "k_cache", bf16),
+        _arg(v_cache, dev, "v_cache", bf16, k_cache.shape), n_pages,
+        _arg(page_table, dev, "page_table", i32), page_table.shape[1],
+        _arg(ctx_len, dev, "ctx_len", i32, (B,)), _arg(cu_seqlens, dev, "cu_seqlens", i32, (B + 1,)),
+        _arg(row_mask, dev, "row_mask", torch.int64, (rows, words)), words, B, rows, Hq, Hkv, page,
+        float(scale), int(max_splits), int(max_block_rows),
+        _arg(out, dev, "out", bf16, (rows, Hq, 128)),
+        _arg(lse, dev, "lse", torch.float32, (rows, Hq)),
+        _arg(workspace, dev, "workspace", torch.uint8), workspace.numel(), _stream(stream, dev)))
+
+
+def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, probs=None,
+           row_req=None, stream=None):
+    """Tokens and distributions from logits (dspark_sample): logits [rows, V] fp32 or bf16, rows
+    possibly apart; temperature, top_p, min_p fp32 [B] and top_k int32 [B], each None where it is
+    off; exp_noise fp32 [rows, V]; tokens int32 [rows] out or None; probs fp32 or bf16 [rows, V]
+    out or None; row_req int32 [rows] (< 0: padding, left as it is) or None: row i has the
+    parameters of index i."""
+    dev = _current(logits)
+    dt = _float_dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [rows, V]")
+    rows, V = logits.shape
+    stride = logits.stride(0) if rows > 1 else V   # the stride of one row is never used
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: the values of a row must be dense")
+    if logits.get_device() != dev:
+        raise ValueError("logits: expected a tensor on the current CUDA device")
+    f32, i32 = torch.float32, torch.int32
+    given = [t for t in (temperature, top_k, top_p, min_p) if t is not None]
+    B = given[0].numel() if given else rows
+    pdt = F32 if probs is None else _float_dtype(probs, "probs")
+
+    def par(t, name, dtype):
+        return None if t is None else _arg(t, dev, name, dtype, (B,))
+
+    _check("dspark_sample", lib().dspark_sample(
+        logits.data_ptr(), stride, dt, rows, V,
+        None if row_req is None else _arg(row_req, dev, "row_req", i32, (rows,)), B,
+        par(temperature, "temperature", f32), par(top_k, "top_k", i32), par(top_p, "top_p", f32),
+        par(min_p, "min_p", f32),
+        None if exp_noise is None else _arg(exp_noise, dev, "exp_noise", f32, (rows, V)),
+        None if tokens is None else _arg(tokens, dev, "tokens", i32, (rows,)),
+        None if probs is None else _arg(probs, dev, "probs", probs.dtype, (rows, V)), pdt,
+        _stream(stream, dev)))
+
+
+def accept_tree(row_tok, row_parent, cu_seqlens, row_sample, path, path_tok, accept_len, out_tok,
+                stream=None):
+    """The walk down each tree along the sampled tokens (dspark_accept_tree): row_tok,
+    row_parent, row_sample int32 [rows]; path int32 [B, gamma + 1], path_tok int32 [B, gamma],
+    accept_len, out_tok int32 [B] out."""
+    i32, dev = torch.int32, _current(row_tok)
+    rows, B = row_tok.numel(), accept_len.numel()
+    if path_tok.dim() != 2:
+        raise ValueError(f"path_tok: expected int32 [{B}, gamma]")
+    gamma = path_tok.shape[1]
+    _check("dspark_accept_tree", lib().dspark_accept_tree(
+        _arg(row_tok, dev, "row_tok", i32, (rows,)), _arg(row_parent, dev, "row_parent", i32, (rows,)),
+        _arg(row_sample, dev, "row_sample", i32, (rows,)),
+        _arg(cu_seqlens, dev, "cu_seqlens", i32, (B + 1,)), B, gamma, rows,
+        _arg(path, dev, "path", i32, (B, gamma + 1)),
+        _arg(path_tok, dev, "path_tok", i32, (B, gamma)),
+        _arg(accept_len, dev, "accept_len", i32, (B,)), _arg(out_tok, dev, "out_tok", i32, (B,)),
+        _stream(stream, dev)))
+
+
 class StepDesc(ctypes.Structure):
     """dspark_step_desc (field for field)."""
     _fields_ = (
@@ -651,6 +776,9 @@ class VerifyStep:
 
     Where ``inp`` holds ``q_in``, ``k_in`` and ``v_in`` (the packed rows' projections), ``run``
     fills q, k_new and v_new from them after the pack (``norm_rope``).
+
+    Where it holds ``logits`` (the packed rows' target logits, [max_rows, V]), ``run`` fills
+    p_target from them before the acceptance (``distributions``).
     """
 
     def __init__(self, B, gamma, Hq, Hkv, d_qk, d_v, vocab, max_rows, p_dtype=torch.float32,
@@ -727,6 +855,12 @@ class VerifyStep:
                      inp["v_new"], inp.get("eps", 1e-6), inp.get("interleaved", False),
                      inp.get("attn_factor", 1.0), stream, n_rows=self.M_pack)
 
+    def distributions(self, inp, stream=None):
+        """p_target of ``inp`` from its logits, filtered by its requests' parameters (temperature,
+        top_k, top_p, min_p [B], each optional), for the rows of the last pack."""
+        sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
+               inp.get("min_p"), None, None, inp["p_target"], self.row_req, stream)
+
     def attention(self, inp, stream=None):
         if self.kv4:
             verify_attn_kv4(inp["q"], inp["k_new"], inp["v_new"], inp["kv_cache"],
@@ -792,6 +926,8 @@ class VerifyStep:
             raise ValueError("the step graph does not take the 4-bit cache")
         if "q_in" in inp:
             raise ValueError("the step graph does not run norm_rope: pass inputs without q_in")
+        if "logits" in inp:
+            raise ValueError("the step graph does not sample: pass inputs without logits")
         pdt = inp["p_target"].dtype
         tiers = inp["tiers"]
         tiers_dev = tiers.to(self.windows.device, torch.int32)
@@ -832,5 +968,84 @@ class VerifyStep:
         if "q_in" in inp:
             self.norm_rope(inp, stream)
         (self.attention if self.kv4 else self.attention_planned)(inp, stream)
+        if "logits" in inp:
+            self.distributions(inp, stream)
         self.accept(inp, mode, stream)
+        self.compact(inp, stream)
+
+
+class TreeStep:
+    """Device buffers and workspaces for repeated verification steps on trees of drafted tokens,
+    of one shape.
+
+    ``run`` enqueues one step on the current stream: tree_pack -> (qk_norm_rope, where ``inp``
+    holds q_in, k_in and v_in) -> verify_attn_tree -> sample -> accept_tree -> compact along the
+    path.  ``inp`` holds cu_seqlens, row_tok, row_parent (the packed trees, row 0 of a segment the
+    anchor), row_req int32 [max_rows] (each row's request, -1 past the last), q, k_new, v_new,
+    logits, exp_noise [max_rows, V], scale, the caches, the state that VerifyStep has too, and
+    optionally temperature, top_k, top_p, min_p [B].
+    """
+
+    def __init__(self, B, gamma, Hq, Hkv, max_rows, max_nodes, max_splits=32, device="cuda"):
+        if not 1 <= max_nodes <= 512:
+            raise ValueError("a tree has 1 to 512 rows")
+        self.B, self.gamma, self.max_rows = B, gamma, max_rows
+        self.max_nodes, self.max_splits = max_nodes, max_splits
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.row_mask = torch.zeros(max_rows, -(-max_nodes // 64), dtype=torch.int64, device=dev)
+        self.row_pos = torch.zeros(max_rows, **i32)
+        self.out = torch.zeros(max_rows, Hq, 128, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros(max_rows, Hq, dtype=torch.float32, device=dev)
+        self.row_sample = torch.zeros(max_rows, **i32)
+        self.path = torch.zeros(B, gamma + 1, **i32)
+        self.path_tok = torch.zeros(B, gamma, **i32)
+        self.accept_len = torch.zeros(B, **i32)
+        self.out_tok = torch.zeros(B, **i32)
+        self.committed = torch.zeros(B, gamma + 1, **i32)
+        self.n_committed = torch.zeros(B, **i32)
+        sz = verify_attn_tree_workspace_size(B, max_rows, Hq, Hkv, max_splits, max_nodes)
+        if sz == 0:
+            raise ValueError("unsupported attention shape")
+        self.ws_attn = torch.empty(sz, dtype=torch.uint8, device=dev)
+        self.ws_compact = torch.empty(compact_workspace_size(B), dtype=torch.uint8, device=dev)
+
+    def pack(self, inp, stream=None):
+        tree_pack(inp["row_parent"], inp["cu_seqlens"], inp["ctx_len"], self.row_mask, self.row_pos,
+                  stream)
+
+    def norm_rope(self, inp, stream=None):
+        """q, k_new, v_new of ``inp`` from q_in, k_in, v_in, at the positions of the last pack."""
+        qk_norm_rope(inp["q_in"], inp["k_in"], inp["v_in"], inp.get("q_weight"),
+                     inp.get("k_weight"), inp["inv_freq"], self.row_pos, inp["q"], inp["k_new"],
+                     inp["v_new"], inp.get("eps", 1e-6), inp.get("interleaved", False),
+                     inp.get("attn_factor", 1.0), stream, n_rows=inp["cu_seqlens"][-1:])
+
+    def attention(self, inp, stream=None):
+        verify_attn_tree(inp["q"], inp["k_new"], inp["v_new"], inp["k_cache"], inp["v_cache"],
+                         inp["page_table"], inp["ctx_len"], inp["cu_seqlens"], self.row_mask,
+                         inp["scale"], self.max_splits, self.out, self.lse, self.ws_attn, stream,
+                         max_block_rows=self.max_nodes)
+
+    def sample(self, inp, stream=None):
+        sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
+               inp.get("min_p"), inp["exp_noise"], self.row_sample, None, inp["row_req"], stream)
+
+    def accept(self, inp, stream=None):
+        accept_tree(inp["row_tok"], inp["row_parent"], inp["cu_seqlens"], self.row_sample, self.path,
+                    self.path_tok, self.accept_len, self.out_tok, stream)
+
+    def compact(self, inp, stream=None):
+        compact(inp["k_new"], inp["v_new"], inp["cu_seqlens"], self.accept_len, self.out_tok,
+                self.path_tok, inp["page_table"], inp["ctx_len"], inp["anchor"], inp["free_pages"],
+                inp["free_top"], inp["k_cache"], inp["v_cache"], self.committed, self.n_committed,
+                self.ws_compact, stream, path=self.path)
+
+    def run(self, inp, stream=None):
+        self.pack(inp, stream)
+        if "q_in" in inp:
+            self.norm_rope(inp, stream)
+        self.attention(inp, stream)
+        self.sample(inp, stream)
+        self.accept(inp, stream)
         self.compact(inp, stream)

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libdspark.so")
 SOURCES = ["api.cu", "schedule_pack.cu", "accept.cu", "compact.cu", "verify_attn.cu", "step_graph.cu",
            "calib.cu", "markov_draft.cu", "qk_norm_rope.cu", "kv4.cu", "verify_attn_kv4.cu",
            "verify_attn_kv4_wide.cu",
-           "verify_attn_gqa.cu", "verify_attn_mla.cu"]
+           "tree.cu", "verify_attn_tree.cu", "sample.cu", "verify_attn_gqa.cu", "verify_attn_mla.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -349,14 +349,13 @@ size_t dspark_compact_workspace_size(int B) {
   return compact_workspace(B);
 }
 
-int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
-                   const int32_t* cu_seqlens,
-                   const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
-                   int B, int gamma, int page_size, int max_pages, int n_pages,
-                   int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
-                   const int32_t* free_pages, int32_t* free_top, void* k_cache, void* v_cache,
-                   int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
-                   void* stream) {
+static int compact_impl(const void* k_new, const void* v_new, int row_bytes, int max_rows,
+                        const int32_t* cu_seqlens, const int32_t* accept_len,
+                        const int32_t* out_tok, const int32_t* draft_tok, const int32_t* path, int B,
+                        int gamma, int page_size, int max_pages, int n_pages, int32_t* page_table,
+                        int32_t* ctx_len, int32_t* anchor, const int32_t* free_pages,
+                        int32_t* free_top, void* k_cache, void* v_cache, int32_t* committed,
+                        int32_t* n_committed, void* workspace, size_t ws_bytes, void* stream) {
   CHECK(k_new && cu_seqlens && accept_len && out_tok && draft_tok && page_table && ctx_len &&
             anchor && free_pages && free_top && k_cache && committed && n_committed && workspace,
         DSPARK_EINVAL);
@@ -371,10 +370,39 @@ int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_
   int rc = device_ok();
   if (rc != DSPARK_OK) return rc;
   CHECK(ws_bytes >= compact_workspace(B), DSPARK_ENOSPACE);
-  return launch_compact(k_new, v_new, row_bytes, max_rows, cu_seqlens, accept_len, out_tok, draft_tok, B,
-                        gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
+  return launch_compact(k_new, v_new, row_bytes, max_rows, cu_seqlens, accept_len, out_tok, draft_tok, path,
+                        B, gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
                         free_pages, free_top, k_cache, v_cache, committed, n_committed, workspace,
                         static_cast<cudaStream_t>(stream));
+}
+
+int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
+                   const int32_t* cu_seqlens,
+                   const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
+                   int B, int gamma, int page_size, int max_pages, int n_pages,
+                   int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
+                   const int32_t* free_pages, int32_t* free_top, void* k_cache, void* v_cache,
+                   int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  return compact_impl(k_new, v_new, row_bytes, max_rows, cu_seqlens, accept_len, out_tok, draft_tok,
+                      nullptr, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
+                      free_pages, free_top, k_cache, v_cache, committed, n_committed, workspace,
+                      ws_bytes, stream);
+}
+
+int dspark_compact_path(const void* k_new, const void* v_new, int row_bytes, int max_rows,
+                        const int32_t* cu_seqlens,
+                        const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
+                        const int32_t* path, int B, int gamma, int page_size, int max_pages, int n_pages,
+                        int32_t* page_table, int32_t* ctx_len, int32_t* anchor,
+                        const int32_t* free_pages, int32_t* free_top, void* k_cache, void* v_cache,
+                        int32_t* committed, int32_t* n_committed, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  CHECK(path, DSPARK_EINVAL);
+  return compact_impl(k_new, v_new, row_bytes, max_rows, cu_seqlens, accept_len, out_tok, draft_tok,
+                      path, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
+                      free_pages, free_top, k_cache, v_cache, committed, n_committed, workspace,
+                      ws_bytes, stream);
 }
 
 int dspark_calib_collect(const float* survival, const float* a_hat, const int32_t* windows,
@@ -599,6 +627,96 @@ int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_ro
                             B, gamma, page_size, max_pages, n_pages, page_table, ctx_len, anchor,
                             free_pages, free_top, kv_cache, k_scale, v_scale, committed,
                             n_committed, workspace, static_cast<cudaStream_t>(stream));
+}
+
+static bool tree_heads_ok(int Hq, int Hkv) {
+  return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 128 && Hq <= kMaxHeads;
+}
+
+int dspark_tree_pack(const int32_t* row_parent, const int32_t* cu_seqlens, const int32_t* ctx_len,
+                     int B, int max_rows, int words, uint64_t* row_mask, int32_t* row_pos,
+                     void* stream) {
+  CHECK(row_parent && cu_seqlens && ctx_len && row_mask && row_pos, DSPARK_EINVAL);
+  CHECK(B >= 1 && B <= DSPARK_MAX_B && max_rows >= 1, DSPARK_EINVAL);
+  CHECK(words >= 1 && words <= DSPARK_MAX_TREE / 64, DSPARK_EINVAL);
+  int rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  return launch_tree_pack(row_parent, cu_seqlens, ctx_len, B, max_rows, words, row_mask, row_pos,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t dspark_verify_attn_tree_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
+                                              int max_block_rows) {
+  if (B < 1 || B > DSPARK_MAX_B || max_rows < 1 || max_splits < 1 || max_splits > 32 ||
+      !tree_heads_ok(Hq, Hkv))
+    return 0;
+  return attn::tree::workspace(B, max_rows, Hq, Hkv, max_block_rows);
+}
+
+int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
+                            const void* k_cache, const void* v_cache, int n_pages,
+                            const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                            const int32_t* cu_seqlens, const uint64_t* row_mask, int words, int B,
+                            int max_rows, int Hq, int Hkv, int page_size, float scale,
+                            int max_splits, int max_block_rows, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  CHECK(tree_heads_ok(Hq, Hkv), DSPARK_EUNSUPPORTED);
+  CHECK(page_size >= 16 && (page_size & (page_size - 1)) == 0, DSPARK_EUNSUPPORTED);
+  CHECK(q && k_new && v_new && k_cache && v_cache && page_table && ctx_len && cu_seqlens &&
+            row_mask && out && lse && workspace,
+        DSPARK_EINVAL);
+  CHECK(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(k_cache) &&
+            aligned16(v_cache) && aligned16(out),
+        DSPARK_EINVAL);
+  CHECK(B >= 1 && B <= DSPARK_MAX_B && max_rows >= 1 && n_pages >= 1 && max_pages >= 1,
+        DSPARK_EINVAL);
+  CHECK(words >= 1 && words <= DSPARK_MAX_TREE / 64, DSPARK_EINVAL);
+  CHECK(max_splits >= 1 && max_splits <= 32, DSPARK_EINVAL);
+  CHECK(normal(scale), DSPARK_EINVAL);
+  CHECK((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, DSPARK_EINVAL);
+  int rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  CHECK(ws_bytes >= attn::tree::workspace(B, max_rows, Hq, Hkv, max_block_rows), DSPARK_ENOSPACE);
+  return attn::tree::launch(q, k_new, v_new, k_cache, v_cache, n_pages, page_table, max_pages,
+                            ctx_len, cu_seqlens, row_mask, words, B, max_rows, Hq, Hkv, page_size,
+                            scale, max_splits, max_block_rows, out, lse, workspace,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
+                  const int32_t* row_req, int B, const float* temperature, const int32_t* top_k,
+                  const float* top_p, const float* min_p, const float* exp_noise, int32_t* tokens,
+                  void* probs, int probs_dtype, void* stream) {
+  CHECK(logits && (tokens || probs) && (!tokens || exp_noise), DSPARK_EINVAL);
+  CHECK(dtype == DSPARK_F32 || dtype == DSPARK_BF16, DSPARK_EINVAL);
+  CHECK(!probs || probs_dtype == DSPARK_F32 || probs_dtype == DSPARK_BF16, DSPARK_EINVAL);
+  CHECK(V >= 1 && rows >= 1 && rows <= (1 << 26) && stride >= V, DSPARK_EINVAL);
+  CHECK(V <= DSPARK_MAX_VOCAB, DSPARK_EUNSUPPORTED);
+  CHECK(B >= 1 && (row_req || B >= rows), DSPARK_EINVAL);
+  const uintptr_t es = dtype == DSPARK_BF16 ? 2 : 4, ps = probs_dtype == DSPARK_BF16 ? 2 : 4;
+  CHECK(reinterpret_cast<uintptr_t>(logits) % es == 0 &&
+            (!probs || reinterpret_cast<uintptr_t>(probs) % ps == 0),
+        DSPARK_EINVAL);
+  int rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  const SampleArgs a = {logits, stride, rows, V, row_req, B, temperature, top_k, top_p, min_p,
+                        exp_noise, tokens, probs, device_error_word()};
+  return launch_sample(a, dtype, probs ? probs_dtype : DSPARK_F32, static_cast<cudaStream_t>(stream));
+}
+
+int dspark_accept_tree(const int32_t* row_tok, const int32_t* row_parent,
+                       const int32_t* row_sample, const int32_t* cu_seqlens, int B, int gamma,
+                       int max_rows, int32_t* path, int32_t* path_tok, int32_t* accept_len,
+                       int32_t* out_tok, void* stream) {
+  CHECK(row_tok && row_parent && row_sample && cu_seqlens && path && path_tok && accept_len &&
+            out_tok,
+        DSPARK_EINVAL);
+  CHECK(B >= 1 && B <= DSPARK_MAX_B && gamma >= 1 && gamma <= DSPARK_MAX_GAMMA && max_rows >= 1,
+        DSPARK_EINVAL);
+  int rc = device_ok();
+  if (rc != DSPARK_OK) return rc;
+  return launch_accept_tree(row_tok, row_parent, row_sample, cu_seqlens, B, gamma, max_rows, path,
+                            path_tok, accept_len, out_tok, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -82,6 +82,16 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* cach
            const Plan& pl, cudaStream_t stream);
 }  // namespace kv4a
 
+namespace tree {
+// The attention of drafted trees over the bf16 cache (verify_attn_tree.cu).
+size_t workspace(int B, int max_rows, int Hq, int Hkv, int max_block_rows);
+int launch(const void* q, const void* k_new, const void* v_new, const void* k_cache,
+           const void* v_cache, int n_pages, const int32_t* page_table, int max_pages,
+           const int32_t* ctx_len, const int32_t* cu_seqlens, const uint64_t* mask, int words, int B,
+           int max_rows, int Hq, int Hkv, int page_size, float scale, int max_splits,
+           int max_block_rows, void* out, float* lse, void* ws, cudaStream_t stream);
+}  // namespace tree
+
 namespace mla {
 constexpr int kKeyTile = 64;
 // Two-CTA clusters that can be resident at once (the kernel's grid, in clusters).

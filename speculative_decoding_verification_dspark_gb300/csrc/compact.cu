@@ -10,6 +10,9 @@
 //                         or a page-table row is too short nothing is changed.
 //   compact_copy_kernel   one CTA per (request, kept row): 16-byte copies of the
 //                         K (and V) row into its cache slot.
+//
+// A segment's kept rows are its first ones or, for a tree of drafts, those that a path
+// names (accept_tree's); such a segment may also be empty (accept_len -1: nothing is kept).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,7 +44,8 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
 __global__ void __launch_bounds__(1024)
     compact_alloc_kernel(const int32_t* __restrict__ cu, int max_rows,
                          const int32_t* __restrict__ accept_len, const int32_t* __restrict__ out_tok,
-                         const int32_t* __restrict__ draft_tok, int B, int gamma, int page_size,
+                         const int32_t* __restrict__ draft_tok, const int32_t* __restrict__ path,
+                         int B, int gamma, int page_size,
                          int max_pages, int n_pages, int32_t* __restrict__ page_table,
                          int32_t* __restrict__ ctx_len, int32_t* __restrict__ anchor,
                          const int32_t* __restrict__ free_pages, int32_t* __restrict__ free_top,
@@ -64,12 +68,20 @@ __global__ void __launch_bounds__(1024)
   int L = 0, c0 = 0, keep = 0, have = 0, need = 0, nn = 0;
   if (tid < B) {
     L = accept_len[tid];
-    if (L < 0 || L > gamma) {
+    if (L < (path ? -1 : 0) || L > gamma) {
       atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);
       L = L < 0 ? 0 : gamma;
     }
     keep = L + 1;
-    if ((long long)cu[tid] + keep > cu[tid + 1]) atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
+    if (path) {
+      const int first = cu[tid], n = cu[tid + 1] - first;
+      bool bad = first < 0 || n < 0 || first + (long long)n > max_rows;
+      for (int i = 0; i < keep; ++i)
+        bad |= (unsigned)path[tid * (gamma + 1) + i] >= (unsigned)n;
+      if (bad) atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);
+    } else if ((long long)cu[tid] + keep > cu[tid + 1]) {
+      atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
+    }
     c0 = ctx_len[tid];
     have = ceil_div(c0, page_size);
     need = ceil_div(c0 + keep, page_size);
@@ -104,8 +116,8 @@ __global__ void __launch_bounds__(1024)
     }
     old_ctx[tid] = c0;
     ctx_len[tid] = c0 + keep;
-    const int tok = out_tok[tid];
-    anchor[tid] = tok;
+    const int tok = keep > 0 ? out_tok[tid] : -1;
+    if (keep > 0) anchor[tid] = tok;
     for (int i = 0; i <= gamma; ++i)
       committed[tid * (gamma + 1) + i] = (i < L) ? draft_tok[tid * gamma + i] : (i == L ? tok : -1);
     n_committed[tid] = keep;
@@ -120,7 +132,8 @@ __global__ void __launch_bounds__(1024)
 __global__ void __launch_bounds__(128)
     compact_copy_kernel(const uint8_t* __restrict__ k_new, const uint8_t* __restrict__ v_new,
                         int row_bytes, const int32_t* __restrict__ cu,
-                        const int32_t* __restrict__ accept_len, int gamma, int page_size,
+                        const int32_t* __restrict__ accept_len, const int32_t* __restrict__ path,
+                        int gamma, int page_size,
                         int max_pages, int n_pages, const int32_t* __restrict__ page_table,
                         const int* __restrict__ old_ctx, const CompactWs* __restrict__ cws,
                         uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
@@ -131,7 +144,7 @@ __global__ void __launch_bounds__(128)
   const int i = blockIdx.y;
   if (!cws->ok) return;
   int L = accept_len[r];
-  L = L < 0 ? 0 : (L > gamma ? gamma : L);
+  if (!path) L = L < 0 ? 0 : (L > gamma ? gamma : L);
   if (i > L) return;
   const int pos = old_ctx[r] + i;
   const int page = page_table[(long long)r * max_pages + pos / page_size];
@@ -140,7 +153,7 @@ __global__ void __launch_bounds__(128)
     return;
   }
   const long long dst = ((long long)page * page_size + pos % page_size) * row_bytes;
-  const long long src = (long long)(cu[r] + i) * row_bytes;
+  const long long src = (long long)(cu[r] + (path ? path[r * (gamma + 1) + i] : i)) * row_bytes;
   for (int b = threadIdx.x * 16; b < row_bytes; b += blockDim.x * 16) {
     *reinterpret_cast<uint4*>(k_cache + dst + b) =
         *reinterpret_cast<const uint4*>(k_new + src + b);
@@ -155,6 +168,7 @@ size_t compact_workspace(int B) { return sizeof(CompactWs) + (((size_t)B * sizeo
 int launch_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
                    const int32_t* cu,
                    const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
+                   const int32_t* path,
                    int B, int gamma, int page_size, int max_pages, int n_pages, int32_t* page_table,
                    int32_t* ctx_len, int32_t* anchor, const int32_t* free_pages, int32_t* free_top,
                    void* k_cache, void* v_cache, int32_t* committed, int32_t* n_committed, void* ws,
@@ -162,13 +176,13 @@ int launch_compact(const void* k_new, const void* v_new, int row_bytes, int max_
   CompactWs* cws = static_cast<CompactWs*>(ws);
   int* old_ctx = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(CompactWs));
   if (launch_pdl(compact_alloc_kernel, dim3(1), dim3(1024), 0, stream, cu, max_rows, accept_len,
-                 out_tok, draft_tok, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len,
+                 out_tok, draft_tok, path, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len,
                  anchor, free_pages, free_top, committed, n_committed, cws, old_ctx,
                  device_error_word()) != cudaSuccess)
     return DSPARK_ECUDA;
   dim3 grid(B, gamma + 1);
   if (launch_pdl(compact_copy_kernel, grid, dim3(128), 0, stream, static_cast<const uint8_t*>(k_new),
-                 static_cast<const uint8_t*>(v_new), row_bytes, cu, accept_len, gamma, page_size,
+                 static_cast<const uint8_t*>(v_new), row_bytes, cu, accept_len, path, gamma, page_size,
                  max_pages, n_pages, page_table, old_ctx, cws, static_cast<uint8_t*>(k_cache),
                  static_cast<uint8_t*>(v_cache), device_error_word()) != cudaSuccess)
     return DSPARK_ECUDA;
@@ -185,8 +199,8 @@ int launch_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_ro
   CompactWs* cws = static_cast<CompactWs*>(ws);
   int* old_ctx = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(CompactWs));
   if (launch_pdl(compact_alloc_kernel, dim3(1), dim3(1024), 0, stream, cu, max_rows, accept_len,
-                 out_tok, draft_tok, B, gamma, page_size, max_pages, n_pages, page_table, ctx_len,
-                 anchor, free_pages, free_top, committed, n_committed, cws, old_ctx,
+                 out_tok, draft_tok, static_cast<const int32_t*>(nullptr), B, gamma, page_size, max_pages,
+                 n_pages, page_table, ctx_len, anchor, free_pages, free_top, committed, n_committed, cws, old_ctx,
                  device_error_word()) != cudaSuccess)
     return DSPARK_ECUDA;
   const long long stride = (long long)Hkv * 128;

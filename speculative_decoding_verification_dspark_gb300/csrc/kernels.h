@@ -94,6 +94,7 @@ size_t compact_workspace(int B);
 int launch_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
                    const int32_t* cu,
                    const int32_t* accept_len, const int32_t* out_tok, const int32_t* draft_tok,
+                   const int32_t* path,  // nullable: the kept rows are a segment's first
                    int B, int gamma, int page_size, int max_pages, int n_pages, int32_t* page_table,
                    int32_t* ctx_len, int32_t* anchor, const int32_t* free_pages, int32_t* free_top,
                    void* k_cache, void* v_cache, int32_t* committed, int32_t* n_committed, void* ws,
@@ -125,5 +126,31 @@ int launch_kv4_store(const void* k, long long k_stride, const void* v, long long
 int launch_kv4_load(const void* cache, const int32_t* cu, const int32_t* pos0, int B, int max_rows,
                     int Hkv, int page_size, const int32_t* page_table, int max_pages, int n_pages,
                     float gk, float gv, int dtype, void* k, void* v, cudaStream_t stream);
+
+// Trees of drafted tokens (tree.cu).
+int launch_tree_pack(const int32_t* parent, const int32_t* cu, const int32_t* ctx_len, int B,
+                     int max_rows, int words, uint64_t* mask, int32_t* pos, cudaStream_t stream);
+int launch_accept_tree(const int32_t* row_tok, const int32_t* parent, const int32_t* row_sample,
+                       const int32_t* cu, int B, int gamma, int max_rows, int32_t* path,
+                       int32_t* path_tok, int32_t* accept_len, int32_t* out_tok,
+                       cudaStream_t stream);
+
+// Sampling from logits (sample.cu).
+struct SampleArgs {
+  const void* logits;
+  long long stride;              // elements between the rows of logits
+  int rows, V;
+  const int32_t* row_req;        // nullable: row i has the parameters of index i
+  int B;
+  const float* temperature;      // [B], nullable: 1
+  const int32_t* top_k;          // [B], nullable: off
+  const float* top_p;            // [B], nullable: off
+  const float* min_p;            // [B], nullable: off
+  const float* noise;            // [rows, V], nullable with tokens
+  int32_t* tokens;               // [rows], nullable
+  void* probs;                   // [rows, V], nullable
+  unsigned int* err;
+};
+int launch_sample(const SampleArgs& a, int dtype, int probs_dtype, cudaStream_t stream);
 
 }  // namespace dspark

@@ -4,120 +4,832 @@
 // the block rows j of its segment whose bit j is set in row_mask: o = softmax(scale q.K^T) V,
 // lse = log-sum-exp.  A row that sees no key gets o = 0, lse = -inf.
 //
-// One warp per (row, query head), four dims to a lane, one pass over the keys with the running
-// maximum and sum.
+// A tree brings many query rows to each key (64 nodes of 4 heads: 256, some 250 FLOP a byte, where
+// HBM and the tensor cores balance), so queries lie on the MMA's M side, 128 rows to a tile, and a
+// work item has up to two tiles that share the keys:
+//   S [128 rows x 128 keys] = Q . K^T         O [128 rows x 128 d] += P . V       (tcgen05)
+// with S and O in tensor memory and P, in bf16, in the columns that held S.  All 512 columns are
+// taken: two S, two O.  An item of one tile's rows runs as two streams of its key tiles, even and
+// odd, each with an S, an O and statistics of its own, joined at the item's end: so that one
+// stream's softmax runs beside the other's products whether there are two tiles or one.
+//
+// Warps (one CTA an SM, persistent over its share of the key tiles, see own_items.cuh):
+//   0      K and V: TMA (128-byte swizzle) into a ring of five 32 KB slots, in the order K V K V
+//   1      issues the products: O += P V of a stream's last tile, then S of its next
+//   2      looks over the V tiles that need it: block rows, and the context's last tile.  Rows past
+//          the visible keys become zero; so do NaN and infinities of block rows, since a row that
+//          does not see them weighs them 0, and 0 times them is NaN: the rows that do see them get
+//          them after the epilogue (write_specials)
+//   3      Q: TMA, the tile's rows as they lie
+//   4-7, 8-11  the softmax of the streams, thread = row: maximum, exponentials and sum of 128 keys
+//          without a word to another thread; O is rescaled only where a row's maximum grows by 2^8
+// Every wait is bounded in time (DSPARK_DEVERR_WAIT_TIMEOUT on expiry).
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "attn.h"
 #include "common.cuh"
+#include "own_items.cuh"
+#include "ptx.cuh"
 
 namespace dspark {
 namespace attn {
 namespace tree {
 
+using namespace ptx;
+
 namespace {
 
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kD = 128;
+constexpr int kM = 128;                // query rows of a tile
+constexpr int kHalf = 128 * 128;       // bytes of 64 columns of a [128 x 128] bf16 tile
+constexpr int kTile = 2 * kHalf;
+constexpr int kStages = 5;
+constexpr int kBoxRows = 16;           // block rows of a TMA box
+constexpr int kThreads = 384;
+constexpr int kKvWarp = 0, kMmaWarp = 1, kLookWarp = 2, kQWarp = 3, kSoftmaxWarp = 4;
+constexpr int kFlags = 8;
+// TMEM columns
+constexpr int kTmemS = 0, kTmemO = 256;
 
-__global__ void __launch_bounds__(128)
-    verify_attn_tree_kernel(const __nv_bfloat16* __restrict__ q,
-                            const __nv_bfloat16* __restrict__ k_new,
-                            const __nv_bfloat16* __restrict__ v_new,
-                            const __nv_bfloat16* __restrict__ k_cache,
-                            const __nv_bfloat16* __restrict__ v_cache, int n_pages,
-                            const int32_t* __restrict__ page_table, int max_pages,
-                            const int32_t* __restrict__ ctx_len, const int32_t* __restrict__ cu, int B,
-                            int max_rows, const uint64_t* __restrict__ mask, int words, int Hq,
-                            int Hkv, int page_size, float scale, __nv_bfloat16* __restrict__ out,
-                            float* __restrict__ lse, unsigned int* __restrict__ err) {
-  pdl_release();
-  pdl_wait();
-  const int row = blockIdx.x, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (cu[B] > max_rows || cu[B] < 0) {
-    if (row == 0 && h == 0 && lane == 0) raise_error(err, DSPARK_DEVERR_ROWS_OVERFLOW);
-    return;
-  }
-  bool bad = false;
-  for (int r = threadIdx.x; r < B; r += blockDim.x) {
-    const long long n = (long long)cu[r + 1] - cu[r];
-    bad |= cu[r] < 0 || n < 0 || ctx_len[r] < 0 || ctx_len[r] + n > 0x7fffffffll - 768;
-  }
-  if (__syncthreads_or(bad)) {
-    if (row == 0 && threadIdx.x == 0) raise_error(err, DSPARK_DEVERR_BAD_INPUT);
-    return;
-  }
-  if (h >= Hq || row >= cu[B] || row < cu[0]) return;
-  const int r = upper_segment(cu, B, row);
-  const int c0 = cu[r], n = cu[r + 1] - c0, ctx = ctx_len[r];
-  const int kvh = h / (Hq / Hkv);
-  auto four = [](const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-  };
-  const float4 x = four(q + ((long long)row * Hq + h) * kD + 4 * lane);
-  float top = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto key = [&](const __nv_bfloat16* kp, const __nv_bfloat16* vp) {
-    const float4 k = four(kp + 4 * lane);
-    float s = x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= scale;
-    const float4 v = four(vp + 4 * lane);
-    const float next = fmaxf(top, s);
-    const float fall = top == next ? 1.f : expf(top - next);
-    const float w = next == -INFINITY ? 0.f : expf(s - next);
-    top = next;
-    sum = sum * fall + w;
-    o.x = o.x * fall + w * v.x;
-    o.y = o.y * fall + w * v.y;
-    o.z = o.z * fall + w * v.z;
-    o.w = o.w * fall + w * v.w;
-  };
-  for (int t = 0; t < ctx; ++t) {
-    const int page = page_table[(long long)r * max_pages + t / page_size];
-    if (page < 0 || page >= n_pages) {
-      if (lane == 0) raise_error(err, DSPARK_DEVERR_BAD_INPUT);
-      continue;
+struct Smem {  // the first 3 KB; then Q (two tiles) and the ring
+  uint64_t full[kStages], empty[kStages], looked[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free, joined;
+  uint32_t tmem;
+  int abort;
+  int special[kFlags];                 // by item: block rows held NaN or infinities
+  float ml[2][kM][2];                  // (reference, sum) of a stream's rows at an item's end
+  AttnItem items[4];
+};
+constexpr int kHead = 3072;
+static_assert(sizeof(Smem) <= kHead, "head of the shared memory");
+constexpr int kSmemBytes = kHead + 2 * kTile + kStages * kTile;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(sizeof(ItemScratch) <= kStages * kTile, "scratch in the ring");
+
+struct Params {
+  const __nv_bfloat16* v_new;
+  const int32_t* page_table;
+  const int32_t *ctx_len, *cu_seqlens;
+  const uint64_t* mask;
+  AttnItem* items;
+  SplitGroup* groups;
+  __nv_bfloat16* out;
+  float *lse, *ws_o, *ws_lse;
+  unsigned int* err;
+  int Hq, Hkv, log2_page, max_pages, n_pages, words;
+  int B, max_rows, rows_per_tile, max_splits;
+  int tile_rows;        // block rows of one query tile; rows_per_tile is this or twice this
+  int slot_rows;
+  float sl2;            // scale * log2(e)
+};
+
+struct Ctx {
+  volatile int* abort;
+  unsigned int* err;
+};
+
+// Bounded wait of a warp, its lanes agreeing on the outcome.
+__device__ __forceinline__ bool wait(uint64_t& b, uint32_t parity, const Ctx& cx) {
+  const uint32_t bar = smem_addr(&b);
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait_sleep(bar, parity, 20000))) {
+      if (*cx.abort) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *cx.abort = 1;
+        raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
+        break;
+      }
     }
-    const long long at = (((long long)page * page_size + t % page_size) * Hkv + kvh) * kD;
-    key(k_cache + at, v_cache + at);
   }
-  for (int j = 0; j < min(n, 64 * words); ++j) {
-    if (!(mask[(long long)row * words + (j >> 6)] >> (j & 63) & 1)) continue;
-    const long long at = ((long long)(c0 + j) * Hkv + kvh) * kD;
-    key(k_new + at, v_new + at);
+  return __all_sync(0xffffffffu, ok);
+}
+// The same by one thread, for copies in flight at the end, whatever the abort flag says.
+__device__ __forceinline__ void drain(uint64_t& b, uint32_t parity, unsigned int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(smem_addr(&b), parity, 20000))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_error(err, DSPARK_DEVERR_WAIT_TIMEOUT);
+      return;
+    }
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fused multiply-adds, or two additions, in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+// No use of a pending tmem load's registers is scheduled before the wait that this follows.
+template <int N>
+__device__ __forceinline__ void tie(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ AttnItem fetch(const Smem& S, const AttnItem* more, int it) {
+  return it < 4 ? S.items[it] : more[it];
+}
+__device__ __forceinline__ int visible(int t, int ct, const AttnItem& x) {
+  return min(t < ct ? x.ctx - t * kKT : x.n_r - (t - ct) * kKT, kKT);
+}
+// Does the V tile want looking over?
+__device__ __forceinline__ bool looked_over(int t, int ct, int vis) { return t >= ct || (vis & 15); }
+
+// After the outputs of query row n (block row b) of an item: the NaN and infinities of the values
+// that it sees among the block rows of the item's tiles, in channels c0 .. c1 - 1.
+__device__ __noinline__ void write_specials(const Params& p, const AttnItem& x, int n, int row,
+                                            int c0, int c1) {
+  const int ct = ceil_div(x.ctx, kKT), G = p.Hq / p.Hkv;
+  const int b0 = max(x.tb - ct, 0) * kKT, b1 = min(min((x.te - ct) * kKT, x.n_r), 64 * p.words);
+  const uint64_t* m = p.mask + (long long)row * p.words;
+  const __nv_bfloat16* v = p.v_new + ((long long)x.c0 * p.Hkv + x.kvh) * kD;
+  const long long step = (long long)p.Hkv * kD;
+  for (int c = c0; c < c1; ++c) {
+    float add = 0.f;
+    for (int j = b0; j < b1; ++j) {
+      if (!(m[j >> 6] >> (j & 63) & 1)) continue;
+      const float f = __bfloat162float(v[j * step + c]);
+      if (!(fabsf(f) <= 3.4e38f)) add += f;
+    }
+    if (add == 0.f) continue;
+    if (x.nsplit > 1) {
+      float* o = p.ws_o + ((long long)x.slot * p.slot_rows + n) * kD + c;
+      *o += add;
+    } else {
+      __nv_bfloat16* o = p.out + ((long long)row * p.Hq + x.kvh * G + n % G) * kD + c;
+      *o = __float2bfloat16(__bfloat162float(*o) + add);
+    }
   }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    verify_attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ CUtensorMap tm_kn,
+                            const __grid_constant__ CUtensorMap tm_vn, const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Smem& S = *reinterpret_cast<Smem*>(smem);
+  const uint32_t q_base = smem_addr(smem) + kHead, ring = q_base + 2 * kTile;
+  const Ctx cx{&S.abort, p.err};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    S.abort = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&S.full[i]), 1);
+      mbar_init(smem_addr(&S.empty[i]), 2);  // the products and the look
+      mbar_init(smem_addr(&S.looked[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&S.q_full[i]), 1);
+      mbar_init(smem_addr(&S.q_empty[i]), 1);
+      mbar_init(smem_addr(&S.s_full[i]), 1);
+      mbar_init(smem_addr(&S.p_full[i]), 4);
+      mbar_init(smem_addr(&S.pv_done[i]), 1);
+    }
+    mbar_init(smem_addr(&S.o_free), 8);
+    mbar_init(smem_addr(&S.joined), 8);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < kFlags) S.special[threadIdx.x] = 0;
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&S.tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_release();
+  pdl_wait();  // inputs come from the kernels before this one
+  const OwnItems own =
+      own_items<kThreads, 4>(p, *reinterpret_cast<ItemScratch*>(smem + kHead + 2 * kTile), S.items);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  const int G = p.Hq / p.Hkv;
+
+  if (warp == kKvWarp) {
+    // ------------------------------------------------------------- K and V
+    const int lp = p.log2_page, P = 1 << lp, box = min(P, kKT);
+    int g = 0;  // slots filled
+    bool ok = true;
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT);
+      const int32_t* tab = p.page_table + (long long)x.r * p.max_pages;
+      // lane j holds the page of slot win + j
+      int win = -1, page_of = 0;
+      for (int t = x.tb; t < x.te && ok; ++t) {
+        const int vis = visible(t, ct, x);
+        const int rows = t < ct ? box : kBoxRows, nb = ceil_div(vis, rows);
+        if (t < ct) {
+          const int s0 = (int)(((long long)t * kKT) >> lp), ns = ceil_div(kKT, P);
+          if (win < 0 || s0 + ns > win + 32) {
+            win = s0;
+            const long long first = (long long)(win + lane) << lp;
+            int pg = 0;
+            if (first < x.ctx) {
+              pg = win + lane < p.max_pages ? tab[win + lane] : -1;
+              // (a page that no cache holds: its keys read as zero)
+              if (pg < 0 || pg >= p.n_pages) {
+                raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
+                pg = p.n_pages;
+              }
+            }
+            page_of = pg;
+          }
+        }
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+          const int slot = g % kStages;
+          if (g >= kStages && !wait(S.empty[slot], (g / kStages - 1) & 1, cx)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
+          if (lane == 0) mbar_arrive_expect_tx(bar, nb * 2 * rows * 128);
+          __syncwarp();
+          for (int o0 = 0; o0 < 2 * nb; o0 += 32) {
+            const int o = o0 + lane, bx = o >> 1, half = o & 1;
+            const uint32_t to = dst + half * kHalf + bx * rows * 128;
+            const int at = t * kKT + bx * rows;  // (of a cache tile: below ctx for bx < nb)
+            const int page = __shfl_sync(0xffffffffu, page_of, bx < nb ? ((at >> lp) - win) & 31 : 0);
+            if (bx < nb) {
+              if (t < ct)
+                tma_load_4d(to, kv ? &tm_v : &tm_k, bar, half * 64, x.kvh, at & (P - 1), page);
+              else
+                tma_load_3d(to, kv ? &tm_vn : &tm_kn, bar, half * 64, x.kvh,
+                            x.c0 + (t - ct) * kKT + bx * kBoxRows);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0)
+      for (int i = max(0, g - kStages); i < g; ++i) drain(S.full[i % kStages], (i / kStages) & 1, p.err);
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------- Q
+    const int rpt = p.tile_rows;
+    const uint32_t bytes = (uint32_t)rpt * G * 256;
+    int used[2] = {0, 0}, turn = 0;
+    bool ok = true;
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const bool two = x.ni > rpt;
+      for (int k = 0; k < (two ? 2 : 1); ++k) {
+        const int b = two ? k : turn;
+        const int u = b ? used[1] : used[0];
+        if (u > 0 && !wait(S.q_empty[b], (u - 1) & 1, cx)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&S.q_full[b]);
+          mbar_arrive_expect_tx(bar, bytes);
+          for (int half = 0; half < 2; ++half)
+            tma_load_3d(q_base + b * kTile + half * kHalf, &tm_q, bar, half * 64, x.kvh * G,
+                        x.c0 + x.i0 + k * rpt);
+        }
+        __syncwarp();
+        if (b) ++used[1]; else ++used[0];
+      }
+      if (!two) turn ^= 1;
+    }
+    if (lane == 0)
+      for (int b = 0; b < 2; ++b) {
+        const int u = b ? used[1] : used[0];
+        if (u > 0) drain(S.q_full[b], (u - 1) & 1, p.err);
+      }
+  } else if (warp == kLookWarp) {
+    // ------------------------------------------------------------- V tiles looked over
+    int g = 0;  // key tiles
+    bool ok = true;
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT);
+      if (lane == 0) S.special[it % kFlags] = 0;
+      __syncwarp();
+      for (int t = x.tb; t < x.te; ++t, ++g) {
+        // every fill is waited for, in order: a barrier that is not followed step by step shows
+        // a phase of the same parity
+        const int vis = visible(t, ct, x), i = 2 * g + 1, slot = i % kStages;
+        ok = wait(S.full[(i - 1) % kStages], ((i - 1) / kStages) & 1, cx);
+        if (ok && lane == 0) mbar_arrive(smem_addr(&S.empty[(i - 1) % kStages]));
+        if (!ok || !(ok = wait(S.full[slot], (i / kStages) & 1, cx))) break;
+        if (!looked_over(t, ct, vis)) {
+          if (lane == 0) mbar_arrive(smem_addr(&S.empty[slot]));
+          continue;
+        }
+        uint8_t* v = smem + kHead + 2 * kTile + slot * kTile;
+        bool odd = false;
+        if (t >= ct) {
+          // rows 0 .. vis - 1, 16 bytes (row, piece) a lane and step, in both halves
+          for (int o = lane; o < vis * 8; o += 32) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint4* at = reinterpret_cast<uint4*>(v + half * kHalf + o * 16);
+              uint4 u = *at;
+              // an exponent of ones carries into the bit above it
+              const uint32_t ones = (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                                     ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
+                                    0x80008000u;
+              if (ones) {
+                odd = true;
+                auto clear = [](uint32_t w) {
+                  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+                  return w;
+                };
+                *at = make_uint4(clear(u.x), clear(u.y), clear(u.z), clear(u.w));
+              }
+            }
+          }
+        }
+        // rows vis .. the end of their chunk of 16
+        const int nz = (-vis & 15) * 8;
+        for (int o = lane; o < 2 * nz; o += 32) {
+          const int half = o >= nz, k = o - (half ? nz : 0);
+          *reinterpret_cast<uint4*>(v + half * kHalf + (vis * 8 + k) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        if (odd) S.special[it % kFlags] = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&S.looked[slot]));
+          mbar_arrive(smem_addr(&S.empty[slot]));
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- products
+    constexpr uint32_t kQk = idesc_bf16_f32(kM, kKT, 0, 0), kPv = idesc_bf16_f32(kM, kD, 0, 1);
+    struct Pending {       // a stream's product P V that is still to be issued
+      int item, slot_use;  // item -1: none; slot_use: index of V's fill
+      int nch;
+      bool first, look, wait_v, release;
+    };
+    Pending pend[2] = {{-1, 0, 0, false, false, false, false}, {-1, 0, 0, false, false, false, false}};
+    int nv[2] = {0, 0};    // tiles of a stream so far
+    int used[2] = {0, 0}, turn = 0, g = 0;
+    uint32_t look_phase = 0;  // bit: the slot's next phase of `looked`
+    bool ok = true;
+    auto flush = [&](int s) -> bool {
+      Pending& w = pend[s];
+      if (w.item < 0) return true;
+      if (w.first && w.item > 0 && !wait(S.o_free, (w.item - 1) & 1, cx)) return false;
+      const int slot = w.slot_use % kStages;
+      if (w.wait_v) {  // (of two streams that share V the first waits)
+        if (w.look) {
+          if (!wait(S.looked[slot], look_phase >> slot & 1, cx)) return false;
+          look_phase ^= 1u << slot;
+        }
+        if (!wait(S.full[slot], (w.slot_use / kStages) & 1, cx)) return false;
+      }
+      if (!wait(S.p_full[s], (nv[s] - 1) & 1, cx)) return false;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t v = ring + slot * kTile, o = tmem + kTmemO + s * 128;
+        for (int k = 0; k < w.nch; ++k)
+          umma_bf16_ts(o, tmem + kTmemS + s * 128 + k * 8, smem_desc(v + k * 2048, kHalf, 1024, SW_128B),
+                       kPv, (w.first && k == 0) ? 0u : 1u);
+        umma_commit(smem_addr(&S.pv_done[s]));
+        if (w.release) umma_commit(smem_addr(&S.empty[slot]));
+      }
+      __syncwarp();
+      w.item = -1;
+      return true;
+    };
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
+      const bool two = x.ni > p.tile_rows;
+      const int nvt = two ? 2 * nt : nt;
+      for (int vt = 0; vt < nvt; ++vt) {
+        const int s = vt & 1, k = two ? vt >> 1 : vt, t = x.tb + k, gk = 2 * (g + k);
+        const int qb = two ? s : turn;
+        if (!flush(s)) { ok = false; break; }
+        if (vt < (two ? 2 : 1) && !wait(S.q_full[qb], (qb ? used[1] : used[0]) & 1, cx)) { ok = false; break; }
+        const int slot = gk % kStages;
+        if ((!two || s == 0) && !wait(S.full[slot], (gk / kStages) & 1, cx)) { ok = false; break; }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t q = q_base + qb * kTile, kb = ring + slot * kTile;
+#pragma unroll
+          for (int d = 0; d < kD / 16; ++d)
+            umma_bf16(tmem + kTmemS + s * 128,
+                      smem_desc(q + (d >> 2) * kHalf + (d & 3) * 32, 16, 1024, SW_128B),
+                      smem_desc(kb + (d >> 2) * kHalf + (d & 3) * 32, 16, 1024, SW_128B), kQk,
+                      d > 0 ? 1u : 0u);
+          umma_commit(smem_addr(&S.s_full[s]));
+          if (!two || s == 1) umma_commit(smem_addr(&S.empty[slot]));
+          if (two ? k == nt - 1 : vt == nvt - 1) umma_commit(smem_addr(&S.q_empty[qb]));
+        }
+        __syncwarp();
+        const int vis = visible(t, ct, x);
+        ++nv[s];
+        pend[s] = {it, gk + 1, ceil_div(vis, 16), two ? k == 0 : vt < 2, looked_over(t, ct, vis),
+                   !two || s == 0, !two || s == 1};
+        // the next item may not come to the other stream at all
+        if (nvt == 1 && !flush(1)) { ok = false; break; }
+      }
+      if (two) {
+        ++used[0];
+        ++used[1];
+      } else {
+        if (turn) ++used[1]; else ++used[0];
+        turn ^= 1;
+      }
+      g += nt;
+    }
+    // (in the order of their slots)
+    if (ok) {
+      const int s0 = pend[1].item >= 0 && (pend[0].item < 0 || pend[1].slot_use < pend[0].slot_use) ? 1 : 0;
+      ok = flush(s0);
+      if (ok) ok = flush(s0 ^ 1);
+    }
+    if (lane == 0) {
+      // whatever was issued completes before the memory is given back
+      for (int s = 0; s < 2; ++s)
+        if (nv[s] > 0) {
+          drain(S.s_full[s], (nv[s] - 1) & 1, p.err);
+          const int done = nv[s] - (pend[s].item >= 0 ? 1 : 0);
+          if (done > 0) drain(S.pv_done[s], (done - 1) & 1, p.err);
+        }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax / epilogue
+    const int sw = warp & 3, s = (warp - kSoftmaxWarp) >> 2;
+    const int n = sw * 32 + lane;  // row of the tile
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(sw * 32) << 16);
+    const uint32_t t_s = t_lane + kTmemS + s * 128, t_o = t_lane + kTmemO + s * 128;
+    const float sl2 = p.sl2;
+    int nv[2] = {0, 0}, joins = 0;
+    bool ok = true;
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb, rpt = p.tile_rows;
+      const bool two = x.ni > rpt;
+      const int first_row = two && s ? rpt : 0;                       // of the item's rows
+      const int nq = (min(x.ni, first_row + rpt) - first_row) * G;    // rows of this tile
+      const bool warp_live = sw * 32 < nq, live = n < nq;
+      const int row = x.c0 + x.i0 + first_row + min(n, nq - 1) / G;   // packed row
+      const uint32_t* mrow = reinterpret_cast<const uint32_t*>(p.mask + (long long)row * p.words);
+      const int mine = two ? nt : (nt + 1 - s) >> 1;                  // key tiles of this stream
+      float ref = -INFINITY, sum = 0.f;
+      for (int k = 0; k < mine; ++k) {
+        const int t = x.tb + (two ? k : 2 * k + s);
+        const int c = (s ? nv[1] : nv[0]) + k;
+        if (!wait(S.s_full[s], c & 1, cx)) { ok = false; break; }
+        if (warp_live) {
+          tc_fence_after();
+          float v[128];
+          {
+            float(&v0)[32] = reinterpret_cast<float(&)[32]>(v[0]);
+            float(&v1)[32] = reinterpret_cast<float(&)[32]>(v[32]);
+            float(&v2)[32] = reinterpret_cast<float(&)[32]>(v[64]);
+            float(&v3)[32] = reinterpret_cast<float(&)[32]>(v[96]);
+            tmem_ld32(t_s, v0);
+            tmem_ld32(t_s + 32, v1);
+            tmem_ld32(t_s + 64, v2);
+            tmem_ld32(t_s + 96, v3);
+            tmem_wait_ld();
+            tie(v);
+          }
+          const int vis = visible(t, ct, x);
+          if (t >= ct) {
+            // bits of the tile's 128 block rows, none past the segment or the mask's words
+            const int w0 = (t - ct) * 4;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t bits = w0 + w < 2 * p.words ? mrow[w0 + w] : 0u;
+              const int left = vis - 32 * w;
+              if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[32 * w + j] = (bits >> j & 1) ? v[32 * w + j] : -INFINITY;
+            }
+          } else if (vis < kKT) {
+#pragma unroll
+            for (int j = 0; j < kKT; ++j) v[j] = j < vis ? v[j] : -INFINITY;
+          }
+          float top = v[0];
+#pragma unroll
+          for (int j = 1; j < kKT; ++j) top = fmaxf(top, v[j]);
+          top *= sl2;
+          const bool move = top > ref + 8.f;  // (from -inf: any key)
+          const float alpha = move && ref != -INFINITY ? fast_exp2(ref - top) : 1.f;
+          if (move) {
+            ref = top;
+            sum *= alpha;
+          }
+          if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O has the products up to the last tile once that is done
+            if (!wait(S.pv_done[s], (c - 1) & 1, cx)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < kD; d += 16) {
+              float o[16];
+              tmem_ld16(t_o + d, o);
+              tmem_wait_ld16(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= alpha;
+              tmem_st16(t_o + d, o);
+            }
+          }
+          const float base = ref == -INFINITY ? 0.f : ref;
+          const float2 f = make_float2(sl2, sl2), b = make_float2(-base, -base);
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 e = fma2(make_float2(v[32 * q + 2 * j], v[32 * q + 2 * j + 1]), f, b);
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
+              if (j & 1) acc1 = add2(acc1, e); else acc0 = add2(acc0, e);
+              pk[j] = pack_bf16(e.x, e.y);
+            }
+            tmem_st16u(t_s + 16 * q, pk);
+          }
+          acc0 = add2(acc0, acc1);
+          sum += acc0.x + acc0.y;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&S.p_full[s]));
+      }
+      if (!ok) break;
+      nv[0] += two ? nt : (nt + 1) >> 1;
+      nv[1] += two ? nt : nt >> 1;
+      // ---- epilogue: this stream's tile, or half the columns of both streams' sums
+      if (two || s == 0 || nt > 1) ok = wait(S.pv_done[s], ((s ? nv[1] : nv[0]) - 1) & 1, cx);
+      if (!two && ok && (s == 1 || nt > 1))
+        ok = wait(S.pv_done[s ^ 1], ((s ? nv[0] : nv[1]) - 1) & 1, cx);
+      if (!ok) break;
+      if (!two) {
+        // (the last item's numbers are read: its O was given back before the products waited for)
+        S.ml[s][n][0] = ref;
+        S.ml[s][n][1] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&S.joined));
+        ok = wait(S.joined, joins & 1, cx);
+        ++joins;
+        if (!ok) break;
+      }
+      float w0 = 1.f, w1 = 0.f;  // weights of this stream's O and the other's
+      if (!two) {
+        const float r1 = S.ml[s ^ 1][n][0], s1 = S.ml[s ^ 1][n][1];
+        const float r = fmaxf(ref, r1);
+        w0 = ref == -INFINITY ? 0.f : fast_exp2(ref - r);
+        w1 = r1 == -INFINITY ? 0.f : fast_exp2(r1 - r);
+        if (sum != sum || s1 != s1) w0 = w1 = sum + s1;  // (NaN)
+        sum = sum * w0 + s1 * w1;
+        ref = r;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const bool split = x.nsplit > 1;
+      const int nn = first_row * G + n;                                 // row of the item
+      const int head = x.kvh * G + n % G;
+      if (warp_live) {
+        tc_fence_after();
+        w0 *= inv;
+        w1 *= inv;
+        const int d0 = two ? 0 : 64 * s, d1 = two ? kD : d0 + 64;
+        const uint32_t t_other = t_lane + kTmemO + (s ^ 1) * 128;
+#pragma unroll 1
+        for (int d = d0; d < d1; d += 32) {
+          float o[32];
+          tmem_ld32(t_o + d, o);
+          tmem_wait_ld();
+          tie(o);
+          if (two) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= w0;
+          } else {
+            float u[32];
+            tmem_ld32(t_other + d, u);
+            tmem_wait_ld();
+            tie(u);
+            // (a stream without keys has no sums, whatever its columns hold)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = (w0 == 0.f ? 0.f : o[j] * w0) + (w1 == 0.f ? 0.f : u[j] * w1);
+          }
+          if (live) {
+            if (split) {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + ((long long)x.slot * p.slot_rows + nn) * kD + d);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + ((long long)row * p.Hq + head) * kD + d);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                    pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+            }
+          }
+        }
+        if (live && (two || s == 0)) {
+          const float l = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994530942f;
+          if (split) p.ws_lse[(long long)x.slot * p.slot_rows + nn] = l;
+          else p.lse[(long long)row * p.Hq + head] = l;
+        }
+        if (live && *(volatile int*)&S.special[it % kFlags]) write_specials(p, x, nn, row, d0, d1);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&S.o_free));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- split combine
+// Block (c, y): the split group recorded by CTA c, query rows 8y .. 8y + 7, a warp per row:
+//   lse = log sum_s e^{lse_s},  o = sum_s e^{lse_s - lse} o_s
+__global__ void __launch_bounds__(256)
+    combine_tree_kernel(const int32_t* __restrict__ cu_seqlens, const SplitGroup* __restrict__ groups,
+                        int G, int Hq, int slot_rows, const float* __restrict__ ws_o,
+                        const float* __restrict__ ws_lse, __nv_bfloat16* __restrict__ out,
+                        float* __restrict__ lse) {
+  pdl_release();
+  pdl_wait();  // inputs come from the kernels before this one
+  const int lane = threadIdx.x & 31;
+  const SplitGroup sg = groups[blockIdx.x];
+  const int ns = sg.nsplit;
+  const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (ns <= 1 || n >= sg.ni * G) return;
+  // piece s is in slot 2 (c_first + s), but for a first piece that is not its CTA's first
+  auto slot = [&](int s) {
+    return (long long)(2 * (sg.c_first + s) + (s == 0 && sg.slot0_last ? 1 : 0)) * slot_rows + n;
+  };
+  float mx = -INFINITY;
+  for (int s = lane; s < ns; s += 32) mx = fmaxf(mx, ws_lse[slot(s)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    // (a piece in which the row sees no key weighs nothing)
+    const float l = s0 + lane < ns ? ws_lse[slot(s0 + lane)] : -INFINITY;
+    const float wgt = l == -INFINITY ? 0.f : expf(l - mx);
+    sum += wgt;
+    const int m = min(32, ns - s0);
+#pragma unroll 4
+    for (int s = 0; s < m; ++s) {
+      const float w = __shfl_sync(0xffffffffu, wgt, s);
+      const float4 v = reinterpret_cast<const float4*>(ws_o + slot(s0 + s) * kD)[lane];
+      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst = out + ((long long)row * Hq + h) * kD + 4 * lane;
-  dst[0] = __float2bfloat16(o.x * inv);
-  dst[1] = __float2bfloat16(o.y * inv);
-  dst[2] = __float2bfloat16(o.z * inv);
-  dst[3] = __float2bfloat16(o.w * inv);
-  if (lane == 0) lse[(long long)row * Hq + h] = top + logf(sum);
+  const long long row = cu_seqlens[sg.r] + sg.i0 + n / G;
+  const int head = sg.kvh * G + n % G;
+  reinterpret_cast<uint2*>(out + (row * Hq + head) * kD)[lane] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) lse[row * Hq + head] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+// ---------------------------------------------------------------- host side
+struct TreePlan {
+  int tile_rows, rows_per_tile, slot_rows, ncta;
+  size_t off_items, off_groups, off_o, off_lse, bytes;
+};
+
+TreePlan plan(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
+  TreePlan p{};
+  const int G = Hq / Hkv;
+  p.tile_rows = kM / G;
+  // Two query tiles to an item wherever a segment may need them: they share the keys.
+  const int tiles = (max_block_rows > 0 ? max_block_rows : 1) > p.tile_rows ? 2 : 1;
+  p.rows_per_tile = tiles * p.tile_rows;
+  p.slot_rows = tiles * kM;
+  p.ncta = num_sms_cached();
+  if (p.ncta > kMaxCtas) p.ncta = kMaxCtas;
+  const long long items = (long long)Hkv * ((long long)max_rows / p.rows_per_tile + B) + p.ncta;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) & ~size_t(255);
+    return at;
+  };
+  p.off_items = take(sizeof(AttnItem) * (size_t)items);
+  p.off_groups = take(sizeof(SplitGroup) * (size_t)p.ncta);
+  p.off_o = take(sizeof(float) * (size_t)2 * p.ncta * p.slot_rows * kD);  // slots 2c, 2c + 1
+  p.off_lse = take(sizeof(float) * (size_t)2 * p.ncta * p.slot_rows);
+  p.bytes = off;
+  return p;
 }
 
 }  // namespace
 
-size_t workspace(int, int, int, int, int) { return 256; }
+size_t workspace(int B, int max_rows, int Hq, int Hkv, int max_block_rows) {
+  return plan(B, max_rows, Hq, Hkv, max_block_rows).bytes;
+}
 
 int launch(const void* q, const void* k_new, const void* v_new, const void* k_cache,
            const void* v_cache, int n_pages, const int32_t* page_table, int max_pages,
-           const int32_t* ctx_len, const int32_t* cu, const uint64_t* mask, int words, int B,
-           int max_rows, int Hq, int Hkv, int page_size, float scale, int, int, void* out,
-           float* lse, void*, cudaStream_t stream) {
-  using bf = __nv_bfloat16;
-  return launch_pdl(verify_attn_tree_kernel, dim3(max_rows, ceil_div(Hq, 4)), dim3(128), 0, stream,
-                    static_cast<const bf*>(q), static_cast<const bf*>(k_new),
-                    static_cast<const bf*>(v_new), static_cast<const bf*>(k_cache),
-                    static_cast<const bf*>(v_cache), n_pages, page_table, max_pages, ctx_len, cu, B,
-                    max_rows, mask, words, Hq, Hkv, page_size, scale, static_cast<bf*>(out), lse,
-                    device_error_word()) == cudaSuccess
+           const int32_t* ctx_len, const int32_t* cu_seqlens, const uint64_t* mask, int words, int B,
+           int max_rows, int Hq, int Hkv, int page_size, float scale, int max_splits,
+           int max_block_rows, void* out, float* lse, void* ws, cudaStream_t stream) {
+  const TreePlan pl = plan(B, max_rows, Hq, Hkv, max_block_rows);
+  const int G = Hq / Hkv;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Params p;
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.page_table = page_table;
+  p.ctx_len = ctx_len;
+  p.cu_seqlens = cu_seqlens;
+  p.mask = mask;
+  p.items = reinterpret_cast<AttnItem*>(w + pl.off_items);
+  p.groups = reinterpret_cast<SplitGroup*>(w + pl.off_groups);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.ws_o = reinterpret_cast<float*>(w + pl.off_o);
+  p.ws_lse = reinterpret_cast<float*>(w + pl.off_lse);
+  p.err = device_error_word();
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.log2_page = 0;
+  while ((1 << p.log2_page) < page_size) ++p.log2_page;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.words = words;
+  p.B = B;
+  p.max_rows = max_rows;
+  p.rows_per_tile = pl.rows_per_tile;
+  // five times as many pieces as asked for, so that 32 reach every SM with one long group
+  p.max_splits = max_splits < 2 ? 2 : 5 * max_splits;
+  p.tile_rows = pl.tile_rows;
+  p.slot_rows = pl.slot_rows;
+  p.sl2 = scale * 1.4426950408889634f;
+
+  CUtensorMap tq, tk, tv, tkn, tvn;
+  {
+    const uint64_t dims[3] = {kD, (uint64_t)Hq, (uint64_t)max_rows};
+    const uint64_t st[2] = {kD * 2, (uint64_t)Hq * kD * 2};
+    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)pl.tile_rows};
+    if (!gqa::encode_bf16_map(&tq, q, 3, dims, st, box)) return DSPARK_ECUDA;
+  }
+  {
+    const uint64_t dims[4] = {kD, (uint64_t)Hkv, (uint64_t)page_size, (uint64_t)n_pages};
+    const uint64_t st[3] = {kD * 2, (uint64_t)Hkv * kD * 2, (uint64_t)page_size * Hkv * kD * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)(page_size < kKT ? page_size : kKT), 1};
+    if (!gqa::encode_bf16_map(&tk, k_cache, 4, dims, st, box)) return DSPARK_ECUDA;
+    if (!gqa::encode_bf16_map(&tv, v_cache, 4, dims, st, box)) return DSPARK_ECUDA;
+  }
+  {
+    const uint64_t dims[3] = {kD, (uint64_t)Hkv, (uint64_t)max_rows};
+    const uint64_t st[2] = {kD * 2, (uint64_t)Hkv * kD * 2};
+    const uint32_t box[3] = {64, 1, kBoxRows};
+    if (!gqa::encode_bf16_map(&tkn, k_new, 3, dims, st, box)) return DSPARK_ECUDA;
+    if (!gqa::encode_bf16_map(&tvn, v_new, 3, dims, st, box)) return DSPARK_ECUDA;
+  }
+  static PerDevice<bool> done;
+  if (!once_per_device(done, false, [] {
+        return cudaFuncSetAttribute(verify_attn_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemBytes) == cudaSuccess;
+      }))
+    return DSPARK_ECUDA;
+  if (launch_pdl(verify_attn_tree_kernel, dim3(pl.ncta), dim3(kThreads), kSmemBytes, stream, tq, tk, tv,
+                 tkn, tvn, p) != cudaSuccess)
+    return DSPARK_ECUDA;
+  return launch_pdl(combine_tree_kernel, dim3(pl.ncta, pl.slot_rows / 8), dim3(256), 0, stream,
+                    cu_seqlens, p.groups, G, Hq, pl.slot_rows, p.ws_o, p.ws_lse, p.out,
+                    lse) == cudaSuccess
              ? DSPARK_OK
              : DSPARK_ECUDA;
 }

@@ -14,13 +14,11 @@
 // stream's softmax runs beside the other's products whether there are two tiles or one.
 //
 // Warps (one CTA an SM, persistent over its share of the key tiles, see own_items.cuh):
-//   0      K and V: TMA (128-byte swizzle) into a ring of five 32 KB slots, in the order K V K V
-//   1      issues the products: O += P V of a stream's last tile, then S of its next
-//   2      looks over the V tiles that need it: block rows, and the context's last tile.  Rows past
-//          the visible keys become zero; so do NaN and infinities of block rows, since a row that
-//          does not see them weighs them 0, and 0 times them is NaN: the rows that do see them get
-//          them after the epilogue (write_specials)
-//   3      Q: TMA, the tile's rows as they lie
+//   0      K and Q, 2  V: TMA (128-byte swizzle), K and V into a ring of five 32 KB slots
+//   1, 3   issue the products of one stream each: O += P V of its last tile, then S of its next
+// Warp 2 also looks over its V tiles: keys past the visible ones of a chunk of 16 become zero; so do
+// NaN and infinities of block rows, since a row that does not see them weighs them 0, and 0 times
+// them is NaN: the rows that do see them get them after the epilogue (write_specials).
 //   4-7, 8-11  the softmax of the streams, thread = row: maximum, exponentials and sum of 128 keys
 //          without a word to another thread; O is rescaled only where a row's maximum grows by 2^8
 // Every wait is bounded in time (DSPARK_DEVERR_WAIT_TIMEOUT on expiry).
@@ -51,16 +49,21 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kBoxRows = 16;           // block rows of a TMA box
 constexpr int kThreads = 384;
-constexpr int kKvWarp = 0, kMmaWarp = 1, kLookWarp = 2, kQWarp = 3, kSoftmaxWarp = 4;
+constexpr int kKWarp = 0, kMmaWarp = 1, kVWarp = 2, kSoftmaxWarp = 4;  // 3: the other stream's kMmaWarp
 constexpr int kFlags = 8;
 // TMEM columns
 constexpr int kTmemS = 0, kTmemO = 256;
 
 struct Smem {  // the first 3 KB; then Q (two tiles) and the ring
-  uint64_t full[kStages], empty[kStages], looked[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free, joined;
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], joined;
   uint32_t tmem;
   int abort;
+  // Counts beside the barriers: a barrier shows the parity of a phase only, and not every waiter comes
+  // by at every phase.
+  uint32_t armed[kStages];             // fills of a slot that were begun
+  uint32_t looked[kStages];            // V's last fill of a slot that was looked over, + 1
+  uint32_t epilogues;                  // softmax warps that are done with an item, over all items
   int special[kFlags];                 // by item: block rows held NaN or infinities
   float ml[2][kM][2];                  // (reference, sum) of a stream's rows at an item's end
   AttnItem items[4];
@@ -93,22 +96,62 @@ struct Ctx {
   unsigned int* err;
 };
 
-// Bounded wait of a warp, its lanes agreeing on the outcome.
-__device__ __forceinline__ bool wait(uint64_t& b, uint32_t parity, const Ctx& cx) {
+// Bounded wait of one thread.  (A poll takes 73 cycles, one that may sleep 131, so the first are
+// plain ones.)
+__device__ __forceinline__ bool wait1(uint64_t& b, uint32_t parity, const Ctx& cx) {
   const uint32_t bar = smem_addr(&b);
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!(ok = mbar_try_wait_sleep(bar, parity, 20000))) {
-      if (*cx.abort) break;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *cx.abort = 1;
-        raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
-        break;
-      }
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000)) {
+    if (*cx.abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *cx.abort = 1;
+      raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, ok);
+  return true;
+}
+// Bounded wait of one thread until a count has come to `least`.
+__device__ __forceinline__ bool wait_count(uint32_t& count, uint32_t least, const Ctx& cx) {
+  auto there = [&] {
+    uint32_t c;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(c) : "r"(smem_addr(&count)) : "memory");
+    return (int)(c - least) >= 0;
+  };
+#pragma unroll 1
+  for (int i = 0; i < 1000; ++i)
+    if (there()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!there()) {
+    if (*cx.abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *cx.abort = 1;
+      raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
+}
+__device__ __forceinline__ void set_count(uint32_t& count, uint32_t to) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(&count)), "r"(to) : "memory");
+}
+// Fill g of the ring: its slot is free / its data is there.
+__device__ __forceinline__ bool wait_free(Smem& S, int g, const Ctx& cx) {
+  const int slot = g % kStages, use = g / kStages;
+  return use == 0 || (wait_count(S.armed[slot], use, cx) && wait1(S.empty[slot], (use - 1) & 1, cx));
+}
+__device__ __forceinline__ bool wait_filled(Smem& S, int g, const Ctx& cx) {
+  const int slot = g % kStages, use = g / kStages;
+  return wait_count(S.armed[slot], use + 1, cx) && wait1(S.full[slot], use & 1, cx);
+}
+// wait1 of a warp, its lanes agreeing on the outcome.
+__device__ __forceinline__ bool wait(uint64_t& b, uint32_t parity, const Ctx& cx) {
+  return __all_sync(0xffffffffu, wait1(b, parity, cx));
 }
 // The same by one thread, for copies in flight at the end, whatever the abort flag says.
 __device__ __forceinline__ void drain(uint64_t& b, uint32_t parity, unsigned int* err) {
@@ -141,6 +184,28 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
+// A product whose operands' descriptors share their high word: one thread issues all of them, and
+// what it computes between two is time the tensor cores wait (descriptors built whole: 150 cycles a
+// product, twice what it takes).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // No use of a pending tmem load's registers is scheduled before the wait that this follows.
 template <int N>
 __device__ __forceinline__ void tie(float (&v)[N]) {
@@ -158,8 +223,36 @@ __device__ __forceinline__ AttnItem fetch(const Smem& S, const AttnItem* more, i
 __device__ __forceinline__ int visible(int t, int ct, const AttnItem& x) {
   return min(t < ct ? x.ctx - t * kKT : x.n_r - (t - ct) * kKT, kKT);
 }
-// Does the V tile want looking over?
-__device__ __forceinline__ bool looked_over(int t, int ct, int vis) { return t >= ct || (vis & 15); }
+// An item's fills of the ring, in the order in which the products take them, so that no slot is held
+// longer than need be: two query tiles take K0 V0 K1 V1 .., two streams K0 K1 V0 K2 V1 .. (a
+// stream's P V comes after the other's next S).
+__device__ __forceinline__ int fill_of_k(int k, bool two) { return two ? 2 * k : max(2 * k - 1, 0); }
+__device__ __forceinline__ int fill_of_v(int k, int nt, bool two) {
+  return two ? 2 * k + 1 : k == nt - 1 ? 2 * nt - 1 : 2 * k + 2;
+}
+
+// A warp's window on a request's page table: lane j holds the page of slot first + j.
+struct Pages {
+  int first = -1, page = 0;
+  __device__ __forceinline__ void look_up(const Params& p, const AttnItem& x, int t) {
+    const int lp = p.log2_page, s0 = (int)(((long long)t * kKT) >> lp), ns = max(kKT >> lp, 1);
+    if (first >= 0 && s0 + ns <= first + 32) return;
+    first = s0;
+    const int slot = first + (threadIdx.x & 31);
+    page = 0;
+    if (((long long)slot << lp) < x.ctx) {
+      page = slot < p.max_pages ? p.page_table[(long long)x.r * p.max_pages + slot] : -1;
+      // (a page that no cache holds: its keys read as zero)
+      if (page < 0 || page >= p.n_pages) {
+        raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
+        page = p.n_pages;
+      }
+    }
+  }
+  __device__ __forceinline__ int of(int slot) const {
+    return __shfl_sync(0xffffffffu, page, (slot - first) & 31);
+  }
+};
 
 // After the outputs of query row n (block row b) of an item: the NaN and infinities of the values
 // that it sees among the block rows of the item's tiles, in channels c0 .. c1 - 1.
@@ -202,19 +295,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     S.abort = 0;
+    S.epilogues = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&S.full[i]), 1);
-      mbar_init(smem_addr(&S.empty[i]), 2);  // the products and the look
-      mbar_init(smem_addr(&S.looked[i]), 1);
+      mbar_init(smem_addr(&S.empty[i]), 2);  // the products of both streams
+      S.armed[i] = S.looked[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&S.q_full[i]), 1);
-      mbar_init(smem_addr(&S.q_empty[i]), 1);
+      mbar_init(smem_addr(&S.q_empty[i]), 2);
       mbar_init(smem_addr(&S.s_full[i]), 1);
       mbar_init(smem_addr(&S.p_full[i]), 4);
       mbar_init(smem_addr(&S.pv_done[i]), 1);
     }
-    mbar_init(smem_addr(&S.o_free), 8);
     mbar_init(smem_addr(&S.joined), 8);
     fence_mbar_init();
   }
@@ -232,132 +325,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   const int G = p.Hq / p.Hkv;
-
-  if (warp == kKvWarp) {
-    // ------------------------------------------------------------- K and V
-    const int lp = p.log2_page, P = 1 << lp, box = min(P, kKT);
-    int g = 0;  // slots filled
+  // 384 threads of 168 registers: 128 x 104 + 256 x 200
+  if (warp < kSoftmaxWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp == kKWarp) {
+    // ------------------------------------------------------------- K and Q
+    const int lp = p.log2_page, rpt = p.tile_rows;
+    int g0 = 0;                                  // fills of the items before
+    int used0 = 0, used1 = 0, turn = 0;          // Q tiles loaded, the buffer of the next single one
     bool ok = true;
     for (int it = 0; it < own.n && ok; ++it) {
       const AttnItem x = fetch(S, own.more, it);
-      const int ct = ceil_div(x.ctx, kKT);
-      const int32_t* tab = p.page_table + (long long)x.r * p.max_pages;
-      // lane j holds the page of slot win + j
-      int win = -1, page_of = 0;
-      for (int t = x.tb; t < x.te && ok; ++t) {
-        const int vis = visible(t, ct, x);
-        const int rows = t < ct ? box : kBoxRows, nb = ceil_div(vis, rows);
-        if (t < ct) {
-          const int s0 = (int)(((long long)t * kKT) >> lp), ns = ceil_div(kKT, P);
-          if (win < 0 || s0 + ns > win + 32) {
-            win = s0;
-            const long long first = (long long)(win + lane) << lp;
-            int pg = 0;
-            if (first < x.ctx) {
-              pg = win + lane < p.max_pages ? tab[win + lane] : -1;
-              // (a page that no cache holds: its keys read as zero)
-              if (pg < 0 || pg >= p.n_pages) {
-                raise_error(p.err, DSPARK_DEVERR_BAD_INPUT);
-                pg = p.n_pages;
-              }
-            }
-            page_of = pg;
-          }
-        }
-        for (int kv = 0; kv < 2; ++kv, ++g) {
-          const int slot = g % kStages;
-          if (g >= kStages && !wait(S.empty[slot], (g / kStages - 1) & 1, cx)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
-          if (lane == 0) mbar_arrive_expect_tx(bar, nb * 2 * rows * 128);
-          __syncwarp();
-          for (int o0 = 0; o0 < 2 * nb; o0 += 32) {
-            const int o = o0 + lane, bx = o >> 1, half = o & 1;
-            const uint32_t to = dst + half * kHalf + bx * rows * 128;
-            const int at = t * kKT + bx * rows;  // (of a cache tile: below ctx for bx < nb)
-            const int page = __shfl_sync(0xffffffffu, page_of, bx < nb ? ((at >> lp) - win) & 31 : 0);
-            if (bx < nb) {
-              if (t < ct)
-                tma_load_4d(to, kv ? &tm_v : &tm_k, bar, half * 64, x.kvh, at & (P - 1), page);
-              else
-                tma_load_3d(to, kv ? &tm_vn : &tm_kn, bar, half * 64, x.kvh,
-                            x.c0 + (t - ct) * kKT + bx * kBoxRows);
-            }
-          }
-          __syncwarp();
-        }
-      }
-    }
-    if (lane == 0)
-      for (int i = max(0, g - kStages); i < g; ++i) drain(S.full[i % kStages], (i / kStages) & 1, p.err);
-  } else if (warp == kQWarp) {
-    // ------------------------------------------------------------- Q
-    const int rpt = p.tile_rows;
-    const uint32_t bytes = (uint32_t)rpt * G * 256;
-    int used[2] = {0, 0}, turn = 0;
-    bool ok = true;
-    for (int it = 0; it < own.n && ok; ++it) {
-      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
       const bool two = x.ni > rpt;
-      for (int k = 0; k < (two ? 2 : 1); ++k) {
-        const int b = two ? k : turn;
-        const int u = b ? used[1] : used[0];
-        if (u > 0 && !wait(S.q_empty[b], (u - 1) & 1, cx)) {
-          ok = false;
-          break;
+      auto load_q = [&]() {
+        for (int k = 0; k < (two ? 2 : 1) && ok; ++k) {
+          const int b = two ? k : turn, u = b ? used1 : used0;
+          if (u > 0) ok = wait(S.q_empty[b], (u - 1) & 1, cx);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_addr(&S.q_full[b]);
+            mbar_arrive_expect_tx(bar, (uint32_t)rpt * G * 256);
+            for (int half = 0; half < 2; ++half)
+              tma_load_3d(q_base + b * kTile + half * kHalf, &tm_q, bar, half * 64, x.kvh * G,
+                          x.c0 + x.i0 + k * rpt);
+          }
+          __syncwarp();
+          ++(b ? used1 : used0);
         }
+        if (!two) turn ^= 1;
+      };
+      Pages pages;
+      if (it == 0) load_q();
+      for (int k = 0; k < nt && ok; ++k) {
+        // Q's buffer is free once the last item's last S is done, which the third K waits for too
+        if (k == min(2, nt - 1) && it > 0) load_q();
+        const int g = g0 + fill_of_k(k, two);
+        const int slot = g % kStages;
+        if (!(ok = __all_sync(0xffffffffu, ok && wait_free(S, g, cx)))) break;
+        const int t = x.tb + k;
+        const bool cached = t < ct;
+        const int lb = cached ? min(lp, 7) : 4;  // log2 of a box's keys
+        const int nb = (visible(t, ct, x) + (1 << lb) - 1) >> lb;
+        const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
         if (lane == 0) {
-          const uint32_t bar = smem_addr(&S.q_full[b]);
-          mbar_arrive_expect_tx(bar, bytes);
-          for (int half = 0; half < 2; ++half)
-            tma_load_3d(q_base + b * kTile + half * kHalf, &tm_q, bar, half * 64, x.kvh * G,
-                        x.c0 + x.i0 + k * rpt);
+          mbar_arrive_expect_tx(bar, nb * (256 << lb));
+          if (!two) mbar_arrive(smem_addr(&S.empty[slot]));  // (for the stream that has no part in it)
+          set_count(S.armed[slot], g / kStages + 1);
         }
         __syncwarp();
-        if (b) ++used[1]; else ++used[0];
-      }
-      if (!two) turn ^= 1;
-    }
-    if (lane == 0)
-      for (int b = 0; b < 2; ++b) {
-        const int u = b ? used[1] : used[0];
-        if (u > 0) drain(S.q_full[b], (u - 1) & 1, p.err);
-      }
-  } else if (warp == kLookWarp) {
-    // ------------------------------------------------------------- V tiles looked over
-    int g = 0;  // key tiles
-    bool ok = true;
-    for (int it = 0; it < own.n && ok; ++it) {
-      const AttnItem x = fetch(S, own.more, it);
-      const int ct = ceil_div(x.ctx, kKT);
-      if (lane == 0) S.special[it % kFlags] = 0;
-      __syncwarp();
-      for (int t = x.tb; t < x.te; ++t, ++g) {
-        // every fill is waited for, in order: a barrier that is not followed step by step shows
-        // a phase of the same parity
-        const int vis = visible(t, ct, x), i = 2 * g + 1, slot = i % kStages;
-        ok = wait(S.full[(i - 1) % kStages], ((i - 1) / kStages) & 1, cx);
-        if (ok && lane == 0) mbar_arrive(smem_addr(&S.empty[(i - 1) % kStages]));
-        if (!ok || !(ok = wait(S.full[slot], (i / kStages) & 1, cx))) break;
-        if (!looked_over(t, ct, vis)) {
-          if (lane == 0) mbar_arrive(smem_addr(&S.empty[slot]));
-          continue;
+        if (cached) pages.look_up(p, x, t);
+        // lane = (box, column half); at most 16 boxes
+        const int bx = lane >> 1, half = lane & 1, at = t * kKT + (bx << lb);
+        const int page = cached ? pages.of(at >> lp) : 0;
+        if (bx < nb) {
+          const uint32_t to = dst + half * kHalf + bx * (128 << lb);
+          if (cached)
+            tma_load_4d(to, &tm_k, bar, half * 64, x.kvh, at & ((1 << lp) - 1), page);
+          else
+            tma_load_3d(to, &tm_kn, bar, half * 64, x.kvh, x.c0 + (t - ct) * kKT + bx * kBoxRows);
         }
-        uint8_t* v = smem + kHead + 2 * kTile + slot * kTile;
+        __syncwarp();
+      }
+      g0 += 2 * nt;
+    }
+    if (lane == 0) {
+      if (used0 > 0) drain(S.q_full[0], (used0 - 1) & 1, p.err);
+      if (used1 > 0) drain(S.q_full[1], (used1 - 1) & 1, p.err);
+    }
+  } else if (warp == kVWarp) {
+    // ------------------------------------------------------------- V, loaded and looked over
+    const int lp = p.log2_page;
+    int g0 = 0, g_last = -1;                     // fills of the items before; the fill to look over
+    // of that fill: log2 of its boxes' keys, visible keys, whether block rows, its item
+    int lb_last = 0, vis_last = 0, it_last = 0;
+    bool new_last = false, ok = true;
+    auto look = [&]() -> bool {
+      if (g_last < 0) return true;
+      const int slot = g_last % kStages;
+      if (!wait(S.full[slot], (g_last / kStages) & 1, cx)) return false;
+      if (new_last || (vis_last & 15)) {
+        uint8_t* const v = smem + kHead + 2 * kTile + slot * kTile;
+        const int lb = lb_last, vis = vis_last;
+        // 16-byte piece o & 7 of key o >> 3 in a column half
+        auto piece = [&](int o, int half) {
+          const int key = o >> 3;
+          return reinterpret_cast<uint4*>(v + ((key >> lb) << (lb + 8)) + (half << (lb + 7)) +
+                                          ((key & ((1 << lb) - 1)) << 7) + (o & 7) * 16);
+        };
         bool odd = false;
-        if (t >= ct) {
-          // rows 0 .. vis - 1, 16 bytes (row, piece) a lane and step, in both halves
+        if (new_last) {
           for (int o = lane; o < vis * 8; o += 32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint4* at = reinterpret_cast<uint4*>(v + half * kHalf + o * 16);
-              uint4 u = *at;
+              uint4* const at = piece(o, half);
+              const uint4 u = *at;
               // an exponent of ones carries into the bit above it
-              const uint32_t ones = (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
-                                     ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
-                                    0x80008000u;
+              const uint32_t ones =
+                  (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                   ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
+                  0x80008000u;
               if (ones) {
                 odd = true;
                 auto clear = [](uint32_t w) {
@@ -370,120 +437,167 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // rows vis .. the end of their chunk of 16
+        // keys vis .. the end of their chunk of 16
         const int nz = (-vis & 15) * 8;
         for (int o = lane; o < 2 * nz; o += 32) {
-          const int half = o >= nz, k = o - (half ? nz : 0);
-          *reinterpret_cast<uint4*>(v + half * kHalf + (vis * 8 + k) * 16) = make_uint4(0, 0, 0, 0);
+          const int half = o >= nz;
+          *piece(vis * 8 + o - (half ? nz : 0), half) = make_uint4(0, 0, 0, 0);
         }
-        if (odd) S.special[it % kFlags] = 1;
+        if (odd) S.special[it_last % kFlags] = 1;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_addr(&S.looked[slot]));
-          mbar_arrive(smem_addr(&S.empty[slot]));
-        }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------- products
-    constexpr uint32_t kQk = idesc_bf16_f32(kM, kKT, 0, 0), kPv = idesc_bf16_f32(kM, kD, 0, 1);
-    struct Pending {       // a stream's product P V that is still to be issued
-      int item, slot_use;  // item -1: none; slot_use: index of V's fill
-      int nch;
-      bool first, look, wait_v, release;
-    };
-    Pending pend[2] = {{-1, 0, 0, false, false, false, false}, {-1, 0, 0, false, false, false, false}};
-    int nv[2] = {0, 0};    // tiles of a stream so far
-    int used[2] = {0, 0}, turn = 0, g = 0;
-    uint32_t look_phase = 0;  // bit: the slot's next phase of `looked`
-    bool ok = true;
-    auto flush = [&](int s) -> bool {
-      Pending& w = pend[s];
-      if (w.item < 0) return true;
-      if (w.first && w.item > 0 && !wait(S.o_free, (w.item - 1) & 1, cx)) return false;
-      const int slot = w.slot_use % kStages;
-      if (w.wait_v) {  // (of two streams that share V the first waits)
-        if (w.look) {
-          if (!wait(S.looked[slot], look_phase >> slot & 1, cx)) return false;
-          look_phase ^= 1u << slot;
-        }
-        if (!wait(S.full[slot], (w.slot_use / kStages) & 1, cx)) return false;
-      }
-      if (!wait(S.p_full[s], (nv[s] - 1) & 1, cx)) return false;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t v = ring + slot * kTile, o = tmem + kTmemO + s * 128;
-        for (int k = 0; k < w.nch; ++k)
-          umma_bf16_ts(o, tmem + kTmemS + s * 128 + k * 8, smem_desc(v + k * 2048, kHalf, 1024, SW_128B),
-                       kPv, (w.first && k == 0) ? 0u : 1u);
-        umma_commit(smem_addr(&S.pv_done[s]));
-        if (w.release) umma_commit(smem_addr(&S.empty[slot]));
-      }
-      __syncwarp();
-      w.item = -1;
+      if (lane == 0) set_count(S.looked[slot], g_last + 1);
+      g_last = -1;
       return true;
     };
     for (int it = 0; it < own.n && ok; ++it) {
       const AttnItem x = fetch(S, own.more, it);
       const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
       const bool two = x.ni > p.tile_rows;
-      const int nvt = two ? 2 * nt : nt;
-      for (int vt = 0; vt < nvt; ++vt) {
-        const int s = vt & 1, k = two ? vt >> 1 : vt, t = x.tb + k, gk = 2 * (g + k);
-        const int qb = two ? s : turn;
-        if (!flush(s)) { ok = false; break; }
-        if (vt < (two ? 2 : 1) && !wait(S.q_full[qb], (qb ? used[1] : used[0]) & 1, cx)) { ok = false; break; }
-        const int slot = gk % kStages;
-        if ((!two || s == 0) && !wait(S.full[slot], (gk / kStages) & 1, cx)) { ok = false; break; }
+      Pages pages;
+      if (lane == 0) S.special[it % kFlags] = 0;
+      __syncwarp();
+      for (int k = 0; k < nt && ok; ++k) {
+        const int g = g0 + fill_of_v(k, nt, two), slot = g % kStages;
+        if (!(ok = __all_sync(0xffffffffu, wait_free(S, g, cx)))) break;
+        const int t = x.tb + k, vis = visible(t, ct, x);
+        const bool cached = t < ct;
+        const int lb = cached ? min(lp, 7) : 4, nb = (vis + (1 << lb) - 1) >> lb;
+        const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
         if (lane == 0) {
-          tc_fence_after();
-          const uint32_t q = q_base + qb * kTile, kb = ring + slot * kTile;
-#pragma unroll
-          for (int d = 0; d < kD / 16; ++d)
-            umma_bf16(tmem + kTmemS + s * 128,
-                      smem_desc(q + (d >> 2) * kHalf + (d & 3) * 32, 16, 1024, SW_128B),
-                      smem_desc(kb + (d >> 2) * kHalf + (d & 3) * 32, 16, 1024, SW_128B), kQk,
-                      d > 0 ? 1u : 0u);
-          umma_commit(smem_addr(&S.s_full[s]));
-          if (!two || s == 1) umma_commit(smem_addr(&S.empty[slot]));
-          if (two ? k == nt - 1 : vt == nvt - 1) umma_commit(smem_addr(&S.q_empty[qb]));
+          mbar_arrive_expect_tx(bar, nb * (256 << lb));
+          if (!two) mbar_arrive(smem_addr(&S.empty[slot]));
+          set_count(S.armed[slot], g / kStages + 1);
         }
         __syncwarp();
-        const int vis = visible(t, ct, x);
-        ++nv[s];
-        pend[s] = {it, gk + 1, ceil_div(vis, 16), two ? k == 0 : vt < 2, looked_over(t, ct, vis),
-                   !two || s == 0, !two || s == 1};
-        // the next item may not come to the other stream at all
-        if (nvt == 1 && !flush(1)) { ok = false; break; }
+        if (cached) pages.look_up(p, x, t);
+        const int bx = lane, at = t * kKT + (bx << lb);
+        const int page = cached ? pages.of(at >> lp) : 0;
+        if (bx < nb) {
+          const uint32_t to = dst + bx * (256 << lb);
+          if (cached)
+            tma_load_5d(to, &tm_v, bar, 0, at & ((1 << lp) - 1), 0, x.kvh, page);
+          else
+            tma_load_4d(to, &tm_vn, bar, 0, x.c0 + (t - ct) * kKT + bx * kBoxRows, 0, x.kvh);
+        }
+        __syncwarp();
+        // the fill before this one; its product comes after the one that made room here
+        ok = look();
+        g_last = g;
+        lb_last = lb;
+        vis_last = vis;
+        new_last = !cached;
+        it_last = it;
+      }
+      // (an item's last fill at once: its product may be what the next item's fills wait for)
+      if (ok) ok = look();
+      g0 += 2 * nt;
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------- products
+    // One thread for each stream: the two share the tensor cores, and the one waits and computes
+    // addresses while the other's products run.
+    constexpr uint32_t kQk = idesc_bf16_f32(kM, kKT, 0, 0), kPv = idesc_bf16_f32(kM, kD, 0, 1);
+    const int s = warp == kMmaWarp ? 0 : 1;
+    // (addresses are the low 14 bits, in 16 bytes, of a descriptor's low word)
+    const uint64_t dq = smem_desc(q_base, 16, 1024, SW_128B), dk = smem_desc(ring, 16, 1024, SW_128B),
+                   dv = smem_desc(ring, 0, 1024, SW_128B);
+    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
+    const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);  // (its column halves: p_lb)
+    const uint32_t t_s = tmem + kTmemS + s * 128, t_o = tmem + kTmemO + s * 128;
+    // the product P V that is still to be issued: its item (-1: none), V's fill, chunks and log2 of
+    // its boxes' keys, and whether it is the item's first
+    int p_item = -1, p_fill = 0, p_nch = 0, p_lb = 4;
+    bool p_first = false;
+    int nv = 0, g = 0, used0 = 0, used1 = 0, turn = 0;
+    bool ok = true;
+    auto flush = [&]() -> bool {
+      if (p_item < 0) return true;
+      if (p_first && !wait_count(S.epilogues, 8 * p_item, cx)) return false;  // O is free
+      const int slot = p_fill % kStages;
+      if (!wait_count(S.looked[slot], p_fill + 1, cx)) return false;
+      // a box of 2^lb keys lies as its two column halves, one behind the other
+      const int lb = p_lb;
+      const uint32_t v = v_lo + slot * (kTile >> 4) + (8u << (lb + 16)), old = p_first ? 0u : 1u;
+      uint32_t at[8];  // (computed before P is waited for: see mma_ss)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t key = 16 * k;
+        at[k] = v + ((key >> lb) << (lb + 4)) + ((key & ((1u << lb) - 1)) << 3);
+      }
+      if (!wait1(S.p_full[s], (nv - 1) & 1, cx)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < p_nch) mma_ts(t_o, t_s + k * 8, at[k], v_hi, kPv, k ? 1u : old);
+      umma_commit(smem_addr(&S.pv_done[s]));
+      umma_commit(smem_addr(&S.empty[slot]));
+      p_item = -1;
+      return true;
+    };
+    for (int it = 0; it < own.n && ok; ++it) {
+      const AttnItem x = fetch(S, own.more, it);
+      const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
+      const bool two = x.ni > p.tile_rows;
+      const int qb = two ? s : turn, step = two ? 1 : 2;
+      const uint32_t q = q_lo + qb * (kTile >> 4);
+      const uint32_t q_par = (qb ? used1 : used0) & 1;
+      int k = two ? 0 : s;
+      if (k >= nt) {  // no tile of the item on this stream: what the last one left
+        ok = flush() && wait1(S.q_full[qb], q_par, cx);
+        if (ok) mbar_arrive(smem_addr(&S.q_empty[qb]));
+      }
+      for (bool first = true; k < nt && ok; k += step, first = false) {
+        const int f = g + fill_of_k(k, two), slot = f % kStages;
+        const int vis = visible(x.tb + k, ct, x);
+        const uint32_t kb = k_lo + slot * (kTile >> 4);
+        const bool last = k + step >= nt;
+        if (!(ok = flush())) break;
+        if (first) {
+          if (!(ok = wait1(S.q_full[qb], q_par, cx))) break;
+          // (each stream follows both buffers' phases)
+          if (two) {
+            if (!(ok = wait1(S.q_full[qb ^ 1], (qb ? used0 : used1) & 1, cx))) break;
+            mbar_arrive(smem_addr(&S.q_empty[qb ^ 1]));
+          }
+        }
+        if (!(ok = wait_filled(S, f, cx))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int d = 0; d < kD / 16; ++d) {
+          const uint32_t at = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
+          mma_ss(t_s, q + at, kb + at, k_hi, kQk, d > 0 ? 1u : 0u);
+        }
+        umma_commit(smem_addr(&S.s_full[s]));
+        umma_commit(smem_addr(&S.empty[slot]));
+        if (last) umma_commit(smem_addr(&S.q_empty[qb]));
+        ++nv;
+        p_item = it;
+        p_fill = g + fill_of_v(k, nt, two);
+        p_lb = x.tb + k < ct ? min(p.log2_page, 7) : 4;
+        p_nch = (vis + 15) >> 4;
+        p_first = first;
       }
       if (two) {
-        ++used[0];
-        ++used[1];
+        ++used0;
+        ++used1;
       } else {
-        if (turn) ++used[1]; else ++used[0];
+        ++(turn ? used1 : used0);
         turn ^= 1;
       }
-      g += nt;
+      g += 2 * nt;
     }
-    // (in the order of their slots)
-    if (ok) {
-      const int s0 = pend[1].item >= 0 && (pend[0].item < 0 || pend[1].slot_use < pend[0].slot_use) ? 1 : 0;
-      ok = flush(s0);
-      if (ok) ok = flush(s0 ^ 1);
-    }
-    if (lane == 0) {
-      // whatever was issued completes before the memory is given back
-      for (int s = 0; s < 2; ++s)
-        if (nv[s] > 0) {
-          drain(S.s_full[s], (nv[s] - 1) & 1, p.err);
-          const int done = nv[s] - (pend[s].item >= 0 ? 1 : 0);
-          if (done > 0) drain(S.pv_done[s], (done - 1) & 1, p.err);
-        }
-    }
-    __syncwarp();
+    if (ok) ok = flush();
+    // whatever was issued completes before the memory is given back
+    if (nv > 0) drain(S.s_full[s], (nv - 1) & 1, p.err);
+    const int done = nv - (p_item >= 0 ? 1 : 0);
+    if (done > 0) drain(S.pv_done[s], (done - 1) & 1, p.err);
+  }
+  __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax / epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int sw = warp & 3, s = (warp - kSoftmaxWarp) >> 2;
     const int n = sw * 32 + lane;  // row of the tile
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(sw * 32) << 16);
@@ -537,10 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kKT; ++j) v[j] = j < vis ? v[j] : -INFINITY;
           }
-          float top = v[0];
+          float m8[8];
 #pragma unroll
-          for (int j = 1; j < kKT; ++j) top = fmaxf(top, v[j]);
-          top *= sl2;
+          for (int j = 0; j < 8; ++j) m8[j] = v[j];
+#pragma unroll
+          for (int j = 8; j < kKT; j += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              m8[i] = j + 8 + i < kKT ? fmaxf(fmaxf(m8[i], v[j + i]), v[j + 8 + i]) : fmaxf(m8[i], v[j + i]);
+          const float top = sl2 * fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                        fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
           const bool move = top > ref + 8.f;  // (from -inf: any key)
           const float alpha = move && ref != -INFINITY ? fast_exp2(ref - top) : 1.f;
           if (move) {
@@ -590,6 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       nv[1] += two ? nt : nt >> 1;
       // ---- epilogue: this stream's tile, or half the columns of both streams' sums
       if (two || s == 0 || nt > 1) ok = wait(S.pv_done[s], ((s ? nv[1] : nv[0]) - 1) & 1, cx);
+      // (the other stream's phase is the last item's until that is done with)
+      if (!two && ok) ok = __all_sync(0xffffffffu, wait_count(S.epilogues, 8 * it, cx));
       if (!two && ok && (s == 1 || nt > 1))
         ok = wait(S.pv_done[s ^ 1], ((s ? nv[0] : nv[1]) - 1) & 1, cx);
       if (!ok) break;
@@ -666,12 +788,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&S.o_free));
+      if (lane == 0)
+        asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_addr(&S.epilogues)) : "memory");
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x < kStages && S.armed[threadIdx.x] > 0)  // no copy is left in flight
+    drain(S.full[threadIdx.x], (S.armed[threadIdx.x] - 1) & 1, p.err);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -804,19 +929,27 @@ int launch(const void* q, const void* k_new, const void* v_new, const void* k_ca
     const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)pl.tile_rows};
     if (!gqa::encode_bf16_map(&tq, q, 3, dims, st, box)) return DSPARK_ECUDA;
   }
+  const uint64_t H = (uint64_t)Hkv, P = (uint64_t)page_size, tok = H * kD * 2;
+  const uint32_t keys = (uint32_t)(page_size < kKT ? page_size : kKT);
   {
-    const uint64_t dims[4] = {kD, (uint64_t)Hkv, (uint64_t)page_size, (uint64_t)n_pages};
-    const uint64_t st[3] = {kD * 2, (uint64_t)Hkv * kD * 2, (uint64_t)page_size * Hkv * kD * 2};
-    const uint32_t box[4] = {64, 1, (uint32_t)(page_size < kKT ? page_size : kKT), 1};
+    const uint64_t dims[4] = {kD, H, P, (uint64_t)n_pages}, st[3] = {kD * 2, tok, P * tok};
+    const uint32_t box[4] = {64, 1, keys, 1};
     if (!gqa::encode_bf16_map(&tk, k_cache, 4, dims, st, box)) return DSPARK_ECUDA;
-    if (!gqa::encode_bf16_map(&tv, v_cache, 4, dims, st, box)) return DSPARK_ECUDA;
+  }
+  {  // V: a box brings both column halves
+    const uint64_t dims[5] = {64, P, 2, H, (uint64_t)n_pages}, st[4] = {tok, 128, kD * 2, P * tok};
+    const uint32_t box[5] = {64, keys, 2, 1, 1};
+    if (!gqa::encode_bf16_map(&tv, v_cache, 5, dims, st, box)) return DSPARK_ECUDA;
   }
   {
-    const uint64_t dims[3] = {kD, (uint64_t)Hkv, (uint64_t)max_rows};
-    const uint64_t st[2] = {kD * 2, (uint64_t)Hkv * kD * 2};
+    const uint64_t dims[3] = {kD, H, (uint64_t)max_rows}, st[2] = {kD * 2, tok};
     const uint32_t box[3] = {64, 1, kBoxRows};
     if (!gqa::encode_bf16_map(&tkn, k_new, 3, dims, st, box)) return DSPARK_ECUDA;
-    if (!gqa::encode_bf16_map(&tvn, v_new, 3, dims, st, box)) return DSPARK_ECUDA;
+  }
+  {
+    const uint64_t dims[4] = {64, (uint64_t)max_rows, 2, H}, st[3] = {tok, 128, kD * 2};
+    const uint32_t box[4] = {64, kBoxRows, 2, 1};
+    if (!gqa::encode_bf16_map(&tvn, v_new, 4, dims, st, box)) return DSPARK_ECUDA;
   }
   static PerDevice<bool> done;
   if (!once_per_device(done, false, [] {

@@ -104,6 +104,19 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// One lane of a converged warp, the same every time.  (Code that only it runs may keep the operands of
+// TMA and tcgen05 instructions in uniform registers; behind a test of the lane number each such
+// instruction becomes a loop.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ------------------------------------------------------------------ proxies / fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -63,6 +63,7 @@ struct Smem {  // the first 3 KB; then Q (two tiles) and the ring
   // by at every phase.
   uint32_t armed[kStages];             // fills of a slot that were begun
   uint32_t looked[kStages];            // V's last fill of a slot that was looked over, + 1
+  uint32_t turns[2];                   // steps that a stream issued of items with two query tiles
   uint32_t epilogues;                  // softmax warps that are done with an item, over all items
   int special[kFlags];                 // by item: block rows held NaN or infinities
   float ml[2][kM][2];                  // (reference, sum) of a stream's rows at an item's end
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     S.abort = 0;
-    S.epilogues = 0;
+    S.epilogues = S.turns[0] = S.turns[1] = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&S.full[i]), 1);
       mbar_init(smem_addr(&S.empty[i]), 2);  // the products of both streams
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int b = two ? k : turn, u = b ? used1 : used0;
           if (u > 0) ok = wait(S.q_empty[b], (u - 1) & 1, cx);
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t bar = smem_addr(&S.q_full[b]);
             mbar_arrive_expect_tx(bar, (uint32_t)rpt * G * 256);
             for (int half = 0; half < 2; ++half)
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lb = cached ? min(lp, 7) : 4;  // log2 of a box's keys
         const int nb = (visible(t, ct, x) + (1 << lb) - 1) >> lb;
         const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, nb * (256 << lb));
           if (!two) mbar_arrive(smem_addr(&S.empty[slot]));  // (for the stream that has no part in it)
           set_count(S.armed[slot], g / kStages + 1);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g0 += 2 * nt;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       if (used0 > 0) drain(S.q_full[0], (used0 - 1) & 1, p.err);
       if (used1 > 0) drain(S.q_full[1], (used1 - 1) & 1, p.err);
     }
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool cached = t < ct;
         const int lb = cached ? min(lp, 7) : 4, nb = (vis + (1 << lb) - 1) >> lb;
         const uint32_t bar = smem_addr(&S.full[slot]), dst = ring + slot * kTile;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, nb * (256 << lb));
           if (!two) mbar_arrive(smem_addr(&S.empty[slot]));
           set_count(S.armed[slot], g / kStages + 1);
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = look();
       g0 += 2 * nt;
     }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ------------------------------------------------------------- products
     // One thread for each stream: the two share the tensor cores, and the one waits and computes
     // addresses while the other's products run.
@@ -512,30 +513,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool p_first = false;
     int nv = 0, g = 0, used0 = 0, used1 = 0, turn = 0;
     bool ok = true;
-    auto flush = [&]() -> bool {
+    uint32_t at[8];          // of that V, each chunk's descriptor (what is computed between two
+                             // products is time that the tensor cores wait)
+    // what the product waits for, then the product
+    auto p_ready = [&]() -> bool {
       if (p_item < 0) return true;
-      if (p_first && !wait_count(S.epilogues, 8 * p_item, cx)) return false;  // O is free
-      const int slot = p_fill % kStages;
-      if (!wait_count(S.looked[slot], p_fill + 1, cx)) return false;
+      const int slot = p_fill % kStages, lb = p_lb;
       // a box of 2^lb keys lies as its two column halves, one behind the other
-      const int lb = p_lb;
-      const uint32_t v = v_lo + slot * (kTile >> 4) + (8u << (lb + 16)), old = p_first ? 0u : 1u;
-      uint32_t at[8];  // (computed before P is waited for: see mma_ss)
+      const uint32_t v = v_lo + slot * (kTile >> 4) + (8u << (lb + 16));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t key = 16 * k;
         at[k] = v + ((key >> lb) << (lb + 4)) + ((key & ((1u << lb) - 1)) << 3);
       }
-      if (!wait1(S.p_full[s], (nv - 1) & 1, cx)) return false;
+      return (!p_first || wait_count(S.epilogues, 8 * p_item, cx)) &&  // O is free
+             wait_count(S.looked[slot], p_fill + 1, cx) && wait1(S.p_full[s], (nv - 1) & 1, cx);
+    };
+    auto issue_pv = [&]() {
+      if (p_item < 0) return;
+      const uint32_t old = p_first ? 0u : 1u;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < p_nch) mma_ts(t_o, t_s + k * 8, at[k], v_hi, kPv, k ? 1u : old);
       umma_commit(smem_addr(&S.pv_done[s]));
-      umma_commit(smem_addr(&S.empty[slot]));
+      umma_commit(smem_addr(&S.empty[p_fill % kStages]));
       p_item = -1;
+    };
+    auto flush = [&]() -> bool {
+      if (!p_ready()) return false;
+      issue_pv();
       return true;
     };
+    uint32_t turns = 0;
     for (int it = 0; it < own.n && ok; ++it) {
       const AttnItem x = fetch(S, own.more, it);
       const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vis = visible(x.tb + k, ct, x);
         const uint32_t kb = k_lo + slot * (kTile >> 4);
         const bool last = k + step >= nt;
-        if (!(ok = flush())) break;
+        if (!(ok = p_ready())) break;
         if (first) {
           if (!(ok = wait1(S.q_full[qb], q_par, cx))) break;
           // (each stream follows both buffers' phases)
@@ -563,12 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!(ok = wait_filled(S, f, cx))) break;
+        // Two query tiles take turns, so that one's softmax runs beside the other's products: left to
+        // themselves both streams fall into step.
+        if (two && !(ok = wait_count(S.turns[s ^ 1], turns + s, cx))) break;
+        issue_pv();
         tc_fence_after();
 #pragma unroll
         for (int d = 0; d < kD / 16; ++d) {
           const uint32_t at = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
           mma_ss(t_s, q + at, kb + at, k_hi, kQk, d > 0 ? 1u : 0u);
         }
+        if (two) set_count(S.turns[s], ++turns);
         umma_commit(smem_addr(&S.s_full[s]));
         umma_commit(smem_addr(&S.empty[slot]));
         if (last) umma_commit(smem_addr(&S.q_empty[qb]));

@@ -651,20 +651,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tie(v);
           }
           const int vis = visible(t, ct, x);
-          if (t >= ct) {
-            // bits of the tile's 128 block rows, none past the segment or the mask's words
+          if (t >= ct || vis < kKT) {
+            // bits of the tile's 128 keys: visible at all, and of block rows those of the mask
             const int w0 = (t - ct) * 4;
+            uint32_t bits[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              uint32_t bits = w0 + w < 2 * p.words ? mrow[w0 + w] : 0u;
               const int left = vis - 32 * w;
-              if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[32 * w + j] = (bits >> j & 1) ? v[32 * w + j] : -INFINITY;
+              bits[w] = t < ct ? ~0u : w0 + w < 2 * p.words ? mrow[w0 + w] : 0u;
+              if (left < 32) bits[w] &= left <= 0 ? 0u : (1u << left) - 1u;
             }
-          } else if (vis < kKT) {
 #pragma unroll
-            for (int j = 0; j < kKT; ++j) v[j] = j < vis ? v[j] : -INFINITY;
+            for (int j = 0; j < kKT; ++j) v[j] = (bits[j >> 5] >> (j & 31) & 1) ? v[j] : -INFINITY;
           }
           float m8[8];
 #pragma unroll

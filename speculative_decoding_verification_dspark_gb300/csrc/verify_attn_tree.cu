@@ -97,46 +97,33 @@ struct Ctx {
   unsigned int* err;
 };
 
-// Bounded wait of one thread.  (A poll takes 73 cycles, one that may sleep 131, so the first are
-// plain ones.)
+// Bounded waits of one thread: on a barrier's phase, and until a count has come to `least`.  Bounded by
+// their number of polls, in few instructions: the roles' loops and a dozen waits by the clock would not
+// fit the instruction cache together.  (A poll of a barrier sleeps up to 20 us, one of a count takes 20
+// ns: the limits are some seconds.)
+constexpr int kBarrierPolls = 400000, kCountPolls = 100000000;
 __device__ __forceinline__ bool wait1(uint64_t& b, uint32_t parity, const Ctx& cx) {
   const uint32_t bar = smem_addr(&b);
   if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < kBarrierPolls; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 20000)) {
     if (*cx.abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *cx.abort = 1;
-      raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
-      return false;
-    }
   }
-  return true;
+  *cx.abort = 1;
+  return false;
 }
-// Bounded wait of one thread until a count has come to `least`.
 __device__ __forceinline__ bool wait_count(uint32_t& count, uint32_t least, const Ctx& cx) {
-  auto there = [&] {
-    uint32_t c;
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(c) : "r"(smem_addr(&count)) : "memory");
-    return (int)(c - least) >= 0;
-  };
+  const uint32_t at = smem_addr(&count);
 #pragma unroll 1
-  for (int i = 0; i < 1000; ++i)
-    if (there()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!there()) {
-    if (*cx.abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *cx.abort = 1;
-      raise_error(cx.err, DSPARK_DEVERR_WAIT_TIMEOUT);
-      return false;
-    }
-    __nanosleep(100);
+  for (int i = 0; i < kCountPolls; ++i) {
+    uint32_t c;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(c) : "r"(at) : "memory");
+    if ((int)(c - least) >= 0) return true;
+    if ((i & 1023) == 1023 && *cx.abort) return false;
   }
-  return true;
+  *cx.abort = 1;
+  return false;
 }
 __device__ __forceinline__ void set_count(uint32_t& count, uint32_t to) {
   asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(&count)), "r"(to) : "memory");
@@ -517,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                              // products is time that the tensor cores wait)
     // what the product waits for, then the product
     auto p_ready = [&]() -> bool {
-      if (p_item < 0) return true;
       const int slot = p_fill % kStages, lb = p_lb;
       // a box of 2^lb keys lies as its two column halves, one behind the other
       const uint32_t v = v_lo + slot * (kTile >> 4) + (8u << (lb + 16));
@@ -530,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1)
              wait_count(S.looked[slot], p_fill + 1, cx) && wait1(S.p_full[s], (nv - 1) & 1, cx);
     };
     auto issue_pv = [&]() {
-      if (p_item < 0) return;
       const uint32_t old = p_first ? 0u : 1u;
       tc_fence_after();
 #pragma unroll
@@ -540,53 +525,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(smem_addr(&S.empty[p_fill % kStages]));
       p_item = -1;
     };
-    auto flush = [&]() -> bool {
-      if (!p_ready()) return false;
-      issue_pv();
-      return true;
-    };
     uint32_t turns = 0;
-    for (int it = 0; it < own.n && ok; ++it) {
-      const AttnItem x = fetch(S, own.more, it);
+    // (one round more, for the product that the last item left)
+    for (int it = 0; it <= own.n && ok; ++it) {
+      const bool end = it == own.n;
+      AttnItem x{};
+      if (!end) x = fetch(S, own.more, it);
       const int ct = ceil_div(x.ctx, kKT), nt = x.te - x.tb;
       const bool two = x.ni > p.tile_rows;
       const int qb = two ? s : turn, step = two ? 1 : 2;
       const uint32_t q = q_lo + qb * (kTile >> 4);
       const uint32_t q_par = (qb ? used1 : used0) & 1;
-      int k = two ? 0 : s;
-      if (k >= nt) {  // no tile of the item on this stream: what the last one left
-        ok = flush() && wait1(S.q_full[qb], q_par, cx);
-        if (ok) mbar_arrive(smem_addr(&S.q_empty[qb]));
-      }
-      for (bool first = true; k < nt && ok; k += step, first = false) {
+      bool first = true;
+      for (int k = two ? 0 : s; first || k < nt; k += step, first = false) {
+        // (a stream without a tile of the item comes by once, for what the last one left)
+        const bool tile = k < nt;
         const int f = g + fill_of_k(k, two), slot = f % kStages;
-        const int vis = visible(x.tb + k, ct, x);
-        const uint32_t kb = k_lo + slot * (kTile >> 4);
-        const bool last = k + step >= nt;
-        if (!(ok = p_ready())) break;
-        if (first) {
+        // Two query tiles take turns, so that one's softmax runs beside the other's products: left to
+        // themselves both fall into step.
+        if (tile && two && !(ok = wait_count(S.turns[s ^ 1], turns + s, cx))) break;
+        if (p_item >= 0) {
+          if (!(ok = p_ready())) break;
+          issue_pv();
+        }
+        if (first && !end) {
           if (!(ok = wait1(S.q_full[qb], q_par, cx))) break;
           // (each stream follows both buffers' phases)
           if (two) {
             if (!(ok = wait1(S.q_full[qb ^ 1], (qb ? used0 : used1) & 1, cx))) break;
             mbar_arrive(smem_addr(&S.q_empty[qb ^ 1]));
           }
+          if (!tile) mbar_arrive(smem_addr(&S.q_empty[qb]));
         }
+        if (!tile) break;
         if (!(ok = wait_filled(S, f, cx))) break;
-        // Two query tiles take turns, so that one's softmax runs beside the other's products: left to
-        // themselves both streams fall into step.
-        if (two && !(ok = wait_count(S.turns[s ^ 1], turns + s, cx))) break;
-        issue_pv();
+        const int vis = visible(x.tb + k, ct, x);
+        const uint32_t kb = k_lo + slot * (kTile >> 4);
         tc_fence_after();
 #pragma unroll
         for (int d = 0; d < kD / 16; ++d) {
-          const uint32_t at = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
-          mma_ss(t_s, q + at, kb + at, k_hi, kQk, d > 0 ? 1u : 0u);
+          const uint32_t o = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
+          mma_ss(t_s, q + o, kb + o, k_hi, kQk, d > 0 ? 1u : 0u);
         }
         if (two) set_count(S.turns[s], ++turns);
         umma_commit(smem_addr(&S.s_full[s]));
         umma_commit(smem_addr(&S.empty[slot]));
-        if (last) umma_commit(smem_addr(&S.q_empty[qb]));
+        if (k + step >= nt) umma_commit(smem_addr(&S.q_empty[qb]));
         ++nv;
         p_item = it;
         p_fill = g + fill_of_v(k, nt, two);
@@ -603,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += 2 * nt;
     }
-    if (ok) ok = flush();
     // whatever was issued completes before the memory is given back
     if (nv > 0) drain(S.s_full[s], (nv - 1) & 1, p.err);
     const int done = nv - (p_item >= 0 ? 1 : 0);
@@ -808,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x == 0 && S.abort) raise_error(p.err, DSPARK_DEVERR_WAIT_TIMEOUT);
   if (threadIdx.x < kStages && S.armed[threadIdx.x] > 0)  // no copy is left in flight
     drain(S.full[threadIdx.x], (S.armed[threadIdx.x] - 1) & 1, p.err);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);

@@ -42,31 +42,43 @@ constexpr float kPerOctave = 32.f;
 constexpr int kList = 1024;            // tokens of a bracket that are sorted
 constexpr int kMaxCluster = 8;
 constexpr int kChunkBytes = 76 * 1024; // of a row in one CTA, while eight CTAs hold the row
+// Masses from fp32 are summed in fixed point, 44 bits behind the point (w <= 1, V <= 400000: below
+// 2^63): without the card's slow 64-bit floating point, which the sums in pairs need.
+typedef long long mass_t;
+constexpr float kUnit = 0x1p44f;
 // Error of the fp32 sums relative to the mass: ex2.approx and the products before it give 2^-21 per
-// token at most for the tokens that matter, far less in the sum of many.
-constexpr double kNear = 1e-6;
+// token at most for the tokens that matter, far less in the sum of many.  About 10^-6.
+__device__ __forceinline__ mass_t near_of(mass_t whole) { return whole >> 20; }
+// What lies before a kept token is short of p of the whole (0 < p < 1).
+__device__ __forceinline__ mass_t goal_of(float p, mass_t whole) {
+  const unsigned long long f = __float2ull_rn(p * 0x1p64f), w = whole;
+  return (mass_t)__umul64hi(f, w) + (f * w != 0);
+}
+__device__ __forceinline__ double goal_of(float p, double whole) { return (double)p * whole; }
+__device__ __forceinline__ mass_t distance(mass_t a, mass_t b) { return a > b ? a - b : b - a; }
 
 struct Shared {
   unsigned hist[kBuckets];             // this CTA's counts
   unsigned tot[kBuckets];              // the row's, in order of falling logits
   uint64_t list[kList];                // (order of the logit, index)
-  double part[2][kMaxCluster][3];      // exchanged between the CTAs, two sets in turn
+  unsigned long long part[2][kMaxCluster][3];  // exchanged between the CTAs, two sets in turn
   float cmax[kMaxCluster];
-  double wsum[kWarps][3];
+  unsigned long long wsum[kWarps][3];
   float wmax[kWarps];
   unsigned wcnt[kWarps];
-  double wmass[kWarps];
+  unsigned long long wmass[kWarps];
+  float wapprox[kWarps];
   float e2h[17], e2l[17];              // 2^(-j / 16), j = -8 .. 8, in two parts
   float c_hi, c_lo;                    // log2(e) / T in two parts
-  double log_min;                      // T ln(min_p)
   int n_list;
   // a decision of one thread or CTA for all
   int b_at;
   unsigned cum_before, cum_in, total;
   float f_lo, f_hi, t_cut;
   int i_cut, n_keep, again;
-  double z_kept;
+  float z_kept;
   float best[kWarps];
+  int n_near[kMaxCluster];             // of each CTA: tokens near the race's best
   double r_best[kWarps];
   int r_idx[kWarps];
   float c_best[kMaxCluster];
@@ -86,6 +98,15 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 template <typename T>
@@ -151,17 +172,20 @@ struct Row {
   int first, n;       // the chunk: tokens first .. first + n - 1
   int shift, groups;  // token i of the chunk is slot i + shift; 16-byte groups of slots
   int set;            // of S.part
-  float m, s;         // largest logit; buckets per unit of logit
+  float m, s, nc;     // largest logit; buckets and (negative) octaves per unit of logit
   float t_min;        // least logit that min-p leaves
   Kept lim;           // what earlier filters left
 
-  __device__ __forceinline__ float y_of(float l) const { return (m - l) * s; }
-  __device__ __forceinline__ float w_of(float l) const { return ex2(y_of(l) * (-1.f / kPerOctave)); }
+  // (rounded by the addition of 2^23: monotone in l, which is all that is asked)
+  __device__ __forceinline__ int bucket_of(float l) const {
+    return __float_as_int(fminf((m - l) * s, (float)(kBuckets - 1)) + 0x1p23f) & (kBuckets - 1);
+  }
+  __device__ __forceinline__ float w_of(float l) const { return ex2((m - l) * nc); }
   __device__ __forceinline__ bool left(float l, int i) const {
     return l > lim.t || (l == lim.t && first + i <= lim.i);
   }
 
-  // fn(l, i) for every token of the chunk.
+  // fn(l, i, j) for every token i of the chunk, j its place in its 16 bytes.
   template <class Fn>
   __device__ __forceinline__ void each(Fn&& fn) const {
     const uint4* p = reinterpret_cast<const uint4*>(data);
@@ -169,31 +193,37 @@ struct Row {
       float x[V::N];
       V::get(p[q], x);
 #pragma unroll
-      for (int j = 0; j < V::N; ++j) fn(x[j], q * V::N + j - shift);
+      for (int j = 0; j < V::N; ++j) fn(x[j], q * V::N + j - shift, j);
     }
   }
 
-  // Sums of three numbers over the row, the same in every thread of the cluster; in fixed order.
-  __device__ void sum3(double (&v)[3]) {
+  // Sums of three numbers (mass_t or double) over the row, the same in every thread of the cluster and
+  // in fixed order.
+  template <typename M>
+  __device__ __forceinline__ void sum3(M (&v)[3]) {
+    static_assert(sizeof(M) == 8, "a word of the exchange");
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     __syncthreads();
-    if (lane == 0)
-      for (int k = 0; k < 3; ++k) S.wsum[wid][k] = v[k];
+    M* const ws = reinterpret_cast<M*>(&S.wsum[0][0]);
+    if (lane < 3) ws[3 * wid + lane] = lane == 0 ? v[0] : lane == 1 ? v[1] : v[2];
     __syncthreads();
-    if (threadIdx.x < 3) {
-      double a = 0;
-      for (int w = 0; w < kWarps; ++w) a += S.wsum[w][threadIdx.x];
-      for (int r = 0; r < C; ++r) cl.map_shared_rank(&S, r)->part[set][rank][threadIdx.x] = a;
+    // thread (r, k): this CTA's sum k to CTA r
+    if (threadIdx.x < 4 * C && (threadIdx.x & 3) < 3) {
+      const int k = threadIdx.x & 3;
+      M a = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) a += ws[3 * w + k];
+      *reinterpret_cast<M*>(&cl.map_shared_rank(&S, threadIdx.x >> 2)->part[set][rank][k]) = a;
     }
     cl.sync();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       v[k] = 0;
-      for (int r = 0; r < C; ++r) v[k] += S.part[set][r][k];
+      for (int r = 0; r < C; ++r) v[k] += *reinterpret_cast<const M*>(&S.part[set][r][k]);
     }
     set ^= 1;
   }
@@ -205,7 +235,7 @@ struct Row {
     __syncthreads();
     for (int b = threadIdx.x; b < kBuckets; b += kThreads) S.hist[b] = 0;
     __syncthreads();
-    each([&](float l, int i) {
+    each([&](float l, int i, int) {
       const int b = bucket(l, i);
       if (b >= 0) atomicAdd(&S.hist[b], 1u);
     });
@@ -224,24 +254,26 @@ struct Row {
   // mass reaches the part `share` of the whole, the mass of bucket b being tot[b] * mass(b).
   // Sets S.b_at, S.cum_before (tokens in the buckets before), S.cum_in and S.total.
   template <class Fn>
-  __device__ void locate(bool weighted, unsigned target, double share, Fn&& mass) {
+  __device__ void locate(bool weighted, unsigned target, float share, Fn&& mass) {
     constexpr int kPer = kBuckets / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    unsigned c[kPer], cs = 0;
+    const uint4 t4 = reinterpret_cast<const uint4*>(S.tot)[tid];
+    static_assert(kPer == 4, "a thread's buckets");
+    const unsigned c[kPer] = {t4.x, t4.y, t4.z, t4.w};
+    unsigned cs = 0;
     float w[kPer], ws = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      c[j] = S.tot[tid * kPer + j];
-      w[j] = weighted ? c[j] * mass(tid * kPer + j) : 0.f;
+      w[j] = weighted && c[j] ? c[j] * mass(tid * kPer + j) : 0.f;
       cs += c[j];
       ws += w[j];
     }
     unsigned ci = cs;
-    double wi = ws;
+    float wi = ws;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned u = __shfl_up_sync(0xffffffffu, ci, o);
-      const double d = __shfl_up_sync(0xffffffffu, wi, o);
+      const float d = __shfl_up_sync(0xffffffffu, wi, o);
       if (lane >= o) {
         ci += u;
         wi += d;
@@ -250,38 +282,49 @@ struct Row {
     __syncthreads();
     if (lane == 31) {
       S.wcnt[wid] = ci;
-      S.wmass[wid] = wi;
+      S.wapprox[wid] = wi;
     }
-    if (tid == 0) S.b_at = -1;
+    if (tid == 0) S.b_at = 0x7fffffff;
     __syncthreads();
     unsigned c0 = ci - cs, last = 0;
-    double w0 = wi - ws, total = 0;
+    float w0 = wi - ws, total = 0;
+#pragma unroll
     for (int v = 0; v < kWarps; ++v) {
       if (v < wid) {
         c0 += S.wcnt[v];
-        w0 += S.wmass[v];
+        w0 += S.wapprox[v];
       }
-      total += S.wmass[v];
+      total += S.wapprox[v];
       last += S.wcnt[v];
     }
-    const double goal = share * total;
+    const float goal = share * total;
+    const unsigned c_first = c0;
     if (tid == 0) S.total = last;
+    // (of masses the first bucket that ends past the goal: fp32 sums of two threads need not join)
+    int mine = -1;
+    unsigned m_before = 0, m_in = 0;
+#pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const bool here = weighted ? (w0 < goal && w0 + w[j] >= goal) : (c0 < target && c0 + c[j] >= target);
-      if (here) {
-        // (rounding may let two buckets meet the goal: either will do)
-        S.b_at = tid * kPer + j;
-        S.cum_before = c0;
-        S.cum_in = c[j];
+      const bool here = weighted ? (c[j] && w0 + w[j] >= goal)
+                                 : (c0 < target && c0 + c[j] >= target);
+      if (here && mine < 0) {
+        mine = tid * kPer + j;
+        m_before = c0;
+        m_in = c[j];
+        atomicMin(&S.b_at, mine);
       }
       c0 += c[j];
       w0 += w[j];
     }
     __syncthreads();
-    if (S.b_at < 0) {  // the goal lies past the last token (rounding): the last bucket that holds one
+    if (mine >= 0 && S.b_at == mine) {
+      S.cum_before = m_before;
+      S.cum_in = m_in;
+    }
+    __syncthreads();
+    if (S.b_at == 0x7fffffff) {  // the goal lies past the last token (rounding): the last bucket that holds one
       __syncthreads();
-      c0 = ci - cs;
-      for (int v = 0; v < wid; ++v) c0 += S.wcnt[v];
+      c0 = c_first;
       for (int j = 0; j < kPer; ++j) {
         if (c[j] && c0 + c[j] == last) {
           S.b_at = tid * kPer + j;
@@ -294,14 +337,14 @@ struct Row {
     }
   }
 
-  // The least float l with y_of(l) < bound; y falls as l grows, so 32 lanes halve the codes five
-  // bits at a time.  By the first warp.
-  __device__ float edge(float bound) const {
+  // The least float l with a bucket below `bound`; buckets fall as l grows, so 32 lanes halve the codes
+  // five bits at a time.  By the first warp.
+  __device__ float edge(int bound) const {
     const int lane = threadIdx.x & 31;
-    uint32_t lo = code_of(-FLT_MAX), hi = code_of(m);  // y(hi) = 0 < bound
+    uint32_t lo = code_of(-FLT_MAX), hi = code_of(m);  // (bucket 0)
     while (hi > lo) {
       const uint32_t step = (hi - lo + 31) / 32, at = lo + min((unsigned)lane * step, hi - lo);
-      const unsigned ok = __ballot_sync(0xffffffffu, y_of(float_of(at)) < bound);
+      const unsigned ok = __ballot_sync(0xffffffffu, bucket_of(float_of(at)) < bound);
       // (at of lane 31 may be below hi: hi stays then)
       const int f = ok ? __ffs(ok) - 1 : 32;
       const uint32_t a = lo + min((unsigned)(f > 0 ? f - 1 : 0) * step, hi - lo);
@@ -315,33 +358,34 @@ struct Row {
 
   // Masses of the tokens left: above f_hi, in [f_lo, f_hi), and all; those of the bracket are listed
   // in S.list where `gather` is set.
-  __device__ void evaluate(float f_lo, float f_hi, bool gather, double (&v)[3]) {
+  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
     __syncthreads();
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
-    float above = 0, in = 0, below = 0;
-    const bool limited = lim.i != 0x7fffffff;
-    each([&](float l, int i) {
-      if (l < lim.t) return;
-      if (limited && !left(l, i)) return;
-      const float w = w_of(l);
-      if (l >= f_hi) {
-        above += w;
-      } else if (l >= f_lo) {
+    if (lim.i != 0x7fffffff) sums<true>(f_lo, f_hi, gather, v);
+    else sums<false>(f_lo, f_hi, gather, v);
+    sum3(v);
+  }
+  template <bool LIMITED>
+  __device__ __forceinline__ void sums(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
+    float above[2] = {0.f, 0.f}, all[2] = {0.f, 0.f}, in = 0.f;
+    const float least = lim.t;
+    each([&](float l, int i, int j) {
+      float w = w_of(l);
+      if (LIMITED ? !left(l, i) : l < least) w = 0.f;
+      all[j & 1] += w;
+      above[j & 1] += l >= f_hi ? w : 0.f;
+      if (l >= f_lo && l < f_hi && (LIMITED ? left(l, i) : l >= least)) {
         in += w;
         if (gather) {
           const int at = atomicAdd(&S.n_list, 1);
-          if (at < kList)
-            S.list[at] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
+          if (at < kList) S.list[at] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
         }
-      } else {
-        below += w;
       }
     });
-    v[0] = above;
-    v[1] = in;
-    v[2] = (double)above + (double)in + (double)below;
-    sum3(v);
+    v[0] = __float2ll_rn((above[0] + above[1]) * kUnit);
+    v[1] = __float2ll_rn(in * kUnit);
+    v[2] = __float2ll_rn((all[0] + all[1]) * kUnit);
   }
 
   // w in two parts, 2^-36 of it or better, by table and polynomial (Tang's scheme for the
@@ -374,7 +418,7 @@ struct Row {
   // evaluate's masses in pairs.
   __device__ void evaluate_pairs(float f_lo, float f_hi, double (&v)[3]) {
     if (threadIdx.x < 17) {
-      const double e = exp2(-((int)threadIdx.x - 8) / 16.0);
+      const double e = exp2(-((int)threadIdx.x - 8) / 16.0);  // (few: 64 bits are slow here)
       S.e2h[threadIdx.x] = (float)e;
       S.e2l[threadIdx.x] = (float)(e - (double)(float)e);
     }
@@ -385,7 +429,7 @@ struct Row {
       sl += ((sh - (t - z)) + (wh - z)) + wl;
       sh = t;
     };
-    each([&](float l, int i) {
+    each([&](float l, int i, int) {
       if (l < lim.t || !left(l, i)) return;
       float wh, wl;
       w_pair(l, wh, wl);
@@ -398,6 +442,12 @@ struct Row {
     v[2] = v[0] + v[1] + ((double)bh + bl);
     sum3(v);
   }
+  __device__ __forceinline__ void w_exact(float l, double& w) const {
+    float h, t;
+    w_pair(l, h, t);
+    w = (double)h + t;
+  }
+  __device__ __forceinline__ void w_exact(float l, mass_t& w) const { w = __float2ll_rn(w_of(l) * kUnit); }
 
   // The lists of all CTAs into this one's, sorted; n tokens in all (at most kList).
   __device__ int collect() {
@@ -434,58 +484,56 @@ struct Row {
     return float_of(~(uint32_t)(S.list[i] >> 32));
   }
 
-  // By the first CTA, over its sorted list of n tokens with masses v[0] above and v[2] in all: the
-  // end of the first `k` of them (k >= n: all) and, where p < 1, of the p part of what these and
-  // the tokens above hold (k_round: v[2] is not that mass yet, the list gives it).  Sets S.t_cut,
-  // S.i_cut, S.z_kept (the mass kept with the tokens above), and S.again if the sums in fp32
-  // do not decide it.
-  __device__ void walk(int n, const double (&v)[3], int k, bool whole_known, bool use_p, double p,
-                       bool pairs) {
+  // By the first CTA, over its sorted list of n tokens with masses v[0] above them and v[2] in all: the
+  // end of the first `k` of them (k >= n: all) and, where use_p, of the part p of the whole, which is
+  // v[2] or (list_only) what these k hold.  Sets S.t_cut, S.i_cut, S.z_kept (the mass kept with
+  // what is above), and S.again if the sums in fp32 do not decide it.
+  template <typename M>
+  __device__ void walk(int n, const M (&v)[3], int k, bool list_only, bool use_p, float p) {
+    constexpr bool kPairs = sizeof(M) == 8 && M(0.5f) != M(0);
     constexpr int kPer = kList / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    M* const wm = reinterpret_cast<M*>(S.wmass);
     n = min(n, k);
-    double w[kPer], ws = 0;
+    M w[kPer], ws = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = tid * kPer + j;
       w[j] = 0;
-      if (i < n) {
-        if (pairs) {
-          float h, l;
-          w_pair(list_l(i), h, l);
-          w[j] = (double)h + l;
-        } else {
-          w[j] = w_of(list_l(i));
-        }
-      }
+      if (i < n) w_exact(list_l(i), w[j]);
       ws += w[j];
     }
-    double wi = ws;
+    M wi = ws;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double d = __shfl_up_sync(0xffffffffu, wi, o);
+      const M d = __shfl_up_sync(0xffffffffu, wi, o);
       if (lane >= o) wi += d;
     }
-    if (lane == 31) S.wmass[wid] = wi;
+    if (lane == 31) wm[wid] = wi;
     if (tid == 0) {
       S.n_keep = n;
       S.again = 0;
     }
     __syncthreads();
-    double w0 = v[0] + wi - ws, all = v[0];
-    for (int q = 0; q < kWarps; ++q) {
-      if (q < wid) w0 += S.wmass[q];
-      all += S.wmass[q];
+    // (each warp adds the totals before it up, and all of them)
+    M t = lane < kWarps ? wm[lane] : M(0), all = t, part = lane < wid ? t : M(0);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      part += __shfl_xor_sync(0xffffffffu, part, o);
     }
-    const double whole = whole_known ? v[2] : all, goal = p * whole, near = pairs ? 0 : kNear * whole;
+    all = v[0] + __shfl_sync(0xffffffffu, all, 0);
+    M w0 = v[0] + __shfl_sync(0xffffffffu, part, 0) + (wi - ws);
     if (use_p) {
-      double run = w0;
+      const M whole = list_only ? all : v[2], goal = goal_of(p, whole);
+      M run = w0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = tid * kPer + j;
         if (i < n) {
           // token i is kept if the mass before it is short of the goal
-          if (i > 0 && fabs(run - goal) <= near) S.again = 1;
+          if constexpr (!kPairs)
+            if (i > 0 && distance(run, goal) <= near_of(whole)) S.again = 1;
           const bool kept = i == 0 || run < goal;
           run += w[j];
           if (kept && (i + 1 == n || !(run < goal))) S.n_keep = i + 1;
@@ -498,7 +546,7 @@ struct Row {
     for (int j = 0; j < kPer; ++j) {
       w0 += w[j];
       if (tid * kPer + j == keep - 1) {
-        S.z_kept = w0;
+        S.z_kept = kPairs ? (float)w0 : (float)w0 * (1.f / kUnit);
         S.t_cut = list_l(keep - 1);
         S.i_cut = (int)(uint32_t)S.list[keep - 1];
       }
@@ -531,7 +579,7 @@ struct Row {
       total += S.wcnt[w];
     }
     if (threadIdx.x == 0)
-      for (int r = 0; r < C; ++r) cl.map_shared_rank(&S, r)->part[set][rank][0] = (double)total;
+      for (int r = 0; r < C; ++r) cl.map_shared_rank(&S, r)->part[set][rank][0] = (unsigned long long)total;
     cl.sync();
     for (int r = 0; r < rank; ++r) before += (long long)S.part[set][r][0];
     set ^= 1;
@@ -547,14 +595,13 @@ struct Row {
 
   // One filter's end (k > 0: top-k, with top-p at once where the list holds all that top-k keeps;
   // else top-p of what is left).  Sets lim; returns the mass kept; done_p: top-p is applied.
-  __device__ double cut(int k, bool use_p, double p, bool& done_p) {
+  __device__ float cut(int k, bool use_p, float p, bool& done_p) {
     const bool by_count = k > 0;
     // 1: buckets of (m - l) / T
     histogram([&](float l, int i) {
-      if (l < lim.t || !left(l, i)) return -1;
-      return (int)fminf(y_of(l), (float)(kBuckets - 1));
+      return l < lim.t || !left(l, i) ? -1 : bucket_of(l);
     });
-    locate(!by_count, (unsigned)k, p, [](int b) { return ex2((b + 0.5f) * (-1.f / kPerOctave)); });
+    locate(!by_count, (unsigned)k, p, [](int b) { return ex2(b * (-1.f / kPerOctave)); });
     // 2: the bracket [f_lo, f_hi): `before` tokens above it, `in` in it, of `total`
     unsigned before = S.cum_before, in = S.cum_in;
     const unsigned total = S.total;
@@ -577,21 +624,33 @@ struct Row {
     float out_lo = -FLT_MAX, out_hi = INFINITY;
     unsigned out_before = 0, out_below = 0;
     bool pairs = false;
-    double v[3];
+    mass_t v[3];    // masses in fixed point from fp32,
+    double d[3];    // or, once those have not told, from pairs
+    float share = 0.f;
     // (each round halves the outer range at least once or cuts it into 2048: far fewer are needed)
     for (int round = 0; round < 100; ++round) {
       const bool gather = in <= (unsigned)kList;
       evaluate(f_lo, f_hi, gather, v);
-      if (pairs) evaluate_pairs(f_lo, f_hi, v);
       if (!by_count) {
         // does the bracket hold the end?
-        if (!pairs && (fabs(v[0] - p * v[2]) <= kNear * v[2] ||
-                       fabs(v[0] + v[1] - p * v[2]) <= kNear * v[2])) {
-          pairs = true;
-          evaluate_pairs(f_lo, f_hi, v);
+        if (!pairs) {
+          const mass_t goal = goal_of(p, v[2]), near = near_of(v[2]);
+          pairs = distance(v[0], goal) <= near || distance(v[0] + v[1], goal) <= near;
         }
-        const double goal = p * v[2];
-        if (before > out_before && !(v[0] < goal)) {
+        bool below_top, reached;
+        if (pairs) {
+          evaluate_pairs(f_lo, f_hi, d);
+          const double goal = goal_of(p, d[2]);
+          below_top = d[0] < goal;
+          reached = !(d[0] + d[1] < goal);
+          share = (float)((goal - d[0]) / d[1]);
+        } else {
+          const mass_t goal = goal_of(p, v[2]);
+          below_top = v[0] < goal;
+          reached = !(v[0] + v[1] < goal);
+          share = (float)(goal - v[0]) / (float)v[1];
+        }
+        if (before > out_before && !below_top) {
           out_lo = f_lo = f_hi;
           f_hi = out_hi;
           out_below = total - before;
@@ -599,7 +658,7 @@ struct Row {
           before = out_before;
           continue;
         }
-        if (f_lo > out_lo && v[0] + v[1] < goal && before + in + out_below < total) {
+        if (f_lo > out_lo && !reached && before + in + out_below < total) {
           out_hi = f_hi = f_lo;
           f_lo = out_lo;
           out_before = before = before + in;
@@ -617,9 +676,9 @@ struct Row {
               if (threadIdx.x == 0) S.n_list = n;
               __syncthreads();
             }
-            const int n = S.n_list;
-            walk(n, v, by_count ? (int)min((unsigned)n, (unsigned)k - before) : n, !by_count,
-                 use_p && done_p, p, pairs);
+            const int n = S.n_list, most = by_count ? (int)min((unsigned)n, (unsigned)k - before) : n;
+            if (pairs) walk(n, d, most, by_count, use_p && done_p, p);
+            else walk(n, v, most, by_count, use_p && done_p, p);
             if (threadIdx.x == 0)
               for (int r = 1; r < C; ++r) {
                 Shared* o = cl.map_shared_rank(&S, r);
@@ -632,32 +691,25 @@ struct Row {
           cl.sync();
           if (!S.again || pairs) break;
           pairs = true;
-          evaluate_pairs(f_lo, f_hi, v);
+          evaluate_pairs(f_lo, f_hi, d);
         }
         lim.t = S.t_cut;
         lim.i = S.i_cut;
-        const double z = S.z_kept;
+        const float z = S.z_kept;
         cl.sync();
         return z;
       }
       const uint32_t ka = code_of(f_lo), kz = f_hi == INFINITY ? code_of(m) : code_of(f_hi) - 1;
       if (kz <= ka) {
         // equal logits: a number of them, the lowest indices first
-        double w1 = w_of(f_lo);
+        const float w1 = w_of(f_lo);
         long long nth = (long long)k - before;
         if (!by_count) {
-          double need = (p * v[2] - v[0]) / w1;
-          if (!pairs && fabs(need - rint(need)) * w1 <= kNear * v[2]) {
-            pairs = true;
-            evaluate_pairs(f_lo, f_hi, v);
-          }
-          if (pairs) {
-            float h, l;
-            w_pair(f_lo, h, l);
-            w1 = (double)h + l;
-            need = (p * v[2] - v[0]) / w1;
-          }
-          nth = (long long)ceil(need);
+          // the first so many that bring the mass to the goal (by one division a row: in 64 bits)
+          if (!pairs) evaluate_pairs(f_lo, f_hi, d);
+          double w;
+          w_exact(f_lo, w);
+          nth = (long long)ceil((goal_of(p, d[2]) - d[0]) / w);
         }
         nth = max(1ll, min(nth, (long long)in));
         nth_equal(f_lo, nth);
@@ -665,7 +717,7 @@ struct Row {
         lim.i = S.i_cut;
         done_p = !by_count;
         cl.sync();
-        return v[0] + nth * w1;
+        return (float)v[0] * (1.f / kUnit) + nth * w1;
       }
       // 2 again: the bracket is cut by the codes of its logits
       out_lo = f_lo;
@@ -678,7 +730,7 @@ struct Row {
         if (!(l >= f_lo && l < f_hi) || l < lim.t || !left(l, i)) return -1;
         return (int)((kz - code_of(l)) >> sh);
       });
-      locate(!by_count, (unsigned)k - before, by_count ? 0. : (p * v[2] - v[0]) / v[1], [&](int b) {
+      locate(!by_count, (unsigned)k - before, share, [&](int b) {
         const uint32_t off = ((uint32_t)b << sh) + ((1u << sh) >> 1);
         return w_of(float_of(off > kz - ka ? ka : kz - off));
       });
@@ -689,7 +741,7 @@ struct Row {
       in = S.cum_in;
     }
     done_p = false;
-    return v[2];
+    return (float)v[2] * (1.f / kUnit);
   }
 };
 
@@ -750,32 +802,45 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (R.n == 0) R.groups = 0;
 
   if (tid == kThreads - 1) {  // (while the others load)
-    const double c = 1.4426950408889634074 / (double)temp;
-    S.c_hi = (float)c;
-    S.c_lo = (float)(c - (double)S.c_hi);
-    S.log_min = mp > 0.f ? (double)temp * log((double)mp) : 0.0;
+    // log2(e) = 1.44269502162933349609375 + 1.92596299112661746887e-8
+    const float h = 1.44269502162933349609375f, c = h / temp;
+    S.c_hi = c;
+    S.c_lo = (fmaf(-c, temp, h) + 1.92596299112661746887e-8f) / temp;
   }
   // the chunk into shared memory, and its maximum
   float mx = -INFINITY;
   {
     const uint4* g = reinterpret_cast<const uint4*>(src - R.shift);
     uint4* d = reinterpret_cast<uint4*>(data);
-    for (int q = tid; q < R.groups; q += kThreads) {
-      const int e0 = q * V::N - R.shift;
-      float x[V::N];
-      if (e0 >= 0 && e0 + V::N <= R.n) {
-        V::get(g[q], x);
-      } else {
+    // four loads of a thread under way
+    for (int q0 = tid; q0 < R.groups; q0 += 4 * kThreads) {
+      uint4 u[4];
 #pragma unroll
-        for (int j = 0; j < V::N; ++j)
-          x[j] = (e0 + j >= 0 && e0 + j < R.n) ? V::one(src, e0 + j) : -INFINITY;
+      for (int k = 0; k < 4; ++k) {
+        const int q = q0 + k * kThreads, e0 = q * V::N - R.shift;
+        if (e0 >= 0 && e0 + V::N <= R.n) {
+          u[k] = ld_stream(g + q);
+        } else if (q < R.groups) {
+          float x[V::N];
+#pragma unroll
+          for (int j = 0; j < V::N; ++j)
+            x[j] = (e0 + j >= 0 && e0 + j < R.n) ? V::one(src, e0 + j) : -INFINITY;
+          u[k] = V::put(x);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < V::N; ++j) {
-        x[j] = clean(x[j], V::kTop);
-        mx = fmaxf(mx, x[j]);
+      for (int k = 0; k < 4; ++k) {
+        const int q = q0 + k * kThreads;
+        if (q >= R.groups) break;
+        float x[V::N];
+        V::get(u[k], x);
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) {
+          x[j] = clean(x[j], V::kTop);
+          mx = fmaxf(mx, x[j]);
+        }
+        d[q] = V::put(x);
       }
-      d[q] = V::put(x);
     }
   }
 #pragma unroll
@@ -793,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int r = 1; r < C; ++r) m = fmaxf(m, S.cmax[r]);
   R.m = m;
   R.s = S.c_hi * kPerOctave;
+  R.nc = -S.c_hi;
   P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V + R.first : nullptr;
   const float* const noise = a.noise ? a.noise + (long long)row * a.V + R.first : nullptr;
   if (m == -INFINITY) {  // no token is left to draw from
@@ -805,14 +871,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.lim.t = -FLT_MAX;
   R.lim.i = 0x7fffffff;
   if (mp > 0.f) {
-    const double t = (double)m + S.log_min;
+    // (64 bits: a border)
+    const double t = (double)m + (double)temp * log((double)mp);
     float f = (float)t;
     if ((double)f < t) f = float_of(code_of(f + 0.f) + 1);
     R.lim.t = fmaxf(fminf(f, m), -FLT_MAX);
   }
 
   // the filters
-  double z = -1;
+  float z = -1.f;
   bool done_p = false;
   if (greedy) {
     R.nth_equal(m, 1);
@@ -821,12 +888,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (use_k) z = R.cut(k, use_p, p, done_p);
   if (use_p && !done_p) z = R.cut(0, true, p, done_p);
-  if (z < 0 && probs) {
-    double v[3];
+  if (z < 0.f && probs) {
+    mass_t v[3];
     R.evaluate(INFINITY, INFINITY, false, v);
-    z = v[2];
+    z = (float)v[2] * (1.f / kUnit);
   }
-  const float inv = probs ? (float)(1.0 / z) : 0.f;
+  const float inv = probs ? 1.f / z : 0.f;
 
   // the distribution, and each thread's two best in the race
   float b1 = -1.f, b2 = -1.f;
@@ -871,15 +938,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   float top = S.c_best[0];
   for (int r = 1; r < C; ++r) top = fmaxf(top, S.c_best[r]);
   const float near = top * (1.f - 0x1p-16f);  // (fp32's error is 2^-18 at most)
+  // mostly there is one
+  const bool near1 = i1 != 0x7fffffff && b1 >= near, near2 = i2 != 0x7fffffff && b2 >= near;
+  int n_near = __syncthreads_count(near1) + __syncthreads_count(near2);
+  if (tid < C) cl.map_shared_rank(&S, tid)->n_near[rank] = n_near;
+  cl.sync();
+  n_near = 0;
+  for (int r = 0; r < C; ++r) n_near += S.n_near[r];
+  if (n_near == 1) {
+    if (near1) a.tokens[row] = R.first + i1;
+    return;
+  }
   double rs = -INFINITY;
   int ri = 0x7fffffff;
-  auto precise = [&](float b, int i) {
-    if (i == 0x7fffffff || !(b >= near)) return;
+  auto precise = [&](bool is, int i) {
+    if (!is) return;
     const double l = V::one(data, i + R.shift);
     better(rs, ri, (l - (double)m) / (double)temp - log((double)noise[i]), R.first + i);
   };
-  precise(b1, i1);
-  precise(b2, i2);
+  precise(near1, i1);
+  precise(near2, i2);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     better(rs, ri, __shfl_xor_sync(0xffffffffu, rs, o), __shfl_xor_sync(0xffffffffu, ri, o));

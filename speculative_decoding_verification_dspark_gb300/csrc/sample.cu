@@ -77,7 +77,6 @@ struct Shared {
   float f_lo, f_hi, t_cut;
   int i_cut, n_keep, again;
   float z_kept;
-  float best[kWarps];
   int n_near[kMaxCluster];             // of each CTA: tokens near the race's best
   double r_best[kWarps];
   int r_idx[kWarps];
@@ -162,6 +161,21 @@ struct Kept {    // tokens with l > t, or l == t and an index of at most i
   int i;
 };
 
+// A thread's two best in the race, the lower index first among equals as they come.
+constexpr int kNone = 0x7fffffff;
+struct Racer {
+  float s1 = -1.f, s2 = -1.f, l1 = 0.f, l2 = 0.f;
+  int i1 = kNone, i2 = kNone;
+  __device__ __forceinline__ void take(float s, float l, int i) {
+    if (s > s1) {
+      s2 = s1; l2 = l1; i2 = i1;
+      s1 = s; l1 = l; i1 = i;
+    } else if (s > s2) {
+      s2 = s; l2 = l; i2 = i;
+    }
+  }
+};
+
 template <typename T>
 struct Row {
   using V = Vec<T>;
@@ -169,12 +183,15 @@ struct Row {
   Shared& S;
   const T* data;      // slots of this CTA's chunk in shared memory
   int C, rank;
-  int first, n;       // the chunk: tokens first .. first + n - 1
+  int first, n;       // the chunk: tokens first .. first + n - 1,
+  int n_row;          // of so many
   int shift, groups;  // token i of the chunk is slot i + shift; 16-byte groups of slots
   int set;            // of S.part
   float m, s, nc;     // largest logit; buckets and (negative) octaves per unit of logit
   float t_min;        // least logit that min-p leaves
   Kept lim;           // what earlier filters left
+  mass_t whole;       // its mass (weigh)
+  bool listed;        // it is the first S.n_keep tokens of the first CTA's list
 
   // (rounded by the addition of 2^23: monotone in l, which is all that is asked)
   __device__ __forceinline__ int bucket_of(float l) const {
@@ -194,6 +211,23 @@ struct Row {
       V::get(p[q], x);
 #pragma unroll
       for (int j = 0; j < V::N; ++j) fn(x[j], q * V::N + j - shift, j);
+    }
+  }
+
+  // fn(l, i) for the tokens with l >= least: groups without one cost a maximum each.
+  template <class Fn>
+  __device__ __forceinline__ void each_from(float least, Fn&& fn) const {
+    const uint4* p = reinterpret_cast<const uint4*>(data);
+    for (int q = threadIdx.x; q < groups; q += kThreads) {
+      float x[V::N];
+      V::get(p[q], x);
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < V::N; ++j) top = fmaxf(top, x[j]);
+      if (top >= least)
+#pragma unroll
+        for (int j = 0; j < V::N; ++j)
+          if (x[j] >= least) fn(x[j], q * V::N + j - shift);
     }
   }
 
@@ -356,26 +390,33 @@ struct Row {
     return float_of(hi);
   }
 
-  // Masses of the tokens left: above f_hi, in [f_lo, f_hi), and all; those of the bracket are listed
-  // in S.list where `gather` is set.
-  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
+  // The mass of the tokens left, into `whole`.
+  __device__ void weigh() {
+    float all[2] = {0.f, 0.f};
+    if (lim.t == -FLT_MAX) {
+      each([&](float l, int, int j) { all[j & 1] += w_of(l); });
+    } else {
+      each_from(lim.t, [&](float l, int i) {
+        if (left(l, i)) all[0] += w_of(l);
+      });
+    }
+    mass_t v[3] = {__float2ll_rn((all[0] + all[1]) * kUnit), 0, 0};
+    sum3(v);
+    whole = v[0];
+  }
+  // Lists the tokens left with f_lo <= l < f_hi; returns this thread's mass of those above f_hi and
+  // adds that of the listed ones to `in`.
+  __device__ __forceinline__ float list_from(float f_lo, float f_hi, bool gather, float& in) {
     __syncthreads();
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
-    if (lim.i != 0x7fffffff) sums<true>(f_lo, f_hi, gather, v);
-    else sums<false>(f_lo, f_hi, gather, v);
-    sum3(v);
-  }
-  template <bool LIMITED>
-  __device__ __forceinline__ void sums(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
-    float above[2] = {0.f, 0.f}, all[2] = {0.f, 0.f}, in = 0.f;
-    const float least = lim.t;
-    each([&](float l, int i, int j) {
-      float w = w_of(l);
-      if (LIMITED ? !left(l, i) : l < least) w = 0.f;
-      all[j & 1] += w;
-      above[j & 1] += l >= f_hi ? w : 0.f;
-      if (l >= f_lo && l < f_hi && (LIMITED ? left(l, i) : l >= least)) {
+    float above = 0.f;
+    each_from(f_lo, [&](float l, int i) {
+      if (!left(l, i)) return;
+      const float w = w_of(l);
+      if (l >= f_hi) {
+        above += w;
+      } else {
         in += w;
         if (gather) {
           const int at = atomicAdd(&S.n_list, 1);
@@ -383,9 +424,18 @@ struct Row {
         }
       }
     });
-    v[0] = __float2ll_rn((above[0] + above[1]) * kUnit);
+    return above;
+  }
+  // Masses of the tokens left: above f_hi, in [f_lo, f_hi), and all; those of the bracket are listed
+  // in S.list where `gather` is set.
+  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
+    float in = 0.f;
+    const float above = list_from(fmaxf(f_lo, lim.t), f_hi, gather, in);
+    v[0] = __float2ll_rn(above * kUnit);
     v[1] = __float2ll_rn(in * kUnit);
-    v[2] = __float2ll_rn((all[0] + all[1]) * kUnit);
+    v[2] = 0;
+    sum3(v);
+    v[2] = whole;
   }
 
   // w in two parts, 2^-36 of it or better, by table and polynomial (Tang's scheme for the
@@ -461,22 +511,30 @@ struct Row {
       n += k;
     }
     n = min(n, kList);
-    int size = 32;
+    int size = 64;
     while (size < n) size <<= 1;
     for (int i = n + threadIdx.x; i < size; i += kThreads) S.list[i] = ~0ull;
     __syncthreads();
-    for (int k = 2; k <= size; k <<= 1)
-      for (int d = k >> 1; d > 0; d >>= 1) {
-        for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-          const int a = 2 * i - (i & (d - 1)), b = a + d;
-          const uint64_t x = S.list[a], y = S.list[b];
-          if ((x > y) == ((a & k) == 0)) {
-            S.list[a] = y;
-            S.list[b] = x;
-          }
-        }
-        __syncthreads();
+    // bitonic; a warp has 64 places to itself while the distance is below 64
+    auto step = [&](int i, int k, int d) {
+      const int a = 2 * i - (i & (d - 1)), b = a + d;
+      const uint64_t x = S.list[a], y = S.list[b];
+      if ((x > y) == ((a & k) == 0)) {
+        S.list[a] = y;
+        S.list[b] = x;
       }
+    };
+    const int i = threadIdx.x;
+    static_assert(kList == 2 * kThreads, "one pair a thread");
+    for (int k = 2; k <= size; k <<= 1) {
+      for (int d = k >> 1; d > 0; d >>= 1) {
+        if (i < size / 2) step(i, k, d);
+        if (d > 32) __syncthreads();
+        else __syncwarp();
+      }
+      if (k >= 64 && k < size) __syncthreads();
+    }
+    __syncthreads();
     return n;
   }
 
@@ -593,10 +651,158 @@ struct Row {
     cl.sync();
   }
 
-  // One filter's end (k > 0: top-k, with top-p at once where the list holds all that top-k keeps;
-  // else top-p of what is left).  Sets lim; returns the mass kept; done_p: top-p is applied.
-  __device__ float cut(int k, bool use_p, float p, bool& done_p) {
+  // The end within a bracket whose tokens all CTAs have listed (kList in all at most): by the first
+  // CTA, `before` tokens and masses v (d, where `pairs`) above it as in walk.  Sets lim and listed;
+  // returns the mass kept.
+  __device__ float resolve(float f_lo, float f_hi, const mass_t (&v)[3], double (&d)[3], bool pairs,
+                           unsigned before, int k, bool use_p, float p) {
     const bool by_count = k > 0;
+    for (int pass = 0;; ++pass) {
+      if (rank == 0) {
+        if (pass == 0) {
+          const int n = collect();
+          if (threadIdx.x == 0) S.n_list = n;
+          __syncthreads();
+        }
+        const int n = S.n_list, most = by_count ? (int)min((unsigned)n, (unsigned)k - before) : n;
+        if (pairs) walk(n, d, most, by_count, use_p, p);
+        else walk(n, v, most, by_count, use_p, p);
+        if (threadIdx.x > 0 && threadIdx.x < C) {
+          Shared* o = cl.map_shared_rank(&S, threadIdx.x);
+          o->t_cut = S.t_cut;
+          o->i_cut = S.i_cut;
+          o->z_kept = S.z_kept;
+          o->again = S.again;
+        }
+      }
+      cl.sync();
+      if (!S.again || pairs) break;
+      pairs = true;
+      if (by_count) d[0] = d[1] = d[2] = 0;  // (the list has it all)
+      else evaluate_pairs(f_lo, f_hi, d);
+    }
+    lim.t = S.t_cut;
+    lim.i = S.i_cut;
+    whole = -1;
+    listed = before == 0;
+    return S.z_kept;
+  }
+
+  // The filter's end where all that may be kept fits the list, without buckets: a bound from below is
+  // known before the row is searched.  false: it does not fit (or there is no bound).
+  __device__ bool cut_short(int k, bool use_p, float p, float mx, float& z) {
+    float least;
+    if (k > 0) {
+      // k threads' own maxima from `least` on: so are k tokens
+      if (k > kThreads) return false;
+      uint32_t lo = code_of(-INFINITY), hi = code_of(m);  // at least k from lo on, or lo is no bound
+      const uint32_t mine = code_of(mx);
+      for (int i = 0; i < 16 && hi - lo > 1; ++i) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (__syncthreads_count(mine >= mid) >= k) lo = mid; else hi = mid;
+      }
+      least = float_of(lo);
+    } else {
+      // n tokens below weigh less than n w(least): the part 1 - p of the whole lies above that
+      const float x = log2f(2.f * n_row / ((1.f - p) * ((float)whole * (1.f / kUnit))));
+      least = m + fmaxf(x, 0.f) / nc;
+    }
+    least = fmaxf(least, lim.t);
+    mass_t v[3] = {0, 0, whole};
+    double d[3];
+    float in = 0.f;
+    list_from(least, INFINITY, true, in);
+    cl.sync();
+    unsigned n = 0;
+    for (int r = 0; r < C; ++r) n += (unsigned)cl.map_shared_rank(&S, r)->n_list;
+    if (n > (unsigned)kList) {
+      cl.sync();  // (n_list is read)
+      return false;
+    }
+    z = resolve(least, INFINITY, v, d, false, 0, k, use_p, p);
+    return true;
+  }
+
+  // The chunk's probabilities w inv (probs and noise: of the whole row), and the race.
+  template <typename P, bool RACE>
+  __device__ __forceinline__ void distribute(P* probs, const float* noise, float inv, Racer& b) const {
+    P* const out = probs + first - shift;              // of slot 0
+    const float* const e = noise + first - shift;
+    const bool out_wide = (reinterpret_cast<uintptr_t>(out) & (sizeof(P) * V::N - 1) & 15) == 0;
+    const bool e_wide = RACE && (reinterpret_cast<uintptr_t>(e) & 15) == 0;
+    const uint4* p = reinterpret_cast<const uint4*>(data);
+    for (int q = threadIdx.x; q < groups; q += kThreads) {
+      const int s0 = q * V::N;
+      float x[V::N], w[V::N];
+      V::get(p[q], x);
+      bool any = false, every = true;
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) {
+        const bool keep = left(x[j], s0 + j - shift);
+        w[j] = keep ? w_of(x[j]) : 0.f;
+        any |= keep;
+        every &= keep;
+      }
+      const bool inside = s0 >= shift && s0 + V::N <= shift + n;
+      if (out_wide && inside) {
+        store_group<P>(out + s0, w, inv);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V::N; ++j)
+          if (s0 + j >= shift && s0 + j < shift + n) out[s0 + j] = P(w[j] * inv);
+      }
+      if (RACE && any) {
+        float f[V::N];
+        if (e_wide && inside && every) {
+#pragma unroll
+          for (int j = 0; j < V::N; j += 4) {
+            const uint4 u = ld_stream(reinterpret_cast<const uint4*>(e + s0 + j));
+            f[j] = __uint_as_float(u.x);
+            f[j + 1] = __uint_as_float(u.y);
+            f[j + 2] = __uint_as_float(u.z);
+            f[j + 3] = __uint_as_float(u.w);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V::N; ++j) f[j] = left(x[j], s0 + j - shift) ? e[s0 + j] : 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V::N; ++j)
+          if (left(x[j], s0 + j - shift)) b.take(__fdividef(w[j], f[j]), x[j], first + s0 + j - shift);
+      }
+    }
+  }
+  template <typename P>
+  static __device__ __forceinline__ void store_group(P* to, const float (&w)[V::N], float inv) {
+    if constexpr (sizeof(P) == 4) {
+#pragma unroll
+      for (int j = 0; j < V::N; j += 4)
+        __stcs(reinterpret_cast<float4*>(to + j),
+               make_float4(w[j] * inv, w[j + 1] * inv, w[j + 2] * inv, w[j + 3] * inv));
+    } else {
+      uint32_t u[V::N / 2];
+#pragma unroll
+      for (int j = 0; j < V::N / 2; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(w[2 * j] * inv, w[2 * j + 1] * inv);
+        u[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if constexpr (V::N == 8) __stcs(reinterpret_cast<uint4*>(to), make_uint4(u[0], u[1], u[2], u[3]));
+      else __stcs(reinterpret_cast<uint2*>(to), make_uint2(u[0], u[1]));
+    }
+  }
+
+  // One filter's end (k > 0: top-k, with top-p at once where the list holds all that top-k keeps;
+  // else top-p of what is left).  Sets lim; returns the mass kept; done_p: top-p is applied.  mx:
+  // the largest logit of this thread's tokens.
+  __device__ float cut(int k, bool use_p, float p, float mx, bool& done_p) {
+    const bool by_count = k > 0;
+    listed = false;
+    if (!by_count && whole < 0) weigh();
+    float z_short;
+    if (cut_short(k, use_p, p, mx, z_short)) {
+      done_p = true;
+      return z_short;
+    }
     // 1: buckets of (m - l) / T
     histogram([&](float l, int i) {
       return l < lim.t || !left(l, i) ? -1 : bucket_of(l);
@@ -667,37 +873,9 @@ struct Row {
         }
       }
       if (gather) {
-        // 3: the list, by the first CTA
+        // 3: the list
         done_p = !by_count || before == 0;
-        for (int pass = 0;; ++pass) {
-          if (rank == 0) {
-            if (pass == 0) {
-              const int n = collect();
-              if (threadIdx.x == 0) S.n_list = n;
-              __syncthreads();
-            }
-            const int n = S.n_list, most = by_count ? (int)min((unsigned)n, (unsigned)k - before) : n;
-            if (pairs) walk(n, d, most, by_count, use_p && done_p, p);
-            else walk(n, v, most, by_count, use_p && done_p, p);
-            if (threadIdx.x == 0)
-              for (int r = 1; r < C; ++r) {
-                Shared* o = cl.map_shared_rank(&S, r);
-                o->t_cut = S.t_cut;
-                o->i_cut = S.i_cut;
-                o->z_kept = S.z_kept;
-                o->again = S.again;
-              }
-          }
-          cl.sync();
-          if (!S.again || pairs) break;
-          pairs = true;
-          evaluate_pairs(f_lo, f_hi, d);
-        }
-        lim.t = S.t_cut;
-        lim.i = S.i_cut;
-        const float z = S.z_kept;
-        cl.sync();
-        return z;
+        return resolve(f_lo, f_hi, v, d, pairs, before, k, use_p && done_p, p);
       }
       const uint32_t ka = code_of(f_lo), kz = f_hi == INFINITY ? code_of(m) : code_of(f_hi) - 1;
       if (kz <= ka) {
@@ -715,6 +893,7 @@ struct Row {
         nth_equal(f_lo, nth);
         lim.t = f_lo;
         lim.i = S.i_cut;
+        whole = -1;
         done_p = !by_count;
         cl.sync();
         return (float)v[0] * (1.f / kUnit) + nth * w1;
@@ -741,9 +920,21 @@ struct Row {
       in = S.cum_in;
     }
     done_p = false;
-    return (float)v[2] * (1.f / kUnit);
+    return (float)v[0] * (1.f / kUnit);
   }
 };
+
+__device__ __forceinline__ float block_max(Shared& S, float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) S.wmax[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = S.wmax[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v = fmaxf(v, S.wmax[w]);
+  return v;
+}
 
 // (score, index) of the better: higher score, lower index.
 __device__ __forceinline__ void better(double& s, int& i, double s2, int i2) {
@@ -796,6 +987,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.first = min(a.V, rank * chunk);
   R.n = min(a.V, R.first + chunk) - R.first;
   R.set = 0;
+  R.n_row = a.V;
+  R.whole = -1;
+  R.listed = false;
   const T* src = static_cast<const T*>(a.logits) + row * a.stride + R.first;
   R.shift = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
   R.groups = (R.n + R.shift + V::N - 1) / V::N;
@@ -843,27 +1037,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) S.wmax[wid] = mx;
-  __syncthreads();
+  const float mx_cta = block_max(S, mx);
   cl.barrier_wait();
-  if (tid < C) {
-    float v = S.wmax[0];
-    for (int w = 1; w < kWarps; ++w) v = fmaxf(v, S.wmax[w]);
-    cl.map_shared_rank(&S, tid)->cmax[rank] = v;
-  }
+  if (tid < C) cl.map_shared_rank(&S, tid)->cmax[rank] = mx_cta;
   cl.sync();
   float m = S.cmax[0];
   for (int r = 1; r < C; ++r) m = fmaxf(m, S.cmax[r]);
   R.m = m;
   R.s = S.c_hi * kPerOctave;
   R.nc = -S.c_hi;
-  P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V + R.first : nullptr;
-  const float* const noise = a.noise ? a.noise + (long long)row * a.V + R.first : nullptr;
+  P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V : nullptr;
+  const float* const noise = a.noise ? a.noise + (long long)row * a.V : nullptr;
   if (m == -INFINITY) {  // no token is left to draw from
     if (probs)
-      for (int i = tid; i < R.n; i += kThreads) probs[i] = P(0.f);
+      for (int i = tid; i < R.n; i += kThreads) probs[R.first + i] = P(0.f);
     if (a.tokens && rank == 0 && tid == 0) a.tokens[row] = -1;
     cl.sync();
     return;
@@ -885,82 +1072,71 @@ __global__ void __launch_bounds__(kThreads, 2)
     R.nth_equal(m, 1);
     R.lim.t = m;
     R.lim.i = S.i_cut;
+    z = 1.f;
   }
-  if (use_k) z = R.cut(k, use_p, p, done_p);
-  if (use_p && !done_p) z = R.cut(0, true, p, done_p);
+  if (use_k) z = R.cut(k, use_p, p, mx, done_p);
+  if (use_p && !done_p) z = R.cut(0, true, p, mx, done_p);
+  const bool race = a.tokens != nullptr;
+  if (greedy && race && rank == 0 && tid == 0) a.tokens[row] = S.i_cut;
+  if (!probs && (greedy || (R.listed && rank != 0))) return;
   if (z < 0.f && probs) {
-    mass_t v[3];
-    R.evaluate(INFINITY, INFINITY, false, v);
-    z = (float)v[2] * (1.f / kUnit);
+    R.weigh();
+    z = (float)R.whole * (1.f / kUnit);
   }
-  const float inv = probs ? 1.f / z : 0.f;
 
   // the distribution, and each thread's two best in the race
-  float b1 = -1.f, b2 = -1.f;
-  int i1 = 0x7fffffff, i2 = 0x7fffffff;
-  const bool race = a.tokens != nullptr;
-  if (race || probs) {
-    for (int i = tid; i < R.n; i += kThreads) {
-      const float l = V::one(data, i + R.shift);
-      const bool keep = R.left(l, i);
-      const float w = keep ? R.w_of(l) : 0.f;
-      if (probs) probs[i] = P(w * inv);
-      if (race && keep) {
-        const float sc = __fdividef(w, noise[i]);
-        if (sc > b1) {
-          b2 = b1;
-          i2 = i1;
-          b1 = sc;
-          i1 = i;
-        } else if (sc > b2) {
-          b2 = sc;
-          i2 = i;
-        }
-      }
+  Racer b;
+  const bool solo = !probs && R.listed;  // the list's tokens alone, by the first CTA
+  if (solo) {
+    for (int i = tid; i < S.n_keep; i += kThreads) {
+      const float l = R.list_l(i);
+      const int at = (int)(uint32_t)S.list[i];
+      b.take(__fdividef(R.w_of(l), noise[at]), l, at);
     }
+  } else if (probs) {
+    if (race && !greedy) R.template distribute<P, true>(probs, noise, 1.f / z, b);
+    else R.template distribute<P, false>(probs, noise, 1.f / z, b);
+  } else {
+    R.each_from(R.lim.t, [&](float l, int i) {
+      if (R.left(l, i)) b.take(__fdividef(R.w_of(l), noise[R.first + i]), l, R.first + i);
+    });
   }
-  if (!race) {
+  if (!race || greedy) return;
+
+  // the best in fp32: mostly nothing comes near it (fp32's error is 2^-18 at most)
+  const float top_cta = block_max(S, b.s1);
+  constexpr float kClose = 1.f - 0x1p-16f;
+  auto close = [&](float s, int i, float top) { return i != kNone && s >= top * kClose; };
+  int n_near = __syncthreads_count(close(b.s1, b.i1, top_cta)) + __syncthreads_count(close(b.s2, b.i2, top_cta));
+  float top = top_cta;
+  if (!solo) {
+    if (tid < C) {
+      Shared* o = cl.map_shared_rank(&S, tid);
+      o->c_best[rank] = top_cta;
+      o->n_near[rank] = n_near;
+    }
     cl.sync();
-    return;
+    for (int r = 0; r < C; ++r) top = fmaxf(top, S.c_best[r]);
+    n_near = 0;
+    for (int r = 0; r < C; ++r) n_near += S.c_best[r] >= top * kClose ? S.n_near[r] : 0;
   }
-  // the best in fp32, then in 64 bits among those that come near it
-  float bb = b1;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bb = fmaxf(bb, __shfl_xor_sync(0xffffffffu, bb, o));
-  if (lane == 0) S.best[wid] = bb;
-  __syncthreads();
-  if (tid < C) {
-    float v = S.best[0];
-    for (int w = 1; w < kWarps; ++w) v = fmaxf(v, S.best[w]);
-    cl.map_shared_rank(&S, tid)->c_best[rank] = v;
-  }
-  cl.sync();
-  float top = S.c_best[0];
-  for (int r = 1; r < C; ++r) top = fmaxf(top, S.c_best[r]);
-  const float near = top * (1.f - 0x1p-16f);  // (fp32's error is 2^-18 at most)
-  // mostly there is one
-  const bool near1 = i1 != 0x7fffffff && b1 >= near, near2 = i2 != 0x7fffffff && b2 >= near;
-  int n_near = __syncthreads_count(near1) + __syncthreads_count(near2);
-  if (tid < C) cl.map_shared_rank(&S, tid)->n_near[rank] = n_near;
-  cl.sync();
-  n_near = 0;
-  for (int r = 0; r < C; ++r) n_near += S.n_near[r];
   if (n_near == 1) {
-    if (near1) a.tokens[row] = R.first + i1;
+    if (close(b.s1, b.i1, top)) a.tokens[row] = b.i1;
     return;
   }
+  // else in 64 bits, among those that come near
   double rs = -INFINITY;
-  int ri = 0x7fffffff;
-  auto precise = [&](bool is, int i) {
-    if (!is) return;
-    const double l = V::one(data, i + R.shift);
-    better(rs, ri, (l - (double)m) / (double)temp - log((double)noise[i]), R.first + i);
+  int ri = kNone;
+  auto precise = [&](float s, float l, int i) {
+    if (close(s, i, top))
+      better(rs, ri, ((double)l - (double)m) / (double)temp - log((double)noise[i]), i);
   };
-  precise(near1, i1);
-  precise(near2, i2);
+  precise(b.s1, b.l1, b.i1);
+  precise(b.s2, b.l2, b.i2);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     better(rs, ri, __shfl_xor_sync(0xffffffffu, rs, o), __shfl_xor_sync(0xffffffffu, ri, o));
+  __syncthreads();
   if (lane == 0) {
     S.r_best[wid] = rs;
     S.r_idx[wid] = ri;
@@ -972,12 +1148,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     o->cr_best[rank] = rs;
     o->cr_idx[rank] = ri;
   }
-  cl.sync();
+  if (solo) __syncthreads();
+  else cl.sync();
   if (rank == 0 && tid == 0) {
     rs = S.cr_best[0];
     ri = S.cr_idx[0];
-    for (int r = 1; r < C; ++r) better(rs, ri, S.cr_best[r], S.cr_idx[r]);
-    a.tokens[row] = ri == 0x7fffffff ? -1 : ri;
+    for (int r = 1; r < (solo ? 1 : C); ++r) better(rs, ri, S.cr_best[r], S.cr_idx[r]);
+    a.tokens[row] = ri == kNone ? -1 : ri;
   }
 }
 

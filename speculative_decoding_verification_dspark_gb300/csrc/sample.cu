@@ -189,7 +189,8 @@ struct Row {
   int set;            // of S.part
   float m, s, nc;     // largest logit; buckets and (negative) octaves per unit of logit
   float t_min;        // least logit that min-p leaves
-  Kept lim;           // what earlier filters left
+  Kept lim;           // what earlier filters left, and of that what this one may keep
+  Kept lim_all;       // what earlier filters left
   mass_t whole;       // its mass (weigh)
   bool listed;        // it is the first S.n_keep tokens of the first CTA's list
 
@@ -269,7 +270,7 @@ struct Row {
     __syncthreads();
     for (int b = threadIdx.x; b < kBuckets; b += kThreads) S.hist[b] = 0;
     __syncthreads();
-    each([&](float l, int i, int) {
+    each_from(lim.t, [&](float l, int i) {
       const int b = bucket(l, i);
       if (b >= 0) atomicAdd(&S.hist[b], 1u);
     });
@@ -372,10 +373,16 @@ struct Row {
   }
 
   // The least float l with a bucket below `bound`; buckets fall as l grows, so 32 lanes halve the codes
-  // five bits at a time.  By the first warp.
+  // five bits at a time.  By a warp.
   __device__ float edge(int bound) const {
     const int lane = threadIdx.x & 31;
     uint32_t lo = code_of(-FLT_MAX), hi = code_of(m);  // (bucket 0)
+    // a few roundings around the inverse, if it lies between them: two rounds in place of seven
+    const float at = m - (bound - 0.5f) / s, off = 4e-7f * (fabsf(m) + fabsf(at));
+    if (at - off > -FLT_MAX && at + off < m && bucket_of(at + off) < bound && bucket_of(at - off) >= bound) {
+      lo = code_of(at - off + 0.f);
+      hi = code_of(at + off + 0.f);
+    }
     while (hi > lo) {
       const uint32_t step = (hi - lo + 31) / 32, at = lo + min((unsigned)lane * step, hi - lo);
       const unsigned ok = __ballot_sync(0xffffffffu, bucket_of(float_of(at)) < bound);
@@ -418,7 +425,8 @@ struct Row {
         above += w;
       } else {
         in += w;
-        if (gather) {
+        // (a list that is full counts no further)
+        if (gather && *(volatile int*)&S.n_list <= kList) {
           const int at = atomicAdd(&S.n_list, 1);
           if (at < kList) S.list[at] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
         }
@@ -480,7 +488,7 @@ struct Row {
       sh = t;
     };
     each([&](float l, int i, int) {
-      if (l < lim.t || !left(l, i)) return;
+      if (l < lim_all.t || (l == lim_all.t && first + i > lim_all.i)) return;
       float wh, wl;
       w_pair(l, wh, wl);
       if (l >= f_hi) add(ah, al, wh, wl);
@@ -501,16 +509,32 @@ struct Row {
 
   // The lists of all CTAs into this one's, sorted; n tokens in all (at most kList).
   __device__ int collect() {
-    int n = S.n_list;  // (every rank's was written before the last cl.sync)
-    __syncthreads();
-    for (int r = 1; r < C; ++r) {
-      Shared* o = cl.map_shared_rank(&S, r);
-      const int k = o->n_list;
-      for (int i = threadIdx.x; i < k; i += kThreads)
-        if (n + i < kList) S.list[n + i] = o->list[i];
-      n += k;
+    // (every rank's list was written before the last cl.sync); token i of all of them
+    int n = 0, from[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      from[r] = n;
+      n += r < C ? cl.map_shared_rank(&S, r)->n_list : 0;
     }
     n = min(n, kList);
+    uint64_t mine[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      int r = 0;
+#pragma unroll
+      for (int q = 1; q < kMaxCluster; ++q)
+        if (q < C && i >= from[q]) r = q;
+      int base = 0;
+#pragma unroll
+      for (int q = 1; q < kMaxCluster; ++q)
+        if (q == r) base = from[q];
+      if (i < n) mine[j] = cl.map_shared_rank(&S, r)->list[i - base];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (threadIdx.x + j * kThreads < n) S.list[threadIdx.x + j * kThreads] = mine[j];
     int size = 64;
     while (size < n) size <<= 1;
     for (int i = n + threadIdx.x; i < size; i += kThreads) S.list[i] = ~0ull;
@@ -688,39 +712,22 @@ struct Row {
     return S.z_kept;
   }
 
-  // The filter's end where all that may be kept fits the list, without buckets: a bound from below is
-  // known before the row is searched.  false: it does not fit (or there is no bound).
-  __device__ bool cut_short(int k, bool use_p, float p, float mx, float& z) {
-    float least;
+  // A logit below which the filter keeps nothing, from what is known before the row is searched.
+  __device__ float bound(int k, float p, float mx) {
+    if (k > kThreads) return lim.t;
     if (k > 0) {
-      // k threads' own maxima from `least` on: so are k tokens
-      if (k > kThreads) return false;
-      uint32_t lo = code_of(-INFINITY), hi = code_of(m);  // at least k from lo on, or lo is no bound
+      // k threads' own maxima lie from there on: so do k tokens
+      uint32_t lo = code_of(-INFINITY), hi = code_of(m);
       const uint32_t mine = code_of(mx);
       for (int i = 0; i < 16 && hi - lo > 1; ++i) {
         const uint32_t mid = lo + (hi - lo) / 2;
         if (__syncthreads_count(mine >= mid) >= k) lo = mid; else hi = mid;
       }
-      least = float_of(lo);
-    } else {
-      // n tokens below weigh less than n w(least): the part 1 - p of the whole lies above that
-      const float x = log2f(2.f * n_row / ((1.f - p) * ((float)whole * (1.f / kUnit))));
-      least = m + fmaxf(x, 0.f) / nc;
+      return fmaxf(float_of(lo), lim.t);
     }
-    least = fmaxf(least, lim.t);
-    mass_t v[3] = {0, 0, whole};
-    double d[3];
-    float in = 0.f;
-    list_from(least, INFINITY, true, in);
-    cl.sync();
-    unsigned n = 0;
-    for (int r = 0; r < C; ++r) n += (unsigned)cl.map_shared_rank(&S, r)->n_list;
-    if (n > (unsigned)kList) {
-      cl.sync();  // (n_list is read)
-      return false;
-    }
-    z = resolve(least, INFINITY, v, d, false, 0, k, use_p, p);
-    return true;
+    // n tokens below weigh less than n times that one's w: the part 1 - p of the whole lies above
+    const float x = log2f(2.f * n_row / ((1.f - p) * ((float)whole * (1.f / kUnit))));
+    return fmaxf(m + fmaxf(x, 0.f) / nc, lim.t);
   }
 
   // The chunk's probabilities w inv (probs and noise: of the whole row), and the race.
@@ -797,17 +804,45 @@ struct Row {
   __device__ float cut(int k, bool use_p, float p, float mx, bool& done_p) {
     const bool by_count = k > 0;
     listed = false;
+    lim_all = lim;
+    mass_t v[3];    // masses in fixed point from fp32,
+    double d[3];    // or, once those have not told, from pairs
+    bool pairs = false;
     if (!by_count && whole < 0) weigh();
-    float z_short;
-    if (cut_short(k, use_p, p, mx, z_short)) {
-      done_p = true;
-      return z_short;
+    // 0: what may be kept at all: mostly it fits the list
+    const float least = bound(k, p, mx);
+    if (least > lim.t || lim.t > -FLT_MAX) {
+      if (least > lim.t) {
+        lim.t = least;
+        lim.i = kNone;
+      }
+      float sum[2] = {0.f, 0.f};
+      int count = 0;
+      each([&](float l, int i, int j) {
+        const bool in = left(l, i);
+        count += in;
+        sum[j & 1] += in ? w_of(l) : 0.f;
+      });
+      v[0] = count;
+      v[1] = __float2ll_rn((sum[0] + sum[1]) * kUnit);
+      v[2] = 0;
+      sum3(v);
+      if (v[0] <= kList) {
+        float in = 0.f;
+        list_from(lim.t, INFINITY, true, in);
+        cl.sync();
+        done_p = true;
+        v[0] = 0;
+        v[2] = whole;
+        return resolve(lim.t, INFINITY, v, d, false, 0, k, use_p, p);
+      }
+    } else {
+      v[1] = whole;
     }
     // 1: buckets of (m - l) / T
-    histogram([&](float l, int i) {
-      return l < lim.t || !left(l, i) ? -1 : bucket_of(l);
-    });
-    locate(!by_count, (unsigned)k, p, [](int b) { return ex2(b * (-1.f / kPerOctave)); });
+    histogram([&](float l, int i) { return left(l, i) ? bucket_of(l) : -1; });
+    float share = by_count ? 0.f : p * ((float)whole / (float)v[1]);  // of what lies in the buckets
+    locate(!by_count, (unsigned)k, share, [](int b) { return ex2(b * (-1.f / kPerOctave)); });
     // 2: the bracket [f_lo, f_hi): `before` tokens above it, `in` in it, of `total`
     unsigned before = S.cum_before, in = S.cum_in;
     const unsigned total = S.total;
@@ -817,22 +852,17 @@ struct Row {
       before = 0;
     }
     if (threadIdx.x < 32) {
-      const float lo = b1 == kBuckets - 1 ? -FLT_MAX : edge(b1 + 1);
+      const float lo = b1 == kBuckets - 1 ? lim.t : fmaxf(edge(b1 + 1), lim.t);
+      if (threadIdx.x == 0) S.f_lo = lo;
+    } else if (threadIdx.x < 64) {
       const float hi = b0 == 0 ? INFINITY : edge(b0);
-      if (threadIdx.x == 0) {
-        S.f_lo = lo;
-        S.f_hi = hi;
-      }
+      if (threadIdx.x == 32) S.f_hi = hi;
     }
     __syncthreads();
     float f_lo = S.f_lo, f_hi = S.f_hi;
     // the end lies in [out_lo, out_hi), with out_before tokens above and out_below below
-    float out_lo = -FLT_MAX, out_hi = INFINITY;
+    float out_lo = lim.t, out_hi = INFINITY;
     unsigned out_before = 0, out_below = 0;
-    bool pairs = false;
-    mass_t v[3];    // masses in fixed point from fp32,
-    double d[3];    // or, once those have not told, from pairs
-    float share = 0.f;
     // (each round halves the outer range at least once or cuts it into 2048: far fewer are needed)
     for (int round = 0; round < 100; ++round) {
       const bool gather = in <= (unsigned)kList;
@@ -906,7 +936,7 @@ struct Row {
       int sh = 0;
       while (((kz - ka) >> sh) >= (uint32_t)kBuckets) ++sh;
       histogram([&](float l, int i) {
-        if (!(l >= f_lo && l < f_hi) || l < lim.t || !left(l, i)) return -1;
+        if (!(l >= f_lo && l < f_hi) || !left(l, i)) return -1;
         return (int)((kz - code_of(l)) >> sh);
       });
       locate(!by_count, (unsigned)k - before, share, [&](int b) {
@@ -957,30 +987,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_release();
   pdl_wait();
 
-  // the row's parameters (every decision below is the same in all threads of the cluster)
   const int req = a.row_req ? a.row_req[row] : row;
-  if (req < 0) return;
-  bool bad = req >= a.B;
-  float temp = 1.f, p = 1.f, mp = 0.f;
-  int k = 0;
-  if (!bad) {
-    if (a.temperature) temp = a.temperature[req];
-    if (a.top_k) k = a.top_k[req];
-    if (a.top_p) p = a.top_p[req];
-    if (a.min_p) mp = a.min_p[req];
-    bad = !(temp == 0.f || (temp >= 0x1p-60f && temp <= 0x1p60f)) || !(p == p) || !(mp == mp);
-  }
-  if (bad) {
-    if (rank == 0 && tid == 0) raise_error(a.err, DSPARK_DEVERR_BAD_INPUT);
-    return;
-  }
-  const bool greedy = temp == 0.f;
-  if (greedy) temp = p = 1.f, k = 0, mp = 0.f;
-  mp = fminf(mp, 1.f);
-  if (p <= 0.f) p = 1.f, k = 1;  // the first token alone
-  const bool use_k = k > 0 && k < a.V, use_p = p < 1.f;
-  cl.barrier_arrive();  // (waited for before the first access to another CTA's memory)
-
   Row<T> R{cl, S, data};
   R.C = C;
   R.rank = rank;
@@ -995,13 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.groups = (R.n + R.shift + V::N - 1) / V::N;
   if (R.n == 0) R.groups = 0;
 
-  if (tid == kThreads - 1) {  // (while the others load)
-    // log2(e) = 1.44269502162933349609375 + 1.92596299112661746887e-8
-    const float h = 1.44269502162933349609375f, c = h / temp;
-    S.c_hi = c;
-    S.c_lo = (fmaf(-c, temp, h) + 1.92596299112661746887e-8f) / temp;
-  }
-  // the chunk into shared memory, and its maximum
+  // the chunk into shared memory, and its maximum (of a padding row too: its parameters come later)
   float mx = -INFINITY;
   {
     const uint4* g = reinterpret_cast<const uint4*>(src - R.shift);
@@ -1036,6 +1037,34 @@ __global__ void __launch_bounds__(kThreads, 2)
         d[q] = V::put(x);
       }
     }
+  }
+  // the row's parameters (every decision below is the same in all threads of the cluster)
+  if (req < 0) return;
+  bool bad = req >= a.B;
+  float temp = 1.f, p = 1.f, mp = 0.f;
+  int k = 0;
+  if (!bad) {
+    if (a.temperature) temp = a.temperature[req];
+    if (a.top_k) k = a.top_k[req];
+    if (a.top_p) p = a.top_p[req];
+    if (a.min_p) mp = a.min_p[req];
+    bad = !(temp == 0.f || (temp >= 0x1p-60f && temp <= 0x1p60f)) || !(p == p) || !(mp == mp);
+  }
+  if (bad) {
+    if (rank == 0 && tid == 0) raise_error(a.err, DSPARK_DEVERR_BAD_INPUT);
+    return;
+  }
+  const bool greedy = temp == 0.f;
+  if (greedy) temp = p = 1.f, k = 0, mp = 0.f;
+  mp = fminf(mp, 1.f);
+  if (p <= 0.f) p = 1.f, k = 1;  // the first token alone
+  const bool use_k = k > 0 && k < a.V, use_p = p < 1.f;
+  cl.barrier_arrive();  // (waited for before the first access to another CTA's memory)
+  if (tid == kThreads - 1) {
+    // log2(e) = 1.44269502162933349609375 + 1.92596299112661746887e-8
+    const float h = 1.44269502162933349609375f, c = h / temp;
+    S.c_hi = c;
+    S.c_lo = (fmaf(-c, temp, h) + 1.92596299112661746887e-8f) / temp;
   }
   const float mx_cta = block_max(S, mx);
   cl.barrier_wait();

@@ -192,6 +192,7 @@ struct Row {
   Kept lim;           // what earlier filters left, and of that what this one may keep
   Kept lim_all;       // what earlier filters left
   mass_t whole;       // its mass (weigh)
+  bool sorted;        // the list in the first CTA is
   bool listed;        // it is the first S.n_keep tokens of the first CTA's list
 
   // (rounded by the addition of 2^23: monotone in l, which is all that is asked)
@@ -286,10 +287,10 @@ struct Row {
   }
 
   // Over S.tot: the bucket in which the running count reaches `target`, or (weighted) the running
-  // mass reaches the part `share` of the whole, the mass of bucket b being tot[b] * mass(b).
+  // mass reaches `share`, of_total of the whole, the mass of bucket b being tot[b] * mass(b).
   // Sets S.b_at, S.cum_before (tokens in the buckets before), S.cum_in and S.total.
   template <class Fn>
-  __device__ void locate(bool weighted, unsigned target, float share, Fn&& mass) {
+  __device__ void locate(bool weighted, unsigned target, float share, bool of_total, Fn&& mass) {
     constexpr int kPer = kBuckets / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const uint4 t4 = reinterpret_cast<const uint4*>(S.tot)[tid];
@@ -332,7 +333,7 @@ struct Row {
       total += S.wapprox[v];
       last += S.wcnt[v];
     }
-    const float goal = share * total;
+    const float goal = of_total ? share * total : share;
     const unsigned c_first = c0;
     if (tid == 0) S.total = last;
     // (of masses the first bucket that ends past the goal: fp32 sums of two threads need not join)
@@ -411,39 +412,38 @@ struct Row {
     sum3(v);
     whole = v[0];
   }
-  // Lists the tokens left with f_lo <= l < f_hi; returns this thread's mass of those above f_hi and
-  // adds that of the listed ones to `in`.
-  __device__ __forceinline__ float list_from(float f_lo, float f_hi, bool gather, float& in) {
+  // Of the tokens left with l >= least: lists those of place 1 and adds up the masses of those of
+  // place 0, which lie above them, and 1 (place(l): 0, 1 or 2, no part), over the row.
+  template <class Fn>
+  __device__ __forceinline__ void list_by(float least, bool gather, mass_t (&v)[3], Fn&& place) {
     __syncthreads();
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
-    float above = 0.f;
-    each_from(f_lo, [&](float l, int i) {
-      if (!left(l, i)) return;
+    float above = 0.f, in = 0.f;
+    each_from(least, [&](float l, int i) {
+      const int at = place(l);
+      if (at == 2 || !left(l, i)) return;
       const float w = w_of(l);
-      if (l >= f_hi) {
+      if (at == 0) {
         above += w;
-      } else {
-        in += w;
-        // (a list that is full counts no further)
-        if (gather && *(volatile int*)&S.n_list <= kList) {
-          const int at = atomicAdd(&S.n_list, 1);
-          if (at < kList) S.list[at] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
-        }
+        return;
+      }
+      in += w;
+      // (a list that is full counts no further)
+      if (gather && *(volatile int*)&S.n_list <= kList) {
+        const int slot = atomicAdd(&S.n_list, 1);
+        if (slot < kList) S.list[slot] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
       }
     });
-    return above;
-  }
-  // Masses of the tokens left: above f_hi, in [f_lo, f_hi), and all; those of the bracket are listed
-  // in S.list where `gather` is set.
-  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
-    float in = 0.f;
-    const float above = list_from(fmaxf(f_lo, lim.t), f_hi, gather, in);
     v[0] = __float2ll_rn(above * kUnit);
     v[1] = __float2ll_rn(in * kUnit);
     v[2] = 0;
     sum3(v);
     v[2] = whole;
+  }
+  // The bracket [f_lo, f_hi).
+  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
+    list_by(fmaxf(f_lo, lim.t), gather, v, [&](float l) { return l >= f_hi ? 0 : 1; });
   }
 
   // w in two parts, 2^-36 of it or better, by table and polynomial (Tang's scheme for the
@@ -676,40 +676,40 @@ struct Row {
   }
 
   // The end within a bracket whose tokens all CTAs have listed (kList in all at most): by the first
-  // CTA, `before` tokens and masses v (d, where `pairs`) above it as in walk.  Sets lim and listed;
-  // returns the mass kept.
-  __device__ float resolve(float f_lo, float f_hi, const mass_t (&v)[3], double (&d)[3], bool pairs,
-                           unsigned before, int k, bool use_p, float p) {
-    const bool by_count = k > 0;
-    for (int pass = 0;; ++pass) {
-      if (rank == 0) {
-        if (pass == 0) {
-          const int n = collect();
-          if (threadIdx.x == 0) S.n_list = n;
-          __syncthreads();
-        }
-        const int n = S.n_list, most = by_count ? (int)min((unsigned)n, (unsigned)k - before) : n;
-        if (pairs) walk(n, d, most, by_count, use_p, p);
-        else walk(n, v, most, by_count, use_p, p);
-        if (threadIdx.x > 0 && threadIdx.x < C) {
-          Shared* o = cl.map_shared_rank(&S, threadIdx.x);
-          o->t_cut = S.t_cut;
-          o->i_cut = S.i_cut;
-          o->z_kept = S.z_kept;
-          o->again = S.again;
-        }
+  // CTA, `before` tokens and masses v (d, where `pairs`) above it as in walk.  Sets lim, listed and z,
+  // the mass kept; false, and none of them, if v does not tell (the list stays sorted in S.n_list).
+  __device__ bool resolve(const mass_t (&v)[3], const double (&d)[3], bool pairs, unsigned before, int k,
+                          bool use_p, float p, float& z) {
+    if (rank == 0) {
+      if (!pairs || !sorted) {
+        const int n = collect();
+        if (threadIdx.x == 0) S.n_list = n;
+        __syncthreads();
       }
-      cl.sync();
-      if (!S.again || pairs) break;
-      pairs = true;
-      if (by_count) d[0] = d[1] = d[2] = 0;  // (the list has it all)
-      else evaluate_pairs(f_lo, f_hi, d);
+      const int n = S.n_list, most = k > 0 ? (int)min((unsigned)n, (unsigned)k - before) : n;
+      if (pairs) walk(n, d, most, k > 0, use_p, p);
+      else walk(n, v, most, k > 0, use_p, p);
+      if (threadIdx.x > 0 && threadIdx.x < C) {
+        Shared* o = cl.map_shared_rank(&S, threadIdx.x);
+        o->t_cut = S.t_cut;
+        o->i_cut = S.i_cut;
+        o->z_kept = S.z_kept;
+        o->again = S.again;
+      }
+    }
+    cl.sync();
+    sorted = S.again && !pairs;
+    if (sorted) {
+      cl.sync();  // (S.again is read)
+      return false;
     }
     lim.t = S.t_cut;
     lim.i = S.i_cut;
+    z = S.z_kept;
     whole = -1;
     listed = before == 0;
-    return S.z_kept;
+    cl.sync();    // (and these)
+    return true;
   }
 
   // A logit below which the filter keeps nothing, from what is known before the row is searched.
@@ -803,7 +803,7 @@ struct Row {
   // the largest logit of this thread's tokens.
   __device__ float cut(int k, bool use_p, float p, float mx, bool& done_p) {
     const bool by_count = k > 0;
-    listed = false;
+    listed = sorted = false;
     lim_all = lim;
     mass_t v[3];    // masses in fixed point from fp32,
     double d[3];    // or, once those have not told, from pairs
@@ -816,33 +816,32 @@ struct Row {
         lim.t = least;
         lim.i = kNone;
       }
-      float sum[2] = {0.f, 0.f};
       int count = 0;
-      each([&](float l, int i, int j) {
-        const bool in = left(l, i);
-        count += in;
-        sum[j & 1] += in ? w_of(l) : 0.f;
-      });
+      const Kept now = lim;
+      if (now.i == kNone) each([&](float l, int, int) { count += l >= now.t; });
+      else each([&](float l, int i, int) { count += left(l, i); });
       v[0] = count;
-      v[1] = __float2ll_rn((sum[0] + sum[1]) * kUnit);
-      v[2] = 0;
+      v[1] = v[2] = 0;
       sum3(v);
       if (v[0] <= kList) {
-        float in = 0.f;
-        list_from(lim.t, INFINITY, true, in);
-        cl.sync();
-        done_p = true;
+        evaluate(lim.t, INFINITY, true, v);
         v[0] = 0;
-        v[2] = whole;
-        return resolve(lim.t, INFINITY, v, d, false, 0, k, use_p, p);
+        done_p = true;
+        float z;
+        if (!resolve(v, d, false, 0, k, use_p, p, z)) {
+          // (what the list holds is all that counts, but for the whole of a top-p)
+          if (by_count) d[0] = d[1] = d[2] = 0;
+          else evaluate_pairs(lim.t, INFINITY, d);
+          resolve(v, d, true, 0, k, use_p, p, z);
+        }
+        return z;
       }
-    } else {
-      v[1] = whole;
     }
     // 1: buckets of (m - l) / T
     histogram([&](float l, int i) { return left(l, i) ? bucket_of(l) : -1; });
-    float share = by_count ? 0.f : p * ((float)whole / (float)v[1]);  // of what lies in the buckets
-    locate(!by_count, (unsigned)k, share, [](int b) { return ex2(b * (-1.f / kPerOctave)); });
+    // (a bucket's tokens weigh its middle to 1%, many of them far closer)
+    locate(!by_count, (unsigned)k, by_count ? 0.f : p * ((float)whole * (1.f / kUnit)), false,
+           [](int b) { return ex2(b * (-1.f / kPerOctave)); });
     // 2: the bracket [f_lo, f_hi): `before` tokens above it, `in` in it, of `total`
     unsigned before = S.cum_before, in = S.cum_in;
     const unsigned total = S.total;
@@ -851,6 +850,25 @@ struct Row {
       in += before;
       before = 0;
     }
+    if (in <= (unsigned)kList) {
+      // mostly that is it: the bracket by its buckets, from a logit that lies safely below
+      const float near = m - (b1 + 1.5f) / s;
+      list_by(fmaxf(b1 == kBuckets - 1 ? -FLT_MAX : near - 4e-7f * (fabsf(m) + fabsf(near)), lim.t), true, v,
+              [&](float l) {
+                const int b = bucket_of(l);
+                return b < b0 ? 0 : b <= b1 ? 1 : 2;
+              });
+      bool holds = true;
+      if (!by_count) {
+        const mass_t goal = goal_of(p, whole), margin = near_of(whole);
+        holds = v[0] + margin < goal && v[0] + v[1] - margin > goal;
+      }
+      float z;
+      done_p = !by_count || before == 0;
+      if (holds && resolve(v, d, false, before, k, use_p && done_p, p, z)) return z;
+    }
+    float share = 0.f;
+    __syncthreads();
     if (threadIdx.x < 32) {
       const float lo = b1 == kBuckets - 1 ? lim.t : fmaxf(edge(b1 + 1), lim.t);
       if (threadIdx.x == 0) S.f_lo = lo;
@@ -905,7 +923,13 @@ struct Row {
       if (gather) {
         // 3: the list
         done_p = !by_count || before == 0;
-        return resolve(f_lo, f_hi, v, d, pairs, before, k, use_p && done_p, p);
+        sorted = false;
+        float z;
+        if (resolve(v, d, pairs, before, k, use_p && done_p, p, z)) return z;
+        if (by_count) d[0] = d[1] = d[2] = 0;
+        else evaluate_pairs(f_lo, f_hi, d);
+        resolve(v, d, true, before, k, use_p && done_p, p, z);
+        return z;
       }
       const uint32_t ka = code_of(f_lo), kz = f_hi == INFINITY ? code_of(m) : code_of(f_hi) - 1;
       if (kz <= ka) {
@@ -939,7 +963,7 @@ struct Row {
         if (!(l >= f_lo && l < f_hi) || !left(l, i)) return -1;
         return (int)((kz - code_of(l)) >> sh);
       });
-      locate(!by_count, (unsigned)k - before, share, [&](int b) {
+      locate(!by_count, (unsigned)k - before, share, true, [&](int b) {
         const uint32_t off = ((uint32_t)b << sh) + ((1u << sh) >> 1);
         return w_of(float_of(off > kz - ka ? ka : kz - off));
       });
@@ -996,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.set = 0;
   R.n_row = a.V;
   R.whole = -1;
-  R.listed = false;
+  R.listed = R.sorted = false;
   const T* src = static_cast<const T*>(a.logits) + row * a.stride + R.first;
   R.shift = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
   R.groups = (R.n + R.shift + V::N - 1) / V::N;

@@ -70,7 +70,7 @@ struct Shared {
   float wapprox[kWarps];
   float e2h[17], e2l[17];              // 2^(-j / 16), j = -8 .. 8, in two parts
   float c_hi, c_lo;                    // log2(e) / T in two parts
-  int n_list;
+  int n_list, n_sorted;                // tokens that this CTA listed; of all, sorted (the first CTA's)
   // a decision of one thread or CTA for all
   int b_at;
   unsigned cum_before, cum_in, total;
@@ -85,9 +85,9 @@ struct Shared {
   int cr_idx[kMaxCluster];
 };
 
-// Order-preserving code of a float (no NaN, no -0).
+// Order-preserving code of a float (no NaN; -0 as 0).
 __device__ __forceinline__ uint32_t code_of(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x + 0.f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float float_of(uint32_t c) {
@@ -150,12 +150,6 @@ struct Vec<__nv_bfloat16> {
   static constexpr float kTop = 3.3895313892515355e38f;
 };
 
-// NaN counts as -inf, -0 as 0, and +inf as the type's largest number.
-__device__ __forceinline__ float clean(float x, float top) {
-  x = x + 0.f;
-  return x == x ? fminf(x, top) : -INFINITY;
-}
-
 struct Kept {    // tokens with l > t, or l == t and an index of at most i
   float t;
   int i;
@@ -164,7 +158,7 @@ struct Kept {    // tokens with l > t, or l == t and an index of at most i
 // A thread's two best in the race, the lower index first among equals as they come.
 constexpr int kNone = 0x7fffffff;
 struct Racer {
-  float s1 = -1.f, s2 = -1.f, l1 = 0.f, l2 = 0.f;
+  float s1 = -0x1p-60f, s2 = -0x1p-60f, l1 = 0.f, l2 = 0.f;
   int i1 = kNone, i2 = kNone;
   __device__ __forceinline__ void take(float s, float l, int i) {
     if (s > s1) {
@@ -216,8 +210,10 @@ struct Row {
     }
   }
 
-  // fn(l, i) for the tokens with l >= least: groups without one cost a maximum each.
-  template <class Fn>
+  // fn(l, in, i) for the tokens of the groups that have one with l >= least, in: it is such a one and
+  // (LIMITED) left.  The others cost a maximum a group.  fn should not branch: in a warp with any
+  // such token all of it runs.
+  template <bool LIMITED, class Fn>
   __device__ __forceinline__ void each_from(float least, Fn&& fn) const {
     const uint4* p = reinterpret_cast<const uint4*>(data);
     for (int q = threadIdx.x; q < groups; q += kThreads) {
@@ -228,9 +224,16 @@ struct Row {
       for (int j = 1; j < V::N; ++j) top = fmaxf(top, x[j]);
       if (top >= least)
 #pragma unroll
-        for (int j = 0; j < V::N; ++j)
-          if (x[j] >= least) fn(x[j], q * V::N + j - shift);
+        for (int j = 0; j < V::N; ++j) {
+          const int i = q * V::N + j - shift;
+          fn(x[j], x[j] >= least && (!LIMITED || left(x[j], i)), i);
+        }
     }
+  }
+  template <class Fn>
+  __device__ __forceinline__ void each_left_from(float least, Fn&& fn) const {
+    if (lim.i == kNone) each_from<false>(least, fn);
+    else each_from<true>(least, fn);
   }
 
   // Sums of three numbers (mass_t or double) over the row, the same in every thread of the cluster and
@@ -264,16 +267,16 @@ struct Row {
     set ^= 1;
   }
 
-  // Counts of the row's tokens by bucket(l, i) (0 .. kBuckets - 1, or negative: not counted), into
+  // Counts of the row's tokens by bucket(l) (0 .. kBuckets - 1, or negative: not counted), into
   // S.tot of every CTA.
   template <class Fn>
   __device__ void histogram(Fn&& bucket) {
     __syncthreads();
     for (int b = threadIdx.x; b < kBuckets; b += kThreads) S.hist[b] = 0;
     __syncthreads();
-    each_from(lim.t, [&](float l, int i) {
-      const int b = bucket(l, i);
-      if (b >= 0) atomicAdd(&S.hist[b], 1u);
+    each_left_from(lim.t, [&](float l, bool in, int) {
+      const int b = bucket(l);
+      if (in && b >= 0) atomicAdd(&S.hist[b], 1u);
     });
     cl.sync();
     const int per = kBuckets / C;
@@ -293,9 +296,15 @@ struct Row {
   __device__ void locate(bool weighted, unsigned target, float share, bool of_total, Fn&& mass) {
     constexpr int kPer = kBuckets / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const uint4 t4 = reinterpret_cast<const uint4*>(S.tot)[tid];
-    static_assert(kPer == 4, "a thread's buckets");
-    const unsigned c[kPer] = {t4.x, t4.y, t4.z, t4.w};
+    unsigned c[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; j += 4) {
+      const uint4 t4 = reinterpret_cast<const uint4*>(S.tot)[(tid * kPer + j) / 4];
+      c[j] = t4.x;
+      c[j + 1] = t4.y;
+      c[j + 2] = t4.z;
+      c[j + 3] = t4.w;
+    }
     unsigned cs = 0;
     float w[kPer], ws = 0;
 #pragma unroll
@@ -404,9 +413,7 @@ struct Row {
     if (lim.t == -FLT_MAX) {
       each([&](float l, int, int j) { all[j & 1] += w_of(l); });
     } else {
-      each_from(lim.t, [&](float l, int i) {
-        if (left(l, i)) all[0] += w_of(l);
-      });
+      each_left_from(lim.t, [&](float l, bool in, int) { all[0] += in ? w_of(l) : 0.f; });
     }
     mass_t v[3] = {__float2ll_rn((all[0] + all[1]) * kUnit), 0, 0};
     sum3(v);
@@ -420,19 +427,17 @@ struct Row {
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
     float above = 0.f, in = 0.f;
-    each_from(least, [&](float l, int i) {
-      const int at = place(l);
-      if (at == 2 || !left(l, i)) return;
+    each_left_from(least, [&](float l, bool is, int i) {
+      const int at = is ? place(l) : 2;
       const float w = w_of(l);
-      if (at == 0) {
-        above += w;
-        return;
-      }
-      in += w;
-      // (a list that is full counts no further)
-      if (gather && *(volatile int*)&S.n_list <= kList) {
-        const int slot = atomicAdd(&S.n_list, 1);
-        if (slot < kList) S.list[slot] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
+      above += at == 0 ? w : 0.f;
+      if (at == 1) {
+        in += w;
+        // (a list that is full counts no further)
+        if (gather && *(volatile int*)&S.n_list <= kList) {
+          const int slot = atomicAdd(&S.n_list, 1);
+          if (slot < kList) S.list[slot] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
+        }
       }
     });
     v[0] = __float2ll_rn(above * kUnit);
@@ -517,9 +522,10 @@ struct Row {
       n += r < C ? cl.map_shared_rank(&S, r)->n_list : 0;
     }
     n = min(n, kList);
-    uint64_t mine[2];
+    constexpr int kEach = kList / kThreads;
+    uint64_t mine[kEach];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kEach; ++j) {
       const int i = threadIdx.x + j * kThreads;
       int r = 0;
 #pragma unroll
@@ -533,7 +539,7 @@ struct Row {
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < kEach; ++j)
       if (threadIdx.x + j * kThreads < n) S.list[threadIdx.x + j * kThreads] = mine[j];
     int size = 64;
     while (size < n) size <<= 1;
@@ -548,11 +554,9 @@ struct Row {
         S.list[b] = x;
       }
     };
-    const int i = threadIdx.x;
-    static_assert(kList == 2 * kThreads, "one pair a thread");
     for (int k = 2; k <= size; k <<= 1) {
       for (int d = k >> 1; d > 0; d >>= 1) {
-        if (i < size / 2) step(i, k, d);
+        for (int i = threadIdx.x; i < size / 2; i += kThreads) step(i, k, d);
         if (d > 32) __syncthreads();
         else __syncwarp();
       }
@@ -636,6 +640,24 @@ struct Row {
     __syncthreads();
   }
 
+  // The lowest index among the largest logits.
+  __device__ int first_top() {
+    int at = kNone;
+    each_from<false>(m, [&](float, bool in, int i) { at = min(at, in ? first + i : kNone); });
+    at = __reduce_min_sync(0xffffffffu, at);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) S.r_idx[threadIdx.x >> 5] = at;
+    __syncthreads();
+    if (threadIdx.x < C) {
+      for (int w = 0; w < kWarps; ++w) at = min(at, S.r_idx[w]);
+      cl.map_shared_rank(&S, threadIdx.x)->n_near[rank] = at;
+    }
+    cl.sync();
+    at = kNone;
+    for (int r = 0; r < C; ++r) at = min(at, S.n_near[r]);
+    return at;
+  }
+
   // Of the row's tokens that equal t, the index of the nth (from 1): into S.i_cut of every CTA.
   __device__ void nth_equal(float t, long long nth) {
     // a contiguous run of slots for each thread
@@ -677,16 +699,16 @@ struct Row {
 
   // The end within a bracket whose tokens all CTAs have listed (kList in all at most): by the first
   // CTA, `before` tokens and masses v (d, where `pairs`) above it as in walk.  Sets lim, listed and z,
-  // the mass kept; false, and none of them, if v does not tell (the list stays sorted in S.n_list).
+  // the mass kept; false, and none of them, if v does not tell (the list stays as it is, sorted).
   __device__ bool resolve(const mass_t (&v)[3], const double (&d)[3], bool pairs, unsigned before, int k,
                           bool use_p, float p, float& z) {
     if (rank == 0) {
       if (!pairs || !sorted) {
         const int n = collect();
-        if (threadIdx.x == 0) S.n_list = n;
+        if (threadIdx.x == 0) S.n_sorted = n;
         __syncthreads();
       }
-      const int n = S.n_list, most = k > 0 ? (int)min((unsigned)n, (unsigned)k - before) : n;
+      const int n = S.n_sorted, most = k > 0 ? (int)min((unsigned)n, (unsigned)k - before) : n;
       if (pairs) walk(n, d, most, k > 0, use_p, p);
       else walk(n, v, most, k > 0, use_p, p);
       if (threadIdx.x > 0 && threadIdx.x < C) {
@@ -699,16 +721,13 @@ struct Row {
     }
     cl.sync();
     sorted = S.again && !pairs;
-    if (sorted) {
-      cl.sync();  // (S.again is read)
-      return false;
-    }
+    // (before they are written again the CTAs meet)
+    if (sorted) return false;
     lim.t = S.t_cut;
     lim.i = S.i_cut;
     z = S.z_kept;
     whole = -1;
     listed = before == 0;
-    cl.sync();    // (and these)
     return true;
   }
 
@@ -731,7 +750,7 @@ struct Row {
   }
 
   // The chunk's probabilities w inv (probs and noise: of the whole row), and the race.
-  template <typename P, bool RACE>
+  template <typename P, bool RACE, bool LIMITED>
   __device__ __forceinline__ void distribute(P* probs, const float* noise, float inv, Racer& b) const {
     P* const out = probs + first - shift;              // of slot 0
     const float* const e = noise + first - shift;
@@ -742,13 +761,13 @@ struct Row {
       const int s0 = q * V::N;
       float x[V::N], w[V::N];
       V::get(p[q], x);
-      bool any = false, every = true;
+      bool any = false, every = true, keep[V::N];
 #pragma unroll
       for (int j = 0; j < V::N; ++j) {
-        const bool keep = left(x[j], s0 + j - shift);
-        w[j] = keep ? w_of(x[j]) : 0.f;
-        any |= keep;
-        every &= keep;
+        keep[j] = LIMITED ? left(x[j], s0 + j - shift) : x[j] >= lim.t;
+        w[j] = keep[j] ? w_of(x[j]) : 0.f;
+        any |= keep[j];
+        every &= keep[j];
       }
       const bool inside = s0 >= shift && s0 + V::N <= shift + n;
       if (out_wide && inside) {
@@ -771,11 +790,13 @@ struct Row {
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < V::N; ++j) f[j] = left(x[j], s0 + j - shift) ? e[s0 + j] : 1.f;
+          for (int j = 0; j < V::N; ++j) f[j] = keep[j] ? e[s0 + j] : 1.f;
         }
 #pragma unroll
         for (int j = 0; j < V::N; ++j)
-          if (left(x[j], s0 + j - shift)) b.take(__fdividef(w[j], f[j]), x[j], first + s0 + j - shift);
+        {
+          if (keep[j] && w[j] > b.s2 * f[j]) b.take(__fdividef(w[j], f[j]), x[j], first + s0 + j - shift);
+        }
       }
     }
   }
@@ -809,36 +830,33 @@ struct Row {
     double d[3];    // or, once those have not told, from pairs
     bool pairs = false;
     if (!by_count && whole < 0) weigh();
-    // 0: what may be kept at all: mostly it fits the list
+    // 0: what may be kept at all
     const float least = bound(k, p, mx);
-    if (least > lim.t || lim.t > -FLT_MAX) {
-      if (least > lim.t) {
-        lim.t = least;
-        lim.i = kNone;
-      }
-      int count = 0;
-      const Kept now = lim;
-      if (now.i == kNone) each([&](float l, int, int) { count += l >= now.t; });
-      else each([&](float l, int i, int) { count += left(l, i); });
-      v[0] = count;
-      v[1] = v[2] = 0;
-      sum3(v);
-      if (v[0] <= kList) {
-        evaluate(lim.t, INFINITY, true, v);
-        v[0] = 0;
+    if (least > lim.t) {
+      lim.t = least;
+      lim.i = kNone;
+    }
+    // Of kThreads threads' tokens about kThreads ln(1 / (1 - k / kThreads)) pass k of their maxima;
+    // where that is well below the list's size in all CTAs together, it is listed at once.
+    if (by_count && k < kThreads && -kThreads * __logf(1.f - k / (float)kThreads) * C < 0.8f * kList) {
+      evaluate(lim.t, INFINITY, true, v);
+      unsigned n = 0;
+      for (int r = 0; r < C; ++r) n += (unsigned)cl.map_shared_rank(&S, r)->n_list;
+      if (n <= (unsigned)kList) {
         done_p = true;
+        v[0] = 0;
         float z;
         if (!resolve(v, d, false, 0, k, use_p, p, z)) {
-          // (what the list holds is all that counts, but for the whole of a top-p)
-          if (by_count) d[0] = d[1] = d[2] = 0;
-          else evaluate_pairs(lim.t, INFINITY, d);
+          cl.sync();
+          d[0] = d[1] = d[2] = 0;  // (the list has it all)
           resolve(v, d, true, 0, k, use_p, p, z);
         }
         return z;
       }
+      cl.sync();  // (n_list is read)
     }
     // 1: buckets of (m - l) / T
-    histogram([&](float l, int i) { return left(l, i) ? bucket_of(l) : -1; });
+    histogram([&](float l) { return bucket_of(l); });
     // (a bucket's tokens weigh its middle to 1%, many of them far closer)
     locate(!by_count, (unsigned)k, by_count ? 0.f : p * ((float)whole * (1.f / kUnit)), false,
            [](int b) { return ex2(b * (-1.f / kPerOctave)); });
@@ -926,6 +944,7 @@ struct Row {
         sorted = false;
         float z;
         if (resolve(v, d, pairs, before, k, use_p && done_p, p, z)) return z;
+        cl.sync();
         if (by_count) d[0] = d[1] = d[2] = 0;
         else evaluate_pairs(f_lo, f_hi, d);
         resolve(v, d, true, before, k, use_p && done_p, p, z);
@@ -959,10 +978,7 @@ struct Row {
       out_below = total - before - in;
       int sh = 0;
       while (((kz - ka) >> sh) >= (uint32_t)kBuckets) ++sh;
-      histogram([&](float l, int i) {
-        if (!(l >= f_lo && l < f_hi) || !left(l, i)) return -1;
-        return (int)((kz - code_of(l)) >> sh);
-      });
+      histogram([&](float l) { return l >= f_lo && l < f_hi ? (int)((kz - code_of(l)) >> sh) : -1; });
       locate(!by_count, (unsigned)k - before, share, true, [&](int b) {
         const uint32_t off = ((uint32_t)b << sh) + ((1u << sh) >> 1);
         return w_of(float_of(off > kz - ka ? ka : kz - off));
@@ -1055,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         V::get(u[k], x);
 #pragma unroll
         for (int j = 0; j < V::N; ++j) {
-          x[j] = clean(x[j], V::kTop);
+          x[j] = fmaxf(x[j], -INFINITY);  // (NaN counts as -inf)
           mx = fmaxf(mx, x[j]);
         }
         d[q] = V::put(x);
@@ -1096,6 +1112,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   cl.sync();
   float m = S.cmax[0];
   for (int r = 1; r < C; ++r) m = fmaxf(m, S.cmax[r]);
+  if (m == INFINITY) {  // +inf counts as the type's largest number
+    m = V::kTop;
+    mx = fminf(mx, m);
+    uint4* const d = reinterpret_cast<uint4*>(data);
+    for (int q = tid; q < R.groups; q += kThreads) {
+      float x[V::N];
+      V::get(d[q], x);
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) x[j] = fminf(x[j], m);
+      d[q] = V::put(x);
+    }
+    __syncthreads();
+  }
   R.m = m;
   R.s = S.c_hi * kPerOctave;
   R.nc = -S.c_hi;
@@ -1122,15 +1151,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   float z = -1.f;
   bool done_p = false;
   if (greedy) {
-    R.nth_equal(m, 1);
     R.lim.t = m;
-    R.lim.i = S.i_cut;
+    R.lim.i = R.first_top();
     z = 1.f;
   }
   if (use_k) z = R.cut(k, use_p, p, mx, done_p);
   if (use_p && !done_p) z = R.cut(0, true, p, mx, done_p);
   const bool race = a.tokens != nullptr;
-  if (greedy && race && rank == 0 && tid == 0) a.tokens[row] = S.i_cut;
+  if (greedy && race && rank == 0 && tid == 0) a.tokens[row] = R.lim.i;
   if (!probs && (greedy || (R.listed && rank != 0))) return;
   if (z < 0.f && probs) {
     R.weigh();
@@ -1147,11 +1175,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       b.take(__fdividef(R.w_of(l), noise[at]), l, at);
     }
   } else if (probs) {
-    if (race && !greedy) R.template distribute<P, true>(probs, noise, 1.f / z, b);
-    else R.template distribute<P, false>(probs, noise, 1.f / z, b);
+    if (race && !greedy) {
+      if (R.lim.i == kNone) R.template distribute<P, true, false>(probs, noise, 1.f / z, b);
+      else R.template distribute<P, true, true>(probs, noise, 1.f / z, b);
+    } else {
+      R.template distribute<P, false, true>(probs, noise, 1.f / z, b);
+    }
   } else {
-    R.each_from(R.lim.t, [&](float l, int i) {
-      if (R.left(l, i)) b.take(__fdividef(R.w_of(l), noise[R.first + i]), l, R.first + i);
+    const float* const mine = noise + R.first;
+    R.each_left_from(R.lim.t, [&](float l, bool in, int i) {
+      const float e = in ? mine[i] : 1.f;
+      if (in && R.w_of(l) > b.s2 * e) b.take(__fdividef(R.w_of(l), e), l, R.first + i);
     });
   }
   if (!race || greedy) return;

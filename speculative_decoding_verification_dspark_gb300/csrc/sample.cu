@@ -11,7 +11,7 @@
 // A row belongs to a cluster of 1 to 8 CTAs, whose shared memory holds it: logits are read from
 // memory once, whatever the filters need.  The end of the kept part is found without sorting the
 // row:
-//   1  tokens are counted in 2048 buckets of (m - l) / T, 1/32 of an octave of w each;
+//   1  tokens are counted in 2048 buckets of (m - l) / T, 1/64 of an octave of w each;
 //   2  a bracket of buckets that must hold the end is taken (for top-p by masses that the counts
 //      estimate), and one pass sums the masses above, in and below it and lists its tokens;
 //   3  one CTA sorts the list and walks it.
@@ -38,7 +38,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBuckets = 2048;
-constexpr float kPerOctave = 32.f;
+constexpr float kPerOctave = 64.f;
 constexpr int kList = 1024;            // tokens of a bracket that are sorted
 constexpr int kMaxCluster = 8;
 constexpr int kChunkBytes = 76 * 1024; // of a row in one CTA, while eight CTAs hold the row
@@ -46,9 +46,12 @@ constexpr int kChunkBytes = 76 * 1024; // of a row in one CTA, while eight CTAs 
 // 2^63): without the card's slow 64-bit floating point, which the sums in pairs need.
 typedef long long mass_t;
 constexpr float kUnit = 0x1p44f;
-// Error of the fp32 sums relative to the mass: ex2.approx and the products before it give 2^-21 per
-// token at most for the tokens that matter, far less in the sum of many.  About 10^-6.
-__device__ __forceinline__ mass_t near_of(mass_t whole) { return whole >> 20; }
+// Error that the fp32 sums may have, as a part of the whole: 2^-22.  What counts is the error of a ratio
+// of two sums.  A token x octaves below the top is off by (x + 1) 2^-24 or so, most of it another
+// amount for every logit; the part that is the same for all (the factor's rounding) moves the ratio by
+// a quarter of the octaves between what is kept and what is not, times 2^-25.  Sums over a thread's
+// tokens add 2^-25 times the root of their number, and average out over 500 threads and more.
+__device__ __forceinline__ mass_t near_of(mass_t whole) { return whole >> 22; }
 // What lies before a kept token is short of p of the whole (0 < p < 1).
 __device__ __forceinline__ mass_t goal_of(float p, mass_t whole) {
   const unsigned long long f = __float2ull_rn(p * 0x1p64f), w = whole;
@@ -761,13 +764,12 @@ struct Row {
       const int s0 = q * V::N;
       float x[V::N], w[V::N];
       V::get(p[q], x);
-      bool any = false, every = true, keep[V::N];
+      bool any = false, keep[V::N];
 #pragma unroll
       for (int j = 0; j < V::N; ++j) {
         keep[j] = LIMITED ? left(x[j], s0 + j - shift) : x[j] >= lim.t;
         w[j] = keep[j] ? w_of(x[j]) : 0.f;
         any |= keep[j];
-        every &= keep[j];
       }
       const bool inside = s0 >= shift && s0 + V::N <= shift + n;
       if (out_wide && inside) {
@@ -779,25 +781,51 @@ struct Row {
       }
       if (RACE && any) {
         float f[V::N];
-        if (e_wide && inside && every) {
-#pragma unroll
-          for (int j = 0; j < V::N; j += 4) {
-            const uint4 u = ld_stream(reinterpret_cast<const uint4*>(e + s0 + j));
-            f[j] = __uint_as_float(u.x);
-            f[j + 1] = __uint_as_float(u.y);
-            f[j + 2] = __uint_as_float(u.z);
-            f[j + 3] = __uint_as_float(u.w);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < V::N; ++j) f[j] = keep[j] ? e[s0 + j] : 1.f;
-        }
+        load_noise(e, s0, e_wide && inside, x, f);
 #pragma unroll
         for (int j = 0; j < V::N; ++j)
-        {
           if (keep[j] && w[j] > b.s2 * f[j]) b.take(__fdividef(w[j], f[j]), x[j], first + s0 + j - shift);
-        }
       }
+    }
+  }
+  // The race alone.
+  template <bool LIMITED>
+  __device__ __forceinline__ void run_race(const float* noise, Racer& b) const {
+    const float* const e = noise + first - shift;      // of slot 0
+    const bool e_wide = (reinterpret_cast<uintptr_t>(e) & 15) == 0;
+    const uint4* p = reinterpret_cast<const uint4*>(data);
+    for (int q = threadIdx.x; q < groups; q += kThreads) {
+      const int s0 = q * V::N;
+      float x[V::N], f[V::N];
+      V::get(p[q], x);
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < V::N; ++j) top = fmaxf(top, x[j]);
+      if (!(top >= lim.t)) continue;
+      // (a group's noise is a sector of memory, or half of one: it comes whole)
+      load_noise(e, s0, e_wide && s0 >= shift && s0 + V::N <= shift + n, x, f);
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) {
+        const bool keep = LIMITED ? left(x[j], s0 + j - shift) : x[j] >= lim.t;
+        const float w = w_of(x[j]);
+        if (keep && w > b.s2 * f[j]) b.take(__fdividef(w, f[j]), x[j], first + s0 + j - shift);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_noise(const float* e, int s0, bool wide, const float (&x)[V::N],
+                                             float (&f)[V::N]) const {
+    if (wide) {
+#pragma unroll
+      for (int j = 0; j < V::N; j += 4) {
+        const uint4 u = ld_stream(reinterpret_cast<const uint4*>(e + s0 + j));
+        f[j] = __uint_as_float(u.x);
+        f[j + 1] = __uint_as_float(u.y);
+        f[j + 2] = __uint_as_float(u.z);
+        f[j + 3] = __uint_as_float(u.w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) f[j] = x[j] >= lim.t ? e[s0 + j] : 1.f;
     }
   }
   template <typename P>
@@ -1182,11 +1210,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       R.template distribute<P, false, true>(probs, noise, 1.f / z, b);
     }
   } else {
-    const float* const mine = noise + R.first;
-    R.each_left_from(R.lim.t, [&](float l, bool in, int i) {
-      const float e = in ? mine[i] : 1.f;
-      if (in && R.w_of(l) > b.s2 * e) b.take(__fdividef(R.w_of(l), e), l, R.first + i);
-    });
+    if (R.lim.i == kNone) R.template run_race<false>(noise, b);
+    else R.template run_race<true>(noise, b);
   }
   if (!race || greedy) return;
 

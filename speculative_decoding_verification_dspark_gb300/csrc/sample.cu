@@ -481,8 +481,9 @@ struct Row {
     wl = rl * scale;
   }
 
-  // evaluate's masses in pairs.
-  __device__ void evaluate_pairs(float f_lo, float f_hi, double (&v)[3]) {
+  // list_by's masses in pairs, v[2] that of all tokens that earlier filters left.
+  template <class Fn>
+  __device__ __forceinline__ void weigh_pairs(double (&v)[3], Fn&& place) {
     if (threadIdx.x < 17) {
       const double e = exp2(-((int)threadIdx.x - 8) / 16.0);  // (few: 64 bits are slow here)
       S.e2h[threadIdx.x] = (float)e;
@@ -499,14 +500,18 @@ struct Row {
       if (l < lim_all.t || (l == lim_all.t && first + i > lim_all.i)) return;
       float wh, wl;
       w_pair(l, wh, wl);
-      if (l >= f_hi) add(ah, al, wh, wl);
-      else if (l >= f_lo) add(ih, il, wh, wl);
+      const int at = place(l);
+      if (at == 0) add(ah, al, wh, wl);
+      else if (at == 1) add(ih, il, wh, wl);
       else add(bh, bl, wh, wl);
     });
     v[0] = (double)ah + al;
     v[1] = (double)ih + il;
     v[2] = v[0] + v[1] + ((double)bh + bl);
     sum3(v);
+  }
+  __device__ void evaluate_pairs(float f_lo, float f_hi, double (&v)[3]) {
+    weigh_pairs(v, [&](float l) { return l >= f_hi ? 0 : l >= f_lo ? 1 : 2; });
   }
   __device__ __forceinline__ void w_exact(float l, double& w) const {
     float h, t;
@@ -899,19 +904,33 @@ struct Row {
     if (in <= (unsigned)kList) {
       // mostly that is it: the bracket by its buckets, from a logit that lies safely below
       const float near = m - (b1 + 1.5f) / s;
+      auto place = [&](float l) {
+        const int b = bucket_of(l);
+        return b < b0 ? 0 : b <= b1 ? 1 : 2;
+      };
       list_by(fmaxf(b1 == kBuckets - 1 ? -FLT_MAX : near - 4e-7f * (fabsf(m) + fabsf(near)), lim.t), true, v,
-              [&](float l) {
-                const int b = bucket_of(l);
-                return b < b0 ? 0 : b <= b1 ? 1 : 2;
-              });
-      bool holds = true;
-      if (!by_count) {
-        const mass_t goal = goal_of(p, whole), margin = near_of(whole);
-        holds = v[0] + margin < goal && v[0] + v[1] - margin > goal;
-      }
+              place);
       float z;
       done_p = !by_count || before == 0;
-      if (holds && resolve(v, d, false, before, k, use_p && done_p, p, z)) return z;
+      const mass_t goal = by_count ? 0 : goal_of(p, whole), margin = near_of(whole);
+      const bool sure = by_count || (v[0] + margin < goal && v[0] + v[1] - margin > goal);
+      if (sure && resolve(v, d, false, before, k, use_p && done_p, p, z)) return z;
+      // fp32 does not tell (or has told that the end lies elsewhere)
+      if (by_count || (v[0] - margin < goal && v[0] + v[1] + margin > goal)) {
+        cl.sync();
+        bool holds = true;
+        if (by_count) {
+          d[0] = d[1] = d[2] = 0;  // (before is 0: the list has it all)
+        } else {
+          weigh_pairs(d, place);
+          const double g = goal_of(p, d[2]);
+          holds = (before == 0 || d[0] < g) && !(d[0] + d[1] < g);
+        }
+        if (holds) {
+          resolve(v, d, true, before, k, use_p && done_p, p, z);
+          return z;
+        }
+      }
     }
     float share = 0.f;
     __syncthreads();

@@ -700,6 +700,8 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  *   row_req     int32 [rows], nullable: the parameters' index of each row (dspark_pack's
  *               row_req); a row with a negative one is padding, its outputs are left as
  *               they are.  NULL: row i has index i (B >= rows)
+ *   n_rows      int32 [1], nullable: rows from *n_rows on (dspark_pack's M_out) are left as
+ *               they are too, whatever row_req holds there
  *   temperature fp32 [B]: 0 (the first token alone) or 2^-60 .. 2^60; NULL: 1
  *   top_k       int32 [B]: off where < 1 or >= V; NULL: off
  *   top_p       fp32 [B]: off where >= 1, the first token alone where <= 0; NULL: off
@@ -708,14 +710,15 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  *   tokens      int32 [rows] out, nullable
  *   probs       [rows, V] fp32 or bf16 (probs_dtype) out, dense, nullable
  * Which tokens are kept and which wins the race is decided as in 64-bit arithmetic (but where
- * sums lie within 10^-10 of a border); probs are fp32 values (2^-18) rounded once.  A row
+ * sums lie within 10^-10 of a border); probs are fp32 values (2^-16) rounded once.  A row
  * without any logit above -inf gets token -1 and probs 0.  An index >= B, or a temperature
  * outside its range, or a NaN parameter sets DSPARK_DEVERR_BAD_INPUT and the row's outputs
  * are left as they are.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
  * ------------------------------------------------------------------------- */
 int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
-                  const int32_t* row_req, int B, const float* temperature, const int32_t* top_k,
-                  const float* top_p, const float* min_p, const float* exp_noise, int32_t* tokens,
+                  const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,
+                  const int32_t* top_k, const float* top_p, const float* min_p,
+                  const float* exp_noise, int32_t* tokens,
                   void* probs, int probs_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------

@@ -86,7 +86,7 @@ _SIGNATURES = {
     "dspark_verify_attn_tree_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
     "dspark_verify_attn_tree": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I,
                                      _I, _F, _I, _I, _P, _P, _P, _Z, _P]),
-    "dspark_sample": (_I, [_P, _L, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "dspark_sample": (_I, [_P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
     "dspark_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _P, _I, _I, _F, _P, _P, _I,
                                  _I, _I, _P, _P, _P, _P]),
     "dspark_kv4_store": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _I, _P, _I, _I, _F, _F, _P,
@@ -618,12 +618,12 @@ def verify_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, cu_
 
 
 def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, probs=None,
-           row_req=None, stream=None):
+           row_req=None, stream=None, n_rows=None):
     """Tokens and distributions from logits (dspark_sample): logits [rows, V] fp32 or bf16, rows
     possibly apart; temperature, top_p, min_p fp32 [B] and top_k int32 [B], each None where it is
     off; exp_noise fp32 [rows, V]; tokens int32 [rows] out or None; probs fp32 or bf16 [rows, V]
     out or None; row_req int32 [rows] (< 0: padding, left as it is) or None: row i has the
-    parameters of index i."""
+    parameters of index i; n_rows int32 [1] or None: rows from there on are left as they are."""
     dev = _current(logits)
     dt = _float_dtype(logits, "logits")
     if logits.dim() != 2:
@@ -644,7 +644,8 @@ def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, pro
 
     _check("dspark_sample", lib().dspark_sample(
         logits.data_ptr(), stride, dt, rows, V,
-        None if row_req is None else _arg(row_req, dev, "row_req", i32, (rows,)), B,
+        None if row_req is None else _arg(row_req, dev, "row_req", i32, (rows,)),
+        None if n_rows is None else _arg(n_rows, dev, "n_rows", i32, (1,)), B,
         par(temperature, "temperature", f32), par(top_k, "top_k", i32), par(top_p, "top_p", f32),
         par(min_p, "min_p", f32),
         None if exp_noise is None else _arg(exp_noise, dev, "exp_noise", f32, (rows, V)),
@@ -859,7 +860,7 @@ class VerifyStep:
         """p_target of ``inp`` from its logits, filtered by its requests' parameters (temperature,
         top_k, top_p, min_p [B], each optional), for the rows of the last pack."""
         sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
-               inp.get("min_p"), None, None, inp["p_target"], self.row_req, stream)
+               inp.get("min_p"), None, None, inp["p_target"], self.row_req, stream, n_rows=self.M_pack)
 
     def attention(self, inp, stream=None):
         if self.kv4:
@@ -981,7 +982,7 @@ class TreeStep:
     ``run`` enqueues one step on the current stream: tree_pack -> (qk_norm_rope, where ``inp``
     holds q_in, k_in and v_in) -> verify_attn_tree -> sample -> accept_tree -> compact along the
     path.  ``inp`` holds cu_seqlens, row_tok, row_parent (the packed trees, row 0 of a segment the
-    anchor), row_req int32 [max_rows] (each row's request, -1 past the last), q, k_new, v_new,
+    anchor), row_req int32 [max_rows] (each row's request), q, k_new, v_new,
     logits, exp_noise [max_rows, V], scale, the caches, the state that VerifyStep has too, and
     optionally temperature, top_k, top_p, min_p [B].
     """
@@ -1029,7 +1030,8 @@ class TreeStep:
 
     def sample(self, inp, stream=None):
         sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
-               inp.get("min_p"), inp["exp_noise"], self.row_sample, None, inp["row_req"], stream)
+               inp.get("min_p"), inp["exp_noise"], self.row_sample, None, inp["row_req"], stream,
+               n_rows=inp["cu_seqlens"][-1:])
 
     def accept(self, inp, stream=None):
         accept_tree(inp["row_tok"], inp["row_parent"], inp["cu_seqlens"], self.row_sample, self.path,

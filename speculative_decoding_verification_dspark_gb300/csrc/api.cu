@@ -684,7 +684,8 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
 }
 
 int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
-                  const int32_t* row_req, int B, const float* temperature, const int32_t* top_k,
+                  const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,
+                  const int32_t* top_k,
                   const float* top_p, const float* min_p, const float* exp_noise, int32_t* tokens,
                   void* probs, int probs_dtype, void* stream) {
   CHECK(logits && (tokens || probs) && (!tokens || exp_noise), DSPARK_EINVAL);
@@ -699,7 +700,7 @@ int dspark_sample(const void* logits, long long stride, int dtype, int rows, int
         DSPARK_EINVAL);
   int rc = device_ok();
   if (rc != DSPARK_OK) return rc;
-  const SampleArgs a = {logits, stride, rows, V, row_req, B, temperature, top_k, top_p, min_p,
+  const SampleArgs a = {logits, stride, rows, V, row_req, n_rows, B, temperature, top_k, top_p, min_p,
                         exp_noise, tokens, probs, device_error_word()};
   return launch_sample(a, dtype, probs ? probs_dtype : DSPARK_F32, static_cast<cudaStream_t>(stream));
 }

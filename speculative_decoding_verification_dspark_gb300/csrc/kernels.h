@@ -141,6 +141,7 @@ struct SampleArgs {
   long long stride;              // elements between the rows of logits
   int rows, V;
   const int32_t* row_req;        // nullable: row i has the parameters of index i
+  const int32_t* n_rows;         // [1], nullable: rows from there on are left as they are
   int B;
   const float* temperature;      // [B], nullable: 1
   const int32_t* top_k;          // [B], nullable: off

@@ -1074,6 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_release();
   pdl_wait();
 
+  if (a.n_rows && row >= *a.n_rows) return;
   const int req = a.row_req ? a.row_req[row] : row;
   Row<T> R{cl, S, data};
   R.C = C;

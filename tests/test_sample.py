@@ -43,8 +43,8 @@ def test_oracle_by_hand():
 def test_host_refusals(pkg):
     lib, f, off = pkg.load(), ctypes.c_void_p(4096), ctypes.c_void_p(4097)
 
-    def call(l=f, stride=100, dt=0, rows=4, V=100, req=f, B=2, e=f, tok=f, probs=f, pdt=0):
-        return lib.dspark_sample(l, stride, dt, rows, V, req, B, f, f, f, f, e, tok, probs, pdt, None)
+    def call(l=f, stride=100, dt=0, rows=4, V=100, req=f, n=None, B=2, e=f, tok=f, probs=f, pdt=0):
+        return lib.dspark_sample(l, stride, dt, rows, V, req, n, B, f, f, f, f, e, tok, probs, pdt, None)
 
     for bad in (dict(l=None), dict(l=off), dict(probs=off), dict(stride=99), dict(dt=2), dict(pdt=2),
                 dict(rows=0), dict(V=0), dict(B=0), dict(req=None), dict(e=None), dict(tok=None, probs=None),
@@ -272,3 +272,37 @@ def test_draws_follow_the_distribution(pkg):
     got = torch.bincount(tok.cpu().long(), minlength=V) / n
     # five standard deviations of a frequency
     assert (got - torch.tensor([0.1, 0.2, 0.3, 0.15, 0.25])).abs().max() < 5 * (0.25 / n) ** 0.5
+
+
+@pytest.mark.gpu
+def test_rows_from_n_rows_on_are_left(pkg):
+    x = logits_of("wide", 6, 40000, torch.float32, 5).cuda()
+    e = torch.full((6, 40000), 0.5, device="cuda")
+    full = torch.zeros(6, dtype=torch.int32, device="cuda")
+    pkg.sample(x, None, None, None, None, e, full)
+    for n in (0, 3, 6, 99):
+        tok = torch.full((6,), -77, dtype=torch.int32, device="cuda")
+        pkg.sample(x, None, None, None, None, e, tok, n_rows=torch.tensor([n], dtype=torch.int32, device="cuda"))
+        assert torch.equal(tok[:n], full[:n]) and (tok[n:] == -77).all()
+    assert pkg.read_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams(pkg):
+    """Two calls at once, and a call on a stream whose inputs another one wrote."""
+    x = [logits_of("wide", 40, 70001, torch.bfloat16, i).cuda() for i in range(2)]
+    e = torch.rand(40, 70001, device="cuda") + 0.01
+    p = torch.full((40,), 0.9, device="cuda")
+    want = []
+    for y in x:
+        want.append(torch.zeros(40, dtype=torch.int32, device="cuda"))
+        pkg.sample(y, None, None, p, None, e, want[-1])
+    torch.cuda.synchronize()
+    got = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in x]
+    for _ in range(3):
+        for s, y, t in zip(streams, x, got):
+            with torch.cuda.stream(s):
+                pkg.sample(y, None, None, p, None, e, t)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -73,6 +73,7 @@ struct Shared {
   float wapprox[kWarps];
   float e2h[17], e2l[17];              // 2^(-j / 16), j = -8 .. 8, in two parts
   float c_hi, c_lo;                    // log2(e) / T in two parts
+  double log_min;                      // T ln(min_p)
   int n_list, n_sorted;                // tokens that this CTA listed; of all, sorted (the first CTA's)
   // a decision of one thread or CTA for all
   int b_at;
@@ -189,6 +190,7 @@ struct Row {
   Kept lim;           // what earlier filters left, and of that what this one may keep
   Kept lim_all;       // what earlier filters left
   mass_t whole;       // its mass (weigh)
+  int n_listed;       // tokens of the last list, in all CTAs (more than kList: it is not whole)
   bool sorted;        // the list in the first CTA is
   bool listed;        // it is the first S.n_keep tokens of the first CTA's list
 
@@ -430,14 +432,15 @@ struct Row {
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
     float above = 0.f, in = 0.f;
+    int count = 0;
     each_left_from(least, [&](float l, bool is, int i) {
       const int at = is ? place(l) : 2;
       const float w = w_of(l);
       above += at == 0 ? w : 0.f;
       if (at == 1) {
         in += w;
-        // (a list that is full counts no further)
-        if (gather && *(volatile int*)&S.n_list <= kList) {
+        ++count;
+        if (gather && *(volatile int*)&S.n_list < kList) {
           const int slot = atomicAdd(&S.n_list, 1);
           if (slot < kList) S.list[slot] = (uint64_t)(~code_of(l)) << 32 | (uint32_t)(first + i);
         }
@@ -445,8 +448,9 @@ struct Row {
     });
     v[0] = __float2ll_rn(above * kUnit);
     v[1] = __float2ll_rn(in * kUnit);
-    v[2] = 0;
+    v[2] = count;
     sum3(v);
+    n_listed = (int)v[2];
     v[2] = whole;
   }
   // The bracket [f_lo, f_hi).
@@ -527,7 +531,7 @@ struct Row {
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       from[r] = n;
-      n += r < C ? cl.map_shared_rank(&S, r)->n_list : 0;
+      n += r < C ? min(cl.map_shared_rank(&S, r)->n_list, kList) : 0;
     }
     n = min(n, kList);
     constexpr int kEach = kList / kThreads;
@@ -553,24 +557,60 @@ struct Row {
     while (size < n) size <<= 1;
     for (int i = n + threadIdx.x; i < size; i += kThreads) S.list[i] = ~0ull;
     __syncthreads();
-    // bitonic; a warp has 64 places to itself while the distance is below 64
-    auto step = [&](int i, int k, int d) {
-      const int a = 2 * i - (i & (d - 1)), b = a + d;
-      const uint64_t x = S.list[a], y = S.list[b];
-      if ((x > y) == ((a & k) == 0)) {
-        S.list[a] = y;
-        S.list[b] = x;
+    // Bitonic.  A warp has 64 places to itself, two to a lane, in registers while the distance is below
+    // 64 (through shared memory throughout: three times as long).
+    static_assert(kList <= 64 * kWarps, "64 places a warp");
+    const int lane = threadIdx.x & 31, base = (threadIdx.x >> 5) * 64;
+    const bool part = base < size;
+    uint64_t x = 0, y = 0;
+    auto within = [&](int k) {  // the distances min(k, 64) / 2 .. 1 of phase k
+      const bool up = k < 64 || (base & k) == 0;
+      if (k >= 64 && (x > y) == up) {
+        const uint64_t t = x;
+        x = y;
+        y = t;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        if (d >= k) continue;
+        const uint64_t a = __shfl_xor_sync(0xffffffffu, x, d), b = __shfl_xor_sync(0xffffffffu, y, d);
+        // places base + lane and base + lane + 32
+        const bool low = (lane & d) == 0;
+        const bool up_x = k < 64 ? (lane & k) == 0 : up, up_y = k < 64 ? ((lane + 32) & k) == 0 : up;
+        x = ((x > a) == (up_x == low)) ? a : x;
+        y = ((y > b) == (up_y == low)) ? b : y;
       }
     };
-    for (int k = 2; k <= size; k <<= 1) {
-      for (int d = k >> 1; d > 0; d >>= 1) {
-        for (int i = threadIdx.x; i < size / 2; i += kThreads) step(i, k, d);
-        if (d > 32) __syncthreads();
-        else __syncwarp();
-      }
-      if (k >= 64 && k < size) __syncthreads();
+    if (part) {
+      x = S.list[base + lane];
+      y = S.list[base + lane + 32];
+#pragma unroll
+      for (int k = 2; k <= 64; k <<= 1) within(k);
+      S.list[base + lane] = x;
+      S.list[base + lane + 32] = y;
     }
     __syncthreads();
+    for (int k = 128; k <= size; k <<= 1) {
+      for (int d = k >> 1; d >= 64; d >>= 1) {
+        for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+          const int a = 2 * i - (i & (d - 1)), b = a + d;
+          const uint64_t u = S.list[a], w = S.list[b];
+          if ((u > w) == ((a & k) == 0)) {
+            S.list[a] = w;
+            S.list[b] = u;
+          }
+        }
+        __syncthreads();
+      }
+      if (part) {
+        x = S.list[base + lane];
+        y = S.list[base + lane + 32];
+        within(k);
+        S.list[base + lane] = x;
+        S.list[base + lane + 32] = y;
+      }
+      __syncthreads();
+    }
     return n;
   }
 
@@ -743,14 +783,23 @@ struct Row {
   __device__ float bound(int k, float p, float mx) {
     if (k > kThreads) return lim.t;
     if (k > 0) {
-      // k threads' own maxima lie from there on: so do k tokens
-      uint32_t lo = code_of(-INFINITY), hi = code_of(m);
+      // From there on lie the maxima of so many threads of each warp that they are k: so do k tokens.
+      const int need = (k + kWarps - 1) / kWarps, lane = threadIdx.x & 31;
       const uint32_t mine = code_of(mx);
-      for (int i = 0; i < 16 && hi - lo > 1; ++i) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (__syncthreads_count(mine >= mid) >= k) lo = mid; else hi = mid;
+      int above = 0;
+#pragma unroll
+      for (int o = 1; o < 32; ++o) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, o);
+        above += other > mine || (other == mine && (lane ^ o) < lane);
       }
-      return fmaxf(float_of(lo), lim.t);
+      const uint32_t at = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == need - 1)) - 1);
+      __syncthreads();
+      if (lane == 0) S.wcnt[threadIdx.x >> 5] = at;
+      __syncthreads();
+      uint32_t least = S.wcnt[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) least = min(least, S.wcnt[w]);
+      return fmaxf(float_of(least), lim.t);
     }
     // n tokens below weigh less than n times that one's w: the part 1 - p of the whole lies above
     const float x = log2f(2.f * n_row / ((1.f - p) * ((float)whole * (1.f / kUnit))));
@@ -764,6 +813,21 @@ struct Row {
     const float* const e = noise + first - shift;
     const bool out_wide = (reinterpret_cast<uintptr_t>(out) & (sizeof(P) * V::N - 1) & 15) == 0;
     const bool e_wide = RACE && (reinterpret_cast<uintptr_t>(e) & 15) == 0;
+    if (!out_wide) {
+      // Rows whose groups lie otherwise in memory than in the logits: token by token, each warp's side
+      // by side.
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float l = V::one(data, i + shift);
+        const bool is = LIMITED ? left(l, i) : l >= lim.t;
+        const float w = is ? w_of(l) : 0.f;
+        probs[first + i] = P(w * inv);
+        if (RACE && is) {
+          const float f = noise[first + i];
+          if (w > b.s2 * f) b.take(__fdividef(w, f), l, first + i);
+        }
+      }
+      return;
+    }
     const uint4* p = reinterpret_cast<const uint4*>(data);
     for (int q = threadIdx.x; q < groups; q += kThreads) {
       const int s0 = q * V::N;
@@ -777,7 +841,7 @@ struct Row {
         any |= keep[j];
       }
       const bool inside = s0 >= shift && s0 + V::N <= shift + n;
-      if (out_wide && inside) {
+      if (inside) {
         store_group<P>(out + s0, w, inv);
       } else {
 #pragma unroll
@@ -798,6 +862,15 @@ struct Row {
   __device__ __forceinline__ void run_race(const float* noise, Racer& b) const {
     const float* const e = noise + first - shift;      // of slot 0
     const bool e_wide = (reinterpret_cast<uintptr_t>(e) & 15) == 0;
+    if (!e_wide) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float l = V::one(data, i + shift);
+        if (!(LIMITED ? left(l, i) : l >= lim.t)) continue;
+        const float w = w_of(l), f = noise[first + i];
+        if (w > b.s2 * f) b.take(__fdividef(w, f), l, first + i);
+      }
+      return;
+    }
     const uint4* p = reinterpret_cast<const uint4*>(data);
     for (int q = threadIdx.x; q < groups; q += kThreads) {
       const int s0 = q * V::N;
@@ -808,7 +881,7 @@ struct Row {
       for (int j = 1; j < V::N; ++j) top = fmaxf(top, x[j]);
       if (!(top >= lim.t)) continue;
       // (a group's noise is a sector of memory, or half of one: it comes whole)
-      load_noise(e, s0, e_wide && s0 >= shift && s0 + V::N <= shift + n, x, f);
+      load_noise(e, s0, s0 >= shift && s0 + V::N <= shift + n, x, f);
 #pragma unroll
       for (int j = 0; j < V::N; ++j) {
         const bool keep = LIMITED ? left(x[j], s0 + j - shift) : x[j] >= lim.t;
@@ -871,11 +944,9 @@ struct Row {
     }
     // Of kThreads threads' tokens about kThreads ln(1 / (1 - k / kThreads)) pass k of their maxima;
     // where that is well below the list's size in all CTAs together, it is listed at once.
-    if (by_count && k < kThreads && -kThreads * __logf(1.f - k / (float)kThreads) * C < 0.8f * kList) {
+    if (by_count && k < kThreads && -kThreads * __logf(1.f - k / (float)kThreads) * C < 0.6f * kList) {
       evaluate(lim.t, INFINITY, true, v);
-      unsigned n = 0;
-      for (int r = 0; r < C; ++r) n += (unsigned)cl.map_shared_rank(&S, r)->n_list;
-      if (n <= (unsigned)kList) {
+      if (n_listed <= kList) {
         done_p = true;
         v[0] = 0;
         float z;
@@ -886,7 +957,6 @@ struct Row {
         }
         return z;
       }
-      cl.sync();  // (n_list is read)
     }
     // 1: buckets of (m - l) / T
     histogram([&](float l) { return bucket_of(l); });
@@ -1148,6 +1218,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p <= 0.f) p = 1.f, k = 1;  // the first token alone
   const bool use_k = k > 0 && k < a.V, use_p = p < 1.f;
   cl.barrier_arrive();  // (waited for before the first access to another CTA's memory)
+  // (one thread: 64 bits are slow here, and only a border needs them)
+  if (mp > 0.f && tid == 0) S.log_min = (double)temp * log((double)mp);
   if (tid == kThreads - 1) {
     // log2(e) = 1.44269502162933349609375 + 1.92596299112661746887e-8
     const float h = 1.44269502162933349609375f, c = h / temp;
@@ -1188,8 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.lim.t = -FLT_MAX;
   R.lim.i = 0x7fffffff;
   if (mp > 0.f) {
-    // (64 bits: a border)
-    const double t = (double)m + (double)temp * log((double)mp);
+    const double t = (double)m + S.log_min;
     float f = (float)t;
     if ((double)f < t) f = float_of(code_of(f + 0.f) + 1);
     R.lim.t = fmaxf(fminf(f, m), -FLT_MAX);

@@ -367,8 +367,8 @@ int dspark_block_accept_estimate(const void* p_target, const void* p_draft, int 
  * If the free stack or a page-table row is too short the device sets
  * DSPARK_DEVERR_NO_FREE_PAGE / _PAGE_ROW_FULL, if cu_seqlens[B] > max_rows it sets
  * DSPARK_DEVERR_ROWS_OVERFLOW, and if cu_seqlens[0] < 0 or accept_len[r] is outside
- * 0..gamma or keeps more rows than request r's packed segment holds it sets
- * DSPARK_DEVERR_BAD_INPUT; in each of these cases it changes nothing.
+ * 0..gamma or keeps more rows than request r's packed segment holds, or ctx_len[r] is
+ * negative or its positions would pass 32 bits, it sets DSPARK_DEVERR_BAD_INPUT; in each of these cases it changes nothing.
  * ------------------------------------------------------------------------- */
 size_t dspark_compact_workspace_size(int B);
 int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,
@@ -663,6 +663,7 @@ int dspark_compact_path(const void* k_new, const void* v_new, int row_bytes, int
  *   out       bf16 [max_rows, Hq, 128]; a row that sees no key, or none with a score
  *             above -inf, gets out = 0 and lse = -inf
  *   scale     a positive normal number
+ *   max_splits  as there, times 5 (so that 32 reach every SM with one long group)
  *   max_block_rows  a hint: the largest tree.  Up to 128 / G rows (G = Hq / Hkv <= 128) one query
  *             tile of 128 rows is used, above that two that share the keys; any segment
  *             length is handled.  The workspace size depends on it.
@@ -672,7 +673,7 @@ int dspark_compact_path(const void* k_new, const void* v_new, int row_bytes, int
  * A page out of range sets DSPARK_DEVERR_BAD_INPUT; its request's outputs are then undefined.
  * A negative length or first row, or ctx_len[r] and the rows of r together past 2^31 - 769,
  * sets it too, and nothing is written; so with cu_seqlens[B] outside 0..max_rows and
- * DSPARK_DEVERR_ROWS_OVERFLOW.
+ * DSPARK_DEVERR_ROWS_OVERFLOW.  Two kernels; nothing waits on another CTA.
  * ------------------------------------------------------------------------- */
 size_t dspark_verify_attn_tree_workspace_size(int B, int max_rows, int Hq, int Hkv, int max_splits,
                                               int max_block_rows);
@@ -706,7 +707,8 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  *   top_k       int32 [B]: off where < 1 or >= V; NULL: off
  *   top_p       fp32 [B]: off where >= 1, the first token alone where <= 0; NULL: off
  *   min_p       fp32 [B]: off where <= 0, as 1 where above; NULL: off
- *   exp_noise   fp32 [rows, V] Exp(1) draws, > 0; NULL without tokens
+ *   exp_noise   fp32 [rows, V] Exp(1) draws, > 0; NULL without tokens (only those of the kept
+ *               tokens' surroundings are read)
  *   tokens      int32 [rows] out, nullable
  *   probs       [rows, V] fp32 or bf16 (probs_dtype) out, dense, nullable
  * Which tokens are kept and which wins the race is decided as in 64-bit arithmetic (but where

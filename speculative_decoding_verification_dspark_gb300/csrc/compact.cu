@@ -83,6 +83,10 @@ __global__ void __launch_bounds__(1024)
       atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
     }
     c0 = ctx_len[tid];
+    if (c0 < 0 || c0 > 0x7fffffff - page_size - keep) {  // (positions past 32 bits)
+      atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);
+      c0 = 0;
+    }
     have = ceil_div(c0, page_size);
     need = ceil_div(c0 + keep, page_size);
     nn = need - have;

@@ -233,7 +233,7 @@ def test_commit_of_a_path(pkg, sizes, page, Hkv, gamma):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("bad", ["entry", "negative", "length", "below", "rows"])
+@pytest.mark.parametrize("bad", ["entry", "negative", "length", "below", "rows", "ctx", "far"])
 def test_commit_refused_changes_nothing(pkg, bad):
     rng = np.random.default_rng(3)
     sizes, gamma = [4, 4], 3
@@ -251,6 +251,10 @@ def test_commit_refused_changes_nothing(pkg, bad):
         n[0] = -2
     if bad == "rows":
         cu = np.array([0, 9, 8], np.int32)
+    if bad == "ctx":
+        s["ctx_len"][1] = -100
+    if bad == "far":
+        s["ctx_len"][1] = 2 ** 31 - 2
     d = {k: torch.tensor(v, device="cuda") for k, v in s.items()}
     kn = torch.ones(8, 2, 128, dtype=torch.int16, device="cuda")
     out = torch.zeros(2, dtype=torch.int32, device="cuda")

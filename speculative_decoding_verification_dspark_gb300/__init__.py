@@ -380,7 +380,7 @@ def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table
     """``path`` (int32 [B, gamma + 1], accept_tree's): the rows of a tree that are kept, with
     accept_tree's path_tok as draft_tok (dspark_compact_path)."""
     B, gamma = draft_tok.shape
-    row_bytes = k_new[0].numel() * k_new.element_size()
+    row_bytes = k_new.numel() // max(k_new.shape[0], 1) * k_new.element_size()
     name, more = "dspark_compact", ()
     if path is not None:
         name = "dspark_compact_path"
@@ -390,7 +390,7 @@ def compact(k_new, v_new, cu_seqlens, accept_len, out_tok, draft_tok, page_table
         _ptr(draft_tok), *more, B, gamma, k_cache.shape[1], page_table.shape[1], k_cache.shape[0],
         _ptr(page_table), _ptr(ctx_len), _ptr(anchor), _ptr(free_pages), _ptr(free_top),
         _ptr(k_cache), _ptr(v_cache), _ptr(committed), _ptr(n_committed), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _stream(stream, _current(k_new))))
 
 
 # ---- query/key norm with rotation, and the 4-bit cache.  These bindings also check types,

@@ -21,7 +21,13 @@
 // them is NaN: the rows that do see them get them after the epilogue (write_specials).
 //   4-7, 8-11  the softmax of the streams, thread = row: maximum, exponentials and sum of 128 keys
 //          without a word to another thread; O is rescaled only where a row's maximum grows by 2^8
-// Every wait is bounded in time (DSPARK_DEVERR_WAIT_TIMEOUT on expiry).
+// Every wait is bounded (DSPARK_DEVERR_WAIT_TIMEOUT on expiry).
+//
+// What bounds it: with one query tile HBM (256 single tokens over 0.5k to 4k keys 397 us, 357 at the copy
+// rate); with two a stream's chain, 3500 cycles a key tile: S to the softmax 150, 128 exponentials a
+// thread and P 1300, P to the issuing thread 150, O += P V and the next S 2 x 520, and 250 more each
+// time the tensor cores change from the one kind of product to the other (32 requests of 17 to 64
+// nodes over 1k to 4k keys 111 us, 52 at the copy rate; 16 of 97 to 256 nodes 294 us).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -69,7 +75,7 @@ struct Smem {  // the first 3 KB; then Q (two tiles) and the ring
   float ml[2][kM][2];                  // (reference, sum) of a stream's rows at an item's end
   AttnItem items[4];
 };
-constexpr int kHead = 3072;
+constexpr int kHead = 3 * 1024;
 static_assert(sizeof(Smem) <= kHead, "head of the shared memory");
 constexpr int kSmemBytes = kHead + 2 * kTile + kStages * kTile;
 static_assert(kSmemBytes <= 232448, "shared memory budget");

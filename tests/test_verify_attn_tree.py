@@ -282,3 +282,13 @@ def test_bad_input(pkg):
     clean = fresh().run(pkg)[0]
     out, _ = c.run(pkg)
     assert c.err == 0x10 and torch.equal(out[:3], clean[:3]) and (out[7:] == 77).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(6))
+def test_shares_of_mixed_batches(pkg, seed):
+    """Segments of one and of two query tiles, whose key tiles count differently in the CTAs' shares."""
+    rng = np.random.default_rng(seed)
+    sizes = [int(rng.choice([0, 1, 31, 32, 33, 64, 65, 130])) for _ in range(9)]
+    ctx = [int(rng.choice([0, 1, 127, 128, 700, 2049])) for _ in range(9)]
+    Case(sizes, ctx, 4, 1, 32, seed=seed).verify(pkg, splits=int(rng.choice([1, 3, 32])))

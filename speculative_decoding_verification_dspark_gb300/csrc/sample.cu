@@ -494,15 +494,20 @@ struct Row {
     wl = rl * scale;
   }
 
-  // list_by's masses in pairs, v[2] that of all tokens that earlier filters left.
-  template <class Fn>
-  __device__ __forceinline__ void weigh_pairs(double (&v)[3], Fn&& place) {
+  // w_pair's table, before its first use in a row.
+  __device__ void make_table() {
+    __syncthreads();
     if (threadIdx.x < 17) {
       const double e = exp2(-((int)threadIdx.x - 8) / 16.0);  // (few: 64 bits are slow here)
       S.e2h[threadIdx.x] = (float)e;
       S.e2l[threadIdx.x] = (float)(e - (double)(float)e);
     }
     __syncthreads();
+  }
+  // list_by's masses in pairs, v[2] that of all tokens that earlier filters left.
+  template <class Fn>
+  __device__ __forceinline__ void weigh_pairs(double (&v)[3], Fn&& place) {
+    make_table();
     float ah = 0, al = 0, ih = 0, il = 0, bh = 0, bl = 0;
     auto add = [](float& sh, float& sl, float wh, float wl) {
       const float t = sh + wh, z = t - sh;
@@ -766,6 +771,7 @@ struct Row {
         __syncthreads();
       }
       const int n = S.n_sorted, most = k > 0 ? (int)min((unsigned)n, (unsigned)k - before) : n;
+      if (pairs) make_table();  // (where the list has it all nothing was weighed in pairs before)
       if (pairs) walk(n, d, most, k > 0, use_p, p);
       else walk(n, v, most, k > 0, use_p, p);
       if (threadIdx.x > 0 && threadIdx.x < C) {

@@ -198,6 +198,19 @@ def test_borders_that_fp32_cannot_tell(pkg):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [700, 1000, 5000])
+def test_borders_of_top_p_within_top_k(pkg, V):
+    """Top-p meets a border exactly among the tokens that top-k leaves, the list holding them all."""
+    n = 6
+    x = torch.full((n, V), -30.0)
+    x[:, 1:V:V // 640] = 0.5                    # some 640 and more equal ones
+    k = [64, 100, 128, 500, 600, 640]
+    for p in (0.5, 0.25, 0.75):
+        compare(pkg, x, (None, k, [p] * n, None), 12)
+        compare(pkg, x.bfloat16(), (None, k, [p] * n, None), 12)
+
+
+@pytest.mark.gpu
 def test_special_values(pkg):
     for dtype in (torch.float32, torch.bfloat16):
         x = logits_of("wide", 6, 3001, dtype, 1)

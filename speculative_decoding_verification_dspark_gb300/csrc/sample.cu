@@ -25,8 +25,8 @@
 //
 // What bounds it: instructions, and the meetings of the cluster (some eight a row, 1500 cycles each).
 // A pass over a chunk costs 6000 cycles for two CTAs of an SM, loading it 7000.  One row of 151936:
-// 16 us; 288 such rows with distributions 235 us (56 at the copy rate); 1024 rows of 129280 in bf16,
-// top-p with wide nuclei, 640 us (39).  512 threads with 76 KB, two to an SM: 256 threads with 38 KB
+// 16 to 19 us; 288 such rows with distributions 233 to 243 us (56 at the copy rate); 1024 rows of 129280 in bf16,
+// top-p with wide nuclei, 612 to 640 us (39).  512 threads with 76 KB, two to an SM: 256 threads with 38 KB
 // take 1143 us where these take 874 (larger clusters), 1024 with 152 KB 926.
 
 #include <cooperative_groups.h>

@@ -74,7 +74,7 @@ struct Shared {
   unsigned tot[kBuckets];              // the row's, in order of falling logits
   uint64_t list[kList];                // (order of the logit, index)
   unsigned long long part[2][kMaxCluster][3];  // exchanged between the CTAs, two sets in turn
-  float cmax[kMaxCluster];
+  float cmax[kMaxCluster], cleast[kMaxCluster];
   unsigned long long wsum[kWarps][3];
   float wmax[kWarps];
   unsigned wcnt[kWarps];
@@ -198,6 +198,7 @@ struct Row {
   float t_min;        // least logit that min-p leaves
   Kept lim;           // what earlier filters left, and of that what this one may keep
   Kept lim_all;       // what earlier filters left
+  float k_least;      // a logit that k of the row's tokens reach (-inf: none is known)
   mass_t whole;       // its mass (weigh)
   int n_listed;       // tokens of the last list, in all CTAs (more than kList: it is not whole)
   bool sorted;        // the list in the first CTA is
@@ -794,28 +795,10 @@ struct Row {
     return true;
   }
 
-  // A logit below which the filter keeps nothing, from what is known before the row is searched.
-  __device__ float bound(int k, float p, float mx) {
-    if (k > kThreads) return lim.t;
-    if (k > 0) {
-      // From there on lie the maxima of so many threads of each warp that they are k: so do k tokens.
-      const int need = (k + kWarps - 1) / kWarps, lane = threadIdx.x & 31;
-      const uint32_t mine = code_of(mx);
-      int above = 0;
-#pragma unroll
-      for (int o = 1; o < 32; ++o) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, o);
-        above += other > mine || (other == mine && (lane ^ o) < lane);
-      }
-      const uint32_t at = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == need - 1)) - 1);
-      __syncthreads();
-      if (lane == 0) S.wcnt[threadIdx.x >> 5] = at;
-      __syncthreads();
-      uint32_t least = S.wcnt[0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) least = min(least, S.wcnt[w]);
-      return fmaxf(float_of(least), lim.t);
-    }
+  // A logit below which the filter keeps nothing, from what is known before the row is searched.  The
+  // same in all CTAs, as the bracket's ends in `cut` follow from it.
+  __device__ float bound(int k, float p) {
+    if (k > 0) return fmaxf(k_least, lim.t);
     // n tokens below weigh less than n times that one's w: the part 1 - p of the whole lies above
     const float x = log2f(2.f * n_row / ((1.f - p) * ((float)whole * (1.f / kUnit))));
     return fmaxf(m + fmaxf(x, 0.f) / nc, lim.t);
@@ -941,9 +924,8 @@ struct Row {
   }
 
   // One filter's end (k > 0: top-k, with top-p at once where the list holds all that top-k keeps;
-  // else top-p of what is left).  Sets lim; returns the mass kept; done_p: top-p is applied.  mx:
-  // the largest logit of this thread's tokens.
-  __device__ float cut(int k, bool use_p, float p, float mx, bool& done_p) {
+  // else top-p of what is left).  Sets lim; returns the mass kept; done_p: top-p is applied.
+  __device__ float cut(int k, bool use_p, float p, bool& done_p) {
     const bool by_count = k > 0;
     listed = sorted = false;
     lim_all = lim;
@@ -952,7 +934,7 @@ struct Row {
     bool pairs = false;
     if (!by_count && whole < 0) weigh();
     // 0: what may be kept at all
-    const float least = bound(k, p, mx);
+    const float least = bound(k, p);
     if (least > lim.t) {
       lim.t = least;
       lim.i = kNone;
@@ -1138,6 +1120,27 @@ __device__ __forceinline__ float block_max(Shared& S, float v) {
   return v;
 }
 
+// A logit that k (1 .. kThreads) of this CTA's tokens reach, from the largest logit of each thread's
+// tokens: from there on lie the maxima of so many threads of each warp that they are k.
+__device__ __forceinline__ float reached_by(Shared& S, int k, float mx) {
+  const int need = (k + kWarps - 1) / kWarps, lane = threadIdx.x & 31;
+  const uint32_t mine = code_of(mx);
+  int above = 0;
+#pragma unroll
+  for (int o = 1; o < 32; ++o) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, o);
+    above += other > mine || (other == mine && (lane ^ o) < lane);
+  }
+  const uint32_t at = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == need - 1)) - 1);
+  __syncthreads();
+  if (lane == 0) S.wcnt[threadIdx.x >> 5] = at;
+  __syncthreads();
+  uint32_t least = S.wcnt[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) least = min(least, S.wcnt[w]);
+  return float_of(least);
+}
+
 // (score, index) of the better: higher score, lower index.
 __device__ __forceinline__ void better(double& s, int& i, double s2, int i2) {
   if (s2 > s || (s2 == s && i2 < i)) {
@@ -1242,14 +1245,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     S.c_lo = (fmaf(-c, temp, h) + 1.92596299112661746887e-8f) / temp;
   }
   const float mx_cta = block_max(S, mx);
+  const float least_cta = use_k && k <= kThreads ? reached_by(S, k, mx) : -INFINITY;
   cl.barrier_wait();
-  if (tid < C) cl.map_shared_rank(&S, tid)->cmax[rank] = mx_cta;
+  if (tid < C) {
+    Shared* o = cl.map_shared_rank(&S, tid);
+    o->cmax[rank] = mx_cta;
+    o->cleast[rank] = least_cta;
+  }
   cl.sync();
-  float m = S.cmax[0];
-  for (int r = 1; r < C; ++r) m = fmaxf(m, S.cmax[r]);
+  // (k tokens of one CTA are k of the row: its best bound is any CTA's)
+  float m = S.cmax[0], least = S.cleast[0];
+  for (int r = 1; r < C; ++r) {
+    m = fmaxf(m, S.cmax[r]);
+    least = fmaxf(least, S.cleast[r]);
+  }
   if (m == INFINITY) {  // +inf counts as the type's largest number
     m = V::kTop;
-    mx = fminf(mx, m);
+    least = fminf(least, m);
     uint4* const d = reinterpret_cast<uint4*>(data);
     for (int q = tid; q < R.groups; q += kThreads) {
       float x[V::N];
@@ -1261,6 +1273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
   R.m = m;
+  R.k_least = least;
   R.s = S.c_hi * kPerOctave;
   R.nc = -S.c_hi;
   P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V : nullptr;
@@ -1289,8 +1302,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     R.lim.i = R.first_top();
     z = 1.f;
   }
-  if (use_k) z = R.cut(k, use_p, p, mx, done_p);
-  if (use_p && !done_p) z = R.cut(0, true, p, mx, done_p);
+  if (use_k) z = R.cut(k, use_p, p, done_p);
+  if (use_p && !done_p) z = R.cut(0, true, p, done_p);
   const bool race = a.tokens != nullptr;
   if (greedy && race && rank == 0 && tid == 0) a.tokens[row] = R.lim.i;
   if (!probs && (greedy || (R.listed && rank != 0))) return;

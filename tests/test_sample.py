@@ -319,3 +319,43 @@ def test_calls_on_two_streams(pkg):
                 pkg.sample(y, None, None, p, None, e, t)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def _over_ctas(kind, n, V, dtype, seed):
+    """n rows and a temperature: logits that lie so close that no list holds those around the k-th, or
+    more equal largest ones than a list holds, in one part of the row alone."""
+    g = torch.Generator().manual_seed(seed)
+    x, T = torch.randn(n, V, generator=g), 1.0
+    at, size = {"first": (0, V // 8), "middle": (3 * V // 8 + 5, V // 8), "last": (V - V // 8, V // 8),
+                "most": (0, V // 4 + 3)}.get(kind, (0, 0))
+    if kind == "narrow":
+        x = 0.001 * x
+    elif kind in ("hot", "hotter"):
+        x, T = 3 * x, 1e3 if kind == "hot" else 1e6
+    elif kind == "masked":                    # all ruled out but one range, of nearly equal ones
+        x = 0.001 * x
+        x[:, :V // 2], x[:, V // 2 + 4000:] = -float("inf"), -float("inf")
+    else:
+        x = x.clamp(max=4.0) - (10.0 if kind == "most" else 0.0)
+        x[:, at:at + size] = 5.0
+    return x.to(dtype), T
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["first", "middle", "last", "most", "masked", "narrow", "hot", "hotter"])
+@pytest.mark.parametrize("V,dtype", [(151936, torch.float32), (129280, torch.bfloat16),
+                                     (50257, torch.float32), (50257, torch.bfloat16)])
+def test_short_top_k_over_several_ctas(pkg, kind, V, dtype):
+    """Where the k-th lies among thousands, all CTAs of a row search the same range for it."""
+    k = [1, 2, 50, 73, 100, 133, 200, 231, 400, 512]
+    n = len(k)
+    x, T = _over_ctas(kind, n, V, dtype, V)
+    compare(pkg, x, ([T] * n, k, None, None), 13)
+    compare(pkg, x, ([T] * n, k, [0.05 + 0.09 * i for i in range(n)], [0.3, 0.9] * (n // 2)), 14, None)
+
+
+@pytest.mark.gpu
+def test_top_p_of_zero_over_several_ctas(pkg):
+    """The first token alone, among thousands of equal ones."""
+    x, _ = _over_ctas("most", 4, 151936, torch.float32, 1)
+    compare(pkg, x, (None, None, [0.0, -1.0, 0.0, 0.5], None), 15)

@@ -715,7 +715,8 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  * sums lie within 10^-10 of a border); probs are fp32 values (2^-16) rounded once.  A row
  * without any logit above -inf gets token -1 and probs 0.  An index >= B, or a temperature
  * outside its range, or a NaN parameter sets DSPARK_DEVERR_BAD_INPUT and the row's outputs
- * are left as they are.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
+ * are left as they are; so with DSPARK_DEVERR_WORK_OVERFLOW should a row's search contradict
+ * itself, which no input is known to bring about.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
  * ------------------------------------------------------------------------- */
 int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
                   const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,

@@ -203,6 +203,7 @@ struct Row {
   int n_listed;       // tokens of the last list, in all CTAs (more than kList: it is not whole)
   bool sorted;        // the list in the first CTA is
   bool listed;        // it is the first S.n_keep tokens of the first CTA's list
+  bool lost;          // the search contradicted itself (counts of one bracket that differ, no end)
 
   // (rounded by the addition of 2^23: monotone in l, which is all that is asked)
   __device__ __forceinline__ int bucket_of(float l) const {
@@ -977,6 +978,8 @@ struct Row {
       };
       list_by(fmaxf(b1 == kBuckets - 1 ? -FLT_MAX : near - 4e-7f * (fabsf(m) + fabsf(near)), lim.t), true, v,
               place);
+      lost = (unsigned)n_listed != in;
+      if (lost) return 0.f;
       float z;
       done_p = !by_count || before == 0;
       const mass_t goal = by_count ? 0 : goal_of(p, whole), margin = near_of(whole);
@@ -1017,6 +1020,8 @@ struct Row {
     for (int round = 0; round < 100; ++round) {
       const bool gather = in <= (unsigned)kList;
       evaluate(f_lo, f_hi, gather, v);
+      lost = (unsigned)n_listed != in;
+      if (lost) return 0.f;
       if (!by_count) {
         // does the bracket hold the end?
         if (!pairs) {
@@ -1103,8 +1108,8 @@ struct Row {
       before += S.cum_before;
       in = S.cum_in;
     }
-    done_p = false;
-    return (float)v[0] * (1.f / kUnit);
+    lost = true;
+    return 0.f;
   }
 };
 
@@ -1172,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.set = 0;
   R.n_row = a.V;
   R.whole = -1;
-  R.listed = R.sorted = false;
+  R.listed = R.sorted = R.lost = false;
   const T* src = static_cast<const T*>(a.logits) + row * a.stride + R.first;
   R.shift = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
   R.groups = (R.n + R.shift + V::N - 1) / V::N;
@@ -1303,7 +1308,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     z = 1.f;
   }
   if (use_k) z = R.cut(k, use_p, p, done_p);
-  if (use_p && !done_p) z = R.cut(0, true, p, done_p);
+  if (use_p && !done_p && !R.lost) z = R.cut(0, true, p, done_p);
+  if (R.lost) {
+    if (rank == 0 && tid == 0) raise_error(a.err, DSPARK_DEVERR_WORK_OVERFLOW);
+    return;
+  }
   const bool race = a.tokens != nullptr;
   if (greedy && race && rank == 0 && tid == 0) a.tokens[row] = R.lim.i;
   if (!probs && (greedy || (R.listed && rank != 0))) return;

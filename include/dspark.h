@@ -712,7 +712,7 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  *   tokens      int32 [rows] out, nullable
  *   probs       [rows, V] fp32 or bf16 (probs_dtype) out, dense, nullable
  * Which tokens are kept and which wins the race is decided as in 64-bit arithmetic (but where
- * sums lie within 10^-10 of a border); probs are fp32 values (2^-16) rounded once.  A row
+ * sums lie within 10^-10 of a border; the race with noise of 2^-100 to 2^20, as Exp(1) draws are); probs are fp32 values (2^-16) rounded once.  A row
  * without any logit above -inf gets token -1 and probs 0.  An index >= B, or a temperature
  * outside its range, or a NaN parameter sets DSPARK_DEVERR_BAD_INPUT and the row's outputs
  * are left as they are; so with DSPARK_DEVERR_WORK_OVERFLOW should a row's search contradict

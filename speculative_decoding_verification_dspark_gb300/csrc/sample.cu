@@ -168,7 +168,8 @@ struct Kept {    // tokens with l > t, or l == t and an index of at most i
   int i;
 };
 
-// A thread's two best in the race, the lower index first among equals as they come.
+// A thread's two best in the race, the lower index first among equals as they come.  (Where the second
+// comes near the row's best the race is run again in 64 bits.)
 constexpr int kNone = 0x7fffffff;
 struct Racer {
   float s1 = -0x1p-60f, s2 = -0x1p-60f, l1 = 0.f, l2 = 0.f;
@@ -1343,9 +1344,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (!race || greedy) return;
 
-  // the best in fp32: mostly nothing comes near it (fp32's error is 2^-18 at most)
+  // The best in fp32: mostly nothing comes near it.  A score whose logit lies x octaves below the top is
+  // off by ln 2 * 3 * 2^-24 x (three roundings of the exponent) + 2^-21 (exponential and division) at
+  // most.  With noise between 2^-100 and 2^20 no token more than 120 octaves down wins or comes near:
+  // two scores are off by 2^-15 together.
   const float top_cta = block_max(S, b.s1);
-  constexpr float kClose = 1.f - 0x1p-16f;
+  constexpr float kClose = 1.f - 0x1p-14f;
   auto close = [&](float s, int i, float top) { return i != kNone && s >= top * kClose; };
   int n_near = __syncthreads_count(close(b.s1, b.i1, top_cta)) + __syncthreads_count(close(b.s2, b.i2, top_cta));
   float top = top_cta;
@@ -1367,12 +1371,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   // else in 64 bits, among those that come near
   double rs = -INFINITY;
   int ri = kNone;
-  auto precise = [&](float s, float l, int i) {
-    if (close(s, i, top))
-      better(rs, ri, ((double)l - (double)m) / (double)temp - log((double)noise[i]), i);
+  float pl = 0.f, pe = 0.f;  // (equal pairs of logit and noise have equal scores: the first one's counts)
+  auto precise = [&](float l, float e, int i) {
+    if (ri != kNone && l == pl && e == pe) return;
+    better(rs, ri, ((double)l - (double)m) / (double)temp - log((double)e), i);
+    pl = l;
+    pe = e;
   };
-  precise(b.s1, b.l1, b.i1);
-  precise(b.s2, b.l2, b.i2);
+  if (__syncthreads_or(!solo && close(b.s2, b.i2, top))) {
+    // a thread whose second comes near may have had a third (not of a list: that is two to a thread)
+    for (int i = tid; i < R.n; i += kThreads) {
+      const float l = V::one(data, i + R.shift);
+      if (!R.left(l, i)) continue;
+      const float e = noise[R.first + i];
+      if (close(__fdividef(R.w_of(l), e), i, top)) precise(l, e, R.first + i);
+    }
+  } else {
+    if (close(b.s1, b.i1, top)) precise(b.l1, noise[b.i1], b.i1);
+    if (close(b.s2, b.i2, top)) precise(b.l2, noise[b.i2], b.i2);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     better(rs, ri, __shfl_xor_sync(0xffffffffu, rs, o), __shfl_xor_sync(0xffffffffu, ri, o));

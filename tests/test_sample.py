@@ -359,3 +359,40 @@ def test_top_p_of_zero_over_several_ctas(pkg):
     """The first token alone, among thousands of equal ones."""
     x, _ = _over_ctas("most", 4, 151936, torch.float32, 1)
     compare(pkg, x, (None, None, [0.0, -1.0, 0.0, 0.5], None), 15)
+
+
+def _race(pkg, logits, noise, T, kind):
+    """Tokens of the call with and without distributions, and what the oracle draws."""
+    rows, V = logits.shape
+    dev = lambda x: None if x is None else torch.full((rows,), x, device="cuda")  # noqa: E731
+    got = []
+    for probs in (None, torch.zeros(rows, V, device="cuda")):
+        tok = torch.full((rows,), -77, dtype=torch.int32, device="cuda")
+        pkg.sample(logits.cuda(), dev(T), None, dev(0.999 if kind == "top_p" else None), None, noise.cuda(), tok, probs)
+        got.append(tok.tolist())
+    assert pkg.read_device_error() == 0
+    p = np.float32(0.999 if kind == "top_p" else 1)
+    return got, [O.sample_row(l.float().numpy(), np.float32(T), 0, p, np.float32(0), e.numpy())[0]
+                 for l, e in zip(logits, noise)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["off", "top_p"])
+@pytest.mark.parametrize("V", [3000, 60000, 151936])
+def test_near_ties_of_the_race(pkg, V, kind):
+    """Many tokens whose scores are one fp32 number, or apart by less than its error: the winner is
+    the definition's, wherever it stands among them."""
+    g = torch.Generator().manual_seed(V)
+    # different logits of one fp32 weight, constant noise
+    x = 1 + torch.randint(0, 64, (4, V), generator=g) * 2.0 ** -20
+    for i in range(4):
+        x[i, (2 * i + 1) * V // 8] = 1 + 64 * 2.0 ** -20
+    got, want = _race(pkg, x, torch.full((4, V), 0.5), 1e5, kind)
+    assert got == [want] * 2
+    # 20 to 90 octaves below the largest, with noise that brings them to a score of 1 +- 2^-24
+    x = -14 - 48 * torch.rand(4, V, generator=g)
+    x[:, 5] = 0.0
+    noise = torch.exp(x.double()).float()
+    noise[:, 5] = 4.0
+    got, want = _race(pkg, x, noise, 1.0, "off")
+    assert got == [want] * 2

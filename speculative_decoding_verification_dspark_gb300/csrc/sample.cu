@@ -55,12 +55,52 @@ constexpr int kChunkBytes = 76 * 1024; // of a row in one CTA, while eight CTAs 
 // 2^63): without the card's slow 64-bit floating point, which the sums in pairs need.
 typedef long long mass_t;
 constexpr float kUnit = 0x1p44f;
-// Error that the fp32 sums may have, as a part of the whole: 2^-22.  What counts is the error of a ratio
-// of two sums.  A token x octaves below the top is off by (x + 1) 2^-24 or so, most of it another
-// amount for every logit; the part that is the same for all (the factor's rounding) moves the ratio by
-// a quarter of the octaves between what is kept and what is not, times 2^-25.  Sums over a thread's
-// tokens add 2^-25 times the root of their number, and average out over 500 threads and more.
-__device__ __forceinline__ mass_t near_of(mass_t whole) { return whole >> 22; }
+// Error that a sum of w in fp32 may have against p of the whole, where it lies near that; of n tokens.
+// u = 2^-24, a = p and b = 1 - p the parts before the border and behind it, W the whole.
+//   w of a token x octaves below the top: its exponent has the roundings of m - l, of the product and of
+//   the factor, each u, and u / 4 from log2(e): ln 2 u x of w for each.  Equal logits share them, so
+//   nothing averages out.  With X and Y the mean octaves of the two parts the sum is off by at most
+//   ln 2 u a b (1.25 (Y - X) + 2 (X + Y)) W, the factor's error being one for all.  A part of mass M
+//   and n tokens has a mean of log2(n / M) octaves at most.
+//   The exponential is off by 2^-22 of w: 8 a b u W.
+//   The sums themselves (Sum): 2 u each, W being 1 at least.
+__device__ __forceinline__ float near_of(float p, float whole, int n) {
+  const float a = p * whole, b = (1 - p) * whole;
+  const float x = __log2f(__fdividef(n, a)), y = __log2f(__fdividef(n, b));
+  return 0x1p-24f * ((1 - p) * a * (2.3f * y + 1.4f * x + 8.5f) + 4.f);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  const float2 one = make_float2(-1.f, -1.f);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(one)),
+        "l"(reinterpret_cast<uint64_t&>(a)));
+  return d;
+}
+// Two running sums of w (0 <= w <= 1) that keep what each addition rounds away: they begin at 1, so that
+// the sum is the larger addend and that is exact.  What is lost of n tokens is n u (1 + sum) at most and
+// its own sum is off by n u of that: over 8192 sums of 49 tokens (the most there are) 1.1 u.
+struct Sum {
+  float2 s = make_float2(1.f, 1.f), lost = make_float2(0.f, 0.f);
+  __device__ __forceinline__ void add(float a, float b) {
+    const float2 w = make_float2(a, b), t = add2(s, w);
+    lost = add2(lost, sub2(w, sub2(t, s)));
+    s = t;
+  }
+  __device__ __forceinline__ mass_t fixed() const {
+    return __float2ll_rn((s.x - 1) * kUnit) + __float2ll_rn((s.y - 1) * kUnit) +
+           __float2ll_rn((lost.x + lost.y) * kUnit);
+  }
+};
+__device__ __forceinline__ mass_t rough_of(mass_t in) { return in >> 17; }
 // What lies before a kept token is short of p of the whole (0 < p < 1).
 __device__ __forceinline__ mass_t goal_of(float p, mass_t whole) {
   const unsigned long long f = __float2ull_rn(p * 0x1p64f), w = whole;
@@ -227,7 +267,7 @@ struct Row {
     }
   }
 
-  // fn(l, in, i) for the tokens of the groups that have one with l >= least, in: it is such a one and
+  // fn(l, in, i, j) for the tokens of the groups that have one with l >= least, in: it is such a one and
   // (LIMITED) left.  The others cost a maximum a group.  fn should not branch: in a warp with any
   // such token all of it runs.
   template <bool LIMITED, class Fn>
@@ -243,7 +283,7 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < V::N; ++j) {
           const int i = q * V::N + j - shift;
-          fn(x[j], x[j] >= least && (!LIMITED || left(x[j], i)), i);
+          fn(x[j], x[j] >= least && (!LIMITED || left(x[j], i)), i, j);
         }
     }
   }
@@ -251,6 +291,10 @@ struct Row {
   __device__ __forceinline__ void each_left_from(float least, Fn&& fn) const {
     if (lim.i == kNone) each_from<false>(least, fn);
     else each_from<true>(least, fn);
+  }
+
+  __device__ __forceinline__ mass_t near_fixed(float p, mass_t of) const {
+    return __float2ll_ru(near_of(p, (float)of * (1.f / kUnit), n_row) * kUnit);
   }
 
   // Sums of three numbers (mass_t or double) over the row, the same in every thread of the cluster and
@@ -291,7 +335,7 @@ struct Row {
     __syncthreads();
     for (int b = threadIdx.x; b < kBuckets; b += kThreads) S.hist[b] = 0;
     __syncthreads();
-    each_left_from(lim.t, [&](float l, bool in, int) {
+    each_left_from(lim.t, [&](float l, bool in, int, int) {
       const int b = bucket(l);
       if (in && b >= 0) atomicAdd(&S.hist[b], 1u);
     });
@@ -426,29 +470,39 @@ struct Row {
 
   // The mass of the tokens left, into `whole`.
   __device__ void weigh() {
-    float all[2] = {0.f, 0.f};
+    Sum all;
+    float even = 0.f;
+    auto take = [&](float w, int j) {
+      if (j & 1) all.add(even, w);
+      else even = w;
+    };
     if (lim.t == -FLT_MAX) {
-      each([&](float l, int, int j) { all[j & 1] += w_of(l); });
+      each([&](float l, int, int j) { take(w_of(l), j); });
     } else {
-      each_left_from(lim.t, [&](float l, bool in, int) { all[0] += in ? w_of(l) : 0.f; });
+      each_left_from(lim.t, [&](float l, bool in, int, int j) { take(in ? w_of(l) : 0.f, j); });
     }
-    mass_t v[3] = {__float2ll_rn((all[0] + all[1]) * kUnit), 0, 0};
+    mass_t v[3] = {all.fixed(), 0, 0};
     sum3(v);
     whole = v[0];
   }
   // Of the tokens left with l >= least: lists those of place 1 and adds up the masses of those of
-  // place 0, which lie above them, and 1 (place(l): 0, 1 or 2, no part), over the row.
+  // place 0, which lie above them, and 1 (place(l): 0, 1 or 2, no part), over the row.  The second only
+  // roughly, to 98 u at a thread's 98 tokens: it says whether the end lies before the bracket's, and a
+  // bracket whose end comes near the goal (rough_of) is rare.
   template <class Fn>
   __device__ __forceinline__ void list_by(float least, bool gather, mass_t (&v)[3], Fn&& place) {
     __syncthreads();
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
-    float above = 0.f, in = 0.f;
+    Sum above;
+    float even = 0.f;
+    float in = 0.f;
     int count = 0;
-    each_left_from(least, [&](float l, bool is, int i) {
+    each_left_from(least, [&](float l, bool is, int i, int j) {
       const int at = is ? place(l) : 2;
-      const float w = w_of(l);
-      above += at == 0 ? w : 0.f;
+      const float w = w_of(l), w0 = at == 0 ? w : 0.f;
+      if (j & 1) above.add(even, w0);
+      else even = w0;
       if (at == 1) {
         in += w;
         ++count;
@@ -458,7 +512,7 @@ struct Row {
         }
       }
     });
-    v[0] = __float2ll_rn(above * kUnit);
+    v[0] = above.fixed();
     v[1] = __float2ll_rn(in * kUnit);
     v[2] = count;
     sum3(v);
@@ -677,6 +731,7 @@ struct Row {
     M w0 = v[0] + __shfl_sync(0xffffffffu, part, 0) + (wi - ws);
     if (use_p) {
       const M whole = list_only ? all : v[2], goal = goal_of(p, whole);
+      const M near = kPairs ? M(0) : M(near_fixed(p, whole));
       M run = w0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -684,7 +739,7 @@ struct Row {
         if (i < n) {
           // token i is kept if the mass before it is short of the goal
           if constexpr (!kPairs)
-            if (i > 0 && distance(run, goal) <= near_of(whole)) S.again = 1;
+            if (i > 0 && distance(run, goal) <= near) S.again = 1;
           const bool kept = i == 0 || run < goal;
           run += w[j];
           if (kept && (i + 1 == n || !(run < goal))) S.n_keep = i + 1;
@@ -708,7 +763,7 @@ struct Row {
   // The lowest index among the largest logits.
   __device__ int first_top() {
     int at = kNone;
-    each_from<false>(m, [&](float, bool in, int i) { at = min(at, in ? first + i : kNone); });
+    each_from<false>(m, [&](float, bool in, int i, int) { at = min(at, in ? first + i : kNone); });
     at = __reduce_min_sync(0xffffffffu, at);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) S.r_idx[threadIdx.x >> 5] = at;
@@ -983,11 +1038,11 @@ struct Row {
       if (lost) return 0.f;
       float z;
       done_p = !by_count || before == 0;
-      const mass_t goal = by_count ? 0 : goal_of(p, whole), margin = near_of(whole);
-      const bool sure = by_count || (v[0] + margin < goal && v[0] + v[1] - margin > goal);
+      const mass_t goal = by_count ? 0 : goal_of(p, whole), margin = by_count ? 0 : near_fixed(p, whole);
+      const bool sure = by_count || (v[0] + margin < goal && v[0] + v[1] - rough_of(v[1]) - margin > goal);
       if (sure && resolve(v, d, false, before, k, use_p && done_p, p, z)) return z;
       // fp32 does not tell (or has told that the end lies elsewhere)
-      if (by_count || (v[0] - margin < goal && v[0] + v[1] + margin > goal)) {
+      if (by_count || (v[0] - margin < goal && v[0] + v[1] + rough_of(v[1]) + margin > goal)) {
         cl.sync();
         bool holds = true;
         if (by_count) {
@@ -1026,8 +1081,8 @@ struct Row {
       if (!by_count) {
         // does the bracket hold the end?
         if (!pairs) {
-          const mass_t goal = goal_of(p, v[2]), near = near_of(v[2]);
-          pairs = distance(v[0], goal) <= near || distance(v[0] + v[1], goal) <= near;
+          const mass_t goal = goal_of(p, v[2]), near = near_fixed(p, v[2]);
+          pairs = distance(v[0], goal) <= near || distance(v[0] + v[1], goal) <= near + rough_of(v[1]);
         }
         bool below_top, reached;
         if (pairs) {

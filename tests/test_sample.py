@@ -396,3 +396,37 @@ def test_near_ties_of_the_race(pkg, V, kind):
     noise[:, 5] = 4.0
     got, want = _race(pkg, x, noise, 1.0, "off")
     assert got == [want] * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(151936, torch.float32), (38000, torch.bfloat16)])
+def test_borders_of_top_p_with_a_common_error(pkg, V, dtype):
+    """Half the mass in equal logits far below the top, whose weights share one rounding error: the whole
+    is off by some 2^-21 in fp32.  Top-p meets the mass before a token between them to 2^-25."""
+    rng, n = np.random.default_rng(V), 32
+    x, T, p = torch.zeros(n, V), [], []
+    f32, bf = np.float32, lambda a: torch.tensor(a, dtype=torch.float32).to(dtype).float().numpy()  # noqa: E731
+    for r in range(n):
+        octaves = np.log2(V)
+        t = rng.uniform(0.6, 1.9, 400).astype(f32)
+        # of many temperatures and values those whose exponent is rounded farthest, up or down
+        c = (f32(1.442695) / t)[:, None]
+        l = bf(-np.log(2) * octaves * t[:, None] * rng.uniform(0.99, 1.01, (400, 400)))
+        err = (-l * c).astype(np.float64) + l.astype(np.float64) / np.log(2) / t[:, None]
+        at = np.unravel_index((err if r % 2 else -err).argmax(), err.shape)
+        T.append(float(t[at[0]]))
+        row = np.full(V, l[at], f32)
+        some = rng.permutation(V)[:301]
+        row[some[0]] = 0
+        mid = bf(-np.log(2) * (octaves - 1) * T[-1] * np.linspace(0.98, 1.02, 300))
+        row[some[1:]] = mid
+        x[r] = torch.tensor(row)
+        e = np.exp(np.sort(row.astype(np.float64))[::-1] / T[-1])
+        before, i = e.cumsum() - e, 100 + 3 * r
+        q = f32(before[i] / e.sum())
+        while r % 4 < 2 and float(q) * e.sum() >= before[i]:
+            q = np.nextafter(q, f32(0))
+        while r % 4 >= 2 and float(q) * e.sum() <= before[i]:
+            q = np.nextafter(q, f32(1))
+        p.append(float(q))
+    compare(pkg, x.to(dtype), (T, None, p, None), 16)

@@ -621,13 +621,15 @@ int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_ro
  *
  * dspark_accept_tree walks each tree from its anchor: from row c to the lowest child whose
  * token row_tok is row_sample[c], the token sampled from the target's distribution at c,
- * until there is none (or gamma drafts are taken, or the sample is negative).
+ * until there is none (or gamma drafts are taken).  A row whose sample is negative has none
+ * (dspark_sample's for a row without a token): the walk ends before it, and a segment whose
+ * anchor has none counts as empty.
  *   row_tok, row_sample  int32 [max_rows]
  *   path        int32 [B, gamma + 1] out: the rows passed, as indices in the segment, the
  *               anchor first, -1 beyond
  *   path_tok    int32 [B, gamma] out: their tokens but the anchor's, -1 beyond
  *   accept_len  int32 [B] out: drafts taken, L (-1 for an empty segment)
- *   out_tok     int32 [B] out: the sample at the last row (-1 for an empty segment)
+ *   out_tok     int32 [B] out: the sample at the last row passed (-1 for an empty segment)
  * The committed tokens are the target's own samples.  A segment that no buffer holds or of
  * more than DSPARK_MAX_TREE rows sets DSPARK_DEVERR_BAD_INPUT and counts as empty;
  * cu_seqlens[B] > max_rows sets DSPARK_DEVERR_ROWS_OVERFLOW and nothing is written.

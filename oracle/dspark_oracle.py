@@ -948,20 +948,21 @@ def verify_attention_tree(q, k_new, v_new, k_cache, v_cache, page_table, ctx_len
 
 
 def accept_tree(row_tok, row_parent, row_sample, cu_seqlens, gamma):
-    """(path, path_tok, accept_len, out_tok) of the walk along the samples."""
+    """(path, path_tok, accept_len, out_tok) of the walk along the samples; a row with a negative
+    one is not passed."""
     B = len(cu_seqlens) - 1
     path, tok = np.full((B, gamma + 1), -1, np.int32), np.full((B, gamma), -1, np.int32)
     n, out = np.full(B, -1, np.int32), np.full(B, -1, np.int32)
     for r in range(B):
         a, z = int(cu_seqlens[r]), int(cu_seqlens[r + 1])
         at = 0 if z > a else None
-        while at is not None:
+        while at is not None and row_sample[a + at] >= 0:
             n[r] += 1
             path[r, n[r]] = at
             if n[r]:
                 tok[r, n[r] - 1] = row_tok[a + at]
             out[r] = row_sample[a + at]
-            if n[r] == gamma or out[r] < 0:
+            if n[r] == gamma:
                 break
             at = next((j for j in range(at + 1, z - a)
                        if row_parent[a + j] == at and row_tok[a + j] == out[r]), None)

@@ -5,7 +5,8 @@
 //   tree_pack     mask_i = bit i | mask of its parent (itself and its ancestors),
 //                 pos_i  = ctx + the number of ancestors
 //   accept_tree   from row 0 down: the lowest child whose token is the one sampled at its
-//                 parent, until none has it; that sample is the bonus or correction token
+//                 parent, until none has it; that sample is the bonus or correction token.  A row
+//                 without a sample (negative) is not passed: nothing could follow it
 // The walk keeps the target's distribution: every committed token is the target's own sample
 // at its position.
 //
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(32)
   __syncwarp();
   int32_t* const p_out = path + (long long)r * (gamma + 1);
   int32_t* const t_out = path_tok + (long long)r * gamma;
-  int len = 0, at = s.n > 0 ? 0 : -1, say = -1;
+  int len = 0, at = s.n > 0 && s_sample[0] >= 0 ? 0 : -1, say = -1;
   while (at >= 0) {
     if (lane == 0) {
       p_out[len] = at;
@@ -122,13 +123,14 @@ __global__ void __launch_bounds__(32)
     say = s_sample[at];
     const int from = at;
     at = -1;
-    if (++len <= gamma && say >= 0) {
+    if (++len <= gamma) {
       for (int j0 = from + 1; j0 < s.n; j0 += 32) {
         const int j = j0 + lane;
         const unsigned hit =
             __ballot_sync(0xffffffffu, j < s.n && s_up[j] == from && s_tok[j] == say);
         if (hit) {
           at = j0 + __ffs(hit) - 1;
+          if (s_sample[at] < 0) at = -1;
           break;
         }
       }

@@ -268,3 +268,21 @@ def test_commit_refused_changes_nothing(pkg, bad):
     for k, v in s.items():
         np.testing.assert_array_equal(d[k].cpu().numpy(), v, err_msg=k)
     assert (com == -9).all() and (ncom == -9).all()
+
+
+@pytest.mark.gpu
+def test_accept_ends_before_a_row_without_a_sample(pkg):
+    """Samples of -1: the anchor's leaves the request as it is, a later row's is not passed."""
+    cu = np.array([0, 4, 8, 12, 13], np.int32)
+    parent = np.array([-1, 0, 1, 1] * 3 + [-1], np.int32)
+    tok = np.array([9, 5, 6, 7] * 3 + [9], np.int32)
+    say = np.array([-1, 6, 1, 1, 5, -1, 1, 1, 5, 7, -1, -1, -1], np.int32)
+    out = [torch.full(s, -77, dtype=torch.int32, device="cuda") for s in ((4, 4), (4, 3), (4,), (4,))]
+    pkg.accept_tree(*(torch.tensor(x, device="cuda") for x in (tok, parent, cu, say)), *out)
+    assert pkg.read_device_error() == 0
+    path, ptok, n, last = (x.tolist() for x in out)
+    assert n == [-1, 0, 1, -1] and last == [-1, 5, 7, -1]
+    assert path == [[-1] * 4, [0, -1, -1, -1], [0, 1, -1, -1], [-1] * 4]
+    assert ptok == [[-1] * 3, [-1] * 3, [5, -1, -1], [-1] * 3]
+    for a, b in zip(out, O.accept_tree(tok, parent, say, cu, 3)):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)

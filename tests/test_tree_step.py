@@ -191,3 +191,28 @@ def test_chain_step_from_logits(pkg, mode):
     torch.cuda.synchronize()
     want = [getattr(step, n) for n in names] + [d[k] for k in ("k_cache", "ctx_len")]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_rows_without_a_token_commit_nothing(pkg):
+    """Logits that are all -inf leave a row without a sample: at an anchor the request keeps its state,
+    on a path the commit ends before that row."""
+    sizes = [30, 30, 30]
+    d, rows = make(sizes, seed=3)
+    # a chain of token 0 in the requests; every sample is token 0
+    d["row_parent"][:90] = torch.tensor([-1] + list(range(29)), dtype=torch.int32, device="cuda").repeat(3)
+    d["row_tok"].zero_()
+    d["logits"][:] = -1.0
+    d["logits"][:, 0] = 50.0
+    d["logits"][30] = -float("inf")               # the second request's anchor
+    d["logits"][60 + 3] = float("nan")            # the fourth row of the third's path
+    step = pkg.TreeStep(3, GAMMA, HQ, HKV, rows, 30)
+    ctx, anchor = d["ctx_len"].clone(), d["anchor"].clone()
+    step.run(d)
+    torch.cuda.synchronize()
+    assert pkg.read_device_error() == 0
+    assert step.row_sample[[30, 63]].tolist() == [-1, -1]
+    assert step.accept_len.tolist() == [GAMMA, -1, 2] and step.out_tok.tolist() == [0, -1, 0]
+    assert (d["ctx_len"] - ctx).tolist() == [GAMMA + 1, 0, 3]
+    assert d["anchor"].tolist() == [0, int(anchor[1]), 0] and step.n_committed.tolist() == [GAMMA + 1, 0, 3]
+    assert (step.committed[1] == -1).all() and step.committed[2].tolist() == [0] * 3 + [-1] * (GAMMA - 2)

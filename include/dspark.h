@@ -604,7 +604,7 @@ int dspark_compact_kv4(const void* k_new, const void* v_new, int Hkv, int max_ro
  * "Ragged verify under full CUDA graphs"); here a request's packed rows may be the nodes
  * of a tree instead, each with the position of its depth, and the target's own samples
  * choose the branch.  A step: dspark_tree_pack, the forward pass with
- * dspark_verify_attn_tree, dspark_sample, dspark_accept_tree, dspark_compact_path.
+ * dspark_verify_attn_tree, dspark_sample_every_row, dspark_accept_tree, dspark_compact_path.
  *
  *   row_parent  int32 [max_rows]: the row's parent as an index in its segment, less than
  *               the row's own; -1: none.  Row 0 of a segment is the anchor.
@@ -725,6 +725,14 @@ int dspark_sample(const void* logits, long long stride, int dtype, int rows, int
                   const int32_t* top_k, const float* top_p, const float* min_p,
                   const float* exp_noise, int32_t* tokens,
                   void* probs, int probs_dtype, void* stream);
+/* dspark_sample, but that every row before *n_rows is written: token -1 and probs 0 where
+ * dspark_sample leaves them as they are (padding by row_req, refused parameters), so that a step does
+ * not go on with those of an earlier call. */
+int dspark_sample_every_row(const void* logits, long long stride, int dtype, int rows, int V,
+                            const int32_t* row_req, const int32_t* n_rows, int B,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const float* exp_noise, int32_t* tokens, void* probs,
+                            int probs_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * dspark_step_graph -- the whole verification step as one CUDA graph, with the

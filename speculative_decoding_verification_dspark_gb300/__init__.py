@@ -87,6 +87,8 @@ _SIGNATURES = {
     "dspark_verify_attn_tree": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I,
                                      _I, _F, _I, _I, _P, _P, _P, _Z, _P]),
     "dspark_sample": (_I, [_P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "dspark_sample_every_row": (_I, [_P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I,
+                                     _P]),
     "dspark_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _P, _I, _I, _F, _P, _P, _I,
                                  _I, _I, _P, _P, _P, _P]),
     "dspark_kv4_store": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _I, _P, _I, _I, _F, _F, _P,
@@ -618,12 +620,14 @@ def verify_attn_tree(q, k_new, v_new, k_cache, v_cache, page_table, ctx_len, cu_
 
 
 def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, probs=None,
-           row_req=None, stream=None, n_rows=None):
+           row_req=None, stream=None, n_rows=None, every_row=False):
     """Tokens and distributions from logits (dspark_sample): logits [rows, V] fp32 or bf16, rows
     possibly apart; temperature, top_p, min_p fp32 [B] and top_k int32 [B], each None where it is
     off; exp_noise fp32 [rows, V]; tokens int32 [rows] out or None; probs fp32 or bf16 [rows, V]
     out or None; row_req int32 [rows] (< 0: padding, left as it is) or None: row i has the
-    parameters of index i; n_rows int32 [1] or None: rows from there on are left as they are."""
+    parameters of index i; n_rows int32 [1] or None: rows from there on are left as they are.
+    every_row: padding and refused rows before n_rows get token -1 and probs 0
+    (dspark_sample_every_row)."""
     dev = _current(logits)
     dt = _float_dtype(logits, "logits")
     if logits.dim() != 2:
@@ -642,7 +646,8 @@ def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, pro
     def par(t, name, dtype):
         return None if t is None else _arg(t, dev, name, dtype, (B,))
 
-    _check("dspark_sample", lib().dspark_sample(
+    name = "dspark_sample_every_row" if every_row else "dspark_sample"
+    _check(name, getattr(lib(), name)(
         logits.data_ptr(), stride, dt, rows, V,
         None if row_req is None else _arg(row_req, dev, "row_req", i32, (rows,)),
         None if n_rows is None else _arg(n_rows, dev, "n_rows", i32, (1,)), B,
@@ -860,7 +865,8 @@ class VerifyStep:
         """p_target of ``inp`` from its logits, filtered by its requests' parameters (temperature,
         top_k, top_p, min_p [B], each optional), for the rows of the last pack."""
         sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
-               inp.get("min_p"), None, None, inp["p_target"], self.row_req, stream, n_rows=self.M_pack)
+               inp.get("min_p"), None, None, inp["p_target"], self.row_req, stream, n_rows=self.M_pack,
+               every_row=True)   # (none of an earlier step)
 
     def attention(self, inp, stream=None):
         if self.kv4:
@@ -1031,7 +1037,7 @@ class TreeStep:
     def sample(self, inp, stream=None):
         sample(inp["logits"], inp.get("temperature"), inp.get("top_k"), inp.get("top_p"),
                inp.get("min_p"), inp["exp_noise"], self.row_sample, None, inp["row_req"], stream,
-               n_rows=inp["cu_seqlens"][-1:])
+               n_rows=inp["cu_seqlens"][-1:], every_row=True)   # (none of an earlier step)
 
     def accept(self, inp, stream=None):
         accept_tree(inp["row_tok"], inp["row_parent"], inp["cu_seqlens"], self.row_sample, self.path,

@@ -683,11 +683,11 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
                             static_cast<cudaStream_t>(stream));
 }
 
-int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
+static int sample_impl(const void* logits, long long stride, int dtype, int rows, int V,
                   const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,
                   const int32_t* top_k,
                   const float* top_p, const float* min_p, const float* exp_noise, int32_t* tokens,
-                  void* probs, int probs_dtype, void* stream) {
+                  void* probs, int probs_dtype, bool every_row, void* stream) {
   CHECK(logits && (tokens || probs) && (!tokens || exp_noise), DSPARK_EINVAL);
   CHECK(dtype == DSPARK_F32 || dtype == DSPARK_BF16, DSPARK_EINVAL);
   CHECK(!probs || probs_dtype == DSPARK_F32 || probs_dtype == DSPARK_BF16, DSPARK_EINVAL);
@@ -701,8 +701,24 @@ int dspark_sample(const void* logits, long long stride, int dtype, int rows, int
   int rc = device_ok();
   if (rc != DSPARK_OK) return rc;
   const SampleArgs a = {logits, stride, rows, V, row_req, n_rows, B, temperature, top_k, top_p, min_p,
-                        exp_noise, tokens, probs, device_error_word()};
+                        exp_noise, tokens, probs, device_error_word(), every_row};
   return launch_sample(a, dtype, probs ? probs_dtype : DSPARK_F32, static_cast<cudaStream_t>(stream));
+}
+
+int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
+                  const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,
+                  const int32_t* top_k, const float* top_p, const float* min_p,
+                  const float* exp_noise, int32_t* tokens, void* probs, int probs_dtype, void* stream) {
+  return sample_impl(logits, stride, dtype, rows, V, row_req, n_rows, B, temperature, top_k, top_p, min_p,
+                     exp_noise, tokens, probs, probs_dtype, false, stream);
+}
+
+int dspark_sample_every_row(const void* logits, long long stride, int dtype, int rows, int V,
+                            const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,
+                            const int32_t* top_k, const float* top_p, const float* min_p,
+                            const float* exp_noise, int32_t* tokens, void* probs, int probs_dtype, void* stream) {
+  return sample_impl(logits, stride, dtype, rows, V, row_req, n_rows, B, temperature, top_k, top_p, min_p,
+                     exp_noise, tokens, probs, probs_dtype, true, stream);
 }
 
 int dspark_accept_tree(const int32_t* row_tok, const int32_t* row_parent,

@@ -151,6 +151,7 @@ struct SampleArgs {
   int32_t* tokens;               // [rows], nullable
   void* probs;                   // [rows, V], nullable
   unsigned int* err;
+  bool every_row;                // rows that are left otherwise, but for those from n_rows on, get token -1 and probs 0
 };
 int launch_sample(const SampleArgs& a, int dtype, int probs_dtype, cudaStream_t stream);
 

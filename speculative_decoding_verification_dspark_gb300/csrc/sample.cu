@@ -1276,7 +1276,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   // the row's parameters (every decision below is the same in all threads of the cluster)
-  if (req < 0) return;
+  P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V : nullptr;
+  auto none = [&]() {  // no token, no probability
+    if (probs)
+      for (int i = tid; i < R.n; i += kThreads) probs[R.first + i] = P(0.f);
+    if (a.tokens && rank == 0 && tid == 0) a.tokens[row] = -1;
+  };
+  if (req < 0) {
+    if (a.every_row) none();
+    return;
+  }
   bool bad = req >= a.B;
   float temp = 1.f, p = 1.f, mp = 0.f;
   int k = 0;
@@ -1289,6 +1298,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (bad) {
     if (rank == 0 && tid == 0) raise_error(a.err, DSPARK_DEVERR_BAD_INPUT);
+    if (a.every_row) none();
     return;
   }
   const bool greedy = temp == 0.f;
@@ -1337,12 +1347,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.k_least = least;
   R.s = S.c_hi * kPerOctave;
   R.nc = -S.c_hi;
-  P* const probs = a.probs ? static_cast<P*>(a.probs) + (long long)row * a.V : nullptr;
   const float* const noise = a.noise ? a.noise + (long long)row * a.V : nullptr;
   if (m == -INFINITY) {  // no token is left to draw from
-    if (probs)
-      for (int i = tid; i < R.n; i += kThreads) probs[R.first + i] = P(0.f);
-    if (a.tokens && rank == 0 && tid == 0) a.tokens[row] = -1;
+    none();
     cl.sync();
     return;
   }
@@ -1367,6 +1374,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (use_p && !done_p && !R.lost) z = R.cut(0, true, p, done_p);
   if (R.lost) {
     if (rank == 0 && tid == 0) raise_error(a.err, DSPARK_DEVERR_WORK_OVERFLOW);
+    if (a.every_row) none();
     return;
   }
   const bool race = a.tokens != nullptr;

@@ -430,3 +430,24 @@ def test_borders_of_top_p_with_a_common_error(pkg, V, dtype):
             q = np.nextafter(q, f32(1))
         p.append(float(q))
     compare(pkg, x.to(dtype), (T, None, p, None), 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [300, 70001])
+def test_every_row_is_written(pkg, V):
+    """Refused and padding rows before n_rows get token -1 and no probability."""
+    x = logits_of("wide", 6, V, torch.float32, 5).cuda()
+    dev = lambda v, d: torch.tensor(v, dtype=d, device="cuda")  # noqa: E731
+    e = torch.full((6, V), 0.5, device="cuda")
+    T, req = dev([1.0, float("nan"), -1.0], torch.float32), dev([0, 1, -1, 2, 7, 0], torch.int32)
+    out = []
+    for every in (False, True):
+        tok = torch.full((6,), -77, dtype=torch.int32, device="cuda")
+        pr = torch.full((6, V), 77.0, device="cuda")
+        pkg.sample(x, T, None, None, None, e, tok, pr, req, n_rows=dev([5], torch.int32), every_row=every)
+        assert pkg.read_device_error() == 0x10
+        out.append((tok, pr))
+    first = int(out[0][0][0])
+    assert first >= 0 and out[0][0].tolist() == [first] + [-77] * 5 and (out[0][1][1:] == 77).all()
+    assert out[1][0].tolist() == [first] + [-1] * 4 + [-77]
+    assert torch.equal(out[0][1][0], out[1][1][0]) and (out[1][1][1:5] == 0).all() and (out[1][1][5] == 77).all()

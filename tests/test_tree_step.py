@@ -216,3 +216,48 @@ def test_rows_without_a_token_commit_nothing(pkg):
     assert (d["ctx_len"] - ctx).tolist() == [GAMMA + 1, 0, 3]
     assert d["anchor"].tolist() == [0, int(anchor[1]), 0] and step.n_committed.tolist() == [GAMMA + 1, 0, 3]
     assert (step.committed[1] == -1).all() and step.committed[2].tolist() == [0] * 3 + [-1] * (GAMMA - 2)
+
+
+@pytest.mark.gpu
+def test_refused_rows_do_not_carry_over(pkg):
+    """A request whose parameters a later step refuses, or whose row it calls padding, takes nothing
+    from the samples of the step before."""
+    sizes = [20, 20, 20]
+    d, rows = make(sizes, seed=5)
+    d["row_parent"][:60] = torch.tensor([-1] + list(range(19)), dtype=torch.int32, device="cuda").repeat(3)
+    d["row_tok"].zero_()
+    d["logits"][:] = -1.0
+    d["logits"][:, 0] = 50.0
+    step = pkg.TreeStep(3, GAMMA, HQ, HKV, rows, 20)
+    step.run(d)
+    assert step.accept_len.tolist() == [GAMMA] * 3
+    d["temperature"][1] = float("nan")
+    d["row_req"][40 + 2] = -1
+    ctx, anchor = d["ctx_len"].clone(), d["anchor"].clone()
+    d["free_top"].fill_(d["free_pages"].numel())       # (pages enough: the caches are not read here)
+    d["page_table"] = torch.nn.functional.pad(d["page_table"], (0, 2))
+    step.run(d)
+    torch.cuda.synchronize()
+    assert pkg.read_device_error() == 0x10
+    assert step.accept_len.tolist() == [GAMMA, -1, 1] and step.row_sample[20:40].tolist() == [-1] * 20
+    assert (d["ctx_len"] - ctx).tolist() == [GAMMA + 1, 0, 2] and int(d["anchor"][1]) == int(anchor[1])
+
+
+@pytest.mark.gpu
+def test_refused_distributions_do_not_carry_over(pkg):
+    """VerifyStep from logits: the rows of a request that the sampler refuses have no distribution."""
+    import harness
+    wl = W.WORKLOADS["tiny"]
+    d, step = harness.prepare(W.make_inputs(wl, seed=4), O.STATIC)
+    rows = step.max_rows
+    d["p_target"] = torch.full((rows, wl.vocab), 77.0, device="cuda")
+    e = dict(d, logits=torch.randn(rows, wl.vocab, device="cuda"), temperature=torch.ones(wl.B, device="cuda"))
+    e["temperature"][1] = float("nan")
+    step.schedule(e, O.STATIC)
+    step.pack(e, O.STATIC)
+    step.distributions(e)
+    assert pkg.read_device_error() == 0x10
+    M = int(step.M_pack)
+    p, req = d["p_target"], step.row_req[:M]
+    assert (p[:M][req == 1] == 0).all() and (p[M:] == 77).all()
+    assert ((p[:M][req != 1].sum(1) - 1).abs() < 1e-4).all()

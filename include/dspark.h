@@ -660,8 +660,8 @@ int dspark_compact_path(const void* k_new, const void* v_new, int row_bytes, int
  * cu_seqlens[r] + i sees the ctx_len[r] committed keys and the block rows j of its segment
  * whose bit j is set in row_mask[cu_seqlens[r] + i] (dspark_tree_pack's, or any other mask:
  * the row itself is seen only if its bit is set).  Arguments as dspark_verify_attn, and
- *   row_mask  [max_rows, words] 64-bit words; rows of the segment from 64 words on are seen
- *             by none, bits past the segment are ignored
+ *   row_mask  [max_rows, words] 64-bit words (8-byte aligned); rows of the segment from 64
+ *             words on are seen by none, bits past the segment are ignored
  *   out       bf16 [max_rows, Hq, 128]; a row that sees no key, or none with a score
  *             above -inf, gets out = 0 and lse = -inf
  *   scale     a positive normal number

@@ -639,6 +639,7 @@ int dspark_tree_pack(const int32_t* row_parent, const int32_t* cu_seqlens, const
   CHECK(row_parent && cu_seqlens && ctx_len && row_mask && row_pos, DSPARK_EINVAL);
   CHECK(B >= 1 && B <= DSPARK_MAX_B && max_rows >= 1, DSPARK_EINVAL);
   CHECK(words >= 1 && words <= DSPARK_MAX_TREE / 64, DSPARK_EINVAL);
+  CHECK((reinterpret_cast<uintptr_t>(row_mask) & 7u) == 0, DSPARK_EINVAL);
   int rc = device_ok();
   if (rc != DSPARK_OK) return rc;
   return launch_tree_pack(row_parent, cu_seqlens, ctx_len, B, max_rows, words, row_mask, row_pos,
@@ -668,6 +669,8 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
   CHECK(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(k_cache) &&
             aligned16(v_cache) && aligned16(out),
         DSPARK_EINVAL);
+  CHECK((reinterpret_cast<uintptr_t>(row_mask) & 7u) == 0 && (reinterpret_cast<uintptr_t>(lse) & 3u) == 0,
+        DSPARK_EINVAL);
   CHECK(B >= 1 && B <= DSPARK_MAX_B && max_rows >= 1 && n_pages >= 1 && max_pages >= 1,
         DSPARK_EINVAL);
   CHECK(words >= 1 && words <= DSPARK_MAX_TREE / 64, DSPARK_EINVAL);
@@ -696,7 +699,8 @@ static int sample_impl(const void* logits, long long stride, int dtype, int rows
   CHECK(B >= 1 && (row_req || B >= rows), DSPARK_EINVAL);
   const uintptr_t es = dtype == DSPARK_BF16 ? 2 : 4, ps = probs_dtype == DSPARK_BF16 ? 2 : 4;
   CHECK(reinterpret_cast<uintptr_t>(logits) % es == 0 &&
-            (!probs || reinterpret_cast<uintptr_t>(probs) % ps == 0),
+            (!probs || reinterpret_cast<uintptr_t>(probs) % ps == 0) &&
+            ((reinterpret_cast<uintptr_t>(exp_noise) | reinterpret_cast<uintptr_t>(tokens)) & 3u) == 0,
         DSPARK_EINVAL);
   int rc = device_ok();
   if (rc != DSPARK_OK) return rc;

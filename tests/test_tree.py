@@ -286,3 +286,19 @@ def test_accept_ends_before_a_row_without_a_sample(pkg):
     assert ptok == [[-1] * 3, [-1] * 3, [5, -1, -1], [-1] * 3]
     for a, b in zip(out, O.accept_tree(tok, parent, say, cu, 3)):
         np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_alignment_refusals(pkg):
+    """Addresses that a kernel's wide accesses could not take, refused before any launch."""
+    lib, f, by1, by4 = pkg.load(), ctypes.c_void_p(4096), ctypes.c_void_p(4097), ctypes.c_void_p(4100)
+    assert lib.dspark_tree_pack(f, f, f, 2, 8, 1, by4, f, None) == -1
+
+    def attn(mask=f, lse=f):
+        return lib.dspark_verify_attn_tree(f, f, f, f, f, 9, f, 4, f, f, mask, 1, 2, 8, 8, 2, 16,
+                                           ctypes.c_float(0.1), 8, 4, f, lse, f, 1 << 40, None)
+
+    def draw(e=f, tok=f, entry=lib.dspark_sample):
+        return entry(f, 100, 0, 4, 100, f, None, 2, f, f, f, f, e, tok, f, 0, None)
+
+    assert attn(mask=by4) == -1 and attn(lse=by1) == -1
+    assert draw(e=by1) == -1 and draw(tok=by1) == -1 and draw(e=by1, entry=lib.dspark_sample_every_row) == -1

@@ -640,7 +640,8 @@ def sample(logits, temperature, top_k, top_p, min_p, exp_noise, tokens=None, pro
         raise ValueError("logits: expected a tensor on the current CUDA device")
     f32, i32 = torch.float32, torch.int32
     given = [t for t in (temperature, top_k, top_p, min_p) if t is not None]
-    B = given[0].numel() if given else rows
+    # (without parameters row_req only says which rows are padding)
+    B = given[0].numel() if given else rows if row_req is None else 0x7fffffff
     pdt = F32 if probs is None else _float_dtype(probs, "probs")
 
     def par(t, name, dtype):

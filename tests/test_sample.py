@@ -451,3 +451,15 @@ def test_every_row_is_written(pkg, V):
     assert first >= 0 and out[0][0].tolist() == [first] + [-77] * 5 and (out[0][1][1:] == 77).all()
     assert out[1][0].tolist() == [first] + [-1] * 4 + [-77]
     assert torch.equal(out[0][1][0], out[1][1][0]) and (out[1][1][1:5] == 0).all() and (out[1][1][5] == 77).all()
+
+
+@pytest.mark.gpu
+def test_request_indices_without_parameters(pkg):
+    """A few rows of a large batch: no parameter is read, so an index past the rows is none out of range."""
+    x = logits_of("wide", 3, 500, torch.float32, 5).cuda()
+    e = torch.full((3, 500), 0.5, device="cuda")
+    want, tok = (torch.full((3,), -77, dtype=torch.int32, device="cuda") for _ in range(2))
+    pkg.sample(x, None, None, None, None, e, want)
+    pkg.sample(x, None, None, None, None, e, tok, row_req=torch.tensor([9, -1, 1000], dtype=torch.int32, device="cuda"))
+    assert pkg.read_device_error() == 0
+    assert tok.tolist() == [int(want[0]), -77, int(want[2])]

@@ -368,7 +368,8 @@ int dspark_block_accept_estimate(const void* p_target, const void* p_draft, int 
  * DSPARK_DEVERR_NO_FREE_PAGE / _PAGE_ROW_FULL, if cu_seqlens[B] > max_rows it sets
  * DSPARK_DEVERR_ROWS_OVERFLOW, and if cu_seqlens[0] < 0 or accept_len[r] is outside
  * 0..gamma or keeps more rows than request r's packed segment holds, or ctx_len[r] is
- * negative or its positions would pass 32 bits, it sets DSPARK_DEVERR_BAD_INPUT; in each of these cases it changes nothing.
+ * negative or its new length would pass 2^31 - 1, it sets DSPARK_DEVERR_BAD_INPUT; in each of
+ * these cases it changes nothing.
  * ------------------------------------------------------------------------- */
 size_t dspark_compact_workspace_size(int B);
 int dspark_compact(const void* k_new, const void* v_new, int row_bytes, int max_rows,

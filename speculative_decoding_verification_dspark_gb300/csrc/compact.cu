@@ -39,6 +39,11 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
   return v;
 }
 
+// Pages of a length up to 2^31 - 1, whatever the page.
+__device__ __forceinline__ int pages_of(int length, int page_size) {
+  return length > 0 ? (length - 1) / page_size + 1 : 0;
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(1024)
@@ -83,12 +88,12 @@ __global__ void __launch_bounds__(1024)
       atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);  // unverified rows
     }
     c0 = ctx_len[tid];
-    if (c0 < 0 || c0 > 0x7fffffff - page_size - keep) {  // (positions past 32 bits)
+    if (c0 < 0 || c0 > 0x7fffffff - keep) {  // (a length past 32 bits)
       atomicOr(&s_flags, DSPARK_DEVERR_BAD_INPUT);
       c0 = 0;
     }
-    have = ceil_div(c0, page_size);
-    need = ceil_div(c0 + keep, page_size);
+    have = pages_of(c0, page_size);
+    need = pages_of(c0 + keep, page_size);
     nn = need - have;
     if (need > max_pages) atomicOr(&s_flags, DSPARK_DEVERR_PAGE_ROW_FULL);
   }

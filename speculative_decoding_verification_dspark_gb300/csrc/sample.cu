@@ -100,7 +100,8 @@ struct Sum {
            __float2ll_rn((lost.x + lost.y) * kUnit);
   }
 };
-__device__ __forceinline__ mass_t rough_of(mass_t in) { return in >> 17; }
+// Error of the mass above a bracket beside that (list_by).
+__device__ __forceinline__ mass_t slack_of(mass_t above, mass_t in) { return above != 0 ? in >> 17 : 0; }
 // What lies before a kept token is short of p of the whole (0 < p < 1).
 __device__ __forceinline__ mass_t goal_of(float p, mass_t whole) {
   const unsigned long long f = __float2ull_rn(p * 0x1p64f), w = whole;
@@ -486,23 +487,23 @@ struct Row {
     whole = v[0];
   }
   // Of the tokens left with l >= least: lists those of place 1 and adds up the masses of those of
-  // place 0, which lie above them, and 1 (place(l): 0, 1 or 2, no part), over the row.  The second only
-  // roughly, to 98 u at a thread's 98 tokens: it says whether the end lies before the bracket's, and a
-  // bracket whose end comes near the goal (rough_of) is rare.
+  // place 0, which lie above them (none_above: none do), and 1 (place(l): 0, 1 or 2, no part), over the
+  // row.  Their sum is exact as Sum is, the second mass alone to 98 u (a thread's tokens one by one), and
+  // so is the first's part in their sum: slack_of.
   template <class Fn>
-  __device__ __forceinline__ void list_by(float least, bool gather, mass_t (&v)[3], Fn&& place) {
+  __device__ __forceinline__ void list_by(float least, bool gather, bool none_above, mass_t (&v)[3], Fn&& place) {
     __syncthreads();
     if (threadIdx.x == 0) S.n_list = 0;
     __syncthreads();
-    Sum above;
+    Sum down;
     float even = 0.f;
     float in = 0.f;
     int count = 0;
     each_left_from(least, [&](float l, bool is, int i, int j) {
       const int at = is ? place(l) : 2;
-      const float w = w_of(l), w0 = at == 0 ? w : 0.f;
-      if (j & 1) above.add(even, w0);
-      else even = w0;
+      const float w = w_of(l), part = at <= 1 ? w : 0.f;
+      if (j & 1) down.add(even, part);
+      else even = part;
       if (at == 1) {
         in += w;
         ++count;
@@ -512,16 +513,18 @@ struct Row {
         }
       }
     });
-    v[0] = above.fixed();
+    v[0] = down.fixed();
     v[1] = __float2ll_rn(in * kUnit);
     v[2] = count;
     sum3(v);
     n_listed = (int)v[2];
+    if (none_above) v[1] = v[0];
+    v[0] -= v[1];
     v[2] = whole;
   }
   // The bracket [f_lo, f_hi).
-  __device__ void evaluate(float f_lo, float f_hi, bool gather, mass_t (&v)[3]) {
-    list_by(fmaxf(f_lo, lim.t), gather, v, [&](float l) { return l >= f_hi ? 0 : 1; });
+  __device__ void evaluate(float f_lo, float f_hi, bool gather, bool none_above, mass_t (&v)[3]) {
+    list_by(fmaxf(f_lo, lim.t), gather, none_above, v, [&](float l) { return l >= f_hi ? 0 : 1; });
   }
 
   // w in two parts, 2^-36 of it or better, by table and polynomial (Tang's scheme for the
@@ -731,7 +734,7 @@ struct Row {
     M w0 = v[0] + __shfl_sync(0xffffffffu, part, 0) + (wi - ws);
     if (use_p) {
       const M whole = list_only ? all : v[2], goal = goal_of(p, whole);
-      const M near = kPairs ? M(0) : M(near_fixed(p, whole));
+      const M near = kPairs ? M(0) : M(near_fixed(p, whole) + slack_of(v[0], v[1]));
       M run = w0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -999,10 +1002,9 @@ struct Row {
     // Of kThreads threads' tokens about kThreads ln(1 / (1 - k / kThreads)) pass k of their maxima;
     // where that is well below the list's size in all CTAs together, it is listed at once.
     if (by_count && k < kThreads && -kThreads * __logf(1.f - k / (float)kThreads) * C < 0.6f * kList) {
-      evaluate(lim.t, INFINITY, true, v);
+      evaluate(lim.t, INFINITY, true, true, v);
       if (n_listed <= kList) {
         done_p = true;
-        v[0] = 0;
         float z;
         if (!resolve(v, d, false, 0, k, use_p, p, z)) {
           cl.sync();
@@ -1032,17 +1034,18 @@ struct Row {
         const int b = bucket_of(l);
         return b < b0 ? 0 : b <= b1 ? 1 : 2;
       };
-      list_by(fmaxf(b1 == kBuckets - 1 ? -FLT_MAX : near - 4e-7f * (fabsf(m) + fabsf(near)), lim.t), true, v,
+      list_by(fmaxf(b1 == kBuckets - 1 ? -FLT_MAX : near - 4e-7f * (fabsf(m) + fabsf(near)), lim.t), true, before == 0, v,
               place);
       lost = (unsigned)n_listed != in;
       if (lost) return 0.f;
       float z;
       done_p = !by_count || before == 0;
       const mass_t goal = by_count ? 0 : goal_of(p, whole), margin = by_count ? 0 : near_fixed(p, whole);
-      const bool sure = by_count || (v[0] + margin < goal && v[0] + v[1] - rough_of(v[1]) - margin > goal);
+      const mass_t slack = slack_of(v[0], v[1]);
+      const bool sure = by_count || (v[0] + slack + margin < goal && v[0] + v[1] - margin > goal);
       if (sure && resolve(v, d, false, before, k, use_p && done_p, p, z)) return z;
       // fp32 does not tell (or has told that the end lies elsewhere)
-      if (by_count || (v[0] - margin < goal && v[0] + v[1] + rough_of(v[1]) + margin > goal)) {
+      if (by_count || (v[0] - slack - margin < goal && v[0] + v[1] + margin > goal)) {
         cl.sync();
         bool holds = true;
         if (by_count) {
@@ -1075,14 +1078,14 @@ struct Row {
     // (each round halves the outer range at least once or cuts it into 2048: far fewer are needed)
     for (int round = 0; round < 100; ++round) {
       const bool gather = in <= (unsigned)kList;
-      evaluate(f_lo, f_hi, gather, v);
+      evaluate(f_lo, f_hi, gather, before == 0, v);
       lost = (unsigned)n_listed != in;
       if (lost) return 0.f;
       if (!by_count) {
         // does the bracket hold the end?
         if (!pairs) {
           const mass_t goal = goal_of(p, v[2]), near = near_fixed(p, v[2]);
-          pairs = distance(v[0], goal) <= near || distance(v[0] + v[1], goal) <= near + rough_of(v[1]);
+          pairs = distance(v[0], goal) <= near + slack_of(v[0], v[1]) || distance(v[0] + v[1], goal) <= near;
         }
         bool below_top, reached;
         if (pairs) {

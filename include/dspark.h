@@ -71,7 +71,7 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
 #define DSPARK_DEVERR_PAGE_ROW_FULL 0x4u   /* page-table row too short (compact)   */
 #define DSPARK_DEVERR_WAIT_TIMEOUT  0x8u   /* a bounded in-kernel wait ran out     */
 #define DSPARK_DEVERR_BAD_INPUT     0x10u  /* index input out of range (token, page) */
-#define DSPARK_DEVERR_WORK_OVERFLOW 0x20u  /* attention work list larger than ws   */
+#define DSPARK_DEVERR_WORK_OVERFLOW 0x20u  /* attention work list larger than ws (and dspark_sample) */
 
 /* Limits checked on the host. */
 #define DSPARK_MAX_B        1024   /* requests per step                          */
@@ -715,11 +715,12 @@ int dspark_verify_attn_tree(const void* q, const void* k_new, const void* v_new,
  *   tokens      int32 [rows] out, nullable
  *   probs       [rows, V] fp32 or bf16 (probs_dtype) out, dense, nullable
  * Which tokens are kept and which wins the race is decided as in 64-bit arithmetic (but where
- * sums lie within 10^-10 of a border; the race with noise of 2^-100 to 2^20, as Exp(1) draws are); probs are fp32 values (2^-16) rounded once.  A row
- * without any logit above -inf gets token -1 and probs 0.  An index >= B, or a temperature
- * outside its range, or a NaN parameter sets DSPARK_DEVERR_BAD_INPUT and the row's outputs
- * are left as they are; so with DSPARK_DEVERR_WORK_OVERFLOW should a row's search contradict
- * itself, which no input is known to bring about.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
+ * sums lie within 10^-10 of a border; the race with noise of 2^-100 to 2^20, as Exp(1) draws
+ * are); probs are fp32 values (2^-16) rounded once.  A row without any logit above -inf gets
+ * token -1 and probs 0.  An index >= B, or a temperature outside its range, or a NaN parameter
+ * sets DSPARK_DEVERR_BAD_INPUT and the row's outputs are left as they are; so with
+ * DSPARK_DEVERR_WORK_OVERFLOW should a row's search contradict itself, which no input is known
+ * to bring about.  V <= DSPARK_MAX_VOCAB.  One kernel, no workspace.
  * ------------------------------------------------------------------------- */
 int dspark_sample(const void* logits, long long stride, int dtype, int rows, int V,
                   const int32_t* row_req, const int32_t* n_rows, int B, const float* temperature,

@@ -16,8 +16,8 @@
 //      estimate), and one pass sums the masses above and in it and lists its tokens;
 //   3  one CTA sorts the list and walks it.
 // Before that a bound from below takes out what cannot be kept (for top-k from the threads' largest
-// logits, for top-p from the row's mass): with k up to some hundred what passes it fits the list at
-// once.  A bracket that does not hold the end gives way to what lies above or below it, one of more
+// logits, the best of the CTAs' bounds; for top-p from the row's mass): with k up to some hundred what
+// passes it fits the list at once.  A bracket that does not hold the end gives way to what lies above or below it, one of more
 // than kList tokens is cut again by the bits of its logits, and one that holds a single value is
 // resolved by counting indices.  Where a sum comes so near to the border that fp32 cannot tell on
 // which side the end lies (near_of), sums are taken again in pairs of fp32 numbers (2^-36 or so): the
@@ -25,9 +25,10 @@
 //
 // What bounds it: instructions, and the meetings of the cluster (some eight a row, 1500 cycles each).
 // A pass over a chunk costs 6000 cycles for two CTAs of an SM, loading it 7000.  One row of 151936:
-// 16 to 19 us; 288 such rows with distributions 233 to 243 us (56 at the copy rate); 1024 rows of 129280 in bf16,
-// top-p with wide nuclei, 612 to 640 us (39).  512 threads with 76 KB, two to an SM: 256 threads with 38 KB
-// take 1143 us where these take 874 (larger clusters), 1024 with 152 KB 926.
+// 16 us; 288 such rows with distributions 234 to 246 us (56 at the copy rate); 1024 rows of 129280 in bf16,
+// top-p with wide nuclei, 655 to 670 us (39; 108 instructions a token).  512 threads with 76 KB, two to an
+// SM: at a stage when these took 874 us for the last, 256 threads with 38 KB (larger clusters) took 1143
+// and 1024 with 152 KB 926.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -1000,7 +1001,8 @@ struct Row {
       lim.i = kNone;
     }
     // Of kThreads threads' tokens about kThreads ln(1 / (1 - k / kThreads)) pass k of their maxima;
-    // where that is well below the list's size in all CTAs together, it is listed at once.
+    // where that is well below the list's size in all CTAs together, it is listed at once (fewer, as the
+    // bound is the best of theirs).
     if (by_count && k < kThreads && -kThreads * __logf(1.f - k / (float)kThreads) * C < 0.6f * kList) {
       evaluate(lim.t, INFINITY, true, true, v);
       if (n_listed <= kList) {

@@ -8,10 +8,12 @@
 // HBM and the tensor cores balance), so queries lie on the MMA's M side, 128 rows to a tile, and a
 // work item has up to two tiles that share the keys:
 //   S [128 rows x 128 keys] = Q . K^T         O [128 rows x 128 d] += P . V       (tcgen05)
-// with S and O in tensor memory and P, in bf16, in the columns that held S.  All 512 columns are
-// taken: two S, two O.  An item of one tile's rows runs as two streams of its key tiles, even and
-// odd, each with an S, an O and statistics of its own, joined at the item's end: so that one
-// stream's softmax runs beside the other's products whether there are two tiles or one.
+// with S and O in tensor memory and P, in bf16, in the columns that held S (the product takes 16-bit
+// operands; against 64 bits the output is off by 0.0019 to 0.0023 with that, by 0.0017 from its own
+// rounding alone).  All 512 columns are taken: two S, two O.  An item of one tile's rows runs as two
+// streams of its key tiles, even and odd, each with an S, an O and statistics of its own, joined at the
+// item's end: so that one stream's softmax runs beside the other's products whether there are two tiles
+// or one.
 //
 // Warps (one CTA an SM, persistent over its share of the key tiles, see own_items.cuh):
 //   0      K and Q, 2  V: TMA (128-byte swizzle), K and V into a ring of five 32 KB slots
@@ -23,11 +25,11 @@
 //          without a word to another thread; O is rescaled only where a row's maximum grows by 2^8
 // Every wait is bounded (DSPARK_DEVERR_WAIT_TIMEOUT on expiry).
 //
-// What bounds it: with one query tile HBM (256 single tokens over 0.5k to 4k keys 397 us, 357 at the copy
+// What bounds it: with one query tile HBM (256 single tokens over 0.5k to 4k keys 402 us, 357 at the copy
 // rate); with two a stream's chain, 3500 cycles a key tile: S to the softmax 150, 128 exponentials a
 // thread and P 1300, P to the issuing thread 150, O += P V and the next S 2 x 520, and 250 more each
 // time the tensor cores change from the one kind of product to the other (32 requests of 17 to 64
-// nodes over 1k to 4k keys 111 us, 52 at the copy rate; 16 of 97 to 256 nodes 294 us).
+// nodes over 1k to 4k keys 111 us, 52 at the copy rate; 16 of 97 to 256 nodes 295 us).
 
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -65,10 +65,11 @@ constexpr float kUnit = 0x1p44f;
 //   and n tokens has a mean of log2(n / M) octaves at most.
 //   The exponential is off by 2^-22 of w: 8 a b u W.
 //   The sums themselves (Sum): 2 u each, W being 1 at least.
+// (At most W / 16, which none of this reaches but a p so small that n / a is infinite.)
 __device__ __forceinline__ float near_of(float p, float whole, int n) {
   const float a = p * whole, b = (1 - p) * whole;
   const float x = __log2f(__fdividef(n, a)), y = __log2f(__fdividef(n, b));
-  return 0x1p-24f * ((1 - p) * a * (2.3f * y + 1.4f * x + 8.5f) + 4.f);
+  return fminf(0x1p-24f * ((1 - p) * a * (2.3f * y + 1.4f * x + 8.5f) + 4.f), whole / 16);
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;

@@ -463,3 +463,11 @@ def test_request_indices_without_parameters(pkg):
     pkg.sample(x, None, None, None, None, e, tok, row_req=torch.tensor([9, -1, 1000], dtype=torch.int32, device="cuda"))
     assert pkg.read_device_error() == 0
     assert tok.tolist() == [int(want[0]), -77, int(want[2])]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [700, 60000])
+def test_the_smallest_and_largest_top_p(pkg, V):
+    p = [1e-45, 1e-38, 1e-30, 1e-12, 1 - 2.0 ** -24, 1 - 2.0 ** -23]
+    for kind in ("wide", "equal", "two", "narrow"):
+        compare(pkg, logits_of(kind, 6, V, torch.float32, 4), (None, None, p, None), 17)
